@@ -380,6 +380,127 @@ dit_status dit_shard_finish_host(const double* partials, int n_partials, const f
                                  float* tensor_scale);
 
 /* ------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one shared projection, and their gradients.
+ *
+ * The frozen projection y = x W^T (any route above) serves a batch of rows that belong to
+ * several requests; row t uses adapter g(t) of a bank of n_adapters, or none:
+ *   forward   h[t]  = scale[g] * (x[t] A[g]^T)           rank values
+ *             y[t] += h[t] B[g]^T
+ *   backward  e[t]  = scale[g] * (dy[t] B[g])             rank values
+ *             dx[t] += e[t] A[g]
+ *             dA[g]  = sum over the rows t of g: e[t]^T x[t]
+ *             dB[g]  = sum over the rows t of g: dy[t]^T h[t]
+ * All sums are fp32; h and e are held with at least 16 significant bits; y and dx are rounded
+ * once.  Every sum has a fixed order (no atomics on values): a call with the same arguments gives
+ * the same bits.  y and dx of rows without an adapter are not touched.  A row's results depend
+ * on that row alone, and an adapter's gradients on its own rows alone, whatever the other
+ * rows hold.
+ *
+ * The plan.  dit_adapter_plan (host, no device work) turns the requests' lengths and adapters
+ * into a table of tiles of rows that share an adapter.  A plan serves every layer and step with
+ * the same batch.  Call it with table = NULL to learn plan->table_ints, then with a host buffer
+ * of that many int32, and copy the table to the device (16-byte aligned).
+ *   lengths  : host int64 [requests], rows of each request (>= 0), in batch order.
+ *   adapters : host int32 [requests], -1 for none, else < n_adapters.
+ *   training : 0 serves only; 1 makes a plan that dit_lora_backward accepts too.
+ * More than 2^31 - 256 rows, a negative length or an adapter outside [-1, n_adapters) is
+ * DIT_ERR_INVALID_ARG.  The kernels check every table entry they use: one outside the batch
+ * or the bank is skipped and raises DIT_ERR_INVALID_ARG in the device status word.
+ *
+ * x, dy : device bf16 [rows x k], [rows x n].       y, dx : device bf16 or fp32, updated.
+ * a     : device bf16 [n_adapters x rank x k].      b : device bf16 [n_adapters x n x rank].
+ * scale : device float [n_adapters].
+ * da, db: device float, the shapes of a and b, overwritten (adapters without rows get zeros).
+ *         dx may be NULL: the gradient of the input is then not computed.
+ * rank  : 8 to 128, a multiple of 8; k % 8 == 0, n % 8 == 0.  32-byte aligned pointers.
+ * saved : device buffer of dit_adapter_saved_bytes that the forward pass fills with h for the
+ *         backward pass (plan->training only), or NULL.  Its layout is the library's own.
+ * scratch : device buffer of dit_adapter_scratch_bytes for this plan, rank, k and n, contents
+ *         free; calls ordered on one stream may share it, so may layers of other sizes if it
+ *         is large enough for each.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  int64_t rows;       /* rows of the batch */
+  int64_t table_ints; /* int32 entries of the table */
+  int32_t n_adapters;
+  int32_t training;
+  int32_t n_tiles; /* tiles of up to 128 consecutive rows */
+  int32_t n_small; /* tiles of up to 16 rows in any places (serving plans: short requests) */
+} dit_adapter_plan_t;
+
+dit_status dit_adapter_plan(const int64_t* lengths, const int32_t* adapters, int64_t requests,
+                            int n_adapters, int training, dit_adapter_plan_t* plan,
+                            int32_t* table, int64_t table_ints);
+size_t dit_adapter_saved_bytes(const dit_adapter_plan_t* plan, int rank);
+size_t dit_adapter_scratch_bytes(const dit_adapter_plan_t* plan, int rank, int64_t k, int64_t n);
+dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int32_t* table_dev, const void* x,
+                            const void* a, const void* b, const float* scale, int rank, int64_t k,
+                            int64_t n, void* y, dit_dtype y_dt, void* saved, size_t saved_bytes,
+                            void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes,
+                            dit_stream_t stream);
+dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const int32_t* table_dev,
+                             const void* x, const void* dy, const void* a, const void* b,
+                             const float* scale, int rank, int64_t k, int64_t n,
+                             const void* saved, size_t saved_bytes, void* dx, dit_dtype dx_dt,
+                             float* da, float* db, void* scratch, size_t scratch_bytes, void* ws,
+                             size_t ws_bytes, dit_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * One AdamW step over many tensors in one launch, with the moments in 32 or in 8 bits.
+ *
+ * Per element, each operation rounded to fp32 (g, p read in their own types):
+ *   g' = g * (*grad_scale)               (grad_scale NULL: g' = g)
+ *   m  = m beta1 + g' (1 - beta1),       v = v beta2 + (g' g') (1 - beta2)
+ *   p  = p (1 - lr wd) - (m lr / (1 - beta1^t)) / (sqrt(v) (1 - beta2^t)^-1/2 + eps)
+ * with t = step (>= 1) and the factors computed in fp64 on the host.  p is rounded once to its
+ * type; copy (bf16, optional) receives p rounded to bf16.
+ *
+ * 8-bit moments.  A tensor is cut into blocks of 256 consecutive elements; m and u = sqrt(v) are
+ * held as E4M3 codes with one fp32 scale per block: scale = amax / 448 (amax * fp32(1/448)),
+ * code = RN_E4M3(value * (448 / amax)); a block with amax < 2^-100 has scale 0 and codes 0.  A
+ * nonzero u never gets code 0 (it would leave eps alone under a nonzero m): the smallest
+ * code, 2^-9, is its floor.  The update of p uses the new moments before they are encoded.  A NaN
+ * stays in its element; an infinite moment makes its block's scale infinite.
+ *
+ * descs : device array of n_tensors dit_adamw_tensor.  chunks : device int32 pairs
+ * (tensor, chunk) of n_chunks entries, one for each DIT_ADAMW_CHUNK consecutive elements of
+ * each tensor (dit_adamw_chunks fills them from host sizes: table NULL returns the count).
+ * The tensors of one call share p_dt, g_dt and moment_bits; every pointer is 32-byte aligned
+ * (the scales 4-byte).  Tensors of one call must not overlap.  The pointers in descs are the
+ * caller's to get right; the chunk table is checked against n_tensors and the tensors' sizes.
+ *
+ * dit_adamw_moments writes the moments' values (m = code * scale, v = (code * scale)^2) of
+ * 8-bit tensors to the descs' m_values / v_values as bf16 (an E4M3 code has four significant
+ * bits, so bf16 costs the values at most 2^-9 of themselves).
+ * ------------------------------------------------------------------------------------ */
+#define DIT_ADAMW_CHUNK 4096
+typedef struct {
+  void* p;           /* parameters: fp32 or bf16 */
+  const void* g;     /* gradients: fp32 or bf16 */
+  void* m;           /* first moment: fp32, or E4M3 codes */
+  void* v;           /* second moment: fp32, or E4M3 codes of its root */
+  float* m_scale;    /* 8-bit moments: [ceil(n / 256)] */
+  float* v_scale;
+  void* copy;        /* bf16 copy of p, or NULL */
+  void* m_values;    /* bf16, for dit_adamw_moments, or NULL */
+  void* v_values;
+  int64_t n;         /* elements (>= 0) */
+} dit_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step; /* t of the formulas: 1 for the first step */
+} dit_adamw_args;
+
+int64_t dit_adamw_chunks(const int64_t* sizes, int64_t n_tensors, int32_t* table, int64_t n_chunks);
+dit_status dit_adamw_step(const dit_adamw_tensor* descs_dev, int64_t n_tensors, const int32_t* chunks_dev,
+                          int64_t n_chunks, dit_dtype p_dt, dit_dtype g_dt, int moment_bits,
+                          const dit_adamw_args* args, const float* grad_scale, void* ws,
+                          size_t ws_bytes, dit_stream_t stream);
+dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensors,
+                             const int32_t* chunks_dev, int64_t n_chunks, void* ws, size_t ws_bytes,
+                             dit_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Block-scale tile layout helpers (host).  The scales of a [rows x k] NVFP4 tensor are
  * cut into atoms of 128 rows x 4 scale columns (512 bytes), ordered with the scale-column
  * atom index fastest; inside an atom row r, column c is at (r%32)*16 + ((r%128)/32)*4 +

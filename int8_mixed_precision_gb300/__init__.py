@@ -606,3 +606,22 @@ class DeltaCachedBlock:
         self.tau, self.alpha, self.beta, self.thr = sd["tau"], list(sd["alpha"]), list(sd["beta"]), list(sd["thr"])
         if sd["delta"] is not None:
             self.d[0].copy_(sd["delta"].to(self.d[0].dtype))
+
+
+# ----------------------------------------------------------------------------------------
+# low-rank adapters beside a projection (adapters.py) and the optimiser that trains them
+# (optim.py), imported on first use: they need torch at import, the rest of the binding does not
+# ----------------------------------------------------------------------------------------
+
+_LATER = {**dict.fromkeys(("AdapterPlan", "AdapterBank", "AdaptedLinear", "adapter_scratch", "adapter_saved",
+                           "lora_forward", "lora_backward"), "adapters"),
+          **dict.fromkeys(("AdamW", "adamw_moments"), "optim")}
+
+
+def __getattr__(name):
+    if name not in _LATER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    value = getattr(importlib.import_module("." + _LATER[name], __name__), name)
+    globals()[name] = value
+    return value

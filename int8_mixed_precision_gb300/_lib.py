@@ -52,6 +52,16 @@ SIGNATURES = {
     "dit_shard_finish": (_i32, [_vp, _i32, _vp, _f, _f, _f, _i32, _vp, _vp, _vp, _vp, _vp]),
     "dit_shard_finish_host": (_i32, [ctypes.POINTER(ctypes.c_double), _i32, _f, _f, _f, _f, _i32, _f, _f,
                                      ctypes.POINTER(ctypes.c_int32), _f]),
+    "dit_adapter_plan": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _i64]),
+    "dit_adapter_saved_bytes": (_sz, [_vp, _i32]),
+    "dit_adapter_scratch_bytes": (_sz, [_vp, _i32, _i64, _i64]),
+    "dit_lora_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp, _sz, _vp, _sz, _vp,
+                                _sz, _vp]),
+    "dit_lora_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _sz, _vp, _i32, _vp, _vp,
+                                 _vp, _sz, _vp, _sz, _vp]),
+    "dit_adamw_chunks": (_i64, [_vp, _i64, _vp, _i64]),
+    "dit_adamw_step": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "dit_adamw_moments": (_i32, [_vp, _i64, _vp, _i64, _vp, _sz, _vp]),
     "dit_sf_index": (_i64, [_i64, _i64, _i64, _i64]),
     "dit_sf_bytes": (_sz, [_i64, _i64]),
 }

@@ -1,0 +1,201 @@
+"""Low-rank adapters of many requests beside one shared (frozen, quantised) projection.
+
+``AdapterPlan`` describes a batch (which rows use which adapter), ``AdapterBank`` holds the factors
+of one layer, ``lora_forward`` and ``lora_backward`` are the calls of the C ABI one for one, and
+``AdaptedLinear`` puts them beside a ``RoutedLinear``.  Argument marshalling and host-side checks
+only: the arithmetic runs in the kernels behind ``include/dit6.h``.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ACT_NONE, DitError, _check, _stream, gemm_bf16
+from ._lib import lib
+
+MAX_RANK = 128
+_F32, _BF16 = torch.float32, torch.bfloat16
+_CODE = {_F32: 0, _BF16: 1}
+
+
+class _Plan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("table_ints", ctypes.c_int64), ("n_adapters", ctypes.c_int32),
+                ("training", ctypes.c_int32), ("n_tiles", ctypes.c_int32), ("n_small", ctypes.c_int32)]
+
+
+class AdapterPlan:
+    """The rows of a batch and the adapter of each request.
+
+    lengths: rows of every request, in batch order (0 is allowed).  adapters: the adapter of
+    every request, -1 for none.  Rows past the last request are no part of the plan.  A plan is made
+    once per batch and serves every layer and step; training=True makes one that the backward
+    pass takes too.  The table is laid out on the host and copied to `device` on the current
+    stream: other streams wait for that one before they use the plan."""
+
+    def __init__(self, lengths, adapters, n_adapters: int, training: bool = False, device="cuda"):
+        lengths, adapters = [int(v) for v in lengths], [int(v) for v in adapters]
+        if len(lengths) != len(adapters):
+            raise DitError(f"AdapterPlan: {len(lengths)} lengths and {len(adapters)} adapters")
+        if any(not -2 ** 31 <= g < 2 ** 31 for g in adapters):
+            raise DitError("AdapterPlan: adapter out of range")
+        if any(not 0 <= v < 2 ** 31 for v in lengths):
+            raise DitError("AdapterPlan: length out of range")
+        ln = torch.tensor(lengths, dtype=torch.int64)
+        ad = torch.tensor(adapters, dtype=torch.int32)
+        self.info = _Plan()
+        args = (ln.data_ptr(), ad.data_ptr(), len(lengths), int(n_adapters), int(bool(training)), ctypes.byref(self.info))
+        _check(lib().dit_adapter_plan(*args, None, 0), "dit_adapter_plan")
+        host = torch.empty(self.info.table_ints, dtype=torch.int32)
+        _check(lib().dit_adapter_plan(*args, host.data_ptr(), host.numel()), "dit_adapter_plan")
+        self.table = host.to(device)
+        self.rows, self.n_adapters, self.training = self.info.rows, int(n_adapters), bool(training)
+        self.n_tiles, self.n_small = self.info.n_tiles, self.info.n_small
+        self._info_p, self._table_p = ctypes.addressof(self.info), self.table.data_ptr()
+
+
+class AdapterBank:
+    """The factors of one layer: a [n_adapters, rank, k] and b [n_adapters, n, rank] in bf16, scale
+    [n_adapters] in fp32.  An adapter of a lower rank than the bank's is padded with zeros.  The
+    tensors are the caller's, held and read as they are at each call."""
+
+    def __init__(self, a, b, scale):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise DitError("AdapterBank: a [n_adapters, rank, k] and b [n_adapters, n, rank]")
+        if a.dtype != _BF16 or b.dtype != _BF16 or scale.dtype != _F32:
+            raise DitError("AdapterBank: a and b in bf16, scale in float32")
+        if scale.numel() != a.shape[0]:
+            raise DitError(f"AdapterBank: {scale.numel()} scales for {a.shape[0]} adapters")
+        if any(not t.is_contiguous() for t in (a, b, scale)):
+            raise DitError("buffers must be contiguous")
+        if a.device != b.device or a.device != scale.device:
+            raise DitError("AdapterBank: buffers on different devices")
+        self.n_adapters, self.rank, self.k = a.shape
+        self.n = b.shape[1]
+        if self.n_adapters < 1 or not 8 <= self.rank <= MAX_RANK or self.rank % 8 or self.k % 8 or self.n % 8 or \
+                self.k < 8 or self.n < 8:
+            raise DitError(f"AdapterBank: rank 8 to {MAX_RANK} in steps of 8, k and n multiples of 8")
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self._ptrs = (a.data_ptr(), b.data_ptr(), scale.data_ptr())
+
+
+def adapter_scratch(plan: AdapterPlan, bank: AdapterBank):
+    """Scratch for the calls with this plan and bank; calls ordered on one stream may share it, and
+    one made for a larger layer serves a smaller one."""
+    n = int(lib().dit_adapter_scratch_bytes(plan._info_p, bank.rank, bank.k, bank.n))
+    return torch.empty(n, dtype=torch.uint8, device=bank.device)
+
+
+def adapter_saved(plan: AdapterPlan, bank: AdapterBank):
+    """What the forward pass of one layer keeps for its backward pass."""
+    n = int(lib().dit_adapter_saved_bytes(plan._info_p, bank.rank))
+    return torch.empty(n, dtype=torch.uint8, device=bank.device)
+
+
+def _rows_of(t, plan, width, types, what, device):
+    if t.dim() != 2 or t.shape[1] != width or t.shape[0] < plan.rows:
+        raise DitError(f"{what}: {tuple(t.shape)}, the call needs [{plan.rows}, {width}]")
+    if t.dtype not in types:
+        raise DitError(f"{what}: unsupported dtype {t.dtype}")
+    return _ptr(t, what, device)
+
+
+def _ptr(t, what, device):
+    if not t.is_cuda:
+        raise DitError(f"buffers must be CUDA tensors ({what} is on {t.device})")
+    if t.device != device:
+        raise DitError(f"{what} is on {t.device}, the bank on {device}")
+    if not t.is_contiguous():
+        raise DitError(f"buffers must be contiguous ({what})")
+    return t.data_ptr()
+
+
+def _bytes_of(t, need, what, device):
+    if t is None:
+        return None, 0
+    n = t.numel() * t.element_size()
+    if n < need:
+        raise DitError(f"{what}: {n} bytes, the call needs {need}")
+    return _ptr(t, what, device), n
+
+
+def _agree(plan, bank):
+    if plan.n_adapters != bank.n_adapters:
+        raise DitError(f"the plan is for {plan.n_adapters} adapters, the bank has {bank.n_adapters}")
+    if plan.table.device != bank.device:
+        raise DitError(f"the plan is on {plan.table.device}, the bank on {bank.device}")
+
+
+def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=None, stream=None):
+    """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
+    the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
+    lora_backward needs."""
+    _agree(plan, bank)
+    dev, a = bank.device, bank._ptrs
+    xp = _rows_of(x, plan, bank.k, (_BF16,), "x", dev)
+    yp = _rows_of(y, plan, bank.n, _CODE, "y", dev)
+    if saved is not None and not plan.training:
+        raise DitError("saved needs AdapterPlan(..., training=True)")
+    vp, vn = _bytes_of(saved, 0, "saved", dev)
+    sp, sn = _bytes_of(scratch, 0, "scratch", dev)
+    wp, wn = _bytes_of(ws, 0, "ws", dev)
+    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, a[0], a[1], a[2], bank.rank, bank.k, bank.n, yp,
+                                _CODE[y.dtype], vp, vn, sp, sn, wp, wn, _stream(stream))
+    _check(st, "dit_lora_forward")
+
+
+def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
+    """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
+    wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
+    adapter over all rows that use it.  saved: filled by lora_forward with the same plan, x, a
+    and scale."""
+    _agree(plan, bank)
+    if not plan.training:
+        raise DitError("lora_backward needs AdapterPlan(..., training=True)")
+    dev, a = bank.device, bank._ptrs
+    xp = _rows_of(x, plan, bank.k, (_BF16,), "x", dev)
+    dyp = _rows_of(dy, plan, bank.n, (_BF16,), "dy", dev)
+    dxp = None if dx is None else _rows_of(dx, plan, bank.k, _CODE, "dx", dev)
+    for t, like, what in ((da, bank.a, "da"), (db, bank.b, "db")):
+        if t.dtype != _F32 or t.shape != like.shape:
+            raise DitError(f"{what}: float32 {tuple(like.shape)} is needed")
+    vp, vn = _bytes_of(saved, 0, "saved", dev)
+    sp, sn = _bytes_of(scratch, 0, "scratch", dev)
+    wp, wn = _bytes_of(ws, 0, "ws", dev)
+    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, a[0], a[1], a[2], bank.rank, bank.k, bank.n, vp,
+                                 vn, dxp, 1 if dx is None else _CODE[dx.dtype], _ptr(da, "da", dev), _ptr(db, "db", dev),
+                                 sp, sn, wp, wn, _stream(stream))
+    _check(st, "dit_lora_backward")
+
+
+class AdaptedLinear:
+    """A routed quantised projection with low-rank adapters beside it.
+
+    The frozen weight stays in its quantised forms; the adapters add to its output.  For training,
+    `w_t` (the untransformed weight transposed, bf16 [k, n]) carries the gradient through the
+    frozen projection; without it `backward` gives the adapters' part of dx alone."""
+
+    def __init__(self, linear, bank: AdapterBank, w_t=None):
+        if linear.w.k != bank.k or linear.w.n != bank.n:
+            raise DitError(f"AdaptedLinear: a projection {linear.w.k} -> {linear.w.n} and adapters {bank.k} -> {bank.n}")
+        if w_t is not None and (tuple(w_t.shape) != (bank.k, bank.n) or w_t.dtype != _BF16):
+            raise DitError(f"AdaptedLinear: w_t is bf16 [{bank.k}, {bank.n}]")
+        self.linear, self.bank, self.w_t = linear, bank, w_t
+
+    def __call__(self, x, route, y, plan, scratch, saved=None, bias=None, act=ACT_NONE, stream=None):
+        """y = x W^T (+ bias) along `route`, plus the adapters.  The adapters add to the projection
+        itself, so an activation cannot be fused into it."""
+        if act != ACT_NONE:
+            raise DitError("AdaptedLinear: the activation follows the adapters and cannot be fused into the projection")
+        self.linear(x, route, y, bias=bias, stream=stream)
+        lora_forward(plan, self.bank, x, y, scratch, self.linear.ws, saved=saved, stream=stream)
+        return y
+
+    def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
+        """dx = dy W + the adapters' part; da, db the adapters' gradients."""
+        if self.w_t is None:
+            dx.zero_()
+        else:
+            gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
+        lora_backward(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx=dx, stream=stream)
+        return dx

@@ -51,6 +51,15 @@ __device__ __forceinline__ U8x32 ld256_nc(const void* p) {
                : "l"(p));
   return r;
 }
+// the same through the ordinary path, for memory that the kernel also writes
+__device__ __forceinline__ U8x32 ld256(const void* p) {
+  U8x32 r;
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                 "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p));
+  return r;
+}
 __device__ __forceinline__ void st256(void* p, const U8x32& r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.w[0]),
                "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]),
