@@ -124,6 +124,7 @@ extern "C" size_t dit_adapter_saved_bytes(const dit_adapter_plan_t* plan, int ra
 }
 
 extern "C" size_t dit_adapter_scratch_bytes(const dit_adapter_plan_t* plan, int rank, int64_t k, int64_t n) {
-  if (!dit6::lora::plan_ok(plan) || rank <= 0 || rank > dit6::lora::MAX_RANK || k <= 0 || n <= 0) return 0;
-  return dit6::lora::held_bytes(plan->n_tiles, rank);
+  using namespace dit6::lora;
+  if (!plan_ok(plan) || rank <= 0 || rank > MAX_RANK || k <= 0 || n <= 0 || !plan->n_tiles) return 0;
+  return held_bytes(plan->n_tiles, rank) + slot_bytes(padded_rank(rank), plan->training != 0);
 }

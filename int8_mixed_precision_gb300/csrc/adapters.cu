@@ -2,125 +2,766 @@
 //
 //   h = scale (x A^T),  y += h B^T;   e = scale (dy B),  dx += e A,  dA = e^T x,  dB = dy^T h
 //
-// One product kernel in fp32 on the CUDA cores, 64 x 64 outputs per CTA, in three modes: to the
-// rank (h, e), from the rank (y, dx) and over the rows (dA, dB).
+// Bound by memory: with ranks of 8 to 128 a product does 2 rank operations for each 2-byte element of x, y or
+// dy that it reads, far below what the tensor cores do meanwhile.  So each product streams its wide
+// operand once through shared memory by TMA and runs on tcgen05 with everything of the rank's
+// size on chip.  Three persistent kernels, one CTA per SM:
+//
+//   k_to_rank    h, e: units are (128 rows, 64 columns of x or dy), cut evenly over the SMs
+//   k_from_rank  y, dx: units are (128 rows, up to 256 columns), read, added to and written once
+//   k_over_rows  dA, dB: units are (128 or 256 columns, 128 rows), cut evenly over the SMs; both
+//                gradients in one launch
+//
+// Weights are read as they lie: A [rank x k] and B [n x rank] serve both the product along their
+// rows (K-major operand) and the one across them (MN-major operand), so no transposed copies are kept.
+//
+// The tensor cores' fp32 accumulation truncates (measured: a relative error of 1.1e-9 per
+// element of the contraction, 4.4e-6 over 4096), so sums are drained to registers every CHUNK
+// elements and added there with rounding to nearest.
+//
+// Warps: 0 loads (TMA), 1 issues the MMAs, 2 to 9 drain and store.  Every wait is bounded.
 #include "adapters.cuh"
 
 namespace dit6 {
 namespace lora {
 
-enum Mode { TO_RANK, FROM_RANK, OVER_ROWS };
+constexpr int EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS;
+constexpr int THREADS = 64 + EPI_THREADS;
+constexpr int CHUNK = 512;                  // elements of a contraction between drains
+constexpr int RING_BYTES = 220 * 1024;      // shared memory for operands
+constexpr int SMEM_BYTES = RING_BYTES + 1024 + 512;
+constexpr int MAX_STAGES = 12;
 
 struct Args {
   const int32_t* table;
-  const int32_t* first;
-  int64_t rows;      // of the batch
+  int64_t rows;  // of the batch
   int n_adapters, n_tiles;
-  const __nv_bfloat16* in;  // x or dy [rows x width]
-  const __nv_bfloat16* w;   // A or B; element (rank j, column c) of adapter g at g * wg + j * wj + c * wc
-  int64_t wg, wj, wc;
-  const float* scale;
-  float* held;       // h or e [n_tiles * 128 x rp]
-  void* out;         // y or dx [rows x width] (FROM_RANK), dA or dB (OVER_ROWS, laid out like w)
-  int out_bf16;
   int rank, rp;
-  int64_t width;     // k or n
+  int parts;     // of held that are written (k_to_rank) or read (k_from_rank)
+  int stages;
+  Split split;
   void* ws;
+  int stall;
 };
 
-template <int MODE>
-__global__ void __launch_bounds__(256) k_lora_product(Args p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ float sa[16][65], sb[16][65];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  // the CTA's tile and place: outputs [m0, m0 + 64) x [n0, n0 + 64)
-  const int m0 = MODE == TO_RANK || MODE == FROM_RANK ? (blockIdx.x & 1) * 64 : (int)blockIdx.z * 64;
-  const int64_t n0 = (int64_t)blockIdx.y * 64;
-  int t0, t1, g;
-  if (MODE == OVER_ROWS) {
-    g = blockIdx.x;
-    t0 = p.first[g];
-    t1 = p.first[g + 1];
-    if (t0 < 0 || t1 < t0 || t1 > p.n_tiles) {
-      raise_status(p.ws, DIT_ERR_INVALID_ARG);
-      t0 = t1 = 0;
+// Barriers and flags behind the operands in shared memory.
+struct Control {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t dfull[2], dempty[2];  // accumulators
+  uint64_t hfull, hempty;        // the tile of held (k_from_rank)
+  uint64_t sync;                 // the epilogue warps among themselves
+  uint64_t done;
+  uint32_t tmem;
+  int abort;
+  int last;
+};
+
+struct Frame {
+  uint32_t smem;  // operands, 1024-byte aligned
+  Control* c;
+};
+__device__ __forceinline__ Frame frame(uint8_t* raw) {
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  return Frame{smem_u32(base), reinterpret_cast<Control*>(base + RING_BYTES)};
+}
+__device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols) {
+  Control* c = f.c;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&c->full[s]), 1);
+      mbar_init(smem_u32(&c->empty[s]), 1);
     }
-  } else {
-    t0 = blockIdx.x >> 1;
-    t1 = t0 + 1;
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&c->dfull[b]), 1);
+      mbar_init(smem_u32(&c->dempty[b]), EPI_WARPS);
+    }
+    mbar_init(smem_u32(&c->hfull), 1);
+    mbar_init(smem_u32(&c->hempty), 1);
+    mbar_init(smem_u32(&c->sync), EPI_WARPS);
+    mbar_init(smem_u32(&c->done), 1);
+    c->abort = 0;
+    fence_barrier_init();
   }
-  float acc[4][4] = {};
-  Tile t{0, 0, 0};
-  for (int ti = t0; ti < t1; ++ti) {
-    t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-    if (MODE == OVER_ROWS && t.g != g) continue;
-    const int64_t depth = MODE == TO_RANK ? p.width : MODE == FROM_RANK ? p.rank : t.rows;
-    for (int64_t k0 = 0; k0 < depth; k0 += 16) {
-      for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        // the faster index runs along memory
-        const int kk = MODE == OVER_ROWS ? i / 64 : i % 16, mm = MODE == OVER_ROWS ? i % 64 : i / 16;
-        const int64_t k = k0 + kk;
-        float va = 0.f, vb = 0.f;
-        if (k < depth) {
-          const int m = m0 + mm;
-          const int64_t n = n0 + mm;
-          if (MODE == TO_RANK) {
-            if (m < t.rows) va = __bfloat162float(p.in[((int64_t)t.row0 + m) * p.width + k]);
-            if (n < p.rank) vb = __bfloat162float(p.w[t.g * p.wg + n * p.wj + k * p.wc]);
-          } else if (MODE == FROM_RANK) {
-            if (m < t.rows) va = p.held[((int64_t)ti * TILE_ROWS + m) * p.rp + k];
-            if (n < p.width) vb = __bfloat162float(p.w[t.g * p.wg + k * p.wj + n * p.wc]);
-          } else {
-            if (m < p.rank) va = p.held[((int64_t)ti * TILE_ROWS + k) * p.rp + m];
-            if (n < p.width) vb = __bfloat162float(p.in[((int64_t)t.row0 + k) * p.width + n]);
-          }
-        }
-        sa[kk][mm] = va;
-        sb[kk][mm] = vb;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[kk][ty + 16 * i], sb[kk][tx + 16 * j], acc[i][j]);
-      __syncthreads();
-    }
+  if (threadIdx.x / 32 == 1) {
+    tmem_alloc(smem_u32(&c->tmem), cols);
+    fence_before();
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i;
-      const int64_t n = n0 + tx + 16 * j;
-      if (MODE == TO_RANK) {
-        if (n < p.rp)
-          p.held[((int64_t)t0 * TILE_ROWS + m) * p.rp + n] = m < t.rows && n < p.rank ? acc[i][j] * p.scale[t.g] : 0.f;
-      } else if (MODE == FROM_RANK) {
-        if (m < t.rows && n < p.width) {
-          const int64_t o = ((int64_t)t.row0 + m) * p.width + n;
-          if (p.out_bf16) {
-            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.out);
-            y[o] = __float2bfloat16_rn(__bfloat162float(y[o]) + acc[i][j]);
-          } else {
-            reinterpret_cast<float*>(p.out)[o] += acc[i][j];
-          }
-        }
-      } else if (m < p.rank && n < p.width) {
-        reinterpret_cast<float*>(p.out)[g * p.wg + m * p.wj + n * p.wc] = acc[i][j];
-      }
-    }
+  __syncthreads();
+  fence_after();
+}
+__device__ __forceinline__ void finish(const Frame& f, uint32_t cols) {
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x / 32 == 1) {
+    fence_after();
+    tmem_free(f.c->tmem, cols);
+  }
+}
+// A producer that gave up waits for its own copies in flight; `n` were started.
+__device__ __forceinline__ void await_copies(const Frame& f, int stages, uint32_t n, void* ws) {
+  volatile int never = 0;
+  for (uint32_t i = n > (uint32_t)stages ? n - stages : 0; i < n; ++i)
+    mbar_wait(smem_u32(&f.c->full[i % stages]), (i / stages) & 1, ws, &never);
+}
+// The MMA issuer's end: everything that it issued has completed.
+__device__ __forceinline__ void await_mmas(const Frame& f, void* ws) {
+  volatile int never = 0;
+  mma_commit(smem_u32(&f.c->done));
+  mbar_wait(smem_u32(&f.c->done), 0, ws, &never);
+}
+__device__ __forceinline__ void clear_tickets(void* ws, size_t off) {
+  if (blockIdx.x == 0 && threadIdx.x < MAX_CTAS) ws_u32(ws, off)[threadIdx.x] = 0;
+}
+// The slot of CTA `cta`'s partial result for an output that CTAs c0 and later ones share.
+__device__ __forceinline__ int slot_of(int cta, int c0) { return 2 * cta + (cta == c0 ? 1 : 0); }
+
+// All epilogue warps meet (a bounded wait: one of them may have given up); `turn` counts the meetings.
+__device__ __forceinline__ bool meet(Control* c, uint32_t& turn, void* ws) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&c->sync));
+  return warp_wait(smem_u32(&c->sync), turn++ & 1, ws, &c->abort);
+}
+// Counts this CTA's partial result (written before) in; true in the CTA that counts last.  `ok` falls
+// to false when a wait ran out.
+__device__ __forceinline__ bool count_in(Control* c, uint32_t* ticket, int shares, uint32_t& turn, bool& ok, void* ws) {
+  __threadfence();
+  ok = meet(c, turn, ws);
+  if (!ok) return false;
+  if (threadIdx.x == 64) c->last = atomicAdd(ticket, 1u) == (uint32_t)(shares - 1);
+  ok = meet(c, turn, ws);
+  const bool last = ok && *reinterpret_cast<volatile int*>(&c->last) != 0;
+  if (last) __threadfence();
+  return last;
 }
 
+// A value's parts: each the bf16 nearest to what is left.  An infinite or NaN first part stands alone.
+template <int N>
+__device__ __forceinline__ void split_parts(float v, float (&part)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    part[i] = __bfloat162float(__float2bfloat16_rn(v));
+    v = isfinite(part[i]) ? v - part[i] : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// To the rank: held = scale * (in W^T), in [rows x width] along its rows, W K-major (A) or
+// MN-major (B).
+// ---------------------------------------------------------------------------------------
+struct ToRank {
+  const float* scale;
+  __nv_bfloat16* held;
+  float* slots;
+  int blocks;  // of 64 along the contraction
+};
+
+template <bool MN>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_to_rank(const __grid_constant__ CUtensorMap m_in, const __grid_constant__ CUtensorMap m_w, Args p, ToRank o) {
+  pdl_launch_dependents();
+  extern __shared__ uint8_t raw[];
+  const Frame f = frame(raw);
+  Control* c = f.c;
+  volatile int* abort = &c->abort;
+  constexpr uint32_t COLS = 256;  // two accumulators of up to 128 columns
+  start(f, p.stages, COLS);
+  const uint32_t tmem = c->tmem;
+  pdl_wait();
+  clear_tickets(p.ws, WS_TICKETS_ROWS);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w_chunks = MN ? (p.rank + 63) / 64 : 1;
+  const uint32_t w_bytes = MN ? w_chunks * 8192 : p.rp * 128;
+  const uint32_t stage_bytes = 16384 + w_bytes;
+  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+
+  if (warp == 0) {
+    if (lane == 0 && !p.stall) {
+      prefetch_tmap(&m_in);
+      prefetch_tmap(&m_w);
+      uint32_t n = 0;
+      bool ok = true;
+      Tile t{0, 0, 0};
+      int64_t held_tile = -1;
+      for (int64_t u = u0; u < u1; ++u, ++n) {
+        const int64_t ti = u / o.blocks;
+        const int kb = (int)(u % o.blocks);
+        if (ti != held_tile) t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
+        const int s = n % p.stages;
+        if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
+        mbar_expect_tx(full, stage_bytes);
+        tma_load_2d(dst, &m_in, full, kb * 64, t.row0);
+        if (MN) {
+          for (int i = 0; i < w_chunks; ++i) tma_load_3d(dst + 16384 + i * 8192, &m_w, full, i * 64, kb * 64, t.g);
+        } else {
+          tma_load_3d(dst + 16384, &m_w, full, kb * 64, 0, t.g);
+        }
+      }
+      if (!ok) await_copies(f, p.stages, n, p.ws);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(128, p.rp, false, MN);
+      uint32_t n = 0, chunk = 0;
+      bool ok = true;
+      for (int64_t u = u0; u < u1 && ok;) {
+        const int64_t end = min(u1, (u / o.blocks + 1) * o.blocks);  // of this tile's share
+        for (; u < end && ok; ++chunk) {
+          const int buf = chunk & 1;
+          if (!mbar_wait(smem_u32(&c->dempty[buf]), ((chunk >> 1) & 1) ^ 1, p.ws, abort)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const int64_t stop = min(end, u + CHUNK / 64);
+          for (int64_t first = u; u < stop; ++u, ++n) {
+            const int s = n % p.stages;
+            if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            const uint32_t a = f.smem + s * stage_bytes, b = a + 16384;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma(tmem + buf * 128, desc_k(a + j * 32), MN ? desc_mn(b + j * 2048, 8192) : desc_k(b + j * 32), id,
+                  u > first || j > 0);
+            mma_commit(smem_u32(&c->empty[s]));
+          }
+          if (ok) mma_commit(smem_u32(&c->dfull[buf]));
+        }
+      }
+      await_mmas(f, p.ws);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int row = quarter * 32 + lane;
+    const int nc = p.rp / 2, col0 = half * nc;  // this thread's columns (a multiple of 8)
+    uint32_t chunk = 0, turn = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int64_t ti = u / o.blocks;
+      const int64_t end = min(u1, (ti + 1) * o.blocks);
+      const bool whole = u == ti * o.blocks && end == (ti + 1) * o.blocks;
+      float acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+      for (; u < end; u = min(end, u + CHUNK / 64), ++chunk) {
+        const int buf = chunk & 1;
+        if (!warp_wait(smem_u32(&c->dfull[buf]), (chunk >> 1) & 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 128 + col0;
+        uint32_t r[64];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * i < nc) tmem_ld8(at + 8 * i, r + 8 * i);
+        tmem_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * i < nc) {
+            pin8(r + 8 * i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[8 * i + j] += __uint_as_float(r[8 * i + j]);
+          }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
+      }
+      if (!ok) break;
+      const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
+      if (!whole) {
+        const int c0 = cta_of(p.split, ti * o.blocks), c1 = cta_of(p.split, (ti + 1) * o.blocks - 1);
+        const int64_t at = (int64_t)row * p.rp + col0, slot = (int64_t)TILE_ROWS * p.rp;
+        float* mine = o.slots + slot_of(blockIdx.x, c0) * slot + at;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (4 * i < nc) reinterpret_cast<float4*>(mine)[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        if (!count_in(c, ws_u32(p.ws, WS_TICKETS_RANK) + c0, c1 - c0 + 1, turn, ok, p.ws)) continue;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+        for (int k = c0; k <= c1; ++k) {
+          const float* part = o.slots + slot_of(k, c0) * slot + at;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (4 * i < nc) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(part) + i);
+              acc[4 * i] += v.x;
+              acc[4 * i + 1] += v.y;
+              acc[4 * i + 2] += v.z;
+              acc[4 * i + 3] += v.w;
+            }
+        }
+      }
+      const float scale = o.scale[t.g];
+      __nv_bfloat16* held = o.held + (ti * TILE_ROWS + row) * (int64_t)(p.parts * p.rp) + col0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * i < nc) {
+          uint32_t w[PARTS][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float lo[PARTS], hi[PARTS];
+            const int col = col0 + 8 * i + 2 * j;
+            split_parts(row < t.rows && col < p.rank ? acc[8 * i + 2 * j] * scale : 0.f, lo);
+            split_parts(row < t.rows && col + 1 < p.rank ? acc[8 * i + 2 * j + 1] * scale : 0.f, hi);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) w[q][j] = f2_to_bf16x2(lo[q], hi[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            if (q < p.parts) *reinterpret_cast<uint4*>(held + q * p.rp + 8 * i) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+        }
+    }
+  }
+  finish(f, COLS);
+}
+
+// ---------------------------------------------------------------------------------------
+// From the rank: out += held W, out [rows x width], W = B^T (K-major) or A (MN-major).
+// ---------------------------------------------------------------------------------------
+struct FromRank {
+  void* out;
+  int64_t width;
+  int nb, n_blocks;  // columns of a unit (64, 128 or 256), units along the width
+};
+
+template <bool MN, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w, Args p, FromRank o) {
+  pdl_launch_dependents();
+  extern __shared__ uint8_t raw[];
+  const Frame f = frame(raw);
+  Control* c = f.c;
+  volatile int* abort = &c->abort;
+  constexpr uint32_t COLS = 512;  // two accumulators of up to 256 columns
+  start(f, p.stages, COLS);
+  const uint32_t tmem = c->tmem;
+  pdl_wait();
+  clear_tickets(p.ws, WS_TICKETS_RANK);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int steps = p.parts * p.rp / 16;           // of the contraction
+  const int h_boxes = (p.parts * p.rp + 63) / 64;  // of 128 rows x 64 columns, 16 KB each
+  const int w_boxes = MN ? o.nb / 64 : (p.rank + 63) / 64;
+  const uint32_t box_bytes = MN ? p.rp * 128 : o.nb * 128;
+  const uint32_t w_bytes = w_boxes * box_bytes;
+  const uint32_t ring = f.smem + h_boxes * 16384;
+  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+
+  if (warp == 0) {
+    if (lane == 0 && !p.stall) {
+      prefetch_tmap(&m_held);
+      prefetch_tmap(&m_w);
+      uint32_t n = 0, tiles = 0;
+      bool ok = true;
+      Tile t{0, 0, 0};
+      int64_t held_tile = -1;
+      for (int64_t u = u0; u < u1; ++u, ++n) {
+        const int64_t ti = u / o.n_blocks;
+        const int n0 = (int)(u % o.n_blocks) * o.nb;
+        if (ti != held_tile) {
+          t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
+          if (!mbar_wait(smem_u32(&c->hempty), (tiles & 1) ^ 1, p.ws, abort)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(smem_u32(&c->hfull), h_boxes * 16384);
+          for (int i = 0; i < h_boxes; ++i)
+            tma_load_2d(f.smem + i * 16384, &m_held, smem_u32(&c->hfull), i * 64, (int)(ti * TILE_ROWS));
+          ++tiles;
+        }
+        const int s = n % p.stages;
+        if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = smem_u32(&c->full[s]), dst = ring + s * w_bytes;
+        mbar_expect_tx(full, w_bytes);
+        for (int i = 0; i < w_boxes; ++i) {
+          if (MN)
+            tma_load_3d(dst + i * box_bytes, &m_w, full, n0 + i * 64, 0, t.g);
+          else
+            tma_load_3d(dst + i * box_bytes, &m_w, full, i * 64, n0, t.g);
+        }
+      }
+      if (!ok) {
+        await_copies(f, p.stages, n, p.ws);
+        volatile int never = 0;
+        if (tiles) mbar_wait(smem_u32(&c->hfull), (tiles - 1) & 1, p.ws, &never);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(128, o.nb, false, MN);
+      uint32_t n = 0, tiles = 0;
+      const int rank_steps = p.rp / 16;
+      int64_t held_tile = -1;
+      for (int64_t u = u0; u < u1; ++u, ++n) {
+        const int64_t ti = u / o.n_blocks;
+        const int buf = n & 1, s = n % p.stages;
+        if (ti != held_tile) {
+          held_tile = ti;
+          if (!mbar_wait(smem_u32(&c->hfull), tiles & 1, p.ws, abort)) break;
+          ++tiles;
+        }
+        if (!mbar_wait(smem_u32(&c->dempty[buf]), ((n >> 1) & 1) ^ 1, p.ws, abort)) break;
+        if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
+        fence_after();
+        const uint32_t b = ring + s * w_bytes;
+        for (int q = 0; q < steps; ++q) {
+          const int j = q % rank_steps;  // every part meets the same weights
+          const uint64_t bd = MN ? desc_mn(b + j * 2048, box_bytes) : desc_k(b + (j / 4) * box_bytes + (j % 4) * 32);
+          mma(tmem + buf * 256, desc_k(f.smem + (q / 4) * 16384 + (q % 4) * 32), bd, id, q > 0);
+        }
+        mma_commit(smem_u32(&c->empty[s]));
+        mma_commit(smem_u32(&c->dfull[buf]));
+        if (u + 1 == u1 || (u + 1) / o.n_blocks != ti) mma_commit(smem_u32(&c->hempty));
+      }
+      await_mmas(f, p.ws);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int row = quarter * 32 + lane;
+    const int cols = o.nb / 2;  // this thread's, 32 at a time
+    constexpr int ES = BF16 ? 2 : 4;
+    const bool vec32 = (o.width * ES) % 32 == 0;  // rows begin on 32-byte boundaries (16 otherwise)
+    uint32_t n = 0;
+    Tile t{0, 0, 0};
+    int64_t held_tile = -1;
+    for (int64_t u = u0; u < u1; ++u, ++n) {
+      const int64_t ti = u / o.n_blocks;
+      if (ti != held_tile) t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
+      const int buf = n & 1;
+      const int64_t col0 = (u % o.n_blocks) * o.nb + half * cols;
+      const bool mine = row < t.rows;
+      char* out = reinterpret_cast<char*>(o.out) + (((int64_t)t.row0 + row) * o.width + col0) * ES;
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256 + half * cols;
+      // the old values, up to 128 bytes a thread ahead of the accumulators
+      constexpr int AHEAD = BF16 ? 64 : 32, VECS = AHEAD * ES / 32;
+      bool waited = false, ok = true;
+      for (int c0 = 0; c0 < cols; c0 += AHEAD) {
+        U8x32 old[VECS];
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+          const int64_t col = col0 + c0 + i * (32 / ES);
+          if (!mine || c0 + i * (32 / ES) >= cols) continue;
+          const char* src = out + (int64_t)c0 * ES + i * 32;
+          if (vec32) {
+            if (col < o.width) old[i] = ld256(src);
+          } else {  // 16-byte halves: the width is a multiple of 8 elements
+            if (col < o.width) reinterpret_cast<uint4*>(old[i].w)[0] = *reinterpret_cast<const uint4*>(src);
+            if (col + 16 / ES < o.width) reinterpret_cast<uint4*>(old[i].w)[1] = *reinterpret_cast<const uint4*>(src + 16);
+          }
+        }
+        if (!waited) {
+          if (!warp_wait(smem_u32(&c->dfull[buf]), (n >> 1) & 1, p.ws, abort)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          waited = true;
+        }
+        __syncwarp();
+        uint32_t r[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD / 8; ++i)
+          if (c0 + 8 * i < cols) tmem_ld8(at + c0 + 8 * i, r + 8 * i);
+        tmem_wait();
+#pragma unroll
+        for (int i = 0; i < AHEAD / 8; ++i)
+          if (c0 + 8 * i < cols) pin8(r + 8 * i);
+        if (c0 + AHEAD >= cols) {  // everything is in registers: the accumulator is free
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
+        }
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+          const int64_t col = col0 + c0 + i * (32 / ES);
+          if (!mine || c0 + i * (32 / ES) >= cols || col >= o.width) continue;
+          U8x32 v;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (BF16) {
+              const float2 was = bf16x2_to_f2(old[i].w[j]);
+              v.w[j] = f2_to_bf16x2(was.x + __uint_as_float(r[16 * i + 2 * j]), was.y + __uint_as_float(r[16 * i + 2 * j + 1]));
+            } else {
+              v.w[j] = __float_as_uint(__uint_as_float(old[i].w[j]) + __uint_as_float(r[8 * i + j]));
+            }
+          }
+          char* dst = out + (int64_t)c0 * ES + i * 32;
+          if (vec32) {
+            st256(dst, v);
+          } else {
+            *reinterpret_cast<uint4*>(dst) = reinterpret_cast<const uint4*>(v.w)[0];
+            if (col + 16 / ES < o.width) *reinterpret_cast<uint4*>(dst + 16) = reinterpret_cast<const uint4*>(v.w)[1];
+          }
+        }
+      }
+      if (!ok) break;
+    }
+  }
+  finish(f, COLS);
+}
+
+// ---------------------------------------------------------------------------------------
+// Over the rows: dA[g] = e^T x and dB[g] = dy^T h over the rows of every adapter g.
+// ---------------------------------------------------------------------------------------
+struct Grad {
+  const __nv_bfloat16* held;
+  float* out;
+  int64_t width;
+  int64_t blocks;  // of the output, along the width
+  int64_t rank_stride, col_stride;  // of the output; one of them is 1
+};
+struct OverRows {
+  Grad g[2];       // dA, dB
+  const int32_t* first;
+  float* slots;
+  int mtiles;
+};
+
+// A unit of k_over_rows: its output tile (problem, adapter, columns) and tile of rows.
+struct RowsUnit {
+  bool ok;
+  int problem, g;
+  int64_t block;       // of columns
+  int64_t tile;        // of the plan
+  int64_t first, count;  // first unit and units of the output tile
+};
+__device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, int64_t u) {
+  RowsUnit r;
+  const int64_t units0 = o.g[0].blocks * p.n_tiles;
+  r.problem = u >= units0;
+  const int64_t base = r.problem ? units0 : 0, v = u - base, blocks = o.g[r.problem].blocks;
+  // An adapter's units follow one another and its tiles are [f0, f1): v / blocks is one of its tiles.
+  r.g = p.table[4 * (v / blocks) + 2];
+  r.ok = r.g >= 0 && r.g < p.n_adapters;
+  if (!r.ok) return r;
+  const int64_t f0 = o.first[r.g], f1 = o.first[r.g + 1];
+  r.ok = f0 >= 0 && f0 <= v / blocks && v / blocks < f1 && f1 <= p.n_tiles;
+  if (!r.ok) return r;
+  r.count = f1 - f0;
+  r.block = (v - blocks * f0) / r.count;
+  r.first = base + blocks * f0 + r.block * r.count;
+  r.tile = f0 + (u - r.first);
+  return r;
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    k_over_rows(const __grid_constant__ CUtensorMap m_x, const __grid_constant__ CUtensorMap m_e,
+                const __grid_constant__ CUtensorMap m_dy, const __grid_constant__ CUtensorMap m_h, Args p, OverRows o) {
+  pdl_launch_dependents();
+  extern __shared__ uint8_t raw[];
+  const Frame f = frame(raw);
+  Control* c = f.c;
+  volatile int* abort = &c->abort;
+  constexpr uint32_t COLS = 512;
+  start(f, p.stages, COLS);
+  const uint32_t tmem = c->tmem;
+  pdl_wait();
+  clear_tickets(p.ws, WS_TICKETS_RANK);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_all = PARTS * p.rp;  // accumulator columns of one M tile
+  const int a_boxes = 2 * o.mtiles, b_boxes = (n_all + 63) / 64;
+  const uint32_t stage_bytes = (a_boxes + b_boxes) * 8192;  // 64 rows
+  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+
+  if (warp == 0) {
+    if (lane == 0 && !p.stall) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t u = u0; u < u1 && ok; ++u) {
+        const RowsUnit r = rows_unit(p, o, u);
+        if (!r.ok) {
+          raise_status(p.ws, DIT_ERR_INVALID_ARG);
+          continue;
+        }
+        const Tile t = load_tile(p.table, r.tile, p.rows, p.n_adapters, p.ws);
+        for (int h = 0; h < 2; ++h, ++n) {
+          const int s = n % p.stages;
+          if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
+          mbar_expect_tx(full, stage_bytes);
+          for (int i = 0; i < a_boxes; ++i)
+            tma_load_2d(dst + i * 8192, r.problem ? &m_dy : &m_x, full, (int)((r.block * a_boxes + i) * 64), t.row0 + 64 * h);
+          for (int i = 0; i < b_boxes; ++i)
+            tma_load_2d(dst + (a_boxes + i) * 8192, r.problem ? &m_h : &m_e, full, i * 64, (int)(r.tile * TILE_ROWS + 64 * h));
+        }
+      }
+      if (!ok) await_copies(f, p.stages, n, p.ws);
+    }
+  } else if (warp == 1) {
+    const int n_one = min(n_all, 256), n_two = n_all - n_one;  // one instruction has at most 256 columns
+    const uint32_t id_one = idesc(128, n_one, true, true), id_two = idesc(128, n_two, true, true);
+    uint32_t n = 0, chunk = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      RowsUnit r = rows_unit(p, o, u);
+      if (!r.ok) {
+        ++u;
+        continue;
+      }
+      const int64_t end = min(u1, r.first + r.count);
+      for (; u < end && ok; ++chunk) {
+        if (!warp_wait(smem_u32(&c->dempty[0]), (chunk & 1) ^ 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const int64_t stop = min(end, u + CHUNK / TILE_ROWS);
+        for (int64_t first = u; u < stop && ok; ++u) {
+          const Tile t = load_tile(p.table, r.tile + (u - first), p.rows, p.n_adapters, p.ws);
+          for (int h = 0; h < 2; ++h, ++n) {
+            const int s = n % p.stages;
+            if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+              ok = false;
+              break;
+            }
+            const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * 8192;
+            const int valid = min(64, max(0, t.rows - 64 * h));
+            if (valid < 64) {
+              // rows of other requests behind the tile's own: zeros, so that what they hold stays out
+              for (int i = valid * 8 + lane; i < 64 * 8; i += 32)
+                for (int q = 0; q < a_boxes; ++q)
+                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a + q * 8192 + i * 16), "r"(0) : "memory");
+              fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) {
+              fence_after();
+              for (int mt = 0; mt < o.mtiles; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint64_t ad = desc_mn(a + mt * 16384 + j * 2048, 8192);
+                  const bool add = u > first || h > 0 || j > 0;
+                  mma(tmem + mt * n_all, ad, desc_mn(b + j * 2048, 8192), id_one, add);
+                  if (n_two) mma(tmem + mt * n_all + 256, ad, desc_mn(b + 4 * 8192 + j * 2048, 8192), id_two, add);
+                }
+              mma_commit(smem_u32(&c->empty[s]));
+            }
+            __syncwarp();
+          }
+        }
+        r.tile += CHUNK / TILE_ROWS;
+        if (ok && lane == 0) mma_commit(smem_u32(&c->dfull[0]));
+      }
+    }
+    if (lane == 0) await_mmas(f, p.ws);
+    __syncwarp();
+  } else {
+    // Two M tiles: a warp group each, all columns of the rank; one: a half of the columns each.
+    const int quarter = warp & 3, group = (warp - 2) >> 2;
+    const int mt = o.mtiles == 2 ? group : 0;
+    const int nc = o.mtiles == 2 ? p.rp : p.rp / 2, col0 = o.mtiles == 2 ? 0 : group * nc;
+    const int m = mt * 128 + quarter * 32 + lane;  // column of x or dy within the output tile
+    const int m_all = o.mtiles * 128;
+    uint32_t chunk = 0, turn = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const RowsUnit r = rows_unit(p, o, u);
+      if (!r.ok) {
+        ++u;
+        continue;
+      }
+      const int64_t end = min(u1, r.first + r.count);
+      const bool whole = u == r.first && end == r.first + r.count;
+      float acc[80];
+#pragma unroll
+      for (int i = 0; i < 80; ++i) acc[i] = 0.f;
+      for (; u < end; u = min(end, u + CHUNK / TILE_ROWS), ++chunk) {
+        if (!warp_wait(smem_u32(&c->dfull[0]), chunk & 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + mt * n_all + col0;
+#pragma unroll
+        for (int i = 0; i < 10; ++i)
+          if (8 * i < nc) {
+            uint32_t v[PARTS][8];
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) tmem_ld8(at + q * p.rp + 8 * i, v[q]);
+            tmem_wait();
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) pin8(v[q]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // the small parts first
+              acc[8 * i + j] += __uint_as_float(v[0][j]) + (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+          }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c->dempty[0]));
+      }
+      if (!ok) break;
+      if (!whole) {
+        const int c0 = cta_of(p.split, r.first), c1 = cta_of(p.split, r.first + r.count - 1);
+        const int64_t slot = (int64_t)m_all * p.rp;
+        float* mine = o.slots + slot_of(blockIdx.x, c0) * slot + (int64_t)col0 * m_all + m;
+#pragma unroll
+        for (int i = 0; i < 80; ++i)
+          if (i < nc) mine[(int64_t)i * m_all] = acc[i];
+        if (!count_in(c, ws_u32(p.ws, WS_TICKETS_ROWS) + c0, c1 - c0 + 1, turn, ok, p.ws)) continue;
+#pragma unroll
+        for (int i = 0; i < 80; ++i) acc[i] = 0.f;
+        for (int k = c0; k <= c1; ++k) {
+          const float* part = o.slots + slot_of(k, c0) * slot + (int64_t)col0 * m_all + m;
+#pragma unroll
+          for (int i = 0; i < 80; ++i)
+            if (i < nc) acc[i] += __ldcg(part + (int64_t)i * m_all);
+        }
+      }
+      const Grad& g = o.g[r.problem];
+      const int64_t col = r.block * m_all + m;
+      if (col < g.width) {
+        float* out = g.out + (int64_t)r.g * p.rank * g.width + col * g.col_stride + col0 * g.rank_stride;
+#pragma unroll
+        for (int i = 0; i < 80; ++i)
+          if (i < nc && col0 + i < p.rank) out[i * g.rank_stride] = acc[i];
+      }
+    }
+  }
+  // adapters without rows
+  for (int g = blockIdx.x; g < p.n_adapters; g += gridDim.x) {
+    if (o.first[g] != o.first[g + 1]) continue;
+    for (int q = 0; q < 2; ++q) {
+      float4* out = reinterpret_cast<float4*>(o.g[q].out + (int64_t)g * p.rank * o.g[q].width);
+      for (int64_t i = threadIdx.x; i < p.rank * o.g[q].width / 4; i += THREADS) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  finish(f, COLS);
+}
+
+// ---------------------------------------------------------------------------------------
 // A small tile: up to 16 rows anywhere in the batch; one CTA, h in shared memory.
-__global__ void __launch_bounds__(256) k_lora_small(Args p, const int32_t* small, int64_t k, const __nv_bfloat16* b) {
+// ---------------------------------------------------------------------------------------
+struct Small {
+  const int32_t* small;
+  const __nv_bfloat16 *x, *a, *b;
+  const float* scale;
+  void* y;
+  int y_bf16;
+  int64_t k, n;
+};
+__global__ void __launch_bounds__(256) k_small(Args p, Small o) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float h[SMALL_ROWS][MAX_RANK];
   __shared__ int rows[SMALL_ROWS];
-  const int32_t* s = small + (int64_t)blockIdx.x * SMALL_INTS;
+  const int32_t* s = o.small + (int64_t)blockIdx.x * SMALL_INTS;
   const int g = s[0], count = s[1];
   bool bad = g < 0 || g >= p.n_adapters || count < 0 || count > SMALL_ROWS;
   for (int i = 0; i < count && !bad; ++i) bad = s[4 + i] < 0 || s[4 + i] >= p.rows;
@@ -131,37 +772,105 @@ __global__ void __launch_bounds__(256) k_lora_small(Args p, const int32_t* small
   if (threadIdx.x < count) rows[threadIdx.x] = s[4 + threadIdx.x];
   __syncthreads();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int o = warp; o < count * p.rank; o += 8) {
-    const int i = o / p.rank, j = o % p.rank;
-    const __nv_bfloat16* xr = p.in + (int64_t)rows[i] * k;
-    const __nv_bfloat16* ar = p.w + g * p.wg + j * p.wj;
+  for (int i = warp; i < count * p.rank; i += 8) {
+    const int row = i / p.rank, j = i % p.rank;
+    const __nv_bfloat16* xr = o.x + (int64_t)rows[row] * o.k;
+    const __nv_bfloat16* ar = o.a + ((int64_t)g * p.rank + j) * o.k;
     float v = 0.f;
-    for (int64_t c = lane; c < k; c += 32) v = fmaf(__bfloat162float(xr[c]), __bfloat162float(ar[c]), v);
+    for (int64_t c = lane; c < o.k; c += 32) v = fmaf(__bfloat162float(xr[c]), __bfloat162float(ar[c]), v);
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0) h[i][j] = v * p.scale[g];
+    if (lane == 0) h[row][j] = v * o.scale[g];
   }
   __syncthreads();
-  for (int64_t c = threadIdx.x; c < p.width; c += 256)
+  for (int64_t c = threadIdx.x; c < o.n; c += 256)
     for (int i = 0; i < count; ++i) {
       float v = 0.f;
-      for (int j = 0; j < p.rank; ++j) v = fmaf(h[i][j], __bfloat162float(b[((int64_t)g * p.width + c) * p.rank + j]), v);
-      const int64_t o = (int64_t)rows[i] * p.width + c;
-      if (p.out_bf16) {
-        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.out);
-        y[o] = __float2bfloat16_rn(__bfloat162float(y[o]) + v);
+      for (int j = 0; j < p.rank; ++j) v = fmaf(h[i][j], __bfloat162float(o.b[((int64_t)g * o.n + c) * p.rank + j]), v);
+      const int64_t at = (int64_t)rows[i] * o.n + c;
+      if (o.y_bf16) {
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(o.y);
+        y[at] = __float2bfloat16_rn(__bfloat162float(y[at]) + v);
       } else {
-        reinterpret_cast<float*>(p.out)[o] += v;
+        reinterpret_cast<float*>(o.y)[at] += v;
       }
     }
 }
 
-template <int MODE>
-static dit_status product(const Args& a, cudaStream_t st) {
-  if (MODE != OVER_ROWS && a.n_tiles == 0) return DIT_OK;
-  const int64_t cols = MODE == TO_RANK ? a.rp : a.width;
-  dim3 grid(MODE == OVER_ROWS ? a.n_adapters : 2 * a.n_tiles, (unsigned)((cols + 63) / 64),
-            MODE == OVER_ROWS ? (a.rank + 63) / 64 : 1);
-  return launch_pdl(k_lora_product<MODE>, grid, dim3(256), 0, st, 1, a) == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+// ---------------------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------------------
+static Args args_of(const dit_adapter_plan_t& plan, const int32_t* table, int rank, void* ws) {
+  Args p = {};
+  p.table = table;
+  p.rows = plan.rows;
+  p.n_adapters = plan.n_adapters;
+  p.n_tiles = plan.n_tiles;
+  p.rank = rank;
+  p.rp = padded_rank(rank);
+  p.ws = ws;
+  p.stall = test_stall();
+  return p;
+}
+static int stages_for(uint32_t room, uint32_t stage_bytes) {
+  const uint32_t s = room / stage_bytes;
+  return (int)(s < (uint32_t)MAX_STAGES ? s : (uint32_t)MAX_STAGES);
+}
+template <auto KERN>
+static bool allow_smem() {
+  static const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  return e == cudaSuccess;
+}
+static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t rows, uint32_t box_rows) {
+  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void*>(base), (uint64_t)width, (uint64_t)rows,
+                        (uint64_t)width * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
+template <bool MN>
+static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, const float* scale, void* held, int parts,
+                          void* slots, cudaStream_t st) {
+  if (!p.n_tiles) return DIT_OK;
+  CUtensorMap m_in, m_w;
+  const bool maps = map_rows(&m_in, in, width, p.rows, TILE_ROWS) &&
+                    (MN ? encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, 64)
+                        : encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp));
+  if (!maps || !allow_smem<k_to_rank<MN>>()) return DIT_ERR_CUDA;
+  ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64)};
+  p.parts = parts;
+  p.stages = stages_for(RING_BYTES, 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128));
+  p.split = split_units((int64_t)p.n_tiles * o.blocks, 2, num_sms());
+  return launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) == cudaSuccess
+             ? DIT_OK
+             : DIT_ERR_CUDA;
+}
+
+// out += held W; MN: w is [n_adapters][rank][width], else [n_adapters][width][rank]; held has `held_parts` parts
+template <bool MN, bool BF16>
+static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, cudaStream_t st) {
+  if (!p.n_tiles) return DIT_OK;
+  FromRank o{out, width, 256, 0};
+  // narrower units where wide ones would leave SMs without work
+  while (o.nb > 64 && (int64_t)p.n_tiles * ((width + o.nb - 1) / o.nb) < num_sms()) o.nb /= 2;
+  o.n_blocks = (int)((width + o.nb - 1) / o.nb);
+  p.parts = BF16 ? 2 : PARTS;
+  CUtensorMap m_held, m_w;
+  const bool maps = map_rows(&m_held, held, held_parts * p.rp, (int64_t)p.n_tiles * TILE_ROWS, TILE_ROWS) &&
+                    (MN ? encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp)
+                        : encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, o.nb));
+  if (!maps || !allow_smem<k_from_rank<MN, BF16>>()) return DIT_ERR_CUDA;
+  const uint32_t w_bytes = MN ? o.nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * o.nb * 128;
+  p.stages = stages_for(RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384, w_bytes);
+  p.split = split_units((int64_t)p.n_tiles * o.n_blocks, 1, num_sms());
+  return launch_pdl(k_from_rank<MN, BF16>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_held, m_w, p, o) ==
+                 cudaSuccess
+             ? DIT_OK
+             : DIT_ERR_CUDA;
+}
+template <bool MN>
+static dit_status from_rank(const Args& p, const void* held, int held_parts, const void* w, void* out, dit_dtype dt,
+                            int64_t width, cudaStream_t st) {
+  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, st)
+                        : from_rank<MN, false>(p, held, held_parts, w, out, width, st);
 }
 
 }  // namespace lora
@@ -180,38 +889,16 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   if (saved && (!plan->training || saved_bytes < held_bytes(plan->n_tiles, rank))) return DIT_ERR_INVALID_ARG;
   if (!aligned32(y) || !aligned32(saved)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Args p = {};
-  p.table = table;
-  p.first = table + off_first(*plan);
-  p.rows = plan->rows;
-  p.n_adapters = plan->n_adapters;
-  p.n_tiles = plan->n_tiles;
-  p.scale = scale;
-  p.held = reinterpret_cast<float*>(saved ? saved : scratch);
-  p.rank = rank;
-  p.rp = padded_rank(rank);
-  p.ws = ws;
-  p.out = y;
-  p.out_bf16 = y_dt == DIT_BF16;
-  p.in = reinterpret_cast<const __nv_bfloat16*>(x);
-  p.w = reinterpret_cast<const __nv_bfloat16*>(a);
-  p.wg = rank * k;
-  p.wj = k;
-  p.wc = 1;
-  p.width = k;
-  dit_status s = product<TO_RANK>(p, st);
-  Args q = p;
-  q.w = reinterpret_cast<const __nv_bfloat16*>(b);
-  q.wg = rank * n;
-  q.wj = 1;
-  q.wc = rank;
-  q.width = n;
-  if (s == DIT_OK) s = product<FROM_RANK>(q, st);
+  const Args p = args_of(*plan, table, rank, ws);
+  void* held = saved ? saved : scratch;
+  char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
+  const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
+  dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
+  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, st);
   if (s == DIT_OK && plan->n_small) {
-    p.width = n;
-    if (launch_pdl(k_lora_small, dim3(plan->n_small), dim3(256), 0, st, 1, p, table + off_small(*plan), k,
-                   reinterpret_cast<const __nv_bfloat16*>(b)) != cudaSuccess)
-      s = DIT_ERR_CUDA;
+    Small o{table + off_small(*plan), reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a),
+            reinterpret_cast<const __nv_bfloat16*>(b), scale, y, y_dt == DIT_BF16, k, n};
+    if (launch_pdl(k_small, dim3(plan->n_small), dim3(256), 0, st, 1, p, o) != cudaSuccess) s = DIT_ERR_CUDA;
   }
   return s;
 }
@@ -228,38 +915,33 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
     return DIT_ERR_INVALID_ARG;
   if (!aligned32(dy) || !aligned32(saved) || !aligned32(dx) || !aligned32(da) || !aligned32(db)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Args p = {};
-  p.table = table;
-  p.first = table + off_first(*plan);
-  p.rows = plan->rows;
-  p.n_adapters = plan->n_adapters;
-  p.n_tiles = plan->n_tiles;
-  p.scale = scale;
-  p.held = reinterpret_cast<float*>(scratch);
-  p.rank = rank;
-  p.rp = padded_rank(rank);
-  p.ws = ws;
-  Args along_n = p, along_k = p;
-  along_n.in = reinterpret_cast<const __nv_bfloat16*>(dy);
-  along_n.w = reinterpret_cast<const __nv_bfloat16*>(b);
-  along_n.wg = rank * n;
-  along_n.wj = 1;
-  along_n.wc = rank;
-  along_n.width = n;
-  along_k.in = reinterpret_cast<const __nv_bfloat16*>(x);
-  along_k.w = reinterpret_cast<const __nv_bfloat16*>(a);
-  along_k.wg = rank * k;
-  along_k.wj = k;
-  along_k.wc = 1;
-  along_k.width = k;
-  dit_status s = product<TO_RANK>(along_n, st);
-  along_k.out = dx;
-  along_k.out_bf16 = dx_dt == DIT_BF16;
-  if (s == DIT_OK && dx) s = product<FROM_RANK>(along_k, st);
-  along_k.out = da;
-  if (s == DIT_OK) s = product<OVER_ROWS>(along_k, st);
-  along_n.out = db;
-  along_n.held = reinterpret_cast<float*>(const_cast<void*>(saved));
-  if (s == DIT_OK) s = product<OVER_ROWS>(along_n, st);
-  return s;
+  Args p = args_of(*plan, table, rank, ws);
+  char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
+  if (!plan->n_tiles) {  // no row has an adapter: every gradient is zero
+    const bool ok = cudaMemsetAsync(da, 0, (size_t)plan->n_adapters * rank * k * 4, st) == cudaSuccess &&
+                    cudaMemsetAsync(db, 0, (size_t)plan->n_adapters * rank * n * 4, st) == cudaSuccess;
+    return ok ? DIT_OK : DIT_ERR_CUDA;
+  }
+  dit_status s = to_rank<true>(p, dy, n, b, scale, scratch, PARTS, slots, st);
+  if (s == DIT_OK && dx) s = from_rank<true>(p, scratch, PARTS, a, dx, dx_dt, k, st);
+  if (s != DIT_OK) return s;
+
+  const int mtiles = grad_mtiles(p.rp), m_all = 128 * mtiles;
+  OverRows o{};
+  o.g[0] = Grad{reinterpret_cast<const __nv_bfloat16*>(scratch), da, k, (k + m_all - 1) / m_all, k, 1};
+  o.g[1] = Grad{reinterpret_cast<const __nv_bfloat16*>(saved), db, n, (n + m_all - 1) / m_all, 1, rank};
+  o.first = table + off_first(*plan);
+  o.slots = reinterpret_cast<float*>(slots);
+  o.mtiles = mtiles;
+  CUtensorMap m_x, m_e, m_dy, m_h;
+  const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
+  if (!map_rows(&m_x, x, k, p.rows, 64) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, 64) ||
+      !map_rows(&m_dy, dy, n, p.rows, 64) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, 64) || !allow_smem<k_over_rows>())
+    return DIT_ERR_CUDA;
+  p.stages = stages_for(RING_BYTES, (2 * mtiles + (PARTS * p.rp + 63) / 64) * 8192);
+  p.split = split_units((o.g[0].blocks + o.g[1].blocks) * p.n_tiles, 1, num_sms());
+  return launch_pdl(k_over_rows, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) ==
+                 cudaSuccess
+             ? DIT_OK
+             : DIT_ERR_CUDA;
 }

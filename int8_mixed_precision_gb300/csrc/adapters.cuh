@@ -1,4 +1,5 @@
-// What the files of the low-rank adapters share: the plan's table and the buffers' layout.
+// What the files of the low-rank adapters share: the plan's table, the buffers' layout, how work is
+// cut over CTAs, and the tensor-core instructions of one CTA.
 #pragma once
 
 #include "common.cuh"
@@ -12,7 +13,8 @@ constexpr int SMALL_INTS = 4 + SMALL_ROWS;
 constexpr int SMALL_RUN = 32;            // serving: a run of up to this many rows goes to small tiles
 constexpr int MAX_RANK = 128;
 constexpr int64_t MAX_ROWS = 0x7fffff00;
-constexpr int64_t MAX_TILES = 1 << 26;
+constexpr int64_t MAX_TILES = 1 << 23;   // 2^30 rows of h: a tensor map's extents stay below 2^32
+constexpr int MAX_CTAS = 160;            // of the persistent kernels (GB300 has 152 SMs)
 
 // The table: n_tiles x {first row, rows, adapter, 0}; n_adapters + 1 indices of each adapter's
 // first tile (tiles are in the adapters' order); from a multiple of 4 on, n_small x {adapter,
@@ -20,16 +22,52 @@ constexpr int64_t MAX_TILES = 1 << 26;
 inline int64_t off_first(const dit_adapter_plan_t& p) { return 4 * (int64_t)p.n_tiles; }
 inline int64_t off_small(const dit_adapter_plan_t& p) { return (off_first(p) + p.n_adapters + 1 + 3) / 4 * 4; }
 
-// h and e: for each 128-row tile of the plan, 128 rows of rank values (the rank rounded up to
-// 16), rows past the tile's own zero.
+// h and e ("held"): for each tile of the plan 128 rows (those past the tile's own are zeros) of
+// PARTS x rp bf16 (rp: the rank rounded up to 16; columns past the rank are zeros).  A value is held
+// as the sum of its parts, each the bf16 nearest to what the earlier ones leave: two parts
+// carry 16 significant bits, which a bf16 output cannot tell from fp32, three carry 24, for
+// the gradients and for fp32 outputs.  All parts are operands of the bf16 tensor pipe, whose
+// products of two bf16 values are exact.
+constexpr int PARTS = 3;
 inline int padded_rank(int rank) { return (rank + 15) / 16 * 16; }
-inline size_t held_bytes(int64_t n_tiles, int rank) { return (size_t)n_tiles * TILE_ROWS * padded_rank(rank) * 4; }
+inline size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
+inline size_t held_bytes(int64_t n_tiles, int rank) {
+  return round_256((size_t)n_tiles * TILE_ROWS * padded_rank(rank) * 2 * PARTS);
+}
+
+// Work is a list of `units` that `ctas` CTAs take in contiguous, equal shares; an output whose
+// units fall to several CTAs is summed from their partial results by the last one to finish, in
+// the order of the CTAs, so the sum does not depend on which one that is.  A CTA has at most
+// two shared outputs (its first and its last), hence two slots for partial results.
+struct Split {
+  int64_t units;
+  int ctas;
+};
+inline Split split_units(int64_t units, int64_t least_per_cta, int sms) {
+  int64_t c = units / least_per_cta;
+  if (c < 1) c = 1;
+  if (c > sms) c = sms;
+  if (c > MAX_CTAS) c = MAX_CTAS;
+  return Split{units, (int)c};
+}
+__host__ __device__ __forceinline__ int64_t first_unit(const Split& s, int cta) { return s.units * cta / s.ctas; }
+__host__ __device__ __forceinline__ int cta_of(const Split& s, int64_t unit) {
+  return (int)(((unit + 1) * s.ctas - 1) / s.units);
+}
+
+// The columns of x or dy that one output tile of a weight gradient covers: two instructions' M of 128,
+// or one where the accumulators of two (PARTS x rp columns each) exceed the 512 of tensor memory.
+inline int grad_mtiles(int rp) { return 2 * PARTS * rp <= 512 ? 2 : 1; }
+
+inline size_t slot_bytes(int rp, bool training) {
+  return (size_t)2 * MAX_CTAS * TILE_ROWS * (training ? grad_mtiles(rp) : 1) * rp * 4;
+}
 
 struct Tile {
   int row0, rows, g;
 };
 // A tile of the table; one outside the batch or the bank has no rows and raises the status word.
-__device__ __forceinline__ Tile load_tile(const int32_t* table, int t, int64_t rows, int n_adapters, void* ws) {
+__device__ __forceinline__ Tile load_tile(const int32_t* table, int64_t t, int64_t rows, int n_adapters, void* ws) {
   const int4 v = reinterpret_cast<const int4*>(table)[t];
   Tile o{v.x, v.y, v.z};
   if (o.row0 < 0 || o.rows <= 0 || o.rows > TILE_ROWS || (int64_t)o.row0 + o.rows > rows || o.g < 0 || o.g >= n_adapters) {
@@ -39,10 +77,73 @@ __device__ __forceinline__ Tile load_tile(const int32_t* table, int t, int64_t r
   return o;
 }
 
+// Completion counters of shared outputs, in the workspace: a call's first kernel leaves those of the
+// later ones at zero and the other way round, so that they are zero again even after a wait
+// that ran out.
+constexpr size_t WS_TICKETS_RANK = 33280;                            // products to the rank
+constexpr size_t WS_TICKETS_ROWS = WS_TICKETS_RANK + 4 * MAX_CTAS;   // products over the rows
+static_assert(WS_TICKETS_RANK >= WS_PARTIALS + 32 * MAX_RED_CTAS && WS_TICKETS_ROWS + 4 * MAX_CTAS <= WS_BYTES, "");
+
 bool plan_ok(const dit_adapter_plan_t* p);
 dit_status check_common(const dit_adapter_plan_t* plan, const int32_t* table, const void* x, const void* a,
                         const void* b, const float* scale, int rank, int64_t k, int64_t n, const void* scratch,
                         size_t scratch_bytes, const void* ws, size_t ws_bytes);
+
+// ---------------------------------------------------------------------------------------
+// tcgen05 of one CTA: operands in 128-byte swizzled shared memory, bf16 x bf16 -> fp32
+// ---------------------------------------------------------------------------------------
+// Rows of 64 bf16 along the contraction (K-major): 8-row groups of 1024 bytes; a step of 16 along
+// the contraction is 32 bytes.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// Rows of 64 bf16 along M or N, one for each index of the contraction (MN-major): 8-row groups of
+// 1024 bytes, the next 64 of M or N `chunk` bytes on; a step of 16 along the contraction is
+// 16 rows, 2048 bytes.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(chunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// arrives on `bar` when every MMA issued so far by this thread has completed
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// eight accumulator columns of this thread's row; complete after tmem_wait()
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// keeps uses of eight loaded columns behind the wait
+__device__ __forceinline__ void pin8(uint32_t* r) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+// A bounded wait of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, void* ws, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ws, abort));
+}
 
 }  // namespace lora
 }  // namespace dit6
