@@ -29,8 +29,10 @@ constexpr int EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS;
 constexpr int THREADS = 64 + EPI_THREADS;
 constexpr int CHUNK = 512;                  // elements of a contraction between drains
 constexpr int RING_BYTES = 220 * 1024;      // shared memory for operands
-constexpr int SMEM_BYTES = RING_BYTES + 1024 + 512;
+constexpr int SMEM_BYTES = RING_BYTES + 1024 + 1024;
 constexpr int MAX_STAGES = 12;
+constexpr int MAX_PANELS = 8;               // k_from_rank: 128 rows x 128 bytes of the output each
+constexpr int ACCS = 4;                     // accumulators in turn (two in k_to_rank, one in k_over_rows)
 
 struct Args {
   const int32_t* table;
@@ -47,14 +49,17 @@ struct Args {
 // Barriers and flags behind the operands in shared memory.
 struct Control {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-  uint64_t dfull[2], dempty[2];  // accumulators
-  uint64_t hfull, hempty;        // the tile of held (k_from_rank)
-  uint64_t sync;                 // the epilogue warps among themselves
+  uint64_t dfull[ACCS], dempty[ACCS];  // accumulators
+  uint64_t hfull, hempty;              // the tile of held (k_from_rank)
+  uint64_t yfull[MAX_PANELS], ydone[MAX_PANELS], yempty[MAX_PANELS];  // panels of the output: loaded, updated, stored
+  uint64_t sync;                       // the epilogue warps among themselves
   uint64_t done;
   uint32_t tmem;
   int abort;
   int last;
 };
+
+static_assert(sizeof(Control) <= 1024, "");
 
 struct Frame {
   uint32_t smem;  // operands, 1024-byte aligned
@@ -71,9 +76,14 @@ __device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols)
       mbar_init(smem_u32(&c->full[s]), 1);
       mbar_init(smem_u32(&c->empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < ACCS; ++b) {
       mbar_init(smem_u32(&c->dfull[b]), 1);
       mbar_init(smem_u32(&c->dempty[b]), EPI_WARPS);
+    }
+    for (int b = 0; b < MAX_PANELS; ++b) {
+      mbar_init(smem_u32(&c->yfull[b]), 1);
+      mbar_init(smem_u32(&c->ydone[b]), EPI_WARPS);
+      mbar_init(smem_u32(&c->yempty[b]), 1);
     }
     mbar_init(smem_u32(&c->hfull), 1);
     mbar_init(smem_u32(&c->hempty), 1);
@@ -182,13 +192,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t n = 0;
       bool ok = true;
       Tile t{0, 0, 0};
-      int64_t held_tile = -1;
+      int64_t ti = u0 / o.blocks;
+      int kb = (int)(u0 % o.blocks), s = 0;
+      uint32_t parity = 1;
       for (int64_t u = u0; u < u1; ++u, ++n) {
-        const int64_t ti = u / o.blocks;
-        const int kb = (int)(u % o.blocks);
-        if (ti != held_tile) t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
-        const int s = n % p.stages;
-        if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+        if (u == u0 || kb == 0) t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
+        if (!mbar_wait(smem_u32(&c->empty[s]), parity, p.ws, abort)) {
           ok = false;
           break;
         }
@@ -200,13 +209,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           tma_load_3d(dst + 16384, &m_w, full, kb * 64, 0, t.g);
         }
+        if (++kb == o.blocks) {
+          kb = 0;
+          ++ti;
+        }
+        if (++s == p.stages) {
+          s = 0;
+          parity ^= 1;
+        }
       }
       if (!ok) await_copies(f, p.stages, n, p.ws);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t id = idesc(128, p.rp, false, MN);
-      uint32_t n = 0, chunk = 0;
+      uint32_t chunk = 0, parity = 0;
+      int s = 0;
       bool ok = true;
       for (int64_t u = u0; u < u1 && ok;) {
         const int64_t end = min(u1, (u / o.blocks + 1) * o.blocks);  // of this tile's share
@@ -218,9 +236,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           fence_after();
           const int64_t stop = min(end, u + CHUNK / 64);
-          for (int64_t first = u; u < stop; ++u, ++n) {
-            const int s = n % p.stages;
-            if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+          for (int64_t first = u; u < stop; ++u) {
+            if (!mbar_wait(smem_u32(&c->full[s]), parity, p.ws, abort)) {
               ok = false;
               break;
             }
@@ -231,6 +248,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               mma(tmem + buf * 128, desc_k(a + j * 32), MN ? desc_mn(b + j * 2048, 8192) : desc_k(b + j * 32), id,
                   u > first || j > 0);
             mma_commit(smem_u32(&c->empty[s]));
+            if (++s == p.stages) {
+              s = 0;
+              parity ^= 1;
+            }
           }
           if (ok) mma_commit(smem_u32(&c->dfull[buf]));
         }
@@ -326,22 +347,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ---------------------------------------------------------------------------------------
 // From the rank: out += held W, out [rows x width], W = B^T (K-major) or A (MN-major).
+//
+// The tile of held stays in shared memory for all its units; weights come through a ring, and so do
+// the output's panels (128 rows x 128 bytes): loaded by TMA well ahead of the accumulators,
+// updated in place and stored by TMA, so that neither direction waits for the other.  With a row
+// to each thread, loads and stores straight to global memory took one wavefront per 32 bytes
+// and the kernel ran at 3.6 TB/s, bound by them.  Panels of a tile that ends inside them are
+// stored row by row, so that rows of other requests are never written.
 // ---------------------------------------------------------------------------------------
 struct FromRank {
   void* out;
   int64_t width;
-  int nb, n_blocks;  // columns of a unit (64, 128 or 256), units along the width
+  int nb, n_blocks;  // columns of a unit (64 or 128), units along the width
+  int panels;        // of the ring
 };
 
+constexpr int FROM_THREADS = THREADS + 32;  // and a warp that stores
+
 template <bool MN, bool BF16>
-__global__ void __launch_bounds__(THREADS, 1)
-    k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w, Args p, FromRank o) {
+__global__ void __launch_bounds__(FROM_THREADS, 1)
+    k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w,
+                const __grid_constant__ CUtensorMap m_out, Args p, FromRank o) {
   pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
   volatile int* abort = &c->abort;
-  constexpr uint32_t COLS = 512;  // two accumulators of up to 256 columns
+  constexpr uint32_t COLS = 512;  // four accumulators of up to 128 columns
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
@@ -353,22 +385,26 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int w_boxes = MN ? o.nb / 64 : (p.rank + 63) / 64;
   const uint32_t box_bytes = MN ? p.rp * 128 : o.nb * 128;
   const uint32_t w_bytes = w_boxes * box_bytes;
-  const uint32_t ring = f.smem + h_boxes * 16384;
+  const uint32_t ring = f.smem + h_boxes * 16384, panels = ring + p.stages * w_bytes;
+  constexpr int ES = BF16 ? 2 : 4, PC = 128 / ES;  // columns of a panel
   const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+  int64_t ti = u0 / o.n_blocks;
+  int block = (int)(u0 % o.n_blocks);
+  // panels of the block (the last one may have fewer)
+  auto panels_of = [&](int b) { return (int)min((int64_t)o.nb / PC, (o.width - (int64_t)b * o.nb + PC - 1) / PC); };
 
   if (warp == 0) {
     if (lane == 0 && !p.stall) {
       prefetch_tmap(&m_held);
       prefetch_tmap(&m_w);
-      uint32_t n = 0, tiles = 0;
+      prefetch_tmap(&m_out);
+      uint32_t n = 0, tiles = 0, np = 0;
       bool ok = true;
       Tile t{0, 0, 0};
-      int64_t held_tile = -1;
-      for (int64_t u = u0; u < u1; ++u, ++n) {
-        const int64_t ti = u / o.n_blocks;
-        const int n0 = (int)(u % o.n_blocks) * o.nb;
-        if (ti != held_tile) {
-          t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
+      for (int64_t u = u0; u < u1 && ok; ++u) {
+        const int n0 = block * o.nb;
+        if (u == u0 || block == 0) {
+          t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
           if (!mbar_wait(smem_u32(&c->hempty), (tiles & 1) ^ 1, p.ws, abort)) {
             ok = false;
             break;
@@ -391,11 +427,27 @@ __global__ void __launch_bounds__(THREADS, 1)
           else
             tma_load_3d(dst + i * box_bytes, &m_w, full, i * 64, n0, t.g);
         }
+        ++n;
+        for (int i = 0, all = panels_of(block); i < all; ++i, ++np) {
+          const int q = np % o.panels;
+          if (!mbar_wait(smem_u32(&c->yempty[q]), ((np / o.panels) & 1) ^ 1, p.ws, abort)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
+          tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
+        }
+        if (++block == o.n_blocks) {
+          block = 0;
+          ++ti;
+        }
       }
       if (!ok) {
         await_copies(f, p.stages, n, p.ws);
         volatile int never = 0;
         if (tiles) mbar_wait(smem_u32(&c->hfull), (tiles - 1) & 1, p.ws, &never);
+        for (uint32_t i = np > (uint32_t)o.panels ? np - o.panels : 0; i < np; ++i)
+          mbar_wait(smem_u32(&c->yfull[i % o.panels]), (i / o.panels) & 1, p.ws, &never);
       }
     }
   } else if (warp == 1) {
@@ -403,112 +455,129 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t id = idesc(128, o.nb, false, MN);
       uint32_t n = 0, tiles = 0;
       const int rank_steps = p.rp / 16;
-      int64_t held_tile = -1;
       for (int64_t u = u0; u < u1; ++u, ++n) {
-        const int64_t ti = u / o.n_blocks;
-        const int buf = n & 1, s = n % p.stages;
-        if (ti != held_tile) {
-          held_tile = ti;
+        const int buf = n % ACCS, s = n % p.stages;
+        if (u == u0 || block == 0) {
           if (!mbar_wait(smem_u32(&c->hfull), tiles & 1, p.ws, abort)) break;
           ++tiles;
         }
-        if (!mbar_wait(smem_u32(&c->dempty[buf]), ((n >> 1) & 1) ^ 1, p.ws, abort)) break;
+        if (++block == o.n_blocks) block = 0;
+        if (!mbar_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort)) break;
         if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
         fence_after();
         const uint32_t b = ring + s * w_bytes;
-        for (int q = 0; q < steps; ++q) {
-          const int j = q % rank_steps;  // every part meets the same weights
+        int j = 0;
+        for (int q = 0; q < steps; ++q) {  // every part meets the same weights
           const uint64_t bd = MN ? desc_mn(b + j * 2048, box_bytes) : desc_k(b + (j / 4) * box_bytes + (j % 4) * 32);
-          mma(tmem + buf * 256, desc_k(f.smem + (q / 4) * 16384 + (q % 4) * 32), bd, id, q > 0);
+          mma(tmem + buf * 128, desc_k(f.smem + (q / 4) * 16384 + (q % 4) * 32), bd, id, q > 0);
+          if (++j == rank_steps) j = 0;
         }
         mma_commit(smem_u32(&c->empty[s]));
         mma_commit(smem_u32(&c->dfull[buf]));
-        if (u + 1 == u1 || (u + 1) / o.n_blocks != ti) mma_commit(smem_u32(&c->hempty));
+        if (block == 0) mma_commit(smem_u32(&c->hempty));
       }
       await_mmas(f, p.ws);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 2 + EPI_WARPS) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;
-    const int cols = o.nb / 2;  // this thread's, 32 at a time
-    constexpr int ES = BF16 ? 2 : 4;
-    const bool vec32 = (o.width * ES) % 32 == 0;  // rows begin on 32-byte boundaries (16 otherwise)
-    uint32_t n = 0;
-    Tile t{0, 0, 0};
-    int64_t held_tile = -1;
-    for (int64_t u = u0; u < u1; ++u, ++n) {
-      const int64_t ti = u / o.n_blocks;
-      if (ti != held_tile) t = load_tile(p.table, held_tile = ti, p.rows, p.n_adapters, p.ws);
-      const int buf = n & 1;
-      const int64_t col0 = (u % o.n_blocks) * o.nb + half * cols;
-      const bool mine = row < t.rows;
-      char* out = reinterpret_cast<char*>(o.out) + (((int64_t)t.row0 + row) * o.width + col0) * ES;
-      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256 + half * cols;
-      // the old values, up to 128 bytes a thread ahead of the accumulators
-      constexpr int AHEAD = BF16 ? 64 : 32, VECS = AHEAD * ES / 32;
-      bool waited = false, ok = true;
-      for (int c0 = 0; c0 < cols; c0 += AHEAD) {
-        U8x32 old[VECS];
+    uint32_t n = 0, np = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
+      const int buf = n % ACCS, all = panels_of(block);
+      if (++block == o.n_blocks) block = 0;
+      if (!warp_wait(smem_u32(&c->dfull[buf]), (n / ACCS) & 1, p.ws, abort)) break;
+      fence_after();
+      for (int i = 0; i < all; ++i, ++np) {
+        constexpr int MINE = PC / 2;  // this thread's columns of the panel
+        const int q = np % o.panels;
+        uint32_t r[MINE];
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 128 + i * PC + half * MINE;
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-          const int64_t col = col0 + c0 + i * (32 / ES);
-          if (!mine || c0 + i * (32 / ES) >= cols) continue;
-          const char* src = out + (int64_t)c0 * ES + i * 32;
-          if (vec32) {
-            if (col < o.width) old[i] = ld256(src);
-          } else {  // 16-byte halves: the width is a multiple of 8 elements
-            if (col < o.width) reinterpret_cast<uint4*>(old[i].w)[0] = *reinterpret_cast<const uint4*>(src);
-            if (col + 16 / ES < o.width) reinterpret_cast<uint4*>(old[i].w)[1] = *reinterpret_cast<const uint4*>(src + 16);
-          }
+        for (int j = 0; j < MINE / 8; ++j) tmem_ld8(at + 8 * j, r + 8 * j);
+        if (!warp_wait(smem_u32(&c->yfull[q]), (np / o.panels) & 1, p.ws, abort)) {
+          ok = false;
+          break;
         }
-        if (!waited) {
-          if (!warp_wait(smem_u32(&c->dfull[buf]), (n >> 1) & 1, p.ws, abort)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          waited = true;
-        }
-        __syncwarp();
-        uint32_t r[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD / 8; ++i)
-          if (c0 + 8 * i < cols) tmem_ld8(at + c0 + 8 * i, r + 8 * i);
         tmem_wait();
 #pragma unroll
-        for (int i = 0; i < AHEAD / 8; ++i)
-          if (c0 + 8 * i < cols) pin8(r + 8 * i);
-        if (c0 + AHEAD >= cols) {  // everything is in registers: the accumulator is free
+        for (int j = 0; j < MINE / 8; ++j) pin8(r + 8 * j);
+        if (i == all - 1) {  // everything is in registers: the accumulator is free
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
         }
+        const uint32_t line = panels + q * 16384 + row * 128;
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-          const int64_t col = col0 + c0 + i * (32 / ES);
-          if (!mine || c0 + i * (32 / ES) >= cols || col >= o.width) continue;
-          U8x32 v;
+        for (int j = 0; j < 4; ++j) {  // 16-byte pieces of the row, swizzled as TMA lays them
+          const uint32_t addr = line + (((half * 4 + j) ^ (row & 7)) << 4);
+          uint4 v = lds128(addr);
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int k = 0; k < 4; ++k) {
             if (BF16) {
-              const float2 was = bf16x2_to_f2(old[i].w[j]);
-              v.w[j] = f2_to_bf16x2(was.x + __uint_as_float(r[16 * i + 2 * j]), was.y + __uint_as_float(r[16 * i + 2 * j + 1]));
+              const float2 was = bf16x2_to_f2(w[k]);
+              w[k] = f2_to_bf16x2(was.x + __uint_as_float(r[8 * j + 2 * k]), was.y + __uint_as_float(r[8 * j + 2 * k + 1]));
             } else {
-              v.w[j] = __float_as_uint(__uint_as_float(old[i].w[j]) + __uint_as_float(r[8 * i + j]));
+              w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(r[4 * j + k]));
             }
           }
-          char* dst = out + (int64_t)c0 * ES + i * 32;
-          if (vec32) {
-            st256(dst, v);
-          } else {
-            *reinterpret_cast<uint4*>(dst) = reinterpret_cast<const uint4*>(v.w)[0];
-            if (col + 16 / ES < o.width) *reinterpret_cast<uint4*>(dst + 16) = reinterpret_cast<const uint4*>(v.w)[1];
+          sts128(addr, v);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c->ydone[q]));
+      }
+    }
+  } else {
+    uint32_t np = 0;
+    bool ok = true;
+    Tile t{0, 0, 0};
+    int pending = -1;  // the panel that the last TMA store reads
+    for (int64_t u = u0; u < u1 && ok; ++u) {
+      if (u == u0 || block == 0) t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
+      for (int i = 0, all = panels_of(block); i < all; ++i, ++np) {
+        const int q = np % o.panels;
+        if (!warp_wait(smem_u32(&c->ydone[q]), (np / o.panels) & 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        const int64_t col = (int64_t)block * o.nb + i * PC;
+        const uint32_t src = panels + q * 16384;
+        const bool whole = t.rows == TILE_ROWS;
+        if (whole) {
+          if (lane == 0) {
+            tma_store_2d(&m_out, src, (int)col, t.row0);
+            if (pending >= 0) {
+              tma_store_read_wait<1>();
+              mbar_arrive(smem_u32(&c->yempty[pending]));
+            }
           }
+          pending = q;
+        } else {
+          const int piece = lane & 7;
+          char* out = reinterpret_cast<char*>(o.out) + ((int64_t)t.row0 * o.width + col) * ES + piece * 16;
+          if (col + piece * (16 / ES) < o.width)
+            for (int r = lane >> 3; r < t.rows; r += 4)
+              *reinterpret_cast<uint4*>(out + (int64_t)r * o.width * ES) = lds128(src + r * 128 + ((piece ^ (r & 7)) << 4));
+          __syncwarp();
+          if (lane == 0) {
+            if (pending >= 0) {
+              tma_store_read_wait<0>();
+              mbar_arrive(smem_u32(&c->yempty[pending]));
+            }
+            mbar_arrive(smem_u32(&c->yempty[q]));
+          }
+          pending = -1;
         }
       }
-      if (!ok) break;
+      if (++block == o.n_blocks) {
+        block = 0;
+        ++ti;
+      }
     }
+    if (lane == 0) tma_store_wait();
   }
   finish(f, COLS);
 }
@@ -848,21 +917,28 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
-  FromRank o{out, width, 256, 0};
+  FromRank o{out, width, 128, 0, 0};
   // narrower units where wide ones would leave SMs without work
-  while (o.nb > 64 && (int64_t)p.n_tiles * ((width + o.nb - 1) / o.nb) < num_sms()) o.nb /= 2;
+  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms()) o.nb = 64;
   o.n_blocks = (int)((width + o.nb - 1) / o.nb);
   p.parts = BF16 ? 2 : PARTS;
-  CUtensorMap m_held, m_w;
-  const bool maps = map_rows(&m_held, held, held_parts * p.rp, (int64_t)p.n_tiles * TILE_ROWS, TILE_ROWS) &&
+  CUtensorMap m_held, m_w, m_out;
+  const bool maps = encode_tmap_2d(&m_out, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
+                                   (uint64_t)width, (uint64_t)p.rows, (uint64_t)width * (BF16 ? 2 : 4), BF16 ? 64 : 32,
+                                   TILE_ROWS, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                    map_rows(&m_held, held, held_parts * p.rp, (int64_t)p.n_tiles * TILE_ROWS, TILE_ROWS) &&
                     (MN ? encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp)
                         : encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, o.nb));
   if (!maps || !allow_smem<k_from_rank<MN, BF16>>()) return DIT_ERR_CUDA;
   const uint32_t w_bytes = MN ? o.nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * o.nb * 128;
-  p.stages = stages_for(RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384, w_bytes);
+  const uint32_t room = RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384;
+  p.stages = 2;
+  while (p.stages < 4 && room - (p.stages + 1) * w_bytes >= MAX_PANELS * 16384) ++p.stages;
+  o.panels = (int)((room - p.stages * w_bytes) / 16384);
+  if (o.panels > MAX_PANELS) o.panels = MAX_PANELS;
   p.split = split_units((int64_t)p.n_tiles * o.n_blocks, 1, num_sms());
-  return launch_pdl(k_from_rank<MN, BF16>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_held, m_w, p, o) ==
-                 cudaSuccess
+  return launch_pdl(k_from_rank<MN, BF16>, dim3(p.split.ctas), dim3(FROM_THREADS), SMEM_BYTES, st, 1, m_held, m_w, m_out, p,
+                    o) == cudaSuccess
              ? DIT_OK
              : DIT_ERR_CUDA;
 }
