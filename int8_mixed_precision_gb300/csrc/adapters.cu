@@ -57,6 +57,7 @@ struct Control {
   uint32_t tmem;
   int abort;
   int last;
+  int valid[MAX_STAGES];               // rows of a stage that belong to its tile (k_over_rows)
 };
 
 static_assert(sizeof(Control) <= 1024, "");
@@ -308,16 +309,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!count_in(c, ws_u32(p.ws, WS_TICKETS_RANK) + c0, c1 - c0 + 1, turn, ok, p.ws)) continue;
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-        for (int k = c0; k <= c1; ++k) {
-          const float* part = o.slots + slot_of(k, c0) * slot + at;
+        for (int k = c0; k <= c1; k += 4) {  // the loads of four CTAs' partial results at a time
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (4 * i < nc) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(part) + i);
-              acc[4 * i] += v.x;
-              acc[4 * i + 1] += v.y;
-              acc[4 * i + 2] += v.z;
-              acc[4 * i + 3] += v.w;
+              float4 v[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                v[h] = k + h <= c1 ? __ldcg(reinterpret_cast<const float4*>(o.slots + slot_of(k + h, c0) * slot + at) + i)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                acc[4 * i] += v[h].x;
+                acc[4 * i + 1] += v[h].y;
+                acc[4 * i + 2] += v[h].z;
+                acc[4 * i + 3] += v[h].w;
+              }
             }
         }
       }
@@ -596,7 +603,7 @@ struct OverRows {
   Grad g[2];       // dA, dB
   const int32_t* first;
   float* slots;
-  int mtiles;
+  int mtiles, accs;  // 128 columns each, and accumulators in turn
 };
 
 // A unit of k_over_rows: its output tile (problem, adapter, columns) and tile of rows.
@@ -650,25 +657,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0 && !p.stall) {
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t u = u0; u < u1 && ok; ++u) {
+      for (int64_t u = u0; u < u1 && ok;) {
         const RowsUnit r = rows_unit(p, o, u);
         if (!r.ok) {
           raise_status(p.ws, DIT_ERR_INVALID_ARG);
+          ++u;
           continue;
         }
-        const Tile t = load_tile(p.table, r.tile, p.rows, p.n_adapters, p.ws);
-        for (int h = 0; h < 2; ++h, ++n) {
-          const int s = n % p.stages;
-          if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
-            ok = false;
-            break;
+        const int64_t end = min(u1, r.first + r.count);
+        const int4* entry = reinterpret_cast<const int4*>(p.table) + r.tile;
+        const int col = (int)(r.block * a_boxes * 64);
+        int held_row = (int)(r.tile * TILE_ROWS);
+        int4 next = *entry;
+        for (; u < end && ok; ++u) {
+          const Tile t = check_tile(next, p.rows, p.n_adapters, p.ws);
+          if (u + 1 < end) next = *++entry;  // used a tile later
+          for (int h = 0; h < 2; ++h, ++n, held_row += 64) {
+            const int s = n % p.stages;
+            if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+              ok = false;
+              break;
+            }
+            const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
+            c->valid[s] = min(64, max(0, t.rows - 64 * h));
+            mbar_expect_tx(full, stage_bytes);
+            for (int i = 0; i < a_boxes; ++i)
+              tma_load_2d(dst + i * 8192, r.problem ? &m_dy : &m_x, full, col + i * 64, t.row0 + 64 * h);
+            for (int i = 0; i < b_boxes; ++i)
+              tma_load_2d(dst + (a_boxes + i) * 8192, r.problem ? &m_h : &m_e, full, i * 64, held_row);
           }
-          const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
-          mbar_expect_tx(full, stage_bytes);
-          for (int i = 0; i < a_boxes; ++i)
-            tma_load_2d(dst + i * 8192, r.problem ? &m_dy : &m_x, full, (int)((r.block * a_boxes + i) * 64), t.row0 + 64 * h);
-          for (int i = 0; i < b_boxes; ++i)
-            tma_load_2d(dst + (a_boxes + i) * 8192, r.problem ? &m_h : &m_e, full, i * 64, (int)(r.tile * TILE_ROWS + 64 * h));
         }
       }
       if (!ok) await_copies(f, p.stages, n, p.ws);
@@ -679,54 +696,51 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t n = 0, chunk = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
-      RowsUnit r = rows_unit(p, o, u);
+      const RowsUnit r = rows_unit(p, o, u);
       if (!r.ok) {
         ++u;
         continue;
       }
       const int64_t end = min(u1, r.first + r.count);
       for (; u < end && ok; ++chunk) {
-        if (!warp_wait(smem_u32(&c->dempty[0]), (chunk & 1) ^ 1, p.ws, abort)) {
+        const uint32_t buf = chunk % o.accs, d = tmem + buf * o.mtiles * n_all;
+        if (!warp_wait(smem_u32(&c->dempty[buf]), ((chunk / o.accs) & 1) ^ 1, p.ws, abort)) {
           ok = false;
           break;
         }
         fence_after();
-        const int64_t stop = min(end, u + CHUNK / TILE_ROWS);
-        for (int64_t first = u; u < stop && ok; ++u) {
-          const Tile t = load_tile(p.table, r.tile + (u - first), p.rows, p.n_adapters, p.ws);
-          for (int h = 0; h < 2; ++h, ++n) {
-            const int s = n % p.stages;
-            if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
-              ok = false;
-              break;
-            }
-            const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * 8192;
-            const int valid = min(64, max(0, t.rows - 64 * h));
-            if (valid < 64) {
-              // rows of other requests behind the tile's own: zeros, so that what they hold stays out
-              for (int i = valid * 8 + lane; i < 64 * 8; i += 32)
-                for (int q = 0; q < a_boxes; ++q)
-                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a + q * 8192 + i * 16), "r"(0) : "memory");
-              fence_proxy_async();
-            }
-            __syncwarp();
-            if (lane == 0) {
-              fence_after();
-              for (int mt = 0; mt < o.mtiles; ++mt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint64_t ad = desc_mn(a + mt * 16384 + j * 2048, 8192);
-                  const bool add = u > first || h > 0 || j > 0;
-                  mma(tmem + mt * n_all, ad, desc_mn(b + j * 2048, 8192), id_one, add);
-                  if (n_two) mma(tmem + mt * n_all + 256, ad, desc_mn(b + 4 * 8192 + j * 2048, 8192), id_two, add);
-                }
-              mma_commit(smem_u32(&c->empty[s]));
-            }
-            __syncwarp();
+        const int stop = 2 * (int)(min(end, u + CHUNK / TILE_ROWS) - u);
+        for (int i = 0; i < stop; ++i, ++n) {
+          const int s = n % p.stages;
+          if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+            ok = false;
+            break;
           }
+          const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * 8192;
+          const int valid = c->valid[s];
+          if (valid < 64) {
+            // rows of other requests behind the tile's own: zeros, so that what they hold stays out
+            for (int k = valid * 8 + lane; k < 64 * 8; k += 32)
+              for (int q = 0; q < a_boxes; ++q) sts128(a + q * 8192 + k * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            fence_after();
+            for (int mt = 0; mt < o.mtiles; ++mt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint64_t ad = desc_mn(a + mt * 16384 + j * 2048, 8192);
+                const bool add = i > 0 || j > 0;
+                mma(d + mt * n_all, ad, desc_mn(b + j * 2048, 8192), id_one, add);
+                if (n_two) mma(d + mt * n_all + 256, ad, desc_mn(b + 4 * 8192 + j * 2048, 8192), id_two, add);
+              }
+            mma_commit(smem_u32(&c->empty[s]));
+          }
+          __syncwarp();
         }
-        r.tile += CHUNK / TILE_ROWS;
-        if (ok && lane == 0) mma_commit(smem_u32(&c->dfull[0]));
+        u += stop / 2;
+        if (ok && lane == 0) mma_commit(smem_u32(&c->dfull[buf]));
       }
     }
     if (lane == 0) await_mmas(f, p.ws);
@@ -752,12 +766,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 80; ++i) acc[i] = 0.f;
       for (; u < end; u = min(end, u + CHUNK / TILE_ROWS), ++chunk) {
-        if (!warp_wait(smem_u32(&c->dfull[0]), chunk & 1, p.ws, abort)) {
+        const uint32_t buf = chunk % o.accs;
+        if (!warp_wait(smem_u32(&c->dfull[buf]), (chunk / o.accs) & 1, p.ws, abort)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + mt * n_all + col0;
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf * o.mtiles + mt) * n_all + col0;
 #pragma unroll
         for (int i = 0; i < 10; ++i)
           if (8 * i < nc) {
@@ -773,7 +788,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c->dempty[0]));
+        if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
       }
       if (!ok) break;
       if (!whole) {
@@ -789,8 +804,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int k = c0; k <= c1; ++k) {
           const float* part = o.slots + slot_of(k, c0) * slot + (int64_t)col0 * m_all + m;
 #pragma unroll
-          for (int i = 0; i < 80; ++i)
-            if (i < nc) acc[i] += __ldcg(part + (int64_t)i * m_all);
+          for (int i = 0; i < 80; i += 16)
+            if (i < nc) {  // nc is a multiple of 8
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = i + j < nc ? __ldcg(part + (int64_t)(i + j) * m_all) : 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[i + j] += v[j];
+            }
         }
       }
       const Grad& g = o.g[r.problem];
@@ -894,6 +915,15 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
                         (uint64_t)width * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Whole tiles to each CTA, or equal shares: a share that ends inside a tile costs its CTA about as
+// much as SHARED units (a partial result written, counted in, read back and summed).
+static Split split_to_rank(int64_t tiles, int64_t blocks) {
+  constexpr int64_t SHARED = 8, LEAST = 4;
+  const int64_t sms = num_sms(), whole = (tiles + sms - 1) / sms * blocks;
+  const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
+  return whole <= (s.units + s.ctas - 1) / s.ctas + SHARED ? split_units(s.units, blocks, blocks, (int)sms) : s;
+}
+
 // held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
 template <bool MN>
 static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, const float* scale, void* held, int parts,
@@ -907,7 +937,7 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64)};
   p.parts = parts;
   p.stages = stages_for(RING_BYTES, 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128));
-  p.split = split_units((int64_t)p.n_tiles * o.blocks, 2, num_sms());
+  p.split = split_to_rank(p.n_tiles, o.blocks);
   return launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) == cudaSuccess
              ? DIT_OK
              : DIT_ERR_CUDA;
@@ -918,10 +948,12 @@ template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
   FromRank o{out, width, 128, 0, 0};
-  // narrower units where wide ones would leave SMs without work
-  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms()) o.nb = 64;
-  o.n_blocks = (int)((width + o.nb - 1) / o.nb);
   p.parts = BF16 ? 2 : PARTS;
+  const uint32_t room = RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384;
+  auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
+  // narrower units where wide ones would leave SMs without work, or the panels without room
+  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms() || room < 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
+  o.n_blocks = (int)((width + o.nb - 1) / o.nb);
   CUtensorMap m_held, m_w, m_out;
   const bool maps = encode_tmap_2d(&m_out, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
                                    (uint64_t)width, (uint64_t)p.rows, (uint64_t)width * (BF16 ? 2 : 4), BF16 ? 64 : 32,
@@ -930,13 +962,12 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
                     (MN ? encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp)
                         : encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, o.nb));
   if (!maps || !allow_smem<k_from_rank<MN, BF16>>()) return DIT_ERR_CUDA;
-  const uint32_t w_bytes = MN ? o.nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * o.nb * 128;
-  const uint32_t room = RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384;
+  const uint32_t w_bytes = bytes_of(o.nb);
   p.stages = 2;
   while (p.stages < 4 && room - (p.stages + 1) * w_bytes >= MAX_PANELS * 16384) ++p.stages;
   o.panels = (int)((room - p.stages * w_bytes) / 16384);
   if (o.panels > MAX_PANELS) o.panels = MAX_PANELS;
-  p.split = split_units((int64_t)p.n_tiles * o.n_blocks, 1, num_sms());
+  p.split = split_units((int64_t)p.n_tiles * o.n_blocks, 1, 1, num_sms());
   return launch_pdl(k_from_rank<MN, BF16>, dim3(p.split.ctas), dim3(FROM_THREADS), SMEM_BYTES, st, 1, m_held, m_w, m_out, p,
                     o) == cudaSuccess
              ? DIT_OK
@@ -1009,13 +1040,14 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   o.first = table + off_first(*plan);
   o.slots = reinterpret_cast<float*>(slots);
   o.mtiles = mtiles;
+  o.accs = 2 * mtiles * PARTS * p.rp <= 512 ? 2 : 1;
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, 64) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, 64) ||
       !map_rows(&m_dy, dy, n, p.rows, 64) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, 64) || !allow_smem<k_over_rows>())
     return DIT_ERR_CUDA;
   p.stages = stages_for(RING_BYTES, (2 * mtiles + (PARTS * p.rp + 63) / 64) * 8192);
-  p.split = split_units((o.g[0].blocks + o.g[1].blocks) * p.n_tiles, 1, num_sms());
+  p.split = split_units((o.g[0].blocks + o.g[1].blocks) * p.n_tiles, 1, 1, num_sms());
   return launch_pdl(k_over_rows, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) ==
                  cudaSuccess
              ? DIT_OK

@@ -35,24 +35,28 @@ inline size_t held_bytes(int64_t n_tiles, int rank) {
   return round_256((size_t)n_tiles * TILE_ROWS * padded_rank(rank) * 2 * PARTS);
 }
 
-// Work is a list of `units` that `ctas` CTAs take in contiguous, equal shares; an output whose
-// units fall to several CTAs is summed from their partial results by the last one to finish, in
-// the order of the CTAs, so the sum does not depend on which one that is.  A CTA has at most
-// two shared outputs (its first and its last), hence two slots for partial results.
+// Work is a list of `units` that `ctas` CTAs take in contiguous shares of equal numbers of grains
+// (`grain` units each); an output whose units fall to several CTAs is summed from their partial
+// results by the last one to finish, in the order of the CTAs, so the sum does not depend on
+// which one that is.  A CTA has at most two shared outputs (its first and its last), hence two
+// slots for partial results.
 struct Split {
-  int64_t units;
+  int64_t units, grain;
   int ctas;
 };
-inline Split split_units(int64_t units, int64_t least_per_cta, int sms) {
+inline Split split_units(int64_t units, int64_t grain, int64_t least_per_cta, int sms) {
   int64_t c = units / least_per_cta;
   if (c < 1) c = 1;
+  if (c > units / grain) c = units / grain;
   if (c > sms) c = sms;
   if (c > MAX_CTAS) c = MAX_CTAS;
-  return Split{units, (int)c};
+  return Split{units, grain, (int)c};
 }
-__host__ __device__ __forceinline__ int64_t first_unit(const Split& s, int cta) { return s.units * cta / s.ctas; }
+__host__ __device__ __forceinline__ int64_t first_unit(const Split& s, int cta) {
+  return s.units / s.grain * cta / s.ctas * s.grain;
+}
 __host__ __device__ __forceinline__ int cta_of(const Split& s, int64_t unit) {
-  return (int)(((unit + 1) * s.ctas - 1) / s.units);
+  return (int)(((unit / s.grain + 1) * s.ctas - 1) / (s.units / s.grain));
 }
 
 // The columns of x or dy that one output tile of a weight gradient covers: two instructions' M of 128,
@@ -67,14 +71,16 @@ struct Tile {
   int row0, rows, g;
 };
 // A tile of the table; one outside the batch or the bank has no rows and raises the status word.
-__device__ __forceinline__ Tile load_tile(const int32_t* table, int64_t t, int64_t rows, int n_adapters, void* ws) {
-  const int4 v = reinterpret_cast<const int4*>(table)[t];
+__device__ __forceinline__ Tile check_tile(const int4& v, int64_t rows, int n_adapters, void* ws) {
   Tile o{v.x, v.y, v.z};
   if (o.row0 < 0 || o.rows <= 0 || o.rows > TILE_ROWS || (int64_t)o.row0 + o.rows > rows || o.g < 0 || o.g >= n_adapters) {
     raise_status(ws, DIT_ERR_INVALID_ARG);
     o = Tile{0, 0, 0};
   }
   return o;
+}
+__device__ __forceinline__ Tile load_tile(const int32_t* table, int64_t t, int64_t rows, int n_adapters, void* ws) {
+  return check_tile(reinterpret_cast<const int4*>(table)[t], rows, n_adapters, ws);
 }
 
 // Completion counters of shared outputs, in the workspace: a call's first kernel leaves those of the
