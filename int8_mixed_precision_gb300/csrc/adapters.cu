@@ -836,57 +836,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// A small tile: up to 16 rows anywhere in the batch; one CTA, h in shared memory.
-// ---------------------------------------------------------------------------------------
-struct Small {
-  const int32_t* small;
-  const __nv_bfloat16 *x, *a, *b;
-  const float* scale;
-  void* y;
-  int y_bf16;
-  int64_t k, n;
-};
-__global__ void __launch_bounds__(256) k_small(Args p, Small o) {
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ float h[SMALL_ROWS][MAX_RANK];
-  __shared__ int rows[SMALL_ROWS];
-  const int32_t* s = o.small + (int64_t)blockIdx.x * SMALL_INTS;
-  const int g = s[0], count = s[1];
-  bool bad = g < 0 || g >= p.n_adapters || count < 0 || count > SMALL_ROWS;
-  for (int i = 0; i < count && !bad; ++i) bad = s[4 + i] < 0 || s[4 + i] >= p.rows;
-  if (bad) {
-    if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
-    return;
-  }
-  if (threadIdx.x < count) rows[threadIdx.x] = s[4 + threadIdx.x];
-  __syncthreads();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int i = warp; i < count * p.rank; i += 8) {
-    const int row = i / p.rank, j = i % p.rank;
-    const __nv_bfloat16* xr = o.x + (int64_t)rows[row] * o.k;
-    const __nv_bfloat16* ar = o.a + ((int64_t)g * p.rank + j) * o.k;
-    float v = 0.f;
-    for (int64_t c = lane; c < o.k; c += 32) v = fmaf(__bfloat162float(xr[c]), __bfloat162float(ar[c]), v);
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0) h[row][j] = v * o.scale[g];
-  }
-  __syncthreads();
-  for (int64_t c = threadIdx.x; c < o.n; c += 256)
-    for (int i = 0; i < count; ++i) {
-      float v = 0.f;
-      for (int j = 0; j < p.rank; ++j) v = fmaf(h[i][j], __bfloat162float(o.b[((int64_t)g * o.n + c) * p.rank + j]), v);
-      const int64_t at = (int64_t)rows[i] * o.n + c;
-      if (o.y_bf16) {
-        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(o.y);
-        y[at] = __float2bfloat16_rn(__bfloat162float(y[at]) + v);
-      } else {
-        reinterpret_cast<float*>(o.y)[at] += v;
-      }
-    }
-}
-
-// ---------------------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------------------
 static Args args_of(const dit_adapter_plan_t& plan, const int32_t* table, int rank, void* ws) {
@@ -1002,11 +951,7 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
   dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
   if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, st);
-  if (s == DIT_OK && plan->n_small) {
-    Small o{table + off_small(*plan), reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a),
-            reinterpret_cast<const __nv_bfloat16*>(b), scale, y, y_dt == DIT_BF16, k, n};
-    if (launch_pdl(k_small, dim3(plan->n_small), dim3(256), 0, st, 1, p, o) != cudaSuccess) s = DIT_ERR_CUDA;
-  }
+  if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
   return s;
 }
 

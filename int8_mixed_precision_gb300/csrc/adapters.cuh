@@ -91,6 +91,9 @@ constexpr size_t WS_TICKETS_ROWS = WS_TICKETS_RANK + 4 * MAX_CTAS;   // products
 static_assert(WS_TICKETS_RANK >= WS_PARTIALS + 32 * MAX_RED_CTAS && WS_TICKETS_ROWS + 4 * MAX_CTAS <= WS_BYTES, "");
 
 bool plan_ok(const dit_adapter_plan_t* p);
+dit_status small_tiles(const dit_adapter_plan_t& plan, const int32_t* table, const void* x, const void* a, const void* b,
+                       const float* scale, int rank, int64_t k, int64_t n, void* y, dit_dtype y_dt, void* ws,
+                       cudaStream_t st);
 dit_status check_common(const dit_adapter_plan_t* plan, const int32_t* table, const void* x, const void* a,
                         const void* b, const float* scale, int rank, int64_t k, int64_t n, const void* scratch,
                         size_t scratch_bytes, const void* ws, size_t ws_bytes);

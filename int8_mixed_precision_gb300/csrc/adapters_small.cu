@@ -1,0 +1,255 @@
+// Low-rank adapters for short requests: y[t] += scale (x[t] A^T) B^T for tiles of up to 16 rows that
+// share an adapter, wherever in the batch they are (single tokens of a serving batch above all).
+//
+// Bound by latency, and then by reading each adapter's A and B once: 16 rows reuse a weight far too
+// little to fill a 128-row tcgen05 instruction, so the products run on mma.sync (16 x 8 x 16) with
+// both operands loaded from global memory straight into fragments; a product's contraction
+// index may be permuted freely, so every lane loads 16 (or 8) contiguous bytes and takes them for the
+// elements that the fragment wants of it.
+//
+// One launch: a cluster of CTAs takes a tile.  Each CTA contracts its share of k and leaves a partial h in
+// its shared memory; after one cluster barrier every CTA sums all of them (in the CTAs' order, so
+// all get the same bits) and takes its share of the n columns.  What that share reads, B and y, is
+// fetched into L2 before the barrier.
+#include "adapters.cuh"
+
+namespace dit6 {
+namespace lora {
+
+constexpr int SMALL_WARPS = 8, SMALL_THREADS = 32 * SMALL_WARPS;
+
+struct Small {
+  const int32_t* tiles;
+  const __nv_bfloat16 *x, *a, *b;
+  const float* scale;
+  void* y;
+  int64_t rows, k, n;
+  int n_adapters, rank, rp, cluster;
+  void* ws;
+};
+
+// d += a b: a 16 x 16 (row), b 16 x 8 (col)
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// RT: tiles of 8 of the rank at least (a bound on registers)
+template <int RT, bool BF16>
+__global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
+  pdl_launch_dependents();
+  extern __shared__ float sm[];
+  float* part = sm;                                // [warps][16][rp], then this CTA's h in the first [16][rp]
+  float* sum = sm + SMALL_WARPS * 16 * p.rp;       // this CTA's partial h [16][rp], read by the cluster
+  const int P = BF16 ? 2 : PARTS;                  // parts of h (see adapters.cuh)
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(sum + 16 * p.rp);  // [P][16][rp + 8]
+  const int hp = p.rp + 8;                         // rows 16 bytes apart in banks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
+  const uint32_t rank_in = p.cluster > 1 ? cluster_rank() : 0;
+  pdl_wait();
+  const int32_t* tile = p.tiles + (int64_t)(blockIdx.x / p.cluster) * SMALL_INTS;
+  const int4 head = *reinterpret_cast<const int4*>(tile);
+  const int g = head.x, count = head.y;
+  // every lane looks at one row of the tile; the whole cluster comes to the same verdict
+  const int mine = lane < 16 ? tile[4 + lane] : 0;
+  const bool bad = g < 0 || g >= p.n_adapters || count < 0 || count > SMALL_ROWS ||
+                   __any_sync(0xffffffffu, lane < count && (mine < 0 || mine >= p.rows));
+  if (bad) {
+    if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
+    return;
+  }
+  const int row_lo = __shfl_sync(0xffffffffu, mine, g8), row_hi = __shfl_sync(0xffffffffu, mine, g8 + 8);
+  const bool has_lo = g8 < count, has_hi = g8 + 8 < count;
+
+  // this CTA's share of the columns, in groups of 16
+  const int64_t groups = (p.n + 15) / 16;
+  const int64_t n_first = groups * rank_in / p.cluster * 16, n_last = min(p.n, groups * (rank_in + 1) / p.cluster * 16);
+  const __nv_bfloat16* b = p.b + (int64_t)g * p.n * p.rank;
+  constexpr int ES = BF16 ? 2 : 4;
+
+  // ---- h over this CTA's share of k, 32 elements of it to a warp at a time
+  float acc[RT][4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  const int64_t steps = (p.k + 31) / 32;
+  const int64_t k_first = steps * rank_in / p.cluster, k_last = steps * (rank_in + 1) / p.cluster;
+  const __nv_bfloat16* a = p.a + (int64_t)g * p.rank * p.k;
+  const int tiles8 = p.rank / 8;
+  for (int64_t s = k_first + warp; s < k_last; s += SMALL_WARPS) {
+    const int64_t k = s * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
+    const bool in = k < p.k;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (in && has_lo) lo = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_lo * p.k + k);
+    if (in && has_hi) hi = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_hi * p.k + k);
+    uint4 w[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (in && i < tiles8) w[i] = *reinterpret_cast<const uint4*>(a + (int64_t)(i * 8 + g8) * p.k + k);
+    }
+    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      if (i < tiles8) {
+        mma_16816(acc[i], a0, w[i].x, w[i].y);
+        mma_16816(acc[i], a1, w[i].z, w[i].w);
+      }
+  }
+  // B and y of this CTA's columns, while the partial sums meet
+  {
+    const char* from = reinterpret_cast<const char*>(b + n_first * p.rank);
+    const int64_t bytes = max((int64_t)0, n_last - n_first) * p.rank * 2;
+    for (int64_t i = threadIdx.x * 128; i < bytes; i += SMALL_THREADS * 128) prefetch_l2(from + i);
+    const int64_t row_bytes = max((int64_t)0, n_last - n_first) * ES;
+    for (int r = warp; r < count; r += SMALL_WARPS) {
+      const char* y = reinterpret_cast<const char*>(p.y) + ((int64_t)tile[4 + r] * p.n + n_first) * ES;
+      for (int64_t i = lane * 128; i < row_bytes; i += 32 * 128) prefetch_l2(y + i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    if (i < tiles8) {
+      float* at = part + ((int64_t)warp * 16 + g8) * p.rp + i * 8 + c4 * 2;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(at + 8 * p.rp) = make_float2(acc[i][2], acc[i][3]);
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * p.rp; i += SMALL_THREADS) {
+    float v = 0.f;
+    if (i % p.rp < p.rank)
+      for (int w = 0; w < SMALL_WARPS; ++w) v += part[w * 16 * p.rp + i];
+    sum[i] = v;
+  }
+  if (p.cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  const float scale = p.scale[g];
+  for (int i = threadIdx.x; i < 16 * p.rp; i += SMALL_THREADS) {
+    float v = 0.f;
+    if (p.cluster > 1) {
+      const uint32_t at = smem_u32(sum + i);
+      float other[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) other[c] = c < p.cluster ? ld_cluster_f32(mapa_rank(at, c)) : 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v += other[c];
+    } else {
+      v = sum[i];
+    }
+    v *= scale;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      if (q >= P) break;
+      const __nv_bfloat16 first = __float2bfloat16_rn(v);
+      h[(q * 16 + i / p.rp) * hp + i % p.rp] = first;
+      const float f = __bfloat162float(first);
+      v = isfinite(f) ? v - f : 0.f;
+    }
+  }
+  if (p.cluster > 1) cluster_arrive();  // this CTA has read the others' sums
+  __syncthreads();
+
+  // ---- y: 16 columns to a warp at a time; a lane ends with four consecutive ones of two rows
+  const int k16 = p.rp / 16;
+  for (int64_t n0 = n_first + warp * 16; n0 < n_last; n0 += SMALL_WARPS * 16) {
+    const int64_t col = n0 + c4 * 4;  // this lane's columns of the result
+    // tile t of the pair has the columns n0 + 4 (s / 2) + 2 t + s % 2 in its slots s
+    const int64_t b0 = n0 + 4 * (g8 >> 1) + (g8 & 1), b1 = b0 + 2;
+    char* out_lo = reinterpret_cast<char*>(p.y) + ((int64_t)row_lo * p.n + col) * ES;
+    char* out_hi = reinterpret_cast<char*>(p.y) + ((int64_t)row_hi * p.n + col) * ES;
+    const bool lo = has_lo && col < p.n, hi = has_hi && col < p.n;
+    uint4 was_lo = make_uint4(0, 0, 0, 0), was_hi = was_lo;
+    if (BF16) {
+      if (lo) reinterpret_cast<uint2*>(&was_lo)[0] = *reinterpret_cast<const uint2*>(out_lo);
+      if (hi) reinterpret_cast<uint2*>(&was_hi)[0] = *reinterpret_cast<const uint2*>(out_hi);
+    } else {
+      if (lo) was_lo = *reinterpret_cast<const uint4*>(out_lo);
+      if (hi) was_hi = *reinterpret_cast<const uint4*>(out_hi);
+    }
+    float d0[4] = {}, d1[4] = {};
+#pragma unroll
+    for (int j = 0; j < (RT + 1) / 2; ++j) {
+      if (j >= k16) break;
+      const int k = j * 16 + c4 * 4;  // this lane's four elements of the step
+      uint2 w0 = make_uint2(0, 0), w1 = w0;
+      if (k < p.rank && b0 < p.n) w0 = *reinterpret_cast<const uint2*>(b + b0 * p.rank + k);
+      if (k < p.rank && b1 < p.n) w1 = *reinterpret_cast<const uint2*>(b + b1 * p.rank + k);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        if (q >= P) break;
+        const uint2 lo2 = *reinterpret_cast<const uint2*>(h + (q * 16 + g8) * hp + k);
+        const uint2 hi2 = *reinterpret_cast<const uint2*>(h + (q * 16 + g8 + 8) * hp + k);
+        const uint32_t af[4] = {lo2.x, hi2.x, lo2.y, hi2.y};
+        mma_16816(d0, af, w0.x, w0.y);
+        mma_16816(d1, af, w1.x, w1.y);
+      }
+    }
+    if (BF16) {
+      auto add = [](const uint4& was, float v0, float v1, float v2, float v3) {
+        const float2 e = bf16x2_to_f2(was.x), f = bf16x2_to_f2(was.y);
+        return make_uint2(f2_to_bf16x2(e.x + v0, e.y + v1), f2_to_bf16x2(f.x + v2, f.y + v3));
+      };
+      if (lo) *reinterpret_cast<uint2*>(out_lo) = add(was_lo, d0[0], d0[1], d1[0], d1[1]);
+      if (hi) *reinterpret_cast<uint2*>(out_hi) = add(was_hi, d0[2], d0[3], d1[2], d1[3]);
+    } else {
+      auto add = [](const uint4& was, float v0, float v1, float v2, float v3) {
+        return make_float4(__uint_as_float(was.x) + v0, __uint_as_float(was.y) + v1, __uint_as_float(was.z) + v2,
+                           __uint_as_float(was.w) + v3);
+      };
+      if (lo) *reinterpret_cast<float4*>(out_lo) = add(was_lo, d0[0], d0[1], d1[0], d1[1]);
+      if (hi) *reinterpret_cast<float4*>(out_hi) = add(was_hi, d0[2], d0[3], d1[2], d1[3]);
+    }
+  }
+  if (p.cluster > 1) cluster_wait();  // nobody still reads this CTA's shared memory
+}
+
+template <int RT, bool BF16>
+static cudaError_t launch_small(const Small& p, int tiles, cudaStream_t st) {
+  const size_t smem = (size_t)(SMALL_WARPS + 1) * 16 * p.rp * 4 + (size_t)PARTS * 16 * (p.rp + 8) * 2;
+  static const cudaError_t allowed =
+      cudaFuncSetAttribute(k_small<RT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+  if (allowed != cudaSuccess) return allowed;
+  return launch_pdl(k_small<RT, BF16>, dim3((unsigned)(tiles * p.cluster)), dim3(SMALL_THREADS), smem, st,
+                    (unsigned)p.cluster, p);
+}
+
+// The small tiles of a plan.
+dit_status small_tiles(const dit_adapter_plan_t& plan, const int32_t* table, const void* x, const void* a, const void* b,
+                       const float* scale, int rank, int64_t k, int64_t n, void* y, dit_dtype y_dt, void* ws,
+                       cudaStream_t st) {
+  if (!plan.n_small) return DIT_OK;
+  Small p{table + off_small(plan), reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a),
+          reinterpret_cast<const __nv_bfloat16*>(b), scale, y, plan.rows, k, n, plan.n_adapters, rank, padded_rank(rank), 8,
+          ws};
+  // CTAs to a tile: as many as the SMs allow
+  while (p.cluster > 1 && (int64_t)plan.n_small * p.cluster > 2 * num_sms()) p.cluster /= 2;
+  const bool bf16 = y_dt == DIT_BF16;
+  cudaError_t e;
+  if (rank <= 16)
+    e = bf16 ? launch_small<2, true>(p, plan.n_small, st) : launch_small<2, false>(p, plan.n_small, st);
+  else if (rank <= 32)
+    e = bf16 ? launch_small<4, true>(p, plan.n_small, st) : launch_small<4, false>(p, plan.n_small, st);
+  else if (rank <= 64)
+    e = bf16 ? launch_small<8, true>(p, plan.n_small, st) : launch_small<8, false>(p, plan.n_small, st);
+  else
+    e = bf16 ? launch_small<16, true>(p, plan.n_small, st) : launch_small<16, false>(p, plan.n_small, st);
+  return e == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+}
+
+}  // namespace lora
+}  // namespace dit6
