@@ -448,7 +448,8 @@ dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const int32_t* tabl
 /* ------------------------------------------------------------------------------------
  * One AdamW step over many tensors in one launch, with the moments in 32 or in 8 bits.
  *
- * Per element, each operation rounded to fp32 (g, p read in their own types):
+ * Per element, each operation rounded to fp32 (g, p read in their own types; with 8-bit moments
+ * the last quotient is within 2 units in the last place of it):
  *   g' = g * (*grad_scale)               (grad_scale NULL: g' = g)
  *   m  = m beta1 + g' (1 - beta1),       v = v beta2 + (g' g') (1 - beta2)
  *   p  = p (1 - lr wd) - (m lr / (1 - beta1^t)) / (sqrt(v) (1 - beta2^t)^-1/2 + eps)
