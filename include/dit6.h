@@ -426,6 +426,8 @@ typedef struct {
   int32_t training;
   int32_t n_tiles; /* tiles of up to 128 consecutive rows */
   int32_t n_small; /* tiles of up to 16 rows in any places (serving plans: short requests) */
+  int32_t most_tiles; /* the largest number of 128-row tiles of one adapter */
+  int32_t reserved;
 } dit_adapter_plan_t;
 
 dit_status dit_adapter_plan(const int64_t* lengths, const int32_t* adapters, int64_t requests,

@@ -21,7 +21,8 @@ _CODE = {_F32: 0, _BF16: 1}
 
 class _Plan(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("table_ints", ctypes.c_int64), ("n_adapters", ctypes.c_int32),
-                ("training", ctypes.c_int32), ("n_tiles", ctypes.c_int32), ("n_small", ctypes.c_int32)]
+                ("training", ctypes.c_int32), ("n_tiles", ctypes.c_int32), ("n_small", ctypes.c_int32),
+                ("most_tiles", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class AdapterPlan:

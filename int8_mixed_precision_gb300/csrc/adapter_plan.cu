@@ -35,9 +35,10 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
     last = g;
     rows += lengths[i];
   }
-  int64_t n_tiles = 0, n_small = 0;
+  int64_t n_tiles = 0, n_small = 0, most = 0;
   for (const auto& rs : runs) {
     int64_t few = 0;
+    const int64_t before = n_tiles;
     for (const Run& r : rs) {
       if (!training && r.rows <= SMALL_RUN)
         few += r.rows;
@@ -45,6 +46,7 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
         n_tiles += (r.rows + TILE_ROWS - 1) / TILE_ROWS;
     }
     n_small += (few + SMALL_ROWS - 1) / SMALL_ROWS;
+    if (n_tiles - before > most) most = n_tiles - before;
   }
   if (n_tiles > MAX_TILES || n_small > MAX_TILES) return DIT_ERR_UNSUPPORTED;
   plan->rows = rows;
@@ -52,6 +54,8 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
   plan->training = training ? 1 : 0;
   plan->n_tiles = (int32_t)n_tiles;
   plan->n_small = (int32_t)n_small;
+  plan->most_tiles = (int32_t)most;
+  plan->reserved = 0;
   plan->table_ints = off_small(*plan) + (int64_t)SMALL_INTS * n_small;
   if (!table) return DIT_OK;
   if (table_ints < plan->table_ints) return DIT_ERR_INVALID_ARG;
@@ -90,7 +94,7 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
 
 bool plan_ok(const dit_adapter_plan_t* p) {
   return p && p->rows >= 0 && p->rows <= MAX_ROWS && p->n_adapters > 0 && p->n_tiles >= 0 && p->n_tiles <= MAX_TILES &&
-         p->n_small >= 0 && p->n_small <= MAX_TILES && p->table_ints == off_small(*p) + (int64_t)SMALL_INTS * p->n_small;
+         p->n_small >= 0 && p->n_small <= MAX_TILES && p->most_tiles >= 0 && p->most_tiles <= p->n_tiles && p->table_ints == off_small(*p) + (int64_t)SMALL_INTS * p->n_small;
 }
 
 dit_status check_common(const dit_adapter_plan_t* plan, const int32_t* table, const void* x, const void* a,

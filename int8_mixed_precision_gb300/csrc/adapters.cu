@@ -9,8 +9,7 @@
 //
 //   k_to_rank    h, e: units are (128 rows, 64 columns of x or dy), cut evenly over the SMs
 //   k_from_rank  y, dx: units are (128 rows, up to 256 columns), read, added to and written once
-//   k_over_rows  dA, dB: units are (128 or 256 columns, 128 rows), cut evenly over the SMs; both
-//                gradients in one launch
+//   k_over_rows  dA, dB: units are (128 to 512 columns, 128 rows); both gradients in one launch
 //
 // Weights are read as they lie: A [rank x k] and B [n x rank] serve both the product along their
 // rows (K-major operand) and the one across them (MN-major operand), so no transposed copies are kept.
@@ -32,7 +31,7 @@ constexpr int RING_BYTES = 220 * 1024;      // shared memory for operands
 constexpr int SMEM_BYTES = RING_BYTES + 1024 + 1024;
 constexpr int MAX_STAGES = 12;
 constexpr int MAX_PANELS = 8;               // k_from_rank: 128 rows x 128 bytes of the output each
-constexpr int ACCS = 4;                     // accumulators in turn (two in k_to_rank, one in k_over_rows)
+constexpr int ACCS = 4;                     // accumulators in turn in k_from_rank (two in the other kernels)
 
 struct Args {
   const int32_t* table;
@@ -52,11 +51,9 @@ struct Control {
   uint64_t dfull[ACCS], dempty[ACCS];  // accumulators
   uint64_t hfull, hempty;              // the tile of held (k_from_rank)
   uint64_t yfull[MAX_PANELS], ydone[MAX_PANELS], yempty[MAX_PANELS];  // panels of the output: loaded, updated, stored
-  uint64_t sync;                       // the epilogue warps among themselves
   uint64_t done;
   uint32_t tmem;
   int abort;
-  int last;
   int valid[MAX_STAGES];               // rows of a stage that belong to its tile (k_over_rows)
 };
 
@@ -70,7 +67,7 @@ __device__ __forceinline__ Frame frame(uint8_t* raw) {
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   return Frame{smem_u32(base), reinterpret_cast<Control*>(base + RING_BYTES)};
 }
-__device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols) {
+__device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols, int epi_warps = EPI_WARPS) {
   Control* c = f.c;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -79,7 +76,7 @@ __device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols)
     }
     for (int b = 0; b < ACCS; ++b) {
       mbar_init(smem_u32(&c->dfull[b]), 1);
-      mbar_init(smem_u32(&c->dempty[b]), EPI_WARPS);
+      mbar_init(smem_u32(&c->dempty[b]), epi_warps);
     }
     for (int b = 0; b < MAX_PANELS; ++b) {
       mbar_init(smem_u32(&c->yfull[b]), 1);
@@ -88,7 +85,6 @@ __device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols)
     }
     mbar_init(smem_u32(&c->hfull), 1);
     mbar_init(smem_u32(&c->hempty), 1);
-    mbar_init(smem_u32(&c->sync), EPI_WARPS);
     mbar_init(smem_u32(&c->done), 1);
     c->abort = 0;
     fence_barrier_init();
@@ -120,29 +116,27 @@ __device__ __forceinline__ void await_mmas(const Frame& f, void* ws) {
   mma_commit(smem_u32(&f.c->done));
   mbar_wait(smem_u32(&f.c->done), 0, ws, &never);
 }
-__device__ __forceinline__ void clear_tickets(void* ws, size_t off) {
-  if (blockIdx.x == 0 && threadIdx.x < MAX_CTAS) ws_u32(ws, off)[threadIdx.x] = 0;
-}
 // The slot of CTA `cta`'s partial result for an output that CTAs c0 and later ones share.
 __device__ __forceinline__ int slot_of(int cta, int c0) { return 2 * cta + (cta == c0 ? 1 : 0); }
 
-// All epilogue warps meet (a bounded wait: one of them may have given up); `turn` counts the meetings.
-__device__ __forceinline__ bool meet(Control* c, uint32_t& turn, void* ws) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&c->sync));
-  return warp_wait(smem_u32(&c->sync), turn++ & 1, ws, &c->abort);
-}
-// Counts this CTA's partial result (written before) in; true in the CTA that counts last.  `ok` falls
-// to false when a wait ran out.
-__device__ __forceinline__ bool count_in(Control* c, uint32_t* ticket, int shares, uint32_t& turn, bool& ok, void* ws) {
-  __threadfence();
-  ok = meet(c, turn, ws);
-  if (!ok) return false;
-  if (threadIdx.x == 64) c->last = atomicAdd(ticket, 1u) == (uint32_t)(shares - 1);
-  ok = meet(c, turn, ws);
-  const bool last = ok && *reinterpret_cast<volatile int*>(&c->last) != 0;
-  if (last) __threadfence();
-  return last;
+// The sum over CTAs c0 to c1 of their partial results at float4 index e, in the CTAs' order.
+__device__ __forceinline__ float4 sum_slots(const float* slots, int64_t slot, int c0, int c1, int e) {
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = c0; k <= c1; k += 4) {  // four loads in flight
+    float4 v[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      v[h] = k + h <= c1 ? __ldcg(reinterpret_cast<const float4*>(slots + slot_of(k + h, c0) * slot) + e)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      sum.x += v[h].x;
+      sum.y += v[h].y;
+      sum.z += v[h].z;
+      sum.w += v[h].w;
+    }
+  }
+  return sum;
 }
 
 // A value's parts: each the bf16 nearest to what is left.  An infinite or NaN first part stands alone.
@@ -175,10 +169,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   Control* c = f.c;
   volatile int* abort = &c->abort;
   constexpr uint32_t COLS = 256;  // two accumulators of up to 128 columns
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&m_in);
+    prefetch_tmap(&m_w);
+  }
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
-  clear_tickets(p.ws, WS_TICKETS_ROWS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w_chunks = MN ? (p.rank + 63) / 64 : 1;
@@ -187,29 +184,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall) {
-      prefetch_tmap(&m_in);
-      prefetch_tmap(&m_w);
-      uint32_t n = 0;
+    if (!p.stall) {
+      uint32_t n = 0, parity = 1;
       bool ok = true;
       Tile t{0, 0, 0};
       int64_t ti = u0 / o.blocks;
       int kb = (int)(u0 % o.blocks), s = 0;
-      uint32_t parity = 1;
       for (int64_t u = u0; u < u1; ++u, ++n) {
         if (u == u0 || kb == 0) t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-        if (!mbar_wait(smem_u32(&c->empty[s]), parity, p.ws, abort)) {
+        if (!warp_wait(smem_u32(&c->empty[s]), parity, p.ws, abort)) {
           ok = false;
           break;
         }
         const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
-        mbar_expect_tx(full, stage_bytes);
-        tma_load_2d(dst, &m_in, full, kb * 64, t.row0);
-        if (MN) {
-          for (int i = 0; i < w_chunks; ++i) tma_load_3d(dst + 16384 + i * 8192, &m_w, full, i * 64, kb * 64, t.g);
-        } else {
-          tma_load_3d(dst + 16384, &m_w, full, kb * 64, 0, t.g);
-        }
+        if (lane == 0) mbar_expect_tx(full, stage_bytes);
+        __syncwarp();
+        if (lane == 0)
+          tma_load_2d(dst, &m_in, full, kb * 64, t.row0);
+        else if (lane <= w_chunks)
+          tma_load_3d(dst + 8192 + lane * 8192, &m_w, full, MN ? (lane - 1) * 64 : kb * 64, MN ? kb * 64 : 0, t.g);
         if (++kb == o.blocks) {
           kb = 0;
           ++ti;
@@ -243,11 +236,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               break;
             }
             fence_after();
-            const uint32_t a = f.smem + s * stage_bytes, b = a + 16384;
+            const uint32_t at = f.smem + s * stage_bytes;
+            const uint32_t a = desc_k(at), b = MN ? desc_mn(at + 16384, 8192) : desc_k(at + 16384);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma(tmem + buf * 128, desc_k(a + j * 32), MN ? desc_mn(b + j * 2048, 8192) : desc_k(b + j * 32), id,
-                  u > first || j > 0);
+              mma(tmem + buf * 128, a + j * (32 >> 4), b + j * ((MN ? 2048 : 32) >> 4), id, u > first || j > 0);
             mma_commit(smem_u32(&c->empty[s]));
             if (++s == p.stages) {
               s = 0;
@@ -264,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;
     const int nc = p.rp / 2, col0 = half * nc;  // this thread's columns (a multiple of 8)
-    uint32_t chunk = 0, turn = 0;
+    uint32_t chunk = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
       const int64_t ti = u / o.blocks;
@@ -300,33 +293,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
       if (!whole) {
-        const int c0 = cta_of(p.split, ti * o.blocks), c1 = cta_of(p.split, (ti + 1) * o.blocks - 1);
-        const int64_t at = (int64_t)row * p.rp + col0, slot = (int64_t)TILE_ROWS * p.rp;
-        float* mine = o.slots + slot_of(blockIdx.x, c0) * slot + at;
+        const int c0 = cta_of(p.split, ti * o.blocks);
+        float* mine = o.slots + slot_of(blockIdx.x, c0) * ((int64_t)TILE_ROWS * p.rp) + (int64_t)row * p.rp + col0;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (4 * i < nc) reinterpret_cast<float4*>(mine)[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-        if (!count_in(c, ws_u32(p.ws, WS_TICKETS_RANK) + c0, c1 - c0 + 1, turn, ok, p.ws)) continue;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-        for (int k = c0; k <= c1; k += 4) {  // the loads of four CTAs' partial results at a time
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (4 * i < nc) {
-              float4 v[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h)
-                v[h] = k + h <= c1 ? __ldcg(reinterpret_cast<const float4*>(o.slots + slot_of(k + h, c0) * slot + at) + i)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                acc[4 * i] += v[h].x;
-                acc[4 * i + 1] += v[h].y;
-                acc[4 * i + 2] += v[h].z;
-                acc[4 * i + 3] += v[h].w;
-              }
-            }
-        }
+        continue;
       }
       const float scale = o.scale[t.g];
       __nv_bfloat16* held = o.held + (ti * TILE_ROWS + row) * (int64_t)(p.parts * p.rp) + col0;
@@ -350,6 +322,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   finish(f, COLS);
+}
+
+// The tiles that several CTAs share: four columns of a row to a thread.
+__global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int quads = p.rp / 4, ctas = TILE_ROWS * quads / 256;  // rp is a multiple of 16
+  const int64_t ti = blockIdx.x / ctas;
+  const int e = blockIdx.x % ctas * 256 + threadIdx.x, r = e / quads, col = e % quads * 4;
+  const int c0 = cta_of(p.split, ti * o.blocks), c1 = cta_of(p.split, (ti + 1) * o.blocks - 1);
+  if (c0 == c1) return;
+  const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
+  const float4 sum = sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e);
+  const float scale = o.scale[t.g], v[4] = {sum.x, sum.y, sum.z, sum.w};
+  float part[4][PARTS];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) split_parts(r < t.rows && col + h < p.rank ? v[h] * scale : 0.f, part[h]);
+  __nv_bfloat16* held = o.held + (ti * TILE_ROWS + r) * (int64_t)(p.parts * p.rp) + col;
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h)
+    if (h < p.parts)
+      *reinterpret_cast<uint2*>(held + h * p.rp) = make_uint2(f2_to_bf16x2(part[0][h], part[1][h]), f2_to_bf16x2(part[2][h], part[3][h]));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -381,10 +375,14 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   Control* c = f.c;
   volatile int* abort = &c->abort;
   constexpr uint32_t COLS = 512;  // four accumulators of up to 128 columns
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&m_held);
+    prefetch_tmap(&m_w);
+    prefetch_tmap(&m_out);
+  }
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
-  clear_tickets(p.ws, WS_TICKETS_RANK);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int steps = p.parts * p.rp / 16;           // of the contraction
@@ -402,9 +400,6 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0 && !p.stall) {
-      prefetch_tmap(&m_held);
-      prefetch_tmap(&m_w);
-      prefetch_tmap(&m_out);
       uint32_t n = 0, tiles = 0, np = 0;
       bool ok = true;
       Tile t{0, 0, 0};
@@ -472,11 +467,12 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
         if (!mbar_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort)) break;
         if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
         fence_after();
-        const uint32_t b = ring + s * w_bytes;
+        const uint32_t b0 = MN ? desc_mn(ring + s * w_bytes, box_bytes) : desc_k(ring + s * w_bytes);
+        const uint32_t a0 = desc_k(f.smem);
         int j = 0;
         for (int q = 0; q < steps; ++q) {  // every part meets the same weights
-          const uint64_t bd = MN ? desc_mn(b + j * 2048, box_bytes) : desc_k(b + (j / 4) * box_bytes + (j % 4) * 32);
-          mma(tmem + buf * 128, desc_k(f.smem + (q / 4) * 16384 + (q % 4) * 32), bd, id, q > 0);
+          const uint32_t b = b0 + (MN ? j * (2048 >> 4) : (j / 4) * (box_bytes >> 4) + (j % 4) * (32 >> 4));
+          mma(tmem + buf * 128, a0 + (q / 4) * (16384 >> 4) + (q % 4) * (32 >> 4), b, id, q > 0);
           if (++j == rank_steps) j = 0;
         }
         mma_commit(smem_u32(&c->empty[s]));
@@ -591,34 +587,61 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
 
 // ---------------------------------------------------------------------------------------
 // Over the rows: dA[g] = e^T x and dB[g] = dy^T h over the rows of every adapter g.
+//
+// An output tile is 128 mtiles columns of x (or dy) by the whole rank; its units are the adapter's
+// tiles of 128 rows.  The columns are M of the instructions (MN-major: x as it lies), the rank is N,
+// and the parts of e (or h) are three instructions into one accumulator.  What bounds it is the
+// traffic into shared memory: e is read again for every output tile, so the tiles are as wide as
+// tensor memory holds twice over (512 columns up to rank 64, 256 above); accumulators are
+// drained after every 128 rows, 24 instructions, while the other ones fill.
 // ---------------------------------------------------------------------------------------
+constexpr int ROW_EPI_WARPS = 16, ROW_THREADS = 64 + 32 * ROW_EPI_WARPS;
+constexpr int ROW_STAGE = 32;       // rows of a stage
+constexpr int ROW_BOX = ROW_STAGE * 128;  // bytes of a box of 64 columns
+
 struct Grad {
-  const __nv_bfloat16* held;
   float* out;
   int64_t width;
   int64_t blocks;  // of the output, along the width
-  int64_t rank_stride, col_stride;  // of the output; one of them is 1
 };
 struct OverRows {
-  Grad g[2];       // dA, dB
+  Grad g[2];       // dA [rank x k], dB [n x rank]
   const int32_t* first;
   float* slots;
-  int mtiles, accs;  // 128 columns each, and accumulators in turn
+  int mtiles;      // 1, 2 or 4
+  int whole;       // whole output tiles to each CTA, else equal shares of the units
+};
+
+// The boxes of a stage of e or h: where parts lie side by side in 64 columns (ranks of 16, 32 and 64 and
+// 128 after padding) they are loaded so, otherwise each part begins a box of its own, since an
+// operand's chunks of 64 columns start at its first column.
+struct HeldBoxes {
+  int boxes, per_part, rp;
+  __device__ __forceinline__ explicit HeldBoxes(int rp_) : rp(rp_) {
+    per_part = 64 % rp == 0 ? 0 : (rp + 63) / 64;
+    boxes = per_part ? PARTS * per_part : (PARTS * rp + 63) / 64;
+  }
+  __device__ __forceinline__ int column(int box) const {
+    return per_part ? box / per_part * rp + box % per_part * 64 : box * 64;
+  }
+  __device__ __forceinline__ uint32_t offset(int part) const {
+    return per_part ? part * per_part * ROW_BOX : part * rp / 64 * ROW_BOX + part * rp % 64 * 2;
+  }
 };
 
 // A unit of k_over_rows: its output tile (problem, adapter, columns) and tile of rows.
 struct RowsUnit {
   bool ok;
   int problem, g;
-  int64_t block;       // of columns
-  int64_t tile;        // of the plan
+  int64_t block;         // of columns
+  int64_t tile;          // of the plan
   int64_t first, count;  // first unit and units of the output tile
 };
 __device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, int64_t u) {
   RowsUnit r;
   const int64_t units0 = o.g[0].blocks * p.n_tiles;
   r.problem = u >= units0;
-  const int64_t base = r.problem ? units0 : 0, v = u - base, blocks = o.g[r.problem].blocks;
+  const int64_t base = r.problem ? units0 : 0, blocks = r.problem ? o.g[1].blocks : o.g[0].blocks, v = u - base;
   // An adapter's units follow one another and its tiles are [f0, f1): v / blocks is one of its tiles.
   r.g = p.table[4 * (v / blocks) + 2];
   r.ok = r.g >= 0 && r.g < p.n_adapters;
@@ -632,8 +655,19 @@ __device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, 
   r.tile = f0 + (u - r.first);
   return r;
 }
+// The first unit of output tile `i` of all (adapters without tiles have empty ones).
+__device__ __forceinline__ int64_t first_of_output(const Args& p, const OverRows& o, int64_t i) {
+  const int64_t outputs0 = o.g[0].blocks * p.n_adapters;
+  const bool second = i >= outputs0;
+  const int64_t blocks = second ? o.g[1].blocks : o.g[0].blocks, v = second ? i - outputs0 : i;
+  const int64_t g = v / blocks;
+  if (g >= p.n_adapters) return p.split.units;
+  const int64_t f0 = o.first[g], f1 = o.first[g + 1];
+  const int64_t u = (second ? o.g[0].blocks * p.n_tiles : 0) + blocks * f0 + v % blocks * (f1 - f0);
+  return max((int64_t)0, min(p.split.units, u));
+}
 
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(ROW_THREADS, 1)
     k_over_rows(const __grid_constant__ CUtensorMap m_x, const __grid_constant__ CUtensorMap m_e,
                 const __grid_constant__ CUtensorMap m_dy, const __grid_constant__ CUtensorMap m_h, Args p, OverRows o) {
   pdl_launch_dependents();
@@ -642,20 +676,37 @@ __global__ void __launch_bounds__(THREADS, 1)
   Control* c = f.c;
   volatile int* abort = &c->abort;
   constexpr uint32_t COLS = 512;
-  start(f, p.stages, COLS);
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&m_x);
+    prefetch_tmap(&m_e);
+    prefetch_tmap(&m_dy);
+    prefetch_tmap(&m_h);
+  }
+  start(f, p.stages, COLS, ROW_EPI_WARPS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
-  clear_tickets(p.ws, WS_TICKETS_RANK);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_all = PARTS * p.rp;  // accumulator columns of one M tile
-  const int a_boxes = 2 * o.mtiles, b_boxes = (n_all + 63) / 64;
-  const uint32_t stage_bytes = (a_boxes + b_boxes) * 8192;  // 64 rows
-  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+  const HeldBoxes hb(p.rp);
+  const int a_boxes = 2 * o.mtiles;
+  const uint32_t stage_bytes = (a_boxes + hb.boxes) * ROW_BOX;
+  int64_t u0, u1;
+  if (o.whole) {
+    const int64_t outputs = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters;
+    u0 = first_of_output(p, o, outputs * blockIdx.x / gridDim.x);
+    u1 = first_of_output(p, o, outputs * (blockIdx.x + 1) / gridDim.x);
+  } else {
+    u0 = first_unit(p.split, blockIdx.x);
+    u1 = first_unit(p.split, blockIdx.x + 1);
+  }
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall) {
-      uint32_t n = 0;
+    if (!p.stall) {
+      // a lane to each box of a stage: one thread would spend longer issuing them than they take
+      const int boxes = a_boxes + hb.boxes, held_box = lane - a_boxes;
+      const int held_col = held_box >= 0 ? hb.column(held_box) : 0;
+      uint32_t parity = 1, n = 0;
+      int s = 0;
       bool ok = true;
       for (int64_t u = u0; u < u1 && ok;) {
         const RowsUnit r = rows_unit(p, o, u);
@@ -666,34 +717,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const int64_t end = min(u1, r.first + r.count);
         const int4* entry = reinterpret_cast<const int4*>(p.table) + r.tile;
-        const int col = (int)(r.block * a_boxes * 64);
+        const CUtensorMap* map = held_box < 0 ? (r.problem ? &m_dy : &m_x) : (r.problem ? &m_h : &m_e);
+        const int col = held_box < 0 ? (int)(r.block * a_boxes + lane) * 64 : held_col;
         int held_row = (int)(r.tile * TILE_ROWS);
         int4 next = *entry;
         for (; u < end && ok; ++u) {
           const Tile t = check_tile(next, p.rows, p.n_adapters, p.ws);
           if (u + 1 < end) next = *++entry;  // used a tile later
-          for (int h = 0; h < 2; ++h, ++n, held_row += 64) {
-            const int s = n % p.stages;
-            if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+          for (int h = 0; h < TILE_ROWS; h += ROW_STAGE, held_row += ROW_STAGE, ++n) {
+            if (!warp_wait(smem_u32(&c->empty[s]), parity, p.ws, abort)) {
               ok = false;
               break;
             }
-            const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
-            c->valid[s] = min(64, max(0, t.rows - 64 * h));
-            mbar_expect_tx(full, stage_bytes);
-            for (int i = 0; i < a_boxes; ++i)
-              tma_load_2d(dst + i * 8192, r.problem ? &m_dy : &m_x, full, col + i * 64, t.row0 + 64 * h);
-            for (int i = 0; i < b_boxes; ++i)
-              tma_load_2d(dst + (a_boxes + i) * 8192, r.problem ? &m_h : &m_e, full, i * 64, held_row);
+            const uint32_t full = smem_u32(&c->full[s]);
+            if (lane == 0) {
+              c->valid[s] = min(ROW_STAGE, max(0, t.rows - h));
+              mbar_expect_tx(full, stage_bytes);
+            }
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_2d(f.smem + s * stage_bytes + lane * ROW_BOX, map, full, col, held_box < 0 ? t.row0 + h : held_row);
+            if (++s == p.stages) {
+              s = 0;
+              parity ^= 1;
+            }
           }
         }
       }
       if (!ok) await_copies(f, p.stages, n, p.ws);
     }
   } else if (warp == 1) {
-    const int n_one = min(n_all, 256), n_two = n_all - n_one;  // one instruction has at most 256 columns
-    const uint32_t id_one = idesc(128, n_one, true, true), id_two = idesc(128, n_two, true, true);
-    uint32_t n = 0, chunk = 0;
+    const uint32_t id = idesc(128, p.rp, true, true);
+    const uint32_t part_at[PARTS] = {hb.offset(0) >> 4, hb.offset(1) >> 4, hb.offset(2) >> 4};
+    uint32_t parity = 0, chunk = 0;
+    int s = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
       const RowsUnit r = rows_unit(p, o, u);
@@ -702,57 +759,60 @@ __global__ void __launch_bounds__(THREADS, 1)
         continue;
       }
       const int64_t end = min(u1, r.first + r.count);
-      for (; u < end && ok; ++chunk) {
-        const uint32_t buf = chunk % o.accs, d = tmem + buf * o.mtiles * n_all;
-        if (!warp_wait(smem_u32(&c->dempty[buf]), ((chunk / o.accs) & 1) ^ 1, p.ws, abort)) {
+      for (; u < end && ok; ++u, ++chunk) {
+        const uint32_t buf = chunk & 1, d = tmem + buf * o.mtiles * p.rp;
+        if (!warp_wait(smem_u32(&c->dempty[buf]), ((chunk >> 1) & 1) ^ 1, p.ws, abort)) {
           ok = false;
           break;
         }
         fence_after();
-        const int stop = 2 * (int)(min(end, u + CHUNK / TILE_ROWS) - u);
-        for (int i = 0; i < stop; ++i, ++n) {
-          const int s = n % p.stages;
-          if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+        for (int h = 0; h < TILE_ROWS; h += ROW_STAGE) {
+          if (!warp_wait(smem_u32(&c->full[s]), parity, p.ws, abort)) {
             ok = false;
             break;
           }
-          const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * 8192;
+          const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * ROW_BOX;
           const int valid = c->valid[s];
-          if (valid < 64) {
+          if (valid < ROW_STAGE) {
             // rows of other requests behind the tile's own: zeros, so that what they hold stays out
-            for (int k = valid * 8 + lane; k < 64 * 8; k += 32)
-              for (int q = 0; q < a_boxes; ++q) sts128(a + q * 8192 + k * 16, make_uint4(0, 0, 0, 0));
+            for (int k = valid * 8 + lane; k < ROW_STAGE * 8; k += 32)
+              for (int q = 0; q < a_boxes; ++q) sts128(a + q * ROW_BOX + k * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async();
           }
           __syncwarp();
           if (lane == 0) {
             fence_after();
-            for (int mt = 0; mt < o.mtiles; ++mt)
+            uint32_t ad = desc_mn(a, ROW_BOX), dd = d;
+            const uint32_t bd = desc_mn(b, ROW_BOX);
+            for (int mt = 0; mt < o.mtiles; ++mt, ad += 2 * ROW_BOX >> 4, dd += p.rp)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint64_t ad = desc_mn(a + mt * 16384 + j * 2048, 8192);
-                const bool add = i > 0 || j > 0;
-                mma(d + mt * n_all, ad, desc_mn(b + j * 2048, 8192), id_one, add);
-                if (n_two) mma(d + mt * n_all + 256, ad, desc_mn(b + 4 * 8192 + j * 2048, 8192), id_two, add);
-              }
+              for (int j = 0; j < ROW_STAGE / 16; ++j)
+#pragma unroll
+                for (int q = PARTS - 1; q >= 0; --q)  // the small parts first
+                  mma(dd, ad + j * (2048 >> 4), bd + part_at[q] + j * (2048 >> 4), id, h > 0 || j > 0 || q < PARTS - 1);
             mma_commit(smem_u32(&c->empty[s]));
           }
           __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            parity ^= 1;
+          }
         }
-        u += stop / 2;
         if (ok && lane == 0) mma_commit(smem_u32(&c->dfull[buf]));
       }
     }
     if (lane == 0) await_mmas(f, p.ws);
     __syncwarp();
   } else {
-    // Two M tiles: a warp group each, all columns of the rank; one: a half of the columns each.
+    // Sixteen warps: four to the quarters of 128 columns; the four groups take an M tile each (mtiles 4), half
+    // the rank of two, or half of one (then two groups have nothing).
     const int quarter = warp & 3, group = (warp - 2) >> 2;
-    const int mt = o.mtiles == 2 ? group : 0;
-    const int nc = o.mtiles == 2 ? p.rp : p.rp / 2, col0 = o.mtiles == 2 ? 0 : group * nc;
+    const int mt = o.mtiles == 4 ? group : o.mtiles == 2 ? group >> 1 : 0;
+    const int nc = o.mtiles == 4 ? p.rp : o.mtiles == 2 || group < 2 ? p.rp / 2 : 0;
+    const int col0 = o.mtiles == 4 ? 0 : (group & 1) * nc;
     const int m = mt * 128 + quarter * 32 + lane;  // column of x or dy within the output tile
     const int m_all = o.mtiles * 128;
-    uint32_t chunk = 0, turn = 0;
+    uint32_t chunk = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
       const RowsUnit r = rows_unit(p, o, u);
@@ -762,65 +822,70 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const int64_t end = min(u1, r.first + r.count);
       const bool whole = u == r.first && end == r.first + r.count;
-      float acc[80];
+      float acc[64];
 #pragma unroll
-      for (int i = 0; i < 80; ++i) acc[i] = 0.f;
-      for (; u < end; u = min(end, u + CHUNK / TILE_ROWS), ++chunk) {
-        const uint32_t buf = chunk % o.accs;
-        if (!warp_wait(smem_u32(&c->dfull[buf]), (chunk / o.accs) & 1, p.ws, abort)) {
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+      for (; u < end; ++u, ++chunk) {
+        const uint32_t buf = chunk & 1;
+        if (!warp_wait(smem_u32(&c->dfull[buf]), (chunk >> 1) & 1, p.ws, abort)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf * o.mtiles + mt) * n_all + col0;
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf * o.mtiles + mt) * p.rp + col0;
 #pragma unroll
-        for (int i = 0; i < 10; ++i)
-          if (8 * i < nc) {
-            uint32_t v[PARTS][8];
+        for (int i = 0; i < 64; i += 16) {
+          if (i >= nc) break;
+          uint32_t v[16];
+          tmem_ld8(at + i, v);
+          if (i + 8 < nc) tmem_ld8(at + i + 8, v + 8);
+          tmem_wait();
+          pin8(v);
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) tmem_ld8(at + q * p.rp + 8 * i, v[q]);
-            tmem_wait();
+          for (int j = 0; j < 8; ++j) acc[i + j] += __uint_as_float(v[j]);
+          if (i + 8 < nc) {
+            pin8(v + 8);
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) pin8(v[q]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)  // the small parts first
-              acc[8 * i + j] += __uint_as_float(v[0][j]) + (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+            for (int j = 8; j < 16; ++j) acc[i + j] += __uint_as_float(v[j]);
           }
+        }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
       }
       if (!ok) break;
       if (!whole) {
-        const int c0 = cta_of(p.split, r.first), c1 = cta_of(p.split, r.first + r.count - 1);
+        const int c0 = cta_of(p.split, r.first);
         const int64_t slot = (int64_t)m_all * p.rp;
-        float* mine = o.slots + slot_of(blockIdx.x, c0) * slot + (int64_t)col0 * m_all + m;
+        // as the output lies: columns along memory for dA, the rank for dB
+        float* mine = o.slots + slot_of(blockIdx.x, c0) * slot;
+        if (r.problem) {
+          mine += (int64_t)m * p.rp + col0;
 #pragma unroll
-        for (int i = 0; i < 80; ++i)
-          if (i < nc) mine[(int64_t)i * m_all] = acc[i];
-        if (!count_in(c, ws_u32(p.ws, WS_TICKETS_ROWS) + c0, c1 - c0 + 1, turn, ok, p.ws)) continue;
+          for (int i = 0; i < 64; i += 4)
+            if (i < nc) *reinterpret_cast<float4*>(mine + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        } else {
+          mine += col0 * m_all + m;
 #pragma unroll
-        for (int i = 0; i < 80; ++i) acc[i] = 0.f;
-        for (int k = c0; k <= c1; ++k) {
-          const float* part = o.slots + slot_of(k, c0) * slot + (int64_t)col0 * m_all + m;
-#pragma unroll
-          for (int i = 0; i < 80; i += 16)
-            if (i < nc) {  // nc is a multiple of 8
-              float v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = i + j < nc ? __ldcg(part + (int64_t)(i + j) * m_all) : 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) acc[i + j] += v[j];
-            }
+          for (int i = 0; i < 64; ++i)
+            if (i < nc) mine[i * m_all] = acc[i];
         }
+        continue;
       }
-      const Grad& g = o.g[r.problem];
-      const int64_t col = r.block * m_all + m;
-      if (col < g.width) {
-        float* out = g.out + (int64_t)r.g * p.rank * g.width + col * g.col_stride + col0 * g.rank_stride;
+      const int64_t col = r.block * m_all + m, width = r.problem ? o.g[1].width : o.g[0].width;
+      if (col < width) {
+        float* out = (r.problem ? o.g[1].out : o.g[0].out) + (int64_t)r.g * p.rank * width;
+        if (r.problem) {  // dB: the rank runs along memory, and is a multiple of 8
+          out += col * p.rank + col0;
 #pragma unroll
-        for (int i = 0; i < 80; ++i)
-          if (i < nc && col0 + i < p.rank) out[i * g.rank_stride] = acc[i];
+          for (int i = 0; i < 64; i += 4)
+            if (i < nc && col0 + i < p.rank) *reinterpret_cast<float4*>(out + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        } else {
+          out += col + col0 * width;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < nc && col0 + i < p.rank) out[i * width] = acc[i];
+        }
       }
     }
   }
@@ -828,11 +893,39 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int g = blockIdx.x; g < p.n_adapters; g += gridDim.x) {
     if (o.first[g] != o.first[g + 1]) continue;
     for (int q = 0; q < 2; ++q) {
-      float4* out = reinterpret_cast<float4*>(o.g[q].out + (int64_t)g * p.rank * o.g[q].width);
-      for (int64_t i = threadIdx.x; i < p.rank * o.g[q].width / 4; i += THREADS) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int64_t n = p.rank * (q ? o.g[1].width : o.g[0].width);
+      float4* out = reinterpret_cast<float4*>((q ? o.g[1].out : o.g[0].out) + g * n);
+      for (int64_t i = threadIdx.x; i < n / 4; i += ROW_THREADS) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   finish(f, COLS);
+}
+
+// The output tiles that several CTAs share: four values to a thread.
+__global__ void __launch_bounds__(256) k_over_rows_sum(Args p, OverRows o) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int m_all = o.mtiles * 128, ctas = m_all * p.rp / 1024;
+  const int64_t i = blockIdx.x / ctas, outputs0 = o.g[0].blocks * p.n_adapters;
+  const int e = blockIdx.x % ctas * 256 + threadIdx.x;
+  const bool second = i >= outputs0;
+  const int64_t blocks = second ? o.g[1].blocks : o.g[0].blocks, v = second ? i - outputs0 : i, g = v / blocks, block = v % blocks;
+  const int64_t width = second ? o.g[1].width : o.g[0].width;
+  const int64_t f0 = o.first[g], f1 = o.first[g + 1];
+  if (f0 < 0 || f0 >= f1 || f1 > p.n_tiles) return;
+  const int64_t first = (second ? o.g[0].blocks * p.n_tiles : 0) + blocks * f0 + block * (f1 - f0);
+  const int c0 = cta_of(p.split, first), c1 = cta_of(p.split, first + f1 - f0 - 1);
+  if (c0 == c1) return;
+  const float4 sum = sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e);
+  if (second) {
+    const int64_t col = block * m_all + e / (p.rp / 4);
+    const int j = e % (p.rp / 4) * 4;
+    if (col < width && j < p.rank) *reinterpret_cast<float4*>(o.g[1].out + (g * width + col) * p.rank + j) = sum;
+  } else {
+    const int j = e / (m_all / 4);
+    const int64_t col = block * m_all + e % (m_all / 4) * 4;
+    if (j < p.rank && col < width) *reinterpret_cast<float4*>(o.g[0].out + (g * p.rank + j) * width + col) = sum;
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -887,9 +980,12 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   p.parts = parts;
   p.stages = stages_for(RING_BYTES, 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128));
   p.split = split_to_rank(p.n_tiles, o.blocks);
-  return launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) == cudaSuccess
-             ? DIT_OK
-             : DIT_ERR_CUDA;
+  if (launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) != cudaSuccess)
+    return DIT_ERR_CUDA;
+  if (p.split.grain == 1 && p.split.ctas > 1 &&  // shares may end inside tiles
+      launch_pdl(k_to_rank_sum, dim3((unsigned)(p.n_tiles * (TILE_ROWS * p.rp / 1024))), dim3(256), 0, st, 1, p, o) != cudaSuccess)
+    return DIT_ERR_CUDA;
+  return DIT_OK;
 }
 
 // out += held W; MN: w is [n_adapters][rank][width], else [n_adapters][width][rank]; held has `held_parts` parts
@@ -978,23 +1074,49 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   if (s == DIT_OK && dx) s = from_rank<true>(p, scratch, PARTS, a, dx, dx_dt, k, st);
   if (s != DIT_OK) return s;
 
-  const int mtiles = grad_mtiles(p.rp), m_all = 128 * mtiles;
   OverRows o{};
-  o.g[0] = Grad{reinterpret_cast<const __nv_bfloat16*>(scratch), da, k, (k + m_all - 1) / m_all, k, 1};
-  o.g[1] = Grad{reinterpret_cast<const __nv_bfloat16*>(saved), db, n, (n + m_all - 1) / m_all, 1, rank};
   o.first = table + off_first(*plan);
   o.slots = reinterpret_cast<float*>(slots);
-  o.mtiles = mtiles;
-  o.accs = 2 * mtiles * PARTS * p.rp <= 512 ? 2 : 1;
+  // The cut of the work, by what a CTA has to move in each (bytes; the widths of the output tiles, whole
+  // output tiles or equal shares of the units): a share that ends inside an output tile costs
+  // its last CTA a round through memory (about SHARED bytes of its time) and the partial results.
+  {
+    constexpr int64_t SHARED = 200 * 1024;
+    const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
+    int64_t best = -1;
+    for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
+      const int64_t bk = (k + 128 * mt - 1) / (128 * mt), bn = (n + 128 * mt - 1) / (128 * mt);
+      const int64_t unit = (2 * mt + boxes) * 16384, outputs = (bk + bn) * p.n_adapters, units = (bk + bn) * p.n_tiles;
+      const int64_t ctas = units < sms ? units : sms, share = (units + ctas - 1) / ctas * unit;
+      const int64_t slot = (int64_t)mt * 128 * p.rp * 4;
+      const int64_t cost[2] = {share + SHARED + (ctas + bk + bn - 1) / (bk + bn) * slot / 2,
+                               (outputs + sms - 1) / sms * plan->most_tiles * unit};
+      for (int whole = 0; whole < 2; ++whole)
+        if (best < 0 || cost[whole] < best) {
+          best = cost[whole];
+          o.mtiles = mt;
+          o.whole = whole;
+          o.g[0] = Grad{da, k, bk};
+          o.g[1] = Grad{db, n, bn};
+          p.split = split_units(units, 1, 1, (int)sms);
+          if (whole) p.split.ctas = (int)(outputs < p.split.ctas ? outputs : p.split.ctas);
+        }
+    }
+  }
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
-  if (!map_rows(&m_x, x, k, p.rows, 64) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, 64) ||
-      !map_rows(&m_dy, dy, n, p.rows, 64) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, 64) || !allow_smem<k_over_rows>())
+  if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
+      !map_rows(&m_dy, dy, n, p.rows, ROW_STAGE) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, ROW_STAGE) ||
+      !allow_smem<k_over_rows>())
     return DIT_ERR_CUDA;
-  p.stages = stages_for(RING_BYTES, (2 * mtiles + (PARTS * p.rp + 63) / 64) * 8192);
-  p.split = split_units((o.g[0].blocks + o.g[1].blocks) * p.n_tiles, 1, 1, num_sms());
-  return launch_pdl(k_over_rows, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) ==
-                 cudaSuccess
-             ? DIT_OK
-             : DIT_ERR_CUDA;
+  const int h_boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
+  p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
+  if (launch_pdl(k_over_rows, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
+    return DIT_ERR_CUDA;
+  const int64_t outputs = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters;
+  if (!o.whole && p.split.ctas > 1 &&
+      launch_pdl(k_over_rows_sum, dim3((unsigned)(outputs * (o.mtiles * 128 * p.rp / 1024))), dim3(256), 0, st, 1, p, o) !=
+          cudaSuccess)
+    return DIT_ERR_CUDA;
+  return DIT_OK;
 }

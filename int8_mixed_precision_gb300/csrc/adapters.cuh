@@ -36,10 +36,9 @@ inline size_t held_bytes(int64_t n_tiles, int rank) {
 }
 
 // Work is a list of `units` that `ctas` CTAs take in contiguous shares of equal numbers of grains
-// (`grain` units each); an output whose units fall to several CTAs is summed from their partial
-// results by the last one to finish, in the order of the CTAs, so the sum does not depend on
-// which one that is.  A CTA has at most two shared outputs (its first and its last), hence two
-// slots for partial results.
+// (`grain` units each).  The CTAs of an output whose units fall to several write partial results, which a
+// second kernel adds up in the order of the CTAs.  A CTA has at most two shared outputs (its
+// first and its last), hence two slots.
 struct Split {
   int64_t units, grain;
   int ctas;
@@ -59,12 +58,9 @@ __host__ __device__ __forceinline__ int cta_of(const Split& s, int64_t unit) {
   return (int)(((unit / s.grain + 1) * s.ctas - 1) / (s.units / s.grain));
 }
 
-// The columns of x or dy that one output tile of a weight gradient covers: two instructions' M of 128,
-// or one where the accumulators of two (PARTS x rp columns each) exceed the 512 of tensor memory.
-inline int grad_mtiles(int rp) { return 2 * PARTS * rp <= 512 ? 2 : 1; }
-
+// Partial results: 128 rows by the rank of h and e; up to 512 columns by the rank of the gradients.
 inline size_t slot_bytes(int rp, bool training) {
-  return (size_t)2 * MAX_CTAS * TILE_ROWS * (training ? grad_mtiles(rp) : 1) * rp * 4;
+  return (size_t)2 * MAX_CTAS * TILE_ROWS * (training ? (rp <= 64 ? 4 : 2) : 1) * rp * 4;
 }
 
 struct Tile {
@@ -83,13 +79,6 @@ __device__ __forceinline__ Tile load_tile(const int32_t* table, int64_t t, int64
   return check_tile(reinterpret_cast<const int4*>(table)[t], rows, n_adapters, ws);
 }
 
-// Completion counters of shared outputs, in the workspace: a call's first kernel leaves those of the
-// later ones at zero and the other way round, so that they are zero again even after a wait
-// that ran out.
-constexpr size_t WS_TICKETS_RANK = 33280;                            // products to the rank
-constexpr size_t WS_TICKETS_ROWS = WS_TICKETS_RANK + 4 * MAX_CTAS;   // products over the rows
-static_assert(WS_TICKETS_RANK >= WS_PARTIALS + 32 * MAX_RED_CTAS && WS_TICKETS_ROWS + 4 * MAX_CTAS <= WS_BYTES, "");
-
 bool plan_ok(const dit_adapter_plan_t* p);
 dit_status small_tiles(const dit_adapter_plan_t& plan, const int32_t* table, const void* x, const void* a, const void* b,
                        const float* scale, int rank, int64_t k, int64_t n, void* y, dit_dtype y_dt, void* ws,
@@ -101,28 +90,28 @@ dit_status check_common(const dit_adapter_plan_t* plan, const int32_t* table, co
 // ---------------------------------------------------------------------------------------
 // tcgen05 of one CTA: operands in 128-byte swizzled shared memory, bf16 x bf16 -> fp32
 // ---------------------------------------------------------------------------------------
-// Rows of 64 bf16 along the contraction (K-major): 8-row groups of 1024 bytes; a step of 16 along
-// the contraction is 32 bytes.
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-// Rows of 64 bf16 along M or N, one for each index of the contraction (MN-major): 8-row groups of
-// 1024 bytes, the next 64 of M or N `chunk` bytes on; a step of 16 along the contraction is
-// 16 rows, 2048 bytes.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(chunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Operand descriptors.  Their upper words are constants and the lower ones advance by bytes / 16, so the
+// issuing thread makes a tile's descriptors by one addition each: it issues an instruction every
+// few dozen cycles, and forming 64-bit descriptors anew cost more than the MMAs themselves.
+//
+// K-major: rows of 64 bf16 along the contraction, in groups of 8 rows (1024 bytes); a step of 16
+// along the contraction is 32 bytes.  MN-major: rows of 64 bf16 along M or N, one for each index
+// of the contraction, in groups of 8; the next 64 of M or N are `chunk` bytes on; a step of 16
+// along the contraction is 16 rows, 2048 bytes.
+constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t chunk) {
+  return (saddr & 0x3FFFFu) >> 4 | (chunk >> 4) << 16;
 }
 __host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate ? 1u : 0u)
+      "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(DESC_HI)
       : "memory");
 }
 // arrives on `bar` when every MMA issued so far by this thread has completed
