@@ -786,10 +786,13 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
             const uint32_t bd = desc_mn(b, ROW_BOX);
             for (int mt = 0; mt < o.mtiles; ++mt, ad += 2 * ROW_BOX >> 4, dd += p.rp)
 #pragma unroll
-              for (int j = 0; j < ROW_STAGE / 16; ++j)
-#pragma unroll
-                for (int q = PARTS - 1; q >= 0; --q)  // the small parts first
-                  mma(dd, ad + j * (2048 >> 4), bd + part_at[q] + j * (2048 >> 4), id, h > 0 || j > 0 || q < PARTS - 1);
+              for (int j = 0; j < ROW_STAGE / 16; ++j) {  // the small parts first
+                const uint32_t aj = ad + j * (2048 >> 4), bj = bd + j * (2048 >> 4);
+                static_assert(PARTS == 3, "three MMAs with one A");
+                mma<KEEP_FIRST>(dd, aj, bj + part_at[2], id, h > 0 || j > 0);
+                mma<KEEP_MIDDLE>(dd, aj, bj + part_at[1], id, true);
+                mma<KEEP_LAST>(dd, aj, bj + part_at[0], id, true);
+              }
             mma_commit(smem_u32(&c->empty[s]));
           }
           __syncwarp();

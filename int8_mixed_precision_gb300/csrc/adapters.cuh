@@ -107,13 +107,27 @@ __host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn)
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// What becomes of the A operand in the tensor core's buffer: consecutive MMAs with one A read it from
+// shared memory once (the first keeps it, the middle ones use it, the last one uses and drops it).
+enum Keep { KEEP_NOT, KEEP_FIRST, KEEP_MIDDLE, KEEP_LAST };
+#define DIT_LORA_MMA(collector)                                                                                  \
+  asm volatile(                                                                                                  \
+      "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5};\n"        \
+      "tcgen05.mma.cta_group::1.kind::f16" collector " [%0], x, y, %3, p; }" ::"r"(d),                           \
+      "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(DESC_HI)                                           \
+      : "memory")
+template <int KEEP = KEEP_NOT>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
-  asm volatile(
-      "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5};\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(DESC_HI)
-      : "memory");
+  if (KEEP == KEEP_FIRST)
+    DIT_LORA_MMA(".collector::a::fill");
+  else if (KEEP == KEEP_MIDDLE)
+    DIT_LORA_MMA(".collector::a::use");
+  else if (KEEP == KEEP_LAST)
+    DIT_LORA_MMA(".collector::a::lastuse");
+  else
+    DIT_LORA_MMA("");
 }
+#undef DIT_LORA_MMA
 // arrives on `bar` when every MMA issued so far by this thread has completed
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
