@@ -215,26 +215,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) await_copies(f, p.stages, n, p.ws);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc(128, p.rp, false, MN);
-      uint32_t chunk = 0, parity = 0;
-      int s = 0;
-      bool ok = true;
-      for (int64_t u = u0; u < u1 && ok;) {
-        const int64_t end = min(u1, (u / o.blocks + 1) * o.blocks);  // of this tile's share
-        for (; u < end && ok; ++chunk) {
-          const int buf = chunk & 1;
-          if (!mbar_wait(smem_u32(&c->dempty[buf]), ((chunk >> 1) & 1) ^ 1, p.ws, abort)) {
+    const uint32_t id = idesc(128, p.rp, false, MN);
+    uint32_t chunk = 0, parity = 0;
+    int s = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int64_t end = min(u1, (u / o.blocks + 1) * o.blocks);  // of this tile's share
+      for (; u < end && ok; ++chunk) {
+        const int buf = chunk & 1;
+        if (!warp_wait(smem_u32(&c->dempty[buf]), ((chunk >> 1) & 1) ^ 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        const int64_t stop = min(end, u + CHUNK / 64);
+        for (int64_t first = u; u < stop; ++u) {
+          if (!warp_wait(smem_u32(&c->full[s]), parity, p.ws, abort)) {
             ok = false;
             break;
           }
-          fence_after();
-          const int64_t stop = min(end, u + CHUNK / 64);
-          for (int64_t first = u; u < stop; ++u) {
-            if (!mbar_wait(smem_u32(&c->full[s]), parity, p.ws, abort)) {
-              ok = false;
-              break;
-            }
+          if (elect_one()) {
             fence_after();
             const uint32_t at = f.smem + s * stage_bytes;
             const uint32_t a = desc_k(at), b = MN ? desc_mn(at + 16384, 8192) : desc_k(at + 16384);
@@ -242,16 +241,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < 4; ++j)
               mma(tmem + buf * 128, a + j * (32 >> 4), b + j * ((MN ? 2048 : 32) >> 4), id, u > first || j > 0);
             mma_commit(smem_u32(&c->empty[s]));
-            if (++s == p.stages) {
-              s = 0;
-              parity ^= 1;
-            }
+            if (u + 1 == stop) mma_commit(smem_u32(&c->dfull[buf]));
           }
-          if (ok) mma_commit(smem_u32(&c->dfull[buf]));
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            parity ^= 1;
+          }
         }
       }
-      await_mmas(f, p.ws);
     }
+    if (elect_one()) await_mmas(f, p.ws);
     __syncwarp();
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -399,45 +399,52 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   auto panels_of = [&](int b) { return (int)min((int64_t)o.nb / PC, (o.width - (int64_t)b * o.nb + PC - 1) / PC); };
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall) {
+    if (!p.stall) {  // a lane to each box
       uint32_t n = 0, tiles = 0, np = 0;
+      int s = 0, q = 0;
+      uint32_t sp = 1, qp = 1;  // parities of the rings' next waits
       bool ok = true;
       Tile t{0, 0, 0};
       for (int64_t u = u0; u < u1 && ok; ++u) {
         const int n0 = block * o.nb;
         if (u == u0 || block == 0) {
           t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-          if (!mbar_wait(smem_u32(&c->hempty), (tiles & 1) ^ 1, p.ws, abort)) {
+          if (!warp_wait(smem_u32(&c->hempty), (tiles & 1) ^ 1, p.ws, abort)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(smem_u32(&c->hfull), h_boxes * 16384);
-          for (int i = 0; i < h_boxes; ++i)
-            tma_load_2d(f.smem + i * 16384, &m_held, smem_u32(&c->hfull), i * 64, (int)(ti * TILE_ROWS));
+          if (lane == 0) mbar_expect_tx(smem_u32(&c->hfull), h_boxes * 16384);
+          __syncwarp();
+          if (lane < h_boxes) tma_load_2d(f.smem + lane * 16384, &m_held, smem_u32(&c->hfull), lane * 64, (int)(ti * TILE_ROWS));
           ++tiles;
         }
-        const int s = n % p.stages;
-        if (!mbar_wait(smem_u32(&c->empty[s]), ((n / p.stages) & 1) ^ 1, p.ws, abort)) {
+        if (!warp_wait(smem_u32(&c->empty[s]), sp, p.ws, abort)) {
           ok = false;
           break;
         }
-        const uint32_t full = smem_u32(&c->full[s]), dst = ring + s * w_bytes;
-        mbar_expect_tx(full, w_bytes);
-        for (int i = 0; i < w_boxes; ++i) {
-          if (MN)
-            tma_load_3d(dst + i * box_bytes, &m_w, full, n0 + i * 64, 0, t.g);
-          else
-            tma_load_3d(dst + i * box_bytes, &m_w, full, i * 64, n0, t.g);
-        }
+        const uint32_t full = smem_u32(&c->full[s]);
+        if (lane == 0) mbar_expect_tx(full, w_bytes);
+        __syncwarp();
+        if (lane < w_boxes)
+          tma_load_3d(ring + s * w_bytes + lane * box_bytes, &m_w, full, MN ? n0 + lane * 64 : lane * 64, MN ? 0 : n0, t.g);
         ++n;
+        if (++s == p.stages) {
+          s = 0;
+          sp ^= 1;
+        }
         for (int i = 0, all = panels_of(block); i < all; ++i, ++np) {
-          const int q = np % o.panels;
-          if (!mbar_wait(smem_u32(&c->yempty[q]), ((np / o.panels) & 1) ^ 1, p.ws, abort)) {
+          if (!warp_wait(smem_u32(&c->yempty[q]), qp, p.ws, abort)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
-          tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
+          if (lane == 0) {
+            mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
+            tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
+          }
+          if (++q == o.panels) {
+            q = 0;
+            qp ^= 1;
+          }
         }
         if (++block == o.n_blocks) {
           block = 0;
@@ -453,19 +460,19 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc(128, o.nb, false, MN);
-      uint32_t n = 0, tiles = 0;
-      const int rank_steps = p.rp / 16;
-      for (int64_t u = u0; u < u1; ++u, ++n) {
-        const int buf = n % ACCS, s = n % p.stages;
-        if (u == u0 || block == 0) {
-          if (!mbar_wait(smem_u32(&c->hfull), tiles & 1, p.ws, abort)) break;
-          ++tiles;
-        }
-        if (++block == o.n_blocks) block = 0;
-        if (!mbar_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort)) break;
-        if (!mbar_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
+    const uint32_t id = idesc(128, o.nb, false, MN);
+    uint32_t n = 0, tiles = 0;
+    const int rank_steps = p.rp / 16;
+    for (int64_t u = u0; u < u1; ++u, ++n) {
+      const int buf = n % ACCS, s = n % p.stages;
+      if (u == u0 || block == 0) {
+        if (!warp_wait(smem_u32(&c->hfull), tiles & 1, p.ws, abort)) break;
+        ++tiles;
+      }
+      if (++block == o.n_blocks) block = 0;
+      if (!warp_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort)) break;
+      if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
+      if (elect_one()) {
         fence_after();
         const uint32_t b0 = MN ? desc_mn(ring + s * w_bytes, box_bytes) : desc_k(ring + s * w_bytes);
         const uint32_t a0 = desc_k(f.smem);
@@ -479,8 +486,9 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
         mma_commit(smem_u32(&c->dfull[buf]));
         if (block == 0) mma_commit(smem_u32(&c->hempty));
       }
-      await_mmas(f, p.ws);
+      __syncwarp();
     }
+    if (elect_one()) await_mmas(f, p.ws);
     __syncwarp();
   } else if (warp < 2 + EPI_WARPS) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -780,7 +788,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
             fence_proxy_async();
           }
           __syncwarp();
-          if (lane == 0) {
+          if (elect_one()) {
             fence_after();
             uint32_t ad = desc_mn(a, ROW_BOX), dd = d;
             const uint32_t bd = desc_mn(b, ROW_BOX);
@@ -801,10 +809,10 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
             parity ^= 1;
           }
         }
-        if (ok && lane == 0) mma_commit(smem_u32(&c->dfull[buf]));
+        if (ok && elect_one()) mma_commit(smem_u32(&c->dfull[buf]));
       }
     }
-    if (lane == 0) await_mmas(f, p.ws);
+    if (elect_one()) await_mmas(f, p.ws);
     __syncwarp();
   } else {
     // Sixteen warps: four to the quarters of 128 columns; the four groups take an M tile each (mtiles 4), half
