@@ -45,15 +45,19 @@ struct Args {
   int stall;
 };
 
+constexpr int JOBS = 4;                     // announced ahead in k_from_rank
+
 // Barriers and flags behind the operands in shared memory.
 struct Control {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t dfull[ACCS], dempty[ACCS];  // accumulators
-  uint64_t hfull, hempty;              // the tile of held (k_from_rank)
+  uint64_t hfull[2], hempty[2];        // tiles of held (k_from_rank)
+  uint64_t jfull[JOBS], jempty[JOBS];  // jobs (k_from_rank)
   uint64_t yfull[MAX_PANELS], ydone[MAX_PANELS], yempty[MAX_PANELS];  // panels of the output: loaded, updated, stored
   uint64_t done;
   uint32_t tmem;
   int abort;
+  int job[JOBS];
   int valid[MAX_STAGES];               // rows of a stage that belong to its tile (k_over_rows)
 };
 
@@ -83,8 +87,14 @@ __device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols,
       mbar_init(smem_u32(&c->ydone[b]), EPI_WARPS);
       mbar_init(smem_u32(&c->yempty[b]), 1);
     }
-    mbar_init(smem_u32(&c->hfull), 1);
-    mbar_init(smem_u32(&c->hempty), 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&c->hfull[b]), 1);
+      mbar_init(smem_u32(&c->hempty[b]), 1);
+    }
+    for (int b = 0; b < JOBS; ++b) {
+      mbar_init(smem_u32(&c->jfull[b]), 1);
+      mbar_init(smem_u32(&c->jempty[b]), 2 + epi_warps);  // the MMA, epilogue and store warps
+    }
     mbar_init(smem_u32(&c->done), 1);
     c->abort = 0;
     fence_barrier_init();
@@ -176,6 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws_u32(p.ws, WS_JOBS) = 0;  // for the next k_from_rank
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w_chunks = MN ? (p.rank + 63) / 64 : 1;
@@ -349,18 +360,47 @@ __global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
 // ---------------------------------------------------------------------------------------
 // From the rank: out += held W, out [rows x width], W = B^T (K-major) or A (MN-major).
 //
-// The tile of held stays in shared memory for all its units; weights come through a ring, and so do
-// the output's panels (128 rows x 128 bytes): loaded by TMA well ahead of the accumulators,
-// updated in place and stored by TMA, so that neither direction waits for the other.  With a row
-// to each thread, loads and stores straight to global memory took one wavefront per 32 bytes
-// and the kernel ran at 3.6 TB/s, bound by them.  Panels of a tile that ends inside them are
-// stored row by row, so that rows of other requests are never written.
+// A job is a few consecutive blocks of columns of one tile.  CTAs take jobs from a counter: with equal
+// shares the fastest SM was done after 138 us and the slowest after 190 (two videos), since SMs
+// differ in their way to memory.  The tile of held stays in shared memory for its job; weights
+// come through a ring, and so do the output's panels (128 rows x 128 bytes): loaded by TMA well
+// ahead of the accumulators, updated in place and stored by TMA, so that neither direction waits
+// for the other.  With a row to each thread, loads and stores straight to global memory took one
+// wavefront per 32 bytes and the kernel ran at 3.6 TB/s, bound by them.  Panels of a tile that
+// ends inside them are stored row by row, so that rows of other requests are never written.
 // ---------------------------------------------------------------------------------------
 struct FromRank {
   void* out;
   int64_t width;
-  int nb, n_blocks;  // columns of a unit (64 or 128), units along the width
-  int panels;        // of the ring
+  int nb, n_blocks;  // columns of a block (64 or 128), blocks along the width
+  int per_job;       // blocks
+  int64_t jobs, tile_jobs;  // all, and of a tile
+  int panels, helds; // of the rings
+};
+// Where a job begins, and its blocks.
+struct Job {
+  int64_t tile;
+  int block, blocks;
+  __device__ __forceinline__ Job(const FromRank& o, int64_t j) {
+    tile = j / o.tile_jobs;
+    block = (int)(j % o.tile_jobs) * o.per_job;
+    blocks = min(o.per_job, o.n_blocks - block);
+  }
+};
+// The jobs as a consuming warp sees them: the next one's number, or -1 (no more, or a wait ran out).
+struct JobQueue {
+  Control* c;
+  void* ws;
+  uint32_t n;
+  __device__ __forceinline__ int next() {
+    const int s = n % JOBS;
+    if (!warp_wait(smem_u32(&c->jfull[s]), (n / JOBS) & 1, ws, &c->abort)) return -1;
+    const int job = *reinterpret_cast<volatile int*>(&c->job[s]);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&c->jempty[s]));
+    ++n;
+    return job;
+  }
 };
 
 constexpr int FROM_THREADS = THREADS + 32;  // and a warp that stores
@@ -389,72 +429,85 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   const int h_boxes = (p.parts * p.rp + 63) / 64;  // of 128 rows x 64 columns, 16 KB each
   const int w_boxes = MN ? o.nb / 64 : (p.rank + 63) / 64;
   const uint32_t box_bytes = MN ? p.rp * 128 : o.nb * 128;
-  const uint32_t w_bytes = w_boxes * box_bytes;
-  const uint32_t ring = f.smem + h_boxes * 16384, panels = ring + p.stages * w_bytes;
+  const uint32_t w_bytes = w_boxes * box_bytes, h_bytes = h_boxes * 16384;
+  const uint32_t ring = f.smem + o.helds * h_bytes, panels = ring + p.stages * w_bytes;
   constexpr int ES = BF16 ? 2 : 4, PC = 128 / ES;  // columns of a panel
-  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
-  int64_t ti = u0 / o.n_blocks;
-  int block = (int)(u0 % o.n_blocks);
-  // panels of the block (the last one may have fewer)
+  // panels of a block (the last one may have fewer)
   auto panels_of = [&](int b) { return (int)min((int64_t)o.nb / PC, (o.width - (int64_t)b * o.nb + PC - 1) / PC); };
 
   if (warp == 0) {
     if (!p.stall) {  // a lane to each box
-      uint32_t n = 0, tiles = 0, np = 0;
+      uint32_t n = 0, tiles = 0, np = 0, announced = 0;
       int s = 0, q = 0;
       uint32_t sp = 1, qp = 1;  // parities of the rings' next waits
       bool ok = true;
-      Tile t{0, 0, 0};
-      for (int64_t u = u0; u < u1 && ok; ++u) {
-        const int n0 = block * o.nb;
-        if (u == u0 || block == 0) {
-          t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-          if (!warp_wait(smem_u32(&c->hempty), (tiles & 1) ^ 1, p.ws, abort)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_expect_tx(smem_u32(&c->hfull), h_boxes * 16384);
-          __syncwarp();
-          if (lane < h_boxes) tma_load_2d(f.smem + lane * 16384, &m_held, smem_u32(&c->hfull), lane * 64, (int)(ti * TILE_ROWS));
-          ++tiles;
-        }
-        if (!warp_wait(smem_u32(&c->empty[s]), sp, p.ws, abort)) {
+      int64_t job = blockIdx.x;
+      while (ok) {
+        const int js = announced % JOBS;
+        if (!warp_wait(smem_u32(&c->jempty[js]), ((announced / JOBS) & 1) ^ 1, p.ws, abort)) {
           ok = false;
           break;
         }
-        const uint32_t full = smem_u32(&c->full[s]);
-        if (lane == 0) mbar_expect_tx(full, w_bytes);
-        __syncwarp();
-        if (lane < w_boxes)
-          tma_load_3d(ring + s * w_bytes + lane * box_bytes, &m_w, full, MN ? n0 + lane * 64 : lane * 64, MN ? 0 : n0, t.g);
-        ++n;
-        if (++s == p.stages) {
-          s = 0;
-          sp ^= 1;
+        const bool more = job < o.jobs;
+        // the job after this one: its number is on its way while this one is loaded
+        unsigned next = 0;
+        if (lane == 0) {
+          c->job[js] = more ? (int)job : -1;
+          mbar_arrive(smem_u32(&c->jfull[js]));
+          if (more) next = atomicAdd(ws_u32(p.ws, WS_JOBS), 1u);
         }
-        for (int i = 0, all = panels_of(block); i < all; ++i, ++np) {
-          if (!warp_wait(smem_u32(&c->yempty[q]), qp, p.ws, abort)) {
+        ++announced;
+        if (!more) break;
+        const Job j(o, job);
+        const Tile t = load_tile(p.table, j.tile, p.rows, p.n_adapters, p.ws);
+        const int hs = tiles % o.helds;
+        if (!warp_wait(smem_u32(&c->hempty[hs]), ((tiles / o.helds) & 1) ^ 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_expect_tx(smem_u32(&c->hfull[hs]), h_bytes);
+        __syncwarp();
+        if (lane < h_boxes)
+          tma_load_2d(f.smem + hs * h_bytes + lane * 16384, &m_held, smem_u32(&c->hfull[hs]), lane * 64, (int)(j.tile * TILE_ROWS));
+        ++tiles;
+        for (int b = j.block; b < j.block + j.blocks && ok; ++b) {
+          const int n0 = b * o.nb;
+          if (!warp_wait(smem_u32(&c->empty[s]), sp, p.ws, abort)) {
             ok = false;
             break;
           }
-          if (lane == 0) {
-            mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
-            tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
+          const uint32_t full = smem_u32(&c->full[s]);
+          if (lane == 0) mbar_expect_tx(full, w_bytes);
+          __syncwarp();
+          if (lane < w_boxes)
+            tma_load_3d(ring + s * w_bytes + lane * box_bytes, &m_w, full, MN ? n0 + lane * 64 : lane * 64, MN ? 0 : n0, t.g);
+          ++n;
+          if (++s == p.stages) {
+            s = 0;
+            sp ^= 1;
           }
-          if (++q == o.panels) {
-            q = 0;
-            qp ^= 1;
+          for (int i = 0, all = panels_of(b); i < all; ++i, ++np) {
+            if (!warp_wait(smem_u32(&c->yempty[q]), qp, p.ws, abort)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
+              tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
+            }
+            if (++q == o.panels) {
+              q = 0;
+              qp ^= 1;
+            }
           }
         }
-        if (++block == o.n_blocks) {
-          block = 0;
-          ++ti;
-        }
+        job = (int64_t)__shfl_sync(0xffffffffu, next, 0) + gridDim.x;
       }
       if (!ok) {
         await_copies(f, p.stages, n, p.ws);
         volatile int never = 0;
-        if (tiles) mbar_wait(smem_u32(&c->hfull), (tiles - 1) & 1, p.ws, &never);
+        for (uint32_t i = tiles > (uint32_t)o.helds ? tiles - o.helds : 0; i < tiles; ++i)
+          mbar_wait(smem_u32(&c->hfull[i % o.helds]), (i / o.helds) & 1, p.ws, &never);
         for (uint32_t i = np > (uint32_t)o.panels ? np - o.panels : 0; i < np; ++i)
           mbar_wait(smem_u32(&c->yfull[i % o.panels]), (i / o.panels) & 1, p.ws, &never);
       }
@@ -463,130 +516,147 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
     const uint32_t id = idesc(128, o.nb, false, MN);
     uint32_t n = 0, tiles = 0;
     const int rank_steps = p.rp / 16;
-    for (int64_t u = u0; u < u1; ++u, ++n) {
-      const int buf = n % ACCS, s = n % p.stages;
-      if (u == u0 || block == 0) {
-        if (!warp_wait(smem_u32(&c->hfull), tiles & 1, p.ws, abort)) break;
-        ++tiles;
-      }
-      if (++block == o.n_blocks) block = 0;
-      if (!warp_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort)) break;
-      if (!warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) break;
-      if (elect_one()) {
-        fence_after();
-        const uint32_t b0 = MN ? desc_mn(ring + s * w_bytes, box_bytes) : desc_k(ring + s * w_bytes);
-        const uint32_t a0 = desc_k(f.smem);
-        int j = 0;
-        for (int q = 0; q < steps; ++q) {  // every part meets the same weights
-          const uint32_t b = b0 + (MN ? j * (2048 >> 4) : (j / 4) * (box_bytes >> 4) + (j % 4) * (32 >> 4));
-          mma(tmem + buf * 128, a0 + (q / 4) * (16384 >> 4) + (q % 4) * (32 >> 4), b, id, q > 0);
-          if (++j == rank_steps) j = 0;
+    JobQueue queue{c, p.ws, 0};
+    bool ok = true;
+    for (int job; ok && (job = queue.next()) >= 0; ++tiles) {
+      const Job j(o, job);
+      const int hs = tiles % o.helds;
+      if (!warp_wait(smem_u32(&c->hfull[hs]), (tiles / o.helds) & 1, p.ws, abort)) break;
+      for (int i = 0; i < j.blocks; ++i, ++n) {
+        const int buf = n % ACCS, s = n % p.stages;
+        if (!warp_wait(smem_u32(&c->dempty[buf]), ((n / ACCS) & 1) ^ 1, p.ws, abort) ||
+            !warp_wait(smem_u32(&c->full[s]), (n / p.stages) & 1, p.ws, abort)) {
+          ok = false;
+          break;
         }
-        mma_commit(smem_u32(&c->empty[s]));
-        mma_commit(smem_u32(&c->dfull[buf]));
-        if (block == 0) mma_commit(smem_u32(&c->hempty));
+        if (elect_one()) {
+          fence_after();
+          const uint32_t b0 = MN ? desc_mn(ring + s * w_bytes, box_bytes) : desc_k(ring + s * w_bytes);
+          const uint32_t a0 = desc_k(f.smem + hs * h_bytes);
+          int k = 0;
+          for (int q = 0; q < steps; ++q) {  // every part meets the same weights
+            const uint32_t b = b0 + (MN ? k * (2048 >> 4) : (k / 4) * (box_bytes >> 4) + (k % 4) * (32 >> 4));
+            mma(tmem + buf * 128, a0 + (q / 4) * (16384 >> 4) + (q % 4) * (32 >> 4), b, id, q > 0);
+            if (++k == rank_steps) k = 0;
+          }
+          mma_commit(smem_u32(&c->empty[s]));
+          mma_commit(smem_u32(&c->dfull[buf]));
+          if (i + 1 == j.blocks) mma_commit(smem_u32(&c->hempty[hs]));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (elect_one()) await_mmas(f, p.ws);
     __syncwarp();
   } else if (warp < 2 + EPI_WARPS) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;
-    uint32_t n = 0, np = 0;
+    uint32_t n = 0;
+    int q = 0;
+    uint32_t qp = 0;
+    JobQueue queue{c, p.ws, 0};
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
-      const int buf = n % ACCS, all = panels_of(block);
-      if (++block == o.n_blocks) block = 0;
-      if (!warp_wait(smem_u32(&c->dfull[buf]), (n / ACCS) & 1, p.ws, abort)) break;
-      fence_after();
-      for (int i = 0; i < all; ++i, ++np) {
-        constexpr int MINE = PC / 2;  // this thread's columns of the panel
-        const int q = np % o.panels;
-        uint32_t r[MINE];
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 128 + i * PC + half * MINE;
-#pragma unroll
-        for (int j = 0; j < MINE / 8; ++j) tmem_ld8(at + 8 * j, r + 8 * j);
-        if (!warp_wait(smem_u32(&c->yfull[q]), (np / o.panels) & 1, p.ws, abort)) {
+    for (int job; ok && (job = queue.next()) >= 0;) {
+      const Job j(o, job);
+      for (int b = j.block; b < j.block + j.blocks && ok; ++b, ++n) {
+        const int buf = n % ACCS, all = panels_of(b);
+        if (!warp_wait(smem_u32(&c->dfull[buf]), (n / ACCS) & 1, p.ws, abort)) {
           ok = false;
           break;
         }
-        tmem_wait();
+        fence_after();
+        for (int i = 0; i < all; ++i) {
+          constexpr int MINE = PC / 2;  // this thread's columns of the panel
+          uint32_t r[MINE];
+          const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 128 + i * PC + half * MINE;
 #pragma unroll
-        for (int j = 0; j < MINE / 8; ++j) pin8(r + 8 * j);
-        if (i == all - 1) {  // everything is in registers: the accumulator is free
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
-        }
-        const uint32_t line = panels + q * 16384 + row * 128;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // 16-byte pieces of the row, swizzled as TMA lays them
-          const uint32_t addr = line + (((half * 4 + j) ^ (row & 7)) << 4);
-          uint4 v = lds128(addr);
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (BF16) {
-              const float2 was = bf16x2_to_f2(w[k]);
-              w[k] = f2_to_bf16x2(was.x + __uint_as_float(r[8 * j + 2 * k]), was.y + __uint_as_float(r[8 * j + 2 * k + 1]));
-            } else {
-              w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(r[4 * j + k]));
-            }
+          for (int k = 0; k < MINE / 8; ++k) tmem_ld8(at + 8 * k, r + 8 * k);
+          if (!warp_wait(smem_u32(&c->yfull[q]), qp, p.ws, abort)) {
+            ok = false;
+            break;
           }
-          sts128(addr, v);
+          tmem_wait();
+#pragma unroll
+          for (int k = 0; k < MINE / 8; ++k) pin8(r + 8 * k);
+          if (i == all - 1) {  // everything is in registers: the accumulator is free
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
+          }
+          const uint32_t line = panels + q * 16384 + row * 128;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {  // 16-byte pieces of the row, swizzled as TMA lays them
+            const uint32_t addr = line + (((half * 4 + h) ^ (row & 7)) << 4);
+            uint4 v = lds128(addr);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (BF16) {
+                const float2 was = bf16x2_to_f2(w[k]);
+                w[k] = f2_to_bf16x2(was.x + __uint_as_float(r[8 * h + 2 * k]), was.y + __uint_as_float(r[8 * h + 2 * k + 1]));
+              } else {
+                w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(r[4 * h + k]));
+              }
+            }
+            sts128(addr, v);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c->ydone[q]));
+          if (++q == o.panels) {
+            q = 0;
+            qp ^= 1;
+          }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c->ydone[q]));
       }
     }
   } else {
-    uint32_t np = 0;
-    bool ok = true;
-    Tile t{0, 0, 0};
+    int q = 0;
+    uint32_t qp = 0;
     int pending = -1;  // the panel that the last TMA store reads
-    for (int64_t u = u0; u < u1 && ok; ++u) {
-      if (u == u0 || block == 0) t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-      for (int i = 0, all = panels_of(block); i < all; ++i, ++np) {
-        const int q = np % o.panels;
-        if (!warp_wait(smem_u32(&c->ydone[q]), (np / o.panels) & 1, p.ws, abort)) {
-          ok = false;
-          break;
-        }
-        const int64_t col = (int64_t)block * o.nb + i * PC;
-        const uint32_t src = panels + q * 16384;
-        const bool whole = t.rows == TILE_ROWS;
-        if (whole) {
-          if (lane == 0) {
-            tma_store_2d(&m_out, src, (int)col, t.row0);
-            if (pending >= 0) {
-              tma_store_read_wait<1>();
-              mbar_arrive(smem_u32(&c->yempty[pending]));
-            }
+    JobQueue queue{c, p.ws, 0};
+    bool ok = true;
+    for (int job; ok && (job = queue.next()) >= 0;) {
+      const Job j(o, job);
+      const Tile t = load_tile(p.table, j.tile, p.rows, p.n_adapters, p.ws);
+      for (int b = j.block; b < j.block + j.blocks && ok; ++b)
+        for (int i = 0, all = panels_of(b); i < all; ++i) {
+          if (!warp_wait(smem_u32(&c->ydone[q]), qp, p.ws, abort)) {
+            ok = false;
+            break;
           }
-          pending = q;
-        } else {
-          const int piece = lane & 7;
-          char* out = reinterpret_cast<char*>(o.out) + ((int64_t)t.row0 * o.width + col) * ES + piece * 16;
-          if (col + piece * (16 / ES) < o.width)
-            for (int r = lane >> 3; r < t.rows; r += 4)
-              *reinterpret_cast<uint4*>(out + (int64_t)r * o.width * ES) = lds128(src + r * 128 + ((piece ^ (r & 7)) << 4));
-          __syncwarp();
-          if (lane == 0) {
-            if (pending >= 0) {
-              tma_store_read_wait<0>();
-              mbar_arrive(smem_u32(&c->yempty[pending]));
+          const int64_t col = (int64_t)b * o.nb + i * PC;
+          const uint32_t src = panels + q * 16384;
+          if (t.rows == TILE_ROWS) {
+            if (lane == 0) {
+              tma_store_2d(&m_out, src, (int)col, t.row0);
+              if (pending >= 0) {
+                tma_store_read_wait<1>();
+                mbar_arrive(smem_u32(&c->yempty[pending]));
+              }
             }
-            mbar_arrive(smem_u32(&c->yempty[q]));
+            pending = q;
+          } else {
+            const int piece = lane & 7;
+            char* out = reinterpret_cast<char*>(o.out) + ((int64_t)t.row0 * o.width + col) * ES + piece * 16;
+            if (col + piece * (16 / ES) < o.width)
+              for (int r = lane >> 3; r < t.rows; r += 4)
+                *reinterpret_cast<uint4*>(out + (int64_t)r * o.width * ES) = lds128(src + r * 128 + ((piece ^ (r & 7)) << 4));
+            __syncwarp();
+            if (lane == 0) {
+              if (pending >= 0) {
+                tma_store_read_wait<0>();
+                mbar_arrive(smem_u32(&c->yempty[pending]));
+              }
+              mbar_arrive(smem_u32(&c->yempty[q]));
+            }
+            pending = -1;
           }
-          pending = -1;
+          if (++q == o.panels) {
+            q = 0;
+            qp ^= 1;
+          }
         }
-      }
-      if (++block == o.n_blocks) {
-        block = 0;
-        ++ti;
-      }
     }
     if (lane == 0) tma_store_wait();
   }
@@ -1003,13 +1073,28 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
-  FromRank o{out, width, 128, 0, 0};
+  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1};
   p.parts = BF16 ? 2 : PARTS;
-  const uint32_t room = RING_BYTES - (p.parts * p.rp + 63) / 64 * 16384;
+  const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
-  // narrower units where wide ones would leave SMs without work, or the panels without room
-  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms() || room < 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
+  // narrower blocks where wide ones would leave SMs without work, or the panels without room
+  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms() || RING_BYTES < h_bytes + 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
+  const uint32_t w_bytes = bytes_of(o.nb);
+  p.stages = 2;
+  // two tiles of held if that leaves six panels; then up to four stages of weights
+  if (RING_BYTES >= 2 * h_bytes + p.stages * w_bytes + 6 * 16384) o.helds = 2;
+  const uint32_t room = RING_BYTES - o.helds * h_bytes;
+  while (p.stages < 4 && room >= (p.stages + 1) * w_bytes + MAX_PANELS * 16384) ++p.stages;
+  o.panels = (int)((room - p.stages * w_bytes) / 16384);
+  if (o.panels > MAX_PANELS) o.panels = MAX_PANELS;
   o.n_blocks = (int)((width + o.nb - 1) / o.nb);
+  // jobs of up to eight blocks, sixteen jobs to an SM where there are that many blocks
+  const int64_t per_job = (int64_t)p.n_tiles * o.n_blocks / (16 * num_sms());
+  o.per_job = per_job < 1 ? 1 : per_job > 8 ? 8 : (int)per_job;
+  o.tile_jobs = (o.n_blocks + o.per_job - 1) / o.per_job;
+  o.jobs = p.n_tiles * o.tile_jobs;
+  if (o.jobs > 0x7fffff00) return DIT_ERR_UNSUPPORTED;
+  const int64_t ctas = o.jobs < num_sms() ? o.jobs : num_sms();
   CUtensorMap m_held, m_w, m_out;
   const bool maps = encode_tmap_2d(&m_out, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
                                    (uint64_t)width, (uint64_t)p.rows, (uint64_t)width * (BF16 ? 2 : 4), BF16 ? 64 : 32,
@@ -1018,13 +1103,7 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
                     (MN ? encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp)
                         : encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, o.nb));
   if (!maps || !allow_smem<k_from_rank<MN, BF16>>()) return DIT_ERR_CUDA;
-  const uint32_t w_bytes = bytes_of(o.nb);
-  p.stages = 2;
-  while (p.stages < 4 && room - (p.stages + 1) * w_bytes >= MAX_PANELS * 16384) ++p.stages;
-  o.panels = (int)((room - p.stages * w_bytes) / 16384);
-  if (o.panels > MAX_PANELS) o.panels = MAX_PANELS;
-  p.split = split_units((int64_t)p.n_tiles * o.n_blocks, 1, 1, num_sms());
-  return launch_pdl(k_from_rank<MN, BF16>, dim3(p.split.ctas), dim3(FROM_THREADS), SMEM_BYTES, st, 1, m_held, m_w, m_out, p,
+  return launch_pdl(k_from_rank<MN, BF16>, dim3((unsigned)ctas), dim3(FROM_THREADS), SMEM_BYTES, st, 1, m_held, m_w, m_out, p,
                     o) == cudaSuccess
              ? DIT_OK
              : DIT_ERR_CUDA;

@@ -79,6 +79,11 @@ __device__ __forceinline__ Tile load_tile(const int32_t* table, int64_t t, int64
   return check_tile(reinterpret_cast<const int4*>(table)[t], rows, n_adapters, ws);
 }
 
+// The counter that hands out jobs (k_from_rank), in the workspace; k_to_rank, which precedes it in each
+// call, sets it to zero.
+constexpr size_t WS_JOBS = 33280;
+static_assert(WS_JOBS >= WS_PARTIALS + 32 * MAX_RED_CTAS && WS_JOBS + 4 <= WS_BYTES, "");
+
 bool plan_ok(const dit_adapter_plan_t* p);
 dit_status small_tiles(const dit_adapter_plan_t& plan, const int32_t* table, const void* x, const void* a, const void* b,
                        const float* scale, int rank, int64_t k, int64_t n, void* y, dit_dtype y_dt, void* ws,
