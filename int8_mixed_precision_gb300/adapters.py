@@ -11,12 +11,19 @@ import ctypes
 
 import torch
 
-from . import ACT_NONE, DitError, _check, _stream, gemm_bf16
+from . import ACT_NONE, DitError, _check, gemm_bf16
 from ._lib import lib
 
 MAX_RANK = 128
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}
+_JUST_BF16 = (_BF16,)
+
+
+def raw_stream(stream, index: int) -> int:
+    """The handle of `stream`, or of device `index`'s current stream (without making a Stream object,
+    which costs more than the checks and the launch of a short call together)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 class _Plan(ctypes.Structure):
@@ -53,6 +60,7 @@ class AdapterPlan:
         self.rows, self.n_adapters, self.training = self.info.rows, int(n_adapters), bool(training)
         self.n_tiles, self.n_small = self.info.n_tiles, self.info.n_small
         self._info_p, self._table_p = ctypes.addressof(self.info), self.table.data_ptr()
+        self._index = self.table.get_device()
 
 
 class AdapterBank:
@@ -77,7 +85,8 @@ class AdapterBank:
                 self.k < 8 or self.n < 8:
             raise DitError(f"AdapterBank: rank 8 to {MAX_RANK} in steps of 8, k and n multiples of 8")
         self.a, self.b, self.scale, self.device = a, b, scale, a.device
-        self._ptrs = (a.data_ptr(), b.data_ptr(), scale.data_ptr())
+        self._index = a.get_device()
+        self._args = (a.data_ptr(), b.data_ptr(), scale.data_ptr(), self.rank, self.k, self.n)
 
 
 def adapter_scratch(plan: AdapterPlan, bank: AdapterBank):
@@ -93,37 +102,38 @@ def adapter_saved(plan: AdapterPlan, bank: AdapterBank):
     return torch.empty(n, dtype=torch.uint8, device=bank.device)
 
 
-def _rows_of(t, plan, width, types, what, device):
-    if t.dim() != 2 or t.shape[1] != width or t.shape[0] < plan.rows:
-        raise DitError(f"{what}: {tuple(t.shape)}, the call needs [{plan.rows}, {width}]")
-    if t.dtype not in types:
-        raise DitError(f"{what}: unsupported dtype {t.dtype}")
-    return _ptr(t, what, device)
+# The checks of a call.  They take one pass over each tensor's properties: a serving call's kernel takes
+# a few microseconds, and so must its checks.
 
-
-def _ptr(t, what, device):
+def _refuse(t, what, index):
     if not t.is_cuda:
         raise DitError(f"buffers must be CUDA tensors ({what} is on {t.device})")
-    if t.device != device:
-        raise DitError(f"{what} is on {t.device}, the bank on {device}")
-    if not t.is_contiguous():
-        raise DitError(f"buffers must be contiguous ({what})")
+    if t.get_device() != index:
+        raise DitError(f"{what} is on {t.device}, the bank on cuda:{index}")
+    raise DitError(f"buffers must be contiguous ({what})")
+
+
+def _rows_of(t, rows, width, types, what, index):
+    if t.dtype not in types:
+        raise DitError(f"{what}: unsupported dtype {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or shape[0] < rows:
+        raise DitError(f"{what}: {tuple(shape)}, the call needs [{rows}, {width}]")
+    if t.get_device() != index or index < 0 or not t.is_contiguous():
+        _refuse(t, what, index)
     return t.data_ptr()
 
 
-def _bytes_of(t, need, what, device):
-    if t is None:
-        return None, 0
-    n = t.numel() * t.element_size()
-    if n < need:
-        raise DitError(f"{what}: {n} bytes, the call needs {need}")
-    return _ptr(t, what, device), n
+def _bytes_of(t, what, index):
+    if t.get_device() != index or index < 0 or not t.is_contiguous():
+        _refuse(t, what, index)
+    return t.data_ptr()
 
 
 def _agree(plan, bank):
     if plan.n_adapters != bank.n_adapters:
         raise DitError(f"the plan is for {plan.n_adapters} adapters, the bank has {bank.n_adapters}")
-    if plan.table.device != bank.device:
+    if plan._index != bank._index:
         raise DitError(f"the plan is on {plan.table.device}, the bank on {bank.device}")
 
 
@@ -132,17 +142,20 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
     lora_backward needs."""
     _agree(plan, bank)
-    dev, a = bank.device, bank._ptrs
-    xp = _rows_of(x, plan, bank.k, (_BF16,), "x", dev)
-    yp = _rows_of(y, plan, bank.n, _CODE, "y", dev)
-    if saved is not None and not plan.training:
+    i, rows = bank._index, plan.rows
+    xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
+    yp = _rows_of(y, rows, bank.n, _CODE, "y", i)
+    if saved is None:
+        vp, vn = None, 0
+    elif plan.training:
+        vp, vn = _bytes_of(saved, "saved", i), saved.nbytes
+    else:
         raise DitError("saved needs AdapterPlan(..., training=True)")
-    vp, vn = _bytes_of(saved, 0, "saved", dev)
-    sp, sn = _bytes_of(scratch, 0, "scratch", dev)
-    wp, wn = _bytes_of(ws, 0, "ws", dev)
-    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, a[0], a[1], a[2], bank.rank, bank.k, bank.n, yp,
-                                _CODE[y.dtype], vp, vn, sp, sn, wp, wn, _stream(stream))
-    _check(st, "dit_lora_forward")
+    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn,
+                                _bytes_of(scratch, "scratch", i), scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes,
+                                raw_stream(stream, i))
+    if st:
+        _check(st, "dit_lora_forward")
 
 
 def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
@@ -153,20 +166,23 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
     _agree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")
-    dev, a = bank.device, bank._ptrs
-    xp = _rows_of(x, plan, bank.k, (_BF16,), "x", dev)
-    dyp = _rows_of(dy, plan, bank.n, (_BF16,), "dy", dev)
-    dxp = None if dx is None else _rows_of(dx, plan, bank.k, _CODE, "dx", dev)
-    for t, like, what in ((da, bank.a, "da"), (db, bank.b, "db")):
-        if t.dtype != _F32 or t.shape != like.shape:
-            raise DitError(f"{what}: float32 {tuple(like.shape)} is needed")
-    vp, vn = _bytes_of(saved, 0, "saved", dev)
-    sp, sn = _bytes_of(scratch, 0, "scratch", dev)
-    wp, wn = _bytes_of(ws, 0, "ws", dev)
-    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, a[0], a[1], a[2], bank.rank, bank.k, bank.n, vp,
-                                 vn, dxp, 1 if dx is None else _CODE[dx.dtype], _ptr(da, "da", dev), _ptr(db, "db", dev),
-                                 sp, sn, wp, wn, _stream(stream))
-    _check(st, "dit_lora_backward")
+    i, rows = bank._index, plan.rows
+    xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
+    dyp = _rows_of(dy, rows, bank.n, _JUST_BF16, "dy", i)
+    if dx is None:
+        dxp, dx_code = None, 1
+    else:
+        dxp, dx_code = _rows_of(dx, rows, bank.k, _CODE, "dx", i), _CODE[dx.dtype]
+    if da.dtype != _F32 or da.shape != bank.a.shape:
+        raise DitError(f"da: float32 {tuple(bank.a.shape)} is needed")
+    if db.dtype != _F32 or db.shape != bank.b.shape:
+        raise DitError(f"db: float32 {tuple(bank.b.shape)} is needed")
+    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, *bank._args, _bytes_of(saved, "saved", i),
+                                 saved.nbytes, dxp, dx_code, _bytes_of(da, "da", i), _bytes_of(db, "db", i),
+                                 _bytes_of(scratch, "scratch", i), scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes,
+                                 raw_stream(stream, i))
+    if st:
+        _check(st, "dit_lora_backward")
 
 
 class AdaptedLinear:

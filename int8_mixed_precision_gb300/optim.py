@@ -9,8 +9,9 @@ import ctypes
 
 import torch
 
-from . import DitError, _check, _stream, workspace
+from . import DitError, _check, workspace
 from ._lib import lib
+from .adapters import raw_stream
 
 BLOCK = 256        # consecutive elements of a tensor that share a scale of an 8-bit moment
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
@@ -101,6 +102,7 @@ class AdamW:
         self._types = (_CODE[lists["p"][0].dtype], _CODE[lists["g"][0].dtype], self.bits)
         self._tail = (self.ws.data_ptr(), self.ws.numel())
         self._args_p = ctypes.addressof(self._args)
+        self._index = self._descs.get_device()
 
     @property
     def lr(self) -> float:
@@ -115,18 +117,20 @@ class AdamW:
         (a clipping factor, or one over a loss scale)."""
         gp = None
         if grad_scale is not None:
-            if grad_scale.dtype != _F32 or grad_scale.numel() != 1 or grad_scale.device != self.device:
+            if grad_scale.dtype != _F32 or grad_scale.numel() != 1 or grad_scale.get_device() != self._index:
                 raise DitError("AdamW: grad_scale is a float32 [1] on the parameters' device")
             gp = grad_scale.data_ptr()
         self._args.step = self.step_count + 1
-        _check(lib().dit_adamw_step(*self._head, *self._types, self._args_p, gp, *self._tail, _stream(stream)), "dit_adamw_step")
+        st = lib().dit_adamw_step(*self._head, *self._types, self._args_p, gp, *self._tail, raw_stream(stream, self._index))
+        if st:
+            _check(st, "dit_adamw_step")
         self.step_count += 1
 
     def export_moments(self, stream=None) -> None:
         """The values of 8-bit moments, in bf16, into m_values and v_values (the second moment itself)."""
         if "m_values" not in self._lists and "v_values" not in self._lists:
             raise DitError("AdamW: export_moments needs 8-bit moments with m_values or v_values")
-        _check(lib().dit_adamw_moments(*self._head, *self._tail, _stream(stream)), "dit_adamw_moments")
+        _check(lib().dit_adamw_moments(*self._head, *self._tail, raw_stream(stream, self._index)), "dit_adamw_moments")
 
     def state_dict(self) -> dict:
         """Host copies of the moments as they are held, and the step count."""
