@@ -208,12 +208,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t full = smem_u32(&c->full[s]), dst = f.smem + s * stage_bytes;
-        if (lane == 0) mbar_expect_tx(full, stage_bytes);
-        __syncwarp();
-        if (lane == 0)
+        if (elect_one()) {
+          mbar_expect_tx(full, stage_bytes);
           tma_load_2d(dst, &m_in, full, kb * 64, t.row0);
-        else if (lane <= w_chunks)
-          tma_load_3d(dst + 8192 + lane * 8192, &m_w, full, MN ? (lane - 1) * 64 : kb * 64, MN ? kb * 64 : 0, t.g);
+          if (MN) {
+            for (int i = 0; i < w_chunks; ++i) tma_load_3d(dst + 16384 + i * 8192, &m_w, full, i * 64, kb * 64, t.g);
+          } else {
+            tma_load_3d(dst + 16384, &m_w, full, kb * 64, 0, t.g);
+          }
+        }
+        __syncwarp();
         if (++kb == o.blocks) {
           kb = 0;
           ++ti;
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   auto panels_of = [&](int b) { return (int)min((int64_t)o.nb / PC, (o.width - (int64_t)b * o.nb + PC - 1) / PC); };
 
   if (warp == 0) {
-    if (!p.stall) {  // a lane to each box
+    if (!p.stall) {
       uint32_t n = 0, tiles = 0, np = 0, announced = 0;
       int s = 0, q = 0;
       uint32_t sp = 1, qp = 1;  // parities of the rings' next waits
@@ -465,10 +469,12 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) mbar_expect_tx(smem_u32(&c->hfull[hs]), h_bytes);
+        if (elect_one()) {
+          mbar_expect_tx(smem_u32(&c->hfull[hs]), h_bytes);
+          for (int i = 0; i < h_boxes; ++i)
+            tma_load_2d(f.smem + hs * h_bytes + i * 16384, &m_held, smem_u32(&c->hfull[hs]), i * 64, (int)(j.tile * TILE_ROWS));
+        }
         __syncwarp();
-        if (lane < h_boxes)
-          tma_load_2d(f.smem + hs * h_bytes + lane * 16384, &m_held, smem_u32(&c->hfull[hs]), lane * 64, (int)(j.tile * TILE_ROWS));
         ++tiles;
         for (int b = j.block; b < j.block + j.blocks && ok; ++b) {
           const int n0 = b * o.nb;
@@ -477,10 +483,12 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
             break;
           }
           const uint32_t full = smem_u32(&c->full[s]);
-          if (lane == 0) mbar_expect_tx(full, w_bytes);
+          if (elect_one()) {
+            mbar_expect_tx(full, w_bytes);
+            for (int i = 0; i < w_boxes; ++i)
+              tma_load_3d(ring + s * w_bytes + i * box_bytes, &m_w, full, MN ? n0 + i * 64 : i * 64, MN ? 0 : n0, t.g);
+          }
           __syncwarp();
-          if (lane < w_boxes)
-            tma_load_3d(ring + s * w_bytes + lane * box_bytes, &m_w, full, MN ? n0 + lane * 64 : lane * 64, MN ? 0 : n0, t.g);
           ++n;
           if (++s == p.stages) {
             s = 0;
@@ -491,10 +499,11 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
               ok = false;
               break;
             }
-            if (lane == 0) {
+            if (elect_one()) {
               mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
               tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
             }
+            __syncwarp();
             if (++q == o.panels) {
               q = 0;
               qp ^= 1;
@@ -699,9 +708,6 @@ struct HeldBoxes {
     per_part = 64 % rp == 0 ? 0 : (rp + 63) / 64;
     boxes = per_part ? PARTS * per_part : (PARTS * rp + 63) / 64;
   }
-  __device__ __forceinline__ int column(int box) const {
-    return per_part ? box / per_part * rp + box % per_part * 64 : box * 64;
-  }
   __device__ __forceinline__ uint32_t offset(int part) const {
     return per_part ? part * per_part * ROW_BOX : part * rp / 64 * ROW_BOX + part * rp % 64 * 2;
   }
@@ -780,9 +786,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
 
   if (warp == 0) {
     if (!p.stall) {
-      // a lane to each box of a stage: one thread would spend longer issuing them than they take
-      const int boxes = a_boxes + hb.boxes, held_box = lane - a_boxes;
-      const int held_col = held_box >= 0 ? hb.column(held_box) : 0;
       uint32_t parity = 1, n = 0;
       int s = 0;
       bool ok = true;
@@ -795,8 +798,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         }
         const int64_t end = min(u1, r.first + r.count);
         const int4* entry = reinterpret_cast<const int4*>(p.table) + r.tile;
-        const CUtensorMap* map = held_box < 0 ? (r.problem ? &m_dy : &m_x) : (r.problem ? &m_h : &m_e);
-        const int col = held_box < 0 ? (int)(r.block * a_boxes + lane) * 64 : held_col;
+        const CUtensorMap *wide = r.problem ? &m_dy : &m_x, *narrow = r.problem ? &m_h : &m_e;
+        const int col = (int)(r.block * a_boxes) * 64;
         int held_row = (int)(r.tile * TILE_ROWS);
         int4 next = *entry;
         for (; u < end && ok; ++u) {
@@ -808,13 +811,20 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
               break;
             }
             const uint32_t full = smem_u32(&c->full[s]);
-            if (lane == 0) {
+            if (elect_one()) {
               c->valid[s] = min(ROW_STAGE, max(0, t.rows - h));
               mbar_expect_tx(full, stage_bytes);
+              uint32_t dst = f.smem + s * stage_bytes;
+              for (int i = 0; i < a_boxes; ++i, dst += ROW_BOX) tma_load_2d(dst, wide, full, col + i * 64, t.row0 + h);
+              if (hb.per_part) {
+                for (int q = 0; q < PARTS; ++q)
+                  for (int i = 0; i < hb.per_part; ++i, dst += ROW_BOX)
+                    tma_load_2d(dst, narrow, full, q * p.rp + i * 64, held_row);
+              } else {
+                for (int i = 0; i < hb.boxes; ++i, dst += ROW_BOX) tma_load_2d(dst, narrow, full, i * 64, held_row);
+              }
             }
             __syncwarp();
-            if (lane < boxes)
-              tma_load_2d(f.smem + s * stage_bytes + lane * ROW_BOX, map, full, col, held_box < 0 ? t.row0 + h : held_row);
             if (++s == p.stages) {
               s = 0;
               parity ^= 1;
