@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *ws_u32(p.ws, WS_JOBS) = 0;  // for the next k_from_rank
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int w_chunks = MN ? (p.rank + 63) / 64 : 1;
   const uint32_t w_bytes = MN ? w_chunks * 8192 : p.rp * 128;
   const uint32_t stage_bytes = 16384 + w_bytes;
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   const uint32_t tmem = c->tmem;
   pdl_wait();
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int steps = p.parts * p.rp / 16;           // of the contraction
   const int h_boxes = (p.parts * p.rp + 63) / 64;  // of 128 rows x 64 columns, 16 KB each
   const int w_boxes = MN ? o.nb / 64 : (p.rank + 63) / 64;
@@ -751,6 +751,7 @@ __device__ __forceinline__ int64_t first_of_output(const Args& p, const OverRows
   return max((int64_t)0, min(p.split.units, u));
 }
 
+template <int MT>  // tiles of 128 columns: 1, 2 or 4
 __global__ void __launch_bounds__(ROW_THREADS, 1)
     k_over_rows(const __grid_constant__ CUtensorMap m_x, const __grid_constant__ CUtensorMap m_e,
                 const __grid_constant__ CUtensorMap m_dy, const __grid_constant__ CUtensorMap m_h, Args p, OverRows o) {
@@ -770,9 +771,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   const uint32_t tmem = c->tmem;
   pdl_wait();
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const HeldBoxes hb(p.rp);
-  const int a_boxes = 2 * o.mtiles;
+  const int a_boxes = 2 * MT;
   const uint32_t stage_bytes = (a_boxes + hb.boxes) * ROW_BOX;
   int64_t u0, u1;
   if (o.whole) {
@@ -846,42 +847,45 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         ++u;
         continue;
       }
-      const int64_t end = min(u1, r.first + r.count);
-      for (; u < end && ok; ++u, ++chunk) {
-        const uint32_t buf = chunk & 1, d = tmem + buf * o.mtiles * p.rp;
+      const int todo = uniform((int)(min(u1, r.first + r.count) - u));
+      u += todo;
+      for (int t = 0; t < todo && ok; ++t, ++chunk) {
+        const uint32_t buf = chunk & 1, d = tmem + buf * MT * p.rp;
         if (!warp_wait(smem_u32(&c->dempty[buf]), ((chunk >> 1) & 1) ^ 1, p.ws, abort)) {
           ok = false;
           break;
         }
         fence_after();
-        for (int h = 0; h < TILE_ROWS; h += ROW_STAGE) {
+#pragma unroll
+        for (int h = 0; h < TILE_ROWS / ROW_STAGE; ++h) {
           if (!warp_wait(smem_u32(&c->full[s]), parity, p.ws, abort)) {
             ok = false;
             break;
           }
-          const uint32_t a = f.smem + s * stage_bytes, b = a + a_boxes * ROW_BOX;
-          const int valid = c->valid[s];
+          const uint32_t a = f.smem + s * stage_bytes;
+          const int valid = uniform(c->valid[s]);
           if (valid < ROW_STAGE) {
             // rows of other requests behind the tile's own: zeros, so that what they hold stays out
             for (int k = valid * 8 + lane; k < ROW_STAGE * 8; k += 32)
               for (int q = 0; q < a_boxes; ++q) sts128(a + q * ROW_BOX + k * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async();
+            __syncwarp();
           }
-          __syncwarp();
           if (elect_one()) {
             fence_after();
-            uint32_t ad = desc_mn(a, ROW_BOX), dd = d;
-            const uint32_t bd = desc_mn(b, ROW_BOX);
-            for (int mt = 0; mt < o.mtiles; ++mt, ad += 2 * ROW_BOX >> 4, dd += p.rp)
+            const uint32_t ad = desc_mn(a, ROW_BOX), bd = desc_mn(a + a_boxes * ROW_BOX, ROW_BOX);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int j = 0; j < ROW_STAGE / 16; ++j) {  // the small parts first
-                const uint32_t aj = ad + j * (2048 >> 4), bj = bd + j * (2048 >> 4);
+                const uint32_t dd = d + mt * p.rp, aj = ad + (mt * 2 * ROW_BOX + j * 2048) / 16, bj = bd + j * (2048 / 16);
                 static_assert(PARTS == 3, "three MMAs with one A");
                 mma<KEEP_FIRST>(dd, aj, bj + part_at[2], id, h > 0 || j > 0);
                 mma<KEEP_MIDDLE>(dd, aj, bj + part_at[1], id, true);
                 mma<KEEP_LAST>(dd, aj, bj + part_at[0], id, true);
               }
             mma_commit(smem_u32(&c->empty[s]));
+            if (h + 1 == TILE_ROWS / ROW_STAGE) mma_commit(smem_u32(&c->dfull[buf]));
           }
           __syncwarp();
           if (++s == p.stages) {
@@ -889,7 +893,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
             parity ^= 1;
           }
         }
-        if (ok && elect_one()) mma_commit(smem_u32(&c->dfull[buf]));
       }
     }
     if (elect_one()) await_mmas(f, p.ws);
@@ -898,11 +901,11 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
     // Sixteen warps: four to the quarters of 128 columns; the four groups take an M tile each (mtiles 4), half
     // the rank of two, or half of one (then two groups have nothing).
     const int quarter = warp & 3, group = (warp - 2) >> 2;
-    const int mt = o.mtiles == 4 ? group : o.mtiles == 2 ? group >> 1 : 0;
-    const int nc = o.mtiles == 4 ? p.rp : o.mtiles == 2 || group < 2 ? p.rp / 2 : 0;
-    const int col0 = o.mtiles == 4 ? 0 : (group & 1) * nc;
+    const int mt = MT == 4 ? group : MT == 2 ? group >> 1 : 0;
+    const int nc = MT == 4 ? p.rp : MT == 2 || group < 2 ? p.rp / 2 : 0;
+    const int col0 = MT == 4 ? 0 : (group & 1) * nc;
     const int m = mt * 128 + quarter * 32 + lane;  // column of x or dy within the output tile
-    const int m_all = o.mtiles * 128;
+    const int m_all = MT * 128;
     uint32_t chunk = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
@@ -923,7 +926,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
           break;
         }
         fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf * o.mtiles + mt) * p.rp + col0;
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf * MT + mt) * p.rp + col0;
 #pragma unroll
         for (int i = 0; i < 64; i += 16) {
           if (i >= nc) break;
@@ -1212,11 +1215,12 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
       !map_rows(&m_dy, dy, n, p.rows, ROW_STAGE) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, ROW_STAGE) ||
-      !allow_smem<k_over_rows>())
+      !allow_smem<k_over_rows<1>>() || !allow_smem<k_over_rows<2>>() || !allow_smem<k_over_rows<4>>())
     return DIT_ERR_CUDA;
+  auto kern = o.mtiles == 4 ? k_over_rows<4> : o.mtiles == 2 ? k_over_rows<2> : k_over_rows<1>;
   const int h_boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
   p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
-  if (launch_pdl(k_over_rows, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
+  if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   const int64_t outputs = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters;
   if (!o.whole && p.split.ctas > 1 &&

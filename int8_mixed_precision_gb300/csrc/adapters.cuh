@@ -133,6 +133,9 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
     DIT_LORA_MMA("");
 }
 #undef DIT_LORA_MMA
+// A value that all lanes of the warp share, so that the compiler keeps what follows from it in uniform
+// registers: instructions that want them (MMAs, TMA) otherwise pay for moving every operand.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 // One lane of a converged warp (always the same one).
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
