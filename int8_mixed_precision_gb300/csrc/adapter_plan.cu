@@ -18,6 +18,7 @@ struct Run {
 static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int64_t requests, int n_adapters,
                             int training, dit_adapter_plan_t* plan, int32_t* table, int64_t table_ints) {
   if (!plan || requests < 0 || n_adapters <= 0 || (requests > 0 && (!lengths || !adapters))) return DIT_ERR_INVALID_ARG;
+  if (n_adapters > MAX_ADAPTERS) return DIT_ERR_UNSUPPORTED;
   std::vector<std::vector<Run>> runs((size_t)n_adapters);
   int64_t rows = 0;
   int32_t last = -1;
@@ -93,7 +94,7 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
 }
 
 bool plan_ok(const dit_adapter_plan_t* p) {
-  return p && p->rows >= 0 && p->rows <= MAX_ROWS && p->n_adapters > 0 && p->n_tiles >= 0 && p->n_tiles <= MAX_TILES &&
+  return p && p->rows >= 0 && p->rows <= MAX_ROWS && p->n_adapters > 0 && p->n_adapters <= MAX_ADAPTERS && p->n_tiles >= 0 && p->n_tiles <= MAX_TILES &&
          p->n_small >= 0 && p->n_small <= MAX_TILES && p->most_tiles >= 0 && p->most_tiles <= p->n_tiles && p->table_ints == off_small(*p) + (int64_t)SMALL_INTS * p->n_small;
 }
 
@@ -101,7 +102,7 @@ dit_status check_common(const dit_adapter_plan_t* plan, const int32_t* table, co
                         const void* b, const float* scale, int rank, int64_t k, int64_t n, const void* scratch,
                         size_t scratch_bytes, const void* ws, size_t ws_bytes) {
   if (!plan_ok(plan) || !table || !a || !b || !scale || !ws || ws_bytes < WS_BYTES) return DIT_ERR_INVALID_ARG;
-  if ((!x && plan->rows > 0) || k <= 0 || n <= 0 || k > 0x7ffffff0 || n > 0x7ffffff0 || rank <= 0) return DIT_ERR_INVALID_ARG;
+  if ((!x && plan->rows > 0) || k <= 0 || n <= 0 || k > MAX_WIDTH || n > MAX_WIDTH || rank <= 0) return DIT_ERR_INVALID_ARG;
   if (rank > MAX_RANK || rank % 8 || k % 8 || n % 8) return DIT_ERR_UNSUPPORTED;
   if (scratch_bytes < dit_adapter_scratch_bytes(plan, rank, k, n) || (scratch_bytes && !scratch)) return DIT_ERR_INVALID_ARG;
   if (!aligned32(x) || !aligned32(a) || !aligned32(b) || !aligned32(ws) || !aligned32(scratch) ||

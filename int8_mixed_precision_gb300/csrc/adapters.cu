@@ -1146,7 +1146,8 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   const dit_status bad = check_common(plan, table, x, a, b, scale, rank, k, n, scratch, scratch_bytes, ws, ws_bytes);
   if (bad != DIT_OK) return bad;
   if ((!y && plan->rows > 0) || (y_dt != DIT_F32 && y_dt != DIT_BF16)) return DIT_ERR_INVALID_ARG;
-  if (saved && (!plan->training || saved_bytes < held_bytes(plan->n_tiles, rank))) return DIT_ERR_INVALID_ARG;
+  if (saved && (!plan->training || saved == scratch || saved_bytes < held_bytes(plan->n_tiles, rank)))
+    return DIT_ERR_INVALID_ARG;
   if (!aligned32(y) || !aligned32(saved)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Args p = args_of(*plan, table, rank, ws);
@@ -1167,7 +1168,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   const dit_status bad = check_common(plan, table, x, a, b, scale, rank, k, n, scratch, scratch_bytes, ws, ws_bytes);
   if (bad != DIT_OK) return bad;
   if (!plan->training || (!dy && plan->rows > 0) || !da || !db || (dx_dt != DIT_F32 && dx_dt != DIT_BF16) ||
-      saved_bytes < held_bytes(plan->n_tiles, rank) || (!saved && plan->n_tiles > 0))
+      saved_bytes < held_bytes(plan->n_tiles, rank) || (plan->n_tiles > 0 && (!saved || saved == scratch)))
     return DIT_ERR_INVALID_ARG;
   if (!aligned32(dy) || !aligned32(saved) || !aligned32(dx) || !aligned32(da) || !aligned32(db)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -1211,6 +1212,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
         }
     }
   }
+  const int64_t sum_ctas = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * (o.mtiles * 128 * p.rp / 1024);
+  if (sum_ctas > 0x7fffffff) return DIT_ERR_UNSUPPORTED;
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
@@ -1222,10 +1225,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
   if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
-  const int64_t outputs = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters;
   if (!o.whole && p.split.ctas > 1 &&
-      launch_pdl(k_over_rows_sum, dim3((unsigned)(outputs * (o.mtiles * 128 * p.rp / 1024))), dim3(256), 0, st, 1, p, o) !=
-          cudaSuccess)
+      launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   return DIT_OK;
 }

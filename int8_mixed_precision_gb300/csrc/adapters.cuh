@@ -14,6 +14,8 @@ constexpr int SMALL_RUN = 32;            // serving: a run of up to this many ro
 constexpr int MAX_RANK = 128;
 constexpr int64_t MAX_ROWS = 0x7fffff00;
 constexpr int64_t MAX_TILES = 1 << 23;   // 2^30 rows of h: a tensor map's extents stay below 2^32
+constexpr int MAX_ADAPTERS = 1 << 20;
+constexpr int64_t MAX_WIDTH = 1 << 30;   // of k and n
 constexpr int MAX_CTAS = 160;            // of the persistent kernels (GB300 has 152 SMs)
 
 // The table: n_tiles x {first row, rows, adapter, 0}; n_adapters + 1 indices of each adapter's

@@ -197,3 +197,24 @@ def test_another_stream():
     opt.step(stream=st)
     st.synchronize()
     assert abs(float(p[0]) - (1 - H["lr"] * 1.1)) < 1e-5
+
+
+def test_a_tensor_of_more_than_2_31_elements():
+    """One tensor whose last block lies past 2^31 elements, in 8 bits: its end is stepped like a small tensor's."""
+    n, tail = 2 ** 31 + 600, 5000
+    p = torch.zeros(n, dtype=BF16, device="cuda")
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    gen = torch.Generator().manual_seed(5)
+    # the tail begins with a block of 256, as the small tensor's blocks do
+    begin = (n - tail) // 256 * 256
+    small_p, small_g = (torch.randn(n - begin, generator=gen).to(BF16).cuda() for _ in range(2))
+    p[begin:], g[begin:] = small_p, small_g
+    opt = dit.AdamW([p], [g], **dit.adamw_moments([p], 8), **H)
+    other = dit.AdamW([small_p], [small_g], **dit.adamw_moments([small_p], 8), **H)
+    for _ in range(2):
+        opt.step()
+        other.step()
+    assert torch.equal(p[begin:], small_p)
+    assert torch.equal(opt._lists["m"][0][begin:].view(torch.uint8), other._lists["m"][0].view(torch.uint8))
+    assert torch.equal(opt._lists["v_scale"][0][begin // 256:], other._lists["v_scale"][0])
+    assert not p[:begin:4099].any()
