@@ -36,12 +36,19 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
     last = g;
     rows += lengths[i];
   }
+  // Serving plans: runs of few rows go to small tiles, which share a tile among runs and are one launch beside those
+  // of the large ones (8 us).  Where there are some large tiles and few short runs, each run gets a large
+  // tile of its own instead, which costs less than that launch.
+  int64_t large = 0, shorts = 0;
+  for (const auto& rs : runs)
+    for (const Run& r : rs) (r.rows <= SMALL_RUN ? shorts : large) += r.rows <= SMALL_RUN ? 1 : (r.rows + TILE_ROWS - 1) / TILE_ROWS;
+  const bool no_small = training || 4 * shorts <= large;
   int64_t n_tiles = 0, n_small = 0, most = 0;
   for (const auto& rs : runs) {
     int64_t few = 0;
     const int64_t before = n_tiles;
     for (const Run& r : rs) {
-      if (!training && r.rows <= SMALL_RUN)
+      if (!no_small && r.rows <= SMALL_RUN)
         few += r.rows;
       else
         n_tiles += (r.rows + TILE_ROWS - 1) / TILE_ROWS;
@@ -69,7 +76,7 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
     first[g] = t;
     int32_t* s = nullptr;  // the adapter's small tile that is being filled
     for (const Run& r : runs[(size_t)g]) {
-      if (!training && r.rows <= SMALL_RUN) {
+      if (!no_small && r.rows <= SMALL_RUN) {
         for (int32_t i = 0; i < r.rows; ++i) {
           if (!s || s[1] == SMALL_ROWS) {
             s = small;

@@ -1051,13 +1051,24 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
                         (uint64_t)width * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Whole tiles to each CTA, or equal shares: a share that ends inside a tile costs its CTA about as
-// much as SHARED units (a partial result written, counted in, read back and summed).
-static Split split_to_rank(int64_t tiles, int64_t blocks) {
-  constexpr int64_t SHARED = 8, LEAST = 4;
-  const int64_t sms = num_sms(), whole = (tiles + sms - 1) / sms * blocks;
+// What the cuts of the work are chosen by: a CTA's own time for its largest share at an SM's rate, or
+// all CTAs' at the device's, whichever is longer; shared outputs add a kernel that sums them.
+// (Products of 4160 and 12000 rows of 1920 columns at rank 32 took 26.1 and 43.2 us a forward call with
+// equal shares and 22.8 and 36.8 with whole tiles, though those keep only 33 and 94 SMs busy;
+// at 130 rows it is 13.5 against 15.7.)
+constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500, SHARED_NS = 5500;
+static double time_ns(double share_ns, double bytes) {
+  const double all = bytes / DEVICE_BYTES_NS;
+  return share_ns > all ? share_ns : all;
+}
+static Split split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes) {
+  constexpr int64_t LEAST = 4;  // units of an equal share
+  const int64_t sms = num_sms();
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
-  return whole <= (s.units + s.ctas - 1) / s.ctas + SHARED ? split_units(s.units, blocks, blocks, (int)sms) : s;
+  const double unit_ns = (double)unit_bytes / SM_BYTES_NS, bytes = (double)s.units * unit_bytes;
+  const double whole = time_ns((double)((tiles + sms - 1) / sms * blocks) * unit_ns, bytes);
+  const double shared = time_ns((double)s.units / s.ctas * unit_ns, bytes) + SHARED_NS;
+  return whole <= shared ? split_units(s.units, blocks, blocks, (int)sms) : s;
 }
 
 // held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
@@ -1072,8 +1083,9 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   if (!maps || !allow_smem<k_to_rank<MN>>()) return DIT_ERR_CUDA;
   ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64)};
   p.parts = parts;
-  p.stages = stages_for(RING_BYTES, 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128));
-  p.split = split_to_rank(p.n_tiles, o.blocks);
+  const uint32_t stage_bytes = 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128);
+  p.stages = stages_for(RING_BYTES, stage_bytes);
+  p.split = split_to_rank(p.n_tiles, o.blocks, stage_bytes);
   if (launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (p.split.grain == 1 && p.split.ctas > 1 &&  // shares may end inside tiles
@@ -1186,20 +1198,20 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   OverRows o{};
   o.first = table + off_first(*plan);
   o.slots = reinterpret_cast<float*>(slots);
-  // The cut of the work, by what a CTA has to move in each (bytes; the widths of the output tiles, whole
-  // output tiles or equal shares of the units): a share that ends inside an output tile costs
-  // its last CTA a round through memory (about SHARED bytes of its time) and the partial results.
+  // The widths of the output tiles, and whole output tiles to each CTA or equal shares of the units.  A unit takes
+  // its bytes' time or its 24 MMAs' for each 128 columns (25 ns measured up to rank 64, 50 at 128).
   {
-    constexpr int64_t SHARED = 200 * 1024;
     const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
-    int64_t best = -1;
+    double best = -1;
     for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
       const int64_t bk = (k + 128 * mt - 1) / (128 * mt), bn = (n + 128 * mt - 1) / (128 * mt);
       const int64_t unit = (2 * mt + boxes) * 16384, outputs = (bk + bn) * p.n_adapters, units = (bk + bn) * p.n_tiles;
-      const int64_t ctas = units < sms ? units : sms, share = (units + ctas - 1) / ctas * unit;
-      const int64_t slot = (int64_t)mt * 128 * p.rp * 4;
-      const int64_t cost[2] = {share + SHARED + (ctas + bk + bn - 1) / (bk + bn) * slot / 2,
-                               (outputs + sms - 1) / sms * plan->most_tiles * unit};
+      const double mma_ns = mt * 24 * (p.rp <= 64 ? 25.0 : 25.0 * p.rp / 64), load_ns = (double)unit / SM_BYTES_NS;
+      const double unit_ns = mma_ns > load_ns ? mma_ns : load_ns, bytes = (double)units * unit;
+      const Split s = split_units(units, 1, 1, (int)sms);
+      const double partial = 2.0 * s.ctas * mt * 128 * p.rp * 4;  // written and read again
+      const double cost[2] = {time_ns((double)units / s.ctas * unit_ns, bytes) + SHARED_NS + partial / DEVICE_BYTES_NS,
+                              time_ns((double)((outputs + sms - 1) / sms * plan->most_tiles) * unit_ns, bytes)};
       for (int whole = 0; whole < 2; ++whole)
         if (best < 0 || cost[whole] < best) {
           best = cost[whole];
@@ -1207,8 +1219,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
           o.whole = whole;
           o.g[0] = Grad{da, k, bk};
           o.g[1] = Grad{db, n, bn};
-          p.split = split_units(units, 1, 1, (int)sms);
-          if (whole) p.split.ctas = (int)(outputs < p.split.ctas ? outputs : p.split.ctas);
+          p.split = s;
+          if (whole) p.split.ctas = (int)(outputs < s.ctas ? outputs : s.ctas);
         }
     }
   }
