@@ -407,7 +407,9 @@ __global__ void __launch_bounds__(THREADS, 2)
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Bound by memory and then by latency: four blocks' loads of a warp are in flight together.
+// Bound by memory and then by latency: four blocks' loads of a warp are in flight together, from four chunks
+// to a CTA where there are enough (59 M elements: 56 us, 6.3 TB/s; 64 with a few persistent CTAs, whose
+// distant streams cost DRAM more), from one where there are few (1 M elements: 4 us against 6).
 __global__ void __launch_bounds__(THREADS)
     k_adamw_moments(const dit_adamw_tensor* __restrict__ descs, int64_t n_tensors, const int2* __restrict__ chunks,
                     int64_t n_chunks, void* ws) {
@@ -548,7 +550,8 @@ extern "C" dit_status dit_adamw_moments(const dit_adamw_tensor* descs, int64_t n
   const dit_status bad = check_tables(descs, n_tensors, chunks, n_chunks, ws, ws_bytes);
   if (bad != DIT_OK) return bad;
   if (n_chunks == 0) return DIT_OK;
-  return launch_pdl(k_adamw_moments, dim3(few(n_chunks, 4)), dim3(THREADS), 0, reinterpret_cast<cudaStream_t>(stream), 1,
+  const int64_t ctas = n_chunks <= 8 * num_sms() ? n_chunks : (n_chunks + 3) / 4;
+  return launch_pdl(k_adamw_moments, dim3((unsigned)ctas), dim3(THREADS), 0, reinterpret_cast<cudaStream_t>(stream), 1,
                     descs, n_tensors, reinterpret_cast<const int2*>(chunks), n_chunks, ws) == cudaSuccess
              ? DIT_OK
              : DIT_ERR_CUDA;

@@ -1052,11 +1052,13 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
 }
 
 // What the cuts of the work are chosen by: a CTA's own time for its largest share at an SM's rate, or
-// all CTAs' at the device's, whichever is longer; shared outputs add a kernel that sums them.
+// all CTAs' at the device's, whichever is longer; shared outputs add a kernel that sums them, which
+// takes longer the more CTAs have shared.
 // (Products of 4160 and 12000 rows of 1920 columns at rank 32 took 26.1 and 43.2 us a forward call with
 // equal shares and 22.8 and 36.8 with whole tiles, though those keep only 33 and 94 SMs busy;
 // at 130 rows it is 13.5 against 15.7.)
-constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500, SHARED_NS = 5500;
+constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500;
+static double shared_ns(int ctas) { return 3700 + 12.0 * ctas; }
 static double time_ns(double share_ns, double bytes) {
   const double all = bytes / DEVICE_BYTES_NS;
   return share_ns > all ? share_ns : all;
@@ -1067,7 +1069,7 @@ static Split split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes) {
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
   const double unit_ns = (double)unit_bytes / SM_BYTES_NS, bytes = (double)s.units * unit_bytes;
   const double whole = time_ns((double)((tiles + sms - 1) / sms * blocks) * unit_ns, bytes);
-  const double shared = time_ns((double)s.units / s.ctas * unit_ns, bytes) + SHARED_NS;
+  const double shared = time_ns((double)s.units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas);
   return whole <= shared ? split_units(s.units, blocks, blocks, (int)sms) : s;
 }
 
@@ -1210,7 +1212,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       const double unit_ns = mma_ns > load_ns ? mma_ns : load_ns, bytes = (double)units * unit;
       const Split s = split_units(units, 1, 1, (int)sms);
       const double partial = 2.0 * s.ctas * mt * 128 * p.rp * 4;  // written and read again
-      const double cost[2] = {time_ns((double)units / s.ctas * unit_ns, bytes) + SHARED_NS + partial / DEVICE_BYTES_NS,
+      const double cost[2] = {time_ns((double)units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas) + partial / DEVICE_BYTES_NS,
                               time_ns((double)((outputs + sms - 1) / sms * plan->most_tiles) * unit_ns, bytes)};
       for (int whole = 0; whole < 2; ++whole)
         if (best < 0 || cost[whole] < best) {
