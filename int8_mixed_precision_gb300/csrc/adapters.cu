@@ -167,10 +167,29 @@ struct ToRank {
   const float* scale;
   __nv_bfloat16* held;
   float* slots;
-  int blocks;  // of 64 along the contraction
+  int blocks;   // of 64 along the contraction
+  int cluster;  // CTAs to a tile (CLUSTER)
 };
 
-template <bool MN>
+// Four columns of row r of tile ti of held, from their sums.
+__device__ __forceinline__ void store_held(const Args& p, const ToRank& o, const Tile& t, int64_t ti, int r, int col,
+                                           const float4& sum) {
+  const float scale = o.scale[t.g], v[4] = {sum.x, sum.y, sum.z, sum.w};
+  float part[4][PARTS];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) split_parts(r < t.rows && col + h < p.rank ? v[h] * scale : 0.f, part[h]);
+  __nv_bfloat16* held = o.held + (ti * TILE_ROWS + r) * (int64_t)(p.parts * p.rp) + col;
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h)
+    if (h < p.parts)
+      *reinterpret_cast<uint2*>(held + h * p.rp) = make_uint2(f2_to_bf16x2(part[0][h], part[1][h]), f2_to_bf16x2(part[2][h], part[3][h]));
+}
+
+// A tile falls to one CTA, to a cluster that splits its contraction (few tiles), or to the CTAs whose equal
+// shares of all units it meets; the cluster sums its partial results through distributed shared memory,
+// the others' are summed by k_to_rank_sum.
+
+template <bool MN, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, 1)
     k_to_rank(const __grid_constant__ CUtensorMap m_in, const __grid_constant__ CUtensorMap m_w, Args p, ToRank o) {
   pdl_launch_dependents();
@@ -192,7 +211,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int w_chunks = MN ? (p.rank + 63) / 64 : 1;
   const uint32_t w_bytes = MN ? w_chunks * 8192 : p.rp * 128;
   const uint32_t stage_bytes = 16384 + w_bytes;
-  const int64_t u0 = first_unit(p.split, blockIdx.x), u1 = first_unit(p.split, blockIdx.x + 1);
+  const int in_cluster = CLUSTER ? (int)cluster_rank() : 0;
+  const int64_t tile0 = CLUSTER ? blockIdx.x / o.cluster * (int64_t)o.blocks : 0;
+  const int64_t u0 = CLUSTER ? tile0 + (int64_t)o.blocks * in_cluster / o.cluster : first_unit(p.split, blockIdx.x);
+  const int64_t u1 = CLUSTER ? tile0 + (int64_t)o.blocks * (in_cluster + 1) / o.cluster : first_unit(p.split, blockIdx.x + 1);
 
   if (warp == 0) {
     if (!p.stall) {
@@ -306,6 +328,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
       }
       if (!ok) break;
+      if (CLUSTER) {  // every MMA of this CTA has read its operands: their place takes the partial result
+        const uint32_t mine = f.smem + (row * (p.rp + 4) + col0) * 4;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (4 * i < nc)
+            sts128(mine + 16 * i, make_uint4(__float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]),
+                                             __float_as_uint(acc[4 * i + 2]), __float_as_uint(acc[4 * i + 3])));
+        continue;
+      }
       const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
       if (!whole) {
         const int c0 = cta_of(p.split, ti * o.blocks);
@@ -336,6 +367,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
   }
+  if (CLUSTER) {
+    // Each CTA sums a share of the rows over the cluster's shared memories.
+    __syncthreads();
+    cluster_sync();
+    const int64_t ti = blockIdx.x / o.cluster;
+    const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
+    const int quads = p.rp / 4, rows = TILE_ROWS / o.cluster;
+    for (int e = threadIdx.x; e < rows * quads; e += THREADS) {
+      const int r = in_cluster * rows + e / quads, col = e % quads * 4;
+      const uint32_t at = f.smem + (r * (p.rp + 4) + col) * 4;
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = k < o.cluster ? ld_cluster_f4(mapa_rank(at, k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 sum = v[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
+      store_held(p, o, t, ti, r, col, sum);
+    }
+    cluster_sync();  // nobody still reads this CTA's shared memory
+  }
   finish(f, COLS);
 }
 
@@ -349,16 +400,7 @@ __global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
   const int c0 = cta_of(p.split, ti * o.blocks), c1 = cta_of(p.split, (ti + 1) * o.blocks - 1);
   if (c0 == c1) return;
   const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-  const float4 sum = sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e);
-  const float scale = o.scale[t.g], v[4] = {sum.x, sum.y, sum.z, sum.w};
-  float part[4][PARTS];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) split_parts(r < t.rows && col + h < p.rank ? v[h] * scale : 0.f, part[h]);
-  __nv_bfloat16* held = o.held + (ti * TILE_ROWS + r) * (int64_t)(p.parts * p.rp) + col;
-#pragma unroll
-  for (int h = 0; h < PARTS; ++h)
-    if (h < p.parts)
-      *reinterpret_cast<uint2*>(held + h * p.rp) = make_uint2(f2_to_bf16x2(part[0][h], part[1][h]), f2_to_bf16x2(part[2][h], part[3][h]));
+  store_held(p, o, t, ti, r, col, sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -413,7 +455,6 @@ template <bool MN, bool BF16>
 __global__ void __launch_bounds__(FROM_THREADS, 1)
     k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w,
                 const __grid_constant__ CUtensorMap m_out, Args p, FromRank o) {
-  pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
@@ -427,6 +468,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
+  pdl_launch_dependents();  // not before: see OverRows::early
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int steps = p.parts * p.rp / 16;           // of the contraction
@@ -697,6 +739,10 @@ struct OverRows {
   float* slots;
   int mtiles;      // 1, 2 or 4
   int whole;       // whole output tiles to each CTA, else equal shares of the units
+  // The kernel before it is k_from_rank, whose dx is no business of this one: it starts while that one still runs.
+  // k_from_rank lets it launch after its own wait, when everything that both read is complete; to
+  // keep the stream's order for what follows, it waits for k_from_rank before it ends.
+  int early;
 };
 
 // The boxes of a stage of e or h: where parts lie side by side in 64 columns (ranks of 16, 32 and 64 and
@@ -769,7 +815,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   }
   start(f, p.stages, COLS, ROW_EPI_WARPS);
   const uint32_t tmem = c->tmem;
-  pdl_wait();
+  if (!o.early) pdl_wait();
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const HeldBoxes hb(p.rp);
@@ -992,6 +1038,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
       for (int64_t i = threadIdx.x; i < n / 4; i += ROW_THREADS) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
+  if (o.early) pdl_wait();
   finish(f, COLS);
 }
 
@@ -1063,14 +1110,53 @@ static double time_ns(double share_ns, double bytes) {
   const double all = bytes / DEVICE_BYTES_NS;
   return share_ns > all ? share_ns : all;
 }
-static Split split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes) {
+struct RankSplit {
+  Split split;
+  int cluster;
+};
+// `clusters`: how many clusters of 2, 4 and 8 CTAs the device runs at a time
+static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const int (&clusters)[3]) {
   constexpr int64_t LEAST = 4;  // units of an equal share
+  constexpr double CLUSTER_NS = 2000;
   const int64_t sms = num_sms();
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
   const double unit_ns = (double)unit_bytes / SM_BYTES_NS, bytes = (double)s.units * unit_bytes;
   const double whole = time_ns((double)((tiles + sms - 1) / sms * blocks) * unit_ns, bytes);
   const double shared = time_ns((double)s.units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas);
-  return whole <= shared ? split_units(s.units, blocks, blocks, (int)sms) : s;
+  RankSplit best{whole <= shared ? split_units(s.units, blocks, blocks, (int)sms) : s, 1};
+  double ns = whole <= shared ? whole : shared;
+  for (int i = 0; i < 3; ++i) {
+    const int c = 2 << i;
+    const double t = time_ns((double)((blocks + c - 1) / c) * unit_ns, bytes) + CLUSTER_NS;
+    if (tiles <= clusters[i] && blocks >= 2 * c && t < ns) {
+      ns = t;
+      best.cluster = c;
+    }
+  }
+  return best;
+}
+template <auto KERN>
+static const int (&max_clusters())[3] {
+  struct Most {
+    int n[3];
+    Most() {
+      for (int i = 0; i < 3; ++i) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2u << i;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(num_sms() / (2 << i) * (2 << i));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n[i], KERN, &cfg) != cudaSuccess) n[i] = 0;
+      }
+    }
+  };
+  static const Most most;
+  return most.n;
 }
 
 // held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
@@ -1082,13 +1168,20 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   const bool maps = map_rows(&m_in, in, width, p.rows, TILE_ROWS) &&
                     (MN ? encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, 64)
                         : encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp));
-  if (!maps || !allow_smem<k_to_rank<MN>>()) return DIT_ERR_CUDA;
-  ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64)};
+  if (!maps || !allow_smem<k_to_rank<MN, false>>() || !allow_smem<k_to_rank<MN, true>>()) return DIT_ERR_CUDA;
+  ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64), 1};
   p.parts = parts;
   const uint32_t stage_bytes = 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128);
   p.stages = stages_for(RING_BYTES, stage_bytes);
-  p.split = split_to_rank(p.n_tiles, o.blocks, stage_bytes);
-  if (launch_pdl(k_to_rank<MN>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) != cudaSuccess)
+  const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>>());
+  p.split = cut.split;
+  o.cluster = cut.cluster;
+  if (cut.cluster > 1)
+    return launch_pdl(k_to_rank<MN, true>, dim3((unsigned)(p.n_tiles * cut.cluster)), dim3(THREADS), SMEM_BYTES, st,
+                      (unsigned)cut.cluster, m_in, m_w, p, o) == cudaSuccess
+               ? DIT_OK
+               : DIT_ERR_CUDA;
+  if (launch_pdl(k_to_rank<MN, false>, dim3(p.split.ctas), dim3(THREADS), SMEM_BYTES, st, 1, m_in, m_w, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (p.split.grain == 1 && p.split.ctas > 1 &&  // shares may end inside tiles
       launch_pdl(k_to_rank_sum, dim3((unsigned)(p.n_tiles * (TILE_ROWS * p.rp / 1024))), dim3(256), 0, st, 1, p, o) != cudaSuccess)
@@ -1104,8 +1197,8 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
-  // narrower blocks where wide ones would leave SMs without work, or the panels without room
-  if ((int64_t)p.n_tiles * ((width + 127) / 128) < num_sms() || RING_BYTES < h_bytes + 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
+  // narrower blocks where all of them run at once, or where wide ones leave the panels too little room
+  if ((int64_t)p.n_tiles * ((width + 63) / 64) <= num_sms() || RING_BYTES < h_bytes + 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
   const uint32_t w_bytes = bytes_of(o.nb);
   p.stages = 2;
   // two tiles of held if that leaves six panels; then up to four stages of weights
@@ -1200,6 +1293,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   OverRows o{};
   o.first = table + off_first(*plan);
   o.slots = reinterpret_cast<float*>(slots);
+  o.early = dx != nullptr;
   // The widths of the output tiles, and whole output tiles to each CTA or equal shares of the units.  A unit takes
   // its bytes' time or its 24 MMAs' for each 128 columns (25 ns measured up to rank 64, 50 at 128).
   {
