@@ -739,6 +739,7 @@ struct OverRows {
   float* slots;
   int mtiles;      // 1, 2 or 4
   int whole;       // whole output tiles to each CTA, else equal shares of the units
+  int cluster;     // CTAs to an output tile (CLUSTER)
   // The kernel before it is k_from_rank, whose dx is no business of this one: it starts while that one still runs.
   // k_from_rank lets it launch after its own wait, when everything that both read is complete; to
   // keep the stream's order for what follows, it waits for k_from_rank before it ends.
@@ -785,19 +786,44 @@ __device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, 
   r.tile = f0 + (u - r.first);
   return r;
 }
-// The first unit of output tile `i` of all (adapters without tiles have empty ones).
-__device__ __forceinline__ int64_t first_of_output(const Args& p, const OverRows& o, int64_t i) {
+// Output tile `i` of all: its problem, adapter, columns and units (none if its adapter has no tiles, or the
+// plan's table is wrong).
+struct Output {
+  bool second;
+  int64_t g, block, first, count;
+};
+__device__ __forceinline__ Output output_at(const Args& p, const OverRows& o, int64_t i) {
+  Output r;
   const int64_t outputs0 = o.g[0].blocks * p.n_adapters;
-  const bool second = i >= outputs0;
-  const int64_t blocks = second ? o.g[1].blocks : o.g[0].blocks, v = second ? i - outputs0 : i;
-  const int64_t g = v / blocks;
-  if (g >= p.n_adapters) return p.split.units;
-  const int64_t f0 = o.first[g], f1 = o.first[g + 1];
-  const int64_t u = (second ? o.g[0].blocks * p.n_tiles : 0) + blocks * f0 + v % blocks * (f1 - f0);
-  return max((int64_t)0, min(p.split.units, u));
+  r.second = i >= outputs0;
+  const int64_t blocks = r.second ? o.g[1].blocks : o.g[0].blocks, v = r.second ? i - outputs0 : i;
+  r.g = v / blocks;
+  r.block = v % blocks;
+  const int64_t f0 = o.first[r.g], f1 = o.first[r.g + 1];
+  const bool fine = f0 >= 0 && f0 <= f1 && f1 <= p.n_tiles;
+  if (!fine && threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
+  r.count = fine ? f1 - f0 : 0;
+  r.first = (r.second ? o.g[0].blocks * p.n_tiles : 0) + (fine ? blocks * f0 + r.block * r.count : 0);
+  return r;
+}
+// Four values of an output tile of m_all columns: e counts them as the output lies, columns along memory for dA,
+// the rank for dB.
+__device__ __forceinline__ void store_grad(const Args& p, const OverRows& o, const Output& r, int m_all, int e, const float4& v) {
+  if (r.second) {
+    const int64_t width = o.g[1].width, col = r.block * m_all + e / (p.rp / 4);
+    const int j = e % (p.rp / 4) * 4;
+    if (col < width && j < p.rank) *reinterpret_cast<float4*>(o.g[1].out + (r.g * width + col) * p.rank + j) = v;
+  } else {
+    const int64_t width = o.g[0].width, col = r.block * m_all + e % (m_all / 4) * 4;
+    const int j = e / (m_all / 4);
+    if (j < p.rank && col < width) *reinterpret_cast<float4*>(o.g[0].out + (r.g * p.rank + j) * width + col) = v;
+  }
 }
 
-template <int MT>  // tiles of 128 columns: 1, 2 or 4
+// MT: tiles of 128 columns, 1, 2 or 4.  An output tile's rows fall to one CTA, to a cluster (CLUSTER: few output
+// tiles; the partial results are summed through distributed shared memory), or to the CTAs whose equal
+// shares of all units it meets (summed by k_over_rows_sum).
+template <int MT, bool CLUSTER>
 __global__ void __launch_bounds__(ROW_THREADS, 1)
     k_over_rows(const __grid_constant__ CUtensorMap m_x, const __grid_constant__ CUtensorMap m_e,
                 const __grid_constant__ CUtensorMap m_dy, const __grid_constant__ CUtensorMap m_h, Args p, OverRows o) {
@@ -822,10 +848,17 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   const int a_boxes = 2 * MT;
   const uint32_t stage_bytes = (a_boxes + hb.boxes) * ROW_BOX;
   int64_t u0, u1;
-  if (o.whole) {
+  Output mine{};
+  const int in_cluster = CLUSTER ? (int)cluster_rank() : 0;
+  if (CLUSTER) {
+    mine = output_at(p, o, blockIdx.x / o.cluster);
+    u0 = mine.first + mine.count * in_cluster / o.cluster;
+    u1 = mine.first + mine.count * (in_cluster + 1) / o.cluster;
+  } else if (o.whole) {
     const int64_t outputs = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters;
-    u0 = first_of_output(p, o, outputs * blockIdx.x / gridDim.x);
-    u1 = first_of_output(p, o, outputs * (blockIdx.x + 1) / gridDim.x);
+    const int64_t i = outputs * (blockIdx.x + 1) / gridDim.x;
+    u0 = output_at(p, o, outputs * blockIdx.x / gridDim.x).first;
+    u1 = i < outputs ? output_at(p, o, i).first : p.split.units;
   } else {
     u0 = first_unit(p.split, blockIdx.x);
     u1 = first_unit(p.split, blockIdx.x + 1);
@@ -994,6 +1027,22 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
       }
       if (!ok) break;
+      if (CLUSTER) {  // every MMA of this CTA has read its operands: their place takes the partial result
+        if (r.problem) {
+          const uint32_t at = f.smem + (m * (p.rp + 4) + col0) * 4;
+#pragma unroll
+          for (int i = 0; i < 64; i += 4)
+            if (i < nc)
+              sts128(at + 4 * i, make_uint4(__float_as_uint(acc[i]), __float_as_uint(acc[i + 1]), __float_as_uint(acc[i + 2]),
+                                            __float_as_uint(acc[i + 3])));
+        } else {
+          const uint32_t at = f.smem + (col0 * m_all + m) * 4;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < nc) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * i * m_all), "f"(acc[i]) : "memory");
+        }
+        continue;
+      }
       if (!whole) {
         const int c0 = cta_of(p.split, r.first);
         const int64_t slot = (int64_t)m_all * p.rp;
@@ -1029,6 +1078,26 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
       }
     }
   }
+  if (CLUSTER) {
+    // Each CTA sums a share of the output tile over the shared memories of the CTAs that have units of it.
+    __syncthreads();
+    cluster_sync();
+    constexpr int m_all = MT * 128;
+    const int all = m_all * p.rp / 4, quads = p.rp / 4;
+    uint32_t with = 0;
+    for (int k = 0; k < o.cluster; ++k)
+      if (mine.count * (k + 1) / o.cluster > mine.count * k / o.cluster) with |= 1u << k;
+    if (with)
+      for (int e = all / o.cluster * in_cluster + threadIdx.x; e < all / o.cluster * (in_cluster + 1); e += ROW_THREADS) {
+        const uint32_t at = f.smem + (mine.second ? (e / quads * (p.rp + 4) + e % quads * 4) * 4 : e * 16);
+        float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = with >> k & 1 ? ld_cluster_f4(mapa_rank(at, k)) : sum;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
+        store_grad(p, o, mine, m_all, e, sum);
+      }
+  }
   // adapters without rows
   for (int g = blockIdx.x; g < p.n_adapters; g += gridDim.x) {
     if (o.first[g] != o.first[g + 1]) continue;
@@ -1039,6 +1108,10 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
     }
   }
   if (o.early) pdl_wait();
+  if (CLUSTER) {
+    __syncwarp();
+    cluster_sync();  // nobody still reads this CTA's shared memory
+  }
   finish(f, COLS);
 }
 
@@ -1047,26 +1120,11 @@ __global__ void __launch_bounds__(256) k_over_rows_sum(Args p, OverRows o) {
   pdl_launch_dependents();
   pdl_wait();
   const int m_all = o.mtiles * 128, ctas = m_all * p.rp / 1024;
-  const int64_t i = blockIdx.x / ctas, outputs0 = o.g[0].blocks * p.n_adapters;
+  const Output r = output_at(p, o, blockIdx.x / ctas);
+  if (!r.count) return;
   const int e = blockIdx.x % ctas * 256 + threadIdx.x;
-  const bool second = i >= outputs0;
-  const int64_t blocks = second ? o.g[1].blocks : o.g[0].blocks, v = second ? i - outputs0 : i, g = v / blocks, block = v % blocks;
-  const int64_t width = second ? o.g[1].width : o.g[0].width;
-  const int64_t f0 = o.first[g], f1 = o.first[g + 1];
-  if (f0 < 0 || f0 >= f1 || f1 > p.n_tiles) return;
-  const int64_t first = (second ? o.g[0].blocks * p.n_tiles : 0) + blocks * f0 + block * (f1 - f0);
-  const int c0 = cta_of(p.split, first), c1 = cta_of(p.split, first + f1 - f0 - 1);
-  if (c0 == c1) return;
-  const float4 sum = sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e);
-  if (second) {
-    const int64_t col = block * m_all + e / (p.rp / 4);
-    const int j = e % (p.rp / 4) * 4;
-    if (col < width && j < p.rank) *reinterpret_cast<float4*>(o.g[1].out + (g * width + col) * p.rank + j) = sum;
-  } else {
-    const int j = e / (m_all / 4);
-    const int64_t col = block * m_all + e % (m_all / 4) * 4;
-    if (j < p.rank && col < width) *reinterpret_cast<float4*>(o.g[0].out + (g * p.rank + j) * width + col) = sum;
-  }
+  const int c0 = cta_of(p.split, r.first), c1 = cta_of(p.split, r.first + r.count - 1);
+  if (c0 != c1) store_grad(p, o, r, m_all, e, sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1105,6 +1163,7 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
 // equal shares and 22.8 and 36.8 with whole tiles, though those keep only 33 and 94 SMs busy;
 // at 130 rows it is 13.5 against 15.7.)
 constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500;
+constexpr double CLUSTER_NS = 2000, CLUSTER_ROWS_NS = 7000;  // what a cluster takes to sum h or e, or a gradient
 static double shared_ns(int ctas) { return 3700 + 12.0 * ctas; }
 static double time_ns(double share_ns, double bytes) {
   const double all = bytes / DEVICE_BYTES_NS;
@@ -1117,7 +1176,6 @@ struct RankSplit {
 // `clusters`: how many clusters of 2, 4 and 8 CTAs the device runs at a time
 static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const int (&clusters)[3]) {
   constexpr int64_t LEAST = 4;  // units of an equal share
-  constexpr double CLUSTER_NS = 2000;
   const int64_t sms = num_sms();
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
   const double unit_ns = (double)unit_bytes / SM_BYTES_NS, bytes = (double)s.units * unit_bytes;
@@ -1135,7 +1193,7 @@ static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes
   }
   return best;
 }
-template <auto KERN>
+template <auto KERN, int N_THREADS>
 static const int (&max_clusters())[3] {
   struct Most {
     int n[3];
@@ -1147,7 +1205,7 @@ static const int (&max_clusters())[3] {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(num_sms() / (2 << i) * (2 << i));
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(N_THREADS);
         cfg.dynamicSmemBytes = SMEM_BYTES;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -1157,6 +1215,11 @@ static const int (&max_clusters())[3] {
   };
   static const Most most;
   return most.n;
+}
+
+static bool over_rows_allowed() {
+  return allow_smem<k_over_rows<1, false>>() && allow_smem<k_over_rows<2, false>>() && allow_smem<k_over_rows<4, false>>() &&
+         allow_smem<k_over_rows<1, true>>() && allow_smem<k_over_rows<2, true>>() && allow_smem<k_over_rows<4, true>>();
 }
 
 // held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
@@ -1173,7 +1236,7 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   p.parts = parts;
   const uint32_t stage_bytes = 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128);
   p.stages = stages_for(RING_BYTES, stage_bytes);
-  const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>>());
+  const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>, THREADS>());
   p.split = cut.split;
   o.cluster = cut.cluster;
   if (cut.cluster > 1)
@@ -1289,6 +1352,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   dit_status s = to_rank<true>(p, dy, n, b, scale, scratch, PARTS, slots, st);
   if (s == DIT_OK && dx) s = from_rank<true>(p, scratch, PARTS, a, dx, dx_dt, k, st);
   if (s != DIT_OK) return s;
+  if (!over_rows_allowed()) return DIT_ERR_CUDA;
 
   OverRows o{};
   o.first = table + off_first(*plan);
@@ -1298,26 +1362,36 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   // its bytes' time or its 24 MMAs' for each 128 columns (25 ns measured up to rank 64, 50 at 128).
   {
     const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
+    const auto& clusters = max_clusters<k_over_rows<2, true>, ROW_THREADS>();
     double best = -1;
     for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
       const int64_t bk = (k + 128 * mt - 1) / (128 * mt), bn = (n + 128 * mt - 1) / (128 * mt);
       const int64_t unit = (2 * mt + boxes) * 16384, outputs = (bk + bn) * p.n_adapters, units = (bk + bn) * p.n_tiles;
       const double mma_ns = mt * 24 * (p.rp <= 64 ? 25.0 : 25.0 * p.rp / 64), load_ns = (double)unit / SM_BYTES_NS;
-      const double unit_ns = mma_ns > load_ns ? mma_ns : load_ns, bytes = (double)units * unit;
+      const double unit_ns = mma_ns > load_ns ? mma_ns : load_ns;
+      const double bytes = (double)units * 16384 * (2 * mt + boxes / 2.5);  // e and h come out of L2, faster
       const Split s = split_units(units, 1, 1, (int)sms);
       const double partial = 2.0 * s.ctas * mt * 128 * p.rp * 4;  // written and read again
-      const double cost[2] = {time_ns((double)units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas) + partial / DEVICE_BYTES_NS,
+      const double cost[2] = {time_ns((double)units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas) + partial / 3000,
                               time_ns((double)((outputs + sms - 1) / sms * plan->most_tiles) * unit_ns, bytes)};
-      for (int whole = 0; whole < 2; ++whole)
-        if (best < 0 || cost[whole] < best) {
-          best = cost[whole];
-          o.mtiles = mt;
-          o.whole = whole;
-          o.g[0] = Grad{da, k, bk};
-          o.g[1] = Grad{db, n, bn};
-          p.split = s;
-          if (whole) p.split.ctas = (int)(outputs < s.ctas ? outputs : s.ctas);
-        }
+      auto take = [&](double ns, int whole, int cluster, int64_t ctas) {
+        if (best >= 0 && ns >= best) return;
+        best = ns;
+        o.mtiles = mt;
+        o.whole = whole;
+        o.cluster = cluster;
+        o.g[0] = Grad{da, k, bk};
+        o.g[1] = Grad{db, n, bn};
+        p.split = s;
+        p.split.ctas = (int)ctas;
+      };
+      take(cost[0], 0, 1, s.ctas);
+      take(cost[1], 1, 1, outputs < s.ctas ? outputs : s.ctas);
+      for (int i = 0; i < 3; ++i) {
+        const int64_t c = 2 << i;
+        if (outputs <= clusters[i] && plan->most_tiles >= c)
+          take(time_ns((double)((plan->most_tiles + c - 1) / c) * unit_ns, bytes) + CLUSTER_ROWS_NS, 1, (int)c, outputs * c);
+      }
     }
   }
   const int64_t sum_ctas = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * (o.mtiles * 128 * p.rp / 1024);
@@ -1325,13 +1399,13 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
-      !map_rows(&m_dy, dy, n, p.rows, ROW_STAGE) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, ROW_STAGE) ||
-      !allow_smem<k_over_rows<1>>() || !allow_smem<k_over_rows<2>>() || !allow_smem<k_over_rows<4>>())
+      !map_rows(&m_dy, dy, n, p.rows, ROW_STAGE) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, ROW_STAGE))
     return DIT_ERR_CUDA;
-  auto kern = o.mtiles == 4 ? k_over_rows<4> : o.mtiles == 2 ? k_over_rows<2> : k_over_rows<1>;
+  auto kern = o.cluster > 1 ? (o.mtiles == 4 ? k_over_rows<4, true> : o.mtiles == 2 ? k_over_rows<2, true> : k_over_rows<1, true>)
+                            : (o.mtiles == 4 ? k_over_rows<4, false> : o.mtiles == 2 ? k_over_rows<2, false> : k_over_rows<1, false>);
   const int h_boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
   p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
-  if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, 1, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
+  if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, (unsigned)o.cluster, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (!o.whole && p.split.ctas > 1 &&
       launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
