@@ -428,6 +428,11 @@ struct FromRank {
   int per_job;       // blocks
   int64_t jobs, tile_jobs;  // all, and of a tile
   int panels, helds; // of the rings
+  // The kernel before it is k_over_rows, whose gradients are no business of this one: it starts while that one
+  // still runs, and its jobs fill the SMs that are done there.  k_over_rows lets it launch after its own
+  // wait, when everything that both read is complete; to keep the stream's order for what
+  // follows, it waits for k_over_rows before it ends.
+  int early;
 };
 // Where a job begins, and its blocks.
 struct Job {
@@ -461,6 +466,7 @@ template <bool MN, bool BF16>
 __global__ void __launch_bounds__(FROM_THREADS, 1)
     k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w,
                 const __grid_constant__ CUtensorMap m_out, Args p, FromRank o) {
+  pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
@@ -473,8 +479,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   }
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
-  pdl_wait();
-  pdl_launch_dependents();  // not before: see OverRows::early
+  if (!o.early) pdl_wait();
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int steps = p.parts * p.rp / 16;           // of the contraction
@@ -717,6 +722,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
     }
     if (lane == 0) tma_store_wait();
   }
+  if (o.early) pdl_wait();
   finish(f, COLS);
 }
 
@@ -746,10 +752,6 @@ struct OverRows {
   int mtiles;      // 1, 2 or 4
   int whole;       // whole output tiles to each CTA, else equal shares of the units
   int cluster;     // CTAs to an output tile (CLUSTER)
-  // The kernel before it is k_from_rank, whose dx is no business of this one: it starts while that one still runs.
-  // k_from_rank lets it launch after its own wait, when everything that both read is complete; to
-  // keep the stream's order for what follows, it waits for k_from_rank before it ends.
-  int early;
 };
 
 // The boxes of a stage of e or h: where parts lie side by side in 64 columns (ranks of 16, 32 and 64 and
@@ -833,7 +835,6 @@ template <int MT, bool CLUSTER>
 __global__ void __launch_bounds__(ROW_THREADS, 1)
     k_over_rows(const __grid_constant__ CUtensorMap m_x, const __grid_constant__ CUtensorMap m_e,
                 const __grid_constant__ CUtensorMap m_dy, const __grid_constant__ CUtensorMap m_h, Args p, OverRows o) {
-  pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
@@ -847,7 +848,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   }
   start(f, p.stages, COLS, ROW_EPI_WARPS);
   const uint32_t tmem = c->tmem;
-  if (!o.early) pdl_wait();
+  pdl_wait();
+  pdl_launch_dependents();  // not before: see FromRank::early
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const HeldBoxes hb(p.rp);
@@ -1113,7 +1115,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
       for (int64_t i = threadIdx.x; i < n / 4; i += ROW_THREADS) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (o.early) pdl_wait();
   if (CLUSTER) {
     __syncwarp();
     cluster_sync();  // nobody still reads this CTA's shared memory
@@ -1260,9 +1261,10 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 
 // out += held W; MN: w is [n_adapters][rank][width], else [n_adapters][width][rank]; held has `held_parts` parts
 template <bool MN, bool BF16>
-static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, cudaStream_t st) {
+static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, bool early,
+                            cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
-  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1};
+  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, early ? 1 : 0};
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
@@ -1304,9 +1306,9 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
 }
 template <bool MN>
 static dit_status from_rank(const Args& p, const void* held, int held_parts, const void* w, void* out, dit_dtype dt,
-                            int64_t width, cudaStream_t st) {
-  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, st)
-                        : from_rank<MN, false>(p, held, held_parts, w, out, width, st);
+                            int64_t width, bool early, cudaStream_t st) {
+  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, early, st)
+                        : from_rank<MN, false>(p, held, held_parts, w, out, width, early, st);
 }
 
 }  // namespace lora
@@ -1331,7 +1333,7 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
   const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
   dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
-  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, st);
+  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, false, st);
   if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
   return s;
 }
@@ -1356,14 +1358,12 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
     return ok ? DIT_OK : DIT_ERR_CUDA;
   }
   dit_status s = to_rank<true>(p, dy, n, b, scale, scratch, PARTS, slots, st);
-  if (s == DIT_OK && dx) s = from_rank<true>(p, scratch, PARTS, a, dx, dx_dt, k, st);
   if (s != DIT_OK) return s;
   if (!over_rows_allowed()) return DIT_ERR_CUDA;
 
   OverRows o{};
   o.first = table + off_first(*plan);
   o.slots = reinterpret_cast<float*>(slots);
-  o.early = dx != nullptr;
   // The widths of the output tiles, and whole output tiles to each CTA or equal shares of the units.  A unit takes
   // its bytes' time or its 24 MMAs' for each 128 columns (25 ns measured up to rank 64, 50 at 128).
   {
@@ -1413,6 +1413,10 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
   if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, (unsigned)o.cluster, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
+  // dx after the gradients of the factors: dy, which the first product has just read, is still in L2 for them
+  // where it fits.
+  if (dx) s = from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, true, st);
+  if (s != DIT_OK) return s;
   if (!o.whole && p.split.ctas > 1 &&
       launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
