@@ -22,6 +22,12 @@
 // element of the contraction, 4.4e-6 over 4096), so sums are drained to registers every CHUNK
 // elements and added there with rounding to nearest.
 //
+// Ahead of the stream.  Each kernel lets the next one launch only after its own wait for the one before, so a kernel
+// that has started finds everything but its immediate predecessor complete, and waits for that one
+// where it first reads what it made (h and e) or writes what it reads: k_from_rank's first weights and
+// old values and k_over_rows' units of dB come in before.  Every kernel waits before it ends, so the
+// stream's order holds for whatever follows.
+//
 // Warps: 0 loads (TMA), 1 issues the MMAs, the others drain and store.  Every wait is bounded.  Loads and MMAs
 // are issued by an elected lane of a converged warp, from values that the warp shares: otherwise the
 // compiler moves every operand to uniform registers first, 50 ns an MMA.
@@ -198,7 +204,6 @@ __device__ __forceinline__ void store_held(const Args& p, const ToRank& o, const
 template <bool MN, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, 1)
     k_to_rank(const __grid_constant__ CUtensorMap m_in, const __grid_constant__ CUtensorMap m_w, Args p, ToRank o) {
-  pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
@@ -211,6 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
   pdl_wait();
+  pdl_launch_dependents();  // not before: see above, ahead of the stream
   if (blockIdx.x == 0 && threadIdx.x == 0) *ws_u32(p.ws, WS_JOBS) = 0;  // for the next k_from_rank
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -398,8 +404,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // The tiles that several CTAs share: four columns of a row to a thread.
 __global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int quads = p.rp / 4, ctas = TILE_ROWS * quads / 256;  // rp is a multiple of 16
   const int64_t ti = blockIdx.x / ctas;
   const int e = blockIdx.x % ctas * 256 + threadIdx.x, r = e / quads, col = e % quads * 4;
@@ -407,6 +413,78 @@ __global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
   if (c0 == c1) return;
   const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
   store_held(p, o, t, ti, r, col, sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e));
+}
+
+// ---------------------------------------------------------------------------------------
+// The gradients' output tiles (see k_over_rows)
+// ---------------------------------------------------------------------------------------
+struct Grad {
+  float* out;
+  int64_t width;
+  int64_t blocks;  // of the output, along the width
+};
+struct OverRows {
+  Grad g[2];       // dB [n x rank], dA [rank x k]
+  const int32_t* first;
+  float* slots;
+  int mtiles;      // 1, 2 or 4
+  int whole;       // whole output tiles to each CTA, else equal shares of the units
+  int cluster;     // CTAs to an output tile (CLUSTER)
+  Split split;     // of the units
+};
+
+// Output tile `i` of all: its problem, adapter, columns and units (none if its adapter has no tiles, or the
+// plan's table is wrong).
+struct Output {
+  bool second;
+  int64_t g, block, first, count;
+};
+__device__ __forceinline__ Output output_at(const Args& p, const OverRows& o, int64_t i) {
+  Output r;
+  const int64_t outputs0 = o.g[0].blocks * p.n_adapters;
+  r.second = i >= outputs0;
+  const int64_t blocks = r.second ? o.g[1].blocks : o.g[0].blocks, v = r.second ? i - outputs0 : i;
+  r.g = v / blocks;
+  r.block = v % blocks;
+  const int64_t f0 = o.first[r.g], f1 = o.first[r.g + 1];
+  const bool fine = f0 >= 0 && f0 <= f1 && f1 <= p.n_tiles;
+  if (!fine && threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
+  r.count = fine ? f1 - f0 : 0;
+  r.first = (r.second ? o.g[0].blocks * p.n_tiles : 0) + (fine ? blocks * f0 + r.block * r.count : 0);
+  return r;
+}
+// Four values of an output tile of m_all columns: e counts them as the output lies, columns along memory for dA,
+// the rank for dB.
+__device__ __forceinline__ void store_grad(const Args& p, const OverRows& o, const Output& r, int m_all, int e, const float4& v) {
+  if (r.second) {
+    const int64_t width = o.g[1].width, col = r.block * m_all + e % (m_all / 4) * 4;
+    const int j = e / (m_all / 4);
+    if (j < p.rank && col < width) *reinterpret_cast<float4*>(o.g[1].out + (r.g * p.rank + j) * width + col) = v;
+  } else {
+    const int64_t width = o.g[0].width, col = r.block * m_all + e / (p.rp / 4);
+    const int j = e % (p.rp / 4) * 4;
+    if (col < width && j < p.rank) *reinterpret_cast<float4*>(o.g[0].out + (r.g * width + col) * p.rank + j) = v;
+  }
+}
+
+// Adds up the output tiles that several CTAs of k_over_rows share, four values to a thread at a time; this CTA is
+// number `cta` of `ctas`, with N threads.
+template <int N>
+__device__ __forceinline__ void add_up_grads(const Args& p, const OverRows& o, int cta, int ctas) {
+  const int m_all = o.mtiles * 128, quads = m_all * p.rp / 4, chunks = (quads + 2 * N - 1) / (2 * N);
+  const int64_t all = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * chunks;
+  for (int64_t c = cta; c < all; c += ctas) {
+    const Output r = output_at(p, o, c / chunks);
+    if (!r.count) continue;
+    const int c0 = cta_of(o.split, r.first), c1 = cta_of(o.split, r.first + r.count - 1);
+    if (c0 == c1) continue;
+    const int first = (int)(c % chunks) * 2 * N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = first + i * N + threadIdx.x;
+      if (e < quads) store_grad(p, o, r, m_all, e, sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e));
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -428,11 +506,10 @@ struct FromRank {
   int per_job;       // blocks
   int64_t jobs, tile_jobs;  // all, and of a tile
   int panels, helds; // of the rings
-  // The kernel before it is k_over_rows, whose gradients are no business of this one: it starts while that one
-  // still runs, and its jobs fill the SMs that are done there.  k_over_rows lets it launch after its own
-  // wait, when everything that both read is complete; to keep the stream's order for what
-  // follows, it waits for k_over_rows before it ends.
+  // The kernel before it is k_over_rows, whose gradients are no business of this one: its jobs fill the SMs that
+  // are done there, without a wait for the others.
   int early;
+  int sums;  // then, this kernel adds up what k_over_rows left in parts (no launch of its own for that)
 };
 // Where a job begins, and its blocks.
 struct Job {
@@ -465,8 +542,7 @@ constexpr int FROM_THREADS = THREADS + 32;  // and a warp that stores
 template <bool MN, bool BF16>
 __global__ void __launch_bounds__(FROM_THREADS, 1)
     k_from_rank(const __grid_constant__ CUtensorMap m_held, const __grid_constant__ CUtensorMap m_w,
-                const __grid_constant__ CUtensorMap m_out, Args p, FromRank o) {
-  pdl_launch_dependents();
+                const __grid_constant__ CUtensorMap m_out, Args p, FromRank o, OverRows rows) {
   extern __shared__ uint8_t raw[];
   const Frame f = frame(raw);
   Control* c = f.c;
@@ -479,7 +555,6 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
   }
   start(f, p.stages, COLS);
   const uint32_t tmem = c->tmem;
-  if (!o.early) pdl_wait();
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int steps = p.parts * p.rp / 16;           // of the contraction
@@ -497,7 +572,8 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
       uint32_t n = 0, tiles = 0, np = 0, announced = 0;
       int s = 0, q = 0;
       uint32_t sp = 1, qp = 1;  // parities of the rings' next waits
-      bool ok = true;
+      bool ok = true, waited = o.early != 0;
+      if (waited) pdl_launch_dependents();
       int64_t job = blockIdx.x;
       while (ok) {
         const int js = announced % JOBS;
@@ -511,12 +587,49 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
         if (lane == 0) {
           c->job[js] = more ? (int)job : -1;
           mbar_arrive(smem_u32(&c->jfull[js]));
-          if (more) next = atomicAdd(ws_u32(p.ws, WS_JOBS), 1u);
         }
         ++announced;
         if (!more) break;
         const Job j(o, job);
         const Tile t = load_tile(p.table, j.tile, p.rows, p.n_adapters, p.ws);
+        auto load_w = [&](int b) {
+          const int n0 = b * o.nb;
+          const uint32_t full = smem_u32(&c->full[s]);
+          if (elect_one()) {
+            mbar_expect_tx(full, w_bytes);
+            for (int i = 0; i < w_boxes; ++i)
+              tma_load_3d(ring + s * w_bytes + i * box_bytes, &m_w, full, MN ? n0 + i * 64 : i * 64, MN ? 0 : n0, t.g);
+          }
+          __syncwarp();
+          ++n;
+          if (++s == p.stages) {
+            s = 0;
+            sp ^= 1;
+          }
+        };
+        auto load_panel = [&](int b, int i) {
+          if (elect_one()) {
+            mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
+            tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), b * o.nb + i * PC, t.row0);
+          }
+          __syncwarp();
+          ++np;
+          if (++q == o.panels) {
+            q = 0;
+            qp ^= 1;
+          }
+        };
+        // Weights and old values of the first block are nobody's business that may still run: they come in while
+        // the last of h is made.
+        int done = 0;  // panels of the first block
+        if (!waited) {
+          load_w(j.block);
+          for (const int all = min(panels_of(j.block), o.panels); done < all; ++done) load_panel(j.block, done);
+          waited = true;
+          pdl_wait();
+          pdl_launch_dependents();
+        }
+        if (lane == 0) next = atomicAdd(ws_u32(p.ws, WS_JOBS), 1u);
         const int hs = tiles % o.helds;
         if (!warp_wait(smem_u32(&c->hempty[hs]), ((tiles / o.helds) & 1) ^ 1, p.ws, abort)) {
           ok = false;
@@ -530,38 +643,21 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
         __syncwarp();
         ++tiles;
         for (int b = j.block; b < j.block + j.blocks && ok; ++b) {
-          const int n0 = b * o.nb;
-          if (!warp_wait(smem_u32(&c->empty[s]), sp, p.ws, abort)) {
-            ok = false;
-            break;
+          if (done == 0) {
+            if (!warp_wait(smem_u32(&c->empty[s]), sp, p.ws, abort)) {
+              ok = false;
+              break;
+            }
+            load_w(b);
           }
-          const uint32_t full = smem_u32(&c->full[s]);
-          if (elect_one()) {
-            mbar_expect_tx(full, w_bytes);
-            for (int i = 0; i < w_boxes; ++i)
-              tma_load_3d(ring + s * w_bytes + i * box_bytes, &m_w, full, MN ? n0 + i * 64 : i * 64, MN ? 0 : n0, t.g);
-          }
-          __syncwarp();
-          ++n;
-          if (++s == p.stages) {
-            s = 0;
-            sp ^= 1;
-          }
-          for (int i = 0, all = panels_of(b); i < all; ++i, ++np) {
+          for (const int all = panels_of(b); done < all; ++done) {
             if (!warp_wait(smem_u32(&c->yempty[q]), qp, p.ws, abort)) {
               ok = false;
               break;
             }
-            if (elect_one()) {
-              mbar_expect_tx(smem_u32(&c->yfull[q]), 16384);
-              tma_load_2d(panels + q * 16384, &m_out, smem_u32(&c->yfull[q]), n0 + i * PC, t.row0);
-            }
-            __syncwarp();
-            if (++q == o.panels) {
-              q = 0;
-              qp ^= 1;
-            }
+            load_panel(b, done);
           }
+          done = 0;
         }
         job = (int64_t)__shfl_sync(0xffffffffu, next, 0) + gridDim.x;
       }
@@ -722,7 +818,8 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
     }
     if (lane == 0) tma_store_wait();
   }
-  if (o.early) pdl_wait();
+  pdl_wait();
+  if (MN && o.sums) add_up_grads<FROM_THREADS>(p, rows, blockIdx.x, gridDim.x);
   finish(f, COLS);
 }
 
@@ -736,23 +833,9 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
 // tensor memory holds twice over (512 columns up to rank 64, 256 above); accumulators are
 // drained after every 128 rows, 24 instructions, while the other ones fill.
 // ---------------------------------------------------------------------------------------
-constexpr int ROW_EPI_WARPS = 16, ROW_THREADS = 64 + 32 * ROW_EPI_WARPS;
+constexpr int ROW_EPI_WARPS = 16, ROW_THREADS = 96 + 32 * ROW_EPI_WARPS;  // and a warp that lets the next kernel launch
 constexpr int ROW_STAGE = 32;       // rows of a stage
 constexpr int ROW_BOX = ROW_STAGE * 128;  // bytes of a box of 64 columns
-
-struct Grad {
-  float* out;
-  int64_t width;
-  int64_t blocks;  // of the output, along the width
-};
-struct OverRows {
-  Grad g[2];       // dA [rank x k], dB [n x rank]
-  const int32_t* first;
-  float* slots;
-  int mtiles;      // 1, 2 or 4
-  int whole;       // whole output tiles to each CTA, else equal shares of the units
-  int cluster;     // CTAs to an output tile (CLUSTER)
-};
 
 // The boxes of a stage of e or h: where parts lie side by side in 64 columns (ranks of 16, 32 and 64 and
 // 128 after padding) they are loaded so, otherwise each part begins a box of its own, since an
@@ -779,7 +862,7 @@ struct RowsUnit {
 __device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, int64_t u) {
   RowsUnit r;
   const int64_t units0 = o.g[0].blocks * p.n_tiles;
-  r.problem = u >= units0;
+  r.problem = u >= units0;  // 0: dB, 1: dA
   const int64_t base = r.problem ? units0 : 0, blocks = r.problem ? o.g[1].blocks : o.g[0].blocks, v = u - base;
   // An adapter's units follow one another and its tiles are [f0, f1): v / blocks is one of its tiles.
   r.g = p.table[4 * (v / blocks) + 2];
@@ -794,40 +877,6 @@ __device__ __forceinline__ RowsUnit rows_unit(const Args& p, const OverRows& o, 
   r.tile = f0 + (u - r.first);
   return r;
 }
-// Output tile `i` of all: its problem, adapter, columns and units (none if its adapter has no tiles, or the
-// plan's table is wrong).
-struct Output {
-  bool second;
-  int64_t g, block, first, count;
-};
-__device__ __forceinline__ Output output_at(const Args& p, const OverRows& o, int64_t i) {
-  Output r;
-  const int64_t outputs0 = o.g[0].blocks * p.n_adapters;
-  r.second = i >= outputs0;
-  const int64_t blocks = r.second ? o.g[1].blocks : o.g[0].blocks, v = r.second ? i - outputs0 : i;
-  r.g = v / blocks;
-  r.block = v % blocks;
-  const int64_t f0 = o.first[r.g], f1 = o.first[r.g + 1];
-  const bool fine = f0 >= 0 && f0 <= f1 && f1 <= p.n_tiles;
-  if (!fine && threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
-  r.count = fine ? f1 - f0 : 0;
-  r.first = (r.second ? o.g[0].blocks * p.n_tiles : 0) + (fine ? blocks * f0 + r.block * r.count : 0);
-  return r;
-}
-// Four values of an output tile of m_all columns: e counts them as the output lies, columns along memory for dA,
-// the rank for dB.
-__device__ __forceinline__ void store_grad(const Args& p, const OverRows& o, const Output& r, int m_all, int e, const float4& v) {
-  if (r.second) {
-    const int64_t width = o.g[1].width, col = r.block * m_all + e / (p.rp / 4);
-    const int j = e % (p.rp / 4) * 4;
-    if (col < width && j < p.rank) *reinterpret_cast<float4*>(o.g[1].out + (r.g * width + col) * p.rank + j) = v;
-  } else {
-    const int64_t width = o.g[0].width, col = r.block * m_all + e % (m_all / 4) * 4;
-    const int j = e / (m_all / 4);
-    if (j < p.rank && col < width) *reinterpret_cast<float4*>(o.g[0].out + (r.g * p.rank + j) * width + col) = v;
-  }
-}
-
 // MT: tiles of 128 columns, 1, 2 or 4.  An output tile's rows fall to one CTA, to a cluster (CLUSTER: few output
 // tiles; the partial results are summed through distributed shared memory), or to the CTAs whose equal
 // shares of all units it meets (summed by k_over_rows_sum).
@@ -848,8 +897,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   }
   start(f, p.stages, COLS, ROW_EPI_WARPS);
   const uint32_t tmem = c->tmem;
-  pdl_wait();
-  pdl_launch_dependents();  // not before: see FromRank::early
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const HeldBoxes hb(p.rp);
@@ -884,9 +931,10 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
           ++u;
           continue;
         }
+        if (r.problem) pdl_wait();  // e is the previous kernel's
         const int64_t end = min(u1, r.first + r.count);
         const int4* entry = reinterpret_cast<const int4*>(p.table) + r.tile;
-        const CUtensorMap *wide = r.problem ? &m_dy : &m_x, *narrow = r.problem ? &m_h : &m_e;
+        const CUtensorMap *wide = r.problem ? &m_x : &m_dy, *narrow = r.problem ? &m_e : &m_h;
         const int col = (int)(r.block * a_boxes) * 64;
         int held_row = (int)(r.tile * TILE_ROWS);
         int4 next = *entry;
@@ -984,6 +1032,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
     }
     if (elect_one()) await_mmas(f, p.ws);
     __syncwarp();
+  } else if (warp == 2 + ROW_EPI_WARPS) {
+    pdl_wait();
+    pdl_launch_dependents();
   } else {
     // Sixteen warps: four to the quarters of 128 columns; the four groups take an M tile each (mtiles 4), half
     // the rank of two, or half of one (then two groups have nothing).
@@ -1035,8 +1086,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(&c->dempty[buf]));
       }
       if (!ok) break;
+      pdl_wait();  // what is written from here on may still be read by the previous kernel
       if (CLUSTER) {  // every MMA of this CTA has read its operands: their place takes the partial result
-        if (r.problem) {
+        if (!r.problem) {
           const uint32_t at = f.smem + (m * (p.rp + 4) + col0) * 4;
 #pragma unroll
           for (int i = 0; i < 64; i += 4)
@@ -1056,7 +1108,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         const int64_t slot = (int64_t)m_all * p.rp;
         // as the output lies: columns along memory for dA, the rank for dB
         float* mine = o.slots + slot_of(blockIdx.x, c0) * slot;
-        if (r.problem) {
+        if (!r.problem) {
           mine += (int64_t)m * p.rp + col0;
 #pragma unroll
           for (int i = 0; i < 64; i += 4)
@@ -1072,7 +1124,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
       const int64_t col = r.block * m_all + m, width = r.problem ? o.g[1].width : o.g[0].width;
       if (col < width) {
         float* out = (r.problem ? o.g[1].out : o.g[0].out) + (int64_t)r.g * p.rank * width;
-        if (r.problem) {  // dB: the rank runs along memory, and is a multiple of 8
+        if (!r.problem) {  // dB: the rank runs along memory, and is a multiple of 8
           out += col * p.rank + col0;
 #pragma unroll
           for (int i = 0; i < 64; i += 4)
@@ -1097,7 +1149,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
       if (mine.count * (k + 1) / o.cluster > mine.count * k / o.cluster) with |= 1u << k;
     if (with)
       for (int e = all / o.cluster * in_cluster + threadIdx.x; e < all / o.cluster * (in_cluster + 1); e += ROW_THREADS) {
-        const uint32_t at = f.smem + (mine.second ? (e / quads * (p.rp + 4) + e % quads * 4) * 4 : e * 16);
+        const uint32_t at = f.smem + (mine.second ? e * 16 : (e / quads * (p.rp + 4) + e % quads * 4) * 4);
         float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = with >> k & 1 ? ld_cluster_f4(mapa_rank(at, k)) : sum;
@@ -1106,6 +1158,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
         store_grad(p, o, mine, m_all, e, sum);
       }
   }
+  pdl_wait();
   // adapters without rows
   for (int g = blockIdx.x; g < p.n_adapters; g += gridDim.x) {
     if (o.first[g] != o.first[g + 1]) continue;
@@ -1122,16 +1175,10 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   finish(f, COLS);
 }
 
-// The output tiles that several CTAs share: four values to a thread.
 __global__ void __launch_bounds__(256) k_over_rows_sum(Args p, OverRows o) {
   pdl_launch_dependents();
   pdl_wait();
-  const int m_all = o.mtiles * 128, ctas = m_all * p.rp / 1024;
-  const Output r = output_at(p, o, blockIdx.x / ctas);
-  if (!r.count) return;
-  const int e = blockIdx.x % ctas * 256 + threadIdx.x;
-  const int c0 = cta_of(p.split, r.first), c1 = cta_of(p.split, r.first + r.count - 1);
-  if (c0 != c1) store_grad(p, o, r, m_all, e, sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e));
+  add_up_grads<256>(p, o, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1261,10 +1308,10 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 
 // out += held W; MN: w is [n_adapters][rank][width], else [n_adapters][width][rank]; held has `held_parts` parts
 template <bool MN, bool BF16>
-static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, bool early,
+static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, const OverRows* after,
                             cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
-  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, early ? 1 : 0};
+  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, after ? 1 : 0, after && !after->whole && after->split.ctas > 1 ? 1 : 0};
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
@@ -1300,15 +1347,15 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
                         : encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, o.nb));
   if (!maps || !allow_smem<k_from_rank<MN, BF16>>()) return DIT_ERR_CUDA;
   return launch_pdl(k_from_rank<MN, BF16>, dim3((unsigned)ctas), dim3(FROM_THREADS), SMEM_BYTES, st, 1, m_held, m_w, m_out, p,
-                    o) == cudaSuccess
+                    o, after ? *after : OverRows{}) == cudaSuccess
              ? DIT_OK
              : DIT_ERR_CUDA;
 }
 template <bool MN>
 static dit_status from_rank(const Args& p, const void* held, int held_parts, const void* w, void* out, dit_dtype dt,
-                            int64_t width, bool early, cudaStream_t st) {
-  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, early, st)
-                        : from_rank<MN, false>(p, held, held_parts, w, out, width, early, st);
+                            int64_t width, const OverRows* after, cudaStream_t st) {
+  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, after, st)
+                        : from_rank<MN, false>(p, held, held_parts, w, out, width, after, st);
 }
 
 }  // namespace lora
@@ -1333,7 +1380,7 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
   const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
   dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
-  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, false, st);
+  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, st);
   if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
   return s;
 }
@@ -1386,8 +1433,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
         o.mtiles = mt;
         o.whole = whole;
         o.cluster = cluster;
-        o.g[0] = Grad{da, k, bk};
-        o.g[1] = Grad{db, n, bn};
+        o.g[0] = Grad{db, n, bn};
+        o.g[1] = Grad{da, k, bk};
         p.split = s;
         p.split.ctas = (int)ctas;
       };
@@ -1400,8 +1447,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       }
     }
   }
-  const int64_t sum_ctas = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * (o.mtiles * 128 * p.rp / 1024);
-  if (sum_ctas > 0x7fffffff) return DIT_ERR_UNSUPPORTED;
+  int64_t sum_ctas = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * ((o.mtiles * 128 * p.rp / 4 + 511) / 512);
+  if (sum_ctas > 8 * num_sms()) sum_ctas = 8 * num_sms();
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
@@ -1415,8 +1462,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
     return DIT_ERR_CUDA;
   // dx after the gradients of the factors: dy, which the first product has just read, is still in L2 for them
   // where it fits.
-  if (dx) s = from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, true, st);
-  if (s != DIT_OK) return s;
+  o.split = p.split;
+  if (dx) return from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, &o, st);
   if (!o.whole && p.split.ctas > 1 &&
       launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
