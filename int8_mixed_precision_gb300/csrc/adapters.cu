@@ -85,30 +85,33 @@ __device__ __forceinline__ Frame frame(uint8_t* raw) {
 }
 __device__ __forceinline__ void start(const Frame& f, int stages, uint32_t cols, int epi_warps = EPI_WARPS) {
   Control* c = f.c;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(smem_u32(&c->full[s]), 1);
-      mbar_init(smem_u32(&c->empty[s]), 1);
+  if (threadIdx.x < 32) {  // some barriers to a lane: sixty in a row take half a microsecond
+    const int i = threadIdx.x;
+    if (i < stages) {
+      mbar_init(smem_u32(&c->full[i]), 1);
+      mbar_init(smem_u32(&c->empty[i]), 1);
     }
-    for (int b = 0; b < ACCS; ++b) {
-      mbar_init(smem_u32(&c->dfull[b]), 1);
-      mbar_init(smem_u32(&c->dempty[b]), epi_warps);
+    if (i < ACCS) {
+      mbar_init(smem_u32(&c->dfull[i]), 1);
+      mbar_init(smem_u32(&c->dempty[i]), epi_warps);
     }
-    for (int b = 0; b < MAX_PANELS; ++b) {
-      mbar_init(smem_u32(&c->yfull[b]), 1);
-      mbar_init(smem_u32(&c->ydone[b]), EPI_WARPS);
-      mbar_init(smem_u32(&c->yempty[b]), 1);
+    if (i < MAX_PANELS) {
+      mbar_init(smem_u32(&c->yfull[i]), 1);
+      mbar_init(smem_u32(&c->ydone[i]), epi_warps);
+      mbar_init(smem_u32(&c->yempty[i]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&c->hfull[b]), 1);
-      mbar_init(smem_u32(&c->hempty[b]), 1);
+    if (i < 2) {
+      mbar_init(smem_u32(&c->hfull[i]), 1);
+      mbar_init(smem_u32(&c->hempty[i]), 1);
     }
-    for (int b = 0; b < JOBS; ++b) {
-      mbar_init(smem_u32(&c->jfull[b]), 1);
-      mbar_init(smem_u32(&c->jempty[b]), 2 + epi_warps);  // the MMA, epilogue and store warps
+    if (i < JOBS) {
+      mbar_init(smem_u32(&c->jfull[i]), 1);
+      mbar_init(smem_u32(&c->jempty[i]), 2 + epi_warps);  // the MMA, epilogue and store warps
     }
-    mbar_init(smem_u32(&c->done), 1);
-    c->abort = 0;
+    if (i == 0) {
+      mbar_init(smem_u32(&c->done), 1);
+      c->abort = 0;
+    }
     fence_barrier_init();
   }
   if (threadIdx.x / 32 == 1) {
@@ -184,9 +187,9 @@ struct ToRank {
 };
 
 // Four columns of row r of tile ti of held, from their sums.
-__device__ __forceinline__ void store_held(const Args& p, const ToRank& o, const Tile& t, int64_t ti, int r, int col,
+__device__ __forceinline__ void store_held(const Args& p, const ToRank& o, const Tile& t, float scale, int64_t ti, int r, int col,
                                            const float4& sum) {
-  const float scale = o.scale[t.g], v[4] = {sum.x, sum.y, sum.z, sum.w};
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
   float part[4][PARTS];
 #pragma unroll
   for (int h = 0; h < 4; ++h) split_parts(r < t.rows && col + h < p.rank ? v[h] * scale : 0.f, part[h]);
@@ -381,10 +384,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (CLUSTER) {
     // Each CTA sums a share of the rows over the cluster's shared memories.
+    const int64_t ti = blockIdx.x / o.cluster;
+    const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);  // while the others come
+    const float scale = o.scale[t.g];
     __syncthreads();
     cluster_sync();
-    const int64_t ti = blockIdx.x / o.cluster;
-    const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
     const int quads = p.rp / 4, rows = TILE_ROWS / o.cluster;
     for (int e = threadIdx.x; e < rows * quads; e += THREADS) {
       const int r = in_cluster * rows + e / quads, col = e % quads * 4;
@@ -395,9 +399,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       float4 sum = v[0];
 #pragma unroll
       for (int k = 1; k < 8; ++k) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
-      store_held(p, o, t, ti, r, col, sum);
+      store_held(p, o, t, scale, ti, r, col, sum);
     }
-    cluster_sync();  // nobody still reads this CTA's shared memory
+    cluster_leave();  // nobody still reads this CTA's shared memory
   }
   finish(f, COLS);
 }
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(256) k_to_rank_sum(Args p, ToRank o) {
   const int c0 = cta_of(p.split, ti * o.blocks), c1 = cta_of(p.split, (ti + 1) * o.blocks - 1);
   if (c0 == c1) return;
   const Tile t = load_tile(p.table, ti, p.rows, p.n_adapters, p.ws);
-  store_held(p, o, t, ti, r, col, sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e));
+  store_held(p, o, t, o.scale[t.g], ti, r, col, sum_slots(o.slots, (int64_t)TILE_ROWS * p.rp, c0, c1, e));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1170,7 +1174,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
   }
   if (CLUSTER) {
     __syncwarp();
-    cluster_sync();  // nobody still reads this CTA's shared memory
+    cluster_leave();  // nobody still reads this CTA's shared memory
   }
   finish(f, COLS);
 }
