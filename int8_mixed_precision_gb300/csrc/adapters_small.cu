@@ -1,8 +1,8 @@
 // Low-rank adapters for short requests: y[t] += scale (x[t] A^T) B^T for tiles of up to 16 rows that
 // share an adapter, wherever in the batch they are (single tokens of a serving batch above all).
 //
-// Bound by latency (one token, 1920 -> 5760 at rank 16: 6.2 us a call; 64 tokens over 16 adapters, 1920 -> 7680 at
-// rank 32: 9.5 us, 1.3 TB/s), and then by reading each adapter's A and B once: 16 rows reuse a weight far too
+// Bound by latency (one token, 1920 -> 5760 at rank 16: 5.7 us a call; 64 tokens over 16 adapters, 1920 -> 7680 at
+// rank 32: 9.4 us, 1.3 TB/s), and then by reading each adapter's A and B once: 16 rows reuse a weight far too
 // little to fill a 128-row tcgen05 instruction, so the products run on mma.sync (16 x 8 x 16) with
 // both operands loaded from global memory straight into fragments; a product's contraction
 // index may be permuted freely, so every lane loads 16 (or 8) contiguous bytes and takes them for the
@@ -11,7 +11,7 @@
 // One launch: a cluster of CTAs takes a tile.  Each CTA contracts its share of k and leaves a partial h in
 // its shared memory; after one cluster barrier every CTA sums all of them (in the CTAs' order, so
 // all get the same bits) and takes its share of the n columns, whose weights and old values are
-// loaded 16 columns ahead, the first ones before the barrier.
+// loaded 16 or 32 columns of a warp ahead, the first ones before the barrier.
 #include "adapters.cuh"
 
 namespace dit6 {
@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
   const int row_lo = __shfl_sync(0xffffffffu, mine, g8), row_hi = __shfl_sync(0xffffffffu, mine, g8 + 8);
   const bool has_lo = g8 < count, has_hi = g8 + 8 < count;
 
+  const float scale = p.scale[g];
+
   // this CTA's share of the columns, in groups of 16
   const int64_t groups = (p.n + 15) / 16;
   const int64_t n_first = groups * rank_in / p.cluster * 16, n_last = min(p.n, groups * (rank_in + 1) / p.cluster * 16);
@@ -151,9 +153,12 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
   // loads (64 tokens over 16 adapters: 14.9 us a call, against 11.3).
   pdl_launch_dependents();
   // The first columns' weights and old values, while the partial sums meet.
-  Columns<RT, BF16> ahead;
+  constexpr int AHEAD = RT <= 8 ? 2 : 1;  // more costs registers and code: 64 tokens 9.4 us with two, 10.5 with four
+  constexpr int STRIDE = SMALL_WARPS * 16;
+  Columns<RT, BF16> ahead[AHEAD];
   int64_t n0 = n_first + warp * 16;
-  ahead.load(p, b, n0, n_last, row_lo, row_hi, has_lo, has_hi);
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) ahead[d].load(p, b, n0 + d * STRIDE, n_last, row_lo, row_hi, has_lo, has_hi);
 #pragma unroll
   for (int i = 0; i < RT; ++i)
     if (i < tiles8) {
@@ -174,7 +179,6 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
   } else {
     __syncthreads();
   }
-  const float scale = p.scale[g];
   for (int i = threadIdx.x; i < 16 * p.rp; i += SMALL_THREADS) {
     float v = 0.f;
     if (p.cluster > 1) {
@@ -197,38 +201,43 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
       v = isfinite(f) ? v - f : 0.f;
     }
   }
-  if (p.cluster > 1) cluster_arrive();  // this CTA has read the others' sums
+  if (p.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has read the others' sums
   __syncthreads();
 
   // ---- y: 16 columns to a warp at a time; a lane ends with four consecutive ones of two rows
-  for (; n0 < n_last; n0 += SMALL_WARPS * 16) {
-    const Columns<RT, BF16> now = ahead;
-    ahead.load(p, b, n0 + SMALL_WARPS * 16, n_last, row_lo, row_hi, has_lo, has_hi);
-    float d0[4] = {}, d1[4] = {};
+  while (n0 < n_last) {
 #pragma unroll
-    for (int j = 0; j < Columns<RT, BF16>::STEPS; ++j) {
-      const int k = j * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
-      if (j * 32 >= p.rp) break;
+    for (int d = 0; d < AHEAD; ++d) {
+      if (n0 >= n_last) break;
+      const Columns<RT, BF16> now = ahead[d];
+      ahead[d].load(p, b, n0 + AHEAD * STRIDE, n_last, row_lo, row_hi, has_lo, has_hi);
+      float d0[4] = {}, d1[4] = {};
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        if (q >= P) break;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (k < p.rp) {
-          lo = *reinterpret_cast<const uint4*>(h + (q * 16 + g8) * hp + k);
-          hi = *reinterpret_cast<const uint4*>(h + (q * 16 + g8 + 8) * hp + k);
+      for (int j = 0; j < Columns<RT, BF16>::STEPS; ++j) {
+        const int k = j * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
+        if (j * 32 >= p.rp) break;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          if (q >= P) break;
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (k < p.rp) {
+            lo = *reinterpret_cast<const uint4*>(h + (q * 16 + g8) * hp + k);
+            hi = *reinterpret_cast<const uint4*>(h + (q * 16 + g8 + 8) * hp + k);
+          }
+          const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+          mma_16816(d0, a0, now.w0[j].x, now.w0[j].y);
+          mma_16816(d1, a0, now.w1[j].x, now.w1[j].y);
+          mma_16816(d0, a1, now.w0[j].z, now.w0[j].w);
+          mma_16816(d1, a1, now.w1[j].z, now.w1[j].w);
         }
-        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-        mma_16816(d0, a0, now.w0[j].x, now.w0[j].y);
-        mma_16816(d1, a0, now.w1[j].x, now.w1[j].y);
-        mma_16816(d0, a1, now.w0[j].z, now.w0[j].w);
-        mma_16816(d1, a1, now.w1[j].z, now.w1[j].w);
       }
+      const int64_t col = n0 + c4 * 4;
+      if (has_lo && col < p.n) now.store(p, row_lo, col, now.was_lo, d0[0], d0[1], d1[0], d1[1]);
+      if (has_hi && col < p.n) now.store(p, row_hi, col, now.was_hi, d0[2], d0[3], d1[2], d1[3]);
+      n0 += STRIDE;
     }
-    const int64_t col = n0 + c4 * 4;
-    if (has_lo && col < p.n) now.store(p, row_lo, col, now.was_lo, d0[0], d0[1], d1[0], d1[1]);
-    if (has_hi && col < p.n) now.store(p, row_hi, col, now.was_hi, d0[2], d0[3], d1[2], d1[3]);
   }
-  if (p.cluster > 1) cluster_wait();  // nobody still reads this CTA's shared memory
+  if (p.cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // nobody still reads this CTA's shared memory
 }
 
 template <int RT, bool BF16>
