@@ -471,23 +471,40 @@ __device__ __forceinline__ void store_grad(const Args& p, const OverRows& o, con
   }
 }
 
-// Adds up the output tiles that several CTAs of k_over_rows share, four values to a thread at a time; this CTA is
-// number `cta` of `ctas`, with N threads.
-template <int N>
+// Adds up the output tiles that several CTAs of k_over_rows share, in the order of the CTAs; this CTA is number
+// `cta` of `ctas`, with N threads.  A thread has the loads of four CTAs' values at PLACES places in flight: where
+// few threads do it, behind k_from_rank, one place at a time took 10 us for one video's gradients.
+template <int N, int PLACES>
 __device__ __forceinline__ void add_up_grads(const Args& p, const OverRows& o, int cta, int ctas) {
-  const int m_all = o.mtiles * 128, quads = m_all * p.rp / 4, chunks = (quads + 2 * N - 1) / (2 * N);
-  const int64_t all = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * chunks;
+  const int m_all = o.mtiles * 128, quads = m_all * p.rp / 4, chunks = (quads + PLACES * N - 1) / (PLACES * N);
+  const int64_t slot = (int64_t)m_all * p.rp, all = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * chunks;
   for (int64_t c = cta; c < all; c += ctas) {
     const Output r = output_at(p, o, c / chunks);
     if (!r.count) continue;
     const int c0 = cta_of(o.split, r.first), c1 = cta_of(o.split, r.first + r.count - 1);
     if (c0 == c1) continue;
-    const int first = (int)(c % chunks) * 2 * N;
+    const int first = (int)(c % chunks) * PLACES * N + threadIdx.x;
+    float4 sum[PLACES];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = first + i * N + threadIdx.x;
-      if (e < quads) store_grad(p, o, r, m_all, e, sum_slots(o.slots, (int64_t)m_all * p.rp, c0, c1, e));
+    for (int i = 0; i < PLACES; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = c0; k <= c1; k += 4) {
+      float4 v[4][PLACES];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < PLACES; ++i)
+          v[h][i] = k + h <= c1 && first + i * N < quads
+                        ? __ldcg(reinterpret_cast<const float4*>(o.slots + slot_of(k + h, c0) * slot) + first + i * N)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < PLACES; ++i)
+          sum[i] = make_float4(sum[i].x + v[h][i].x, sum[i].y + v[h][i].y, sum[i].z + v[h][i].z, sum[i].w + v[h][i].w);
     }
+#pragma unroll
+    for (int i = 0; i < PLACES; ++i)
+      if (first + i * N < quads) store_grad(p, o, r, m_all, first + i * N, sum[i]);
   }
 }
 
@@ -823,7 +840,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
     if (lane == 0) tma_store_wait();
   }
   pdl_wait();
-  if (MN && o.sums) add_up_grads<FROM_THREADS>(p, rows, blockIdx.x, gridDim.x);
+  if (MN && o.sums) add_up_grads<FROM_THREADS, 4>(p, rows, blockIdx.x, gridDim.x);
   finish(f, COLS);
 }
 
@@ -1182,7 +1199,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
 __global__ void __launch_bounds__(256) k_over_rows_sum(Args p, OverRows o) {
   pdl_launch_dependents();
   pdl_wait();
-  add_up_grads<256>(p, o, blockIdx.x, gridDim.x);
+  add_up_grads<256, 1>(p, o, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1451,8 +1468,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       }
     }
   }
-  int64_t sum_ctas = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * ((o.mtiles * 128 * p.rp / 4 + 511) / 512);
-  if (sum_ctas > 8 * num_sms()) sum_ctas = 8 * num_sms();
+  const int64_t sum_chunks = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * (o.mtiles * 128 * p.rp / 1024);
+  const int64_t sum_ctas = sum_chunks < 65536 ? sum_chunks : 65536;
   CUtensorMap m_x, m_e, m_dy, m_h;
   const int64_t held_rows = (int64_t)p.n_tiles * TILE_ROWS;
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
