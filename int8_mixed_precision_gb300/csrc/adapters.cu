@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float scale = o.scale[t.g];
     __syncthreads();
     cluster_sync();
-    const int quads = p.rp / 4, rows = TILE_ROWS / o.cluster;
-    for (int e = threadIdx.x; e < rows * quads; e += THREADS) {
-      const int r = in_cluster * rows + e / quads, col = e % quads * 4;
+    const int quads = p.rp / 4, row0 = TILE_ROWS * in_cluster / o.cluster, row1 = TILE_ROWS * (in_cluster + 1) / o.cluster;
+    for (int e = threadIdx.x; e < (row1 - row0) * quads; e += THREADS) {
+      const int r = row0 + e / quads, col = e % quads * 4;
       const uint32_t at = f.smem + (r * (p.rp + 4) + col) * 4;
       float4 v[8];
 #pragma unroll
@@ -1169,7 +1169,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
     for (int k = 0; k < o.cluster; ++k)
       if (mine.count * (k + 1) / o.cluster > mine.count * k / o.cluster) with |= 1u << k;
     if (with)
-      for (int e = all / o.cluster * in_cluster + threadIdx.x; e < all / o.cluster * (in_cluster + 1); e += ROW_THREADS) {
+      for (int e = all * in_cluster / o.cluster + threadIdx.x; e < all * (in_cluster + 1) / o.cluster; e += ROW_THREADS) {
         const uint32_t at = f.smem + (mine.second ? e * 16 : (e / quads * (p.rp + 4) + e % quads * 4) * 4);
         float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1248,18 +1248,19 @@ struct RankSplit {
   Split split;
   int cluster;
 };
-// `clusters`: how many clusters of 2, 4 and 8 CTAs the device runs at a time
-static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const int (&clusters)[3]) {
+// `clusters`: how many clusters of 2 to 8 CTAs the device runs at a time
+static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const int (&clusters)[7]) {
   constexpr int64_t LEAST = 4;  // units of an equal share
   const int64_t sms = num_sms();
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
-  const double unit_ns = (double)unit_bytes / SM_BYTES_NS, bytes = (double)s.units * unit_bytes;
+  const double unit_ns = (double)unit_bytes / SM_BYTES_NS;
+  const double bytes = (double)s.units * (16384 + (unit_bytes - 16384) / 2.5);  // the weights come out of L2, faster
   const double whole = time_ns((double)((tiles + sms - 1) / sms * blocks) * unit_ns, bytes);
   const double shared = time_ns((double)s.units / s.ctas * unit_ns, bytes) + shared_ns(s.ctas);
   RankSplit best{whole <= shared ? split_units(s.units, blocks, blocks, (int)sms) : s, 1};
   double ns = whole <= shared ? whole : shared;
-  for (int i = 0; i < 3; ++i) {
-    const int c = 2 << i;
+  for (int i = 0; i < 7; ++i) {
+    const int c = 2 + i;
     const double t = time_ns((double)((blocks + c - 1) / c) * unit_ns, bytes) + CLUSTER_NS;
     if (tiles <= clusters[i] && blocks >= 2 * c && t < ns) {
       ns = t;
@@ -1269,17 +1270,17 @@ static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes
   return best;
 }
 template <auto KERN, int N_THREADS>
-static const int (&max_clusters())[3] {
+static const int (&max_clusters())[7] {
   struct Most {
-    int n[3];
+    int n[7];
     Most() {
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < 7; ++i) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2u << i;
+        attr[0].val.clusterDim.x = 2u + i;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_sms() / (2 << i) * (2 << i));
+        cfg.gridDim = dim3(num_sms() / (2 + i) * (2 + i));
         cfg.blockDim = dim3(N_THREADS);
         cfg.dynamicSmemBytes = SMEM_BYTES;
         cfg.attrs = attr;
@@ -1461,8 +1462,8 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       };
       take(cost[0], 0, 1, s.ctas);
       take(cost[1], 1, 1, outputs < s.ctas ? outputs : s.ctas);
-      for (int i = 0; i < 3; ++i) {
-        const int64_t c = 2 << i;
+      for (int i = 0; i < 7; ++i) {
+        const int64_t c = 2 + i;
         if (outputs <= clusters[i] && plan->most_tiles >= c)
           take(time_ns((double)((plan->most_tiles + c - 1) / c) * unit_ns, bytes) + CLUSTER_ROWS_NS, 1, (int)c, outputs * c);
       }
