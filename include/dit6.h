@@ -412,6 +412,8 @@ dit_status dit_shard_finish_host(const double* partials, int n_partials, const f
  * scale : device float [n_adapters].
  * da, db: device float, the shapes of a and b, overwritten (adapters without rows get zeros).
  *         dx may be NULL: the gradient of the input is then not computed.
+ *         dx may be dy itself (bf16, n == k), and y may be x: what is read is read before it
+ *         is updated.  No other buffers of a call may overlap.
  * rank  : 8 to 128, a multiple of 8; k % 8 == 0, n % 8 == 0, both up to 2^30; up to 2^20 adapters
  *         (else DIT_ERR_UNSUPPORTED).  32-byte aligned pointers.
  * saved : device buffer of dit_adapter_saved_bytes that the forward pass fills with h for the

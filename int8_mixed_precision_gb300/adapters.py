@@ -161,8 +161,8 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
 def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
     """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
     wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
-    adapter over all rows that use it.  saved: filled by lora_forward with the same plan, x, a
-    and scale."""
+    adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
+    lora_forward with the same plan, x, a and scale."""
     _agree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")

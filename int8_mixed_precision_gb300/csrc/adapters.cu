@@ -528,9 +528,9 @@ struct FromRank {
   int64_t jobs, tile_jobs;  // all, and of a tile
   int panels, helds; // of the rings
   // The kernel before it is k_over_rows, whose gradients are no business of this one: its jobs fill the SMs that
-  // are done there, without a wait for the others.
+  // are done there, without a wait for the others.  Not where out is what that kernel still reads.
   int early;
-  int sums;  // then, this kernel adds up what k_over_rows left in parts (no launch of its own for that)
+  int sums;  // behind k_over_rows: this kernel adds up what k_over_rows left in parts (no launch of its own for that)
 };
 // Where a job begins, and its blocks.
 struct Job {
@@ -1331,9 +1331,9 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 // out += held W; MN: w is [n_adapters][rank][width], else [n_adapters][width][rank]; held has `held_parts` parts
 template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, const OverRows* after,
-                            cudaStream_t st) {
+                            bool early, cudaStream_t st) {
   if (!p.n_tiles) return DIT_OK;
-  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, after ? 1 : 0, after && !after->whole && after->split.ctas > 1 ? 1 : 0};
+  FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, early ? 1 : 0, after && !after->whole && after->split.ctas > 1 ? 1 : 0};
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
@@ -1375,9 +1375,9 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
 }
 template <bool MN>
 static dit_status from_rank(const Args& p, const void* held, int held_parts, const void* w, void* out, dit_dtype dt,
-                            int64_t width, const OverRows* after, cudaStream_t st) {
-  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, after, st)
-                        : from_rank<MN, false>(p, held, held_parts, w, out, width, after, st);
+                            int64_t width, const OverRows* after, bool early, cudaStream_t st) {
+  return dt == DIT_BF16 ? from_rank<MN, true>(p, held, held_parts, w, out, width, after, early, st)
+                        : from_rank<MN, false>(p, held, held_parts, w, out, width, after, early, st);
 }
 
 }  // namespace lora
@@ -1402,7 +1402,7 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
   char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
   const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
   dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
-  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, st);
+  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, false, st);
   if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
   return s;
 }
@@ -1485,7 +1485,14 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   // dx after the gradients of the factors: dy, which the first product has just read, is still in L2 for them
   // where it fits.
   o.split = p.split;
-  if (dx) return from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, &o, st);
+  if (dx) {
+    // dx may be dy itself (a residual's gradient), or x: then k_over_rows has to be done with it first.
+    auto apart = [&](const void* in, int64_t width) {
+      const char *d = reinterpret_cast<const char*>(dx), *i = reinterpret_cast<const char*>(in);
+      return d + plan->rows * k * (dx_dt == DIT_BF16 ? 2 : 4) <= i || i + plan->rows * width * 2 <= d;
+    };
+    return from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, &o, apart(x, k) && apart(dy, n), st);
+  }
   if (!o.whole && p.split.ctas > 1 &&
       launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;

@@ -189,6 +189,29 @@ def test_nothing_to_do(training):
         assert torch.equal(s.d["y"].cpu(), c["y"])
 
 
+@pytest.mark.parametrize("shape", [([9000, 3000, 40, 77], [0, 1, -1, 1], 2, 64, 1920), ([300, 5, 64, 1], [0, 1, -1, 0], 2, 128, 264)],
+                         ids=["large", "small"])
+@pytest.mark.parametrize("training", [False, True])
+def test_y_may_be_x_and_dx_may_be_dy(shape, training):
+    lengths, adapters, G, r, k = shape
+    c = inputs(lengths, adapters, G, r, k, k, BF16, seed=12)
+    s = Setup(c, training)
+    s.d["y"].copy_(s.d["x"])
+    s.d["dx"].copy_(s.d["dy"])
+    y = s.forward().clone()
+    if training:
+        dx = s.backward().clone()
+        for _ in range(5):
+            t = Setup(c, True)
+            dit.lora_forward(t.plan, t.bank, t.d["x"], t.d["y"], t.scratch, t.ws, saved=t.saved)
+            dit.lora_backward(t.plan, t.bank, t.d["x"], t.d["dy"], t.saved, t.da, t.db, t.scratch, t.ws, dx=t.d["dy"])
+            assert torch.equal(t.d["dy"], dx) and torch.equal(t.da, s.da) and torch.equal(t.db, s.db)
+            t.ok()
+    dit.lora_forward(s.plan, s.bank, s.d["x"], s.d["x"], s.scratch, s.ws)
+    assert torch.equal(s.d["x"], y)
+    s.ok()
+
+
 def test_the_same_call_gives_the_same_bits():
     lengths, adapters = [700, 33, 1500, 260], [0, 1, 0, 2]
     c = inputs(lengths, adapters, 3, 48, 1032, 520, BF16, seed=6)
