@@ -38,7 +38,7 @@ namespace lora {
 
 constexpr int EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS;
 constexpr int THREADS = 64 + EPI_THREADS;
-constexpr int CHUNK = 512;                  // elements of a contraction between drains
+constexpr int CHUNK = 256;                  // elements of a contraction between drains
 constexpr int RING_BYTES = 220 * 1024;      // shared memory for operands
 constexpr int SMEM_BYTES = RING_BYTES + 1024 + 1024;
 constexpr int MAX_STAGES = 12;
@@ -712,11 +712,12 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
           fence_after();
           const uint32_t b0 = MN ? desc_mn(ring + s * w_bytes, box_bytes) : desc_k(ring + s * w_bytes);
           const uint32_t a0 = desc_k(f.smem + hs * h_bytes);
-          int k = 0;
-          for (int q = 0; q < steps; ++q) {  // every part meets the same weights
+          // Every part meets the same weights; the small parts first, while truncation takes little of the sum.
+          int k = rank_steps - 1;
+          for (int q = steps - 1; q >= 0; --q) {
             const uint32_t b = b0 + (MN ? k * (2048 >> 4) : (k / 4) * (box_bytes >> 4) + (k % 4) * (32 >> 4));
-            mma(tmem + buf * 128, a0 + (q / 4) * (16384 >> 4) + (q % 4) * (32 >> 4), b, id, q > 0);
-            if (++k == rank_steps) k = 0;
+            mma(tmem + buf * 128, a0 + (q / 4) * (16384 >> 4) + (q % 4) * (32 >> 4), b, id, q < steps - 1);
+            if (--k < 0) k = rank_steps - 1;
           }
           mma_commit(smem_u32(&c->empty[s]));
           mma_commit(smem_u32(&c->dfull[buf]));
