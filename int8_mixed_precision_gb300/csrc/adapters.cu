@@ -7,13 +7,14 @@
 // operand once through shared memory by TMA and runs on tcgen05 with everything of the rank's
 // size on chip.  Three kernels of one CTA per SM, and two short ones that add up partial results:
 //
-//   k_to_rank    h, e: units are (128 rows, 64 columns of x or dy).  35552 x 1920 at rank 64: 28 us, 4.9 TB/s
-//                of x; 17776 x 7680: 50 us, 5.5 TB/s.  What keeps it below the copy rate is the weights'
+//   k_to_rank    h, e: units are (128 rows, 64 columns of x or dy).  35552 x 1920 at rank 64: 31 us, 4.4 TB/s
+//                of x; 17776 x 7680: 51 us, 5.4 TB/s.  What keeps it below the copy rate is the weights'
 //                way from L2 (half as many bytes again at rank 64).
 //   k_from_rank  y, dx: jobs are (128 rows, a few blocks of 128 columns), read, added to and written once.
-//                35552 x 7680 in bf16 at rank 64: 165 us, 6.6 TB/s, 0.97 of the copy rate.
+//                35552 x 7680 in bf16 at rank 64: 168 us, 6.5 TB/s, 0.96 of the copy rate.
 //   k_over_rows  dA, dB: units are (128 to 512 columns, 128 rows), both gradients in one launch.  17776 rows of
-//                7680 + 1920 columns at rank 64: 68 us, 5.0 TB/s of x and dy (tensor pipe 41 %).
+//                7680 + 1920 columns at rank 64: 81 us, 4.2 TB/s of x and dy, on 114 SMs, while the other 38
+//                begin with dx (on all SMs 69 us, but with 20 MB of partial results to add up).
 //
 // Weights are read as they lie: A [rank x k] and B [n x rank] serve both the product along their
 // rows (K-major operand) and the one across them (MN-major operand), so no transposed copies are kept.
@@ -25,8 +26,8 @@
 // Ahead of the stream.  Each kernel lets the next one launch only after its own wait for the one before, so a kernel
 // that has started finds everything but its immediate predecessor complete, and waits for that one
 // where it first reads what it made (h and e) or writes what it reads: k_from_rank's first weights and
-// old values and k_over_rows' units of dB come in before.  Every kernel waits before it ends, so the
-// stream's order holds for whatever follows.
+// old values and k_over_rows' units of dB come in before, and dx, which needs nothing of k_over_rows, is
+// updated beside it.  Every kernel waits before it ends, so the stream's order holds for whatever follows.
 //
 // Warps: 0 loads (TMA), 1 issues the MMAs, the others drain and store.  Every wait is bounded.  Loads and MMAs
 // are issued by an elected lane of a converged warp, from values that the warp shares: otherwise the
@@ -1235,9 +1236,9 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
 // What the cuts of the work are chosen by: a CTA's own time for its largest share at an SM's rate, or
 // all CTAs' at the device's, whichever is longer; shared outputs add a kernel that sums them, which
 // takes longer the more CTAs have shared.
-// (Products of 4160 and 12000 rows of 1920 columns at rank 32 took 26.1 and 43.2 us a forward call with
-// equal shares and 22.8 and 36.8 with whole tiles, though those keep only 33 and 94 SMs busy;
-// at 130 rows it is 13.5 against 15.7.)
+// (12000 rows of 1920 columns at rank 32 took 43.2 us a forward call with equal shares and 36.8 with whole
+// tiles, though those keep only 94 SMs busy; 4160 rows 26.1, 22.8, and 19.0 in clusters of four;
+// 130 rows 13.5, 15.7, and 9.6 in clusters of eight.)
 constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500;
 constexpr double CLUSTER_NS = 2000, CLUSTER_ROWS_NS = 7000;  // what a cluster takes to sum h or e, or a gradient
 static double shared_ns(int ctas) { return 3700 + 12.0 * ctas; }
