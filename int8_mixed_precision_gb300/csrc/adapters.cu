@@ -1236,11 +1236,11 @@ static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t ro
 // What the cuts of the work are chosen by: a CTA's own time for its largest share at an SM's rate, or
 // all CTAs' at the device's, whichever is longer; shared outputs add a kernel that sums them, which
 // takes longer the more CTAs have shared.
-// (12000 rows of 1920 columns at rank 32 took 43.2 us a forward call with equal shares and 36.8 with whole
-// tiles, though those keep only 94 SMs busy; 4160 rows 26.1, 22.8, and 19.0 in clusters of four;
-// 130 rows 13.5, 15.7, and 9.6 in clusters of eight.)
+// (12000 rows of 1920 columns at rank 32 took 6 us less a forward call with whole tiles than with equal shares,
+// though those keep only 94 SMs busy; 4160 rows 3 us less, and 4 less again in clusters of four; 130 rows
+// take 13.5 us in equal shares, 15.7 whole, and 9.6 in clusters of eight.)
 constexpr double SM_BYTES_NS = 90, DEVICE_BYTES_NS = 6500;
-constexpr double CLUSTER_NS = 2000, CLUSTER_ROWS_NS = 7000;  // what a cluster takes to sum h or e, or a gradient
+constexpr double CLUSTER_NS = 2000, CLUSTER_ROWS_NS = 3000;  // what a cluster takes to sum h or e, or a gradient
 static double shared_ns(int ctas) { return 3700 + 12.0 * ctas; }
 static double time_ns(double share_ns, double bytes) {
   const double all = bytes / DEVICE_BYTES_NS;
