@@ -1352,9 +1352,12 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
   o.n_blocks = (int)((width + o.nb - 1) / o.nb);
   // Jobs of up to eight blocks, sixteen jobs to an SM where there are that many blocks; but enough blocks to a
   // job that its tile of held (read again for each job) stays behind what it updates, as long as
-  // every SM has two jobs.  (17776 x 1920 in fp32 at rank 128: 90 us with one block, 79 with four.)
+  // every SM has two jobs.  (17776 x 1920 in fp32 at rank 128: 90 us with one block, 79 with four.)  At least two
+  // blocks even where the tile of held is small, since a job's number is a round trip to memory
+  // (12000 x 1920 in bf16 at rank 32, forward: 37.4 us with one block, 34.1 with two, 35.4 with three).
   const int64_t blocks = (int64_t)p.n_tiles * o.n_blocks, even = blocks / (16 * num_sms()), two = blocks / (2 * num_sms());
   int64_t per_job = 1 + h_bytes / (o.nb * TILE_ROWS * (BF16 ? 2 : 4));
+  if (per_job < 2) per_job = 2;
   if (per_job > two) per_job = two;
   if (per_job < even) per_job = even;
   o.per_job = per_job < 1 ? 1 : per_job > 8 ? 8 : (int)per_job;
