@@ -747,6 +747,7 @@ __global__ void __launch_bounds__(FROM_THREADS, 1)
         }
         fence_after();
         for (int i = 0; i < all; ++i) {
+          __syncwarp();  // lane 0 is back from its arrival: the loads want all lanes
           constexpr int MINE = PC / 2;  // this thread's columns of the panel
           uint32_t r[MINE];
           const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 128 + i * PC + half * MINE;
@@ -1192,7 +1193,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1)
     }
   }
   if (CLUSTER) {
-    __syncwarp();
     cluster_leave();  // nobody still reads this CTA's shared memory
   }
   finish(f, COLS);

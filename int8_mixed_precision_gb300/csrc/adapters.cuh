@@ -189,8 +189,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// The cluster's CTAs meet without ordering what they wrote (only its lifetime is at stake).
+// The cluster's CTAs meet without ordering what they wrote (only its lifetime is at stake).  The barrier wants
+// converged warps, and lanes leave the loops before it after different numbers of rounds.
 __device__ __forceinline__ void cluster_leave() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {

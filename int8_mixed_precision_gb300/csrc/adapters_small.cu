@@ -41,8 +41,19 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();  // the barriers want converged warps
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the same about the lifetime of what other CTAs read alone
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 
 // What a lane loads for 16 columns of the result: its share of their weights and its four old values of two
 // rows.  Tile t of the two has the columns n0 + 4 (s / 2) + 2 t + s % 2 in its slots s, so that a
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
       v = isfinite(f) ? v - f : 0.f;
     }
   }
-  if (p.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has read the others' sums
+  if (p.cluster > 1) cluster_arrive_relaxed();  // this CTA has read the others' sums
   __syncthreads();
 
   // ---- y: 16 columns to a warp at a time; a lane ends with four consecutive ones of two rows
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
       n0 += STRIDE;
     }
   }
-  if (p.cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // nobody still reads this CTA's shared memory
+  if (p.cluster > 1) cluster_wait();  // nobody still reads this CTA's shared memory
 }
 
 template <int RT, bool BF16>
