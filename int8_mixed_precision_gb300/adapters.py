@@ -7,6 +7,7 @@ only: the arithmetic runs in the kernels behind ``include/dit6.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -211,7 +212,8 @@ class AdaptedLinear:
     def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
         """dx = dy W + the adapters' part; da, db the adapters' gradients."""
         if self.w_t is None:
-            dx.zero_()
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                dx.zero_()
         else:
             gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
         lora_backward(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx=dx, stream=stream)

@@ -1,0 +1,122 @@
+"""AdaptedLinear and the calls beside it on the host: what runs on which stream, and what is refused before anything
+is launched.  The tensors are stand-ins that claim to be on a CUDA device; the launches are recorded."""
+import contextlib
+import os
+import types
+
+import pytest
+import torch
+
+import int8_mixed_precision_gb300 as dit
+from int8_mixed_precision_gb300 import adapters
+
+BF16, F32 = torch.bfloat16, torch.float32
+BYTES = {BF16: 2, F32: 4, torch.uint8: 1, torch.int32: 4}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from int8_mixed_precision_gb300 import _lib, build
+    if not os.path.exists(_lib.library_path()):
+        try:
+            build.build_library()
+        except RuntimeError as e:          # no nvcc on this machine
+            pytest.skip(str(e))
+
+
+class Buffer:
+    """A contiguous tensor of CUDA device `index` at an address, as the binding sees one."""
+    is_cuda = True
+
+    def __init__(self, address, shape, dtype=BF16, index=0, log=None):
+        self.address, self.shape, self.dtype, self.index, self.log = address, torch.Size(shape), dtype, index, log
+        self.device = torch.device("cuda", index)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    @property
+    def nbytes(self):
+        return self.numel() * BYTES[self.dtype]
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return self.address
+
+    def zero_(self):
+        self.log.append(("zero", torch.cuda.current_stream()))
+
+
+class Library:
+    """The real sizes and names; launches are recorded with the stream they went to."""
+
+    def __init__(self, real, log):
+        self.real, self.log = real, log
+
+    def __getattr__(self, name):
+        if name not in ("dit_lora_forward", "dit_lora_backward"):
+            return getattr(self.real, name)
+        return lambda *args: self.log.append((name, args[-1])) or 0
+
+
+class Scene:
+    T, G, R, K, N = 40, 2, 16, 64, 64
+
+    def __init__(self, monkeypatch, training=True, index=0):
+        self.log = log = []
+        real = adapters.lib()
+        monkeypatch.setattr(adapters, "lib", lambda: Library(real, log))
+        self.current = 0x10
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: self.current, raising=False)
+
+        @contextlib.contextmanager
+        def stream(s):
+            was, self.current = self.current, s.cuda_stream
+            yield
+            self.current = was
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        T, G, R, K, N = self.T, self.G, self.R, self.K, self.N
+        at = iter(range(1 << 20, 1 << 30, 1 << 20))
+        new = lambda *shape, dtype=BF16: Buffer(next(at), shape, dtype, index, log)  # noqa: E731
+        self.bank = dit.AdapterBank(new(G, R, K), new(G, N, R), new(G, dtype=F32))
+        self.plan = dit.AdapterPlan([T], [0], G, training=training, device="cpu")
+        self.plan._index = index
+        self.x, self.y, self.dy, self.dx = new(T, K), new(T, N, dtype=F32), new(T, N), new(T, K, dtype=F32)
+        self.da, self.db = new(G, R, K, dtype=F32), new(G, N, R, dtype=F32)
+        size = lambda f: int(f)  # noqa: E731
+        scratch = real.dit_adapter_scratch_bytes(self.plan._info_p, R, K, N)
+        saved = real.dit_adapter_saved_bytes(self.plan._info_p, R)
+        self.scratch, self.saved = new(size(scratch), dtype=torch.uint8), new(size(saved), dtype=torch.uint8)
+        self.ws = new(dit.workspace_bytes(), dtype=torch.uint8)
+        self.new = new
+
+        def linear(x, route, y, bias=None, stream=None):
+            log.append(("projection", stream))
+        linear.w, linear.ws = types.SimpleNamespace(k=K, n=N), self.ws
+        self.layer = dit.AdaptedLinear(linear, self.bank)
+
+    def forward(self, **kw):
+        return self.layer(**{**dict(x=self.x, route=dit.ROUTE_INT8, y=self.y, plan=self.plan, scratch=self.scratch), **kw})
+
+    def backward(self, **kw):
+        return self.layer.backward(**{**dict(x=self.x, dy=self.dy, plan=self.plan, saved=self.saved, da=self.da, db=self.db,
+                                             dx=self.dx, scratch=self.scratch), **kw})
+
+
+def test_the_input_gradient_is_cleared_on_the_stream_of_the_call(monkeypatch):
+    s = Scene(monkeypatch)
+    s.backward(stream=types.SimpleNamespace(cuda_stream=0x77))
+    assert s.log == [("zero", 0x77), ("dit_lora_backward", 0x77)]
+    del s.log[:]
+    s.backward()
+    assert s.log == [("zero", 0x10), ("dit_lora_backward", 0x10)]
