@@ -186,6 +186,15 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
         _check(st, "dit_lora_backward")
 
 
+def _apart(out, out_name, *inputs):
+    """Refuses an output over an input that is read after the output is first written."""
+    o0 = out.data_ptr()
+    for t, name in inputs:
+        i0 = t.data_ptr()
+        if o0 < i0 + t.nbytes and i0 < o0 + out.nbytes:
+            raise DitError(f"AdaptedLinear: {out_name} overlaps {name}, which the adapters read after {out_name} is written")
+
+
 class AdaptedLinear:
     """A routed quantised projection with low-rank adapters beside it.
 
@@ -202,15 +211,17 @@ class AdaptedLinear:
 
     def __call__(self, x, route, y, plan, scratch, saved=None, bias=None, act=ACT_NONE, stream=None):
         """y = x W^T (+ bias) along `route`, plus the adapters.  The adapters add to the projection
-        itself, so an activation cannot be fused into it."""
+        itself, so an activation cannot be fused into it.  y shares no memory with x."""
         if act != ACT_NONE:
             raise DitError("AdaptedLinear: the activation follows the adapters and cannot be fused into the projection")
+        _apart(y, "y", (x, "x"))
         self.linear(x, route, y, bias=bias, stream=stream)
         lora_forward(plan, self.bank, x, y, scratch, self.linear.ws, saved=saved, stream=stream)
         return y
 
     def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
-        """dx = dy W + the adapters' part; da, db the adapters' gradients."""
+        """dx = dy W + the adapters' part; da, db the adapters' gradients.  dx shares no memory with dy or x."""
+        _apart(dx, "dx", (dy, "dy"), (x, "x"))
         if self.w_t is None:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 dx.zero_()

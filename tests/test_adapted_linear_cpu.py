@@ -120,3 +120,20 @@ def test_the_input_gradient_is_cleared_on_the_stream_of_the_call(monkeypatch):
     del s.log[:]
     s.backward()
     assert s.log == [("zero", 0x10), ("dit_lora_backward", 0x10)]
+
+
+def test_outputs_over_inputs_are_refused_before_anything_is_written(monkeypatch):
+    """The projection (or the zeros) would be written over x or dy before the adapters read them, so what the calls
+    themselves allow (y over x, dx over dy) is no option beside a projection."""
+    s = Scene(monkeypatch)
+    behind = lambda t, n: Buffer(t.address + n, t.shape, t.dtype, 0, s.log)  # noqa: E731
+    over = lambda t: Buffer(t.address, t.shape, BF16, 0, s.log)  # noqa: E731
+    for y in (over(s.x), behind(s.x, 64), behind(s.x, s.x.nbytes - 32), behind(s.x, -32)):
+        with pytest.raises(dit.DitError, match="y overlaps x"):
+            s.forward(y=y)
+    for kw, what in ((dict(dx=over(s.dy)), "dy"), (dict(dx=over(s.x)), "x"), (dict(dx=behind(s.dy, 32)), "dy")):
+        with pytest.raises(dit.DitError, match=f"dx overlaps {what}"):
+            s.backward(**kw)
+    assert not s.log
+    s.forward(y=behind(over(s.x), s.x.nbytes))           # next to it is fine
+    assert [e[0] for e in s.log] == ["projection", "dit_lora_forward"]
