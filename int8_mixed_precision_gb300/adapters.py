@@ -138,10 +138,8 @@ def _agree(plan, bank):
         raise DitError(f"the plan is on {plan.table.device}, the bank on {bank.device}")
 
 
-def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=None, stream=None):
-    """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
-    the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
-    lora_backward needs."""
+def _forward_args(plan, bank, x, y, scratch, ws, saved):
+    """The checked arguments of dit_lora_forward, but for the stream."""
     _agree(plan, bank)
     i, rows = bank._index, plan.rows
     xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
@@ -152,18 +150,12 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
         vp, vn = _bytes_of(saved, "saved", i), saved.nbytes
     else:
         raise DitError("saved needs AdapterPlan(..., training=True)")
-    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn,
-                                _bytes_of(scratch, "scratch", i), scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes,
-                                raw_stream(stream, i))
-    if st:
-        _check(st, "dit_lora_forward")
+    return (plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn, _bytes_of(scratch, "scratch", i),
+            scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes)
 
 
-def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
-    """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
-    wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
-    adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
-    lora_forward with the same plan, x, a and scale."""
+def _backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx):
+    """The checked arguments of dit_lora_backward, but for the stream."""
     _agree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")
@@ -178,12 +170,51 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
         raise DitError(f"da: float32 {tuple(bank.a.shape)} is needed")
     if db.dtype != _F32 or db.shape != bank.b.shape:
         raise DitError(f"db: float32 {tuple(bank.b.shape)} is needed")
-    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, *bank._args, _bytes_of(saved, "saved", i),
-                                 saved.nbytes, dxp, dx_code, _bytes_of(da, "da", i), _bytes_of(db, "db", i),
-                                 _bytes_of(scratch, "scratch", i), scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes,
-                                 raw_stream(stream, i))
+    return (plan._info_p, plan._table_p, xp, dyp, *bank._args, _bytes_of(saved, "saved", i), saved.nbytes, dxp, dx_code,
+            _bytes_of(da, "da", i), _bytes_of(db, "db", i), _bytes_of(scratch, "scratch", i), scratch.nbytes,
+            _bytes_of(ws, "ws", i), ws.nbytes)
+
+
+def _forward(args, stream, index):
+    st = lib().dit_lora_forward(*args, raw_stream(stream, index))
+    if st:
+        _check(st, "dit_lora_forward")
+
+
+def _backward(args, stream, index):
+    st = lib().dit_lora_backward(*args, raw_stream(stream, index))
     if st:
         _check(st, "dit_lora_backward")
+
+
+def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=None, stream=None):
+    """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
+    the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
+    lora_backward needs."""
+    _forward(_forward_args(plan, bank, x, y, scratch, ws, saved), stream, bank._index)
+
+
+def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
+    """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
+    wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
+    adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
+    lora_forward with the same plan, x, a and scale."""
+    _backward(_backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx), stream, bank._index)
+
+
+def _launchable(plan, bank, scratch, ws, saved, *tensors):
+    """What the library itself refuses, for callers that launch something before its call."""
+    sizes = [(scratch, "scratch", lib().dit_adapter_scratch_bytes(plan._info_p, bank.rank, bank.k, bank.n)),
+             (ws, "ws", lib().dit_workspace_bytes())]
+    if saved is not None:
+        sizes.append((saved, "saved", lib().dit_adapter_saved_bytes(plan._info_p, bank.rank)))
+        if plan.n_tiles and saved.data_ptr() == scratch.data_ptr():
+            raise DitError("AdaptedLinear: saved is scratch")
+    for t, name, need in sizes:
+        if t.nbytes < need:
+            raise DitError(f"AdaptedLinear: {name} of {t.nbytes} bytes, {need} are needed")
+    if any(t.data_ptr() % 32 for t in (bank.a, bank.b, *(s[0] for s in sizes), *tensors)):
+        raise DitError(f"AdaptedLinear: {lib().dit_status_str(2).decode()}")
 
 
 def _apart(out, out_name, *inputs):
@@ -214,18 +245,22 @@ class AdaptedLinear:
         itself, so an activation cannot be fused into it.  y shares no memory with x."""
         if act != ACT_NONE:
             raise DitError("AdaptedLinear: the activation follows the adapters and cannot be fused into the projection")
+        args = _forward_args(plan, self.bank, x, y, scratch, self.linear.ws, saved)
+        _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, y)
         _apart(y, "y", (x, "x"))
         self.linear(x, route, y, bias=bias, stream=stream)
-        lora_forward(plan, self.bank, x, y, scratch, self.linear.ws, saved=saved, stream=stream)
+        _forward(args, stream, self.bank._index)
         return y
 
     def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
         """dx = dy W + the adapters' part; da, db the adapters' gradients.  dx shares no memory with dy or x."""
+        args = _backward_args(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx)
+        _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, dy, dx, da, db)
         _apart(dx, "dx", (dy, "dy"), (x, "x"))
         if self.w_t is None:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 dx.zero_()
         else:
             gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
-        lora_backward(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx=dx, stream=stream)
+        _backward(args, stream, self.bank._index)
         return dx

@@ -137,3 +137,33 @@ def test_outputs_over_inputs_are_refused_before_anything_is_written(monkeypatch)
     assert not s.log
     s.forward(y=behind(over(s.x), s.x.nbytes))           # next to it is fine
     assert [e[0] for e in s.log] == ["projection", "dit_lora_forward"]
+
+
+def test_what_the_adapters_refuse_is_refused_before_the_projection_writes(monkeypatch):
+    """Types, shapes, sizes, alignment and plans that the adapters' calls refuse, in either of their layers: y and dx
+    are still what they were."""
+    s = Scene(monkeypatch)
+    serving = dit.AdapterPlan([s.T], [0], s.G, device="cpu")
+    serving._index = 0
+    other = dit.AdapterPlan([s.T], [0], 3, device="cpu")
+    longer = dit.AdapterPlan([s.T + 1], [0], s.G, training=True, device="cpu")
+    longer._index = 0
+    odd = lambda t: Buffer(t.address + 16, t.shape, t.dtype, 0, s.log)  # noqa: E731
+    small = lambda t: s.new(t.nbytes - 256, dtype=torch.uint8)  # noqa: E731
+    shared = (dict(plan=other), dict(plan=longer), dict(scratch=small(s.scratch)), dict(scratch=odd(s.scratch)),
+              dict(x=s.new(s.T, s.K, dtype=F32)), dict(x=s.new(s.T - 1, s.K)), dict(x=odd(s.x)), dict(saved=small(s.saved)),
+              dict(saved=odd(s.saved)), dict(saved=s.scratch))
+    for kw in (*shared, dict(y=s.new(s.T, s.N + 8)), dict(y=odd(s.y)), dict(plan=serving, saved=s.saved)):
+        with pytest.raises(dit.DitError):
+            s.forward(**{"saved": s.saved, **kw})
+        assert not s.log, kw
+    for kw in (*shared, dict(plan=serving), dict(dx=s.new(s.T, s.K + 8)), dict(dx=odd(s.dx)), dict(dy=s.new(s.T, s.N, dtype=F32)),
+               dict(dy=odd(s.dy)), dict(da=s.db), dict(da=odd(s.da)), dict(db=odd(s.db)), dict(db=s.new(s.G, s.N, s.R))):
+        with pytest.raises(dit.DitError):
+            s.backward(**kw)
+        assert not s.log, kw
+    s.layer.linear.ws = s.new(64, dtype=torch.uint8)
+    for call in (s.forward, s.backward):
+        with pytest.raises(dit.DitError):
+            call()
+    assert not s.log
