@@ -23,7 +23,13 @@ _JUST_BF16 = (_BF16,)
 
 def raw_stream(stream, index: int) -> int:
     """The handle of `stream`, or of device `index`'s current stream (without making a Stream object,
-    which costs more than the checks and the launch of a short call together)."""
+    which costs more than the checks and the launch of a short call together).  The library launches on
+    the current device, so both have to be on it."""
+    current = torch.cuda.current_device()
+    if stream is not None and getattr(stream, "device_index", index) != index:
+        raise DitError(f"the buffers are on cuda:{index}, the stream is on cuda:{stream.device_index}")
+    if current != index:
+        raise DitError(f"the buffers are on cuda:{index}, the current device is cuda:{current}")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
@@ -175,14 +181,14 @@ def _backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx):
             _bytes_of(ws, "ws", i), ws.nbytes)
 
 
-def _forward(args, stream, index):
-    st = lib().dit_lora_forward(*args, raw_stream(stream, index))
+def _forward(args, raw):
+    st = lib().dit_lora_forward(*args, raw)
     if st:
         _check(st, "dit_lora_forward")
 
 
-def _backward(args, stream, index):
-    st = lib().dit_lora_backward(*args, raw_stream(stream, index))
+def _backward(args, raw):
+    st = lib().dit_lora_backward(*args, raw)
     if st:
         _check(st, "dit_lora_backward")
 
@@ -191,7 +197,7 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
     the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
     lora_backward needs."""
-    _forward(_forward_args(plan, bank, x, y, scratch, ws, saved), stream, bank._index)
+    _forward(_forward_args(plan, bank, x, y, scratch, ws, saved), raw_stream(stream, bank._index))
 
 
 def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
@@ -199,7 +205,7 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
     wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
     adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
     lora_forward with the same plan, x, a and scale."""
-    _backward(_backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx), stream, bank._index)
+    _backward(_backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx), raw_stream(stream, bank._index))
 
 
 def _launchable(plan, bank, scratch, ws, saved, *tensors):
@@ -248,8 +254,9 @@ class AdaptedLinear:
         args = _forward_args(plan, self.bank, x, y, scratch, self.linear.ws, saved)
         _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, y)
         _apart(y, "y", (x, "x"))
+        raw = raw_stream(stream, self.bank._index)
         self.linear(x, route, y, bias=bias, stream=stream)
-        _forward(args, stream, self.bank._index)
+        _forward(args, raw)
         return y
 
     def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
@@ -257,10 +264,11 @@ class AdaptedLinear:
         args = _backward_args(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx)
         _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, dy, dx, da, db)
         _apart(dx, "dx", (dy, "dy"), (x, "x"))
+        raw = raw_stream(stream, self.bank._index)
         if self.w_t is None:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 dx.zero_()
         else:
             gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
-        _backward(args, stream, self.bank._index)
+        _backward(args, raw)
         return dx

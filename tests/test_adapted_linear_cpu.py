@@ -167,3 +167,30 @@ def test_what_the_adapters_refuse_is_refused_before_the_projection_writes(monkey
         with pytest.raises(dit.DitError):
             call()
     assert not s.log
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_a_call_for_another_device_than_the_current_one_is_refused(monkeypatch, index):
+    """The library launches on the current device: with buffers of another one it would hand it foreign pointers."""
+    from int8_mixed_precision_gb300 import optim
+    s = Scene(monkeypatch, index=index)
+    stream = types.SimpleNamespace(cuda_stream=0x77, device_index=1 - index)
+    opt = object.__new__(optim.AdamW)
+    opt._index, opt._lists, opt._head, opt._tail = index, {"m_values": []}, (), ()
+    calls = (lambda **kw: dit.lora_forward(s.plan, s.bank, s.x, s.y, s.scratch, s.ws, **kw),
+             lambda **kw: dit.lora_backward(s.plan, s.bank, s.x, s.dy, s.saved, s.da, s.db, s.scratch, s.ws, **kw),
+             s.forward, s.backward, lambda **kw: adapters.raw_stream(kw.get("stream"), index))
+    if index:
+        calls += (lambda **kw: opt.export_moments(**kw),)
+    for call in calls:
+        with pytest.raises(dit.DitError, match="stream is on cuda"):
+            call(stream=stream)
+        if index == 0:
+            call()
+            assert s.log or call is calls[-1]
+        else:
+            for kw in ({}, dict(stream=types.SimpleNamespace(cuda_stream=0x77, device_index=1))):
+                with pytest.raises(dit.DitError, match="current device is cuda:0"):
+                    call(**kw)
+            assert not s.log
+        del s.log[:]
