@@ -26,7 +26,8 @@
  * - Tensors are row-major and contiguous.  Activation and delta tensors are bf16 or fp32
  *   (dit_dtype).  Device pointers must be 32-byte aligned (256-bit vector loads).
  * - All entry points are thread-compatible.  The library's only global mutable state is a
- *   cached driver entry point, per-device caches of the SM count, and the fixed scratch
+ *   cached driver entry point, per-device caches of the SM count and of what was asked or set
+ *   for a kernel (its shared-memory limit, how many clusters run at a time), and the fixed scratch
  *   array of dit_gamma_route_noalloc (with its per-device address cache); calls of that entry
  *   point share the array and race when they overlap on the GPU (see its comment).
  */

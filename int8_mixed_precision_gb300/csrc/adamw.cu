@@ -478,8 +478,8 @@ static cudaError_t launch(bool codes, const dit_adamw_tensor* descs, int64_t n_t
     return launch_pdl(k_adamw<P, G>, dim3((unsigned)n_chunks), dim3(THREADS), 0, st, 1, descs, n_tensors, chunks, n_chunks, f,
                       gs, ws);
   constexpr int SMEM = sizeof(Stage<P, G>) * DEPTH * BLOCKS * WARPS;
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(k_adamw_codes<P, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  static OncePerDevice once;
+  const cudaError_t allowed = opt_in_smem(once, k_adamw_codes<P, G>, SMEM);
   if (allowed != cudaSuccess) return allowed;
   return launch_pdl(k_adamw_codes<P, G>, dim3(few(n_chunks, 2)), dim3(THREADS), SMEM, st, 1, descs, n_tensors, chunks, n_chunks,
                     f, gs, ws);

@@ -1225,8 +1225,8 @@ static int stages_for(uint32_t room, uint32_t stage_bytes) {
 }
 template <auto KERN>
 static bool allow_smem() {
-  static const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  return e == cudaSuccess;
+  static OncePerDevice once;
+  return opt_in_smem(once, KERN, SMEM_BYTES) == cudaSuccess;
 }
 static bool map_rows(CUtensorMap* m, const void* base, int64_t width, int64_t rows, uint32_t box_rows) {
   return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void*>(base), (uint64_t)width, (uint64_t)rows,
@@ -1246,12 +1246,15 @@ static double time_ns(double share_ns, double bytes) {
   const double all = bytes / DEVICE_BYTES_NS;
   return share_ns > all ? share_ns : all;
 }
+// how many clusters of 2 to 8 CTAs the device runs at a time
+struct Clusters {
+  int most[7];
+};
 struct RankSplit {
   Split split;
   int cluster;
 };
-// `clusters`: how many clusters of 2 to 8 CTAs the device runs at a time
-static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const int (&clusters)[7]) {
+static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const Clusters& clusters) {
   constexpr int64_t LEAST = 4;  // units of an equal share
   const int64_t sms = num_sms();
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
@@ -1264,7 +1267,7 @@ static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes
   for (int i = 0; i < 7; ++i) {
     const int c = 2 + i;
     const double t = time_ns((double)((blocks + c - 1) / c) * unit_ns, bytes) + CLUSTER_NS;
-    if (tiles <= clusters[i] && blocks >= 2 * c && t < ns) {
+    if (tiles <= clusters.most[i] && blocks >= 2 * c && t < ns) {
       ns = t;
       best.cluster = c;
     }
@@ -1272,27 +1275,29 @@ static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes
   return best;
 }
 template <auto KERN, int N_THREADS>
-static const int (&max_clusters())[7] {
-  struct Most {
-    int n[7];
-    Most() {
-      for (int i = 0; i < 7; ++i) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2u + i;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_sms() / (2 + i) * (2 + i));
-        cfg.blockDim = dim3(N_THREADS);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n[i], KERN, &cfg) != cudaSuccess) n[i] = 0;
-      }
+static Clusters max_clusters() {
+  static Clusters of_device[OncePerDevice::DEVICES];
+  static OncePerDevice once;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= OncePerDevice::DEVICES) return Clusters{};
+  const cudaError_t e = once.run(device, [device] {
+    for (int i = 0; i < 7; ++i) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u + i;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(num_sms() / (2 + i) * (2 + i));
+      cfg.blockDim = dim3(N_THREADS);
+      cfg.dynamicSmemBytes = SMEM_BYTES;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      const cudaError_t bad = cudaOccupancyMaxActiveClusters(&of_device[device].most[i], KERN, &cfg);
+      if (bad != cudaSuccess) return bad;
     }
-  };
-  static const Most most;
-  return most.n;
+    return cudaSuccess;
+  });
+  return e == cudaSuccess ? of_device[device] : Clusters{};
 }
 
 static bool over_rows_allowed() {
@@ -1442,7 +1447,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   // its bytes' time or its 24 MMAs' for each 128 columns (25 ns measured up to rank 64, 50 at 128).
   {
     const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
-    const auto& clusters = max_clusters<k_over_rows<2, true>, ROW_THREADS>();
+    const Clusters clusters = max_clusters<k_over_rows<2, true>, ROW_THREADS>();
     double best = -1;
     for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
       const int64_t bk = (k + 128 * mt - 1) / (128 * mt), bn = (n + 128 * mt - 1) / (128 * mt);
@@ -1469,7 +1474,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       take(cost[1], 1, 1, outputs < s.ctas ? outputs : s.ctas);
       for (int i = 0; i < 7; ++i) {
         const int64_t c = 2 + i;
-        if (outputs <= clusters[i] && plan->most_tiles >= c)
+        if (outputs <= clusters.most[i] && plan->most_tiles >= c)
           take(time_ns((double)((plan->most_tiles + c - 1) / c) * unit_ns, bytes) + CLUSTER_ROWS_NS, 1, (int)c, outputs * c);
       }
     }

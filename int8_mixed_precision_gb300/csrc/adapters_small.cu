@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
 template <int RT, bool BF16>
 static cudaError_t launch_small(const Small& p, int tiles, cudaStream_t st) {
   const size_t smem = (size_t)(SMALL_WARPS + 1) * 16 * p.rp * 4 + (size_t)PARTS * 16 * (p.rp + 8) * 2;
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(k_small<RT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+  static OncePerDevice once;
+  const cudaError_t allowed = opt_in_smem(once, k_small<RT, BF16>, 96 * 1024);
   if (allowed != cudaSuccess) return allowed;
   return launch_pdl(k_small<RT, BF16>, dim3((unsigned)(tiles * p.cluster)), dim3(SMALL_THREADS), smem, st,
                     (unsigned)p.cluster, p);

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/dit6.h"
+#include "per_device.cuh"
 
 namespace dit6 {
 
@@ -460,6 +461,16 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The opt-in of `kern` to `bytes` of dynamic shared memory on the current device; `once` (one for each kernel)
+// remembers it.
+template <typename... KArgs>
+cudaError_t opt_in_smem(OncePerDevice& once, void (*kern)(KArgs...), int bytes) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  return once.run(device, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
 
 // Launches `kern` on `st` with the programmatic stream serialisation attribute, plus a
 // cluster dimension when cluster_x > 1.

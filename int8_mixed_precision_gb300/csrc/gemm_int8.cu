@@ -199,13 +199,8 @@ extern "C" dit_status dit_qgemm_int8(const void* a, const float* a_scale, const 
       !encode_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(b), (uint64_t)k,
                       (uint64_t)n, (uint64_t)k, i8::BK, i8::BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return DIT_ERR_CUDA;
-  static bool attr_done = false;
-  if (!attr_done) {
-    if (cudaFuncSetAttribute(i8::k_gemm_int8, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             i8::SMEM_BYTES) != cudaSuccess)
-      return DIT_ERR_CUDA;
-    attr_done = true;
-  }
+  static OncePerDevice once;
+  if (opt_in_smem(once, i8::k_gemm_int8, i8::SMEM_BYTES) != cudaSuccess) return DIT_ERR_CUDA;
   dim3 grid((unsigned)((n + i8::BN - 1) / i8::BN), (unsigned)((m + i8::BM - 1) / i8::BM));
   if (grid.y > 65535) return DIT_ERR_UNSUPPORTED;
   if (launch_pdl(i8::k_gemm_int8, grid, dim3(i8::THREADS), i8::SMEM_BYTES, reinterpret_cast<cudaStream_t>(stream), 1,

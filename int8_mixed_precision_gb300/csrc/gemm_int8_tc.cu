@@ -495,12 +495,8 @@ dit_status launch_pair_k(const CUtensorMap& ta, const CUtensorMap& tb, const flo
                          void* ws, cudaStream_t st, int band, const ReqArgs& req) {
   using P = PairCfgFor<REQ>;
   auto kern = k_gemm_int8_pair<GELU, ACCM, BANDED, REQ>;
-  static bool attr_done = false;
-  if (!attr_done) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM_BYTES) != cudaSuccess)
-      return DIT_ERR_CUDA;
-    attr_done = true;
-  }
+  static OncePerDevice once;
+  if (opt_in_smem(once, kern, P::SMEM_BYTES) != cudaSuccess) return DIT_ERR_CUDA;
   const int64_t items = ((m + 255) / 256) * ((n + 255) / 256);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

@@ -531,13 +531,9 @@ static dit_status launch_s(const uint8_t* a, const uint8_t* b, const uint8_t* a_
       !encode_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(b), (uint64_t)(K / 2), (uint64_t)N,
                       (uint64_t)(K / 2), BK / 2, BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return DIT_ERR_CUDA;
-  static bool attr_done = false;
+  static OncePerDevice once;
   auto kern = k_gemm_nvfp4_s<BN, STAGES, CTAS, EPW, AHB>;
-  if (!attr_done) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
-      return DIT_ERR_CUDA;
-    attr_done = true;
-  }
+  if (opt_in_smem(once, kern, C::SMEM_BYTES) != cudaSuccess) return DIT_ERR_CUDA;
   const int64_t tiles = (int64_t)((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   int64_t grid = (int64_t)num_sms() * CTAS;
   if (grid > tiles) grid = tiles;
