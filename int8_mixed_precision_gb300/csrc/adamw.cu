@@ -188,6 +188,7 @@ struct Walk {
     }
     d = descs[c.x];
     begin = (int64_t)c.y * CHUNK;
+    if (begin >= d.n && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
     // the rest of the tensor or of the share, if the table's last entry of it says the same
     int64_t n = min(last - at, (d.n - begin + CHUNK - 1) / CHUNK);
     if (n > 1) {
@@ -313,7 +314,11 @@ struct Ahead {
   __device__ __forceinline__ uint64_t field(int i) const {
     return (uint64_t)__shfl_sync(0xffffffffu, word, 2 * i + 1) << 32 | __shfl_sync(0xffffffffu, word, 2 * i);
   }
-  __device__ __forceinline__ void clip() { end = max(begin, min(end, (int64_t)field(9))); }
+  __device__ __forceinline__ void clip(void* ws) {
+    const int64_t n = (int64_t)field(9);
+    if (end > begin && n <= begin && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
+    end = max(begin, min(end, n));
+  }
 };
 static_assert(sizeof(dit_adamw_tensor) == 80, "ten words of 64 bits");
 
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   Ahead now, next, later;
   now.load(descs, n_tensors, e0, at < n_chunks, ws);
   next.load(descs, n_tensors, e1, at + step < n_chunks, ws);
-  now.clip();
+  now.clip(ws);
 
   // whole blocks go through shared memory, a tensor's last partial one does not
   auto fetch = [&](const Ahead& c, Stage<P, G>* to) {
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   for (int s = 0; at < n_chunks; at += step, s ^= 1) {
     later.load(descs, n_tensors, e2, at + 2 * step < n_chunks, ws);
     e2 = entry_at(at + 3 * step);
-    next.clip();
+    next.clip(ws);
     fetch(next, stages + (s ^ 1) * BLOCKS);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();  // the other lanes' copies too
