@@ -22,10 +22,10 @@ _JUST_BF16 = (_BF16,)
 
 
 def raw_stream(stream, index: int) -> int:
-    """The handle of `stream`, or of device `index`'s current stream (without making a Stream object,
-    which costs more than the checks and the launch of a short call together).  The library launches on
+    """The handle of `stream`, or of device `index`'s current stream (by torch's bare functions: a Stream object
+    costs more than the checks and the launch of a short call together).  The library launches on
     the current device, so both have to be on it."""
-    current = torch.cuda.current_device()
+    current = torch._C._cuda_getDevice()
     if stream is not None and getattr(stream, "device_index", index) != index:
         raise DitError(f"the buffers are on cuda:{index}, the stream is on cuda:{stream.device_index}")
     if current != index:

@@ -76,7 +76,7 @@ class Scene:
         monkeypatch.setattr(adapters, "lib", lambda: Library(real, log))
         self.current = 0x10
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: self.current, raising=False)
 
         @contextlib.contextmanager
