@@ -458,7 +458,7 @@ dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const int32_t* tabl
  * the last quotient is within 2 units in the last place of it):
  *   g' = g * (*grad_scale)               (grad_scale NULL: g' = g)
  *   m  = m beta1 + g' (1 - beta1),       v = v beta2 + (g' g') (1 - beta2)
- *   p  = p (1 - lr wd) - (m lr / (1 - beta1^t)) / (sqrt(v) (1 - beta2^t)^-1/2 + eps)
+ *   p  = p - (p (lr wd) + (m lr / (1 - beta1^t)) / (sqrt(v) (1 - beta2^t)^-1/2 + eps))
  * with t = step (>= 1) and the factors computed in fp64 on the host.  p is rounded once to its
  * type; copy (bf16, optional) receives p rounded to bf16.
  *
