@@ -223,13 +223,15 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
       const Columns<RT, BF16> now = ahead[d];
       ahead[d].load(p, b, n0 + AHEAD * STRIDE, n_last, row_lo, row_hi, has_lo, has_hi);
       float d0[4] = {}, d1[4] = {};
+      // The small parts first: an addition cuts the sum to 24 bits, and then only those of the largest parts meet
+      // it at its full size.
 #pragma unroll
-      for (int j = 0; j < Columns<RT, BF16>::STEPS; ++j) {
-        const int k = j * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
-        if (j * 32 >= p.rp) break;
+      for (int q = PARTS - 1; q >= 0; --q) {
+        if (q >= P) continue;
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
-          if (q >= P) break;
+        for (int j = 0; j < Columns<RT, BF16>::STEPS; ++j) {
+          const int k = j * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
+          if (j * 32 >= p.rp) break;
           uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
           if (k < p.rp) {
             lo = *reinterpret_cast<const uint4*>(h + (q * 16 + g8) * hp + k);
