@@ -19,18 +19,21 @@ MAX_RANK = 128
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}
 _JUST_BF16 = (_BF16,)
+_C = torch._C
 
 
 def raw_stream(stream, index: int) -> int:
     """The handle of `stream`, or of device `index`'s current stream (by torch's bare functions: a Stream object
     costs more than the checks and the launch of a short call together).  The library launches on
     the current device, so both have to be on it."""
-    current = torch._C._cuda_getDevice()
+    current = _C._cuda_getDevice()
+    if stream is None and current == index:
+        return _C._cuda_getCurrentRawStream(index)
     if stream is not None and getattr(stream, "device_index", index) != index:
         raise DitError(f"the buffers are on cuda:{index}, the stream is on cuda:{stream.device_index}")
     if current != index:
         raise DitError(f"the buffers are on cuda:{index}, the current device is cuda:{current}")
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return stream.cuda_stream
 
 
 class _Plan(ctypes.Structure):
@@ -137,17 +140,20 @@ def _bytes_of(t, what, index):
     return t.data_ptr()
 
 
-def _agree(plan, bank):
+def _disagree(plan, bank):
     if plan.n_adapters != bank.n_adapters:
         raise DitError(f"the plan is for {plan.n_adapters} adapters, the bank has {bank.n_adapters}")
-    if plan._index != bank._index:
-        raise DitError(f"the plan is on {plan.table.device}, the bank on {bank.device}")
+    raise DitError(f"the plan is on {plan.table.device}, the bank on {bank.device}")
 
 
-def _forward_args(plan, bank, x, y, scratch, ws, saved):
-    """The checked arguments of dit_lora_forward, but for the stream."""
-    _agree(plan, bank)
+def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=None, stream=None, _first=None):
+    """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
+    the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
+    lora_backward needs."""
+    # _first: what a caller launches ahead of the adapters, once they have refused nothing
     i, rows = bank._index, plan.rows
+    if plan._index != i or plan.n_adapters != bank.n_adapters:
+        _disagree(plan, bank)
     xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
     yp = _rows_of(y, rows, bank.n, _CODE, "y", i)
     if saved is None:
@@ -156,16 +162,25 @@ def _forward_args(plan, bank, x, y, scratch, ws, saved):
         vp, vn = _bytes_of(saved, "saved", i), saved.nbytes
     else:
         raise DitError("saved needs AdapterPlan(..., training=True)")
-    return (plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn, _bytes_of(scratch, "scratch", i),
-            scratch.nbytes, _bytes_of(ws, "ws", i), ws.nbytes)
+    sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
+    if _first is not None:
+        _first()
+    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn, sp, scratch.nbytes,
+                                wp, ws.nbytes, raw)
+    if st:
+        _check(st, "dit_lora_forward")
 
 
-def _backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx):
-    """The checked arguments of dit_lora_backward, but for the stream."""
-    _agree(plan, bank)
+def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None, _first=None):
+    """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
+    wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
+    adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
+    lora_forward with the same plan, x, a and scale."""
+    i, rows = bank._index, plan.rows
+    if plan._index != i or plan.n_adapters != bank.n_adapters:
+        _disagree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")
-    i, rows = bank._index, plan.rows
     xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
     dyp = _rows_of(dy, rows, bank.n, _JUST_BF16, "dy", i)
     if dx is None:
@@ -176,36 +191,14 @@ def _backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx):
         raise DitError(f"da: float32 {tuple(bank.a.shape)} is needed")
     if db.dtype != _F32 or db.shape != bank.b.shape:
         raise DitError(f"db: float32 {tuple(bank.b.shape)} is needed")
-    return (plan._info_p, plan._table_p, xp, dyp, *bank._args, _bytes_of(saved, "saved", i), saved.nbytes, dxp, dx_code,
-            _bytes_of(da, "da", i), _bytes_of(db, "db", i), _bytes_of(scratch, "scratch", i), scratch.nbytes,
-            _bytes_of(ws, "ws", i), ws.nbytes)
-
-
-def _forward(args, raw):
-    st = lib().dit_lora_forward(*args, raw)
-    if st:
-        _check(st, "dit_lora_forward")
-
-
-def _backward(args, raw):
-    st = lib().dit_lora_backward(*args, raw)
+    vp, dap, dbp = _bytes_of(saved, "saved", i), _bytes_of(da, "da", i), _bytes_of(db, "db", i)
+    sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
+    if _first is not None:
+        _first()
+    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, *bank._args, vp, saved.nbytes, dxp, dx_code, dap, dbp,
+                                 sp, scratch.nbytes, wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_lora_backward")
-
-
-def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=None, stream=None):
-    """y[t] += scale[g] (x[t] A[g]^T) B[g]^T for every row t with an adapter g (y bf16 or fp32, holding
-    the shared projection's output; other rows are not touched).  saved (adapter_saved) keeps what
-    lora_backward needs."""
-    _forward(_forward_args(plan, bank, x, y, scratch, ws, saved), raw_stream(stream, bank._index))
-
-
-def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, scratch, ws, dx=None, stream=None):
-    """dx[t] += scale[g] (dy[t] B[g]) A[g] (bf16 or fp32, holding the shared projection's part; None: not
-    wanted), and da, db (fp32, the shapes of the bank's a and b, overwritten) the gradients of every
-    adapter over all rows that use it.  dx may be dy itself (a residual's gradient).  saved: filled by
-    lora_forward with the same plan, x, a and scale."""
-    _backward(_backward_args(plan, bank, x, dy, saved, da, db, scratch, ws, dx), raw_stream(stream, bank._index))
 
 
 def _launchable(plan, bank, scratch, ws, saved, *tensors):
@@ -251,24 +244,23 @@ class AdaptedLinear:
         itself, so an activation cannot be fused into it.  y shares no memory with x."""
         if act != ACT_NONE:
             raise DitError("AdaptedLinear: the activation follows the adapters and cannot be fused into the projection")
-        args = _forward_args(plan, self.bank, x, y, scratch, self.linear.ws, saved)
-        _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, y)
-        _apart(y, "y", (x, "x"))
-        raw = raw_stream(stream, self.bank._index)
-        self.linear(x, route, y, bias=bias, stream=stream)
-        _forward(args, raw)
+
+        def project():
+            _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, y)
+            _apart(y, "y", (x, "x"))
+            self.linear(x, route, y, bias=bias, stream=stream)
+        lora_forward(plan, self.bank, x, y, scratch, self.linear.ws, saved=saved, stream=stream, _first=project)
         return y
 
     def backward(self, x, dy, plan, saved, da, db, dx, scratch, stream=None):
         """dx = dy W + the adapters' part; da, db the adapters' gradients.  dx shares no memory with dy or x."""
-        args = _backward_args(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx)
-        _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, dy, dx, da, db)
-        _apart(dx, "dx", (dy, "dy"), (x, "x"))
-        raw = raw_stream(stream, self.bank._index)
-        if self.w_t is None:
+        def project():
+            _launchable(plan, self.bank, scratch, self.linear.ws, saved, x, dy, dx, da, db)
+            _apart(dx, "dx", (dy, "dy"), (x, "x"))
+            if self.w_t is not None:
+                gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
+                return
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 dx.zero_()
-        else:
-            gemm_bf16(dy, self.w_t, dx, self.linear.ws, stream=stream)
-        _backward(args, raw)
+        lora_backward(plan, self.bank, x, dy, saved, da, db, scratch, self.linear.ws, dx=dx, stream=stream, _first=project)
         return dx

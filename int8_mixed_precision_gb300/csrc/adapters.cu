@@ -1309,7 +1309,6 @@ static bool over_rows_allowed() {
 template <bool MN>
 static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, const float* scale, void* held, int parts,
                           void* slots, cudaStream_t st) {
-  if (!p.n_tiles) return DIT_OK;
   CUtensorMap m_in, m_w;
   const bool maps = map_rows(&m_in, in, width, p.rows, TILE_ROWS) &&
                     (MN ? encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, 64)
@@ -1339,7 +1338,6 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, const OverRows* after,
                             bool early, cudaStream_t st) {
-  if (!p.n_tiles) return DIT_OK;
   FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, early ? 1 : 0, after && !after->whole && after->split.ctas > 1 ? 1 : 0};
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
@@ -1407,12 +1405,15 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
     return DIT_ERR_INVALID_ARG;
   if (!aligned32(y) || !aligned32(saved)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const Args p = args_of(*plan, table, rank, ws);
-  void* held = saved ? saved : scratch;
-  char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
-  const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
-  dit_status s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
-  if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, false, st);
+  dit_status s = DIT_OK;
+  if (plan->n_tiles) {
+    const Args p = args_of(*plan, table, rank, ws);
+    void* held = saved ? saved : scratch;
+    char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
+    const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
+    s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
+    if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, false, st);
+  }
   if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
   return s;
 }
