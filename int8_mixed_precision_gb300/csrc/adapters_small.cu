@@ -140,25 +140,52 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
   const int64_t k_first = steps * rank_in / p.cluster, k_last = steps * (rank_in + 1) / p.cluster;
   const __nv_bfloat16* a = p.a + (int64_t)g * p.rank * p.k;
   const int tiles8 = p.rank / 8;
-  for (int64_t s = k_first + warp; s < k_last; s += SMALL_WARPS) {
-    const int64_t k = s * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
-    const bool in = k < p.k;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (in && has_lo) lo = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_lo * p.k + k);
-    if (in && has_hi) hi = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_hi * p.k + k);
-    uint4 w[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (in && i < tiles8) w[i] = *reinterpret_cast<const uint4*>(a + (int64_t)(i * 8 + g8) * p.k + k);
-    }
-    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+  // The tensor cores' additions cut their sums to 24 bits, so every DRAIN steps (256 elements) the sums are added to
+  // those of before, with rounding to nearest, where the warp's share of h is left at the end anyway.
+  constexpr int DRAIN = 8;
+  bool drained = false;
+  auto drain = [&](bool again) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       if (i < tiles8) {
-        mma_16816(acc[i], a0, w[i].x, w[i].y);
-        mma_16816(acc[i], a1, w[i].z, w[i].w);
+        float2* at = reinterpret_cast<float2*>(part + ((int64_t)warp * 16 + g8) * p.rp + i * 8 + c4 * 2);
+#pragma unroll
+        for (int half = 0; half < 2; ++half, at += 4 * p.rp) {
+          float2 sum = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+          if (again) sum = make_float2(at->x + sum.x, at->y + sum.y);
+          *at = sum;
+        }
       }
+  };
+  int64_t s = k_first + warp;
+  for (int64_t stop = k_first + DRAIN * SMALL_WARPS;; stop += DRAIN * SMALL_WARPS) {
+    for (; s < min(k_last, stop); s += SMALL_WARPS) {
+      const int64_t k = s * 32 + c4 * 8;  // this lane's eight elements: four of each 16-deep step
+      const bool in = k < p.k;
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+      if (in && has_lo) lo = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_lo * p.k + k);
+      if (in && has_hi) hi = *reinterpret_cast<const uint4*>(p.x + (int64_t)row_hi * p.k + k);
+      uint4 w[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (in && i < tiles8) w[i] = *reinterpret_cast<const uint4*>(a + (int64_t)(i * 8 + g8) * p.k + k);
+      }
+      const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        if (i < tiles8) {
+          mma_16816(acc[i], a0, w[i].x, w[i].y);
+          mma_16816(acc[i], a1, w[i].z, w[i].w);
+        }
+    }
+    if (stop >= k_last) break;
+    drain(drained);
+    drained = true;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   }
   // The next kernel's CTAs come in from here on: earlier, they would take issue slots and L1 from this one's
   // loads (64 tokens over 16 adapters: 14.9 us a call, against 11.3).
@@ -170,13 +197,10 @@ __global__ void __launch_bounds__(SMALL_THREADS) k_small(Small p) {
   int64_t n0 = n_first + warp * 16;
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d) ahead[d].load(p, b, n0 + d * STRIDE, n_last, row_lo, row_hi, has_lo, has_hi);
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    if (i < tiles8) {
-      float* at = part + ((int64_t)warp * 16 + g8) * p.rp + i * 8 + c4 * 2;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[i][0], acc[i][1]);
-      *reinterpret_cast<float2*>(at + 8 * p.rp) = make_float2(acc[i][2], acc[i][3]);
-    }
+  if (drained)
+    drain(true);
+  else
+    drain(false);
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * p.rp; i += SMALL_THREADS) {
     float v = 0.f;
