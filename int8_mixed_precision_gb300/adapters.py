@@ -66,17 +66,19 @@ class AdapterPlan:
         _check(lib().dit_adapter_plan(*args, None, 0), "dit_adapter_plan")
         host = torch.empty(self.info.table_ints, dtype=torch.int32)
         _check(lib().dit_adapter_plan(*args, host.data_ptr(), host.numel()), "dit_adapter_plan")
-        self.table = host.to(device)
+        self._table = host.to(device)
         self.rows, self.n_adapters, self.training = self.info.rows, int(n_adapters), bool(training)
         self.n_tiles, self.n_small = self.info.n_tiles, self.info.n_small
-        self._info_p, self._table_p = ctypes.addressof(self.info), self.table.data_ptr()
-        self._index = self.table.get_device()
+        self._info_p, self._table_p = ctypes.addressof(self.info), self._table.data_ptr()
+        self._index = self._table.get_device()
+
+    table = property(lambda self: self._table)
 
 
 class AdapterBank:
     """The factors of one layer: a [n_adapters, rank, k] and b [n_adapters, n, rank] in bf16, scale
     [n_adapters] in fp32.  An adapter of a lower rank than the bank's is padded with zeros.  The
-    tensors are the caller's, held and read as they are at each call."""
+    tensors are the caller's, held and read as they are at each call; other tensors are another bank."""
 
     def __init__(self, a, b, scale):
         if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
@@ -94,9 +96,12 @@ class AdapterBank:
         if self.n_adapters < 1 or not 8 <= self.rank <= MAX_RANK or self.rank % 8 or self.k % 8 or self.n % 8 or \
                 self.k < 8 or self.n < 8:
             raise DitError(f"AdapterBank: rank 8 to {MAX_RANK} in steps of 8, k and n multiples of 8")
-        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self._a, self._b, self._scale, self.device = a, b, scale, a.device
         self._index = a.get_device()
-        self._args = (a.data_ptr(), b.data_ptr(), scale.data_ptr(), self.rank, self.k, self.n)
+        self._at = (a.data_ptr(), b.data_ptr(), scale.data_ptr())
+        self._sizes = (self.rank, self.k, self.n)
+
+    a, b, scale = (property(lambda self, name=name: getattr(self, name)) for name in ("_a", "_b", "_scale"))
 
 
 def adapter_scratch(plan: AdapterPlan, bank: AdapterBank):
@@ -140,6 +145,10 @@ def _bytes_of(t, what, index):
     return t.data_ptr()
 
 
+def _moved():
+    raise DitError("the storage of the bank's tensors was exchanged: make a new AdapterBank")
+
+
 def _disagree(plan, bank):
     if plan.n_adapters != bank.n_adapters:
         raise DitError(f"the plan is for {plan.n_adapters} adapters, the bank has {bank.n_adapters}")
@@ -154,6 +163,9 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     i, rows = bank._index, plan.rows
     if plan._index != i or plan.n_adapters != bank.n_adapters:
         _disagree(plan, bank)
+    at = (bank._a.data_ptr(), bank._b.data_ptr(), bank._scale.data_ptr())
+    if at != bank._at:
+        _moved()
     xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
     yp = _rows_of(y, rows, bank.n, _CODE, "y", i)
     if saved is None:
@@ -165,7 +177,7 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
     if _first is not None:
         _first()
-    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *bank._args, yp, _CODE[y.dtype], vp, vn, sp, scratch.nbytes,
+    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *at, *bank._sizes, yp, _CODE[y.dtype], vp, vn, sp, scratch.nbytes,
                                 wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_lora_forward")
@@ -181,6 +193,9 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
         _disagree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")
+    at = (bank._a.data_ptr(), bank._b.data_ptr(), bank._scale.data_ptr())
+    if at != bank._at:
+        _moved()
     xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
     dyp = _rows_of(dy, rows, bank.n, _JUST_BF16, "dy", i)
     if dx is None:
@@ -195,7 +210,7 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
     sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
     if _first is not None:
         _first()
-    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, *bank._args, vp, saved.nbytes, dxp, dx_code, dap, dbp,
+    st = lib().dit_lora_backward(plan._info_p, plan._table_p, xp, dyp, *at, *bank._sizes, vp, saved.nbytes, dxp, dx_code, dap, dbp,
                                  sp, scratch.nbytes, wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_lora_backward")

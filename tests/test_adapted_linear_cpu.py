@@ -194,3 +194,25 @@ def test_a_call_for_another_device_than_the_current_one_is_refused(monkeypatch, 
                     call(**kw)
             assert not s.log
         del s.log[:]
+
+
+def test_a_bank_keeps_to_the_tensors_it_was_made_of(monkeypatch):
+    """The bank's calls take the addresses that it checked.  Its tensors cannot be replaced, and one whose storage was
+    exchanged underneath (``.data = ...``) is refused instead of read where it no longer is."""
+    s = Scene(monkeypatch)
+    for name in ("a", "b", "scale"):
+        with pytest.raises(AttributeError):
+            setattr(s.bank, name, getattr(s.bank, name))
+    with pytest.raises(AttributeError):
+        s.plan.table = s.plan.table
+    call = lambda: dit.lora_forward(s.plan, s.bank, s.x, s.y, s.scratch, s.ws)  # noqa: E731
+    back = lambda: dit.lora_backward(s.plan, s.bank, s.x, s.dy, s.saved, s.da, s.db, s.scratch, s.ws)  # noqa: E731
+    for t in (s.bank.a, s.bank.b, s.bank.scale):
+        call(), back()
+        del s.log[:]
+        was, t.address = t.address, 1 << 29
+        for c in (call, back, s.forward, s.backward):
+            with pytest.raises(dit.DitError, match="storage"):
+                c()
+        assert not s.log
+        t.address = was
