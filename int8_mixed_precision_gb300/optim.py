@@ -45,7 +45,11 @@ class AdamW:
     params fp32 or bf16; grads fp32 or bf16; m, v fp32, or float8_e4m3fn codes with m_scale and
     v_scale (fp32, one for each 256 elements; v then holds the codes of the second moment's
     root).  copies: bf16 tensors that receive the parameters rounded to bf16 (for fp32
-    masters).  m_values, v_values: bf16 tensors for export_moments.  step: steps made so far."""
+    masters).  m_values, v_values: bf16 tensors for export_moments.  step: steps made so far.
+
+    The tables hold the tensors' addresses: a tensor that is given another storage (``.data = ...``) is no longer
+    the one that is stepped.  They are copied on the current stream; other streams wait for that one before their
+    first step.  The step count lives on the host: a step captured in a CUDA graph keeps its own."""
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None, m_values=None, v_values=None,
                  lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -82,6 +86,8 @@ class AdamW:
                 if t.numel() and t.data_ptr() % (4 if name.endswith("_scale") else 32):
                     raise DitError(f"AdamW: {name}: {lib().dit_status_str(2).decode()}")
         self._lists, self.device, self.step_count = lists, device, int(step)
+        # the memory behind the tables' addresses, should a tensor be given another storage
+        self._storages = [t.untyped_storage() for ts in lists.values() for t in ts]
         self._args = _Args(lr, beta1, beta2, eps, weight_decay, 0)
         descs = (_Tensor * count)()
         for i in range(count):
