@@ -69,7 +69,8 @@ class AdapterPlan:
         self._table = host.to(device)
         self.rows, self.n_adapters, self.training = self.info.rows, int(n_adapters), bool(training)
         self.n_tiles, self.n_small = self.info.n_tiles, self.info.n_small
-        self._info_p, self._table_p = ctypes.addressof(self.info), self._table.data_ptr()
+        # converted once: a call of few microseconds passes twenty arguments
+        self._info_p, self._table_p = ctypes.c_void_p(ctypes.addressof(self.info)), ctypes.c_void_p(self._table.data_ptr())
         self._index = self._table.get_device()
 
     table = property(lambda self: self._table)
@@ -99,7 +100,7 @@ class AdapterBank:
         self._a, self._b, self._scale, self.device = a, b, scale, a.device
         self._index = a.get_device()
         self._at = (a.data_ptr(), b.data_ptr(), scale.data_ptr())
-        self._sizes = (self.rank, self.k, self.n)
+        self._sizes = (ctypes.c_int(self.rank), ctypes.c_int64(self.k), ctypes.c_int64(self.n))
 
     a, b, scale = (property(lambda self, name=name: getattr(self, name)) for name in ("_a", "_b", "_scale"))
 

@@ -104,10 +104,11 @@ class AdamW:
         self._chunks = chunks.to(device)
         self._count, self._n_chunks = count, n
         self.ws = workspace(device)
-        self._head = (self._descs.data_ptr(), count, self._chunks.data_ptr(), n)
-        self._types = (_CODE[lists["p"][0].dtype], _CODE[lists["g"][0].dtype], self.bits)
-        self._tail = (self.ws.data_ptr(), self.ws.numel())
-        self._args_p = ctypes.addressof(self._args)
+        self._head = (ctypes.c_void_p(self._descs.data_ptr()), ctypes.c_int64(count), ctypes.c_void_p(self._chunks.data_ptr()),
+                      ctypes.c_int64(n))
+        self._types = tuple(ctypes.c_int(v) for v in (_CODE[lists["p"][0].dtype], _CODE[lists["g"][0].dtype], self.bits))
+        self._tail = (ctypes.c_void_p(self.ws.data_ptr()), ctypes.c_size_t(self.ws.numel()))
+        self._args_p = ctypes.c_void_p(ctypes.addressof(self._args))
         self._index = self._descs.get_device()
 
     @property
