@@ -145,14 +145,15 @@ class AdamW:
         return {"step": self.step_count, "bits": self.bits, **{n: [t.detach().cpu() for t in self._lists[n]] for n in names}}
 
     def load_state_dict(self, sd: dict) -> None:
-        if sd["bits"] != self.bits or any(len(sd[n]) != self._count for n in ("m", "v")):
-            raise DitError("AdamW: the state of another set of tensors")
+        """The state of the same set of tensors; one that does not fit is refused before anything is copied."""
         names = [n for n in ("m", "v", "m_scale", "v_scale") if n in self._lists]
+        if sd["bits"] != self.bits or int(sd["step"]) < 0 or any(n not in sd or len(sd[n]) != self._count for n in names):
+            raise DitError("AdamW: the state of another set of tensors")
         for n in names:
             for t, s in zip(self._lists[n], sd[n]):
-                if t.numel() != s.numel():
+                if t.numel() != s.numel() or t.dtype != s.dtype:
                     raise DitError("AdamW: the state of another set of tensors")
         for n in names:
             for t, s in zip(self._lists[n], sd[n]):
-                t.view(-1).copy_(s.view(-1))
+                t.view(-1).copy_(s.reshape(-1))
         self.step_count = int(sd["step"])

@@ -24,3 +24,21 @@ def test_memory_that_the_tables_point_to_is_not_given_away():
     opt.step()
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in since) and not p.any()
+
+
+def test_states_that_do_not_fit_are_refused_before_anything_is_copied():
+    p, g = [torch.ones(300, device="cuda"), torch.ones(700, device="cuda")], [torch.ones(300, device="cuda"), torch.ones(700, device="cuda")]
+    opt = dit.AdamW(p, g, **dit.adamw_moments(p, 8))
+    opt.step()
+    good = opt.state_dict()
+    other = dit.AdamW(p, g, **dit.adamw_moments(p, 8))
+    short = lambda name, ts: {**good, name: ts}  # noqa: E731
+    for bad in (short("m_scale", good["m_scale"][:1]), short("v_scale", []), {k: v for k, v in good.items() if k != "v_scale"},
+                short("v", good["v"][:1]), short("m", [t.float() for t in good["m"]]), short("bits", 32), short("step", -1),
+                short("v_scale", [t[:1] for t in good["v_scale"]]), short("m_scale", [t.double() for t in good["m_scale"]])):
+        with pytest.raises(dit.DitError):
+            other.load_state_dict(bad)
+        assert other.step_count == 0 and not any(t.float().any() for name in ("m", "v", "m_scale", "v_scale") for t in other._lists[name])
+    other.load_state_dict(good)
+    assert other.step_count == 1
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for n in ("m", "v") for a, b in zip(opt._lists[n], other._lists[n]))
