@@ -32,6 +32,9 @@
 // Warps: 0 loads (TMA), 1 issues the MMAs, the others drain and store.  Every wait is bounded.  Loads and MMAs
 // are issued by an elected lane of a converged warp, from values that the warp shares: otherwise the
 // compiler moves every operand to uniform registers first, 50 ns an MMA.
+#include <stdio.h>
+#include <stdlib.h>
+
 #include "adapters.cuh"
 
 namespace dit6 {
@@ -1252,11 +1255,31 @@ struct Clusters {
 };
 struct RankSplit {
   Split split;
-  int cluster;
+  int cluster;  // 0: the sizes do not allow what is forced
 };
+// Test hook: DIT6_TEST_CUT="cut,n,width" forces the cut of the work of k_to_rank and k_over_rows, where the sizes allow
+// it (else the call is DIT_ERR_UNSUPPORTED): 1 whole outputs to n CTAs, 2 equal shares of the units to n CTAs (0: as
+// many as there are), 3 clusters of n CTAs; and the columns of k_over_rows' output tiles, 128 times width (0: chosen).
+enum { CUT_CHOSEN, CUT_WHOLE, CUT_SHARES, CUT_CLUSTERS };
+struct ForcedCut {
+  int cut, n, width;
+};
+static ForcedCut forced_cut() {
+  ForcedCut f{CUT_CHOSEN, 0, 0};
+  const char* e = getenv("DIT6_TEST_CUT");
+  if (e && sscanf(e, "%d,%d,%d", &f.cut, &f.n, &f.width) != 3) f = ForcedCut{CUT_CHOSEN, 0, 0};
+  return f;
+}
 static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const Clusters& clusters) {
   constexpr int64_t LEAST = 4;  // units of an equal share
   const int64_t sms = num_sms();
+  const ForcedCut force = forced_cut();
+  if (force.cut != CUT_CHOSEN) {
+    const int64_t grain = force.cut == CUT_WHOLE ? blocks : 1;
+    const int ctas = force.cut != CUT_CLUSTERS && force.n > 0 && force.n < sms ? force.n : (int)sms, c = force.n;
+    const bool fits = force.cut != CUT_CLUSTERS || (c >= 2 && c <= 8 && blocks >= c && tiles <= clusters.most[c - 2]);
+    return RankSplit{split_units(tiles * blocks, grain, grain, ctas), !fits ? 0 : force.cut == CUT_CLUSTERS ? c : 1};
+  }
   const Split s = split_units(tiles * blocks, 1, LEAST, (int)sms);
   const double unit_ns = (double)unit_bytes / SM_BYTES_NS;
   const double bytes = (double)s.units * (16384 + (unit_bytes - 16384) / 2.5);  // the weights come out of L2, faster
@@ -1319,6 +1342,7 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
   const uint32_t stage_bytes = 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128);
   p.stages = stages_for(RING_BYTES, stage_bytes);
   const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>, THREADS>());
+  if (!cut.cluster) return DIT_ERR_UNSUPPORTED;
   p.split = cut.split;
   o.cluster = cut.cluster;
   if (cut.cluster > 1)
@@ -1449,8 +1473,10 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   {
     const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
     const Clusters clusters = max_clusters<k_over_rows<2, true>, ROW_THREADS>();
+    const ForcedCut force = forced_cut();
     double best = -1;
     for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
+      if (force.width && mt != force.width) continue;
       const int64_t bk = (k + 128 * mt - 1) / (128 * mt), bn = (n + 128 * mt - 1) / (128 * mt);
       const int64_t unit = (2 * mt + boxes) * 16384, outputs = (bk + bn) * p.n_adapters, units = (bk + bn) * p.n_tiles;
       const double mma_ns = mt * 24 * (p.rp <= 64 ? 25.0 : 25.0 * p.rp / 64), load_ns = (double)unit / SM_BYTES_NS;
@@ -1471,6 +1497,13 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
         p.split = s;
         p.split.ctas = (int)ctas;
       };
+      if (force.cut != CUT_CHOSEN) {
+        const int ctas = force.n > 0 && force.n < sms ? force.n : (int)sms, c = force.n;
+        if (force.cut == CUT_WHOLE) take(0, 1, 1, outputs < ctas ? outputs : ctas);
+        if (force.cut == CUT_SHARES) take(0, 0, 1, split_units(units, 1, 1, ctas).ctas);
+        if (force.cut == CUT_CLUSTERS && c >= 2 && c <= 8 && outputs <= clusters.most[c - 2]) take(0, 1, c, outputs * c);
+        continue;
+      }
       take(cost[0], 0, 1, s.ctas);
       take(cost[1], 1, 1, outputs < s.ctas ? outputs : s.ctas);
       for (int i = 0; i < 7; ++i) {
@@ -1480,6 +1513,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       }
     }
   }
+  if (!o.mtiles) return DIT_ERR_UNSUPPORTED;  // what is forced does not fit
   const int64_t sum_chunks = (o.g[0].blocks + o.g[1].blocks) * p.n_adapters * (o.mtiles * 128 * p.rp / 1024);
   const int64_t sum_ctas = sum_chunks < 65536 ? sum_chunks : 65536;
   CUtensorMap m_x, m_e, m_dy, m_h;
