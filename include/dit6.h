@@ -15,14 +15,22 @@
  * - The library never allocates, frees or synchronises.  Every call only enqueues work on
  *   `stream` and returns.  Its kernels are launched with programmatic dependent launch: one
  *   may start its prologue while the previous kernel on the stream drains, but waits for that
- *   kernel to complete before touching memory, so stream order holds as for plain launches.  The return code covers argument errors found on the host;
+ *   kernel to complete before touching memory, so stream order holds as for plain launches.
+ *   Inside a call of dit_lora_forward or dit_lora_backward the kernels behind the first one touch some memory
+ *   ahead of that wait: they read what was complete before their predecessor started (y, dx, dy, h, the weights
+ *   and, for dx, e), and dx is updated beside the kernel of the factors' gradients, which it shares nothing
+ *   with.  This rests on every kernel of these calls waiting itself before it lets the next one launch: what
+ *   precedes it has then completed and reached global memory.  The first kernel of a call waits before any
+ *   access and every kernel before its end, so for other work on the stream the order is that of plain launches.
+ * - The return code covers argument errors found on the host;
  *   errors found on the device (a bounded wait that ran out) are OR-ed into the status
  *   word at byte 0 of the workspace (see dit_ws_status_offset), which the caller reads
  *   after synchronising.
  * - Workspace: `ws` is a caller-owned device buffer of at least dit_workspace_bytes()
  *   bytes, zero-filled once by the caller before its first use.  The kernels keep it in a
- *   reusable state (every counter they bump is reset by the same launch).  Two calls that
- *   run concurrently on the GPU must not share one workspace.
+ *   reusable state (every counter they bump is reset by the same launch, or by the first
+ *   kernel of the call that uses it).  Two calls that run concurrently on the GPU must not
+ *   share one workspace.
  * - Tensors are row-major and contiguous.  Activation and delta tensors are bf16 or fp32
  *   (dit_dtype).  Device pointers must be 32-byte aligned (256-bit vector loads).
  * - All entry points are thread-compatible.  The library's only global mutable state is a

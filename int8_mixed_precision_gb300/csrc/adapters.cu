@@ -24,10 +24,13 @@
 // elements and added there with rounding to nearest.
 //
 // Ahead of the stream.  Each kernel lets the next one launch only after its own wait for the one before, so a kernel
-// that has started finds everything but its immediate predecessor complete, and waits for that one
+// that has started finds everything but its immediate predecessor complete and in global memory (the wait returns when
+// the grids before have completed and flushed their results), and waits for that one
 // where it first reads what it made (h and e) or writes what it reads: k_from_rank's first weights and
 // old values and k_over_rows' units of dB come in before, and dx, which needs nothing of k_over_rows, is
-// updated beside it.  Every kernel waits before it ends, so the stream's order holds for whatever follows.
+// updated beside it; its e is two kernels back.  The instruction's own text speaks of a grid and its direct
+// predecessors, so a new kernel in between has to keep the order of wait and trigger.  Every kernel waits before it
+// ends, so the stream's order holds for whatever follows.
 //
 // Warps: 0 loads (TMA), 1 issues the MMAs, the others drain and store.  Every wait is bounded.  Loads and MMAs
 // are issued by an elected lane of a converged warp, from values that the warp shares: otherwise the

@@ -454,7 +454,8 @@ int num_sms();  // SM count of the current device (cached per device)
 // (pdl_launch_dependents), and it waits for the previous kernel to complete, with that
 // kernel's memory operations visible, before its own first global memory access (pdl_wait).
 // The next kernel's CTAs thus launch and run their prologue (barrier initialisation, tensor
-// memory allocation) while this one drains.  After a launch without the attribute, or after a
+// memory allocation) while this one drains.  The adapters' kernels order the two the other way round and read
+// ahead of the wait (adapters.cu says what and why that is sound).  After a launch without the attribute, or after a
 // stream operation other than a kernel, both are no-ops.
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_launch_dependents() {
