@@ -37,12 +37,15 @@ static dit_status make_plan(const int64_t* lengths, const int32_t* adapters, int
     rows += lengths[i];
   }
   // Serving plans: runs of few rows go to small tiles, which share a tile among runs and are one launch beside those
-  // of the large ones (8 us).  Where there are some large tiles and few short runs, each run gets a large
-  // tile of its own instead, which costs less than that launch.
+  // of the large ones (12 to 17 us).  Where there are some large tiles and few short runs, each run gets a large
+  // tile of its own instead: at 1920 -> 7680 and rank 64 in bf16, 4 runs beside 16 large tiles take 22.0 us (33.8 with
+  // the launch), 16 beside 64 65.2 (72.9), and in long batches 0.55 us a run, which is the launch's time at
+  // about 30: 34 beside 276 take 215.5, 69 take 230.1 (209.7).
+  constexpr int64_t FEW = 24;
   int64_t large = 0, shorts = 0;
   for (const auto& rs : runs)
     for (const Run& r : rs) (r.rows <= SMALL_RUN ? shorts : large) += r.rows <= SMALL_RUN ? 1 : (r.rows + TILE_ROWS - 1) / TILE_ROWS;
-  const bool no_small = training || 4 * shorts <= large;
+  const bool no_small = training || (4 * shorts <= large && shorts <= FEW);
   int64_t n_tiles = 0, n_small = 0, most = 0;
   for (const auto& rs : runs) {
     int64_t few = 0;
