@@ -403,7 +403,11 @@ dit_status dit_shard_finish_host(const double* partials, int n_partials, const f
  * once.  Every sum has a fixed order (no atomics on values): a call with the same arguments gives
  * the same bits.  y and dx of rows without an adapter are not touched.  A row's results depend
  * on that row alone, and an adapter's gradients on its own rows alone, whatever the other
- * rows hold.
+ * rows hold; the last bits depend on the plan too (the other requests' number and lengths), which
+ * decides how sums are cut.
+ * Infinities and NaN: results are infinite or NaN where the formulas' are, and NaN in some places
+ * where those are infinite, since h and e enter as two or three parts and a part of 0 may meet an
+ * infinite factor.  An h or e that rounds to infinity in bf16 (above 3.39e38) counts as infinite.
  *
  * The plan.  dit_adapter_plan (host, no device work) turns the requests' lengths and adapters
  * into a table of tiles of rows that share an adapter.  A plan serves every layer and step with

@@ -26,9 +26,10 @@ inline int64_t off_small(const dit_adapter_plan_t& p) { return (off_first(p) + p
 
 // h and e ("held"): for each tile of the plan 128 rows (those past the tile's own are zeros) of
 // PARTS x rp bf16 (rp: the rank rounded up to 16; columns past the rank are zeros).  A value is held
-// as the sum of its parts, each the bf16 nearest to what the earlier ones leave: two parts
-// carry 16 significant bits, which a bf16 output cannot tell from fp32, three carry 24, for
-// the gradients and for fp32 outputs.  All parts are operands of the bf16 tensor pipe, whose
+// as the sum of its parts, each the bf16 nearest to what the earlier ones leave: three parts
+// carry 24 significant bits, for the gradients and for fp32 outputs, two carry 16, for bf16 outputs.  There
+// they cost at most 2^-17 of the sum of |h B|, less than the output's own rounding (2^-9 of it) unless y all
+// but cancels, to less than 2^-8 of that sum; a third part would make half as many MMAs more.  All parts are operands of the bf16 tensor pipe, whose
 // products of two bf16 values are exact.
 constexpr int PARTS = 3;
 inline int padded_rank(int rank) { return (rank + 15) / 16 * 16; }

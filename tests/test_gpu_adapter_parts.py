@@ -38,3 +38,37 @@ def test_three_parts(rank, training, cut, monkeypatch):
     for name, v in got.items():
         assert P.worst(v, want[name])[0] <= P.BOUND, (name, P.worst(v, want[name])[0])
     assert dit.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), 3.0e38])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("training", [False, True])
+def test_infinities_in_the_factors_reach_what_the_formulas_say(training, dtype, value):
+    """An infinity or NaN in B (one row of it) makes that column of y infinite or NaN for the rows of the adapter, one in
+    A (one element) every column of theirs; every other element has the bits of a clean call.  With parts of h, an
+    infinity may come out as NaN.  A finite factor of any size changes nothing of this."""
+    g = torch.Generator().manual_seed(3)
+    G, r, k, n, lengths, adapters = 2, 24, 136, 264, [5, 140, 9], [0, 1, 0]
+    x, a, b = torch.randn(154, k, generator=g), torch.randn(G, r, k, generator=g) * 0.1, torch.randn(G, n, r, generator=g) * 0.1
+    out = []
+    for where in (None, "b", "a"):
+        a1, b1 = a.clone(), b.clone()
+        if where == "b":
+            b1[0, 77, 3] = value
+        if where == "a":
+            a1[0, 3, 50] = value
+        bank = dit.AdapterBank(a1.bfloat16().cuda(), b1.bfloat16().cuda(), torch.ones(G, device="cuda"))
+        plan, ws = dit.AdapterPlan(lengths, adapters, G, training=training), dit.workspace()
+        y = torch.ones(154, n, dtype=dtype, device="cuda")
+        dit.lora_forward(plan, bank, x.bfloat16().cuda(), y, dit.adapter_scratch(plan, bank), ws)
+        out.append(y.cpu())
+        assert dit.device_status(ws) == 0
+    clean, in_b, in_a = out
+    mine = torch.ones(154, dtype=torch.bool)
+    mine[5:145] = False
+    assert torch.equal(in_b[~mine], clean[~mine]) and torch.equal(in_a[~mine], clean[~mine])
+    others = torch.arange(n) != 77
+    assert torch.equal(in_b[mine][:, others], clean[mine][:, others])
+    if value != 3.0e38:
+        assert not torch.isfinite(in_b[mine][:, 77]).any() and not torch.isfinite(in_a[mine]).any()
+        assert torch.isfinite(clean).all()
