@@ -18,7 +18,6 @@ from ._lib import lib
 MAX_RANK = 128
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}
-_JUST_BF16 = (_BF16,)
 _C = torch._C
 
 
@@ -99,7 +98,8 @@ class AdapterBank:
             raise DitError(f"AdapterBank: rank 8 to {MAX_RANK} in steps of 8, k and n multiples of 8")
         self._a, self._b, self._scale, self.device = a, b, scale, a.device
         self._index = a.get_device()
-        self._at = (a.data_ptr(), b.data_ptr(), scale.data_ptr())
+        self._pointers = (a.data_ptr, b.data_ptr, scale.data_ptr)
+        self._at = tuple(at() for at in self._pointers)
         self._sizes = (ctypes.c_int(self.rank), ctypes.c_int64(self.k), ctypes.c_int64(self.n))
 
     a, b, scale = (property(lambda self, name=name: getattr(self, name)) for name in ("_a", "_b", "_scale"))
@@ -129,19 +129,28 @@ def _refuse(t, what, index):
     raise DitError(f"buffers must be contiguous ({what})")
 
 
-def _rows_of(t, rows, width, types, what, index):
-    if t.dtype not in types:
+def _not_bf16(t, what):
+    raise DitError(f"{what}: unsupported dtype {t.dtype}")
+
+
+def _type_code(t, what):
+    code = _CODE.get(t.dtype)
+    if code is None:
         raise DitError(f"{what}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _rows_of(t, rows, width, what, index):
     shape = t.shape
     if len(shape) != 2 or shape[1] != width or shape[0] < rows:
         raise DitError(f"{what}: {tuple(shape)}, the call needs [{rows}, {width}]")
-    if t.get_device() != index or index < 0 or not t.is_contiguous():
+    if t.get_device() != index or not t.is_contiguous():
         _refuse(t, what, index)
     return t.data_ptr()
 
 
 def _bytes_of(t, what, index):
-    if t.get_device() != index or index < 0 or not t.is_contiguous():
+    if t.get_device() != index or not t.is_contiguous():
         _refuse(t, what, index)
     return t.data_ptr()
 
@@ -164,11 +173,16 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     i, rows = bank._index, plan.rows
     if plan._index != i or plan.n_adapters != bank.n_adapters:
         _disagree(plan, bank)
-    at = (bank._a.data_ptr(), bank._b.data_ptr(), bank._scale.data_ptr())
+    a, b, scale = bank._pointers
+    at = a(), b(), scale()
     if at != bank._at:
         _moved()
-    xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
-    yp = _rows_of(y, rows, bank.n, _CODE, "y", i)
+    if x.dtype is not _BF16:
+        _not_bf16(x, "x")
+    xp, y_code = _rows_of(x, rows, bank.k, "x", i), _type_code(y, "y")
+    yp = _rows_of(y, rows, bank.n, "y", i)
+    if i < 0:
+        _refuse(x, "x", i)
     if saved is None:
         vp, vn = None, 0
     elif plan.training:
@@ -178,7 +192,7 @@ def lora_forward(plan: AdapterPlan, bank: AdapterBank, x, y, scratch, ws, saved=
     sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
     if _first is not None:
         _first()
-    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *at, *bank._sizes, yp, _CODE[y.dtype], vp, vn, sp, scratch.nbytes,
+    st = lib().dit_lora_forward(plan._info_p, plan._table_p, xp, *at, *bank._sizes, yp, y_code, vp, vn, sp, scratch.nbytes,
                                 wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_lora_forward")
@@ -194,15 +208,20 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
         _disagree(plan, bank)
     if not plan.training:
         raise DitError("lora_backward needs AdapterPlan(..., training=True)")
-    at = (bank._a.data_ptr(), bank._b.data_ptr(), bank._scale.data_ptr())
+    a, b, scale = bank._pointers
+    at = a(), b(), scale()
     if at != bank._at:
         _moved()
-    xp = _rows_of(x, rows, bank.k, _JUST_BF16, "x", i)
-    dyp = _rows_of(dy, rows, bank.n, _JUST_BF16, "dy", i)
+    for t, what in ((x, "x"), (dy, "dy")):
+        if t.dtype is not _BF16:
+            _not_bf16(t, what)
+    xp, dyp = _rows_of(x, rows, bank.k, "x", i), _rows_of(dy, rows, bank.n, "dy", i)
+    if i < 0:
+        _refuse(x, "x", i)
     if dx is None:
         dxp, dx_code = None, 1
     else:
-        dxp, dx_code = _rows_of(dx, rows, bank.k, _CODE, "dx", i), _CODE[dx.dtype]
+        dx_code, dxp = _type_code(dx, "dx"), _rows_of(dx, rows, bank.k, "dx", i)
     if da.dtype != _F32 or da.shape != bank.a.shape:
         raise DitError(f"da: float32 {tuple(bank.a.shape)} is needed")
     if db.dtype != _F32 or db.shape != bank.b.shape:
