@@ -1,7 +1,7 @@
 // One AdamW step over many tensors, with the moments in 32 or in 8 bits.
 //
-// Bound by memory: per element 2 x p + g + 4 x moment (+ copy) bytes and about 15 operations.  (32-bit moments,
-// fp32 parameters, bf16 gradients, 265 M elements: 0.99 ms, 6.9 TB/s, the copy rate.)  One
+// Bound by memory: per element 2 x p + g + 4 x moment (+ copy) bytes and about 16 operations.  (32-bit moments,
+// fp32 parameters, bf16 gradients, 265 M elements: 1.00 ms, 6.9 TB/s, the copy rate.)  One
 // launch covers all tensors: a CTA takes one chunk of 4096 consecutive elements of one tensor
 // from a table, a warp 256 of them at a time (8 to a lane: 32-byte vectors of fp32), which is
 // also the block that shares a scale of the 8-bit moments, so its largest magnitude is

@@ -1,8 +1,8 @@
 // Low-rank adapters for short requests: y[t] += scale (x[t] A^T) B^T for tiles of up to 16 rows that
 // share an adapter, wherever in the batch they are (single tokens of a serving batch above all).
 //
-// Bound by latency (one token, 1920 -> 5760 at rank 16: 5.7 us a call; 64 tokens over 16 adapters, 1920 -> 7680 at
-// rank 32: 9.4 us, 1.3 TB/s), and then by reading each adapter's A and B once: 16 rows reuse a weight far too
+// Bound by latency (one token, 1920 -> 5760 at rank 16: 5.9 us a call, 5.4 in a graph; 64 tokens over 16 adapters,
+// 1920 -> 7680 at rank 32: 9.6 us, 1.2 TB/s), and then by reading each adapter's A and B once: 16 rows reuse a weight far too
 // little to fill a 128-row tcgen05 instruction, so the products run on mma.sync (16 x 8 x 16) with
 // both operands loaded from global memory straight into fragments; a product's contraction
 // index may be permuted freely, so every lane loads 16 (or 8) contiguous bytes and takes them for the
