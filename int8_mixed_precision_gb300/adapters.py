@@ -74,6 +74,9 @@ class AdapterPlan:
 
     table = property(lambda self: self._table)
 
+    def __reduce_ex__(self, protocol):
+        raise DitError("an AdapterPlan holds addresses: make another plan instead of a copy")
+
 
 class AdapterBank:
     """The factors of one layer: a [n_adapters, rank, k] and b [n_adapters, n, rank] in bf16, scale
@@ -103,6 +106,9 @@ class AdapterBank:
         self._sizes = (ctypes.c_int(self.rank), ctypes.c_int64(self.k), ctypes.c_int64(self.n))
 
     a, b, scale = (property(lambda self, name=name: getattr(self, name)) for name in ("_a", "_b", "_scale"))
+
+    def __reduce__(self):
+        return AdapterBank, (self._a, self._b, self._scale)
 
 
 def adapter_scratch(plan: AdapterPlan, bank: AdapterBank):
