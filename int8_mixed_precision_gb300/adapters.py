@@ -101,6 +101,7 @@ class AdapterBank:
             raise DitError(f"AdapterBank: rank 8 to {MAX_RANK} in steps of 8, k and n multiples of 8")
         self._a, self._b, self._scale, self.device = a, b, scale, a.device
         self._index = a.get_device()
+        self._shapes = (a.shape, b.shape)
         self._pointers = (a.data_ptr, b.data_ptr, scale.data_ptr)
         self._at = tuple(at() for at in self._pointers)
         self._sizes = (ctypes.c_int(self.rank), ctypes.c_int64(self.k), ctypes.c_int64(self.n))
@@ -218,9 +219,10 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
     at = a(), b(), scale()
     if at != bank._at:
         _moved()
-    for t, what in ((x, "x"), (dy, "dy")):
-        if t.dtype is not _BF16:
-            _not_bf16(t, what)
+    if x.dtype is not _BF16:
+        _not_bf16(x, "x")
+    if dy.dtype is not _BF16:
+        _not_bf16(dy, "dy")
     xp, dyp = _rows_of(x, rows, bank.k, "x", i), _rows_of(dy, rows, bank.n, "dy", i)
     if i < 0:
         _refuse(x, "x", i)
@@ -228,10 +230,11 @@ def lora_backward(plan: AdapterPlan, bank: AdapterBank, x, dy, saved, da, db, sc
         dxp, dx_code = None, 1
     else:
         dx_code, dxp = _type_code(dx, "dx"), _rows_of(dx, rows, bank.k, "dx", i)
-    if da.dtype != _F32 or da.shape != bank.a.shape:
-        raise DitError(f"da: float32 {tuple(bank.a.shape)} is needed")
-    if db.dtype != _F32 or db.shape != bank.b.shape:
-        raise DitError(f"db: float32 {tuple(bank.b.shape)} is needed")
+    a_shape, b_shape = bank._shapes
+    if da.dtype is not _F32 or da.shape != a_shape:
+        raise DitError(f"da: float32 {tuple(a_shape)} is needed")
+    if db.dtype is not _F32 or db.shape != b_shape:
+        raise DitError(f"db: float32 {tuple(b_shape)} is needed")
     vp, dap, dbp = _bytes_of(saved, "saved", i), _bytes_of(da, "da", i), _bytes_of(db, "db", i)
     sp, wp, raw = _bytes_of(scratch, "scratch", i), _bytes_of(ws, "ws", i), raw_stream(stream, i)
     if _first is not None:

@@ -1273,10 +1273,10 @@ static ForcedCut forced_cut() {
   if (e && sscanf(e, "%d,%d,%d", &f.cut, &f.n, &f.width) != 3) f = ForcedCut{CUT_CHOSEN, 0, 0};
   return f;
 }
-static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const Clusters& clusters) {
+static RankSplit split_to_rank(int64_t tiles, int64_t blocks, int64_t unit_bytes, const Clusters& clusters,
+                               const ForcedCut& force) {
   constexpr int64_t LEAST = 4;  // units of an equal share
   const int64_t sms = num_sms();
-  const ForcedCut force = forced_cut();
   if (force.cut != CUT_CHOSEN) {
     const int64_t grain = force.cut == CUT_WHOLE ? blocks : 1;
     const int ctas = force.cut != CUT_CLUSTERS && force.n > 0 && force.n < sms ? force.n : (int)sms, c = force.n;
@@ -1307,6 +1307,7 @@ static Clusters max_clusters() {
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= OncePerDevice::DEVICES) return Clusters{};
   const cudaError_t e = once.run(device, [device] {
+    if (!allow_smem<KERN>()) return cudaErrorInvalidValue;
     for (int i = 0; i < 7; ++i) {
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1326,28 +1327,24 @@ static Clusters max_clusters() {
   return e == cudaSuccess ? of_device[device] : Clusters{};
 }
 
-static bool over_rows_allowed() {
-  return allow_smem<k_over_rows<1, false>>() && allow_smem<k_over_rows<2, false>>() && allow_smem<k_over_rows<4, false>>() &&
-         allow_smem<k_over_rows<1, true>>() && allow_smem<k_over_rows<2, true>>() && allow_smem<k_over_rows<4, true>>();
-}
-
 // held = scale * (in W^T); MN: w is [n_adapters][width][rank], else [n_adapters][rank][width]
 template <bool MN>
 static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, const float* scale, void* held, int parts,
-                          void* slots, cudaStream_t st) {
+                          void* slots, const ForcedCut& force, cudaStream_t st) {
   CUtensorMap m_in, m_w;
   const bool maps = map_rows(&m_in, in, width, p.rows, TILE_ROWS) &&
                     (MN ? encode_tmap_bf16_3d(&m_w, w, p.rank, width, p.n_adapters, 64)
                         : encode_tmap_bf16_3d(&m_w, w, width, p.rank, p.n_adapters, p.rp));
-  if (!maps || !allow_smem<k_to_rank<MN, false>>() || !allow_smem<k_to_rank<MN, true>>()) return DIT_ERR_CUDA;
+  if (!maps) return DIT_ERR_CUDA;
   ToRank o{scale, reinterpret_cast<__nv_bfloat16*>(held), reinterpret_cast<float*>(slots), (int)((width + 63) / 64), 1};
   p.parts = parts;
   const uint32_t stage_bytes = 16384 + (MN ? (p.rank + 63) / 64 * 8192 : p.rp * 128);
   p.stages = stages_for(RING_BYTES, stage_bytes);
-  const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>, THREADS>());
+  const RankSplit cut = split_to_rank(p.n_tiles, o.blocks, stage_bytes, max_clusters<k_to_rank<MN, true>, THREADS>(), force);
   if (!cut.cluster) return DIT_ERR_UNSUPPORTED;
   p.split = cut.split;
   o.cluster = cut.cluster;
+  if (!(cut.cluster > 1 ? allow_smem<k_to_rank<MN, true>>() : allow_smem<k_to_rank<MN, false>>())) return DIT_ERR_CUDA;
   if (cut.cluster > 1)
     return launch_pdl(k_to_rank<MN, true>, dim3((unsigned)(p.n_tiles * cut.cluster)), dim3(THREADS), SMEM_BYTES, st,
                       (unsigned)cut.cluster, m_in, m_w, p, o) == cudaSuccess
@@ -1365,12 +1362,13 @@ static dit_status to_rank(Args p, const void* in, int64_t width, const void* w, 
 template <bool MN, bool BF16>
 static dit_status from_rank(Args p, const void* held, int held_parts, const void* w, void* out, int64_t width, const OverRows* after,
                             bool early, cudaStream_t st) {
+  const int64_t sms = num_sms();
   FromRank o{out, width, 128, 0, 1, 0, 0, 0, 1, early ? 1 : 0, after && !after->whole && after->split.ctas > 1 ? 1 : 0};
   p.parts = BF16 ? 2 : PARTS;
   const uint32_t h_bytes = (p.parts * p.rp + 63) / 64 * 16384;
   auto bytes_of = [&](int nb) { return (uint32_t)(MN ? nb / 64 * p.rp * 128 : (p.rank + 63) / 64 * nb * 128); };
   // narrower blocks where all of them run at once, or where wide ones leave the panels too little room
-  if ((int64_t)p.n_tiles * ((width + 63) / 64) <= num_sms() || RING_BYTES < h_bytes + 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
+  if ((int64_t)p.n_tiles * ((width + 63) / 64) <= sms || RING_BYTES < h_bytes + 2 * bytes_of(128) + 5 * 16384) o.nb = 64;
   const uint32_t w_bytes = bytes_of(o.nb);
   p.stages = 2;
   // two tiles of held if that leaves six panels; then up to four stages of weights
@@ -1385,7 +1383,7 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
   // every SM has two jobs.  (17776 x 1920 in fp32 at rank 128: 90 us with one block, 79 with four.)  At least two
   // blocks even where the tile of held is small, since a job's number is a round trip to memory
   // (12000 x 1920 in bf16 at rank 32, forward: 37.4 us with one block, 34.1 with two, 35.4 with three).
-  const int64_t blocks = (int64_t)p.n_tiles * o.n_blocks, even = blocks / (16 * num_sms()), two = blocks / (2 * num_sms());
+  const int64_t blocks = (int64_t)p.n_tiles * o.n_blocks, even = blocks / (16 * sms), two = blocks / (2 * sms);
   int64_t per_job = 1 + h_bytes / (o.nb * TILE_ROWS * (BF16 ? 2 : 4));
   if (per_job < 2) per_job = 2;
   if (per_job > two) per_job = two;
@@ -1394,7 +1392,7 @@ static dit_status from_rank(Args p, const void* held, int held_parts, const void
   o.tile_jobs = (o.n_blocks + o.per_job - 1) / o.per_job;
   o.jobs = p.n_tiles * o.tile_jobs;
   if (o.jobs > 0x7fffff00) return DIT_ERR_UNSUPPORTED;
-  const int64_t ctas = o.jobs < num_sms() ? o.jobs : num_sms();
+  const int64_t ctas = o.jobs < sms ? o.jobs : sms;
   CUtensorMap m_held, m_w, m_out;
   const bool maps = encode_tmap_2d(&m_out, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
                                    (uint64_t)width, (uint64_t)p.rows, (uint64_t)width * (BF16 ? 2 : 4), BF16 ? 64 : 32,
@@ -1438,7 +1436,7 @@ extern "C" dit_status dit_lora_forward(const dit_adapter_plan_t* plan, const int
     void* held = saved ? saved : scratch;
     char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
     const int parts = saved || y_dt == DIT_F32 ? PARTS : 2;
-    s = to_rank<false>(p, x, k, a, scale, held, parts, slots, st);
+    s = to_rank<false>(p, x, k, a, scale, held, parts, slots, forced_cut(), st);
     if (s == DIT_OK) s = from_rank<false>(p, held, parts, b, y, y_dt, n, nullptr, false, st);
   }
   if (s == DIT_OK) s = small_tiles(*plan, table, x, a, b, scale, rank, k, n, y, y_dt, ws, st);
@@ -1457,16 +1455,17 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
     return DIT_ERR_INVALID_ARG;
   if (!aligned32(dy) || !aligned32(saved) || !aligned32(dx) || !aligned32(da) || !aligned32(db)) return DIT_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Args p = args_of(*plan, table, rank, ws);
+  const Args plain = args_of(*plan, table, rank, ws);
+  Args p = plain;
   char* slots = reinterpret_cast<char*>(scratch) + held_bytes(plan->n_tiles, rank);
   if (!plan->n_tiles) {  // no row has an adapter: every gradient is zero
     const bool ok = cudaMemsetAsync(da, 0, (size_t)plan->n_adapters * rank * k * 4, st) == cudaSuccess &&
                     cudaMemsetAsync(db, 0, (size_t)plan->n_adapters * rank * n * 4, st) == cudaSuccess;
     return ok ? DIT_OK : DIT_ERR_CUDA;
   }
-  dit_status s = to_rank<true>(p, dy, n, b, scale, scratch, PARTS, slots, st);
+  const ForcedCut force = forced_cut();
+  dit_status s = to_rank<true>(p, dy, n, b, scale, scratch, PARTS, slots, force, st);
   if (s != DIT_OK) return s;
-  if (!over_rows_allowed()) return DIT_ERR_CUDA;
 
   OverRows o{};
   o.first = table + off_first(*plan);
@@ -1476,7 +1475,6 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   {
     const int64_t sms = num_sms(), boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
     const Clusters clusters = max_clusters<k_over_rows<2, true>, ROW_THREADS>();
-    const ForcedCut force = forced_cut();
     double best = -1;
     for (int mt = p.rp <= 64 ? 4 : 2; mt >= 1; mt /= 2) {
       if (force.width && mt != force.width) continue;
@@ -1524,11 +1522,21 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
   if (!map_rows(&m_x, x, k, p.rows, ROW_STAGE) || !map_rows(&m_e, scratch, PARTS * p.rp, held_rows, ROW_STAGE) ||
       !map_rows(&m_dy, dy, n, p.rows, ROW_STAGE) || !map_rows(&m_h, saved, PARTS * p.rp, held_rows, ROW_STAGE))
     return DIT_ERR_CUDA;
-  auto kern = o.cluster > 1 ? (o.mtiles == 4 ? k_over_rows<4, true> : o.mtiles == 2 ? k_over_rows<2, true> : k_over_rows<1, true>)
-                            : (o.mtiles == 4 ? k_over_rows<4, false> : o.mtiles == 2 ? k_over_rows<2, false> : k_over_rows<1, false>);
+  struct Kernel {
+    void (*run)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Args, OverRows);
+    bool (*allowed)();
+  };
+  static const Kernel kernels[2][3] = {{{k_over_rows<1, false>, allow_smem<k_over_rows<1, false>>},
+                                        {k_over_rows<2, false>, allow_smem<k_over_rows<2, false>>},
+                                        {k_over_rows<4, false>, allow_smem<k_over_rows<4, false>>}},
+                                       {{k_over_rows<1, true>, allow_smem<k_over_rows<1, true>>},
+                                        {k_over_rows<2, true>, allow_smem<k_over_rows<2, true>>},
+                                        {k_over_rows<4, true>, allow_smem<k_over_rows<4, true>>}}};
+  const Kernel& kern = kernels[o.cluster > 1][o.mtiles / 2];
+  if (!kern.allowed()) return DIT_ERR_CUDA;
   const int h_boxes = 64 % p.rp == 0 ? (PARTS * p.rp + 63) / 64 : PARTS * ((p.rp + 63) / 64);
   p.stages = stages_for(RING_BYTES, (2 * o.mtiles + h_boxes) * ROW_BOX);
-  if (launch_pdl(kern, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, (unsigned)o.cluster, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
+  if (launch_pdl(kern.run, dim3(p.split.ctas), dim3(ROW_THREADS), SMEM_BYTES, st, (unsigned)o.cluster, m_x, m_e, m_dy, m_h, p, o) != cudaSuccess)
     return DIT_ERR_CUDA;
   // dx after the gradients of the factors: dy, which the first product has just read, is still in L2 for them
   // where it fits.
@@ -1539,7 +1547,7 @@ extern "C" dit_status dit_lora_backward(const dit_adapter_plan_t* plan, const in
       const char *d = reinterpret_cast<const char*>(dx), *i = reinterpret_cast<const char*>(in);
       return d + plan->rows * k * (dx_dt == DIT_BF16 ? 2 : 4) <= i || i + plan->rows * width * 2 <= d;
     };
-    return from_rank<true>(args_of(*plan, table, rank, ws), scratch, PARTS, a, dx, dx_dt, k, &o, apart(x, k) && apart(dy, n), st);
+    return from_rank<true>(plain, scratch, PARTS, a, dx, dx_dt, k, &o, apart(x, k) && apart(dy, n), st);
   }
   if (!o.whole && p.split.ctas > 1 &&
       launch_pdl(k_over_rows_sum, dim3((unsigned)sum_ctas), dim3(256), 0, st, 1, p, o) != cudaSuccess)
