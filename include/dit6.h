@@ -520,6 +520,146 @@ dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensor
                              dit_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Norms of query and key heads with the position rotation, and their gradients.
+ *
+ * Every head x (dim values) of q and of k, with w and b of the kind (query or key):
+ *   DIT_NORM_LAYER  n = (x - mean) r w + b,   r = (mean((x - mean)^2) + eps)^-1/2
+ *   DIT_NORM_RMS    n = x r w,                r = (mean(x^2) + eps)^-1/2
+ *   DIT_NORM_NONE   n = x
+ * and its rotation: pair p of the first 2 * pairs dimensions turns by the token's angle of p,
+ *   (y1, y2) = (n1 cos - n2 sin, n1 sin + n2 cos),
+ * the pair's dimensions being (2p, 2p + 1) if interleaved, else (p, p + pairs); dimensions behind
+ * them are not turned.  The angle of pair p is position[axis(p)] times the pair's frequency.  Frequencies
+ * are held in turns as 64-bit fractions, so an angle is exact modulo a turn to 2^-21 of a radian at
+ * every 32-bit position.  Sums are fp32; y is rounded once to bf16.
+ *   backward: with dn the gradient dy turned back, per parameter (sums over all tokens and heads)
+ *   dw = sum dn xhat, db = sum dn  (xhat = (x - mean) r), and
+ *   dx = r (g - mean(g) - xhat mean(g xhat)), g = dn w  (RMS: without mean(g)).
+ * The sums have a fixed order: a call with the same arguments gives the same bits.
+ *
+ * dit_heads_t views one tensor [tokens, heads, dim]: dims are contiguous, strides are in elements.
+ * ptr is 16-byte aligned and the strides multiples of 8 (DIT_ERR_ALIGNMENT); dim is a multiple of 8
+ * up to 256 (DIT_ERR_UNSUPPORTED).  A stride of a single token or head is not used.
+ *
+ * q, k      : device bf16; k NULL: queries alone (then k_out, dk_out and dk are NULL too).
+ * q_out, k_out: device bf16, may be the views q and k themselves; otherwise apart from what is read.
+ * params    : device float, rows of dim: (q_weight, q_bias, k_weight, k_bias) for the layer norm,
+ *             (q_weight, k_weight) for RMS; NULL without a norm.  4-byte aligned.
+ * rot       : dit_rotary_t (host struct) with the device table that dit_rotary_table lays out, or NULL: no
+ *             rotation.  positions: device int32 [tokens, axes].
+ * dq, dk    : device bf16, may be the views dq_out and dk_out themselves.
+ * dparams   : device float, the shape of params, overwritten; NULL: not wanted.
+ * scratch   : device buffer of dit_qk_norm_scratch_bytes(dim), 16-byte aligned, contents free; calls
+ *             ordered on one stream may share it (only needed with dparams).
+ * ------------------------------------------------------------------------------------ */
+#define DIT_NORM_NONE 0
+#define DIT_NORM_RMS 1
+#define DIT_NORM_LAYER 2
+#define DIT_MAX_AXES 4
+typedef struct {
+  const void* ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t heads;
+  int32_t reserved;
+} dit_heads_t;
+typedef struct {
+  const void* table; /* device: 16 bytes a pair */
+  int32_t pairs;
+  int32_t axes;
+  int32_t interleaved;
+  int32_t reserved;
+} dit_rotary_t;
+
+/* Host: the table of a rotation.  dims [axes]: even numbers of dimensions of each axis, in the pairs'
+ * order; index i of axis a's pairs has the frequency scale[a] * theta^(-2 i / dims[a]) radians a
+ * position.  table: sum(dims) / 2 entries of 16 bytes. */
+dit_status dit_rotary_table(const int32_t* dims, int axes, double theta, const double* scale, void* table,
+                            size_t table_bytes);
+size_t dit_qk_norm_scratch_bytes(int dim);
+dit_status dit_qk_norm_rope(const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* q_out,
+                            const dit_heads_t* k_out, int64_t tokens, int dim, int norm,
+                            const float* params, double eps, const dit_rotary_t* rot,
+                            const int32_t* positions, dit_stream_t stream);
+dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* dq_out,
+                                     const dit_heads_t* dk_out, const dit_heads_t* dq,
+                                     const dit_heads_t* dk, int64_t tokens, int dim, int norm,
+                                     const float* params, double eps, const dit_rotary_t* rot,
+                                     const int32_t* positions, float* dparams, void* scratch,
+                                     size_t scratch_bytes, void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Softmax attention over documents packed in one batch, and its gradients.
+ *
+ *   s = scale q k^T,  o = sum p v,  p = exp(s - lse),  lse = log sum exp(s), over the keys a query sees
+ *   delta = sum over dim of do o;  ds = p (do v^T - delta);
+ *   dq = scale ds k,  dk = scale ds^T q,  dv = p^T do
+ * A document has `queries` query tokens, consecutive in the batch, and `keys` key tokens from key row
+ * `begin` on (keys in place, or a cache with room behind them); its queries are the last tokens of its
+ * keys.  frame == 0: a query sees every key of its document.  frame > 0: token number t of the document
+ * (t = index + keys - queries) sees the first `prefix` keys if t < prefix, else those and the frames of
+ * `frame` tokens behind them up to its own (frame 1: causal); t < 0 sees none.  A query that sees
+ * no key gets o = 0 and passes no gradient.  Query head h uses key head h / (heads / kv_heads).
+ * Operands enter the tensor cores in bf16 (p and ds are rounded to bf16), sums are fp32; outputs are
+ * rounded once.  All sums have a fixed order (no atomics on values): a call with the same arguments
+ * gives the same bits.  What a document's tokens hold reaches no other document's results, nor
+ * does what lies in rows of no document (NaN included); rows of no document are not written.
+ *
+ * The plan.  dit_attention_plan (host, no device work) cuts the documents into work for the kernels; a plan
+ * serves every block and step with the same batch.  Call it with table = NULL to learn the sizes,
+ * then with a host buffer of table_ints int32, and copy the table to the device (16-byte aligned).
+ *   queries, keys : host int64 [documents].   begins : host int64 [documents], or NULL: packed in order.
+ *   prefix : host int64 [documents], or NULL: none.   training : 1 for plans that the backward pass takes:
+ *   there no key row belongs to two documents (DIT_ERR_INVALID_ARG).
+ *   heads, kv_heads: heads % kv_heads == 0, heads up to 4096; dim: a multiple of 8 up to 128.
+ * The kernels check the table's entries against the plan: a wrong one is skipped and raises
+ * DIT_ERR_INVALID_ARG in the device status word.
+ *
+ * q, out, dout, dq : views of [query rows, heads, dim], at least plan->q_rows rows.
+ * k, v, dk, dv     : views of [key rows, kv_heads, dim], at least plan->k_rows rows.
+ *                    bf16; dims contiguous, pointers 16-byte aligned, strides multiples of 8 below 2^31
+ *                    elements.  Outputs are apart from everything that is read.
+ * scale   : finite and > 0.
+ * saved   : device buffer of plan->saved_bytes, 16-byte aligned, that the forward pass fills for
+ *           the backward pass (training plans; otherwise NULL).
+ * scratch : device buffer of plan->scratch_bytes, 16-byte aligned, contents free; calls ordered on one
+ *           stream may share it.
+ * ------------------------------------------------------------------------------------ */
+#define DIT_ATTENTION_LISTS 4
+#define DIT_ATTENTION_BUCKETS 32
+typedef struct {
+  int64_t q_rows;        /* query tokens */
+  int64_t k_rows;        /* 1 + the last key row that a document has */
+  int64_t padded_rows;   /* query rows with each document rounded up to 128 */
+  int64_t table_ints;
+  int64_t saved_bytes;
+  int64_t scratch_bytes;
+  int32_t documents;
+  int32_t heads, kv_heads, dim;
+  int32_t frame;
+  int32_t training;
+  int32_t slots;         /* partial results of a head */
+  int32_t items[DIT_ATTENTION_LISTS]; /* forward, joins, gradient of queries, gradients of keys */
+  int32_t buckets[DIT_ATTENTION_LISTS]; /* runs of items of like cost, in the table */
+  int32_t reserved;
+} dit_attention_plan_t;
+
+dit_status dit_attention_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins,
+                              const int64_t* prefix, int64_t documents, int64_t frame, int heads,
+                              int kv_heads, int dim, int training, dit_attention_plan_t* plan,
+                              int32_t* table, int64_t table_ints);
+dit_status dit_attention(const dit_attention_plan_t* plan, const int32_t* table_dev, const dit_heads_t* q,
+                         const dit_heads_t* k, const dit_heads_t* v, const dit_heads_t* out, double scale,
+                         void* saved, size_t saved_bytes, void* scratch, size_t scratch_bytes, void* ws,
+                         size_t ws_bytes, dit_stream_t stream);
+dit_status dit_attention_backward(const dit_attention_plan_t* plan, const int32_t* table_dev,
+                                  const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* v,
+                                  const dit_heads_t* out, const dit_heads_t* dout, const dit_heads_t* dq,
+                                  const dit_heads_t* dk, const dit_heads_t* dv, double scale,
+                                  const void* saved, size_t saved_bytes, void* scratch,
+                                  size_t scratch_bytes, void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Block-scale tile layout helpers (host).  The scales of a [rows x k] NVFP4 tensor are
  * cut into atoms of 128 rows x 4 scale columns (512 bytes), ordered with the scale-column
  * atom index fastest; inside an atom row r, column c is at (r%32)*16 + ((r%128)/32)*4 +

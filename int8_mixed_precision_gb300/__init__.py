@@ -615,7 +615,9 @@ class DeltaCachedBlock:
 
 _LATER = {**dict.fromkeys(("AdapterPlan", "AdapterBank", "AdaptedLinear", "adapter_scratch", "adapter_saved",
                            "lora_forward", "lora_backward"), "adapters"),
-          **dict.fromkeys(("AdamW", "adamw_moments"), "optim")}
+          **dict.fromkeys(("AdamW", "adamw_moments"), "optim"),
+          **dict.fromkeys(("Rotary", "QKNorm", "qk_norm_scratch", "qk_norm_rope", "qk_norm_rope_backward", "AttentionPlan",
+                           "attention_scratch", "attention_saved", "attention", "attention_backward", "RoutedAttention"), "block_attention")}
 
 
 def __getattr__(name):

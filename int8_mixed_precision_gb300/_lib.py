@@ -62,6 +62,14 @@ SIGNATURES = {
     "dit_adamw_chunks": (_i64, [_vp, _i64, _vp, _i64]),
     "dit_adamw_step": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "dit_adamw_moments": (_i32, [_vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "dit_rotary_table": (_i32, [_vp, _i32, ctypes.c_double, _vp, _vp, _sz]),
+    "dit_qk_norm_scratch_bytes": (_sz, [_i32]),
+    "dit_qk_norm_rope": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, ctypes.c_double, _vp, _vp, _vp]),
+    "dit_qk_norm_rope_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, ctypes.c_double, _vp, _vp, _vp, _vp, _sz, _vp, _sz,
+                                         _vp]),
+    "dit_attention_plan": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64]),
+    "dit_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_double, _vp, _sz, _vp, _sz, _vp, _sz, _vp]),
+    "dit_attention_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_double, _vp, _sz, _vp, _sz, _vp, _sz, _vp]),
     "dit_sf_index": (_i64, [_i64, _i64, _i64, _i64]),
     "dit_sf_bytes": (_sz, [_i64, _i64]),
 }

@@ -96,6 +96,19 @@ bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_heads(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads, uint64_t rows, uint64_t head_bytes,
+                       uint64_t row_bytes, uint32_t box_heads, uint32_t box_rows) {
+  encode_tiled_fn fn = get_encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {dim, heads, rows};
+  cuuint64_t strides[2] = {head_bytes, row_bytes};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dit6
 
 extern "C" {

@@ -1,0 +1,209 @@
+// What the files of the attention share: the plan's table, which keys a query sees, and the instructions of
+// one CTA that the adapters' files do not have.
+#pragma once
+
+#include "adapters.cuh"
+
+namespace dit6 {
+namespace attn {
+
+constexpr int TILE = 128;                 // rows of the stationary operand: the M of one instruction
+constexpr int MAX_DIM = 128;
+constexpr int MAX_HEADS = 4096;
+constexpr int MAX_GROUP = 128;            // query heads to a key head
+constexpr int64_t MAX_ROWS = 0x7fffff00;
+constexpr int64_t MAX_DOCUMENTS = 1 << 22;
+enum List { FORWARD, JOIN, GRAD_Q, GRAD_KV };
+
+// The head's dimensions as the tensor cores see them (columns behind dim are zeros that TMA fills in), and the
+// streamed operand's rows to a tile: as many as tensor memory holds beside the accumulators.
+__host__ __device__ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int tile_cols(int dim) { return dim <= 64 ? 128 : 64; }
+
+// The table, in int32: documents of DOC_INTS, items of ITEM_INTS (the four lists behind one another), and
+// DIT_ATTENTION_BUCKETS pairs (first item, items) for each list.
+constexpr int DOC_INTS = 8, ITEM_INTS = 8;
+struct Doc {
+  int32_t q0, queries, k0, keys, prefix;
+  int32_t tile0;  // its first padded row / 128
+  int32_t unused[2];
+};
+struct Item {
+  int32_t doc, row0;    // rows of the document: queries, or keys (GRAD_KV)
+  int32_t begin, end;   // tiles of the streamed operand; JOIN: the first partial row, the pieces
+  int32_t slot;         // FORWARD: the first partial row, -1: the output itself; JOIN: the rows
+  int32_t unused[3];
+};
+static_assert(sizeof(Doc) == 4 * DOC_INTS && sizeof(Item) == 4 * ITEM_INTS, "");
+__host__ __device__ inline int64_t first_item(const dit_attention_plan_t& p, int list) {
+  int64_t n = 0;
+  for (int i = 0; i < list; ++i) n += p.items[i];
+  return (int64_t)DOC_INTS * p.documents + ITEM_INTS * n;
+}
+__host__ __device__ inline int64_t first_bucket(const dit_attention_plan_t& p, int list) {
+  return first_item(p, DIT_ATTENTION_LISTS) + (int64_t)list * 2 * DIT_ATTENTION_BUCKETS;
+}
+
+// The keys [0, end) that query `row` of a document sees, and the first query that sees key `key` (monotone both).
+__host__ __device__ inline int64_t seen_end(const Doc& d, int64_t frame, int64_t row) {
+  if (frame == 0) return d.keys;
+  const int64_t t = row + d.keys - d.queries;
+  if (t < 0) return 0;
+  const int64_t e = t < d.prefix ? (int64_t)d.prefix : d.prefix + ((t - d.prefix) / frame + 1) * frame;
+  return e < d.keys ? e : d.keys;
+}
+__host__ __device__ inline int64_t seen_from(const Doc& d, int64_t frame, int64_t key) {
+  if (frame == 0) return 0;
+  const int64_t t = key < d.prefix ? 0 : d.prefix + (key - d.prefix) / frame * frame;
+  const int64_t row = t - ((int64_t)d.keys - d.queries);
+  return row < 0 ? 0 : row;
+}
+
+// Query heads of one key head share a forward tile: its rows are (query, head of the group), so that a key's
+// tile is read once for all of them.
+__host__ __device__ inline int rows_per_tile(int group) { return TILE / group; }
+
+// A tensor of heads, strides in elements.
+struct Heads {
+  __nv_bfloat16* ptr;
+  int64_t row, head;
+};
+
+// What a CTA works at: the item and the head of its index in the list's order.  Items of like cost are a bucket, the
+// costliest first; within one a head's items follow one another and share its keys in L2.
+struct Work {
+  Doc doc;
+  Item item;
+  int head;
+  bool ok;
+};
+__device__ __forceinline__ Work find_work(const int32_t* table, const dit_attention_plan_t& p, int list, int heads, void* ws) {
+  Work w;
+  w.ok = false;
+  const int2* bucket = reinterpret_cast<const int2*>(table + first_bucket(p, list));
+  const int64_t at = blockIdx.x;
+  for (int b = 0; b < p.buckets[list]; ++b) {
+    const int2 v = __ldg(bucket + b);
+    if (at < (int64_t)(v.x + v.y) * heads && at >= (int64_t)v.x * heads && v.y > 0) {
+      const int r = (int)(at - (int64_t)v.x * heads);
+      w.head = r / v.y;
+      const int i = v.x + r % v.y;
+      if (i < 0 || i >= p.items[list] || w.head >= heads) break;
+      const int4* it = reinterpret_cast<const int4*>(table + first_item(p, list)) + 2 * (int64_t)i;
+      const int4 a = __ldg(it), c = __ldg(it + 1);
+      w.item = Item{a.x, a.y, a.z, a.w, c.x, {0, 0, 0}};
+      if (a.x < 0 || a.x >= p.documents) break;
+      const int4* dt = reinterpret_cast<const int4*>(table) + 2 * (int64_t)a.x;
+      const int4 d0 = __ldg(dt), d1 = __ldg(dt + 1);
+      w.doc = Doc{d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, {0, 0}};
+      const Doc& d = w.doc;
+      w.ok = d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 &&
+             (int64_t)d.k0 + d.keys <= p.k_rows && d.prefix >= 0 && d.tile0 >= 0 &&
+             (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.item.row0 >= 0 && w.item.begin >= 0;
+      break;
+    }
+  }
+  if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
+  return w;
+}
+
+bool plan_ok(const dit_attention_plan_t* p);
+dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, Heads* o);
+bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows);
+
+// ---------------------------------------------------------------------------------------
+// A CTA of three warpgroups: one loads and issues, two hold a tile's rows in registers and take over most of the first
+// one's.  The block is launched with 3 x LAUNCH_REGS registers a thread and the shares add up to those:
+// taking more than the launch brought would wait for ever, so the host checks what the kernel was compiled to.
+// ---------------------------------------------------------------------------------------
+constexpr int THREADS = 384;
+constexpr int LAUNCH_REGS = 168, ISSUE_REGS = 72, ROW_REGS = 216;
+static_assert(ISSUE_REGS + 2 * ROW_REGS <= 3 * LAUNCH_REGS, "");
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE_REGS)); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROW_REGS)); }
+template <typename... KArgs>
+cudaError_t prepare_kernel(OncePerDevice& once, void (*kern)(KArgs...), int smem) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  return once.run(device, [&] {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs != LAUNCH_REGS) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+}
+
+// ---------------------------------------------------------------------------------------
+// device helpers
+// ---------------------------------------------------------------------------------------
+// D += A B with A in tensor memory (its 16 bf16 of a step are eight columns)
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %4, 0; mov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(lora::DESC_HI)
+      : "memory");
+}
+// 32 accumulator columns of this thread's row; complete after lora::tmem_wait() and pin()
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+  static_assert(N % 8 == 0, "");
+#pragma unroll
+  for (int i = 0; i < N; i += 8) lora::pin8(r + i);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Columns of a tile outside [lo, hi) become -infinity.
+template <int N>
+__device__ __forceinline__ void mask_cols(uint32_t (&s)[N], int first, int64_t lo, int64_t hi) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (first + i < lo || first + i >= hi) s[i] = 0xff800000u;
+}
+// Zeroes rows [from, rows) of a tile of 64-column chunks in shared memory (a row of a chunk is 128 bytes, whatever the
+// swizzle), by a whole warp: what lies behind a document's end must not meet the zeros of p or ds in a product, which
+// NaN or infinity would turn into NaN.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int chunk_bytes, int chunks, int from, int rows) {
+  for (int c = 0; c < chunks; ++c)
+    for (int i = from * 128 + (threadIdx.x & 31) * 16; i < rows * 128; i += 512)
+      lora::sts128(tile + c * chunk_bytes + i, make_uint4(0, 0, 0, 0));
+  fence_proxy_async();
+  __syncwarp();
+}
+// Eight columns of fp32 as bf16, 16 bytes.
+__device__ __forceinline__ uint4 pack8(const uint32_t* r, float f) {
+  const float* v = reinterpret_cast<const float*>(r);
+  return make_uint4(f2_to_bf16x2(v[0] * f, v[1] * f), f2_to_bf16x2(v[2] * f, v[3] * f), f2_to_bf16x2(v[4] * f, v[5] * f),
+                    f2_to_bf16x2(v[6] * f, v[7] * f));
+}
+
+}  // namespace attn
+}  // namespace dit6

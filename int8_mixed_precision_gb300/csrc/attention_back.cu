@@ -1,0 +1,437 @@
+// Attention, backward: dq = scale ds k, dk = scale ds^T q, dv = p^T do, with p = exp(s - lse), ds = p (do v^T - delta),
+// delta = sum over dim of do o.
+//
+// Two kernels of one form, so that every gradient is a sum in a fixed order that ends in one rounding: neither atomics
+// nor an fp32 copy of dq in memory.  The price is that s and do v^T are made twice, seven products instead of five.  A CTA
+// keeps 128 rows of a pair (X1, X2) and streams tiles of a pair (Y1, Y2):
+//
+//   S = X1 Y1^T,  T = X2 Y2^T,  ds = p (T - delta),  A += ds Y1,  B += p Y2
+//
+//   queries stay: X = (q, do), Y = (k, v):  A = dq / scale
+//   keys stay:    X = (k, v), Y = (q, do):  A = dk / scale, B = dv; S, T, p and ds are the transposed ones, and the
+//                                           queries of all heads that share the keys pass by
+//
+// S and T lie in tensor memory; p and ds go back there in bf16 as A operands of the next products (each rounding at most 2^-8 of its
+// value), so nothing but the streamed tiles passes through shared memory.  The next tile's S and T are made while the
+// warps work at the present one's.  Two warpgroups share a tile's columns.
+#include <math.h>
+
+#include "attention.cuh"
+
+namespace dit6 {
+namespace attn {
+
+using namespace lora;
+
+constexpr int BACK_STAGES = 5;  // most
+
+template <int PD>
+struct Back {
+  static constexpr int COLS = tile_cols(PD);
+  static constexpr int CHUNKS = PD / 64;
+  static constexpr int X_CHUNK = TILE * 128, X_BYTES = CHUNKS * X_CHUNK;
+  static constexpr int Y_CHUNK = COLS * 128, Y_BYTES = CHUNKS * Y_CHUNK;
+  static constexpr int STAGES = PD == 64 ? 5 : 4;
+  static constexpr int STATS = 2 * X_BYTES + 2 * STAGES * Y_BYTES;  // lse and delta of a stage's columns
+  static constexpr int STAT_BYTES = 2 * COLS * 4;
+  static constexpr int CONTROL = STATS + STAGES * STAT_BYTES;
+  static constexpr int SMEM = CONTROL + 1024 + 1024;
+  static constexpr uint32_t S = 0, T = COLS, P = 2 * COLS, DS = P + COLS / 2, A = 3 * COLS, B = A + PD;
+  static_assert(3 * COLS + 2 * PD <= 512 && SMEM <= 227 * 1024, "");
+};
+
+struct BackControl {
+  uint64_t xfull, done, sfull, sfree, pready, pdone;
+  uint64_t yfull[BACK_STAGES], yempty[BACK_STAGES];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(BackControl) <= 1024, "");
+
+struct BackArgs {
+  dit_attention_plan_t plan;
+  const int32_t* table;
+  const float* lse;   // [heads][padded rows], in base 2
+  float* delta;       // the same
+  Heads out, dout;
+  Heads a, b;         // dq; dk and dv
+  void* ws;
+  float c, scale;     // scale log2(e); scale
+  int group;
+  int stall;
+};
+
+// delta of 128 queries of a head, sixteen bytes to a lane.
+__global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__ BackArgs p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const Work w = find_work(p.table, p.plan, GRAD_Q, p.plan.heads, p.ws);
+  if (!w.ok) return;
+  const int lane = threadIdx.x % 16, dim = p.plan.dim;
+  for (int r = threadIdx.x / 16; r < TILE; r += 16) {
+    const int64_t row = (int64_t)w.item.row0 + r;
+    const bool mine = row < w.doc.queries;
+    float sum = 0.f;
+    if (mine && 8 * lane < dim) {
+      const int64_t at = w.doc.q0 + row;
+      const uint4 o = __ldg(reinterpret_cast<const uint4*>(p.out.ptr + at * p.out.row + w.head * p.out.head + 8 * lane));
+      const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.dout.ptr + at * p.dout.row + w.head * p.dout.head + 8 * lane));
+      const uint32_t a[4] = {o.x, o.y, o.z, o.w}, b[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = bf16x2_to_f2(a[i]), y = bf16x2_to_f2(b[i]);
+        sum += x.x * y.x + x.y * y.y;
+      }
+    }
+#pragma unroll
+    for (int i = 8; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    // the rows that pad a document to whole tiles are written too
+    if (lane == 0) p.delta[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = sum;
+  }
+}
+
+template <int PD, bool KEYS>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_attention_back(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
+                     const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2, const __grid_constant__ BackArgs p) {
+  pdl_launch_dependents();
+  using F = Back<PD>;
+  constexpr int COLS = F::COLS, HALF = COLS / 2;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t smem = smem_u32(base);
+  BackControl* c = reinterpret_cast<BackControl*>(base + F::CONTROL);
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+  if (warp == 0) {
+    if (lane < F::STAGES) {
+      mbar_init(smem_u32(&c->yfull[lane]), 1);
+      mbar_init(smem_u32(&c->yempty[lane]), 1);
+    } else if (lane == 8) {
+      mbar_init(smem_u32(&c->xfull), 1);
+      mbar_init(smem_u32(&c->done), 1);
+      mbar_init(smem_u32(&c->sfull), 1);
+      mbar_init(smem_u32(&c->sfree), 8);
+      mbar_init(smem_u32(&c->pready), 8);
+      mbar_init(smem_u32(&c->pdone), 1);
+      c->abort = 0;
+    }
+    fence_barrier_init();
+    __syncwarp();
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(&c->tmem), 512);
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = c->tmem;
+  volatile int* abort = &c->abort;
+  pdl_wait();
+
+  const Work w = find_work(p.table, p.plan, KEYS ? GRAD_KV : GRAD_Q, KEYS ? p.plan.kv_heads : p.plan.heads, p.ws);
+  const Doc& d = w.doc;
+  const int row0 = w.item.row0;
+  const int x_rows = KEYS ? d.keys : d.queries, y_rows = KEYS ? d.queries : d.keys;  // of the document
+  const int x0 = KEYS ? d.k0 : d.q0, y0 = KEYS ? d.q0 : d.k0;
+  const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
+  const int n = tiles * (KEYS ? p.group : 1);
+  // tile j of the stream: its first row in the document, and the head it belongs to
+  auto y_row = [&](int j) { return (w.item.begin + (KEYS ? j % tiles : j)) * COLS; };
+  auto q_head = [&](int j) { return KEYS ? w.head * p.group + j / tiles : w.head; };
+
+  if (warp < 4) give_registers();
+  if (warp == 0) {
+    if (n > 0 && elect_one()) {
+      uint32_t ny = 0;
+      bool ok = true;
+      if (!p.stall) {
+        mbar_expect_tx(smem_u32(&c->xfull), 2 * F::X_BYTES);
+        for (int i = 0; i < 2; ++i)
+          for (int k = 0; k < F::CHUNKS; ++k)
+            tma_load_3d(smem + i * F::X_BYTES + k * F::X_CHUNK, i ? &mx2 : &mx1, smem_u32(&c->xfull), k * 64, w.head, x0 + row0);
+      }
+      for (int j = 0; j < n; ++j) {
+        const int s = j % F::STAGES;
+        if (j >= F::STAGES && !mbar_wait(smem_u32(&c->yempty[s]), ((j / F::STAGES) - 1) & 1, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        if (p.stall) continue;
+        const uint32_t full = smem_u32(&c->yfull[s]);
+        const int row = y_row(j), head = q_head(j);
+        mbar_expect_tx(full, 2 * F::Y_BYTES + (KEYS ? F::STAT_BYTES : 0));
+        for (int i = 0; i < 2; ++i)
+          for (int k = 0; k < F::CHUNKS; ++k)
+            tma_load_3d(smem + 2 * F::X_BYTES + (i * F::STAGES + s) * F::Y_BYTES + k * F::Y_CHUNK, i ? &my2 : &my1, full, k * 64,
+                        KEYS ? head : w.head / p.group, y0 + row);
+        if (KEYS) {
+          const int64_t at = (int64_t)head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
+          bulk_load(smem + F::STATS + s * F::STAT_BYTES, p.lse + at, COLS * 4, full);
+          bulk_load(smem + F::STATS + s * F::STAT_BYTES + COLS * 4, p.delta + at, COLS * 4, full);
+        }
+        ++ny;
+      }
+      if (!ok || *abort) {  // its own copies land before the CTA ends
+        volatile int never = 0;
+        if (!p.stall) mbar_wait(smem_u32(&c->xfull), 0, p.ws, &never);
+        for (uint32_t i = ny > F::STAGES ? ny - F::STAGES : 0; i < ny; ++i) mbar_wait(smem_u32(&c->yfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
+      }
+    }
+  } else if (warp == 1) {
+    if (n > 0) {
+      const uint32_t id_s = idesc(128, COLS, false, false);
+      const uint32_t id_a = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
+      const int steps = (p.plan.dim + 15) / 16;
+      bool ok = warp_wait(smem_u32(&c->xfull), 0, p.ws, abort);
+      auto y_at = [&](int j, int i) { return smem + 2 * F::X_BYTES + (i * F::STAGES + j % F::STAGES) * F::Y_BYTES; };
+      auto scores = [&](int j) {  // S and T of tile j
+        ok = ok && warp_wait(smem_u32(&c->yfull[j % F::STAGES]), (j / F::STAGES) & 1, p.ws, abort);
+        if (!ok) return;
+        const int left = y_rows - y_row(j);
+        if (left < COLS)
+          for (int i = 0; i < 2; ++i) zero_rows(y_at(j, i), F::Y_CHUNK, F::CHUNKS, left, COLS);
+        if (j > 0) ok = warp_wait(smem_u32(&c->sfree), (j - 1) & 1, p.ws, abort);
+        if (!ok) return;
+        fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a = desc_k(smem + i * F::X_BYTES), b = desc_k(y_at(j, i));
+#pragma unroll
+            for (int k = 0; k < PD / 16; ++k)
+              if (k < steps)
+                mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id_s, k > 0);
+          }
+          mma_commit(smem_u32(&c->sfull));
+        }
+        __syncwarp();
+      };
+      scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) scores(j + 1);
+        ok = ok && warp_wait(smem_u32(&c->pready), j & 1, p.ws, abort);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          const uint32_t y1 = desc_mn(y_at(j, 0), F::Y_CHUNK), y2 = desc_mn(y_at(j, 1), F::Y_CHUNK);
+          if (KEYS) {
+#pragma unroll
+            for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::B, tmem + F::P + k * 8, y2 + k * (2048 >> 4), id_a, j > 0 || k > 0);
+          }
+#pragma unroll
+          for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::A, tmem + F::DS + k * 8, y1 + k * (2048 >> 4), id_a, j > 0 || k > 0);
+          mma_commit(smem_u32(&c->pdone));
+          mma_commit(smem_u32(&c->yempty[j % F::STAGES]));
+        }
+        __syncwarp();
+      }
+      volatile int never = 0;
+      if (elect_one()) mma_commit(smem_u32(&c->done));
+      __syncwarp();
+      warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+    }
+  } else if (warp >= 4) {
+    take_registers();
+    const int half = (warp - 4) / 4;
+    const int r = (warp % 4) * 32 + lane;
+    const int row = row0 + r;
+    const bool live = w.ok && row < x_rows;
+    const uint32_t at = tmem + ((uint32_t)(warp % 4) << 21);
+    // the columns that this row meets; rows behind the last one: whatever they hold is not stored
+    int64_t lo = 0, hi = INT64_MAX;
+    if (live && KEYS) {
+      lo = seen_from(d, p.plan.frame, row);
+      hi = d.queries;
+    } else if (live) {
+      hi = seen_end(d, p.plan.frame, row);
+    }
+    float lse = 0.f, delta = 0.f;
+    if (!KEYS && live) {
+      const int64_t i = (int64_t)w.head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
+      lse = p.lse[i];
+      delta = p.delta[i];
+    }
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = warp_wait(smem_u32(&c->sfull), j & 1, p.ws, abort);
+      if (!ok) break;
+      fence_after();
+      uint32_t s[HALF], g[HALF];
+#pragma unroll
+      for (int k = 0; k < HALF; k += 32) {
+        tmem_ld32(at + F::S + half * HALF + k, s + k);
+        tmem_ld32(at + F::T + half * HALF + k, g + k);
+      }
+      tmem_wait();
+      pin(s);
+      pin(g);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c->sfree));
+      const int col0 = y_row(j) + half * HALF;
+      const bool whole = __all_sync(0xffffffffu, lo <= col0 && hi >= (int64_t)col0 + HALF);
+      const uint32_t stats = smem + F::STATS + (j % F::STAGES) * F::STAT_BYTES + half * HALF * 4;
+      uint32_t pk[HALF / 2], dk[HALF / 2];
+      const float2 c2 = make_float2(p.c, p.c);
+      float l4[4] = {lse, lse, lse, lse}, d4[4] = {delta, delta, delta, delta};
+#pragma unroll
+      for (int i = 0; i < HALF; i += 4) {
+        if (KEYS) {  // the columns' own
+          const uint4 l = lds128(stats + i * 4), d = lds128(stats + COLS * 4 + i * 4);
+          l4[0] = __uint_as_float(l.x), l4[1] = __uint_as_float(l.y), l4[2] = __uint_as_float(l.z), l4[3] = __uint_as_float(l.w);
+          d4[0] = __uint_as_float(d.x), d4[1] = __uint_as_float(d.y), d4[2] = __uint_as_float(d.z), d4[3] = __uint_as_float(d.w);
+        }
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[i + h]), __uint_as_float(s[i + h + 1])), c2, make_float2(-l4[h], -l4[h + 1]));
+          const float2 t = sub2(make_float2(__uint_as_float(g[i + h]), __uint_as_float(g[i + h + 1])), make_float2(d4[h], d4[h + 1]));
+          s[i + h] = __float_as_uint(exp2_approx(x.x));
+          s[i + h + 1] = __float_as_uint(exp2_approx(x.y));
+          g[i + h] = __float_as_uint(t.x);
+          g[i + h + 1] = __float_as_uint(t.y);
+        }
+      }
+      if (!whole) {  // masked pairs: p and ds are zero, whatever was there
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+          if (col0 + i < lo || col0 + i >= hi) s[i] = g[i] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < HALF / 2; ++i) {
+        const float2 e = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        const float2 t = mul2(e, make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1])));
+        if (KEYS) pk[i] = f2_to_bf16x2(e.x, e.y);
+        dk[i] = f2_to_bf16x2(t.x, t.y);
+      }
+      if (j > 0) {
+        ok = warp_wait(smem_u32(&c->pdone), (j - 1) & 1, p.ws, abort);
+        if (!ok) break;
+        fence_after();
+      }
+#pragma unroll
+      for (int k = 0; k < HALF / 2; k += 16) {
+        if (KEYS) tmem_st16(at + F::P + half * (HALF / 2) + k, pk + k);
+        tmem_st16(at + F::DS + half * (HALF / 2) + k, dk + k);
+      }
+      tmem_st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c->pready));
+    }
+    if (n > 0 && ok) {
+      ok = warp_wait(smem_u32(&c->pdone), (n - 1) & 1, p.ws, abort);
+      fence_after();
+    }
+    if (ok) {
+#pragma unroll
+      for (int out = 0; out < (KEYS ? 2 : 1); ++out) {
+        const Heads& to = out ? p.b : p.a;
+        const float f = out ? 1.f : p.scale;
+#pragma unroll
+        for (int k = half * (PD / 2); k < (half + 1) * (PD / 2); k += 32) {
+          uint32_t o[32];
+          tmem_ld32(at + (out ? F::B : F::A) + k, o);
+          tmem_wait();
+          pin(o);
+          if (n == 0)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          if (live) {
+            __nv_bfloat16* dst = to.ptr + (int64_t)(x0 + row) * to.row + w.head * to.head + k;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (k + i < p.plan.dim) *reinterpret_cast<uint4*>(dst + i) = pack8(o + i, f);
+          }
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+struct Inputs {
+  Heads q, k, v, dout;
+};
+
+template <int PD, bool KEYS>
+static dit_status launch(BackArgs a, const Inputs& in, cudaStream_t st) {
+  using F = Back<PD>;
+  static OncePerDevice once;
+  const dit_attention_plan_t& p = a.plan;
+  const int items = p.items[KEYS ? GRAD_KV : GRAD_Q], heads = KEYS ? p.kv_heads : p.heads;
+  if (!items) return DIT_OK;
+  // Without queries or without keys nothing is loaded: any tensor makes a map.
+  const bool q_any = p.q_rows > 0, k_any = p.k_rows > 0;
+  auto map = [&](CUtensorMap* m, const Heads& own, const Heads& other, bool query, int rows) {
+    const bool mine = query ? q_any : k_any, of_query = mine ? query : !query;
+    return map_heads(m, mine ? own : other, p.dim, of_query ? p.heads : p.kv_heads, of_query ? p.q_rows : p.k_rows, 1, rows);
+  };
+  CUtensorMap mq, mo, mk, mv;
+  const int q_box = KEYS ? F::COLS : TILE, k_box = KEYS ? TILE : F::COLS;
+  if (!map(&mq, in.q, in.k, true, q_box) || !map(&mo, in.dout, in.v, true, q_box) || !map(&mk, in.k, in.q, false, k_box) || !map(&mv, in.v, in.dout, false, k_box))
+    return DIT_ERR_CUDA;
+  if (prepare_kernel(once, k_attention_back<PD, KEYS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  const cudaError_t e = KEYS ? launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mk, mv, mq, mo, a)
+                             : launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mq, mo, mk, mv, a);
+  return e == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+}
+
+template <int PD>
+static dit_status backward(BackArgs a, const Inputs& in, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
+  if (a.plan.items[GRAD_Q] &&
+      launch_pdl(k_attention_delta, dim3((unsigned)(a.plan.items[GRAD_Q] * a.plan.heads)), dim3(256), 0, st, 1, a) != cudaSuccess)
+    return DIT_ERR_CUDA;
+  a.a = dq;
+  const dit_status e = launch<PD, false>(a, in, st);
+  if (e != DIT_OK) return e;
+  a.a = dk;
+  a.b = dv;
+  return launch<PD, true>(a, in, st);
+}
+
+}  // namespace attn
+}  // namespace dit6
+
+using namespace dit6;
+
+extern "C" dit_status dit_attention_backward(const dit_attention_plan_t* plan, const int32_t* table, const dit_heads_t* q,
+                                             const dit_heads_t* k, const dit_heads_t* v, const dit_heads_t* out,
+                                             const dit_heads_t* dout, const dit_heads_t* dq, const dit_heads_t* dk,
+                                             const dit_heads_t* dv, double scale, const void* saved, size_t saved_bytes,
+                                             void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes,
+                                             dit_stream_t stream) {
+  using namespace attn;
+  if (!plan_ok(plan) || !table || !ws || ws_bytes < WS_BYTES || !(scale > 0.0) || !isfinite(scale) || !plan->training) return DIT_ERR_INVALID_ARG;
+  if (saved_bytes < (size_t)plan->saved_bytes || (plan->saved_bytes && !saved)) return DIT_ERR_INVALID_ARG;
+  if (scratch_bytes < (size_t)plan->scratch_bytes || (plan->scratch_bytes && !scratch)) return DIT_ERR_INVALID_ARG;
+  BackArgs a = {};
+  Inputs in;
+  Heads hdq, hdk, hdv;
+  const int h = plan->heads, hk = plan->kv_heads, dim = plan->dim;
+  dit_status e = check_view(q, h, plan->q_rows, dim, &in.q);
+  if (e == DIT_OK) e = check_view(k, hk, plan->k_rows, dim, &in.k);
+  if (e == DIT_OK) e = check_view(v, hk, plan->k_rows, dim, &in.v);
+  if (e == DIT_OK) e = check_view(out, h, plan->q_rows, dim, &a.out);
+  if (e == DIT_OK) e = check_view(dout, h, plan->q_rows, dim, &a.dout);
+  if (e == DIT_OK) e = check_view(dq, h, plan->q_rows, dim, &hdq);
+  if (e == DIT_OK) e = check_view(dk, hk, plan->k_rows, dim, &hdk);
+  if (e == DIT_OK) e = check_view(dv, hk, plan->k_rows, dim, &hdv);
+  if (e != DIT_OK) return e;
+  if (!aligned32(ws) || (reinterpret_cast<uintptr_t>(table) & 15) || (reinterpret_cast<uintptr_t>(saved) & 15) || (reinterpret_cast<uintptr_t>(scratch) & 15))
+    return DIT_ERR_ALIGNMENT;
+  in.dout = a.dout;
+  a.plan = *plan;
+  a.table = table;
+  a.lse = reinterpret_cast<const float*>(saved);
+  a.delta = reinterpret_cast<float*>(scratch);
+  a.ws = ws;
+  a.c = (float)(scale * 1.4426950408889634);
+  a.scale = (float)scale;
+  a.group = h / hk;
+  a.stall = test_stall();
+  return dim <= 64 ? backward<64>(a, in, hdq, hdk, hdv, stream) : backward<128>(a, in, hdq, hdk, hdv, stream);
+}

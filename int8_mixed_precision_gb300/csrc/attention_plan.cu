@@ -1,0 +1,241 @@
+// Host side of the attention: the plan (documents cut into work for the kernels), buffer sizes and the checks of
+// arguments that both directions share.
+#include <math.h>
+
+#include <algorithm>
+#include <functional>
+#include <new>
+#include <queue>
+#include <vector>
+
+#include "attention.cuh"
+
+namespace dit6 {
+namespace attn {
+
+constexpr int SMS = 152;  // a plan is made on the host, for this chip
+
+struct Costed {
+  Item item;
+  double cost;
+};
+
+// The end of the last of `pieces` on SMS processors that take them in order.
+static double makespan(std::vector<double> pieces, int heads) {
+  std::sort(pieces.begin(), pieces.end(), std::greater<double>());
+  std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
+  double last = 0.0;
+  for (double c : pieces)
+    for (int h = 0; h < heads; ++h) {
+      double begin = 0.0;
+      if ((int)ends.size() == SMS) {
+        begin = ends.top();
+        ends.pop();
+      }
+      ends.push(begin + c);
+      last = std::max(last, begin + c);
+    }
+  return last;
+}
+
+// A forward CTA's time in tiles of one row block: its start and end, then its tiles.  Pieces of a split item write and
+// read partial results besides.
+constexpr double START = 4.0, SPLIT_END = 3.0;
+
+static dit_status make_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
+                            int64_t documents, int64_t frame, int heads, int kv_heads, int dim, int training,
+                            dit_attention_plan_t* plan, int32_t* table, int64_t table_ints) {
+  if (!plan || documents < 0 || (documents > 0 && (!queries || !keys)) || frame < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 1)
+    return DIT_ERR_INVALID_ARG;
+  const int group = heads / kv_heads;
+  if (documents > MAX_DOCUMENTS || heads > MAX_HEADS || group > MAX_GROUP || dim % 8 || dim > MAX_DIM || frame > MAX_ROWS) return DIT_ERR_UNSUPPORTED;
+  *plan = dit_attention_plan_t{};
+  plan->documents = (int32_t)documents;
+  plan->heads = heads;
+  plan->kv_heads = kv_heads;
+  plan->dim = dim;
+  plan->frame = (int32_t)frame;
+  plan->training = training ? 1 : 0;
+  std::vector<Doc> docs((size_t)documents);
+  int64_t q_rows = 0, k_next = 0, tiles = 0;
+  for (int64_t i = 0; i < documents; ++i) {
+    const int64_t begin = begins ? begins[i] : k_next, pre = prefix ? prefix[i] : 0;
+    if (queries[i] < 0 || keys[i] < 0 || begin < 0 || pre < 0 || queries[i] > MAX_ROWS || keys[i] > MAX_ROWS || begin > MAX_ROWS ||
+        pre > MAX_ROWS || q_rows + queries[i] > MAX_ROWS || begin + keys[i] > MAX_ROWS)
+      return DIT_ERR_INVALID_ARG;
+    if (frame == 0 && pre > 0) return DIT_ERR_INVALID_ARG;
+    docs[(size_t)i] = Doc{(int32_t)q_rows, (int32_t)queries[i], keys[i] ? (int32_t)begin : 0, (int32_t)keys[i], (int32_t)pre, (int32_t)tiles, {0, 0}};
+    q_rows += queries[i];
+    k_next = begin + keys[i];
+    if (keys[i] && k_next > plan->k_rows) plan->k_rows = k_next;
+    tiles += (queries[i] + TILE - 1) / TILE;
+  }
+  if (tiles > MAX_ROWS) return DIT_ERR_UNSUPPORTED;
+  plan->q_rows = q_rows;
+  plan->padded_rows = tiles * TILE;
+  if (training) {
+    std::vector<std::pair<int64_t, int64_t>> spans;
+    for (const Doc& d : docs)
+      if (d.keys) spans.push_back({d.k0, (int64_t)d.k0 + d.keys});
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      if (spans[i].first < spans[i - 1].second) return DIT_ERR_INVALID_ARG;
+  }
+
+  const int cols = tile_cols(dim), rt = rows_per_tile(group), pd = padded_dim(dim);
+  std::vector<Costed> lists[DIT_ATTENTION_LISTS];
+  // forward: two row blocks to an item.  The second one costs about as much again less what its MMAs hide.
+  std::vector<double> costs;
+  for (size_t i = 0; i < docs.size(); ++i)
+    for (int64_t r = 0; r < docs[i].queries; r += 2 * rt) {
+      const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
+      const int64_t n = (seen_end(docs[i], frame, last) + cols - 1) / cols;
+      const double each = last - r >= rt ? 1.0 : 0.6;
+      lists[FORWARD].push_back({Item{(int32_t)i, (int32_t)r, 0, (int32_t)n, -1, {0, 0, 0}}, START + each * (double)n});
+    }
+  // Few items: their keys are cut into pieces, as many as bring the last CTA's end forward most.
+  int64_t ctas = (int64_t)lists[FORWARD].size() * kv_heads;
+  if (ctas && ctas < 4 * SMS) {
+    std::vector<double> now;
+    int64_t most = 0;
+    for (const Costed& c : lists[FORWARD]) {
+      now.push_back(c.cost);
+      most = std::max<int64_t>(most, c.item.end);
+    }
+    double best = makespan(now, kv_heads);
+    int64_t longest = 0;  // tiles of a piece; 0: items stay whole
+    for (int64_t len = most; len >= 2; len = len > 16 ? len * 7 / 8 : len - 1) {
+      now.clear();
+      int64_t total = 0;
+      for (const Costed& c : lists[FORWARD]) {
+        const int64_t n = c.item.end, pieces = (n + len - 1) / len;
+        const double each = n ? (c.cost - START) / (double)n : 0.0;
+        if (pieces <= 1) {
+          now.push_back(c.cost);
+        } else {
+          for (int64_t k = 0; k < pieces; ++k) now.push_back(START + SPLIT_END + each * (double)(n * (k + 1) / pieces - n * k / pieces));
+        }
+        total += std::max<int64_t>(pieces, 1);
+      }
+      if (total * kv_heads > 6 * SMS) break;
+      const double t = makespan(now, kv_heads) + SPLIT_END;
+      if (t < best) {
+        best = t;
+        longest = len;
+      }
+    }
+    if (longest) {
+      std::vector<Costed> whole;
+      whole.swap(lists[FORWARD]);
+      for (const Costed& c : whole) {
+        const int64_t n = c.item.end, pieces = (n + longest - 1) / longest;
+        if (pieces <= 1) {
+          lists[FORWARD].push_back(c);
+          continue;
+        }
+        const Doc& d = docs[(size_t)c.item.doc];
+        const int32_t rows = (int32_t)std::min<int64_t>(2 * rt, d.queries - c.item.row0);
+        const double each = (c.cost - START) / (double)n;
+        lists[JOIN].push_back({Item{c.item.doc, c.item.row0, plan->slots, (int32_t)pieces, rows, {0, 0, 0}}, 1.0});
+        for (int64_t k = 0; k < pieces; ++k) {
+          Item it = c.item;
+          it.begin = (int32_t)(n * k / pieces);
+          it.end = (int32_t)(n * (k + 1) / pieces);
+          it.slot = plan->slots;
+          plan->slots += rows;
+          lists[FORWARD].push_back({it, START + SPLIT_END + each * (double)(it.end - it.begin)});
+        }
+      }
+    }
+  }
+  if (training)
+    for (size_t i = 0; i < docs.size(); ++i) {
+      const Doc& d = docs[i];
+      for (int64_t r = 0; r < d.queries; r += TILE) {
+        const int64_t n = (seen_end(d, frame, std::min<int64_t>(d.queries, r + TILE) - 1) + cols - 1) / cols;
+        lists[GRAD_Q].push_back({Item{(int32_t)i, (int32_t)r, 0, (int32_t)n, -1, {0, 0, 0}}, START + (double)n});
+      }
+      const int64_t end = ((int64_t)d.queries + cols - 1) / cols;
+      for (int64_t k = 0; k < d.keys; k += TILE) {
+        const int64_t begin = std::min(end, seen_from(d, frame, k) / cols);
+        lists[GRAD_KV].push_back({Item{(int32_t)i, (int32_t)k, (int32_t)begin, (int32_t)end, -1, {0, 0, 0}}, START + (double)(end - begin)});
+      }
+    }
+  std::vector<std::pair<int32_t, int32_t>> buckets[DIT_ATTENTION_LISTS];
+  for (int l = 0; l < DIT_ATTENTION_LISTS; ++l) {
+    auto& list = lists[l];
+    if ((int64_t)list.size() * heads > MAX_ROWS) return DIT_ERR_UNSUPPORTED;
+    std::stable_sort(list.begin(), list.end(), [](const Costed& a, const Costed& b) { return a.cost > b.cost; });
+    double top = 0.0;
+    for (size_t i = 0; i < list.size(); ++i) {
+      if (i == 0 || (list[i].cost < 0.7 * top && buckets[l].size() < DIT_ATTENTION_BUCKETS)) {
+        buckets[l].push_back({(int32_t)i, 0});
+        top = list[i].cost;
+      }
+      ++buckets[l].back().second;
+    }
+    plan->items[l] = (int32_t)list.size();
+    plan->buckets[l] = (int32_t)buckets[l].size();
+  }
+  plan->table_ints = first_bucket(*plan, DIT_ATTENTION_LISTS);
+  plan->saved_bytes = training ? (int64_t)heads * plan->padded_rows * 4 : 0;
+  const int64_t joins = (int64_t)heads * plan->slots * (pd + 2) * 4, deltas = plan->saved_bytes;
+  plan->scratch_bytes = std::max(joins, deltas);
+  if (!table) return DIT_OK;
+  if (table_ints < plan->table_ints) return DIT_ERR_INVALID_ARG;
+  std::fill(table, table + plan->table_ints, 0);
+  std::copy_n(reinterpret_cast<const int32_t*>(docs.data()), docs.size() * DOC_INTS, table);
+  for (int l = 0; l < DIT_ATTENTION_LISTS; ++l) {
+    int32_t* o = table + first_item(*plan, l);
+    for (const Costed& c : lists[l]) {
+      std::copy_n(reinterpret_cast<const int32_t*>(&c.item), ITEM_INTS, o);
+      o += ITEM_INTS;
+    }
+    o = table + first_bucket(*plan, l);
+    for (const auto& b : buckets[l]) {
+      *o++ = b.first;
+      *o++ = b.second;
+    }
+  }
+  return DIT_OK;
+}
+
+bool plan_ok(const dit_attention_plan_t* p) {
+  if (!p || p->documents < 0 || p->heads < 1 || p->heads > MAX_HEADS || p->kv_heads < 1 || p->heads % p->kv_heads || p->heads / p->kv_heads > MAX_GROUP ||
+      p->dim < 8 || p->dim > MAX_DIM || p->dim % 8 || p->frame < 0 || p->q_rows < 0 || p->q_rows > MAX_ROWS || p->k_rows < 0 || p->k_rows > MAX_ROWS ||
+      p->padded_rows < p->q_rows || p->padded_rows % TILE || p->slots < 0)
+    return false;
+  for (int l = 0; l < DIT_ATTENTION_LISTS; ++l)
+    if (p->items[l] < 0 || (int64_t)p->items[l] * p->heads > MAX_ROWS || p->buckets[l] < 0 || p->buckets[l] > DIT_ATTENTION_BUCKETS || (p->items[l] && !p->buckets[l])) return false;
+  const int64_t saved = p->training ? (int64_t)p->heads * p->padded_rows * 4 : 0;
+  return p->table_ints == first_bucket(*p, DIT_ATTENTION_LISTS) && p->saved_bytes == saved &&
+         p->scratch_bytes == std::max(saved, (int64_t)p->heads * p->slots * (padded_dim(p->dim) + 2) * 4);
+}
+
+// A view's checks; strides that no access uses are replaced by ones that a tensor map takes.
+dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, Heads* o) {
+  if (!v || v->heads != heads || (!v->ptr && rows > 0)) return DIT_ERR_INVALID_ARG;
+  *o = Heads{reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(v->ptr)), rows > 1 ? v->token_stride : dim, heads > 1 ? v->head_stride : dim};
+  if (o->row <= 0 || o->head <= 0) return DIT_ERR_INVALID_ARG;
+  if (o->row > 0x7fffffff || o->head > 0x7fffffff) return DIT_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(o->ptr) & 15) || o->row % 8 || o->head % 8) return DIT_ERR_ALIGNMENT;
+  return DIT_OK;
+}
+
+bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows) {
+  return encode_tmap_heads(map, t.ptr, (uint64_t)dim, (uint64_t)heads, (uint64_t)rows, (uint64_t)t.head * 2, (uint64_t)t.row * 2,
+                           (uint32_t)box_heads, (uint32_t)box_rows);
+}
+
+}  // namespace attn
+}  // namespace dit6
+
+extern "C" dit_status dit_attention_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
+                                         int64_t documents, int64_t frame, int heads, int kv_heads, int dim, int training,
+                                         dit_attention_plan_t* plan, int32_t* table, int64_t table_ints) {
+  try {
+    return dit6::attn::make_plan(queries, keys, begins, prefix, documents, frame, heads, kv_heads, dim, training, plan, table, table_ints);
+  } catch (...) {  // out of host memory
+    return DIT_ERR_UNSUPPORTED;
+  }
+}

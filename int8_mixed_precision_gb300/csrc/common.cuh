@@ -506,6 +506,9 @@ bool encode_tmap_sf(CUtensorMap* map, const void* sf, int64_t rows, int64_t k, u
 // a bf16 tensor [outer2][outer1][inner], contiguous, in 128-byte swizzled boxes of 64 x box_outer1 x 1
 bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2,
                          uint32_t box_outer1);
+// a bf16 tensor [rows][heads][dim] with strides in bytes, in 128-byte swizzled boxes of 64 x box_heads x box_rows
+bool encode_tmap_heads(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads, uint64_t rows, uint64_t head_bytes,
+                       uint64_t row_bytes, uint32_t box_heads, uint32_t box_rows);
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, void* base, uint64_t inner,
                     uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                     CUtensorMapSwizzle swz);

@@ -1,0 +1,298 @@
+"""Host side of the norms and the attention, without a GPU: the rotation's table, the plan's cuts and what is refused."""
+import copy
+import ctypes
+import math
+import os
+import random
+
+import pytest
+import torch
+
+import attention_reference as R
+
+INVALID, ALIGNMENT, UNSUPPORTED = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def dit():
+    import int8_mixed_precision_gb300 as d
+    from int8_mixed_precision_gb300 import _lib, build
+    if not os.path.exists(_lib.library_path()):
+        try:
+            build.build_library()
+        except RuntimeError as e:
+            pytest.skip(str(e))
+    return d
+
+
+# ----------------------------------------------------------------------------------------
+# the rotation's table
+# ----------------------------------------------------------------------------------------
+
+def test_rotary_table_holds_turns(dit):
+    rot = dit.Rotary((16, 24, 24), 64, theta=10000.0, scale=(1.0, 0.375, 7.5), device="cpu")
+    words = rot.table.view(-1, 2)
+    assert words.shape[0] == 32
+    p = 0
+    for a, (d, s) in enumerate(zip((16, 24, 24), (1.0, 0.375, 7.5))):
+        for i in range(d // 2):
+            turns = s * 10000.0 ** (-2 * i / d) / (2 * math.pi) % 1.0
+            held = (int(words[p, 0]) & (2 ** 64 - 1)) / 2 ** 64
+            assert abs(held - turns) < 2.0 ** -49
+            assert int(words[p, 1]) & 0xffffffff == a
+            p += 1
+
+
+@pytest.mark.parametrize("kw", [dict(dims=(16, 23, 25)), dict(dims=(32, 48)), dict(dims=(8,) * 5), dict(dims=()), dict(dims=(64,), scale=(1.0, 1.0)),
+                                dict(dims=(-2, 4)), dict(dims=(12,), interleaved=False), dict(dims=(64,), theta=0.0), dict(dims=(64,), theta=math.inf),
+                                dict(dims=(64,), scale=math.nan)])
+def test_rotary_refusals(dit, kw):
+    with pytest.raises(dit.DitError):
+        dit.Rotary(head_dim=64, device="cpu", **kw)
+
+
+def test_norm_refusals(dit):
+    for params, kind, eps in ((torch.ones(2, 64), "layer", 1e-6), (torch.ones(4, 64), "rms", 1e-6), (torch.ones(2, 64), "other", 1e-6),
+                              (torch.ones(2, 64).double(), "rms", 1e-6), (torch.ones(64, 2).T, "rms", 1e-6), (torch.ones(2, 64), "rms", -1.0),
+                              (torch.ones(2, 64), "rms", math.nan)):
+        with pytest.raises(dit.DitError):
+            dit.QKNorm(params, kind, eps)
+
+
+# ----------------------------------------------------------------------------------------
+# the plan
+# ----------------------------------------------------------------------------------------
+
+def lists(plan):
+    """Documents, and the four lists of items, from the table."""
+    i, t = plan.info, plan.table.tolist()
+    docs = [t[8 * k:8 * k + 8] for k in range(i.documents)]
+    at, out = 8 * i.documents, []
+    for n in i.items:
+        out.append([t[at + 8 * k:at + 8 * k + 8] for k in range(n)])
+        at += 8 * n
+    buckets = []
+    for n in i.buckets:
+        buckets.append([t[at + 2 * k:at + 2 * k + 2] for k in range(n)])
+        at += 64
+    assert at == i.table_ints
+    return docs, out, buckets
+
+
+def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
+    plan = dit.AttentionPlan(queries, heads, dim, kv_heads=kv_heads, kv_lengths=keys, frame=frame, prefix=prefix, training=True, device="cpu")
+    docs, (fwd, joins, gq, gk), buckets = lists(plan)
+    cols, rt = (128 if dim <= 64 else 64), 128 // (heads // kv_heads)
+    assert plan.q_rows == sum(queries)
+    for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
+        at = 0
+        for first, count in found:
+            assert first == at and count > 0
+            at += count
+        assert at == len(items)
+    seen = [R.visible(n, m, frame, prefix) for n, m in zip(queries, keys)]
+    # forward: every query once, or in pieces that a join adds up; each pair that is seen lies in exactly one piece
+    met = [torch.zeros(n, m, dtype=torch.int32) for n, m in zip(queries, keys)]
+    rows = [torch.zeros(n, dtype=torch.int32) for n in queries]
+    slots = {}
+    for doc, row0, begin, end, slot, *_ in fwd:
+        part = slice(row0, min(queries[doc], row0 + 2 * rt))
+        met[doc][part, begin * cols:end * cols] += 1
+        assert end * cols < keys[doc] + cols
+        if slot < 0:
+            rows[doc][part] += 1
+        else:
+            n = part.stop - part.start
+            slots[slot] = (doc, row0, n, begin, end)
+            assert slot + n <= plan.info.slots
+    used = torch.zeros(plan.info.slots, dtype=torch.int32)
+    for doc, row0, first, pieces, n, *_ in joins:
+        rows[doc][row0:row0 + n] += 1
+        at = 0
+        for k in range(pieces):
+            d, r, c, begin, end = slots[first + k * n]
+            assert (d, r, c, begin) == (doc, row0, n, at) and end > begin
+            at = end
+            used[first + k * n:first + (k + 1) * n] += 1
+    assert (used == 1).all()
+    for n, m, r, s in zip(queries, keys, rows, seen):
+        assert (r == 1).all()
+    assert all((m <= 1).all() and (m[s] == 1).all() for m, s in zip(met, seen))
+    # gradients: every query and key once, with all that it meets
+    for items, of_keys in ((gq, False), (gk, True)):
+        whole = [torch.zeros(m if of_keys else n, dtype=torch.int32) for n, m in zip(queries, keys)]
+        for doc, row0, begin, end, *_ in items:
+            s = seen[doc].T if of_keys else seen[doc]
+            part = slice(row0, row0 + 128)
+            whole[doc][part] += 1
+            left = s[part].clone()
+            left[:, begin * cols:end * cols] = False
+            assert not left.any()
+            assert end * cols < s.shape[1] + cols
+        assert all((w == 1).all() for w in whole)
+    # each document's statistics begin at a multiple of 128
+    at = 0
+    for d, n in zip(docs, queries):
+        assert d[5] * 128 == at
+        at += -(-n // 128) * 128
+    assert plan.info.padded_rows == at
+    return plan
+
+
+@pytest.mark.parametrize("c", [
+    ([300, 0, 17], [300, 0, 17], 4, 4, 64, 0, 0),
+    ([300, 1, 517], [300, 1, 517], 6, 2, 128, 1, 0),
+    ([1, 1, 1], [4000, 1, 333], 8, 1, 128, 1, 0),
+    ([1350], [8326], 30, 30, 64, 1350, 226),
+    ([5, 2, 9], [3, 0, 1], 2, 2, 64, 1, 0),
+    ([40, 3], [0, 5], 2, 2, 64, 0, 0),
+    ([200], [900], 12, 4, 96, 37, 50),
+    ([7], [2000], 128, 1, 64, 0, 0),
+    ([], [], 1, 1, 64, 0, 0),
+])
+def test_plan_covers_every_pair_once(dit, c):
+    check_plan(dit, *c)
+
+
+def test_plans_of_random_batches(dit):
+    rng = random.Random(0)
+    for _ in range(25):
+        n = rng.randint(1, 6)
+        queries = [rng.choice([0, 1, rng.randint(2, 900)]) for _ in range(n)]
+        keys = [rng.choice([q, q + rng.randint(0, 700), rng.randint(0, 300)]) for q in queries]
+        kv = rng.randint(1, 4)
+        frame = rng.choice([0, 1, rng.randint(2, 100)])
+        check_plan(dit, queries, keys, kv * rng.choice([1, 2, 3]), kv, 8 * rng.randint(1, 16), frame, rng.choice([0, rng.randint(1, 90)]) if frame else 0)
+
+
+def test_few_rows_are_split_over_the_keys(dit):
+    plan = dit.AttentionPlan([1], 4, 128, kv_heads=1, kv_lengths=[20000], frame=1, device="cpu")
+    assert plan.info.items[0] > 50 and plan.info.items[1] == 1
+    whole = dit.AttentionPlan([17776], 30, 64, device="cpu")  # enough work for every SM
+    assert whole.info.slots == 0 and whole._scratch_bytes == 0
+
+
+def test_plan_refusals(dit):
+    ok = dict(lengths=[5, 6], heads=4, dim=64, device="cpu")
+    dit.AttentionPlan(**ok)
+    for change in (dict(lengths=[-1, 3]), dict(kv_heads=3), dict(dim=68), dict(dim=136), dict(dim=0), dict(heads=0), dict(heads=8192), dict(frame=-1),
+                   dict(prefix=3), dict(prefix=[1, 2]), dict(frame=2, prefix=[1]), dict(frame=2, prefix=-1), dict(kv_lengths=[5]), dict(kv_begins=[0]),
+                   dict(kv_begins=[0, -1]), dict(lengths=[2 ** 31 - 1, 5]), dict(lengths=[2 ** 31, 5]), dict(kv_lengths=[2 ** 31 - 300, 600]),
+                   dict(heads=129 * 2, kv_heads=2), dict(frame=2 ** 31), dict(training=True, kv_lengths=[5, 6], kv_begins=[0, 4])):
+        with pytest.raises(dit.DitError):
+            dit.AttentionPlan(**{**ok, **change})
+    dit.AttentionPlan(**{**ok, "kv_lengths": [5, 6], "kv_begins": [0, 4]})  # shared keys serve
+    with pytest.raises(dit.DitError):
+        copy.copy(dit.AttentionPlan(**ok))
+    with pytest.raises(dit.DitError):
+        copy.deepcopy(dit.Rotary((8,), 64, device="cpu"))
+
+
+# ----------------------------------------------------------------------------------------
+# refusals of the calls (nothing is launched)
+# ----------------------------------------------------------------------------------------
+
+def heads(ptr, n, dim, stride=None, head=None):
+    from int8_mixed_precision_gb300.block_attention import _Heads
+    return _Heads(ptr, n * dim if stride is None else stride, dim if head is None else head, n, 0)
+
+
+def test_attention_refusals(dit):
+    L, A = dit.lib(), 1 << 20
+    plan = dit.AttentionPlan([300], 4, 64, kv_heads=2, training=True, device="cpu")
+
+    def call(backward=False, p=plan.info, table=A, ws=A, ws_bytes=1 << 16, scale=0.125, saved=A, saved_bytes=1 << 30, scratch=A, scratch_bytes=1 << 30, **views):
+        v = {n: heads(A, 4, 64) for n in ("q", "out", "dout", "dq")}
+        v.update({n: heads(A, 2, 64) for n in ("k", "v", "dk", "dv")})
+        v.update(views)
+        names = ("q", "k", "v", "out") + (("dout", "dq", "dk", "dv") if backward else ())
+        f = L.dit_attention_backward if backward else L.dit_attention
+        return f(ctypes.byref(p) if p is not None else None, table, *(ctypes.byref(v[n]) if v[n] is not None else None for n in names), scale, saved, saved_bytes,
+                 scratch, scratch_bytes, ws, ws_bytes, None)
+    for back in (False, True):
+        assert call(back, p=None) == INVALID
+        assert call(back, table=None) == INVALID
+        assert call(back, table=A + 4) == ALIGNMENT
+        assert call(back, ws=None) == INVALID
+        assert call(back, ws=A + 16) == ALIGNMENT
+        assert call(back, ws_bytes=100) == INVALID
+        for scale in (0.0, -1.0, math.inf, math.nan):
+            assert call(back, scale=scale) == INVALID
+        assert call(back, saved_bytes=plan._saved_bytes - 1) == INVALID
+        assert call(back, scratch_bytes=plan._scratch_bytes - 1) == INVALID
+        assert call(back, scratch=None) == INVALID
+        for name in ("q", "k", "v", "out") + (("dout", "dq", "dk", "dv") if back else ()):
+            n = 2 if name in ("k", "v", "dk", "dv") else 4
+            assert call(back, **{name: None}) == INVALID
+            assert call(back, **{name: heads(None, n, 64)}) == INVALID
+            assert call(back, **{name: heads(A, n + 1, 64)}) == INVALID
+            assert call(back, **{name: heads(A + 8, n, 64)}) == ALIGNMENT
+            assert call(back, **{name: heads(A, n, 64, stride=n * 64 + 4)}) == ALIGNMENT
+            assert call(back, **{name: heads(A, n, 64, head=68)}) == ALIGNMENT
+            assert call(back, **{name: heads(A, n, 64, stride=0)}) == INVALID
+            assert call(back, **{name: heads(A, n, 64, head=0)}) == INVALID
+            assert call(back, **{name: heads(A, n, 64, stride=1 << 31)}) == UNSUPPORTED
+    serving = dit.AttentionPlan([300], 4, 64, kv_heads=2, device="cpu")
+    assert call(True, p=serving.info) == INVALID
+    assert call(False, p=serving.info) == INVALID  # saved goes with training plans
+    from int8_mixed_precision_gb300.block_attention import _Plan
+    for field, value in (("heads", 3), ("dim", 72 + 4), ("dim", 256), ("table_ints", 1), ("slots", -1), ("slots", 500), ("q_rows", -1), ("padded_rows", 1), ("saved_bytes", 0)):
+        bad = _Plan.from_buffer_copy(plan.info)
+        setattr(bad, field, value)
+        assert call(p=bad) == INVALID, field
+
+
+def test_norm_call_refusals(dit):
+    L, A = dit.lib(), 1 << 20
+    from int8_mixed_precision_gb300.block_attention import _Rotary
+
+    def call(backward=False, tokens=10, dim=64, norm=1, params=A, eps=1e-6, rot=_Rotary(A, 32, 3, 1, 0), positions=A, dparams=A, scratch=A, scratch_bytes=1 << 30,
+             ws=A, ws_bytes=1 << 16, **views):
+        v = {n: heads(A, 4, 64) for n in ("q", "q_out", "dq_out", "dq")}
+        v.update({n: heads(A, 2, 64) for n in ("k", "k_out", "dk_out", "dk")})
+        v.update(views)
+        names = ("q", "k", "dq_out", "dk_out", "dq", "dk") if backward else ("q", "k", "q_out", "k_out")
+        args = (*(ctypes.byref(v[n]) if v[n] is not None else None for n in names), tokens, dim, norm, params, eps, ctypes.byref(rot) if rot is not None else None, positions)
+        return L.dit_qk_norm_rope_backward(*args, dparams, scratch, scratch_bytes, ws, ws_bytes, None) if backward else L.dit_qk_norm_rope(*args, None)
+    for back in (False, True):
+        for change in (dict(tokens=-1), dict(dim=0), dict(norm=3), dict(norm=-1), dict(params=None), dict(eps=-1.0), dict(eps=math.nan), dict(q=None),
+                       dict(rot=_Rotary(A, 33, 3, 1, 0)), dict(rot=_Rotary(A, 32, 5, 1, 0)), dict(rot=_Rotary(A, 32, 0, 1, 0)), dict(rot=_Rotary(None, 32, 3, 1, 0)),
+                       dict(positions=None), dict(q=heads(None, 4, 64)), dict(k=None)):
+            assert call(back, **change) == INVALID, change
+        for change in (dict(dim=60), dict(dim=264), dict(rot=_Rotary(A, 30, 3, 0, 0))):
+            assert call(back, **change) == UNSUPPORTED, change
+        for change in (dict(params=A + 2), dict(positions=A + 2), dict(rot=_Rotary(A + 8, 32, 3, 1, 0)), dict(q=heads(A + 8, 4, 64)), dict(k=heads(A, 2, 64, stride=132))):
+            assert call(back, **change) == ALIGNMENT, change
+    for change in (dict(ws=None), dict(ws_bytes=3), dict(scratch=None), dict(scratch_bytes=100), dict(norm=0)):
+        assert call(True, **change) == INVALID, change
+    assert call(True, ws=A + 16) == ALIGNMENT
+    assert call(False, tokens=0) == 0  # nothing to do
+
+
+def test_views_that_share_memory_are_found(dit):
+    from int8_mixed_precision_gb300.block_attention import _meet
+
+    def view(t):
+        return heads(t.data_ptr(), t.shape[1], t.shape[2], t.stride(0), t.stride(1))
+
+    def meet(a, b):
+        got = _meet(view(a), a.shape[0], view(b), b.shape[0], a.shape[2])
+        assert got == _meet(view(b), b.shape[0], view(a), a.shape[0], a.shape[2])
+        return got
+    x = torch.empty(10, 7, 8, dtype=torch.bfloat16)
+    assert not meet(x[:, :3], x[:, 3:]) and meet(x[:, :4], x[:, 3:]) and meet(x, x)
+    assert not meet(x[:5], x[5:]) and meet(x[:6], x[5:])
+    y = torch.empty(10, 4, 3, 8, dtype=torch.bfloat16)  # query, key and value of a head side by side
+    assert not meet(y[:, :, 0], y[:, :, 1]) and not meet(y[:, :, 2], y[:, :, 0]) and meet(y[:, :, 1], y[:, :, 1])
+    assert not meet(y[:, 1:, 0], y[:, :, 1]) and meet(y[:, :1, 1], y[:, :, 1])
+    z = torch.empty(10, 7, 8, dtype=torch.bfloat16)
+    assert not meet(x, z) and not meet(x[:0], x)
+
+
+def test_host_tensors_are_refused(dit):
+    x = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
+    with pytest.raises(dit.DitError):
+        dit.qk_norm_rope(x[:, :2], x[:, 2:4], x[:, :2], x[:, 2:4])
+    plan = dit.AttentionPlan([4], 2, 64, device="cpu")
+    with pytest.raises(dit.DitError):
+        dit.attention(plan, x[:, :2], x[:, 2:4], x[:, 4:], torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.empty(0), torch.empty(0))

@@ -1,0 +1,287 @@
+"""Attention over packed documents and its gradients, against the formulas in 64 bits."""
+import pytest
+import torch
+
+import attention_reference as R
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dit():
+    import int8_mixed_precision_gb300 as d
+    return d
+
+
+class Batch:
+    """A batch in one buffer [rows, heads + 2 kv_heads, dim], or with keys in a cache; rows of no document hold NaN."""
+
+    def __init__(self, dit, lengths, heads, kv_heads, dim, frame=0, prefix=0, kv_lengths=None, room=None, train=True, seed=0, sharp=1.0, tail=3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        new = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+        self.dit, self.lengths, self.h, self.hk, self.d, self.frame = dit, lengths, heads, kv_heads, dim, frame
+        self.keys = lengths if kv_lengths is None else kv_lengths
+        self.prefix = [prefix] * len(lengths) if isinstance(prefix, int) else prefix
+        n = sum(lengths)
+        self.q = torch.full((n + tail, heads, dim), float("nan"), dtype=BF16, device="cuda")
+        self.q[:n] = (new(n, heads, dim) * sharp).to(BF16)
+        self.begins = [sum(self.keys[:i]) for i in range(len(self.keys))] if room is None else [i * room + 1 for i in range(len(self.keys))]
+        rows = max([b + m for b, m in zip(self.begins, self.keys)] + [0]) + tail
+        kv = torch.full((rows, 2 * kv_heads, dim), float("nan"), dtype=BF16, device="cuda")
+        for b, m in zip(self.begins, self.keys):
+            kv[b:b + m] = new(m, 2 * kv_heads, dim).to(BF16)
+        self.k, self.v = kv[:, :kv_heads], kv[:, kv_heads:]
+        self.out = torch.full((n + tail, heads, dim), 7.0, dtype=BF16, device="cuda")
+        self.plan = dit.AttentionPlan(lengths, heads, dim, kv_heads=kv_heads, kv_lengths=self.keys, kv_begins=None if room is None else self.begins,
+                                      frame=frame, prefix=self.prefix, training=train)
+        self.ws, self.scratch = dit.workspace(), dit.attention_scratch(self.plan)
+        self.scratch.fill_(255)
+        self.saved = dit.attention_saved(self.plan) if train else None
+        if train:
+            self.saved.fill_(255)
+            self.dout = torch.full_like(self.q, float("nan"))
+            self.dout[:n] = new(n, heads, dim).to(BF16)
+            self.dq = torch.full_like(self.q, 5.0)
+            grad = torch.full_like(kv, 5.0)
+            self.dk, self.dv = grad[:, :kv_heads], grad[:, kv_heads:]
+
+    def forward(self, **more):
+        self.dit.attention(self.plan, self.q, self.k, self.v, self.out, self.scratch, self.ws, saved=self.saved, **more)
+
+    def backward(self, **more):
+        self.dit.attention_backward(self.plan, self.q, self.k, self.v, self.out, self.dout, self.saved, self.dq, self.dk, self.dv, self.scratch,
+                                    self.ws, **more)
+
+    def check(self, scale=None):
+        scale = self.d ** -0.5 if scale is None else scale
+        train, group, q0 = self.saved is not None, self.h // self.hk, 0
+        covered = torch.zeros(self.k.shape[0], dtype=torch.bool)
+        for n, m, b, pre in zip(self.lengths, self.keys, self.begins, self.prefix):
+            seen = R.visible(n, m, self.frame, pre, "cuda")
+            covered[b:b + m] = True
+            rows, keys = slice(q0, q0 + n), slice(b, b + m)
+            for j in range(self.hk):
+                k, v = self.k[keys, j].double(), self.v[keys, j].double()
+                sums = [[0.0, 0.0], [0.0, 0.0]]
+                for head in range(j * group, (j + 1) * group):
+                    q = self.q[rows, head].double()
+                    o, p, bound = R.attention(q, k, v, seen, scale)
+                    self.close("out", self.out[rows, head], o, bound)
+                    if not train:
+                        continue
+                    dq, dk, dv = R.attention_grads(q, k, v, p, o, self.dout[rows, head].double(), scale)
+                    self.close("dq", self.dq[rows, head], *dq)
+                    for s, t in zip(sums, (dk, dv)):
+                        s[0], s[1] = s[0] + t[0], s[1] + t[1]
+                if train and m:
+                    zero = torch.zeros(m, self.d, dtype=torch.float64, device="cuda")
+                    self.close("dk", self.dk[keys, j], sums[0][0] + zero, sums[0][1] + zero)
+                    self.close("dv", self.dv[keys, j], sums[1][0] + zero, sums[1][1] + zero)
+            q0 += n
+        assert (self.out[q0:] == 7.0).all()  # rows of no document are as they were
+        if train:
+            assert (self.dq[q0:] == 5.0).all() and (self.dk[~covered] == 5.0).all() and (self.dv[~covered] == 5.0).all()
+        assert self.dit.device_status(self.ws) == 0
+
+    def close(self, what, got, want, bound):
+        if not want.numel():
+            return
+        off = (got.double() - want).abs()
+        assert torch.isfinite(got).all(), what
+        assert (off <= bound).all(), (what, float((off / bound).max()), float(off.max()))
+
+
+CASES = [
+    # lengths, heads, kv_heads, dim, frame, prefix
+    ([128], 1, 1, 64, 0, 0),
+    ([1], 1, 1, 64, 0, 0),
+    ([300], 2, 2, 64, 0, 0),
+    ([257, 1, 0, 130, 64], 3, 3, 64, 0, 0),
+    ([700], 1, 1, 64, 1, 0),
+    ([700, 45], 2, 2, 64, 60, 33),
+    ([64, 65, 63], 4, 2, 128, 0, 0),
+    ([513], 3, 1, 128, 1, 17),
+    ([200, 31], 6, 2, 40, 7, 100),
+    ([90], 2, 2, 8, 0, 0),
+    ([333], 5, 1, 72, 50, 0),
+    ([130, 257], 1, 1, 96, 0, 0),
+    ([1, 1, 1, 2], 8, 1, 128, 1, 0),
+    ([20], 4, 4, 64, 1000000000, 2000000000),
+    ([5, 0, 0, 3], 2, 2, 64, 0, 0),
+]
+
+
+@pytest.mark.parametrize("c", CASES)
+def test_forward_and_backward(dit, c):
+    lengths, heads, kv_heads, dim, frame, prefix = c
+    b = Batch(dit, lengths, heads, kv_heads, dim, frame, prefix)
+    b.forward()
+    b.backward()
+    b.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_longer_than_every_ring(dit, dim):
+    b = Batch(dit, [1700, 900], 4, 2, dim, 0, 0)
+    b.forward()
+    b.backward()
+    b.check()
+
+
+@pytest.mark.parametrize("c", [
+    # queries, keys, heads, kv_heads, dim, frame, prefix, room
+    ([1, 1, 1, 1], [700, 1, 65, 3000], 16, 4, 128, 1, 0, 3100),
+    ([1], [5000], 1, 1, 64, 1, 0, 5003),
+    ([135], [900], 3, 3, 64, 135, 90, 1000),
+    ([3, 0, 7], [1300, 5, 129], 6, 1, 64, 4, 2, 1400),
+    ([5, 2], [3, 0], 2, 2, 64, 1, 0, 10),          # fewer keys than queries: the first queries see none
+    ([6], [2], 2, 1, 128, 2, 1, 4),
+    ([40], [0], 2, 2, 64, 0, 0, 4),                # no keys at all
+    ([200], [77], 3, 3, 64, 0, 0, 80),             # a few keys for many queries
+    ([1, 1], [2000, 2000], 128, 1, 64, 1, 0, 2000),
+])
+def test_keys_in_a_cache(dit, c):
+    queries, keys, heads, kv_heads, dim, frame, prefix, room = c
+    for train in (False, True):
+        b = Batch(dit, queries, heads, kv_heads, dim, frame, prefix, kv_lengths=keys, room=room, train=train)
+        b.forward()
+        if train:
+            b.backward()
+        b.check()
+
+
+def test_many_splits(dit):
+    """Long keys of one head are cut among the SMs and joined."""
+    b = Batch(dit, [3], 1, 1, 64, kv_lengths=[40000], train=False)
+    assert b.plan.info.slots > 0
+    b.forward()
+    b.check()
+
+
+@pytest.mark.parametrize("sharp", [0.0, 20.0, 200.0])
+def test_flat_and_sharp_scores(dit, sharp):
+    """All weights equal, and maxima that grow from tile to tile by far more than the exponent's range."""
+    b = Batch(dit, [520], 2, 2, 64, sharp=sharp)
+    b.forward(scale=0.5)
+    b.backward(scale=0.5)
+    q0 = b.q[:520].double()
+    # scores of this size: fp32 leaves them off by 2^-22 of the sum of magnitudes, which the weights feel in full
+    worst = (q0.abs().transpose(0, 1) @ b.k[:520].double().abs().permute(1, 2, 0)).amax() * 0.5 * 2.0 ** -22
+    fine, R.FINE = R.FINE, R.FINE + float(worst)
+    try:
+        b.check(scale=0.5)
+    finally:
+        R.FINE = fine
+
+
+def test_other_documents_do_not_reach_a_result(dit):
+    """NaN and infinity in one document leave every bit of the others as it was."""
+    lengths = [70, 200, 33]
+    b = Batch(dit, lengths, 2, 1, 64)
+    b.forward()
+    b.backward()
+    first = [t.clone() for t in (b.out, b.dq, b.dk, b.dv)]
+    for t, bad in ((b.q, float("nan")), (b.k, float("inf")), (b.v, float("nan")), (b.dout, float("-inf"))):
+        t[70:270] = bad
+    b.forward()
+    b.backward()
+    for a, t in zip(first, (b.out, b.dq, b.dk, b.dv)):
+        assert torch.equal(a[:70], t[:70]) and torch.equal(a[270:303], t[270:303])
+    assert torch.isnan(b.out[70:270]).all() and torch.isnan(b.dv[70:270]).all()
+
+
+def test_nan_stays_in_its_rows(dit):
+    """Under a causal mask NaN in a query reaches that query's output alone."""
+    b = Batch(dit, [200], 1, 1, 64, frame=1, train=False)
+    b.forward()
+    first = b.out.clone()
+    b.q[77] = float("nan")
+    b.forward()
+    assert torch.isnan(b.out[77]).all()
+    b.out[77] = first[77]
+    assert torch.equal(b.out, first)
+
+
+def test_same_bits_and_graph(dit):
+    """Eager calls and a replay give the same bits, and a replay reads new inputs."""
+    b = Batch(dit, [400, 77, 1300], 6, 2, 64, frame=50, prefix=11)
+    b.forward()
+    b.backward()
+    names = ("out", "dq", "dk", "dv")
+    first = [getattr(b, n).clone() for n in names]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.forward()
+        b.backward()
+    for n in names:
+        getattr(b, n)[:1777] = 0
+    graph.replay()
+    assert all(torch.equal(a, getattr(b, n)) for a, n in zip(first, names))
+    b.v[:1777] *= 2
+    graph.replay()
+    b.check()
+
+
+def test_streams_share_nothing_but_inputs(dit):
+    """Two batches of one plan on two streams at a time, each with its own scratch and workspace."""
+    a = Batch(dit, [900, 300], 4, 4, 64, seed=1)
+    b = Batch(dit, [900, 300], 4, 4, 64, seed=2)
+    b.plan = a.plan
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        a.forward()
+        b.forward(stream=side)
+        a.backward()
+        b.backward(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    a.check()
+    b.check()
+
+
+def test_gradients_match_differences(dit):
+    """The gradients against differences of the 64-bit formula, so that both could not share a mistake."""
+    b = Batch(dit, [9, 20], 2, 1, 64, frame=3, prefix=4)
+    b.forward()
+    b.backward()
+    n = 29
+    leaves = [t[:n].double().clone().requires_grad_() for t in (b.q, b.k, b.v)]
+
+    def loss(q, k, v):
+        total, q0 = 0.0, 0
+        for m in (9, 20):
+            seen = R.visible(m, m, 3, 4, "cuda")
+            for head in range(2):
+                s = (q[q0:q0 + m, head] @ k[q0:q0 + m, 0].T) / 8.0
+                p = torch.softmax(s.masked_fill(~seen, float("-inf")), 1)
+                total = total + (p @ v[q0:q0 + m, 0] * b.dout[q0:q0 + m, head].double()).sum()
+            q0 += m
+        return total
+    loss(*leaves).backward()
+    for leaf, got in zip(leaves, (b.dq, b.dk, b.dv)):
+        # bf16 operands and results: some 2^-8 of the largest entries
+        assert (leaf.grad - got[:n].double()).abs().max() <= 4 * R.HALF * leaf.grad.abs().max()
+        at, step = (5, 0, 7), 1e-5
+        moved = []
+        for sign in (1, -1):
+            args = [t.detach().clone() for t in leaves]
+            args[[i for i, t in enumerate(leaves) if t is leaf][0]][at] += sign * step
+            moved.append(loss(*args))
+        assert abs(float((moved[0] - moved[1]) / (2 * step) - leaf.grad[at])) < 1e-6
+
+
+def test_bounded_wait_reports_timeout_and_recovers(dit, monkeypatch):
+    b = Batch(dit, [300, 64], 2, 2, 64)
+    monkeypatch.setenv("DIT6_TEST_STALL_PRODUCER", "1")
+    b.forward()
+    assert dit.device_status(b.ws) & (1 << 5)
+    dit.clear_device_status(b.ws)
+    b.backward()
+    assert dit.device_status(b.ws) & (1 << 5)
+    dit.clear_device_status(b.ws)
+    monkeypatch.delenv("DIT6_TEST_STALL_PRODUCER")
+    b.out[:364], b.dq[:364], b.dk[:364], b.dv[:364] = 0, 0, 0, 0
+    b.forward()
+    b.backward()
+    b.check()
