@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!ok) break;
           fence_after();
         }
+        __syncwarp();
         if (rescale) {
 #pragma unroll
           for (int k = 0; k < PD; k += 32) {
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int k = 0; k < PD; k += 32) {
         uint32_t o[32];
+        __syncwarp();
         tmem_ld32(at + F::O + t * PD + k, o);
         tmem_wait();
         pin(o);
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ 
 template <int PD>
 static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads& v, cudaStream_t st) {
   using F = Fwd<PD>;
-  static OncePerDevice once;
+  static OncePerDevice checked, once;
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded: any tensor makes a map
   const bool keys = a.plan.k_rows > 0;
@@ -380,7 +382,7 @@ static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads
   if (!map_heads(&mq, q, a.plan.dim, a.plan.heads, a.plan.q_rows, a.group, a.rows) ||
       !map_heads(&mk, keys ? k : q, a.plan.dim, k_heads, k_rows, 1, F::COLS) || !map_heads(&mv, keys ? v : q, a.plan.dim, k_heads, k_rows, 1, F::COLS))
     return DIT_ERR_CUDA;
-  if (prepare_kernel(once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  if (prepare_kernel(checked, once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
   if (launch_pdl(k_attention<PD>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads)), dim3(256), 0, st, 1, a) != cudaSuccess)

@@ -104,6 +104,7 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
     }
   }
   if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
+  __syncwarp();
   return w;
 }
 
@@ -122,17 +123,16 @@ static_assert(ISSUE_REGS + 2 * ROW_REGS <= 3 * LAUNCH_REGS, "");
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE_REGS)); }
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROW_REGS)); }
 template <typename... KArgs>
-cudaError_t prepare_kernel(OncePerDevice& once, void (*kern)(KArgs...), int smem) {
+cudaError_t prepare_kernel(OncePerDevice& checked, OncePerDevice& once, void (*kern)(KArgs...), int smem) {
   int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
+  const cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  return once.run(device, [&] {
+  const cudaError_t fits = checked.run(device, [&] {
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, kern);
-    if (e != cudaSuccess) return e;
-    if (a.numRegs != LAUNCH_REGS) return cudaErrorInvalidKernelImage;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t got = cudaFuncGetAttributes(&a, kern);
+    return got != cudaSuccess ? got : a.numRegs == LAUNCH_REGS ? cudaSuccess : cudaErrorInvalidKernelImage;
   });
+  return fits == cudaSuccess ? opt_in_smem(once, kern, smem) : fits;
 }
 
 // ---------------------------------------------------------------------------------------

@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         fence_after();
       }
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < HALF / 2; k += 16) {
         if (KEYS) tmem_st16(at + F::P + half * (HALF / 2) + k, pk + k);
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int k = half * (PD / 2); k < (half + 1) * (PD / 2); k += 32) {
           uint32_t o[32];
+          __syncwarp();
           tmem_ld32(at + (out ? F::B : F::A) + k, o);
           tmem_wait();
           pin(o);
@@ -360,7 +362,7 @@ struct Inputs {
 template <int PD, bool KEYS>
 static dit_status launch(BackArgs a, const Inputs& in, cudaStream_t st) {
   using F = Back<PD>;
-  static OncePerDevice once;
+  static OncePerDevice checked, once;
   const dit_attention_plan_t& p = a.plan;
   const int items = p.items[KEYS ? GRAD_KV : GRAD_Q], heads = KEYS ? p.kv_heads : p.heads;
   if (!items) return DIT_OK;
@@ -374,7 +376,7 @@ static dit_status launch(BackArgs a, const Inputs& in, cudaStream_t st) {
   const int q_box = KEYS ? F::COLS : TILE, k_box = KEYS ? TILE : F::COLS;
   if (!map(&mq, in.q, in.k, true, q_box) || !map(&mo, in.dout, in.v, true, q_box) || !map(&mk, in.k, in.q, false, k_box) || !map(&mv, in.v, in.dout, false, k_box))
     return DIT_ERR_CUDA;
-  if (prepare_kernel(once, k_attention_back<PD, KEYS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  if (prepare_kernel(checked, once, k_attention_back<PD, KEYS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
   const cudaError_t e = KEYS ? launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mk, mv, mq, mo, a)
                              : launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mq, mo, mk, mv, a);
   return e == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
