@@ -16,6 +16,7 @@
 //
 // Warps: 0 loads, 1 issues the MMAs, 4 to 7 and 8 to 11 are the blocks' rows and take over most of the first four
 // warps' registers.  Every wait is bounded.
+#include <limits.h>
 #include <math.h>
 
 #include "attention.cuh"
@@ -30,22 +31,23 @@ constexpr int FWD_STAGES = 6;  // most
 
 template <int PD>
 struct Fwd {
-  static constexpr int COLS = tile_cols(PD);
+  static constexpr int COLS = FORWARD_COLS;
   static constexpr int CHUNKS = PD / 64;
+  static constexpr bool OVER_S = PD > 64;  // P takes the place of S
   static constexpr int Q_CHUNK = TILE * 128, Q_BYTES = CHUNKS * Q_CHUNK;
   static constexpr int KV_CHUNK = COLS * 128, KV_BYTES = CHUNKS * KV_CHUNK;
-  static constexpr int STAGES = PD == 64 ? 6 : 5;
+  static constexpr int STAGES = PD == 64 ? 6 : 2;
   static constexpr int CONTROL = 2 * Q_BYTES + 2 * STAGES * KV_BYTES;
   static constexpr int SMEM = CONTROL + 1024 + 1024;
   // tensor memory: S and P of each block, then O
-  static constexpr uint32_t S = 0, P = 2 * COLS, O = 3 * COLS;
-  static_assert(3 * COLS + 2 * PD <= 512 && SMEM <= 227 * 1024, "");
+  static constexpr uint32_t S = 0, P = OVER_S ? S : 2 * COLS, P_STEP = OVER_S ? COLS : COLS / 2, O = OVER_S ? 2 * COLS : 3 * COLS;
+  static_assert(O + 2 * PD <= 512 && SMEM <= 227 * 1024, "");
 };
 
 struct FwdControl {
   uint64_t qfull, done;
   uint64_t kfull[FWD_STAGES], kempty[FWD_STAGES], vfull[FWD_STAGES], vempty[FWD_STAGES];
-  uint64_t sfull[2], sfree[2], pready[2], pdone[2];
+  uint64_t sfull[2], sfree[2], pready[2], pdone[2], tail;
   uint32_t tmem;
   int abort;
 };
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&c->kfull[lane]), 1);
       mbar_init(smem_u32(&c->kempty[lane]), 1);
       mbar_init(smem_u32(&c->vfull[lane]), 1);
-      mbar_init(smem_u32(&c->vempty[lane]), 1);
+      mbar_init(smem_u32(&c->vempty[lane]), 2);
     } else if (lane >= 8 && lane < 10) {
       const int t = lane - 8;
       mbar_init(smem_u32(&c->sfull[t]), 1);
@@ -89,7 +91,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&c->pdone[t]), 1);
     } else if (lane == 10) {
       mbar_init(smem_u32(&c->qfull), 1);
-      mbar_init(smem_u32(&c->done), 1);
+      mbar_init(smem_u32(&c->done), 3);
+      mbar_init(smem_u32(&c->tail), 1);
       c->abort = 0;
     }
     fence_barrier_init();
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   fence_after();
-  const uint32_t tmem = c->tmem;
+  const uint32_t tmem = uniform(c->tmem);
   volatile int* abort = &c->abort;
   pdl_wait();
 
@@ -114,88 +117,119 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < 4) give_registers();
   if (warp == 0) {
     if (work && elect_one()) {
-      uint32_t nk = 0, nv = 0;
+      const uint32_t ring = smem + 2 * F::Q_BYTES;
+      int s = 0, parity = 1, issued = 0;  // of K; V has as many or one less
       bool ok = true;
       if (!p.stall) {
         mbar_expect_tx(smem_u32(&c->qfull), blocks * F::CHUNKS * p.rows * p.group * 128);
         for (int t = 0; t < blocks; ++t)
+#pragma unroll
           for (int k = 0; k < F::CHUNKS; ++k)
             tma_load_3d(smem + t * F::Q_BYTES + k * F::Q_CHUNK, &mq, smem_u32(&c->qfull), k * 64, w.head * p.group, d.q0 + row0 + t * p.rows);
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int s = j % F::STAGES;
-        const int row = d.k0 + (w.item.begin + j) * COLS;
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const uint32_t full = smem_u32(kv ? &c->vfull[s] : &c->kfull[s]), empty = smem_u32(kv ? &c->vempty[s] : &c->kempty[s]);
-          if (j >= F::STAGES && !mbar_wait(empty, ((j / F::STAGES) - 1) & 1, p.ws, abort)) {
-            ok = false;
-            break;
-          }
-          if (p.stall) continue;
-          mbar_expect_tx(full, F::KV_BYTES);
-          for (int k = 0; k < F::CHUNKS; ++k)
-            tma_load_3d(smem + 2 * F::Q_BYTES + (kv * F::STAGES + s) * F::KV_BYTES + k * F::KV_CHUNK, kv ? &mv : &mk, full, k * 64, w.head, row);
-          ++(kv ? nv : nk);
+      int row = d.k0 + w.item.begin * COLS;
+      for (int j = 0; j < n; ++j, row += COLS) {
+        if (j >= F::STAGES && !mbar_wait(smem_u32(&c->kempty[s]), parity, p.ws, abort)) {
+          ok = false;
+          break;
         }
+        if (!p.stall) {
+          const uint32_t full = smem_u32(&c->kfull[s]), at = ring + s * F::KV_BYTES;
+          mbar_expect_tx(full, F::KV_BYTES);
+#pragma unroll
+          for (int k = 0; k < F::CHUNKS; ++k) tma_load_3d(at + k * F::KV_CHUNK, &mk, full, k * 64, w.head, row);
+          issued = 2 * j + 1;
+        }
+        if (j >= F::STAGES && !mbar_wait(smem_u32(&c->vempty[s]), parity, p.ws, abort)) {
+          ok = false;
+          break;
+        }
+        if (!p.stall) {
+          const uint32_t full = smem_u32(&c->vfull[s]), at = ring + (F::STAGES + s) * F::KV_BYTES;
+          mbar_expect_tx(full, F::KV_BYTES);
+#pragma unroll
+          for (int k = 0; k < F::CHUNKS; ++k) tma_load_3d(at + k * F::KV_CHUNK, &mv, full, k * 64, w.head, row);
+          issued = 2 * j + 2;
+        }
+        if (++s == F::STAGES) s = 0, parity ^= 1;
       }
-      if (!ok || *abort) {  // its own copies land before the CTA ends
+      if ((!ok || *abort) && !p.stall) {  // its own copies land before the CTA ends
         volatile int never = 0;
-        if (!p.stall) mbar_wait(smem_u32(&c->qfull), 0, p.ws, &never);
-        for (uint32_t i = nk > F::STAGES ? nk - F::STAGES : 0; i < nk; ++i) mbar_wait(smem_u32(&c->kfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
-        for (uint32_t i = nv > F::STAGES ? nv - F::STAGES : 0; i < nv; ++i) mbar_wait(smem_u32(&c->vfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
+        mbar_wait(smem_u32(&c->qfull), 0, p.ws, &never);
+        for (int i = issued > 2 * F::STAGES ? issued - 2 * F::STAGES : 0; i < issued; ++i) {
+          const int j = i / 2;
+          mbar_wait(smem_u32(i % 2 ? &c->vfull[j % F::STAGES] : &c->kfull[j % F::STAGES]), (j / F::STAGES) & 1, p.ws, &never);
+        }
       }
     }
   } else if (warp == 1) {
-    if (work) {
-      const uint32_t id_s = idesc(128, COLS, false, false);
-      const uint32_t id_o = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
-      const int steps = (p.plan.dim + 15) / 16;
+    if (work) {  // S of each tile and block, once its warps have the tile before in registers (OVER_S: once P is used up)
+      constexpr uint32_t id = idesc(128, COLS, false, false);
+      const uint32_t ring = smem + 2 * F::Q_BYTES;
       bool ok = warp_wait(smem_u32(&c->qfull), 0, p.ws, abort);
-      auto scores = [&](int j) {  // S of tile j for each block
-        const int s = j % F::STAGES;
-        ok = ok && warp_wait(smem_u32(&c->kfull[s]), (j / F::STAGES) & 1, p.ws, abort);
+      int s = 0, parity = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = warp_wait(smem_u32(&c->kfull[s]), parity, p.ws, abort);
         for (int t = 0; t < blocks && ok; ++t) {
-          if (j > 0) ok = warp_wait(smem_u32(&c->sfree[t]), (j - 1) & 1, p.ws, abort);
+          if (j > 0) ok = warp_wait(smem_u32(F::OVER_S ? &c->pdone[t] : &c->sfree[t]), (j - 1) & 1, p.ws, abort);
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            const uint32_t a = desc_k(smem + t * F::Q_BYTES), b = desc_k(smem + 2 * F::Q_BYTES + s * F::KV_BYTES);
+            const uint32_t a = desc_k(smem + t * F::Q_BYTES), b = desc_k(ring + s * F::KV_BYTES), to = tmem + F::S + t * COLS;
 #pragma unroll
-            for (int k = 0; k < PD / 16; ++k)
-              if (k < steps)
-                mma(tmem + F::S + t * COLS, a + (k / 4) * (F::Q_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::KV_CHUNK >> 4) + (k % 4) * 2, id_s, k > 0);
+            for (int k = 0; k < PD / 16; ++k) mma(to, a + (k / 4) * (F::Q_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::KV_CHUNK >> 4) + (k % 4) * 2, id, k > 0);
             mma_commit(smem_u32(&c->sfull[t]));
             if (t == blocks - 1) mma_commit(smem_u32(&c->kempty[s]));
           }
           __syncwarp();
         }
-      };
-      scores(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) scores(j + 1);
-        const int s = j % F::STAGES;
-        const uint32_t v = smem + 2 * F::Q_BYTES + (F::STAGES + s) * F::KV_BYTES;
-        ok = ok && warp_wait(smem_u32(&c->vfull[s]), (j / F::STAGES) & 1, p.ws, abort);
-        const int64_t left = (int64_t)d.keys - (int64_t)(w.item.begin + j) * COLS;
-        if (ok && left < COLS) zero_rows(v, F::KV_CHUNK, F::CHUNKS, (int)left, COLS);
-        for (int t = 0; t < blocks && ok; ++t) {
-          ok = warp_wait(smem_u32(&c->pready[t]), j & 1, p.ws, abort);
-          if (!ok) break;
-          fence_after();
-          if (elect_one()) {
-            const uint32_t a = tmem + F::P + t * (COLS / 2), b = desc_mn(v, F::KV_CHUNK);
-#pragma unroll
-            for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::O + t * PD, a + k * 8, b + k * (2048 >> 4), id_o, j > 0 || k > 0);
-            mma_commit(smem_u32(&c->pdone[t]));
-            if (t == blocks - 1) mma_commit(smem_u32(&c->vempty[s]));
-          }
-          __syncwarp();
-        }
+        if (++s == F::STAGES) s = 0, parity ^= 1;
       }
-      volatile int never = 0;
       if (elect_one()) mma_commit(smem_u32(&c->done));
       __syncwarp();
-      warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+    }
+  } else if (warp < 4) {
+    const int t = warp - 2;
+    if (work && t < blocks) {  // O += P V of a block
+      const uint32_t id = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
+      const uint32_t a = tmem + F::P + t * F::P_STEP, to = tmem + F::O + t * PD;
+      bool ok = true;
+      int s = 0, parity = 0;
+      int left = d.keys - w.item.begin * COLS;  // keys from this tile's first on
+      for (int j = 0; j < n && ok; ++j, left -= COLS) {
+        const uint32_t v = smem + 2 * F::Q_BYTES + (F::STAGES + s) * F::KV_BYTES;
+        ok = warp_wait(smem_u32(&c->vfull[s]), parity, p.ws, abort);
+        if (ok && left < COLS) {  // the last tile, for both blocks
+          if (t == 0) {
+            zero_rows(v, F::KV_CHUNK, F::CHUNKS, left, COLS);
+            if (lane == 0) mbar_arrive(smem_u32(&c->tail));
+            __syncwarp();
+          } else {
+            ok = warp_wait(smem_u32(&c->tail), 0, p.ws, abort);
+          }
+        }
+        ok = ok && warp_wait(smem_u32(&c->pready[t]), j & 1, p.ws, abort);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          const uint32_t b = desc_mn(v, F::KV_CHUNK);
+#pragma unroll
+          for (int k = 0; k < COLS / 16; ++k) mma_ta(to, a + k * 8, b + k * (2048 >> 4), id, j > 0 || k > 0);
+          mma_commit(smem_u32(&c->pdone[t]));
+          mma_commit(smem_u32(&c->vempty[s]));
+          if (blocks == 1) mma_commit(smem_u32(&c->vempty[s]));
+        }
+        __syncwarp();
+        if (++s == F::STAGES) s = 0, parity ^= 1;
+      }
+    }
+    if (work) {
+      if (elect_one()) mma_commit(smem_u32(&c->done));
+      __syncwarp();
+      if (t == 0) {  // every MMA has completed before the CTA ends
+        volatile int never = 0;
+        warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+      }
     }
   } else if (warp >= 4) {
     take_registers();
@@ -207,77 +241,92 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t at = tmem + ((uint32_t)(warp % 4) << 21);
     // rows behind the last one: nothing is masked and nothing stored
     const int64_t hi = live ? seen_end(d, p.plan.frame, row) : INT64_MAX;
-    float m = -INFINITY, l = 0.f;
+    // tiles up to the first one that some row does not see whole
+    const int whole = __reduce_min_sync(0xffffffffu, (int)(min(hi, (int64_t)INT_MAX - COLS) / COLS)) - w.item.begin;
+    float m = -INFINITY, mc = 0.f, l = 0.f;  // the maximum in use, -m c, and the sum
     bool ok = true;
     if (work && t < blocks) {
+      const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
+      bool seen = false;
       for (int j = 0; j < n; ++j) {
-        ok = warp_wait(smem_u32(&c->sfull[t]), j & 1, p.ws, abort);
+        ok = warp_wait_after(seen, smem_u32(&c->sfull[t]), j & 1, p.ws, abort);
         if (!ok) break;
         fence_after();
         uint32_t s[COLS];
         if (any) {
 #pragma unroll
-          for (int k = 0; k < COLS; k += 32) tmem_ld32(at + F::S + t * COLS + k, s + k);
+          for (int k = 0; k < COLS; k += 32) tmem_ld32(s_at + k, s + k);
           tmem_wait();
           pin(s);
         }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c->sfree[t]));
-        uint32_t pk[COLS / 2];
+        seen = j == 0 || mbar_test(smem_u32(&c->pdone[t]), (j - 1) & 1);
+        bool grows = false, rescale = false;
         float grow = 1.f;
-        bool rescale = false;
         if (any) {
-          const int col0 = (w.item.begin + j) * COLS;
-          if (!__all_sync(0xffffffffu, hi >= (int64_t)col0 + COLS)) mask_cols(s, col0, 0, hi);
+          if (j >= whole) {
+            const int upto = cols_before<COLS>(hi, (int64_t)(w.item.begin + j) * COLS);
+#pragma unroll
+            for (int i = 0; i < COLS; ++i)
+              if (i >= upto) s[i] = 0xff800000u;  // -infinity
+          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < COLS; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(s[i]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if ((top - m) * p.c > GROWTH || (m == -INFINITY && top > m)) {
+          for (int i = 0; i < COLS; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          mx[0] = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          grows = (top - m) * p.c > GROWTH;  // also from no maximum to any
+          rescale = __any_sync(0xffffffffu, grows);
+          if (grows) {
             grow = exp2_approx((m - top) * p.c);
             m = top;
+            mc = -m * p.c;
             l *= grow;
           }
-          rescale = j > 0 && __any_sync(0xffffffffu, grow != 1.f);
-          const float mc = m == -INFINITY ? 0.f : -m * p.c;
+        }
+        if (j > 0) {  // the products that read P and write O are done
+          ok = warp_wait_after(seen, smem_u32(&c->pdone[t]), (j - 1) & 1, p.ws, abort);
+          if (!ok) break;
+          fence_after();
+        }
+        if (any) {
+          if (rescale && j > 0) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < PD; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + k, o);
+              tmem_wait();
+              pin(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * grow);
+              tmem_st16(o_at + k, o);
+              tmem_st16(o_at + k + 16, o + 16);
+            }
+          }
+          __syncwarp();
           const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(mc, mc);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < COLS / 2; ++i) {
-            float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
-            x.x = exp2_approx(x.x);
-            x.y = exp2_approx(x.y);
-            sum[i % 2] = add2(sum[i % 2], x);
-            pk[i] = f2_to_bf16x2(x.x, x.y);
+          for (int k = 0; k < COLS / 2; k += 16) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 x = fma2(make_float2(__uint_as_float(s[2 * (k + i)]), __uint_as_float(s[2 * (k + i) + 1])), c2, m2);
+              x.x = exp2_approx(x.x);
+              x.y = exp2_approx(x.y);
+              sum[i % 2] = add2(sum[i % 2], x);
+              pk[i] = f2_to_bf16x2(x.x, x.y);
+            }
+            tmem_st16(p_at + k, pk);
           }
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
         }
-        if (j > 0) {
-          ok = warp_wait(smem_u32(&c->pdone[t]), (j - 1) & 1, p.ws, abort);
-          if (!ok) break;
-          fence_after();
-        }
-        __syncwarp();
-        if (rescale) {
-#pragma unroll
-          for (int k = 0; k < PD; k += 32) {
-            uint32_t o[32];
-            tmem_ld32(at + F::O + t * PD + k, o);
-            tmem_wait();
-            pin(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * grow);
-            tmem_st16(at + F::O + t * PD + k, o);
-            tmem_st16(at + F::O + t * PD + k + 16, o + 16);
-          }
-        }
-        if (any) {
-#pragma unroll
-          for (int k = 0; k < COLS / 2; k += 16) tmem_st16(at + F::P + t * (COLS / 2) + k, pk + k);
-          tmem_st_wait();
-        }
+        seen = j + 1 < n && mbar_test(smem_u32(&c->sfull[t]), (j + 1) & 1);
+        if (any) tmem_st_wait();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c->pready[t]));

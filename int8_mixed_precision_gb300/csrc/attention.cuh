@@ -18,7 +18,8 @@ enum List { FORWARD, JOIN, GRAD_Q, GRAD_KV };
 // The head's dimensions as the tensor cores see them (columns behind dim are zeros that TMA fills in), and the
 // streamed operand's rows to a tile: as many as tensor memory holds beside the accumulators.
 __host__ __device__ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
-__host__ __device__ constexpr int tile_cols(int dim) { return dim <= 64 ? 128 : 64; }
+constexpr int FORWARD_COLS = 128;
+__host__ __device__ constexpr int tile_cols(int dim) { return dim <= 64 ? 128 : 64; }  // backward
 
 // The table, in int32: documents of DOC_INTS, items of ITEM_INTS (the four lists behind one another), and
 // DIT_ATTENTION_BUCKETS pairs (first item, items) for each list.
@@ -78,7 +79,7 @@ struct Work {
   bool ok;
 };
 __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attention_plan_t& p, int list, int heads, void* ws) {
-  Work w;
+  Work w = {};
   w.ok = false;
   const int2* bucket = reinterpret_cast<const int2*>(table + first_bucket(p, list));
   const int64_t at = blockIdx.x;
@@ -105,6 +106,19 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
   }
   if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
   __syncwarp();
+  // What follows from these is the same for all lanes: in uniform registers, where the MMAs and TMA want their operands.
+  w.doc.q0 = lora::uniform(w.doc.q0);
+  w.doc.queries = lora::uniform(w.doc.queries);
+  w.doc.k0 = lora::uniform(w.doc.k0);
+  w.doc.keys = lora::uniform(w.doc.keys);
+  w.doc.prefix = lora::uniform(w.doc.prefix);
+  w.doc.tile0 = lora::uniform(w.doc.tile0);
+  w.item.row0 = lora::uniform(w.item.row0);
+  w.item.begin = lora::uniform(w.item.begin);
+  w.item.end = lora::uniform(w.item.end);
+  w.item.slot = lora::uniform(w.item.slot);
+  w.head = lora::uniform(w.head);
+  w.ok = lora::uniform(w.ok);
   return w;
 }
 
@@ -146,6 +160,16 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(lora::DESC_HI)
       : "memory");
 }
+// Whether the phase of `parity` has completed, without waiting.  A wait for what has long completed takes 150 cycles; asked
+// ahead, the answer is there when it is needed, and only a warp that got no goes on to wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait_after(bool seen, uint32_t bar, uint32_t parity, void* ws, volatile int* abort) {
+  return __all_sync(0xffffffffu, seen) || lora::warp_wait(bar, parity, ws, abort);
+}
 // 32 accumulator columns of this thread's row; complete after lora::tmem_wait() and pin()
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
   asm volatile(
@@ -176,17 +200,21 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ float log2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Columns of a tile outside [lo, hi) become -infinity.
+// How many of a tile's columns lie in front of `end`: 0 to N.
 template <int N>
-__device__ __forceinline__ void mask_cols(uint32_t (&s)[N], int first, int64_t lo, int64_t hi) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (first + i < lo || first + i >= hi) s[i] = 0xff800000u;
+__device__ __forceinline__ int cols_before(int64_t end, int64_t first) {
+  const int64_t n = end - first;
+  return n < 0 ? 0 : n > N ? N : (int)n;
 }
 // Zeroes rows [from, rows) of a tile of 64-column chunks in shared memory (a row of a chunk is 128 bytes, whatever the
 // swizzle), by a whole warp: what lies behind a document's end must not meet the zeros of p or ds in a product, which

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   fence_after();
-  const uint32_t tmem = c->tmem;
+  const uint32_t tmem = uniform(c->tmem);
   volatile int* abort = &c->abort;
   pdl_wait();
 
@@ -134,85 +134,91 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int x0 = KEYS ? d.k0 : d.q0, y0 = KEYS ? d.q0 : d.k0;
   const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
-  // tile j of the stream: its first row in the document, and the head it belongs to
-  auto y_row = [&](int j) { return (w.item.begin + (KEYS ? j % tiles : j)) * COLS; };
-  auto q_head = [&](int j) { return KEYS ? w.head * p.group + j / tiles : w.head; };
 
   if (warp < 4) give_registers();
+  const uint32_t ring = smem + 2 * F::X_BYTES;
   if (warp == 0) {
     if (n > 0 && elect_one()) {
-      uint32_t ny = 0;
+      int s = 0, parity = 1, issued = 0;
       bool ok = true;
       if (!p.stall) {
         mbar_expect_tx(smem_u32(&c->xfull), 2 * F::X_BYTES);
         for (int i = 0; i < 2; ++i)
+#pragma unroll
           for (int k = 0; k < F::CHUNKS; ++k)
             tma_load_3d(smem + i * F::X_BYTES + k * F::X_CHUNK, i ? &mx2 : &mx1, smem_u32(&c->xfull), k * 64, w.head, x0 + row0);
       }
+      int tile = 0, head = KEYS ? w.head * p.group : w.head / p.group;
       for (int j = 0; j < n; ++j) {
-        const int s = j % F::STAGES;
-        if (j >= F::STAGES && !mbar_wait(smem_u32(&c->yempty[s]), ((j / F::STAGES) - 1) & 1, p.ws, abort)) {
+        if (j >= F::STAGES && !mbar_wait(smem_u32(&c->yempty[s]), parity, p.ws, abort)) {
           ok = false;
           break;
         }
-        if (p.stall) continue;
-        const uint32_t full = smem_u32(&c->yfull[s]);
-        const int row = y_row(j), head = q_head(j);
-        mbar_expect_tx(full, 2 * F::Y_BYTES + (KEYS ? F::STAT_BYTES : 0));
-        for (int i = 0; i < 2; ++i)
-          for (int k = 0; k < F::CHUNKS; ++k)
-            tma_load_3d(smem + 2 * F::X_BYTES + (i * F::STAGES + s) * F::Y_BYTES + k * F::Y_CHUNK, i ? &my2 : &my1, full, k * 64,
-                        KEYS ? head : w.head / p.group, y0 + row);
-        if (KEYS) {
-          const int64_t at = (int64_t)head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
-          bulk_load(smem + F::STATS + s * F::STAT_BYTES, p.lse + at, COLS * 4, full);
-          bulk_load(smem + F::STATS + s * F::STAT_BYTES + COLS * 4, p.delta + at, COLS * 4, full);
+        if (!p.stall) {
+          const uint32_t full = smem_u32(&c->yfull[s]), to = ring + s * F::Y_BYTES, stats = smem + F::STATS + s * F::STAT_BYTES;
+          const int row = (w.item.begin + tile) * COLS;
+          mbar_expect_tx(full, 2 * F::Y_BYTES + (KEYS ? F::STAT_BYTES : 0));
+#pragma unroll
+          for (int k = 0; k < F::CHUNKS; ++k) {
+            tma_load_3d(to + k * F::Y_CHUNK, &my1, full, k * 64, head, y0 + row);
+            tma_load_3d(to + F::STAGES * F::Y_BYTES + k * F::Y_CHUNK, &my2, full, k * 64, head, y0 + row);
+          }
+          if (KEYS) {
+            const int64_t at = (int64_t)head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
+            bulk_load(stats, p.lse + at, COLS * 4, full);
+            bulk_load(stats + COLS * 4, p.delta + at, COLS * 4, full);
+          }
+          issued = j + 1;
         }
-        ++ny;
+        if (++s == F::STAGES) s = 0, parity ^= 1;
+        if (++tile == tiles) tile = 0, head += KEYS;
       }
-      if (!ok || *abort) {  // its own copies land before the CTA ends
+      if ((!ok || *abort) && !p.stall) {  // its own copies land before the CTA ends
         volatile int never = 0;
-        if (!p.stall) mbar_wait(smem_u32(&c->xfull), 0, p.ws, &never);
-        for (uint32_t i = ny > F::STAGES ? ny - F::STAGES : 0; i < ny; ++i) mbar_wait(smem_u32(&c->yfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
+        mbar_wait(smem_u32(&c->xfull), 0, p.ws, &never);
+        for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i) mbar_wait(smem_u32(&c->yfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
       }
     }
   } else if (warp == 1) {
     if (n > 0) {
       const uint32_t id_s = idesc(128, COLS, false, false);
       const uint32_t id_a = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
-      const int steps = (p.plan.dim + 15) / 16;
       bool ok = warp_wait(smem_u32(&c->xfull), 0, p.ws, abort);
-      auto y_at = [&](int j, int i) { return smem + 2 * F::X_BYTES + (i * F::STAGES + j % F::STAGES) * F::Y_BYTES; };
-      auto scores = [&](int j) {  // S and T of tile j
-        ok = ok && warp_wait(smem_u32(&c->yfull[j % F::STAGES]), (j / F::STAGES) & 1, p.ws, abort);
-        if (!ok) return;
-        const int left = y_rows - y_row(j);
-        if (left < COLS)
-          for (int i = 0; i < 2; ++i) zero_rows(y_at(j, i), F::Y_CHUNK, F::CHUNKS, left, COLS);
-        if (j > 0) ok = warp_wait(smem_u32(&c->sfree), (j - 1) & 1, p.ws, abort);
+      int ss = 0, sp = 0, tile = 0;  // stage and parity of the next S and T, and their tile
+      auto scores = [&](bool first, int parity) {
+        const uint32_t y = ring + ss * F::Y_BYTES;
+        ok = ok && warp_wait(smem_u32(&c->yfull[ss]), sp, p.ws, abort);
+        const int left = y_rows - (w.item.begin + tile) * COLS;
+        if (ok && left < COLS) {
+          zero_rows(y, F::Y_CHUNK, F::CHUNKS, left, COLS);
+          zero_rows(y + F::STAGES * F::Y_BYTES, F::Y_CHUNK, F::CHUNKS, left, COLS);
+        }
+        if (!first) ok = ok && warp_wait(smem_u32(&c->sfree), parity, p.ws, abort);
         if (!ok) return;
         fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t a = desc_k(smem + i * F::X_BYTES), b = desc_k(y_at(j, i));
+            const uint32_t a = desc_k(smem + i * F::X_BYTES), b = desc_k(y + i * F::STAGES * F::Y_BYTES);
 #pragma unroll
             for (int k = 0; k < PD / 16; ++k)
-              if (k < steps)
-                mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id_s, k > 0);
+              mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id_s, k > 0);
           }
           mma_commit(smem_u32(&c->sfull));
         }
         __syncwarp();
+        if (++ss == F::STAGES) ss = 0, sp ^= 1;
+        if (++tile == tiles) tile = 0;
       };
-      scores(0);
+      scores(true, 0);
+      int s = 0;
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) scores(j + 1);
+        if (j + 1 < n) scores(false, j & 1);
         ok = ok && warp_wait(smem_u32(&c->pready), j & 1, p.ws, abort);
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          const uint32_t y1 = desc_mn(y_at(j, 0), F::Y_CHUNK), y2 = desc_mn(y_at(j, 1), F::Y_CHUNK);
+          const uint32_t y1 = desc_mn(ring + s * F::Y_BYTES, F::Y_CHUNK), y2 = desc_mn(ring + (F::STAGES + s) * F::Y_BYTES, F::Y_CHUNK);
           if (KEYS) {
 #pragma unroll
             for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::B, tmem + F::P + k * 8, y2 + k * (2048 >> 4), id_a, j > 0 || k > 0);
@@ -220,9 +226,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::A, tmem + F::DS + k * 8, y1 + k * (2048 >> 4), id_a, j > 0 || k > 0);
           mma_commit(smem_u32(&c->pdone));
-          mma_commit(smem_u32(&c->yempty[j % F::STAGES]));
+          mma_commit(smem_u32(&c->yempty[s]));
         }
         __syncwarp();
+        if (++s == F::STAGES) s = 0;
       }
       volatile int never = 0;
       if (elect_one()) mma_commit(smem_u32(&c->done));
@@ -251,6 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       delta = p.delta[i];
     }
     bool ok = true;
+    int stage = 0, tile = 0;
     for (int j = 0; j < n; ++j) {
       ok = warp_wait(smem_u32(&c->sfull), j & 1, p.ws, abort);
       if (!ok) break;
@@ -267,9 +275,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c->sfree));
-      const int col0 = y_row(j) + half * HALF;
-      const bool whole = __all_sync(0xffffffffu, lo <= col0 && hi >= (int64_t)col0 + HALF);
-      const uint32_t stats = smem + F::STATS + (j % F::STAGES) * F::STAT_BYTES + half * HALF * 4;
+      const int col0 = (w.item.begin + tile) * COLS + half * HALF;
+      const int from = cols_before<HALF>(lo, col0), to = cols_before<HALF>(hi, col0);
+      const bool whole = __all_sync(0xffffffffu, from == 0 && to == HALF);
+      const uint32_t stats = smem + F::STATS + stage * F::STAT_BYTES + half * HALF * 4;
       uint32_t pk[HALF / 2], dk[HALF / 2];
       const float2 c2 = make_float2(p.c, p.c);
       float l4[4] = {lse, lse, lse, lse}, d4[4] = {delta, delta, delta, delta};
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!whole) {  // masked pairs: p and ds are zero, whatever was there
 #pragma unroll
         for (int i = 0; i < HALF; ++i)
-          if (col0 + i < lo || col0 + i >= hi) s[i] = g[i] = 0u;
+          if (i < from || i >= to) s[i] = g[i] = 0u;
       }
 #pragma unroll
       for (int i = 0; i < HALF / 2; ++i) {
@@ -317,6 +326,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c->pready));
+      if (++stage == F::STAGES) stage = 0;
+      if (++tile == tiles) tile = 0;
     }
     if (n > 0 && ok) {
       ok = warp_wait(smem_u32(&c->pdone), (n - 1) & 1, p.ws, abort);

@@ -89,7 +89,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   for (size_t i = 0; i < docs.size(); ++i)
     for (int64_t r = 0; r < docs[i].queries; r += 2 * rt) {
       const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
-      const int64_t n = (seen_end(docs[i], frame, last) + cols - 1) / cols;
+      const int64_t n = (seen_end(docs[i], frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
       const double each = last - r >= rt ? 1.0 : 0.6;
       lists[FORWARD].push_back({Item{(int32_t)i, (int32_t)r, 0, (int32_t)n, -1, {0, 0, 0}}, START + each * (double)n});
     }

@@ -82,7 +82,7 @@ def lists(plan):
 def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     plan = dit.AttentionPlan(queries, heads, dim, kv_heads=kv_heads, kv_lengths=keys, frame=frame, prefix=prefix, training=True, device="cpu")
     docs, (fwd, joins, gq, gk), buckets = lists(plan)
-    cols, rt = (128 if dim <= 64 else 64), 128 // (heads // kv_heads)
+    cols, rt, back = 128, 128 // (heads // kv_heads), (128 if dim <= 64 else 64)
     assert plan.q_rows == sum(queries)
     for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
         at = 0
@@ -126,9 +126,9 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
             part = slice(row0, row0 + 128)
             whole[doc][part] += 1
             left = s[part].clone()
-            left[:, begin * cols:end * cols] = False
+            left[:, begin * back:end * back] = False
             assert not left.any()
-            assert end * cols < s.shape[1] + cols
+            assert end * back < s.shape[1] + back
         assert all((w == 1).all() for w in whole)
     # each document's statistics begin at a multiple of 128
     at = 0
