@@ -14,8 +14,8 @@
 // P is rounded to bf16 (an operand of the bf16 tensor pipe), 2^-8 of each weight at most; the sum of the weights is of the unrounded
 // ones.  Scores are scaled inside the exponent's multiply-add, in base 2.
 //
-// Warps: 0 loads, 1 issues the MMAs, 4 to 7 and 8 to 11 are the blocks' rows and take over most of the first four
-// warps' registers.  Every wait is bounded.
+// Warps: 0 loads, 1 issues S, 2 and 3 issue O += P V of a block each, 4 to 7 relay the MMAs' completion to the rows' warps, which are
+// 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  Every wait on memory is bounded.
 #include <limits.h>
 #include <math.h>
 
@@ -28,6 +28,7 @@ using namespace lora;
 
 constexpr float GROWTH = 8.f;
 constexpr int FWD_STAGES = 6;  // most
+using Regs = Registers<4, 128, 56, 200>;
 
 template <int PD>
 struct Fwd {
@@ -66,7 +67,7 @@ struct FwdArgs {
 };
 
 template <int PD>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Regs::THREADS, 1)
     k_attention(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ FwdArgs p) {
   pdl_launch_dependents();
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int blocks = w.ok && row0 + p.rows < d.queries ? 2 : 1;
   const bool work = n > 0 && (int64_t)w.item.end * COLS < (int64_t)d.keys + COLS;
 
-  if (warp < 4) give_registers();
+  if (warp < Regs::FIRST_ROWS) Regs::give();
   if (warp == 0) {
     if (work && elect_one()) {
       const uint32_t ring = smem + 2 * F::Q_BYTES;
@@ -231,9 +232,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         warp_wait(smem_u32(&c->done), 0, p.ws, &never);
       }
     }
-  } else if (warp >= 4) {
-    take_registers();
-    const int t = (warp - 4) / 4;
+  } else if (warp < Regs::FIRST_ROWS) {
+    const int t = warp % 2, what = (warp - 4) / 2;
+    if (work && t < blocks) relay(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, n, p.ws, abort);
+  } else {
+    Regs::take();
+    const int t = (warp - Regs::FIRST_ROWS) / 4;
     const int r = (warp % 4) * 32 + lane;  // this thread's row: a lane of tensor memory
     const int row = row0 + t * p.rows + r / p.group, head = w.head * p.group + r % p.group;
     const bool live = w.ok && t < blocks && r < p.rows * p.group && row < d.queries;
@@ -244,26 +248,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     // tiles up to the first one that some row does not see whole
     const int whole = __reduce_min_sync(0xffffffffu, (int)(min(hi, (int64_t)INT_MAX - COLS) / COLS)) - w.item.begin;
     float m = -INFINITY, mc = 0.f, l = 0.f;  // the maximum in use, -m c, and the sum
-    bool ok = true;
     if (work && t < blocks) {
       const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
-      bool seen = false;
+      const uint32_t sfree = smem_u32(&c->sfree[t]), pready = smem_u32(&c->pready[t]);
       for (int j = 0; j < n; ++j) {
-        ok = warp_wait_after(seen, smem_u32(&c->sfull[t]), j & 1, p.ws, abort);
-        if (!ok) break;
+        __syncwarp();
+        meet(1 + t);
         fence_after();
         uint32_t s[COLS];
+        float mx[4];
         if (any) {
 #pragma unroll
-          for (int k = 0; k < COLS; k += 32) tmem_ld32(s_at + k, s + k);
+          for (int k = 0; k < 4; ++k) tmem_ld32_max(s_at + k * 32, s + k * 32, mx[k]);
           tmem_wait();
           pin(s);
+          asm volatile("" : "+f"(mx[0]), "+f"(mx[1]), "+f"(mx[2]), "+f"(mx[3]));
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c->sfree[t]));
-        seen = j == 0 || mbar_test(smem_u32(&c->pdone[t]), (j - 1) & 1);
-        bool grows = false, rescale = false;
+        if (lane == 0) mbar_arrive(sfree);
+        bool rescale = false;
         float grow = 1.f;
         if (any) {
           if (j >= whole) {
@@ -271,13 +275,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < COLS; ++i)
               if (i >= upto) s[i] = 0xff800000u;  // -infinity
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < COLS; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          mx[0] = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < COLS; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          }
           const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          grows = (top - m) * p.c > GROWTH;  // also from no maximum to any
+          const bool grows = (top - m) * p.c > GROWTH;  // also from no maximum to any
           rescale = __any_sync(0xffffffffu, grows);
           if (grows) {
             grow = exp2_approx((m - top) * p.c);
@@ -286,14 +290,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             l *= grow;
           }
         }
+        __syncwarp();
         if (j > 0) {  // the products that read P and write O are done
-          ok = warp_wait_after(seen, smem_u32(&c->pdone[t]), (j - 1) & 1, p.ws, abort);
-          if (!ok) break;
+          meet(3 + t);
           fence_after();
         }
         if (any) {
           if (rescale && j > 0) {
-            __syncwarp();
 #pragma unroll
             for (int k = 0; k < PD; k += 32) {
               uint32_t o[32];
@@ -306,7 +309,6 @@ __global__ void __launch_bounds__(THREADS, 1)
               tmem_st16(o_at + k + 16, o + 16);
             }
           }
-          __syncwarp();
           const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(mc, mc);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -324,18 +326,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
+          tmem_st_wait();
         }
-        seen = j + 1 < n && mbar_test(smem_u32(&c->sfull[t]), (j + 1) & 1);
-        if (any) tmem_st_wait();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c->pready[t]));
+        if (lane == 0) mbar_arrive(pready);
       }
-      if (ok) {
-        ok = warp_wait(smem_u32(&c->pdone[t]), (n - 1) & 1, p.ws, abort);
-        fence_after();
-      }
+      __syncwarp();
+      meet(3 + t);
+      fence_after();
     }
+    const bool ok = !__any_sync(0xffffffffu, *abort);
     if (ok && any) {  // a warp's loads of tensor memory are whole; what is not live is not stored
       const bool empty = !live || hi == 0 || !work;
       const float inv = 1.f / l;
@@ -431,8 +432,8 @@ static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads
   if (!map_heads(&mq, q, a.plan.dim, a.plan.heads, a.plan.q_rows, a.group, a.rows) ||
       !map_heads(&mk, keys ? k : q, a.plan.dim, k_heads, k_rows, 1, F::COLS) || !map_heads(&mv, keys ? v : q, a.plan.dim, k_heads, k_rows, 1, F::COLS))
     return DIT_ERR_CUDA;
-  if (prepare_kernel(checked, once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
-  if (launch_pdl(k_attention<PD>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
+  if (prepare_kernel<Regs>(checked, once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  if (launch_pdl(k_attention<PD>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads)), dim3(256), 0, st, 1, a) != cudaSuccess)
     return DIT_ERR_CUDA;

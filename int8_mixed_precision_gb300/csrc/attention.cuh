@@ -127,16 +127,18 @@ dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, He
 bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows);
 
 // ---------------------------------------------------------------------------------------
-// A CTA of three warpgroups: one loads and issues, two hold a tile's rows in registers and take over most of the first
-// one's.  The block is launched with 3 x LAUNCH_REGS registers a thread and the shares add up to those:
-// taking more than the launch brought would wait for ever, so the host checks what the kernel was compiled to.
+// A CTA of warpgroups that load and issue and of two that hold a tile's rows in registers and take over what the first
+// ones need not.  The block is launched with so many registers a thread and the shares add up to those: taking
+// more than the launch brought would wait for ever, so the host checks what the kernel was compiled to.
 // ---------------------------------------------------------------------------------------
-constexpr int THREADS = 384;
-constexpr int LAUNCH_REGS = 168, ISSUE_REGS = 72, ROW_REGS = 216;
-static_assert(ISSUE_REGS + 2 * ROW_REGS <= 3 * LAUNCH_REGS, "");
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE_REGS)); }
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROW_REGS)); }
-template <typename... KArgs>
+template <int WARPGROUPS, int LAUNCH, int ISSUE, int ROWS>
+struct Registers {
+  static constexpr int THREADS = 128 * WARPGROUPS, LAUNCHED = LAUNCH, FIRST_ROWS = 4 * (WARPGROUPS - 2);
+  static_assert((WARPGROUPS - 2) * ISSUE + 2 * ROWS <= WARPGROUPS * LAUNCH && THREADS * LAUNCH <= 65536, "");
+  static __device__ __forceinline__ void give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE)); }
+  static __device__ __forceinline__ void take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROWS)); }
+};
+template <typename R, typename... KArgs>
 cudaError_t prepare_kernel(OncePerDevice& checked, OncePerDevice& once, void (*kern)(KArgs...), int smem) {
   int device = 0;
   const cudaError_t e = cudaGetDevice(&device);
@@ -144,7 +146,7 @@ cudaError_t prepare_kernel(OncePerDevice& checked, OncePerDevice& once, void (*k
   const cudaError_t fits = checked.run(device, [&] {
     cudaFuncAttributes a;
     const cudaError_t got = cudaFuncGetAttributes(&a, kern);
-    return got != cudaSuccess ? got : a.numRegs == LAUNCH_REGS ? cudaSuccess : cudaErrorInvalidKernelImage;
+    return got != cudaSuccess ? got : a.numRegs == R::LAUNCHED ? cudaSuccess : cudaErrorInvalidKernelImage;
   });
   return fits == cudaSuccess ? opt_in_smem(once, kern, smem) : fits;
 }
@@ -160,15 +162,31 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(lora::DESC_HI)
       : "memory");
 }
-// Whether the phase of `parity` has completed, without waiting.  A wait for what has long completed takes 150 cycles; asked
-// ahead, the answer is there when it is needed, and only a warp that got no goes on to wait.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
+// A block of 128 rows' warps and their relay meet.  Looking at an mbarrier takes a warp 130 to 160 cycles even where its phase
+// has long completed; a warp of its own does that ahead of the row warps, whose barrier costs them a few dozen.
+__device__ __forceinline__ void meet(int barrier) { asm volatile("barrier.cta.sync.aligned %0, 160;" ::"r"(barrier) : "memory"); }
+// The relay: passes on the completion of `n` phases.  It meets the row warps in each round, whatever its waits say, so
+// that none is left behind; they look at the flag at the end.
+__device__ __forceinline__ void relay(uint32_t bar, int barrier, int n, void* ws, volatile int* abort) {
+  for (int j = 0; j < n; ++j) {
+    if (!__any_sync(0xffffffffu, *abort)) lora::warp_wait(bar, j & 1, ws, abort);
+    lora::fence_after();
+    lora::fence_before();
+    __syncwarp();
+    meet(barrier);
+  }
 }
-__device__ __forceinline__ bool warp_wait_after(bool seen, uint32_t bar, uint32_t parity, void* ws, volatile int* abort) {
-  return __all_sync(0xffffffffu, seen) || lora::warp_wait(bar, parity, ws, abort);
+// 32 accumulator columns of this thread's row and the largest of them (NaN counts for nothing); complete after lora::tmem_wait()
+// and pin()
+__device__ __forceinline__ void tmem_ld32_max(uint32_t addr, uint32_t* r, float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+      : "r"(addr));
 }
 // 32 accumulator columns of this thread's row; complete after lora::tmem_wait() and pin()
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {

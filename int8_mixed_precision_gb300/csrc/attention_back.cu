@@ -24,6 +24,7 @@ namespace attn {
 using namespace lora;
 
 constexpr int BACK_STAGES = 5;  // most
+using Regs = Registers<3, 168, 72, 216>;
 
 template <int PD>
 struct Back {
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__
 }
 
 template <int PD, bool KEYS>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Regs::THREADS, 1)
     k_attention_back(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
                      const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2, const __grid_constant__ BackArgs p) {
   pdl_launch_dependents();
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
 
-  if (warp < 4) give_registers();
+  if (warp < 4) Regs::give();
   const uint32_t ring = smem + 2 * F::X_BYTES;
   if (warp == 0) {
     if (n > 0 && elect_one()) {
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       warp_wait(smem_u32(&c->done), 0, p.ws, &never);
     }
   } else if (warp >= 4) {
-    take_registers();
+    Regs::take();
     const int half = (warp - 4) / 4;
     const int r = (warp % 4) * 32 + lane;
     const int row = row0 + r;
@@ -387,9 +388,9 @@ static dit_status launch(BackArgs a, const Inputs& in, cudaStream_t st) {
   const int q_box = KEYS ? F::COLS : TILE, k_box = KEYS ? TILE : F::COLS;
   if (!map(&mq, in.q, in.k, true, q_box) || !map(&mo, in.dout, in.v, true, q_box) || !map(&mk, in.k, in.q, false, k_box) || !map(&mv, in.v, in.dout, false, k_box))
     return DIT_ERR_CUDA;
-  if (prepare_kernel(checked, once, k_attention_back<PD, KEYS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
-  const cudaError_t e = KEYS ? launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mk, mv, mq, mo, a)
-                             : launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(THREADS), F::SMEM, st, 1, mq, mo, mk, mv, a);
+  if (prepare_kernel<Regs>(checked, once, k_attention_back<PD, KEYS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  const cudaError_t e = KEYS ? launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mk, mv, mq, mo, a)
+                             : launch_pdl(k_attention_back<PD, KEYS>, dim3((unsigned)(items * heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mo, mk, mv, a);
   return e == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
