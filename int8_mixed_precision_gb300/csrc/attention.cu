@@ -251,52 +251,51 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     if (work && t < blocks) {
       const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
       const uint32_t sfree = smem_u32(&c->sfree[t]), pready = smem_u32(&c->pready[t]);
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n && !any; ++j) {  // rows behind the last one alone: nothing to do but to keep step
+        __syncwarp();
+        meet(1 + t);
+        if (lane == 0) mbar_arrive(sfree);
+        __syncwarp();
+        if (j > 0) meet(3 + t);
+        if (lane == 0) mbar_arrive(pready);
+      }
+      for (int j = 0; j < n && any; ++j) {
         __syncwarp();
         meet(1 + t);
         fence_after();
         uint32_t s[COLS];
         float mx[4];
-        if (any) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32_max(s_at + k * 32, s + k * 32, mx[k]);
-          tmem_wait();
-          pin(s);
-          asm volatile("" : "+f"(mx[0]), "+f"(mx[1]), "+f"(mx[2]), "+f"(mx[3]));
-        }
+        for (int k = 0; k < 4; ++k) tmem_ld32_max(s_at + k * 32, s + k * 32, mx[k]);
+        tmem_wait();
+        pin(s);
+        asm volatile("" : "+f"(mx[0]), "+f"(mx[1]), "+f"(mx[2]), "+f"(mx[3]));
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree);
-        bool rescale = false;
-        float grow = 1.f;
-        if (any) {
-          if (j >= whole) {
-            const int upto = cols_before<COLS>(hi, (int64_t)(w.item.begin + j) * COLS);
+        if (j >= whole) {
+          const int upto = cols_before<COLS>(hi, (int64_t)(w.item.begin + j) * COLS);
 #pragma unroll
-            for (int i = 0; i < COLS; ++i)
-              if (i >= upto) s[i] = 0xff800000u;  // -infinity
+          for (int i = 0; i < COLS; ++i)
+            if (i >= upto) s[i] = 0xff800000u;  // -infinity
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+          for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < COLS; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          }
-          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          const bool grows = (top - m) * p.c > GROWTH;  // also from no maximum to any
-          rescale = __any_sync(0xffffffffu, grows);
-          if (grows) {
-            grow = exp2_approx((m - top) * p.c);
-            m = top;
-            mc = -m * p.c;
-            l *= grow;
-          }
+          for (int i = 0; i < COLS; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
         }
-        __syncwarp();
+        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        const bool moves = __any_sync(0xffffffffu, (top - m) * p.c > GROWTH);  // also from no maximum to any
         if (j > 0) {  // the products that read P and write O are done
           meet(3 + t);
           fence_after();
         }
-        if (any) {
-          if (rescale && j > 0) {
+        if (moves) {
+          const float next = (top - m) * p.c > GROWTH ? top : m;
+          const float grow = next == m ? 1.f : exp2_approx((m - next) * p.c);
+          m = next;
+          mc = m == -INFINITY ? 0.f : -m * p.c;
+          l *= grow;
+          if (j > 0) {
 #pragma unroll
             for (int k = 0; k < PD; k += 32) {
               uint32_t o[32];
@@ -309,25 +308,25 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
               tmem_st16(o_at + k + 16, o + 16);
             }
           }
-          const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(mc, mc);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int k = 0; k < COLS / 2; k += 16) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 x = fma2(make_float2(__uint_as_float(s[2 * (k + i)]), __uint_as_float(s[2 * (k + i) + 1])), c2, m2);
-              x.x = exp2_approx(x.x);
-              x.y = exp2_approx(x.y);
-              sum[i % 2] = add2(sum[i % 2], x);
-              pk[i] = f2_to_bf16x2(x.x, x.y);
-            }
-            tmem_st16(p_at + k, pk);
-          }
-          const float2 both = add2(sum[0], sum[1]);
-          l += both.x + both.y;
-          tmem_st_wait();
         }
+        const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(mc, mc);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int k = 0; k < COLS / 2; k += 16) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 x = fma2(make_float2(__uint_as_float(s[2 * (k + i)]), __uint_as_float(s[2 * (k + i) + 1])), c2, m2);
+            x.x = exp2_approx(x.x);
+            x.y = exp2_approx(x.y);
+            sum[i % 2] = add2(sum[i % 2], x);
+            pk[i] = f2_to_bf16x2(x.x, x.y);
+          }
+          tmem_st16(p_at + k, pk);
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        tmem_st_wait();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pready);
