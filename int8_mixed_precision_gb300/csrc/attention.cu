@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     }
   } else if (warp < Regs::FIRST_ROWS) {
     const int t = warp % 2, what = (warp - 4) / 2;
-    if (work && t < blocks) relay(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, n, p.ws, abort);
+    if (work && t < blocks) relay<160>(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, n, p.ws, abort);
   } else {
     Regs::take();
     const int t = (warp - Regs::FIRST_ROWS) / 4;
@@ -253,15 +253,15 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       const uint32_t sfree = smem_u32(&c->sfree[t]), pready = smem_u32(&c->pready[t]);
       for (int j = 0; j < n && !any; ++j) {  // rows behind the last one alone: nothing to do but to keep step
         __syncwarp();
-        meet(1 + t);
+        meet<160>(1 + t);
         if (lane == 0) mbar_arrive(sfree);
         __syncwarp();
-        if (j > 0) meet(3 + t);
+        if (j > 0) meet<160>(3 + t);
         if (lane == 0) mbar_arrive(pready);
       }
       for (int j = 0; j < n && any; ++j) {
         __syncwarp();
-        meet(1 + t);
+        meet<160>(1 + t);
         fence_after();
         uint32_t s[COLS];
         float mx[4];
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         const bool moves = __any_sync(0xffffffffu, (top - m) * p.c > GROWTH);  // also from no maximum to any
         if (j > 0) {  // the products that read P and write O are done
-          meet(3 + t);
+          meet<160>(3 + t);
           fence_after();
         }
         if (moves) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         if (lane == 0) mbar_arrive(pready);
       }
       __syncwarp();
-      meet(3 + t);
+      meet<160>(3 + t);
       fence_after();
     }
     const bool ok = !__any_sync(0xffffffffu, *abort);

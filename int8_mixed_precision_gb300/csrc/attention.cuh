@@ -162,18 +162,22 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(accumulate ? 1u : 0u), "n"(lora::DESC_HI)
       : "memory");
 }
-// A block of 128 rows' warps and their relay meet.  Looking at an mbarrier takes a warp 130 to 160 cycles even where its phase
+// The row warps (of THREADS with their relay) and the relay meet.  Looking at an mbarrier takes a warp 130 to 160 cycles even where its phase
 // has long completed; a warp of its own does that ahead of the row warps, whose barrier costs them a few dozen.
-__device__ __forceinline__ void meet(int barrier) { asm volatile("barrier.cta.sync.aligned %0, 160;" ::"r"(barrier) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void meet(int barrier) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(barrier), "n"(THREADS) : "memory");
+}
 // The relay: passes on the completion of `n` phases.  It meets the row warps in each round, whatever its waits say, so
 // that none is left behind; they look at the flag at the end.
+template <int THREADS>
 __device__ __forceinline__ void relay(uint32_t bar, int barrier, int n, void* ws, volatile int* abort) {
   for (int j = 0; j < n; ++j) {
     if (!__any_sync(0xffffffffu, *abort)) lora::warp_wait(bar, j & 1, ws, abort);
     lora::fence_after();
     lora::fence_before();
     __syncwarp();
-    meet(barrier);
+    meet<THREADS>(barrier);
   }
 }
 // 32 accumulator columns of this thread's row and the largest of them (NaN counts for nothing); complete after lora::tmem_wait()

@@ -14,6 +14,7 @@
 // S and T lie in tensor memory; p and ds go back there in bf16 as A operands of the next products (each rounding at most 2^-8 of its
 // value), so nothing but the streamed tiles passes through shared memory.  The next tile's S and T are made while the
 // warps work at the present one's.  Two warpgroups share a tile's columns.
+#include <limits.h>
 #include <math.h>
 
 #include "attention.cuh"
@@ -24,7 +25,7 @@ namespace attn {
 using namespace lora;
 
 constexpr int BACK_STAGES = 5;  // most
-using Regs = Registers<3, 168, 72, 216>;
+using Regs = Registers<4, 128, 56, 200>;
 
 template <int PD>
 struct Back {
@@ -106,14 +107,14 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   if (warp == 0) {
     if (lane < F::STAGES) {
       mbar_init(smem_u32(&c->yfull[lane]), 1);
-      mbar_init(smem_u32(&c->yempty[lane]), 1);
+      mbar_init(smem_u32(&c->yempty[lane]), KEYS ? 2 : 1);
     } else if (lane == 8) {
       mbar_init(smem_u32(&c->xfull), 1);
-      mbar_init(smem_u32(&c->done), 1);
+      mbar_init(smem_u32(&c->done), 3);
       mbar_init(smem_u32(&c->sfull), 1);
       mbar_init(smem_u32(&c->sfree), 8);
       mbar_init(smem_u32(&c->pready), 8);
-      mbar_init(smem_u32(&c->pdone), 1);
+      mbar_init(smem_u32(&c->pdone), KEYS ? 2 : 1);
       c->abort = 0;
     }
     fence_barrier_init();
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
 
-  if (warp < 4) Regs::give();
+  if (warp < Regs::FIRST_ROWS) Regs::give();
   const uint32_t ring = smem + 2 * F::X_BYTES;
   if (warp == 0) {
     if (n > 0 && elect_one()) {
@@ -181,21 +182,20 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (n > 0) {
-      const uint32_t id_s = idesc(128, COLS, false, false);
-      const uint32_t id_a = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
+    if (n > 0) {  // S and T of each tile, once the rows' warps have the tile before in registers
+      constexpr uint32_t id = idesc(128, COLS, false, false);
       bool ok = warp_wait(smem_u32(&c->xfull), 0, p.ws, abort);
-      int ss = 0, sp = 0, tile = 0;  // stage and parity of the next S and T, and their tile
-      auto scores = [&](bool first, int parity) {
-        const uint32_t y = ring + ss * F::Y_BYTES;
-        ok = ok && warp_wait(smem_u32(&c->yfull[ss]), sp, p.ws, abort);
+      int s = 0, parity = 0, tile = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t y = ring + s * F::Y_BYTES;
+        ok = warp_wait(smem_u32(&c->yfull[s]), parity, p.ws, abort);
         const int left = y_rows - (w.item.begin + tile) * COLS;
         if (ok && left < COLS) {
           zero_rows(y, F::Y_CHUNK, F::CHUNKS, left, COLS);
           zero_rows(y + F::STAGES * F::Y_BYTES, F::Y_CHUNK, F::CHUNKS, left, COLS);
         }
-        if (!first) ok = ok && warp_wait(smem_u32(&c->sfree), parity, p.ws, abort);
-        if (!ok) return;
+        if (j > 0) ok = ok && warp_wait(smem_u32(&c->sfree), (j - 1) & 1, p.ws, abort);
+        if (!ok) break;
         fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -203,43 +203,52 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
             const uint32_t a = desc_k(smem + i * F::X_BYTES), b = desc_k(y + i * F::STAGES * F::Y_BYTES);
 #pragma unroll
             for (int k = 0; k < PD / 16; ++k)
-              mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id_s, k > 0);
+              mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id, k > 0);
           }
           mma_commit(smem_u32(&c->sfull));
         }
         __syncwarp();
-        if (++ss == F::STAGES) ss = 0, sp ^= 1;
+        if (++s == F::STAGES) s = 0, parity ^= 1;
         if (++tile == tiles) tile = 0;
-      };
-      scores(true, 0);
+      }
+      if (elect_one()) mma_commit(smem_u32(&c->done));
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    const bool second = warp == 3;  // B += P Y2, else A += dS Y1
+    if (n > 0 && (KEYS || !second)) {
+      const uint32_t id = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
+      const uint32_t a = tmem + (second ? F::P : F::DS), to = tmem + (second ? F::B : F::A), y = ring + (second ? F::STAGES * F::Y_BYTES : 0);
+      bool ok = true;
       int s = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) scores(false, j & 1);
-        ok = ok && warp_wait(smem_u32(&c->pready), j & 1, p.ws, abort);
+      for (int j = 0; j < n; ++j) {
+        ok = warp_wait(smem_u32(&c->pready), j & 1, p.ws, abort);  // the tile has long been there: S and T were made of it
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          const uint32_t y1 = desc_mn(ring + s * F::Y_BYTES, F::Y_CHUNK), y2 = desc_mn(ring + (F::STAGES + s) * F::Y_BYTES, F::Y_CHUNK);
-          if (KEYS) {
+          const uint32_t b = desc_mn(y + s * F::Y_BYTES, F::Y_CHUNK);
 #pragma unroll
-            for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::B, tmem + F::P + k * 8, y2 + k * (2048 >> 4), id_a, j > 0 || k > 0);
-          }
-#pragma unroll
-          for (int k = 0; k < COLS / 16; ++k) mma_ta(tmem + F::A, tmem + F::DS + k * 8, y1 + k * (2048 >> 4), id_a, j > 0 || k > 0);
+          for (int k = 0; k < COLS / 16; ++k) mma_ta(to, a + k * 8, b + k * (2048 >> 4), id, j > 0 || k > 0);
           mma_commit(smem_u32(&c->pdone));
           mma_commit(smem_u32(&c->yempty[s]));
         }
         __syncwarp();
         if (++s == F::STAGES) s = 0;
       }
-      volatile int never = 0;
+    }
+    if (n > 0) {
       if (elect_one()) mma_commit(smem_u32(&c->done));
       __syncwarp();
-      warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+      if (!second) {  // every MMA has completed before the CTA ends
+        volatile int never = 0;
+        warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+      }
     }
-  } else if (warp >= 4) {
+  } else if (warp < Regs::FIRST_ROWS) {
+    if (warp < 6 && n > 0) relay<288>(smem_u32(warp == 4 ? &c->sfull : &c->pdone), warp - 3, n, p.ws, abort);
+  } else {
     Regs::take();
-    const int half = (warp - 4) / 4;
+    const int half = (warp - Regs::FIRST_ROWS) / 4;
     const int r = (warp % 4) * 32 + lane;
     const int row = row0 + r;
     const bool live = w.ok && row < x_rows;
@@ -252,88 +261,92 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     } else if (live) {
       hi = seen_end(d, p.plan.frame, row);
     }
+    // tiles that every row of the warp meets whole
+    const int whole_from = __reduce_max_sync(0xffffffffu, (int)min((lo + COLS - 1) / COLS, (int64_t)INT_MAX));
+    const int whole_to = __reduce_min_sync(0xffffffffu, (int)min(hi / COLS, (int64_t)INT_MAX));
     float lse = 0.f, delta = 0.f;
     if (!KEYS && live) {
       const int64_t i = (int64_t)w.head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
-      lse = p.lse[i];
-      delta = p.delta[i];
+      lse = -p.lse[i];
+      delta = -p.delta[i];
     }
-    bool ok = true;
-    int stage = 0, tile = 0;
+    const uint32_t s_at = at + F::S + half * HALF, t_at = at + F::T + half * HALF, p_at = at + F::P + half * (HALF / 2), ds_at = at + F::DS + half * (HALF / 2);
+    const uint32_t sfree = smem_u32(&c->sfree), pready = smem_u32(&c->pready);
+    const float2 c2 = make_float2(p.c, p.c);
+    int stage = 0, tile = w.item.begin;
     for (int j = 0; j < n; ++j) {
-      ok = warp_wait(smem_u32(&c->sfull), j & 1, p.ws, abort);
-      if (!ok) break;
+      __syncwarp();
+      meet<288>(1);
       fence_after();
       uint32_t s[HALF], g[HALF];
 #pragma unroll
       for (int k = 0; k < HALF; k += 32) {
-        tmem_ld32(at + F::S + half * HALF + k, s + k);
-        tmem_ld32(at + F::T + half * HALF + k, g + k);
+        tmem_ld32(s_at + k, s + k);
+        tmem_ld32(t_at + k, g + k);
       }
       tmem_wait();
       pin(s);
       pin(g);
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c->sfree));
-      const int col0 = (w.item.begin + tile) * COLS + half * HALF;
-      const int from = cols_before<HALF>(lo, col0), to = cols_before<HALF>(hi, col0);
-      const bool whole = __all_sync(0xffffffffu, from == 0 && to == HALF);
+      if (lane == 0) mbar_arrive(sfree);
       const uint32_t stats = smem + F::STATS + stage * F::STAT_BYTES + half * HALF * 4;
-      uint32_t pk[HALF / 2], dk[HALF / 2];
-      const float2 c2 = make_float2(p.c, p.c);
       float l4[4] = {lse, lse, lse, lse}, d4[4] = {delta, delta, delta, delta};
 #pragma unroll
       for (int i = 0; i < HALF; i += 4) {
         if (KEYS) {  // the columns' own
           const uint4 l = lds128(stats + i * 4), d = lds128(stats + COLS * 4 + i * 4);
-          l4[0] = __uint_as_float(l.x), l4[1] = __uint_as_float(l.y), l4[2] = __uint_as_float(l.z), l4[3] = __uint_as_float(l.w);
-          d4[0] = __uint_as_float(d.x), d4[1] = __uint_as_float(d.y), d4[2] = __uint_as_float(d.z), d4[3] = __uint_as_float(d.w);
+          l4[0] = -__uint_as_float(l.x), l4[1] = -__uint_as_float(l.y), l4[2] = -__uint_as_float(l.z), l4[3] = -__uint_as_float(l.w);
+          d4[0] = -__uint_as_float(d.x), d4[1] = -__uint_as_float(d.y), d4[2] = -__uint_as_float(d.z), d4[3] = -__uint_as_float(d.w);
         }
 #pragma unroll
         for (int h = 0; h < 4; h += 2) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[i + h]), __uint_as_float(s[i + h + 1])), c2, make_float2(-l4[h], -l4[h + 1]));
-          const float2 t = sub2(make_float2(__uint_as_float(g[i + h]), __uint_as_float(g[i + h + 1])), make_float2(d4[h], d4[h + 1]));
+          const float2 x = fma2(make_float2(__uint_as_float(s[i + h]), __uint_as_float(s[i + h + 1])), c2, make_float2(l4[h], l4[h + 1]));
+          const float2 t = add2(make_float2(__uint_as_float(g[i + h]), __uint_as_float(g[i + h + 1])), make_float2(d4[h], d4[h + 1]));
           s[i + h] = __float_as_uint(exp2_approx(x.x));
           s[i + h + 1] = __float_as_uint(exp2_approx(x.y));
           g[i + h] = __float_as_uint(t.x);
           g[i + h + 1] = __float_as_uint(t.y);
         }
       }
-      if (!whole) {  // masked pairs: p and ds are zero, whatever was there
+      if (tile < whole_from || tile >= whole_to) {  // masked pairs: p and ds are zero, whatever was there
+        const int64_t col0 = (int64_t)tile * COLS + half * HALF;
+        const int from = cols_before<HALF>(lo, col0), to = cols_before<HALF>(hi, col0);
 #pragma unroll
         for (int i = 0; i < HALF; ++i)
           if (i < from || i >= to) s[i] = g[i] = 0u;
       }
-#pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) {
-        const float2 e = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-        const float2 t = mul2(e, make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1])));
-        if (KEYS) pk[i] = f2_to_bf16x2(e.x, e.y);
-        dk[i] = f2_to_bf16x2(t.x, t.y);
-      }
-      if (j > 0) {
-        ok = warp_wait(smem_u32(&c->pdone), (j - 1) & 1, p.ws, abort);
-        if (!ok) break;
+      __syncwarp();
+      if (j > 0) {  // the products that read P and dS are done
+        meet<288>(2);
         fence_after();
       }
-      __syncwarp();
 #pragma unroll
       for (int k = 0; k < HALF / 2; k += 16) {
-        if (KEYS) tmem_st16(at + F::P + half * (HALF / 2) + k, pk + k);
-        tmem_st16(at + F::DS + half * (HALF / 2) + k, dk + k);
+        uint32_t pk[16], dk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 e = make_float2(__uint_as_float(s[2 * (k + i)]), __uint_as_float(s[2 * (k + i) + 1]));
+          const float2 t = mul2(e, make_float2(__uint_as_float(g[2 * (k + i)]), __uint_as_float(g[2 * (k + i) + 1])));
+          if (KEYS) pk[i] = f2_to_bf16x2(e.x, e.y);
+          dk[i] = f2_to_bf16x2(t.x, t.y);
+        }
+        if (KEYS) tmem_st16(p_at + k, pk);
+        tmem_st16(ds_at + k, dk);
       }
       tmem_st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c->pready));
+      if (lane == 0) mbar_arrive(pready);
       if (++stage == F::STAGES) stage = 0;
-      if (++tile == tiles) tile = 0;
+      if (++tile == w.item.end) tile = w.item.begin;
     }
-    if (n > 0 && ok) {
-      ok = warp_wait(smem_u32(&c->pdone), (n - 1) & 1, p.ws, abort);
+    if (n > 0) {
+      __syncwarp();
+      meet<288>(2);
       fence_after();
     }
+    const bool ok = !__any_sync(0xffffffffu, *abort);
     if (ok) {
 #pragma unroll
       for (int out = 0; out < (KEYS ? 2 : 1); ++out) {
