@@ -13,7 +13,11 @@
 //
 // S and T lie in tensor memory; p and ds go back there in bf16 as A operands of the next products (each rounding at most 2^-8 of its
 // value), so nothing but the streamed tiles passes through shared memory.  The next tile's S and T are made while the
-// warps work at the present one's.  Two warpgroups share a tile's columns.
+// warps work at the present one's.  Where tensor memory holds two of everything, the two warpgroups work at tiles in turn
+// (STREAMS 2), so that one's exponentials hide the other's waits; else they share each tile's columns.
+//
+// Warps: 0 loads; 1 and 6 issue S and T of a stream each; 2 issues A, 3 B; 4, 5 and 7 relay the MMAs' completion; the others hold
+// the rows and take over most of the first ones' registers.  Every wait on memory is bounded.
 #include <limits.h>
 #include <math.h>
 
@@ -24,26 +28,30 @@ namespace attn {
 
 using namespace lora;
 
-constexpr int BACK_STAGES = 5;  // most
+constexpr int BACK_STAGES = 10;  // most
 using Regs = Registers<4, 128, 56, 200>;
 
-template <int PD>
+template <int PD, bool KEYS>
 struct Back {
-  static constexpr int COLS = tile_cols(PD);
+  static constexpr int COLS = BACK_COLS;
+  static constexpr int STREAMS = PD == 64 || !KEYS ? 2 : 1;
+  static constexpr int MINE = COLS * STREAMS / 2;  // columns of a thread
   static constexpr int CHUNKS = PD / 64;
   static constexpr int X_CHUNK = TILE * 128, X_BYTES = CHUNKS * X_CHUNK;
   static constexpr int Y_CHUNK = COLS * 128, Y_BYTES = CHUNKS * Y_CHUNK;
-  static constexpr int STAGES = PD == 64 ? 5 : 4;
+  static constexpr int STAGES = PD == 64 ? 10 : 4;
   static constexpr int STATS = 2 * X_BYTES + 2 * STAGES * Y_BYTES;  // lse and delta of a stage's columns
   static constexpr int STAT_BYTES = 2 * COLS * 4;
   static constexpr int CONTROL = STATS + STAGES * STAT_BYTES;
   static constexpr int SMEM = CONTROL + 1024 + 1024;
-  static constexpr uint32_t S = 0, T = COLS, P = 2 * COLS, DS = P + COLS / 2, A = 3 * COLS, B = A + PD;
-  static_assert(3 * COLS + 2 * PD <= 512 && SMEM <= 227 * 1024, "");
+  // tensor memory: S and T of each stream, p and dS of each stream, A, B
+  static constexpr uint32_t S = 0, T = COLS, S_STEP = 2 * COLS, P = STREAMS * S_STEP, DS = P + COLS / 2, P_STEP = COLS, A = P + STREAMS * P_STEP, B = A + PD;
+  static constexpr int MMA_WARPS = STREAMS + 1 + KEYS, ROW_WARPS = 8 / STREAMS, MEET = 32 + 32 * ROW_WARPS;
+  static_assert((KEYS ? B : A) + PD <= 512 && SMEM <= 227 * 1024, "");
 };
 
 struct BackControl {
-  uint64_t xfull, done, sfull, sfree, pready, pdone;
+  uint64_t xfull, done, sfull[2], sfree[2], pready[2], pdone[2];
   uint64_t yfull[BACK_STAGES], yempty[BACK_STAGES];
   uint32_t tmem;
   int abort;
@@ -97,8 +105,8 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     k_attention_back(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
                      const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2, const __grid_constant__ BackArgs p) {
   pdl_launch_dependents();
-  using F = Back<PD>;
-  constexpr int COLS = F::COLS, HALF = COLS / 2;
+  using F = Back<PD, KEYS>;
+  constexpr int COLS = F::COLS, STREAMS = F::STREAMS, MINE = F::MINE;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_u32(base);
@@ -108,13 +116,15 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     if (lane < F::STAGES) {
       mbar_init(smem_u32(&c->yfull[lane]), 1);
       mbar_init(smem_u32(&c->yempty[lane]), KEYS ? 2 : 1);
-    } else if (lane == 8) {
+    } else if (lane >= 16 && lane < 18) {
+      const int w = lane - 16;
+      mbar_init(smem_u32(&c->sfull[w]), 1);
+      mbar_init(smem_u32(&c->sfree[w]), F::ROW_WARPS);
+      mbar_init(smem_u32(&c->pready[w]), F::ROW_WARPS);
+      mbar_init(smem_u32(&c->pdone[w]), KEYS ? 2 : 1);
+    } else if (lane == 18) {
       mbar_init(smem_u32(&c->xfull), 1);
-      mbar_init(smem_u32(&c->done), 3);
-      mbar_init(smem_u32(&c->sfull), 1);
-      mbar_init(smem_u32(&c->sfree), 8);
-      mbar_init(smem_u32(&c->pready), 8);
-      mbar_init(smem_u32(&c->pdone), KEYS ? 2 : 1);
+      mbar_init(smem_u32(&c->done), F::MMA_WARPS);
       c->abort = 0;
     }
     fence_barrier_init();
@@ -137,6 +147,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
 
+  const int w_begin = w.item.begin;
   if (warp < Regs::FIRST_ROWS) Regs::give();
   const uint32_t ring = smem + 2 * F::X_BYTES;
   if (warp == 0) {
@@ -181,35 +192,39 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i) mbar_wait(smem_u32(&c->yfull[i % F::STAGES]), (i / F::STAGES) & 1, p.ws, &never);
       }
     }
-  } else if (warp == 1) {
-    if (n > 0) {  // S and T of each tile, once the rows' warps have the tile before in registers
+  } else if (warp == 1 || (warp == 6 && STREAMS == 2)) {
+    if (n > 0) {  // S and T of every tile of a stream, once the rows' warps have the tile before in registers
       constexpr uint32_t id = idesc(128, COLS, false, false);
+      const int w = warp == 6;
+      const uint32_t sfull = smem_u32(&c->sfull[w]), sfree = smem_u32(&c->sfree[w]), to = tmem + F::S + w * F::S_STEP;
       bool ok = warp_wait(smem_u32(&c->xfull), 0, p.ws, abort);
-      int s = 0, parity = 0, tile = 0;
-      for (int j = 0; j < n && ok; ++j) {
+      int s = w, parity = 0, tile = tiles > 1 ? w : 0;
+      for (int j = w, i = 0; j < n && ok; j += STREAMS, ++i) {
         const uint32_t y = ring + s * F::Y_BYTES;
         ok = warp_wait(smem_u32(&c->yfull[s]), parity, p.ws, abort);
-        const int left = y_rows - (w.item.begin + tile) * COLS;
+        const int left = y_rows - (w_begin + tile) * COLS;
         if (ok && left < COLS) {
           zero_rows(y, F::Y_CHUNK, F::CHUNKS, left, COLS);
           zero_rows(y + F::STAGES * F::Y_BYTES, F::Y_CHUNK, F::CHUNKS, left, COLS);
         }
-        if (j > 0) ok = ok && warp_wait(smem_u32(&c->sfree), (j - 1) & 1, p.ws, abort);
+        if (i > 0) ok = ok && warp_wait(sfree, (i - 1) & 1, p.ws, abort);
         if (!ok) break;
         fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a = desc_k(smem + i * F::X_BYTES), b = desc_k(y + i * F::STAGES * F::Y_BYTES);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = desc_k(smem + h * F::X_BYTES), b = desc_k(y + h * F::STAGES * F::Y_BYTES);
 #pragma unroll
             for (int k = 0; k < PD / 16; ++k)
-              mma(tmem + (i ? F::T : F::S), a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id, k > 0);
+              mma(to + h * COLS, a + (k / 4) * (F::X_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::Y_CHUNK >> 4) + (k % 4) * 2, id, k > 0);
           }
-          mma_commit(smem_u32(&c->sfull));
+          mma_commit(sfull);
         }
         __syncwarp();
-        if (++s == F::STAGES) s = 0, parity ^= 1;
-        if (++tile == tiles) tile = 0;
+        s += STREAMS;
+        if (s >= F::STAGES) s -= F::STAGES, parity ^= 1;
+        tile += STREAMS;
+        while (tile >= tiles) tile -= tiles;
       }
       if (elect_one()) mma_commit(smem_u32(&c->done));
       __syncwarp();
@@ -218,37 +233,55 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     const bool second = warp == 3;  // B += P Y2, else A += dS Y1
     if (n > 0 && (KEYS || !second)) {
       const uint32_t id = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
-      const uint32_t a = tmem + (second ? F::P : F::DS), to = tmem + (second ? F::B : F::A), y = ring + (second ? F::STAGES * F::Y_BYTES : 0);
+      const uint32_t a0 = tmem + (second ? F::P : F::DS), to = tmem + (second ? F::B : F::A), y = ring + (second ? F::STAGES * F::Y_BYTES : 0);
       bool ok = true;
-      int s = 0;
+      int s = 0, w = 0, parity = 0;
       for (int j = 0; j < n; ++j) {
-        ok = warp_wait(smem_u32(&c->pready), j & 1, p.ws, abort);  // the tile has long been there: S and T were made of it
+        ok = warp_wait(smem_u32(&c->pready[w]), parity, p.ws, abort);  // the tile has long been there: S and T were made of it
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          const uint32_t b = desc_mn(y + s * F::Y_BYTES, F::Y_CHUNK);
+          const uint32_t a = a0 + w * F::P_STEP, b = desc_mn(y + s * F::Y_BYTES, F::Y_CHUNK);
 #pragma unroll
           for (int k = 0; k < COLS / 16; ++k) mma_ta(to, a + k * 8, b + k * (2048 >> 4), id, j > 0 || k > 0);
-          mma_commit(smem_u32(&c->pdone));
+          mma_commit(smem_u32(&c->pdone[w]));
           mma_commit(smem_u32(&c->yempty[s]));
         }
         __syncwarp();
         if (++s == F::STAGES) s = 0;
+        if (++w == STREAMS) w = 0, parity ^= 1;
       }
-    }
-    if (n > 0) {
       if (elect_one()) mma_commit(smem_u32(&c->done));
       __syncwarp();
-      if (!second) {  // every MMA has completed before the CTA ends
-        volatile int never = 0;
-        warp_wait(smem_u32(&c->done), 0, p.ws, &never);
-      }
     }
   } else if (warp < Regs::FIRST_ROWS) {
-    if (warp < 6 && n > 0) relay<288>(smem_u32(warp == 4 ? &c->sfull : &c->pdone), warp - 3, n, p.ws, abort);
+    if (n > 0) {
+      if (warp == 4 || (warp == 5 && STREAMS == 2)) {
+        const int w = warp - 4;
+        relay<F::MEET>(smem_u32(&c->sfull[w]), 1 + w, (n - w + STREAMS - 1) / STREAMS, p.ws, abort);
+        if (w == 0) {  // every MMA has completed before the rows' warps read the results, and before the CTA ends
+          volatile int never = 0;
+          warp_wait(smem_u32(&c->done), 0, p.ws, &never);
+          fence_after();
+          fence_before();
+          __syncwarp();
+          meet<288>(5);
+        }
+      } else if (warp == 7) {  // of each stream's tiles but its last
+        for (int j = 0; j < n - STREAMS; ++j) {
+          const int w = j % STREAMS;
+          if (!__any_sync(0xffffffffu, *abort)) warp_wait(smem_u32(&c->pdone[w]), (j / STREAMS) & 1, p.ws, abort);
+          fence_after();
+          fence_before();
+          __syncwarp();
+          meet<F::MEET>(3 + w);
+        }
+      }
+    }
   } else {
     Regs::take();
-    const int half = (warp - Regs::FIRST_ROWS) / 4;
+    const int half = (warp - Regs::FIRST_ROWS) / 4;  // of the columns; STREAMS 2: the stream
+    const int stream = STREAMS == 2 ? half : 0, col = STREAMS == 2 ? 0 : half * MINE;
     const int r = (warp % 4) * 32 + lane;
     const int row = row0 + r;
     const bool live = w.ok && row < x_rows;
@@ -270,17 +303,18 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       lse = -p.lse[i];
       delta = -p.delta[i];
     }
-    const uint32_t s_at = at + F::S + half * HALF, t_at = at + F::T + half * HALF, p_at = at + F::P + half * (HALF / 2), ds_at = at + F::DS + half * (HALF / 2);
-    const uint32_t sfree = smem_u32(&c->sfree), pready = smem_u32(&c->pready);
+    const uint32_t s_at = at + F::S + stream * F::S_STEP + col, t_at = s_at + COLS;
+    const uint32_t p_at = at + F::P + stream * F::P_STEP + col / 2, ds_at = p_at + COLS / 2;
+    const uint32_t sfree = smem_u32(&c->sfree[stream]), pready = smem_u32(&c->pready[stream]);
     const float2 c2 = make_float2(p.c, p.c);
-    int stage = 0, tile = w.item.begin;
-    for (int j = 0; j < n; ++j) {
+    int stage = stream, tile = tiles > 1 ? stream : 0;
+    for (int j = stream; j < n; j += STREAMS) {
       __syncwarp();
-      meet<288>(1);
+      meet<F::MEET>(1 + stream);
       fence_after();
-      uint32_t s[HALF], g[HALF];
+      uint32_t s[MINE], g[MINE];
 #pragma unroll
-      for (int k = 0; k < HALF; k += 32) {
+      for (int k = 0; k < MINE; k += 32) {
         tmem_ld32(s_at + k, s + k);
         tmem_ld32(t_at + k, g + k);
       }
@@ -290,10 +324,10 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sfree);
-      const uint32_t stats = smem + F::STATS + stage * F::STAT_BYTES + half * HALF * 4;
+      const uint32_t stats = smem + F::STATS + stage * F::STAT_BYTES + col * 4;
       float l4[4] = {lse, lse, lse, lse}, d4[4] = {delta, delta, delta, delta};
 #pragma unroll
-      for (int i = 0; i < HALF; i += 4) {
+      for (int i = 0; i < MINE; i += 4) {
         if (KEYS) {  // the columns' own
           const uint4 l = lds128(stats + i * 4), d = lds128(stats + COLS * 4 + i * 4);
           l4[0] = -__uint_as_float(l.x), l4[1] = -__uint_as_float(l.y), l4[2] = -__uint_as_float(l.z), l4[3] = -__uint_as_float(l.w);
@@ -309,20 +343,21 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
           g[i + h + 1] = __float_as_uint(t.y);
         }
       }
-      if (tile < whole_from || tile >= whole_to) {  // masked pairs: p and ds are zero, whatever was there
-        const int64_t col0 = (int64_t)tile * COLS + half * HALF;
-        const int from = cols_before<HALF>(lo, col0), to = cols_before<HALF>(hi, col0);
+      const int at_tile = w.item.begin + tile;
+      if (at_tile < whole_from || at_tile >= whole_to) {  // masked pairs: p and ds are zero, whatever was there
+        const int64_t col0 = (int64_t)at_tile * COLS + col;
+        const int from = cols_before<MINE>(lo, col0), to = cols_before<MINE>(hi, col0);
 #pragma unroll
-        for (int i = 0; i < HALF; ++i)
+        for (int i = 0; i < MINE; ++i)
           if (i < from || i >= to) s[i] = g[i] = 0u;
       }
       __syncwarp();
-      if (j > 0) {  // the products that read P and dS are done
-        meet<288>(2);
+      if (j >= STREAMS) {  // the products that read p and dS are done
+        meet<F::MEET>(3 + stream);
         fence_after();
       }
 #pragma unroll
-      for (int k = 0; k < HALF / 2; k += 16) {
+      for (int k = 0; k < MINE / 2; k += 16) {
         uint32_t pk[16], dk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -338,12 +373,14 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pready);
-      if (++stage == F::STAGES) stage = 0;
-      if (++tile == w.item.end) tile = w.item.begin;
+      stage += STREAMS;
+      if (stage >= F::STAGES) stage -= F::STAGES;
+      tile += STREAMS;
+      while (tile >= tiles) tile -= tiles;
     }
     if (n > 0) {
       __syncwarp();
-      meet<288>(2);
+      meet<288>(5);
       fence_after();
     }
     const bool ok = !__any_sync(0xffffffffu, *abort);
@@ -386,7 +423,7 @@ struct Inputs {
 
 template <int PD, bool KEYS>
 static dit_status launch(BackArgs a, const Inputs& in, cudaStream_t st) {
-  using F = Back<PD>;
+  using F = Back<PD, KEYS>;
   static OncePerDevice checked, once;
   const dit_attention_plan_t& p = a.plan;
   const int items = p.items[KEYS ? GRAD_KV : GRAD_Q], heads = KEYS ? p.kv_heads : p.heads;

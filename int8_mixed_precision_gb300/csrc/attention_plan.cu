@@ -82,7 +82,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       if (spans[i].first < spans[i - 1].second) return DIT_ERR_INVALID_ARG;
   }
 
-  const int cols = tile_cols(dim), rt = rows_per_tile(group), pd = padded_dim(dim);
+  const int cols = BACK_COLS, rt = rows_per_tile(group), pd = padded_dim(dim);
   std::vector<Costed> lists[DIT_ATTENTION_LISTS];
   // forward: two row blocks to an item.  The second one costs about as much again less what its MMAs hide.
   std::vector<double> costs;

@@ -82,7 +82,7 @@ def lists(plan):
 def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     plan = dit.AttentionPlan(queries, heads, dim, kv_heads=kv_heads, kv_lengths=keys, frame=frame, prefix=prefix, training=True, device="cpu")
     docs, (fwd, joins, gq, gk), buckets = lists(plan)
-    cols, rt, back = 128, 128 // (heads // kv_heads), (128 if dim <= 64 else 64)
+    cols, rt, back = 128, 128 // (heads // kv_heads), 64
     assert plan.q_rows == sum(queries)
     for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
         at = 0
