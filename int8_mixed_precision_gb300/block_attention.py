@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
+import threading
 
 import torch
 
@@ -19,11 +21,6 @@ from .adapters import raw_stream
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 NORMS = {None: 0, "rms": 1, "layer": 2}
 MAX_AXES = 4
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class _Rotary(ctypes.Structure):
@@ -38,26 +35,60 @@ class _Plan(ctypes.Structure):
 
 
 # ----------------------------------------------------------------------------------------
-# checks of a call, one pass over each tensor's properties
+# checks of a call, one pass over each tensor's properties: a short call's kernel takes a few microseconds
 # ----------------------------------------------------------------------------------------
 
+class _Views(threading.local):
+    """Where a thread's call lays out its dit_heads_t structures: (pointer, token stride, head stride, heads, 0) each."""
+    MOST = 8
+
+    def __init__(self):
+        self.room = ctypes.create_string_buffer(32 * self.MOST)
+        base = ctypes.addressof(self.room)
+        self.at = tuple(base + 32 * i for i in range(self.MOST))
+
+
+_views = _Views()
+_pack = tuple(struct.Struct("=" + "Qqqii" * n).pack_into for n in range(_Views.MOST + 1))
+
+
+def _lay(*views):
+    """The addresses of the views' structures, valid until the thread's next call; None stays None."""
+    there = [v for v in views if v is not None]
+    flat = []
+    for v in there:
+        flat += v[:4]
+        flat.append(0)
+    _pack[len(there)](_views.room, 0, *flat)
+    if len(there) == len(views):
+        return _views.at[:len(views)]
+    at = iter(_views.at)
+    return tuple(None if v is None else next(at) for v in views)
+
+
 def _view(t, rows, heads, dim, what, index, exact=False):
-    """`t` as [tokens, heads, dim] with at least `rows` tokens (exactly, if `exact`)."""
-    shape, stride = t.shape, t.stride()
+    """`t` as [tokens, heads, dim] with at least `rows` tokens (exactly, if `exact`): pointer, strides, heads, and the end of
+    the memory that `rows` tokens span."""
+    shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim or shape[0] < rows or (exact and shape[0] != rows):
         raise DitError(f"{what}: {tuple(shape)}, the call needs [{rows}, {heads}, {dim}]")
     if t.dtype is not _BF16:
         raise DitError(f"{what}: unsupported dtype {t.dtype}")
     if t.get_device() != index or index < 0:
         raise DitError(f"buffers must be CUDA tensors on one device ({what} is on {t.device})")
-    if stride[2] != 1:
+    row, head, one = t.stride()
+    if one != 1:
         raise DitError(f"{what}: a head's dimensions must be contiguous")
     at = t.data_ptr()
-    if at % 16 or (rows > 1 and stride[0] % 8) or (heads > 1 and stride[1] % 8):
+    if rows <= 1:
+        row = heads * dim
+    if heads <= 1:
+        head = dim
+    if at & 15 or row & 7 or head & 7:
         raise DitError(f"{what}: 16-byte aligned heads are needed ({lib().dit_status_str(2).decode()})")
-    if rows and ((rows > 1 and stride[0] <= 0) or (heads > 1 and stride[1] <= 0)):
+    if row <= 0 or head <= 0:
         raise DitError(f"{what}: an expanded tensor")
-    return _Heads(at, stride[0], stride[1], heads, 0)
+    return at, row, head, heads, at + 2 * ((rows - 1) * row + (heads - 1) * head + dim) if rows else at
 
 
 def _flat(t, nbytes, what, index, dtype=None, align=4):
@@ -75,43 +106,32 @@ def _flat(t, nbytes, what, index, dtype=None, align=4):
     return at
 
 
-def _extent(h: _Heads, rows: int, dim: int):
-    return h.ptr, h.ptr + 2 * ((rows - 1) * h.token_stride + (h.heads - 1) * h.head_stride + dim)
-
-
-def _meet(a: _Heads, a_rows: int, b: _Heads, b_rows: int, dim: int) -> bool:
+def _meet(a, b, dim: int) -> bool:
     """Whether two views share memory (columns of one buffer side by side do not; other interleavings count as shared)."""
-    if not a_rows or not b_rows:
+    if a[4] <= b[0] or b[4] <= a[0] or a[4] == a[0] or b[4] == b[0]:
         return False
-    a0, a1 = _extent(a, a_rows, dim)
-    b0, b1 = _extent(b, b_rows, dim)
-    if a1 <= b0 or b1 <= a0:
-        return False
-    pitch = a.token_stride
-    if pitch != b.token_stride or pitch <= 0:
+    pitch = a[1]
+    if pitch != b[1]:
         return True
-    apart = (b0 - a0) // 2
-    wide_a, wide_b = (a.heads - 1) * a.head_stride + dim, (b.heads - 1) * b.head_stride + dim
+    apart = (b[0] - a[0]) // 2
+    wide_a, wide_b = (a[3] - 1) * a[2] + dim, (b[3] - 1) * b[2] + dim
     d = apart % pitch
     if d >= wide_a and d + wide_b <= pitch:
         return False
-    step = a.head_stride if a.heads > 1 else b.head_stride
-    if (a.heads == 1 or b.heads == 1 or a.head_stride == b.head_stride) and step > 0 and pitch % step == 0:
+    step = a[2] if a[3] > 1 else b[2]
+    if (a[3] == 1 or b[3] == 1 or a[2] == b[2]) and pitch % step == 0:
         d = apart % step
         if d >= dim and d + dim <= step:
             return False
     return True
 
 
-def _same(a: _Heads, b: _Heads) -> bool:
-    return a.ptr == b.ptr and a.token_stride == b.token_stride and a.head_stride == b.head_stride and a.heads == b.heads
-
-
 def _apart(outputs, inputs, dim, own=()):
     """Refuses outputs that share memory with one another or with an input, but for the pairs `own` that may be one view."""
-    for i, (name, out, rows) in enumerate(outputs):
-        for other, t, t_rows in (*inputs, *outputs[:i]):
-            if _meet(out, rows, t, t_rows, dim) and not ((name, other) in own and _same(out, t)):
+    for i, (name, out) in enumerate(outputs):
+        begin, end = out[0], out[4]
+        for other, t in (*inputs, *outputs[:i]):
+            if begin < t[4] and t[0] < end and _meet(out, t, dim) and not ((name, other) in own and out == t):
                 raise DitError(f"{name} overlaps {other}")
 
 
@@ -166,6 +186,7 @@ class QKNorm:
         if not (math.isfinite(eps) and eps >= 0):
             raise DitError("QKNorm: eps is finite and not negative")
         self.params, self.kind, self.eps, self.dim = params, kind, float(eps), params.shape[1]
+        self._code = NORMS[kind]
 
 
 def qk_norm_scratch(dim: int, device="cuda"):
@@ -173,27 +194,20 @@ def qk_norm_scratch(dim: int, device="cuda"):
     return torch.empty(int(lib().dit_qk_norm_scratch_bytes(dim)), dtype=torch.uint8, device=device)
 
 
-def _norm_args(q, k, norm, rotary, positions, others):
-    """The views of q, k and `others` ((name, of q or k, tensor)), and the call's other arguments."""
+def _norm_args(q, k, norm, rotary, positions):
+    """The views of q and k, and the call's other arguments."""
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise DitError("q and k: [tokens, heads, dim]")
-    rows, _, dim = q.shape
+    rows, heads, dim = q.shape
     index = q.get_device()
-    heads = (q.shape[1], 0 if k is None else k.shape[1])
-    if dim < 8 or dim % 8 or dim > 256 or heads[0] < 1 or (k is not None and heads[1] < 1):
+    if dim < 8 or dim % 8 or dim > 256 or heads < 1 or (k is not None and k.shape[1] < 1):
         raise DitError(f"a head of {dim} dimensions: multiples of 8 up to 256 are supported")
-    views = {"q": _view(q, rows, heads[0], dim, "q", index, True)}
-    if k is not None:
-        views["k"] = _view(k, rows, heads[1], dim, "k", index, True)
-    for name, of, t in others:
-        if (t is None) != (of == 1 and k is None):
-            raise DitError(f"{name}: goes with {'k' if of else 'q'}")
-        if t is not None:
-            views[name] = _view(t, rows, heads[of], dim, name, index, True)
+    qv = _view(q, rows, heads, dim, "q", index)
+    kv = None if k is None else _view(k, rows, k.shape[1], dim, "k", index, True)
     if norm is None:
         kind, params, eps = 0, None, 0.0
     else:
-        kind, eps = NORMS[norm.kind], norm.eps
+        kind, eps = norm._code, norm.eps
         if norm.dim != dim:
             raise DitError(f"a norm of {norm.dim} dimensions, heads of {dim}")
         params = _flat(norm.params, 8 * dim * kind, "params", index, _F32)
@@ -203,26 +217,33 @@ def _norm_args(q, k, norm, rotary, positions, others):
             raise DitError(f"a rotation of heads of {rotary.head_dim} dimensions, heads of {dim}")
         if rotary._index != index:
             raise DitError(f"the rotation is on {rotary.table.device}, q on {q.device}")
-        if positions is None or tuple(positions.shape) != (rows, rotary.axes):
+        if positions is None or positions.shape != (rows, rotary.axes):
             raise DitError(f"positions: int32 [{rows}, {rotary.axes}] is needed")
         at, rot = _flat(positions, 4 * rows * rotary.axes, "positions", index, _I32), rotary._p
     elif positions is not None:
         raise DitError("positions without a rotation")
-    return views, rows, dim, index, (ctypes.c_int64(rows), dim, kind, params, eps, rot, at)
+    return qv, kv, index, (rows, dim, kind, params, eps, rot, at)
 
 
-def _ref(views, name):
-    return ctypes.byref(views[name]) if name in views else None
+def _beside(t, of, name, dim, rows, index):
+    """The view of a tensor that goes with q or k."""
+    if (t is None) != (of is None):
+        raise DitError(f"{name}: goes with k")
+    return None if t is None else _view(t, rows, of[3], dim, name, index, True)
 
 
 def _norm_rope_call(q, k, q_out, k_out, norm, rotary, positions, stream):
-    views, rows, dim, index, rest = _norm_args(q, k, norm, rotary, positions, (("q_out", 0, q_out), ("k_out", 1, k_out)))
-    _apart([(n, views[n], rows) for n in ("q_out", "k_out") if n in views], [(n, views[n], rows) for n in ("q", "k") if n in views], dim,
-           (("q_out", "q"), ("k_out", "k")))
+    qv, kv, index, rest = _norm_args(q, k, norm, rotary, positions)
+    rows, dim = rest[0], rest[1]
+    qo, ko = _beside(q_out, qv, "q_out", dim, rows, index), _beside(k_out, kv, "k_out", dim, rows, index)
+    if kv is None:
+        _apart((("q_out", qo),), (("q", qv),), dim, (("q_out", "q"),))
+    else:
+        _apart((("q_out", qo), ("k_out", ko)), (("q", qv), ("k", kv)), dim, (("q_out", "q"), ("k_out", "k")))
     raw = raw_stream(stream, index)
 
     def call():
-        st = lib().dit_qk_norm_rope(_ref(views, "q"), _ref(views, "k"), _ref(views, "q_out"), _ref(views, "k_out"), *rest, raw)
+        st = lib().dit_qk_norm_rope(*_lay(qv, kv, qo, ko), *rest, raw)
         if st:
             _check(st, "dit_qk_norm_rope")
     return call
@@ -239,10 +260,11 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, norm, rotary, positions,
     """dq, dk (bf16; may be dq_out and dk_out themselves) from the outputs' gradients dq_out, dk_out and the forward pass'
     inputs q, k; dparams (fp32, the shape of norm.params, overwritten; None: not wanted, and scratch may be
     None) over all tokens and heads."""
-    views, rows, dim, index, rest = _norm_args(q, k, norm, rotary, positions,
-                                               (("dq_out", 0, dq_out), ("dk_out", 1, dk_out), ("dq", 0, dq), ("dk", 1, dk)))
-    _apart([(n, views[n], rows) for n in ("dq", "dk") if n in views],
-           [(n, views[n], rows) for n in ("q", "k", "dq_out", "dk_out") if n in views], dim, (("dq", "dq_out"), ("dk", "dk_out")))
+    qv, kv, index, rest = _norm_args(q, k, norm, rotary, positions)
+    rows, dim = rest[0], rest[1]
+    views = [_beside(t, of, name, dim, rows, index) for t, of, name in ((dq_out, qv, "dq_out"), (dk_out, kv, "dk_out"), (dq, qv, "dq"), (dk, kv, "dk"))]
+    names = [n for n in (("q", qv), ("k", kv), ("dq_out", views[0]), ("dk_out", views[1])) if n[1] is not None]
+    _apart([n for n in (("dq", views[2]), ("dk", views[3])) if n[1] is not None], names, dim, (("dq", "dq_out"), ("dk", "dk_out")))
     dp, sp, sn = None, None, 0
     if dparams is not None:
         if norm is None:
@@ -255,8 +277,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, norm, rotary, positions,
         sn = scratch.nbytes if scratch is not None else 0
         sp = _flat(scratch, int(lib().dit_qk_norm_scratch_bytes(dim)), "scratch", index, align=16) if scratch is not None else None
     wp = _flat(ws, 0, "ws", index)
-    st = lib().dit_qk_norm_rope_backward(_ref(views, "q"), _ref(views, "k"), _ref(views, "dq_out"), _ref(views, "dk_out"), _ref(views, "dq"),
-                                         _ref(views, "dk"), *rest, dp, sp, sn, wp, ws.nbytes, raw_stream(stream, index))
+    raw = raw_stream(stream, index)
+    st = lib().dit_qk_norm_rope_backward(*_lay(qv, kv, *views), *rest, dp, sp, sn, wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_qk_norm_rope_backward")
 
@@ -306,6 +328,8 @@ class AttentionPlan:
         self._info_p, self._table_p = ctypes.c_void_p(ctypes.addressof(self.info)), ctypes.c_void_p(self._table.data_ptr())
         self._index = self._table.get_device()
         self._scratch_bytes, self._saved_bytes = self.info.scratch_bytes, self.info.saved_bytes
+        self._shape = (self._index, self.dim, self.q_rows, self.k_rows, self.heads, kv_heads)
+        self._default_scale = self.dim ** -0.5
 
     table = property(lambda self: self._table)
 
@@ -324,18 +348,19 @@ def attention_saved(plan: AttentionPlan):
 
 
 def _scale_of(plan, scale):
-    scale = plan.dim ** -0.5 if scale is None else float(scale)
+    if scale is None:
+        return plan._default_scale
+    scale = float(scale)
     if not (scale > 0 and math.isfinite(scale)):
         raise DitError("attention: scale is finite and positive")
     return scale
 
 
 def _attention_call(plan, q, k, v, out, scratch, ws, scale, saved, stream):
-    i, dim = plan._index, plan.dim
-    hq = _view(q, plan.q_rows, plan.heads, dim, "q", i)
-    hk, hv = _view(k, plan.k_rows, plan.kv_heads, dim, "k", i), _view(v, plan.k_rows, plan.kv_heads, dim, "v", i)
-    ho = _view(out, plan.q_rows, plan.heads, dim, "out", i)
-    _apart([("out", ho, plan.q_rows)], [("q", hq, plan.q_rows), ("k", hk, plan.k_rows), ("v", hv, plan.k_rows)], dim)
+    i, dim, rows, keys, heads, kv_heads = plan._shape
+    hq, hk, hv = _view(q, rows, heads, dim, "q", i), _view(k, keys, kv_heads, dim, "k", i), _view(v, keys, kv_heads, dim, "v", i)
+    ho = _view(out, rows, heads, dim, "out", i)
+    _apart((("out", ho),), (("q", hq), ("k", hk), ("v", hv)), dim)
     scale = _scale_of(plan, scale)
     if saved is None:
         vp, vn = None, 0
@@ -343,12 +368,11 @@ def _attention_call(plan, q, k, v, out, scratch, ws, scale, saved, stream):
         vp, vn = _flat(saved, plan._saved_bytes, "saved", i, align=16), saved.nbytes
     else:
         raise DitError("saved needs AttentionPlan(..., training=True)")
-    sp, wp = _flat(scratch, plan._scratch_bytes, "scratch", i, align=16), _flat(ws, 0, "ws", i, align=32)
+    sp, wp = _flat(scratch, plan._scratch_bytes, "scratch", i, align=16), _flat(ws, 65536, "ws", i, align=32)
     raw = raw_stream(stream, i)
 
     def call():
-        st = lib().dit_attention(plan._info_p, plan._table_p, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), ctypes.byref(ho), scale, vp, vn,
-                                 sp, scratch.nbytes, wp, ws.nbytes, raw)
+        st = lib().dit_attention(plan._info_p, plan._table_p, *_lay(hq, hk, hv, ho), scale, vp, vn, sp, scratch.nbytes, wp, ws.nbytes, raw)
         if st:
             _check(st, "dit_attention")
     return call
@@ -366,17 +390,17 @@ def attention_backward(plan: AttentionPlan, q, k, v, out, dout, saved, dq, dk, d
     same plan, q, k, v and scale."""
     if not plan.training:
         raise DitError("attention_backward needs AttentionPlan(..., training=True)")
-    i, dim, qn, kn = plan._index, plan.dim, plan.q_rows, plan.k_rows
-    h, hk = plan.heads, plan.kv_heads
-    ins = [("q", _view(q, qn, h, dim, "q", i), qn), ("k", _view(k, kn, hk, dim, "k", i), kn), ("v", _view(v, kn, hk, dim, "v", i), kn),
-           ("out", _view(out, qn, h, dim, "out", i), qn), ("dout", _view(dout, qn, h, dim, "dout", i), qn)]
-    outs = [("dq", _view(dq, qn, h, dim, "dq", i), qn), ("dk", _view(dk, kn, hk, dim, "dk", i), kn), ("dv", _view(dv, kn, hk, dim, "dv", i), kn)]
+    i, dim, qn, kn, h, hk = plan._shape
+    ins = (("q", _view(q, qn, h, dim, "q", i)), ("k", _view(k, kn, hk, dim, "k", i)), ("v", _view(v, kn, hk, dim, "v", i)),
+           ("out", _view(out, qn, h, dim, "out", i)), ("dout", _view(dout, qn, h, dim, "dout", i)))
+    outs = (("dq", _view(dq, qn, h, dim, "dq", i)), ("dk", _view(dk, kn, hk, dim, "dk", i)), ("dv", _view(dv, kn, hk, dim, "dv", i)))
     _apart(outs, ins, dim)
     scale = _scale_of(plan, scale)
     vp = _flat(saved, plan._saved_bytes, "saved", i, align=16)
-    sp, wp = _flat(scratch, plan._scratch_bytes, "scratch", i, align=16), _flat(ws, 0, "ws", i, align=32)
-    st = lib().dit_attention_backward(plan._info_p, plan._table_p, *(ctypes.byref(t[1]) for t in (*ins, *outs)), scale, vp, saved.nbytes, sp,
-                                      scratch.nbytes, wp, ws.nbytes, raw_stream(stream, i))
+    sp, wp = _flat(scratch, plan._scratch_bytes, "scratch", i, align=16), _flat(ws, 65536, "ws", i, align=32)
+    raw = raw_stream(stream, i)
+    st = lib().dit_attention_backward(plan._info_p, plan._table_p, *_lay(*(t[1] for t in (*ins, *outs))), scale, vp, saved.nbytes, sp,
+                                      scratch.nbytes, wp, ws.nbytes, raw)
     if st:
         _check(st, "dit_attention_backward")
 
