@@ -19,6 +19,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "attention.cuh"
 
 namespace dit6 {
@@ -54,12 +56,15 @@ struct FwdControl {
 };
 static_assert(sizeof(FwdControl) <= 1024, "");
 
+template <int PD>
+constexpr int PARTIAL = partial_floats(PD);
+
 struct FwdArgs {
   dit_attention_plan_t plan;
   const int32_t* table;
   Heads out;
   float* lse;       // [heads][padded rows], in base 2, or nullptr
-  float* partial;   // [heads][slots][PD + 2]
+  float* partial;   // [heads][slots][PARTIAL]: o unnormalised, the maximum (in base 2) and the sum
   void* ws;
   float c;          // scale log2(e)
   int group, rows;  // heads of a group, queries of a block
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       __nv_bfloat16* out = p.out.ptr + at_row * p.out.row + head * p.out.head;
       const bool part = w.item.slot >= 0;
       const bool room = !part || (int64_t)w.item.slot + row - row0 < p.plan.slots;
-      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.item.slot + row - row0) * (PD + 2) : nullptr;
+      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.item.slot + row - row0) * PARTIAL<PD> : nullptr;
 #pragma unroll
       for (int k = 0; k < PD; k += 32) {
         uint32_t o[32];
@@ -377,9 +382,10 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
 }
 
 // The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order, a warp to each row
-// and head.
+// and head.  A lane looks at the maxima and sums of every 32nd piece; the weights then pass from lane to lane.
+constexpr int JOIN_ROWS = 8;  // rows of a CTA
 template <int PD>
-__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ FwdArgs p) {
+__global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_constant__ FwdArgs p) {
   pdl_launch_dependents();
   pdl_wait();
   const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
@@ -390,33 +396,51 @@ __global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ 
     return;
   }
   constexpr int EACH = PD / 32;
-  for (int r = threadIdx.x / 32; r < rows; r += 8) {
-    const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.item.begin + r) * (PD + 2);
-    const int64_t step = (int64_t)rows * (PD + 2);
-    float m = -INFINITY;
-    for (int i = 0; i < pieces; ++i) m = fmaxf(m, __ldcg(from + i * step + PD));
-    float sum = 0.f, o[EACH] = {};
-    const bool empty = m == -INFINITY;
-    for (int i = 0; i < pieces && !empty; ++i) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + i * step + PD));
-      const float f = exp2_approx(ml.x - m);
-      sum += f * ml.y;
-      if (ml.x == -INFINITY) continue;
+  using Vec = typename std::conditional<EACH == 2, float2, float4>::type;
+  const int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32;
+  if (r >= rows) return;
+  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.item.begin + r) * PARTIAL<PD>;
+  const int64_t step = (int64_t)rows * PARTIAL<PD>;
+  float m = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(from + i * step + PD));
+  m = warp_max_f(m);
+  const bool empty = m == -INFINITY;  // a query that sees no key (or whose scores are all -infinity: no weight anywhere)
+  float sum = 0.f;
+  Vec o = {};
+  for (int first = 0; first < pieces; first += 32) {
+    const int many = min(32, pieces - first);
+    float f = 0.f, l = 0.f;
+    if (lane < many) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (first + lane) * step + PD));
+      f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
+      l = f == 0.f ? 0.f : f * ml.y;
+    }
+    for (int i = 0; i < many; i += 4) {
+      Vec v[4];
 #pragma unroll
-      for (int k = 0; k < EACH; k += 2) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(from + i * step + lane * EACH + k));
-        o[k] += f * v.x;
-        o[k + 1] += f * v.y;
+      for (int k = 0; k < 4; ++k)
+        if (i + k < many) v[k] = __ldcg(reinterpret_cast<const Vec*>(from + (first + i + k) * step) + lane);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, (i + k) & 31);
+        sum += __shfl_sync(0xffffffffu, l, (i + k) & 31) * (i + k < many ? 1.f : 0.f);
+        if (i + k < many && g != 0.f) {  // a piece without weight has no part, whatever it holds
+          float* a = reinterpret_cast<float*>(&o);
+          const float* b = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+          for (int e = 0; e < EACH; ++e) a[e] += g * b[e];
+        }
       }
     }
-    const int64_t row = (int64_t)w.item.row0 + r;
-    __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head;
-    const float inv = empty ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int k = 0; k < EACH; k += 2)
-      if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + lane * EACH + k) = f2_to_bf16x2(o[k] * inv, o[k + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
   }
+  const int64_t row = (int64_t)w.item.row0 + r;
+  __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
+  const float inv = empty ? 0.f : 1.f / sum;
+  const float* v = reinterpret_cast<const float*>(&o);
+#pragma unroll
+  for (int k = 0; k < EACH; k += 2)
+    if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(v[k] * inv, v[k + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
 }
 
 template <int PD>
@@ -434,7 +458,7 @@ static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads
   if (prepare_kernel<Regs>(checked, once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
   if (launch_pdl(k_attention<PD>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
     return DIT_ERR_CUDA;
-  if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads)), dim3(256), 0, st, 1, a) != cudaSuccess)
+  if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads), (unsigned)(2 * a.rows + JOIN_ROWS - 1) / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, 1, a) != cudaSuccess)
     return DIT_ERR_CUDA;
   return DIT_OK;
 }

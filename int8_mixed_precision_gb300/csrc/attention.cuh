@@ -18,6 +18,8 @@ enum List { FORWARD, JOIN, GRAD_Q, GRAD_KV };
 // The head's dimensions as the tensor cores see them (columns behind dim are zeros that TMA fills in), and the
 // streamed operand's rows to a tile: as many as tensor memory holds beside the accumulators.
 __host__ __device__ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
+// Floats of a row's partial result: its dimensions, the maximum and the sum, in whole 16 bytes.
+__host__ __device__ constexpr int partial_floats(int padded) { return padded + 4; }
 constexpr int FORWARD_COLS = 128, BACK_COLS = 64;
 
 // The table, in int32: documents of DOC_INTS, items of ITEM_INTS (the four lists behind one another), and

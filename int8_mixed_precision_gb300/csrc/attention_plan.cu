@@ -179,7 +179,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   }
   plan->table_ints = first_bucket(*plan, DIT_ATTENTION_LISTS);
   plan->saved_bytes = training ? (int64_t)heads * plan->padded_rows * 4 : 0;
-  const int64_t joins = (int64_t)heads * plan->slots * (pd + 2) * 4, deltas = plan->saved_bytes;
+  const int64_t joins = (int64_t)heads * plan->slots * partial_floats(pd) * 4, deltas = plan->saved_bytes;
   plan->scratch_bytes = std::max(joins, deltas);
   if (!table) return DIT_OK;
   if (table_ints < plan->table_ints) return DIT_ERR_INVALID_ARG;
@@ -209,7 +209,7 @@ bool plan_ok(const dit_attention_plan_t* p) {
     if (p->items[l] < 0 || (int64_t)p->items[l] * p->heads > MAX_ROWS || p->buckets[l] < 0 || p->buckets[l] > DIT_ATTENTION_BUCKETS || (p->items[l] && !p->buckets[l])) return false;
   const int64_t saved = p->training ? (int64_t)p->heads * p->padded_rows * 4 : 0;
   return p->table_ints == first_bucket(*p, DIT_ATTENTION_LISTS) && p->saved_bytes == saved &&
-         p->scratch_bytes == std::max(saved, (int64_t)p->heads * p->slots * (padded_dim(p->dim) + 2) * 4);
+         p->scratch_bytes == std::max(saved, (int64_t)p->heads * p->slots * partial_floats(padded_dim(p->dim)) * 4);
 }
 
 // A view's checks; strides that no access uses are replaced by ones that a tensor map takes.

@@ -92,9 +92,9 @@ __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, const Place&
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 template <bool SPLIT>
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& at, const float (&v)[8]) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& at, const float2 (&v)[4]) {
   if (!at.active) return;
-  const uint4 o = make_uint4(f2_to_bf16x2(v[0], v[1]), f2_to_bf16x2(v[2], v[3]), f2_to_bf16x2(v[4], v[5]), f2_to_bf16x2(v[6], v[7]));
+  const uint4 o = make_uint4(f2_to_bf16x2(v[0].x, v[0].y), f2_to_bf16x2(v[1].x, v[1].y), f2_to_bf16x2(v[2].x, v[2].y), f2_to_bf16x2(v[3].x, v[3].y));
   if (!SPLIT || !at.split) {
     *reinterpret_cast<uint4*>(row + at.d0) = o;
   } else {
@@ -102,59 +102,72 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& at, c
     *reinterpret_cast<uint2*>(row + at.d1) = make_uint2(o.z, o.w);
   }
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack(const uint4& u, float2 (&v)[4]) {
+  v[0] = bf16x2_to_f2(u.x);
+  v[1] = bf16x2_to_f2(u.y);
+  v[2] = bf16x2_to_f2(u.z);
+  v[3] = bf16x2_to_f2(u.w);
+}
+__device__ __forceinline__ void load_weights(const float* w, const Place& at, float2 (&v)[4], float other) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_f2(w[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    const float* from = w + (i < 2 ? at.d0 + 2 * i : at.d1 + 2 * i - 4);
+    v[i] = at.active ? make_float2(__ldg(from), __ldg(from + 1)) : make_float2(other, other);
   }
 }
-__device__ __forceinline__ void load_weights(const float* w, const Place& at, float (&v)[8], float other) {
+// Sum over the lanes of a row; LANES 0: `lanes` of them.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+  if (LANES) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = w && at.active ? __ldg(w + (i < 4 ? at.d0 + i : at.d1 + i - 4)) : other;
-}
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
-// Sum of eight as a tree.
-__device__ __forceinline__ float sum8(const float (&v)[8]) {
-  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+__device__ __forceinline__ float sum8(const float2 (&v)[4]) {
+  const float2 s = add2(add2(v[0], v[1]), add2(v[2], v[3]));
+  return s.x + s.y;
 }
-// Turns the thread's four pairs forward (BACK: back).
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// Turns the thread's four pairs forward (BACK: back).  cs: cosines and sines of pairs 0 and 1, 2 and 3.
+struct Angles {
+  float2 c[2], s[2];
+};
 template <bool SPLIT, bool BACK>
-__device__ __forceinline__ void turn(float (&v)[8], const float2 (&cs)[4], const Place& at) {
+__device__ __forceinline__ void turn(float2 (&v)[4], const Angles& a, const Place& at) {
+  const float2 s[2] = {BACK ? make_float2(-a.s[0].x, -a.s[0].y) : a.s[0], BACK ? make_float2(-a.s[1].x, -a.s[1].y) : a.s[1]};
+  if (SPLIT && at.split) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float c = cs[i].x, s = BACK ? -cs[i].y : cs[i].y;
-    if (SPLIT && at.split) {
-      const float a = v[i], b = v[i + 4];
-      v[i] = a * c - b * s;
-      v[i + 4] = a * s + b * c;
-    } else {
-      const float a = v[2 * i], b = v[2 * i + 1];
-      v[2 * i] = a * c - b * s;
-      v[2 * i + 1] = a * s + b * c;
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = v[i], y = v[i + 2];
+      v[i] = fma2(make_float2(-y.x, -y.y), s[i], mul2(x, a.c[i]));
+      v[i + 2] = fma2(x, s[i], mul2(y, a.c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float cc = i % 2 ? a.c[i / 2].y : a.c[i / 2].x, ss = i % 2 ? s[i / 2].y : s[i / 2].x;
+      const float x = v[i].x, y = v[i].y;
+      v[i] = make_float2(x * cc - y * ss, x * ss + y * cc);
     }
   }
 }
-// xhat in v, returns r.
-template <int NORM>
-__device__ __forceinline__ float normalise(float (&v)[8], const Args& p, const Place& at, float inv) {
+// xhat in v, returns r (to 2 units of fp32).
+template <int NORM, int LANES>
+__device__ __forceinline__ float normalise(float2 (&v)[4], const Args& p, const Place& at, float inv) {
   if (NORM == DIT_NORM_NONE) return 1.f;
-  float sq[8];
   if (NORM == DIT_NORM_LAYER) {
-    const float mean = group_sum(sum8(v), p.lanes) * inv;
+    const float mean = row_sum<LANES>(sum8(v), p.lanes) * inv;
+    const float2 m = both(at.active ? -mean : 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = at.active ? v[i] - mean : 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], m);
   }
+  const float2 q = fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0]))));
+  const float r = rsqrtf(row_sum<LANES>(q.x + q.y, p.lanes) * inv + p.eps);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sq[i] = v[i] * v[i];
-  const float r = 1.f / sqrtf(group_sum(sum8(sq), p.lanes) * inv + p.eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= r;
+  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(r));
   return r;
 }
 // cos and sin of the tokens of a CTA, one thread to a pair.
@@ -172,133 +185,145 @@ __device__ __forceinline__ void fill_angles(const Args& p, float2* cs, int64_t t
     cs[i] = make_float2(c, s);
   }
 }
-__device__ __forceinline__ void load_angles(const Args& p, const float2* cs, int t, const Place& at, float2 (&o)[4]) {
+__device__ __forceinline__ Angles load_angles(const Args& p, const float2* cs, int t, const Place& at) {
+  float2 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = at.active && at.pair + i < p.pairs ? cs[t * p.pairs + at.pair + i] : make_float2(1.f, 0.f);
+  return Angles{{make_float2(o[0].x, o[1].x), make_float2(o[2].x, o[3].x)}, {make_float2(o[0].y, o[1].y), make_float2(o[2].y, o[3].y)}};
 }
 
-template <int NORM, bool SPLIT>
-__global__ void __launch_bounds__(THREADS) k_norm_rope(Args p) {
+template <int NORM, bool SPLIT, int LANES>
+__global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ Args p) {
   pdl_launch_dependents();
   __shared__ float2 cs[THREADS * 4];
   pdl_wait();
   const Side& s = p.side[blockIdx.y];
-  const int groups = THREADS / p.lanes, tokens = groups / p.per_token;
-  const int g = threadIdx.x / p.lanes, t = g / p.per_token, h0 = g - t * p.per_token;
-  const Place at = place_of(p, threadIdx.x & (p.lanes - 1));
+  const int lanes = LANES ? LANES : p.lanes;
+  const int groups = THREADS / lanes, tokens = groups / p.per_token;
+  const int g = threadIdx.x / lanes, t = g / p.per_token, h0 = g - t * p.per_token;
+  const Place at = place_of(p, threadIdx.x & (lanes - 1));
   const int64_t token0 = (int64_t)blockIdx.x * tokens, token = token0 + t;
-  const bool live = token < p.tokens;
-  const __nv_bfloat16* x = s.x.ptr + token * s.x.token;
-  __nv_bfloat16* y = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token;
+  const int mine = token < p.tokens ? s.heads : 0;  // heads that there are
+  const int64_t x_step = p.per_token * s.x.head, y_step = p.per_token * s.y.head;
+  const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
+  __nv_bfloat16* y = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token + h0 * s.y.head;
   uint4 raw[AHEAD];
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) {
-    const int h = h0 + j * p.per_token;
-    if (live && h < s.heads) raw[j] = load_row<SPLIT>(x + h * s.x.head, at);
+    if (h0 + j * p.per_token < mine) raw[j] = load_row<SPLIT>(x, at);
+    x += x_step;
   }
   fill_angles(p, cs, token0, tokens);
   __syncthreads();
-  float2 a[4];
-  load_angles(p, cs, t, at, a);
-  float w[8], b[8];
+  const Angles a = load_angles(p, cs, t, at);
+  float2 w[4], b[4];
   if (NORM != DIT_NORM_NONE) load_weights(s.w, at, w, 1.f);
   if (NORM == DIT_NORM_LAYER) load_weights(s.b, at, b, 0.f);
   const float inv = 1.f / (float)p.dim;
   // every thread makes every round: the sums' shuffles want whole warps
+  int h = h0;
   for (int base = 0; base < s.heads; base += AHEAD * p.per_token) {
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      const int h = base + h0 + j * p.per_token;
-      const bool mine = live && h < s.heads;
-      float v[8];
+      float2 v[4];
       unpack(raw[j], v);
-      if (mine && h + AHEAD * p.per_token < s.heads) raw[j] = load_row<SPLIT>(x + (h + AHEAD * p.per_token) * s.x.head, at);
-      normalise<NORM>(v, p, at, inv);
+      if (h + AHEAD * p.per_token < mine) raw[j] = load_row<SPLIT>(x, at);
+      x += x_step;
+      normalise<NORM, LANES>(v, p, at, inv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (NORM == DIT_NORM_RMS) v[i] *= w[i];
-        if (NORM == DIT_NORM_LAYER) v[i] = v[i] * w[i] + b[i];
+      for (int i = 0; i < 4; ++i) {
+        if (NORM == DIT_NORM_RMS) v[i] = mul2(v[i], w[i]);
+        if (NORM == DIT_NORM_LAYER) v[i] = fma2(v[i], w[i], b[i]);
       }
       turn<SPLIT, false>(v, a, at);
-      if (mine) store_row<SPLIT>(y + h * s.y.head, at, v);
+      if (h < mine) store_row<SPLIT>(y, at, v);
+      y += y_step;
+      h += p.per_token;
     }
   }
 }
 
 // Tokens are dealt to the CTAs in turn; each thread sums its parameters' gradients over all of its rows, the CTA adds
 // them up over its groups, and the CTA that finishes last over the CTAs, always in the same order.
-template <int NORM, bool SPLIT>
-__global__ void __launch_bounds__(THREADS) k_norm_rope_back(Args p) {
+template <int NORM, bool SPLIT, int LANES>
+__global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constant__ Args p) {
   pdl_launch_dependents();
   __shared__ float2 cs[THREADS * 4];
   __shared__ float sums[THREADS * 8];
   __shared__ bool last;
   pdl_wait();
   const Side& s = p.side[blockIdx.y];
-  const int groups = THREADS / p.lanes, tokens = groups / p.per_token;
-  const int g = threadIdx.x / p.lanes, t = g / p.per_token, h0 = g - t * p.per_token;
-  const Place at = place_of(p, threadIdx.x & (p.lanes - 1));
+  const int lanes = LANES ? LANES : p.lanes;
+  const int groups = THREADS / lanes, tokens = groups / p.per_token;
+  const int g = threadIdx.x / lanes, t = g / p.per_token, h0 = g - t * p.per_token;
+  const Place at = place_of(p, threadIdx.x & (lanes - 1));
   const float inv = 1.f / (float)p.dim;
-  float w[8], dw[8], db[8];
+  float2 w[4], dw[4], db[4];
   if (NORM != DIT_NORM_NONE) load_weights(s.w, at, w, 1.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
   const int64_t blocks = (p.tokens + tokens - 1) / tokens;
+  const int64_t x_step = p.per_token * s.x.head, d_step = p.per_token * s.dy.head, y_step = p.per_token * s.y.head;
   for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
     const int64_t token0 = blk * tokens, token = token0 + t;
-    const bool live = token < p.tokens;
-    const __nv_bfloat16* x = s.x.ptr + token * s.x.token;
-    const __nv_bfloat16* dy = s.dy.ptr + token * s.dy.token;
-    __nv_bfloat16* dx = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token;
+    const int mine = token < p.tokens ? s.heads : 0;  // heads that there are
+    const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
+    const __nv_bfloat16* dy = s.dy.ptr + token * s.dy.token + h0 * s.dy.head;
+    __nv_bfloat16* dx = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token + h0 * s.y.head;
     uint4 rx[BACK_AHEAD], rd[BACK_AHEAD];
 #pragma unroll
     for (int j = 0; j < BACK_AHEAD; ++j) {
-      const int h = h0 + j * p.per_token;
-      if (live && h < s.heads) {
-        rd[j] = load_row<SPLIT>(dy + h * s.dy.head, at);
-        if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x + h * s.x.head, at);
+      if (h0 + j * p.per_token < mine) {
+        rd[j] = load_row<SPLIT>(dy, at);
+        if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
       }
+      x += x_step;
+      dy += d_step;
     }
     __syncthreads();  // the angles of the round before have been read
     fill_angles(p, cs, token0, tokens);
     __syncthreads();
-    float2 a[4];
-    load_angles(p, cs, t, at, a);
+    const Angles a = load_angles(p, cs, t, at);
+    int h = h0;
     for (int base = 0; base < s.heads; base += BACK_AHEAD * p.per_token) {
 #pragma unroll
       for (int j = 0; j < BACK_AHEAD; ++j) {
-        const int h = base + h0 + j * p.per_token;
-        const bool mine = live && h < s.heads;
-        float v[8], d[8];
+        float2 v[4], d[4];
         unpack(rd[j], d);
         if (NORM != DIT_NORM_NONE) unpack(rx[j], v);
-        const int next = h + BACK_AHEAD * p.per_token;
-        if (mine && next < s.heads) {
-          rd[j] = load_row<SPLIT>(dy + next * s.dy.head, at);
-          if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x + next * s.x.head, at);
+        if (h + BACK_AHEAD * p.per_token < mine) {
+          rd[j] = load_row<SPLIT>(dy, at);
+          if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
         }
+        x += x_step;
+        dy += d_step;
         turn<SPLIT, true>(d, a, at);
         if (NORM != DIT_NORM_NONE) {
-          const float r = normalise<NORM>(v, p, at, inv);
-          float e[8];
-          if (mine && at.active) {
+          const float r = normalise<NORM, LANES>(v, p, at, inv);
+          float2 e[4];
+          if (h < mine) {  // lanes without dimensions add zeros to what is not read
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dw[i] += d[i] * v[i];
-              if (NORM == DIT_NORM_LAYER) db[i] += d[i];
+            for (int i = 0; i < 4; ++i) {
+              dw[i] = fma2(d[i], v[i], dw[i]);
+              if (NORM == DIT_NORM_LAYER) db[i] = add2(db[i], d[i]);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            d[i] = at.active ? d[i] * w[i] : 0.f;
-            e[i] = d[i] * v[i];
+          for (int i = 0; i < 4; ++i) {
+            d[i] = mul2(d[i], w[i]);
+            e[i] = mul2(d[i], v[i]);
           }
-          const float me = group_sum(sum8(e), p.lanes) * inv;
-          const float m = NORM == DIT_NORM_LAYER ? group_sum(sum8(d), p.lanes) * inv : 0.f;
+          const float me = -row_sum<LANES>(sum8(e), p.lanes) * inv;
+          const float m = NORM == DIT_NORM_LAYER ? -row_sum<LANES>(sum8(d), p.lanes) * inv : 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = (d[i] - m - v[i] * me) * r;
+          for (int i = 0; i < 4; ++i) {
+            if (NORM == DIT_NORM_LAYER) d[i] = add2(d[i], both(m));
+            d[i] = mul2(fma2(v[i], both(me), d[i]), both(r));
+          }
         }
-        if (mine) store_row<SPLIT>(dx + h * s.y.head, at, d);
+        if (h < mine) store_row<SPLIT>(dx, at, d);
+        dx += y_step;
+        h += p.per_token;
       }
     }
   }
@@ -311,11 +336,14 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(Args p) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (at.active) sums[g * p.lanes * 8 + (i < 4 ? at.d0 + i : at.d1 + i - 4)] = row ? db[i] : dw[i];
+      if (at.active) {
+        const float2 v = row ? db[i / 2] : dw[i / 2];
+        sums[g * lanes * 8 + (i < 4 ? at.d0 + i : at.d1 + i - 4)] = i % 2 ? v.y : v.x;
+      }
     __syncthreads();
     for (int d = threadIdx.x; d < p.dim; d += THREADS) {
       float v = 0.f;
-      for (int k = 0; k < groups; ++k) v += sums[k * p.lanes * 8 + d];
+      for (int k = 0; k < groups; ++k) v += sums[k * lanes * 8 + d];
       __stcg(mine + row * p.dim + d, v);
     }
   }
@@ -335,7 +363,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(Args p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (c + i < (int)gridDim.x) v[i] += __ldcg(from + (int64_t)(c + i) * outs);
-    (e < p.dim ? p.side[side].dw : p.side[side].db)[e < p.dim ? e : e - p.dim] = sum8(v);
+    (e < p.dim ? p.side[side].dw : p.side[side].db)[e < p.dim ? e : e - p.dim] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
   }
   if (threadIdx.x == 0) *ws_u32(p.ws, WS_TICKET) = 0u;
 }
@@ -402,11 +430,16 @@ static dit_status fill(Args& p, const dit_heads_t* q, const dit_heads_t* k, cons
   return DIT_OK;
 }
 
+// Heads of 40 to 64 and of 72 to 128 dimensions have kernels of their own, whose sums over a row's lanes are unrolled.
+template <bool BACK, int NORM, bool SPLIT>
+static cudaError_t launch(const Args& p, dim3 grid, cudaStream_t st) {
+  auto go = [&](auto* kernel) { return launch_pdl(kernel, grid, dim3(THREADS), 0, st, 1, p); };
+  if (BACK) return p.lanes == 8 ? go(k_norm_rope_back<NORM, SPLIT, 8>) : p.lanes == 16 ? go(k_norm_rope_back<NORM, SPLIT, 16>) : go(k_norm_rope_back<NORM, SPLIT, 0>);
+  return p.lanes == 8 ? go(k_norm_rope<NORM, SPLIT, 8>) : p.lanes == 16 ? go(k_norm_rope<NORM, SPLIT, 16>) : go(k_norm_rope<NORM, SPLIT, 0>);
+}
 template <bool BACK, int NORM>
 static cudaError_t launch(const Args& p, dim3 grid, cudaStream_t st) {
-  const bool split = !p.interleaved && p.pairs;
-  if (BACK) return split ? launch_pdl(k_norm_rope_back<NORM, true>, grid, dim3(THREADS), 0, st, 1, p) : launch_pdl(k_norm_rope_back<NORM, false>, grid, dim3(THREADS), 0, st, 1, p);
-  return split ? launch_pdl(k_norm_rope<NORM, true>, grid, dim3(THREADS), 0, st, 1, p) : launch_pdl(k_norm_rope<NORM, false>, grid, dim3(THREADS), 0, st, 1, p);
+  return !p.interleaved && p.pairs ? launch<BACK, NORM, true>(p, grid, st) : launch<BACK, NORM, false>(p, grid, st);
 }
 template <bool BACK>
 static dit_status launch(const Args& p, int norm, int64_t ctas, cudaStream_t st) {
