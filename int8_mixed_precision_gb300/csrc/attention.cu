@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
 
   const Work w = find_work(p.table, p.plan, FORWARD, p.plan.kv_heads, p.ws);
   const Doc& d = w.doc;
-  const int row0 = w.item.row0;
-  const int n = w.ok ? w.item.end - w.item.begin : 0;  // tiles
+  const int row0 = w.row0;
+  const int n = w.ok ? w.end - w.begin : 0;  // tiles
   const int blocks = w.ok && row0 + p.rows < d.queries ? 2 : 1;
-  const bool work = n > 0 && (int64_t)w.item.end * COLS < (int64_t)d.keys + COLS;
+  const bool work = n > 0 && (int64_t)w.end * COLS < (int64_t)d.keys + COLS;
 
   if (warp < Regs::FIRST_ROWS) Regs::give();
   if (warp == 0) {
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
           for (int k = 0; k < F::CHUNKS; ++k)
             tma_load_3d(smem + t * F::Q_BYTES + k * F::Q_CHUNK, &mq, smem_u32(&c->qfull), k * 64, w.head * p.group, d.q0 + row0 + t * p.rows);
       }
-      int row = d.k0 + w.item.begin * COLS;
+      int row = d.k0 + w.begin * COLS;
       for (int j = 0; j < n; ++j, row += COLS) {
         if (j >= F::STAGES && !mbar_wait(smem_u32(&c->kempty[s]), parity, p.ws, abort)) {
           ok = false;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       const uint32_t a = tmem + F::P + t * F::P_STEP, to = tmem + F::O + t * PD;
       bool ok = true;
       int s = 0, parity = 0;
-      int left = d.keys - w.item.begin * COLS;  // keys from this tile's first on
+      int left = d.keys - w.begin * COLS;  // keys from this tile's first on
       for (int j = 0; j < n && ok; ++j, left -= COLS) {
         const uint32_t v = smem + 2 * F::Q_BYTES + (F::STAGES + s) * F::KV_BYTES;
         ok = warp_wait(smem_u32(&c->vfull[s]), parity, p.ws, abort);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     // rows behind the last one: nothing is masked and nothing stored
     const int64_t hi = live ? seen_end(d, p.plan.frame, row) : INT64_MAX;
     // tiles up to the first one that some row does not see whole
-    const int whole = __reduce_min_sync(0xffffffffu, (int)(min(hi, (int64_t)INT_MAX - COLS) / COLS)) - w.item.begin;
+    const int whole = __reduce_min_sync(0xffffffffu, (int)(min(hi, (int64_t)INT_MAX - COLS) / COLS)) - w.begin;
     float m = -INFINITY, mc = 0.f, l = 0.f;  // the maximum in use, -m c, and the sum
     if (work && t < blocks) {
       const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree);
         if (j >= whole) {
-          const int upto = cols_before<COLS>(hi, (int64_t)(w.item.begin + j) * COLS);
+          const int upto = cols_before<COLS>(hi, (int64_t)(w.begin + j) * COLS);
 #pragma unroll
           for (int i = 0; i < COLS; ++i)
             if (i >= upto) s[i] = 0xff800000u;  // -infinity
@@ -346,9 +346,9 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       const float inv = 1.f / l;
       const int64_t at_row = (int64_t)d.q0 + row;
       __nv_bfloat16* out = p.out.ptr + at_row * p.out.row + head * p.out.head;
-      const bool part = w.item.slot >= 0;
-      const bool room = !part || (int64_t)w.item.slot + row - row0 < p.plan.slots;
-      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.item.slot + row - row0) * PARTIAL<PD> : nullptr;
+      const bool part = w.slot >= 0;
+      const bool room = !part || (int64_t)w.slot + row - row0 < p.plan.slots;
+      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.slot + row - row0) * PARTIAL<PD> : nullptr;
 #pragma unroll
       for (int k = 0; k < PD; k += 32) {
         uint32_t o[32];
@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
   pdl_wait();
   const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
   if (!w.ok) return;
-  const int rows = w.item.slot, pieces = w.item.end, lane = threadIdx.x % 32;
-  if (rows <= 0 || (int64_t)w.item.row0 + rows > w.doc.queries || (int64_t)w.item.begin + (int64_t)rows * pieces > p.plan.slots) {
+  const int rows = w.slot, pieces = w.end, lane = threadIdx.x % 32;
+  if (rows <= 0 || (int64_t)w.row0 + rows > w.doc.queries || (int64_t)w.begin + (int64_t)rows * pieces > p.plan.slots) {
     if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
     return;
   }
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
   using Vec = typename std::conditional<EACH == 2, float2, float4>::type;
   const int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32;
   if (r >= rows) return;
-  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.item.begin + r) * PARTIAL<PD>;
+  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r) * PARTIAL<PD>;
   const int64_t step = (int64_t)rows * PARTIAL<PD>;
   float m = -INFINITY;
   for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(from + i * step + PD));
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
     if (lane < many) {
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (first + lane) * step + PD));
       f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-      l = f == 0.f ? 0.f : f * ml.y;
+      l = ml.x == -INFINITY ? ml.y : f * ml.y;
+      if (ml.x == -INFINITY && ml.y == 0.f) f = -1.f;  // it has seen no key of this row
     }
     for (int i = 0; i < many; i += 4) {
       Vec v[4];
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
       for (int k = 0; k < 4; ++k) {
         const float g = __shfl_sync(0xffffffffu, f, (i + k) & 31);
         sum += __shfl_sync(0xffffffffu, l, (i + k) & 31) * (i + k < many ? 1.f : 0.f);
-        if (i + k < many && g != 0.f) {  // a piece without weight has no part, whatever it holds
+        if (i + k < many && !(g < 0.f)) {
           float* a = reinterpret_cast<float*>(&o);
           const float* b = reinterpret_cast<const float*>(&v[k]);
 #pragma unroll
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
       }
     }
   }
-  const int64_t row = (int64_t)w.item.row0 + r;
+  const int64_t row = (int64_t)w.row0 + r;
   __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
   const float inv = empty ? 0.f : 1.f / sum;
   const float* v = reinterpret_cast<const float*>(&o);

@@ -22,25 +22,25 @@ __host__ __device__ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : 
 __host__ __device__ constexpr int partial_floats(int padded) { return padded + 4; }
 constexpr int FORWARD_COLS = 128, BACK_COLS = 64;
 
-// The table, in int32: documents of DOC_INTS, items of ITEM_INTS (the four lists behind one another), and
-// DIT_ATTENTION_BUCKETS pairs (first item, items) for each list.
-constexpr int DOC_INTS = 8, ITEM_INTS = 8;
+// The table, in int32: the items of the four lists behind one another, and DIT_ATTENTION_BUCKETS pairs (first item,
+// items) for each list.  An item has its document with it, so that one load brings all that a CTA asks of the plan.
 struct Doc {
   int32_t q0, queries, k0, keys, prefix;
   int32_t tile0;  // its first padded row / 128
-  int32_t unused[2];
 };
 struct Item {
-  int32_t doc, row0;    // rows of the document: queries, or keys (GRAD_KV)
+  Doc doc;
+  int32_t row0;         // rows of the document: queries, or keys (GRAD_KV)
   int32_t begin, end;   // tiles of the streamed operand; JOIN: the first partial row, the pieces
   int32_t slot;         // FORWARD: the first partial row, -1: the output itself; JOIN: the rows
-  int32_t unused[3];
+  int32_t unused[6];
 };
-static_assert(sizeof(Doc) == 4 * DOC_INTS && sizeof(Item) == 4 * ITEM_INTS, "");
+constexpr int ITEM_INTS = 16;
+static_assert(sizeof(Item) == 4 * ITEM_INTS, "");
 __host__ __device__ inline int64_t first_item(const dit_attention_plan_t& p, int list) {
   int64_t n = 0;
   for (int i = 0; i < list; ++i) n += p.items[i];
-  return (int64_t)DOC_INTS * p.documents + ITEM_INTS * n;
+  return ITEM_INTS * n;
 }
 __host__ __device__ inline int64_t first_bucket(const dit_attention_plan_t& p, int list) {
   return first_item(p, DIT_ATTENTION_LISTS) + (int64_t)list * 2 * DIT_ATTENTION_BUCKETS;
@@ -71,39 +71,53 @@ struct Heads {
   int64_t row, head;
 };
 
-// What a CTA works at: the item and the head of its index in the list's order.  Items of like cost are a bucket, the
-// costliest first; within one a head's items follow one another and share its keys in L2.
+// What a CTA works at: an item and a head.  Items of like cost are a bucket, the costliest first; within one a
+// head's items follow one another and share its keys in L2.
 struct Work {
   Doc doc;
-  Item item;
-  int head;
-  bool ok;
+  int32_t row0, begin, end, slot;
+  int32_t head;
+  bool ok;  // the entry fits the plan
 };
+__device__ __forceinline__ bool fits(const Work& w, const dit_attention_plan_t& p) {
+  const Doc& d = w.doc;
+  return d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 && (int64_t)d.k0 + d.keys <= p.k_rows &&
+         d.prefix >= 0 && d.tile0 >= 0 && (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.row0 >= 0 && w.begin >= 0;
+}
+// The item and head of index `at`, by a whole warp, each of whose lanes holds a bucket (first item, items; none: 0 items).
+struct Buckets {
+  int first, many;
+  __device__ __forceinline__ Buckets(const int32_t* table, const dit_attention_plan_t& p, int list) : first(0x7fffffff), many(0) {
+    const int lane = threadIdx.x % 32;
+    if (lane < p.buckets[list]) {
+      const int2 v = __ldg(reinterpret_cast<const int2*>(table + first_bucket(p, list)) + lane);
+      first = v.x;
+      many = v.y;
+    }
+  }
+  // the item's index, -1: none
+  __device__ __forceinline__ int find(int64_t at, int heads, int items, int* head) const {
+    const uint32_t below = __ballot_sync(0xffffffffu, (int64_t)first * heads <= at);
+    if (!below) return -1;
+    const int b = 31 - __clz(below), f = __shfl_sync(0xffffffffu, first, b), m = __shfl_sync(0xffffffffu, many, b);
+    const int64_t r = at - (int64_t)f * heads;
+    if (m <= 0 || f < 0 || r < 0 || r >= (int64_t)m * heads) return -1;
+    *head = (int)(r / m);
+    const int i = f + (int)(r % m);
+    return i < items ? i : -1;
+  }
+};
+// The work of this CTA.
 __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attention_plan_t& p, int list, int heads, void* ws) {
   Work w = {};
-  w.ok = false;
-  const int2* bucket = reinterpret_cast<const int2*>(table + first_bucket(p, list));
-  const int64_t at = blockIdx.x;
-  for (int b = 0; b < p.buckets[list]; ++b) {
-    const int2 v = __ldg(bucket + b);
-    if (at < (int64_t)(v.x + v.y) * heads && at >= (int64_t)v.x * heads && v.y > 0) {
-      const int r = (int)(at - (int64_t)v.x * heads);
-      w.head = r / v.y;
-      const int i = v.x + r % v.y;
-      if (i < 0 || i >= p.items[list] || w.head >= heads) break;
-      const int4* it = reinterpret_cast<const int4*>(table + first_item(p, list)) + 2 * (int64_t)i;
-      const int4 a = __ldg(it), c = __ldg(it + 1);
-      w.item = Item{a.x, a.y, a.z, a.w, c.x, {0, 0, 0}};
-      if (a.x < 0 || a.x >= p.documents) break;
-      const int4* dt = reinterpret_cast<const int4*>(table) + 2 * (int64_t)a.x;
-      const int4 d0 = __ldg(dt), d1 = __ldg(dt + 1);
-      w.doc = Doc{d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, {0, 0}};
-      const Doc& d = w.doc;
-      w.ok = d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 &&
-             (int64_t)d.k0 + d.keys <= p.k_rows && d.prefix >= 0 && d.tile0 >= 0 &&
-             (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.item.row0 >= 0 && w.item.begin >= 0;
-      break;
-    }
+  const Buckets buckets(table, p, list);
+  const int i = buckets.find(blockIdx.x, heads, p.items[list], &w.head);
+  if (i >= 0) {
+    const int4* it = reinterpret_cast<const int4*>(table + first_item(p, list)) + (ITEM_INTS / 4) * (int64_t)i;
+    const int4 a = __ldg(it), b = __ldg(it + 1), c = __ldg(it + 2);
+    w.doc = Doc{a.x, a.y, a.z, a.w, b.x, b.y};
+    w.row0 = b.z, w.begin = b.w, w.end = c.x, w.slot = c.y;
+    w.ok = fits(w, p);
   }
   if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
   __syncwarp();
@@ -114,10 +128,10 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
   w.doc.keys = lora::uniform(w.doc.keys);
   w.doc.prefix = lora::uniform(w.doc.prefix);
   w.doc.tile0 = lora::uniform(w.doc.tile0);
-  w.item.row0 = lora::uniform(w.item.row0);
-  w.item.begin = lora::uniform(w.item.begin);
-  w.item.end = lora::uniform(w.item.end);
-  w.item.slot = lora::uniform(w.item.slot);
+  w.row0 = lora::uniform(w.row0);
+  w.begin = lora::uniform(w.begin);
+  w.end = lora::uniform(w.end);
+  w.slot = lora::uniform(w.slot);
   w.head = lora::uniform(w.head);
   w.ok = lora::uniform(w.ok);
   return w;

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__
   if (!w.ok) return;
   const int lane = threadIdx.x % 16, dim = p.plan.dim;
   for (int r = threadIdx.x / 16; r < TILE; r += 16) {
-    const int64_t row = (int64_t)w.item.row0 + r;
+    const int64_t row = (int64_t)w.row0 + r;
     const bool mine = row < w.doc.queries;
     float sum = 0.f;
     if (mine && 8 * lane < dim) {
@@ -141,13 +141,13 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
 
   const Work w = find_work(p.table, p.plan, KEYS ? GRAD_KV : GRAD_Q, KEYS ? p.plan.kv_heads : p.plan.heads, p.ws);
   const Doc& d = w.doc;
-  const int row0 = w.item.row0;
+  const int row0 = w.row0;
   const int x_rows = KEYS ? d.keys : d.queries, y_rows = KEYS ? d.queries : d.keys;  // of the document
   const int x0 = KEYS ? d.k0 : d.q0, y0 = KEYS ? d.q0 : d.k0;
-  const int tiles = w.ok && w.item.end > w.item.begin && (int64_t)w.item.end * COLS < (int64_t)y_rows + COLS ? w.item.end - w.item.begin : 0;
+  const int tiles = w.ok && w.end > w.begin && (int64_t)w.end * COLS < (int64_t)y_rows + COLS ? w.end - w.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
 
-  const int w_begin = w.item.begin;
+  const int w_begin = w.begin;
   if (warp < Regs::FIRST_ROWS) Regs::give();
   const uint32_t ring = smem + 2 * F::X_BYTES;
   if (warp == 0) {
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         }
         if (!p.stall) {
           const uint32_t full = smem_u32(&c->yfull[s]), to = ring + s * F::Y_BYTES, stats = smem + F::STATS + s * F::STAT_BYTES;
-          const int row = (w.item.begin + tile) * COLS;
+          const int row = (w.begin + tile) * COLS;
           mbar_expect_tx(full, 2 * F::Y_BYTES + (KEYS ? F::STAT_BYTES : 0));
 #pragma unroll
           for (int k = 0; k < F::CHUNKS; ++k) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
           g[i + h + 1] = __float_as_uint(t.y);
         }
       }
-      const int at_tile = w.item.begin + tile;
+      const int at_tile = w.begin + tile;
       if (at_tile < whole_from || at_tile >= whole_to) {  // masked pairs: p and ds are zero, whatever was there
         const int64_t col0 = (int64_t)at_tile * COLS + col;
         const int from = cols_before<MINE>(lo, col0), to = cols_before<MINE>(hi, col0);

@@ -64,7 +64,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
         pre > MAX_ROWS || q_rows + queries[i] > MAX_ROWS || begin + keys[i] > MAX_ROWS)
       return DIT_ERR_INVALID_ARG;
     if (frame == 0 && pre > 0) return DIT_ERR_INVALID_ARG;
-    docs[(size_t)i] = Doc{(int32_t)q_rows, (int32_t)queries[i], keys[i] ? (int32_t)begin : 0, (int32_t)keys[i], (int32_t)pre, (int32_t)tiles, {0, 0}};
+    docs[(size_t)i] = Doc{(int32_t)q_rows, (int32_t)queries[i], keys[i] ? (int32_t)begin : 0, (int32_t)keys[i], (int32_t)pre, (int32_t)tiles};
     q_rows += queries[i];
     k_next = begin + keys[i];
     if (keys[i] && k_next > plan->k_rows) plan->k_rows = k_next;
@@ -91,7 +91,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
       const int64_t n = (seen_end(docs[i], frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
       const double each = last - r >= rt ? 1.0 : 0.6;
-      lists[FORWARD].push_back({Item{(int32_t)i, (int32_t)r, 0, (int32_t)n, -1, {0, 0, 0}}, START + each * (double)n});
+      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, {}}, START + each * (double)n});
     }
   // Few items: their keys are cut into pieces, as many as bring the last CTA's end forward most.
   int64_t ctas = (int64_t)lists[FORWARD].size() * kv_heads;
@@ -133,10 +133,10 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
           lists[FORWARD].push_back(c);
           continue;
         }
-        const Doc& d = docs[(size_t)c.item.doc];
+        const Doc& d = c.item.doc;
         const int32_t rows = (int32_t)std::min<int64_t>(2 * rt, d.queries - c.item.row0);
         const double each = (c.cost - START) / (double)n;
-        lists[JOIN].push_back({Item{c.item.doc, c.item.row0, plan->slots, (int32_t)pieces, rows, {0, 0, 0}}, 1.0});
+        lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)pieces, rows, {}}, 1.0});
         for (int64_t k = 0; k < pieces; ++k) {
           Item it = c.item;
           it.begin = (int32_t)(n * k / pieces);
@@ -153,12 +153,12 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const Doc& d = docs[i];
       for (int64_t r = 0; r < d.queries; r += TILE) {
         const int64_t n = (seen_end(d, frame, std::min<int64_t>(d.queries, r + TILE) - 1) + cols - 1) / cols;
-        lists[GRAD_Q].push_back({Item{(int32_t)i, (int32_t)r, 0, (int32_t)n, -1, {0, 0, 0}}, START + (double)n});
+        lists[GRAD_Q].push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, {}}, START + (double)n});
       }
       const int64_t end = ((int64_t)d.queries + cols - 1) / cols;
       for (int64_t k = 0; k < d.keys; k += TILE) {
         const int64_t begin = std::min(end, seen_from(d, frame, k) / cols);
-        lists[GRAD_KV].push_back({Item{(int32_t)i, (int32_t)k, (int32_t)begin, (int32_t)end, -1, {0, 0, 0}}, START + (double)(end - begin)});
+        lists[GRAD_KV].push_back({Item{d, (int32_t)k, (int32_t)begin, (int32_t)end, -1, {}}, START + (double)(end - begin)});
       }
     }
   std::vector<std::pair<int32_t, int32_t>> buckets[DIT_ATTENTION_LISTS];
@@ -184,7 +184,6 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   if (!table) return DIT_OK;
   if (table_ints < plan->table_ints) return DIT_ERR_INVALID_ARG;
   std::fill(table, table + plan->table_ints, 0);
-  std::copy_n(reinterpret_cast<const int32_t*>(docs.data()), docs.size() * DOC_INTS, table);
   for (int l = 0; l < DIT_ATTENTION_LISTS; ++l) {
     int32_t* o = table + first_item(*plan, l);
     for (const Costed& c : lists[l]) {

@@ -64,24 +64,30 @@ def test_norm_refusals(dit):
 # ----------------------------------------------------------------------------------------
 
 def lists(plan):
-    """Documents, and the four lists of items, from the table."""
+    """The four lists of items, each (document's q0, queries, k0, keys, prefix, first padded tile; row, begin, end, slot), and the buckets."""
     i, t = plan.info, plan.table.tolist()
-    docs = [t[8 * k:8 * k + 8] for k in range(i.documents)]
-    at, out = 8 * i.documents, []
+    at, out = 0, []
     for n in i.items:
-        out.append([t[at + 8 * k:at + 8 * k + 8] for k in range(n)])
-        at += 8 * n
+        out.append([t[at + 16 * k:at + 16 * k + 10] for k in range(n)])
+        at += 16 * n
     buckets = []
     for n in i.buckets:
         buckets.append([t[at + 2 * k:at + 2 * k + 2] for k in range(n)])
         at += 64
     assert at == i.table_ints
-    return docs, out, buckets
+    return out, buckets
 
 
 def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     plan = dit.AttentionPlan(queries, heads, dim, kv_heads=kv_heads, kv_lengths=keys, frame=frame, prefix=prefix, training=True, device="cpu")
-    docs, (fwd, joins, gq, gk), buckets = lists(plan)
+    found, buckets = lists(plan)
+    # each document's statistics begin at a multiple of 128
+    places, q0, k0, at = {}, 0, 0, 0
+    for i, (n, m, pre) in enumerate(zip(queries, keys, [prefix] * len(keys))):
+        places[(q0, n, k0 if m else 0, m, pre, at)] = i
+        q0, k0, at = q0 + n, k0 + m, at + -(-n // 128)
+    assert plan.info.padded_rows == at * 128
+    fwd, joins, gq, gk = ([(places[tuple(item[:6])], *item[6:]) for item in items] for items in found)
     cols, rt, back = 128, 128 // (heads // kv_heads), 64
     assert plan.q_rows == sum(queries)
     for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
@@ -95,7 +101,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     met = [torch.zeros(n, m, dtype=torch.int32) for n, m in zip(queries, keys)]
     rows = [torch.zeros(n, dtype=torch.int32) for n in queries]
     slots = {}
-    for doc, row0, begin, end, slot, *_ in fwd:
+    for doc, row0, begin, end, slot in fwd:
         part = slice(row0, min(queries[doc], row0 + 2 * rt))
         met[doc][part, begin * cols:end * cols] += 1
         assert end * cols < keys[doc] + cols
@@ -106,7 +112,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
             slots[slot] = (doc, row0, n, begin, end)
             assert slot + n <= plan.info.slots
     used = torch.zeros(plan.info.slots, dtype=torch.int32)
-    for doc, row0, first, pieces, n, *_ in joins:
+    for doc, row0, first, pieces, n in joins:
         rows[doc][row0:row0 + n] += 1
         at = 0
         for k in range(pieces):
@@ -130,12 +136,6 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
             assert not left.any()
             assert end * back < s.shape[1] + back
         assert all((w == 1).all() for w in whole)
-    # each document's statistics begin at a multiple of 128
-    at = 0
-    for d, n in zip(docs, queries):
-        assert d[5] * 128 == at
-        at += -(-n // 128) * 128
-    assert plan.info.padded_rows == at
     return plan
 
 
