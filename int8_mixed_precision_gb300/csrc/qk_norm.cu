@@ -19,11 +19,11 @@
 namespace dit6 {
 namespace qk {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256, BACK_THREADS = 512;
 constexpr int MAX_DIM = 256;
 constexpr int AHEAD = 4;         // heads of a thread in flight
 constexpr int BACK_AHEAD = 2;
-constexpr int MAX_CTAS = 152 * 2;  // of the backward pass, for each of q and k
+constexpr int BACK_CTAS = 152;  // of the backward pass, most: one to an SM, divided between q and k by their heads
 constexpr int64_t MAX_TOKENS = 0x7fffff00;
 
 struct Pair {
@@ -51,7 +51,8 @@ struct Args {
   float* partials;
   void* ws;
   int dim, pairs, axes, interleaved;
-  int lanes, per_token, ctas;  // lanes to a row, groups of lanes to a token, CTAs to a side
+  int lanes, per_token;  // lanes to a row, groups of lanes to a token
+  int ctas[2];           // backward: of q and of k
   int sides;
   float eps;
   int want;  // gradients of the parameters
@@ -171,6 +172,7 @@ __device__ __forceinline__ float normalise(float2 (&v)[4], const Args& p, const 
   return r;
 }
 // cos and sin of the tokens of a CTA, one thread to a pair.
+template <int THREADS>
 __device__ __forceinline__ void fill_angles(const Args& p, float2* cs, int64_t token0, int tokens) {
   for (int i = threadIdx.x; i < tokens * p.pairs; i += THREADS) {
     const int t = i / p.pairs, pair = i - t * p.pairs;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ A
     if (h0 + j * p.per_token < mine) raw[j] = load_row<SPLIT>(x, at);
     x += x_step;
   }
-  fill_angles(p, cs, token0, tokens);
+  fill_angles<THREADS>(p, cs, token0, tokens);
   __syncthreads();
   const Angles a = load_angles(p, cs, t, at);
   float2 w[4], b[4];
@@ -246,15 +248,16 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ A
 // Tokens are dealt to the CTAs in turn; each thread sums its parameters' gradients over all of its rows, the CTA adds
 // them up over its groups, and the CTA that finishes last over the CTAs, always in the same order.
 template <int NORM, bool SPLIT, int LANES>
-__global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid_constant__ Args p) {
   pdl_launch_dependents();
-  __shared__ float2 cs[THREADS * 4];
-  __shared__ float sums[THREADS * 8];
+  __shared__ float2 cs[BACK_THREADS * 4];
+  __shared__ float sums[BACK_THREADS * 8];
   __shared__ bool last;
   pdl_wait();
-  const Side& s = p.side[blockIdx.y];
+  const int which = (int)blockIdx.x >= p.ctas[0], cta = blockIdx.x - (which ? p.ctas[0] : 0);
+  const Side& s = p.side[which];
   const int lanes = LANES ? LANES : p.lanes;
-  const int groups = THREADS / lanes, tokens = groups / p.per_token;
+  const int groups = BACK_THREADS / lanes, tokens = groups / p.per_token;
   const int g = threadIdx.x / lanes, t = g / p.per_token, h0 = g - t * p.per_token;
   const Place at = place_of(p, threadIdx.x & (lanes - 1));
   const float inv = 1.f / (float)p.dim;
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constan
   for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
   const int64_t blocks = (p.tokens + tokens - 1) / tokens;
   const int64_t x_step = p.per_token * s.x.head, d_step = p.per_token * s.dy.head, y_step = p.per_token * s.y.head;
-  for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+  for (int64_t blk = cta; blk < blocks; blk += p.ctas[which]) {
     const int64_t token0 = blk * tokens, token = token0 + t;
     const int mine = token < p.tokens ? s.heads : 0;  // heads that there are
     const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constan
       dy += d_step;
     }
     __syncthreads();  // the angles of the round before have been read
-    fill_angles(p, cs, token0, tokens);
+    fill_angles<BACK_THREADS>(p, cs, token0, tokens);
     __syncthreads();
     const Angles a = load_angles(p, cs, t, at);
     int h = h0;
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constan
   if (NORM == DIT_NORM_NONE || !p.want) return;
   constexpr int ROWS = NORM == DIT_NORM_LAYER ? 2 : 1;
   const int outs = ROWS * p.dim;  // of one side
-  float* mine = p.partials + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * outs;
+  float* mine = p.partials + (int64_t)blockIdx.x * outs;
 #pragma unroll
   for (int row = 0; row < ROWS; ++row) {
     __syncthreads();
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constan
         sums[g * lanes * 8 + (i < 4 ? at.d0 + i : at.d1 + i - 4)] = i % 2 ? v.y : v.x;
       }
     __syncthreads();
-    for (int d = threadIdx.x; d < p.dim; d += THREADS) {
+    for (int d = threadIdx.x; d < p.dim; d += BACK_THREADS) {
       float v = 0.f;
       for (int k = 0; k < groups; ++k) v += sums[k * lanes * 8 + d];
       __stcg(mine + row * p.dim + d, v);
@@ -350,20 +353,24 @@ __global__ void __launch_bounds__(THREADS) k_norm_rope_back(const __grid_constan
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    last = atomicAdd(ws_u32(p.ws, WS_TICKET), 1u) == gridDim.x * gridDim.y - 1;
+    last = atomicAdd(ws_u32(p.ws, WS_TICKET), 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  for (int o = threadIdx.x; o < p.sides * outs; o += THREADS) {
-    const int side = o / outs, e = o - side * outs;
-    const float* from = p.partials + (int64_t)side * gridDim.x * outs + e;
-    float v[8] = {};
-    for (int c = 0; c < (int)gridDim.x; c += 8)
+  for (int o = threadIdx.x; o < p.sides * outs; o += BACK_THREADS) {
+    const int side = o / outs, e = o - side * outs, many = p.ctas[side];
+    const float* from = p.partials + (int64_t)(side ? p.ctas[0] : 0) * outs + e;
+    float v[16] = {};
+    for (int c = 0; c < many; c += 16)  // sixteen loads in flight
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < (int)gridDim.x) v[i] += __ldcg(from + (int64_t)(c + i) * outs);
-    (e < p.dim ? p.side[side].dw : p.side[side].db)[e < p.dim ? e : e - p.dim] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      for (int i = 0; i < 16; ++i)
+        if (c + i < many) v[i] += __ldcg(from + (int64_t)(c + i) * outs);
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+      for (int i = 0; i < w; ++i) v[i] += v[i + w];
+    (e < p.dim ? p.side[side].dw : p.side[side].db)[e < p.dim ? e : e - p.dim] = v[0];
   }
   if (threadIdx.x == 0) *ws_u32(p.ws, WS_TICKET) = 0u;
 }
@@ -422,18 +429,18 @@ static dit_status fill(Args& p, const dit_heads_t* q, const dit_heads_t* k, cons
   p.lanes = lanes_of(dim);
   // About AHEAD heads to a group of lanes: the angles and weights are then read once for four rows.  Batches that
   // fill less than two CTAs an SM get more groups to a token.
-  const int groups = THREADS / p.lanes;
+  const int groups = (back ? BACK_THREADS : THREADS) / p.lanes;
   const int heads = p.sides == 2 && p.side[1].heads > p.side[0].heads ? p.side[1].heads : p.side[0].heads;
   p.per_token = 1;
   while (p.per_token < groups && p.per_token * AHEAD < heads) p.per_token *= 2;
-  while (p.per_token < groups && p.per_token < heads && tokens * p.per_token < (int64_t)groups * 2 * num_sms()) p.per_token *= 2;
+  while (p.per_token < groups && p.per_token < heads && tokens * p.per_token < (int64_t)groups * (back ? 1 : 2) * num_sms()) p.per_token *= 2;
   return DIT_OK;
 }
 
 // Heads of 40 to 64 and of 72 to 128 dimensions have kernels of their own, whose sums over a row's lanes are unrolled.
 template <bool BACK, int NORM, bool SPLIT>
 static cudaError_t launch(const Args& p, dim3 grid, cudaStream_t st) {
-  auto go = [&](auto* kernel) { return launch_pdl(kernel, grid, dim3(THREADS), 0, st, 1, p); };
+  auto go = [&](auto* kernel) { return launch_pdl(kernel, grid, dim3(BACK ? BACK_THREADS : THREADS), 0, st, 1, p); };
   if (BACK) return p.lanes == 8 ? go(k_norm_rope_back<NORM, SPLIT, 8>) : p.lanes == 16 ? go(k_norm_rope_back<NORM, SPLIT, 16>) : go(k_norm_rope_back<NORM, SPLIT, 0>);
   return p.lanes == 8 ? go(k_norm_rope<NORM, SPLIT, 8>) : p.lanes == 16 ? go(k_norm_rope<NORM, SPLIT, 16>) : go(k_norm_rope<NORM, SPLIT, 0>);
 }
@@ -442,8 +449,7 @@ static cudaError_t launch(const Args& p, dim3 grid, cudaStream_t st) {
   return !p.interleaved && p.pairs ? launch<BACK, NORM, true>(p, grid, st) : launch<BACK, NORM, false>(p, grid, st);
 }
 template <bool BACK>
-static dit_status launch(const Args& p, int norm, int64_t ctas, cudaStream_t st) {
-  const dim3 grid((unsigned)ctas, (unsigned)p.sides);
+static dit_status launch(const Args& p, int norm, const dim3& grid, cudaStream_t st) {
   const cudaError_t e = norm == DIT_NORM_LAYER ? launch<BACK, DIT_NORM_LAYER>(p, grid, st)
                         : norm == DIT_NORM_RMS ? launch<BACK, DIT_NORM_RMS>(p, grid, st)
                                                : launch<BACK, DIT_NORM_NONE>(p, grid, st);
@@ -477,7 +483,7 @@ extern "C" dit_status dit_rotary_table(const int32_t* dims, int axes, double the
 
 extern "C" size_t dit_qk_norm_scratch_bytes(int dim) {
   if (dim <= 0 || dim > qk::MAX_DIM) return 0;
-  return (size_t)2 * qk::MAX_CTAS * 2 * dim * sizeof(float);
+  return (size_t)qk::BACK_CTAS * 2 * dim * sizeof(float);
 }
 
 extern "C" dit_status dit_qk_norm_rope(const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* q_out, const dit_heads_t* k_out,
@@ -487,7 +493,7 @@ extern "C" dit_status dit_qk_norm_rope(const dit_heads_t* q, const dit_heads_t* 
   const dit_status e = qk::fill(p, q, k, nullptr, nullptr, q_out, k_out, tokens, dim, norm, params, eps, rot, positions, false);
   if (e != DIT_OK || tokens == 0) return e;
   const int per_cta = qk::THREADS / p.lanes / p.per_token;
-  return qk::launch<false>(p, norm, (tokens + per_cta - 1) / per_cta, stream);
+  return qk::launch<false>(p, norm, dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)p.sides), stream);
 }
 
 extern "C" dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* dq_out,
@@ -514,9 +520,17 @@ extern "C" dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_
   p.partials = reinterpret_cast<float*>(scratch);
   p.ws = ws;
   if (tokens == 0 && !p.want) return DIT_OK;
-  const int per_cta = qk::THREADS / p.lanes / p.per_token;
-  int64_t ctas = (tokens + per_cta - 1) / per_cta;
-  if (ctas > qk::MAX_CTAS) ctas = qk::MAX_CTAS;
-  if (ctas < 1) ctas = 1;  // no tokens: the parameters' gradients are zeros
-  return qk::launch<true>(p, norm, ctas, stream);
+  const int per_cta = qk::BACK_THREADS / p.lanes / p.per_token;
+  const int64_t blocks = (tokens + per_cta - 1) / per_cta;
+  for (int i = 0; i < p.sides; ++i) {
+    int64_t share = qk::BACK_CTAS;
+    if (p.sides == 2) {
+      const int64_t q_share = (int64_t)qk::BACK_CTAS * p.side[0].heads / ((int64_t)p.side[0].heads + p.side[1].heads);
+      share = q_share < 1 ? 1 : q_share > qk::BACK_CTAS - 1 ? qk::BACK_CTAS - 1 : q_share;
+      if (i) share = qk::BACK_CTAS - share;
+    }
+    // without tokens a CTA still writes the parameters' gradients, zeros
+    p.ctas[i] = (int)(blocks < 1 ? 1 : blocks < share ? blocks : share);
+  }
+  return qk::launch<true>(p, norm, dim3((unsigned)(p.ctas[0] + p.ctas[1])), stream);
 }
