@@ -103,17 +103,19 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     }
     fence_barrier_init();
     __syncwarp();
+  } else if (warp == 2) {
+    if (lane < 3) prefetch_tmap(lane == 0 ? &mq : lane == 1 ? &mk : &mv);
+    __syncwarp();
   } else if (warp == 1) {
     tmem_alloc(smem_u32(&c->tmem), 512);
     fence_before();
   }
+  pdl_wait();
+  const Work w = find_work(p.table, p.plan, FORWARD, p.plan.kv_heads, p.ws);
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(c->tmem);
   volatile int* abort = &c->abort;
-  pdl_wait();
-
-  const Work w = find_work(p.table, p.plan, FORWARD, p.plan.kv_heads, p.ws);
   const Doc& d = w.doc;
   const int row0 = w.row0;
   const int n = w.ok ? w.end - w.begin : 0;  // tiles
@@ -383,9 +385,9 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
 
 // The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order, a warp to each row
 // and head.  A lane looks at the maxima and sums of every 32nd piece; the weights then pass from lane to lane.
-constexpr int JOIN_ROWS = 8;  // rows of a CTA
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 32;  // of a CTA
 template <int PD>
-__global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_constant__ FwdArgs p) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid_constant__ FwdArgs p) {
   pdl_launch_dependents();
   pdl_wait();
   const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
@@ -397,51 +399,49 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) k_attention_join(const __grid_
   }
   constexpr int EACH = PD / 32;
   using Vec = typename std::conditional<EACH == 2, float2, float4>::type;
-  const int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32;
-  if (r >= rows) return;
-  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r) * PARTIAL<PD>;
-  const int64_t step = (int64_t)rows * PARTIAL<PD>;
-  float m = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(from + i * step + PD));
-  m = warp_max_f(m);
-  const bool empty = m == -INFINITY;  // a query that sees no key (or whose scores are all -infinity: no weight anywhere)
-  float sum = 0.f;
-  Vec o = {};
-  for (int first = 0; first < pieces; first += 32) {
-    const int many = min(32, pieces - first);
-    float f = 0.f, l = 0.f;
-    if (lane < many) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (first + lane) * step + PD));
-      f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-      l = ml.x == -INFINITY ? ml.y : f * ml.y;
-      if (ml.x == -INFINITY && ml.y == 0.f) f = -1.f;  // it has seen no key of this row
-    }
-    for (int i = 0; i < many; i += 4) {
-      Vec v[4];
+  for (int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32; r < min(rows, (int)(blockIdx.y + 1) * JOIN_ROWS); r += JOIN_WARPS) {
+    const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r) * PARTIAL<PD>;
+    const int64_t step = (int64_t)rows * PARTIAL<PD>;
+    float m = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(from + i * step + PD));
+    m = warp_max_f(m);
+    const bool empty = m == -INFINITY;  // a query that sees no key (or whose scores are all -infinity: no weight anywhere)
+    float sum = 0.f, o[EACH] = {};
+    for (int first = 0; first < pieces; first += 32) {
+      const int many = min(32, pieces - first);
+      float f = 0.f, l = 0.f;
+      if (lane < many) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (first + lane) * step + PD));
+        f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
+        l = ml.x == -INFINITY ? ml.y : f * ml.y;
+        if (ml.x == -INFINITY && ml.y == 0.f) f = -1.f;  // it has seen no key of this row
+      }
+      for (int i = 0; i < many; i += 4) {
+        Vec v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k < many) v[k] = __ldcg(reinterpret_cast<const Vec*>(from + (first + i + k) * step) + lane);
+        for (int k = 0; k < 4; ++k)
+          if (i + k < many) v[k] = __ldcg(reinterpret_cast<const Vec*>(from + (first + i + k) * step) + lane);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float g = __shfl_sync(0xffffffffu, f, (i + k) & 31);
-        sum += __shfl_sync(0xffffffffu, l, (i + k) & 31) * (i + k < many ? 1.f : 0.f);
-        if (i + k < many && !(g < 0.f)) {
-          float* a = reinterpret_cast<float*>(&o);
-          const float* b = reinterpret_cast<const float*>(&v[k]);
+        for (int k = 0; k < 4; ++k) {
+          const float g = __shfl_sync(0xffffffffu, f, (i + k) & 31), part = __shfl_sync(0xffffffffu, l, (i + k) & 31);
+          if (i + k < many) {
+            sum += part;
+            const float* b = reinterpret_cast<const float*>(&v[k]);
 #pragma unroll
-          for (int e = 0; e < EACH; ++e) a[e] += g * b[e];
+            for (int e = 0; e < EACH; ++e)
+              if (!(g < 0.f)) o[e] += g * b[e];
+          }
         }
       }
     }
-  }
-  const int64_t row = (int64_t)w.row0 + r;
-  __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
-  const float inv = empty ? 0.f : 1.f / sum;
-  const float* v = reinterpret_cast<const float*>(&o);
+    const int64_t row = (int64_t)w.row0 + r;
+    __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
+    const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int k = 0; k < EACH; k += 2)
-    if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(v[k] * inv, v[k + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
+    for (int k = 0; k < EACH; k += 2)
+      if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(o[k] * inv, o[k + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
+  }
 }
 
 template <int PD>
@@ -459,7 +459,7 @@ static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads
   if (prepare_kernel<Regs>(checked, once, k_attention<PD>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
   if (launch_pdl(k_attention<PD>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
     return DIT_ERR_CUDA;
-  if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads), (unsigned)(2 * a.rows + JOIN_ROWS - 1) / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, 1, a) != cudaSuccess)
+  if (a.plan.items[JOIN] && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads), (unsigned)(2 * a.rows + JOIN_ROWS - 1) / JOIN_ROWS), dim3(32 * JOIN_WARPS), 0, st, 1, a) != cudaSuccess)
     return DIT_ERR_CUDA;
   return DIT_OK;
 }

@@ -129,17 +129,19 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     }
     fence_barrier_init();
     __syncwarp();
+  } else if (warp == 2) {
+    if (lane < 4) prefetch_tmap(lane == 0 ? &mx1 : lane == 1 ? &mx2 : lane == 2 ? &my1 : &my2);
+    __syncwarp();
   } else if (warp == 1) {
     tmem_alloc(smem_u32(&c->tmem), 512);
     fence_before();
   }
+  pdl_wait();
+  const Work w = find_work(p.table, p.plan, KEYS ? GRAD_KV : GRAD_Q, KEYS ? p.plan.kv_heads : p.plan.heads, p.ws);
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(c->tmem);
   volatile int* abort = &c->abort;
-  pdl_wait();
-
-  const Work w = find_work(p.table, p.plan, KEYS ? GRAD_KV : GRAD_Q, KEYS ? p.plan.kv_heads : p.plan.heads, p.ws);
   const Doc& d = w.doc;
   const int row0 = w.row0;
   const int x_rows = KEYS ? d.keys : d.queries, y_rows = KEYS ? d.queries : d.keys;  // of the document

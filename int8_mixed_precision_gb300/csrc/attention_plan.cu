@@ -40,7 +40,7 @@ static double makespan(std::vector<double> pieces, int heads) {
 
 // A forward CTA's time in tiles of one row block: its start and end, then its tiles.  Pieces of a split item write and
 // read partial results besides.
-constexpr double START = 4.0, SPLIT_END = 3.0;
+constexpr double START = 5.0, SPLIT_END = 2.0, JOIN_TIME = 6.0;
 
 static dit_status make_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
                             int64_t documents, int64_t frame, int heads, int kv_heads, int dim, int training,
@@ -93,8 +93,13 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const double each = last - r >= rt ? 1.0 : 0.6;
       lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, {}}, START + each * (double)n});
     }
-  // Few items: their keys are cut into pieces, as many as bring the last CTA's end forward most.
-  int64_t ctas = (int64_t)lists[FORWARD].size() * kv_heads;
+  // Few items: their keys are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
+  // brings the end of the last CTA forward most.
+  auto cut = [](int64_t n, int64_t len, bool even, int64_t k) {  // where piece k begins
+    const int64_t pieces = (n + len - 1) / len;
+    return even ? n * k / pieces : std::min(n, k * len);
+  };
+  const int64_t ctas = (int64_t)lists[FORWARD].size() * kv_heads;
   if (ctas && ctas < 4 * SMS) {
     std::vector<double> now;
     int64_t most = 0;
@@ -104,24 +109,27 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     }
     double best = makespan(now, kv_heads);
     int64_t longest = 0;  // tiles of a piece; 0: items stay whole
-    for (int64_t len = most; len >= 2; len = len > 16 ? len * 7 / 8 : len - 1) {
-      now.clear();
+    bool evenly = true;
+    for (int64_t len = most; len >= 2; len = len > 24 ? len * 15 / 16 : len - 1) {
       int64_t total = 0;
-      for (const Costed& c : lists[FORWARD]) {
-        const int64_t n = c.item.end, pieces = (n + len - 1) / len;
-        const double each = n ? (c.cost - START) / (double)n : 0.0;
-        if (pieces <= 1) {
-          now.push_back(c.cost);
-        } else {
-          for (int64_t k = 0; k < pieces; ++k) now.push_back(START + SPLIT_END + each * (double)(n * (k + 1) / pieces - n * k / pieces));
-        }
-        total += std::max<int64_t>(pieces, 1);
-      }
+      for (const Costed& c : lists[FORWARD]) total += std::max<int64_t>((c.item.end + len - 1) / len, 1);
       if (total * kv_heads > 6 * SMS) break;
-      const double t = makespan(now, kv_heads) + SPLIT_END;
-      if (t < best) {
-        best = t;
-        longest = len;
+      for (int even = 0; even < 2; ++even) {
+        now.clear();
+        for (const Costed& c : lists[FORWARD]) {
+          const int64_t n = c.item.end, pieces = (n + len - 1) / len;
+          const double each = n ? (c.cost - START) / (double)n : 0.0;
+          if (pieces <= 1)
+            now.push_back(c.cost);
+          else
+            for (int64_t k = 0; k < pieces; ++k) now.push_back(START + SPLIT_END + each * (double)(cut(n, len, even, k + 1) - cut(n, len, even, k)));
+        }
+        const double t = makespan(now, kv_heads) + JOIN_TIME;
+        if (t < best) {
+          best = t;
+          longest = len;
+          evenly = even;
+        }
       }
     }
     if (longest) {
@@ -139,8 +147,8 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
         lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)pieces, rows, {}}, 1.0});
         for (int64_t k = 0; k < pieces; ++k) {
           Item it = c.item;
-          it.begin = (int32_t)(n * k / pieces);
-          it.end = (int32_t)(n * (k + 1) / pieces);
+          it.begin = (int32_t)cut(n, longest, evenly, k);
+          it.end = (int32_t)cut(n, longest, evenly, k + 1);
           it.slot = plan->slots;
           plan->slots += rows;
           lists[FORWARD].push_back({it, START + SPLIT_END + each * (double)(it.end - it.begin)});
