@@ -383,9 +383,10 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   }
 }
 
-// The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order, a warp to each row
-// and head.  A lane looks at the maxima and sums of every 32nd piece; the weights then pass from lane to lane.
-constexpr int JOIN_WARPS = 8, JOIN_ROWS = 32;  // of a CTA
+// The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order, a warp to two rows of
+// a head.  Bound by latency: a lane holds the maximum and the sum of every 32nd piece, and those and the first pieces' values are
+// asked for at once.
+constexpr int JOIN_WARPS = 8, JOIN_EACH = 2, JOIN_ROWS = JOIN_WARPS * JOIN_EACH;  // rows of a warp and of a CTA
 template <int PD>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid_constant__ FwdArgs p) {
   pdl_launch_dependents();
@@ -397,50 +398,74 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid
     if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
     return;
   }
-  constexpr int EACH = PD / 32;
+  constexpr int EACH = PD / 32, AHEAD = 4;
   using Vec = typename std::conditional<EACH == 2, float2, float4>::type;
-  for (int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32; r < min(rows, (int)(blockIdx.y + 1) * JOIN_ROWS); r += JOIN_WARPS) {
-    const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r) * PARTIAL<PD>;
-    const int64_t step = (int64_t)rows * PARTIAL<PD>;
-    float m = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(from + i * step + PD));
-    m = warp_max_f(m);
-    const bool empty = m == -INFINITY;  // a query that sees no key (or whose scores are all -infinity: no weight anywhere)
-    float sum = 0.f, o[EACH] = {};
-    for (int first = 0; first < pieces; first += 32) {
-      const int many = min(32, pieces - first);
-      float f = 0.f, l = 0.f;
-      if (lane < many) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + (first + lane) * step + PD));
-        f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-        l = ml.x == -INFINITY ? ml.y : f * ml.y;
-        if (ml.x == -INFINITY && ml.y == 0.f) f = -1.f;  // it has seen no key of this row
-      }
-      for (int i = 0; i < many; i += 4) {
-        Vec v[4];
+  const int r0 = blockIdx.y * JOIN_ROWS + threadIdx.x / 32 * JOIN_EACH;
+  const int64_t step = (int64_t)rows * PARTIAL<PD>;
+  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r0) * PARTIAL<PD>;
+  auto stat = [&](int r, int i) {  // maximum and sum of piece i; none: no key seen
+    return r0 + r < rows && i < pieces ? __ldcg(reinterpret_cast<const float2*>(from + r * PARTIAL<PD> + i * step + PD)) : make_float2(-INFINITY, 0.f);
+  };
+  auto value = [&](int r, int i) {
+    return r0 + r < rows && i < pieces ? __ldcg(reinterpret_cast<const Vec*>(from + r * PARTIAL<PD> + i * step) + lane) : Vec{};
+  };
+  float2 ml[JOIN_EACH];
+  Vec v[JOIN_EACH][AHEAD];
+  float m[JOIN_EACH], sum[JOIN_EACH], o[JOIN_EACH][EACH];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (i + k < many) v[k] = __ldcg(reinterpret_cast<const Vec*>(from + (first + i + k) * step) + lane);
+  for (int r = 0; r < JOIN_EACH; ++r) {
+    ml[r] = stat(r, lane);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float g = __shfl_sync(0xffffffffu, f, (i + k) & 31), part = __shfl_sync(0xffffffffu, l, (i + k) & 31);
-          if (i + k < many) {
-            sum += part;
-            const float* b = reinterpret_cast<const float*>(&v[k]);
+    for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, k);
+  }
 #pragma unroll
-            for (int e = 0; e < EACH; ++e)
-              if (!(g < 0.f)) o[e] += g * b[e];
-          }
+  for (int r = 0; r < JOIN_EACH; ++r) {
+    m[r] = ml[r].x;
+    for (int i = lane + 32; i < pieces; i += 32) m[r] = fmaxf(m[r], stat(r, i).x);
+    m[r] = warp_max_f(m[r]);
+    sum[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) o[r][e] = 0.f;
+  }
+  for (int first = 0; first < pieces; first += 32) {
+    float f[JOIN_EACH], l[JOIN_EACH];
+#pragma unroll
+    for (int r = 0; r < JOIN_EACH; ++r) {
+      if (first) ml[r] = stat(r, first + lane);
+      f[r] = ml[r].x == -INFINITY ? 0.f : exp2_approx(ml[r].x - m[r]);
+      l[r] = ml[r].x == -INFINITY ? ml[r].y : f[r] * ml[r].y;
+      if (ml[r].x == -INFINITY && ml[r].y == 0.f) f[r] = -1.f;  // it has seen no key of this row
+    }
+    const int many = min(32, pieces - first);
+    for (int i = 0; i < many; i += AHEAD) {
+#pragma unroll
+      for (int r = 0; r < JOIN_EACH; ++r) {
+        if (first + i)
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, first + i + k);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {  // lanes behind the last piece have f -1 and l 0
+          const float g = __shfl_sync(0xffffffffu, f[r], i + k);
+          sum[r] += __shfl_sync(0xffffffffu, l[r], i + k);
+          const float* b = reinterpret_cast<const float*>(&v[r][k]);
+#pragma unroll
+          for (int e = 0; e < EACH; ++e)
+            if (!(g < 0.f)) o[r][e] += g * b[e];
         }
       }
     }
-    const int64_t row = (int64_t)w.row0 + r;
+  }
+#pragma unroll
+  for (int r = 0; r < JOIN_EACH; ++r) {
+    if (r0 + r >= rows) break;
+    const bool empty = m[r] == -INFINITY && sum[r] == 0.f;  // a query that sees no key
+    const int64_t row = (int64_t)w.row0 + r0 + r;
     __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
-    const float inv = empty ? 0.f : 1.f / sum;
+    const float inv = empty ? 0.f : 1.f / sum[r];
 #pragma unroll
     for (int k = 0; k < EACH; k += 2)
-      if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(o[k] * inv, o[k + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
+      if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(o[r][k] * inv, o[r][k + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m[r] + log2_approx(sum[r]);
   }
 }
 
