@@ -21,8 +21,8 @@ namespace qk {
 
 constexpr int THREADS = 256, BACK_THREADS = 512;
 constexpr int MAX_DIM = 256;
-constexpr int AHEAD = 4;         // heads of a thread in flight
-constexpr int BACK_AHEAD = 2;
+constexpr int AHEAD = 4, BACK_AHEAD = 2;  // rows of a thread in flight
+constexpr int CTAS_PER_SM = 3;            // forward
 constexpr int BACK_CTAS = 152;  // of the backward pass, most: one to an SM, divided between q and k by their heads
 constexpr int64_t MAX_TOKENS = 0x7fffff00;
 
@@ -42,6 +42,7 @@ struct Side {           // q or k
   const float *w, *b;
   float *dw, *db;
   int heads;
+  int per_token, ctas;  // groups of lanes to a token, CTAs
 };
 struct Args {
   Side side[2];
@@ -51,8 +52,7 @@ struct Args {
   float* partials;
   void* ws;
   int dim, pairs, axes, interleaved;
-  int lanes, per_token;  // lanes to a row, groups of lanes to a token
-  int ctas[2];           // backward: of q and of k
+  int lanes;  // to a row
   int sides;
   float eps;
   int want;  // gradients of the parameters
@@ -69,7 +69,7 @@ __device__ __forceinline__ uint2 load8(const __nv_bfloat16* p) {
   return v;
 }
 
-// The eight dimensions of lane `c`: four from d0 on and four from d1 on.
+// The eight dimensions of lane `c` (a lane without any neither loads nor stores, and holds zeros): four from d0 on and four from d1 on.
 struct Place {
   int d0, d1;
   int pair;     // its first pair; pairs >= the rotation's number are not turned
@@ -87,14 +87,12 @@ __device__ __forceinline__ Place place_of(const Args& p, int c) {
 }
 template <bool SPLIT>
 __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, const Place& at) {
-  if (!at.active) return make_uint4(0, 0, 0, 0);
   if (!SPLIT || !at.split) return load16(row + at.d0);
   const uint2 a = load8(row + at.d0), b = load8(row + at.d1);
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 template <bool SPLIT>
 __device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& at, const float2 (&v)[4]) {
-  if (!at.active) return;
   const uint4 o = make_uint4(f2_to_bf16x2(v[0].x, v[0].y), f2_to_bf16x2(v[1].x, v[1].y), f2_to_bf16x2(v[2].x, v[2].y), f2_to_bf16x2(v[3].x, v[3].y));
   if (!SPLIT || !at.split) {
     *reinterpret_cast<uint4*>(row + at.d0) = o;
@@ -194,117 +192,158 @@ __device__ __forceinline__ Angles load_angles(const Args& p, const float2* cs, i
   return Angles{{make_float2(o[0].x, o[1].x), make_float2(o[2].x, o[3].x)}, {make_float2(o[0].y, o[1].y), make_float2(o[2].y, o[3].y)}};
 }
 
+// CTAs are persistent and take every ctas-th block of tokens; a thread's next rows are always on their way, into the next block, and
+// the angles of that block are made during the present one.
 template <int NORM, bool SPLIT, int LANES>
-__global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid_constant__ Args p) {
   pdl_launch_dependents();
-  __shared__ float2 cs[THREADS * 4];
+  __shared__ float2 cs[2][THREADS * 4];
   pdl_wait();
-  const Side& s = p.side[blockIdx.y];
+  const int which = (int)blockIdx.x >= p.side[0].ctas, cta = blockIdx.x - (which ? p.side[0].ctas : 0);
+  const Side& s = p.side[which];
   const int lanes = LANES ? LANES : p.lanes;
-  const int groups = THREADS / lanes, tokens = groups / p.per_token;
-  const int g = threadIdx.x / lanes, t = g / p.per_token, h0 = g - t * p.per_token;
+  const int groups = THREADS / lanes, tokens = groups / s.per_token;
+  const int g = threadIdx.x / lanes, t = g / s.per_token, h0 = g - t * s.per_token;
   const Place at = place_of(p, threadIdx.x & (lanes - 1));
-  const int64_t token0 = (int64_t)blockIdx.x * tokens, token = token0 + t;
-  const int mine = token < p.tokens ? s.heads : 0;  // heads that there are
-  const int64_t x_step = p.per_token * s.x.head, y_step = p.per_token * s.y.head;
+  const int rounds = (s.heads + AHEAD * s.per_token - 1) / (AHEAD * s.per_token);  // of AHEAD rows of a thread
+  const int64_t stride = (int64_t)s.ctas * tokens, first = (int64_t)cta * tokens;
+  const int64_t x_step = s.per_token * s.x.head, y_step = s.per_token * s.y.head;
+  int64_t token = first + t;  // whose rows are asked for
   const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
-  __nv_bfloat16* y = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token + h0 * s.y.head;
-  uint4 raw[AHEAD];
+  int ask_h = h0;
+  bool ask_live = at.active && token < p.tokens;
+  uint4 raw[AHEAD] = {};
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) {
-    if (h0 + j * p.per_token < mine) raw[j] = load_row<SPLIT>(x, at);
-    x += x_step;
-  }
-  fill_angles<THREADS>(p, cs, token0, tokens);
-  __syncthreads();
-  const Angles a = load_angles(p, cs, t, at);
+      if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
+      x += x_step;
+      ask_h += s.per_token;
+    }
+  fill_angles<THREADS>(p, cs[0], first, tokens);
+  const float inv = 1.f / (float)p.dim;
   float2 w[4], b[4];
   if (NORM != DIT_NORM_NONE) load_weights(s.w, at, w, 1.f);
   if (NORM == DIT_NORM_LAYER) load_weights(s.b, at, b, 0.f);
-  const float inv = 1.f / (float)p.dim;
-  // every thread makes every round: the sums' shuffles want whole warps
-  int h = h0;
-  for (int base = 0; base < s.heads; base += AHEAD * p.per_token) {
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      float2 v[4];
-      unpack(raw[j], v);
-      if (h + AHEAD * p.per_token < mine) raw[j] = load_row<SPLIT>(x, at);
-      x += x_step;
-      normalise<NORM, LANES>(v, p, at, inv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (NORM == DIT_NORM_RMS) v[i] = mul2(v[i], w[i]);
-        if (NORM == DIT_NORM_LAYER) v[i] = fma2(v[i], w[i], b[i]);
+  // every thread makes every round: the sums' shuffles want whole warps, the barrier whole CTAs
+  int buf = 0;
+#pragma unroll 1
+  for (int64_t block = first; block < p.tokens; block += stride, buf ^= 1) {
+    __syncthreads();  // this block's angles are there, and those of the block before have been read
+    const Angles a = load_angles(p, cs[buf], t, at);
+    fill_angles<THREADS>(p, cs[buf ^ 1], block + stride, tokens);
+    __nv_bfloat16* y = const_cast<__nv_bfloat16*>(s.y.ptr) + (block + t) * s.y.token + h0 * s.y.head;
+    const int heads = at.active && block + t < p.tokens ? s.heads : 0;
+    int h = h0;
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+      if (round + 1 == rounds) {  // from here on the next block's rows are asked for
+        token += stride;
+        ask_live = at.active && token < p.tokens;
+        ask_h = h0;
+        x = s.x.ptr + token * s.x.token + h0 * s.x.head;
       }
-      turn<SPLIT, false>(v, a, at);
-      if (h < mine) store_row<SPLIT>(y, at, v);
-      y += y_step;
-      h += p.per_token;
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        float2 v[4];
+        unpack(raw[j], v);
+        {
+          if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
+          x += x_step;
+          ask_h += s.per_token;
+        }
+        normalise<NORM, LANES>(v, p, at, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (NORM == DIT_NORM_RMS) v[i] = mul2(v[i], w[i]);
+          if (NORM == DIT_NORM_LAYER) v[i] = fma2(v[i], w[i], b[i]);
+        }
+        turn<SPLIT, false>(v, a, at);
+        if (h < heads) store_row<SPLIT>(y, at, v);
+        y += y_step;
+        h += s.per_token;
+      }
     }
   }
 }
 
-// Tokens are dealt to the CTAs in turn; each thread sums its parameters' gradients over all of its rows, the CTA adds
-// them up over its groups, and the CTA that finishes last over the CTAs, always in the same order.
+// Each thread sums its parameters' gradients over all of its rows, the CTA adds them up over its groups, and the CTA that finishes
+// last over the CTAs, always in the same order.
 template <int NORM, bool SPLIT, int LANES>
 __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid_constant__ Args p) {
   pdl_launch_dependents();
-  __shared__ float2 cs[BACK_THREADS * 4];
-  __shared__ float sums[BACK_THREADS * 8];
+  __shared__ float2 cs[2][BACK_THREADS * 4];
   __shared__ bool last;
+  float* sums = reinterpret_cast<float*>(&cs[0][0]);  // once the angles are done with
   pdl_wait();
-  const int which = (int)blockIdx.x >= p.ctas[0], cta = blockIdx.x - (which ? p.ctas[0] : 0);
+  const int which = (int)blockIdx.x >= p.side[0].ctas, cta = blockIdx.x - (which ? p.side[0].ctas : 0);
   const Side& s = p.side[which];
   const int lanes = LANES ? LANES : p.lanes;
-  const int groups = BACK_THREADS / lanes, tokens = groups / p.per_token;
-  const int g = threadIdx.x / lanes, t = g / p.per_token, h0 = g - t * p.per_token;
+  const int groups = BACK_THREADS / lanes, tokens = groups / s.per_token;
+  const int g = threadIdx.x / lanes, t = g / s.per_token, h0 = g - t * s.per_token;
   const Place at = place_of(p, threadIdx.x & (lanes - 1));
-  const float inv = 1.f / (float)p.dim;
-  float2 w[4], dw[4], db[4];
-  if (NORM != DIT_NORM_NONE) load_weights(s.w, at, w, 1.f);
+  const int rounds = (s.heads + BACK_AHEAD * s.per_token - 1) / (BACK_AHEAD * s.per_token);  // of BACK_AHEAD rows of a thread
+  const int64_t stride = (int64_t)s.ctas * tokens, first = (int64_t)cta * tokens;
+  const int64_t x_step = s.per_token * s.x.head, y_step = s.per_token * s.y.head, d_step = s.per_token * s.dy.head;
+  int64_t token = first + t;  // whose rows are asked for
+  const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
+  const __nv_bfloat16* dy = s.dy.ptr + token * s.dy.token + h0 * s.dy.head;
+  int ask_h = h0;
+  bool ask_live = at.active && token < p.tokens;
+  uint4 rx[BACK_AHEAD] = {}, rd[BACK_AHEAD] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
-  const int64_t blocks = (p.tokens + tokens - 1) / tokens;
-  const int64_t x_step = p.per_token * s.x.head, d_step = p.per_token * s.dy.head, y_step = p.per_token * s.y.head;
-  for (int64_t blk = cta; blk < blocks; blk += p.ctas[which]) {
-    const int64_t token0 = blk * tokens, token = token0 + t;
-    const int mine = token < p.tokens ? s.heads : 0;  // heads that there are
-    const __nv_bfloat16* x = s.x.ptr + token * s.x.token + h0 * s.x.head;
-    const __nv_bfloat16* dy = s.dy.ptr + token * s.dy.token + h0 * s.dy.head;
-    __nv_bfloat16* dx = const_cast<__nv_bfloat16*>(s.y.ptr) + token * s.y.token + h0 * s.y.head;
-    uint4 rx[BACK_AHEAD], rd[BACK_AHEAD];
-#pragma unroll
-    for (int j = 0; j < BACK_AHEAD; ++j) {
-      if (h0 + j * p.per_token < mine) {
+  for (int j = 0; j < BACK_AHEAD; ++j) {
+      if (ask_live && ask_h < s.heads) {
         rd[j] = load_row<SPLIT>(dy, at);
         if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
       }
       x += x_step;
       dy += d_step;
+      ask_h += s.per_token;
     }
-    __syncthreads();  // the angles of the round before have been read
-    fill_angles<BACK_THREADS>(p, cs, token0, tokens);
-    __syncthreads();
-    const Angles a = load_angles(p, cs, t, at);
+  fill_angles<BACK_THREADS>(p, cs[0], first, tokens);
+  const float inv = 1.f / (float)p.dim;
+  float2 w[4], dw[4], db[4];
+  if (NORM != DIT_NORM_NONE) load_weights(s.w, at, w, 1.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
+  // every thread makes every round: the sums' shuffles want whole warps, the barrier whole CTAs
+  int buf = 0;
+#pragma unroll 1
+  for (int64_t block = first; block < p.tokens; block += stride, buf ^= 1) {
+    __syncthreads();  // this block's angles are there, and those of the block before have been read
+    const Angles a = load_angles(p, cs[buf], t, at);
+    fill_angles<BACK_THREADS>(p, cs[buf ^ 1], block + stride, tokens);
+    __nv_bfloat16* y = const_cast<__nv_bfloat16*>(s.y.ptr) + (block + t) * s.y.token + h0 * s.y.head;
+    const int heads = at.active && block + t < p.tokens ? s.heads : 0;
     int h = h0;
-    for (int base = 0; base < s.heads; base += BACK_AHEAD * p.per_token) {
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+      if (round + 1 == rounds) {  // from here on the next block's rows are asked for
+        token += stride;
+        ask_live = at.active && token < p.tokens;
+        ask_h = h0;
+        x = s.x.ptr + token * s.x.token + h0 * s.x.head;
+        dy = s.dy.ptr + token * s.dy.token + h0 * s.dy.head;
+      }
 #pragma unroll
       for (int j = 0; j < BACK_AHEAD; ++j) {
         float2 v[4], d[4];
         unpack(rd[j], d);
         if (NORM != DIT_NORM_NONE) unpack(rx[j], v);
-        if (h + BACK_AHEAD * p.per_token < mine) {
-          rd[j] = load_row<SPLIT>(dy, at);
-          if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
+        {
+          if (ask_live && ask_h < s.heads) {
+            rd[j] = load_row<SPLIT>(dy, at);
+            if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
+          }
+          x += x_step;
+          dy += d_step;
+          ask_h += s.per_token;
         }
-        x += x_step;
-        dy += d_step;
         turn<SPLIT, true>(d, a, at);
         if (NORM != DIT_NORM_NONE) {
           const float r = normalise<NORM, LANES>(v, p, at, inv);
           float2 e[4];
-          if (h < mine) {  // lanes without dimensions add zeros to what is not read
+          if (h < heads) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               dw[i] = fma2(d[i], v[i], dw[i]);
@@ -324,9 +363,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid
             d[i] = mul2(fma2(v[i], both(me), d[i]), both(r));
           }
         }
-        if (h < mine) store_row<SPLIT>(dx, at, d);
-        dx += y_step;
-        h += p.per_token;
+        if (h < heads) store_row<SPLIT>(y, at, d);
+        y += y_step;
+        h += s.per_token;
       }
     }
   }
@@ -359,8 +398,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid
   if (!last) return;
   __threadfence();
   for (int o = threadIdx.x; o < p.sides * outs; o += BACK_THREADS) {
-    const int side = o / outs, e = o - side * outs, many = p.ctas[side];
-    const float* from = p.partials + (int64_t)(side ? p.ctas[0] : 0) * outs + e;
+    const int side = o / outs, e = o - side * outs, many = p.side[side].ctas;
+    const float* from = p.partials + (int64_t)(side ? p.side[0].ctas : 0) * outs + e;
     float v[16] = {};
     for (int c = 0; c < many; c += 16)  // sixteen loads in flight
 #pragma unroll
@@ -427,13 +466,25 @@ static dit_status fill(Args& p, const dit_heads_t* q, const dit_heads_t* k, cons
   p.table = rot ? reinterpret_cast<const Pair*>(rot->table) : nullptr;
   p.positions = positions;
   p.lanes = lanes_of(dim);
-  // About AHEAD heads to a group of lanes: the angles and weights are then read once for four rows.  Batches that
-  // fill less than two CTAs an SM get more groups to a token.
+  // CTAs for q and for k in the proportion of their heads, no more than there are blocks of tokens.  About AHEAD heads go to a group
+  // of lanes: the angles and weights are then read once for four rows.  Batches that leave CTAs without a block get more
+  // groups to a token.
   const int groups = (back ? BACK_THREADS : THREADS) / p.lanes;
-  const int heads = p.sides == 2 && p.side[1].heads > p.side[0].heads ? p.side[1].heads : p.side[0].heads;
-  p.per_token = 1;
-  while (p.per_token < groups && p.per_token * AHEAD < heads) p.per_token *= 2;
-  while (p.per_token < groups && p.per_token < heads && tokens * p.per_token < (int64_t)groups * (back ? 1 : 2) * num_sms()) p.per_token *= 2;
+  const int64_t most = back ? BACK_CTAS : (int64_t)CTAS_PER_SM * num_sms();
+  for (int i = 0; i < p.sides; ++i) {
+    Side& s = p.side[i];
+    int64_t n = most;
+    if (p.sides == 2) {
+      const int64_t q = most * p.side[0].heads / ((int64_t)p.side[0].heads + p.side[1].heads);
+      n = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
+      if (i) n = most - n;
+    }
+    s.per_token = 1;
+    while (s.per_token < groups && s.per_token * AHEAD < s.heads) s.per_token *= 2;
+    while (s.per_token < groups && s.per_token < s.heads && tokens * s.per_token < groups * n) s.per_token *= 2;
+    const int64_t blocks = (tokens * s.per_token + groups - 1) / groups;
+    s.ctas = (int)(blocks < 1 ? 1 : blocks < n ? blocks : n);
+  }
   return DIT_OK;
 }
 
@@ -449,7 +500,8 @@ static cudaError_t launch(const Args& p, dim3 grid, cudaStream_t st) {
   return !p.interleaved && p.pairs ? launch<BACK, NORM, true>(p, grid, st) : launch<BACK, NORM, false>(p, grid, st);
 }
 template <bool BACK>
-static dit_status launch(const Args& p, int norm, const dim3& grid, cudaStream_t st) {
+static dit_status launch(const Args& p, int norm, cudaStream_t st) {
+  const dim3 grid((unsigned)(p.side[0].ctas + (p.sides == 2 ? p.side[1].ctas : 0)));
   const cudaError_t e = norm == DIT_NORM_LAYER ? launch<BACK, DIT_NORM_LAYER>(p, grid, st)
                         : norm == DIT_NORM_RMS ? launch<BACK, DIT_NORM_RMS>(p, grid, st)
                                                : launch<BACK, DIT_NORM_NONE>(p, grid, st);
@@ -492,8 +544,7 @@ extern "C" dit_status dit_qk_norm_rope(const dit_heads_t* q, const dit_heads_t* 
   qk::Args p = {};
   const dit_status e = qk::fill(p, q, k, nullptr, nullptr, q_out, k_out, tokens, dim, norm, params, eps, rot, positions, false);
   if (e != DIT_OK || tokens == 0) return e;
-  const int per_cta = qk::THREADS / p.lanes / p.per_token;
-  return qk::launch<false>(p, norm, dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)p.sides), stream);
+  return qk::launch<false>(p, norm, stream);
 }
 
 extern "C" dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k, const dit_heads_t* dq_out,
@@ -520,17 +571,5 @@ extern "C" dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_
   p.partials = reinterpret_cast<float*>(scratch);
   p.ws = ws;
   if (tokens == 0 && !p.want) return DIT_OK;
-  const int per_cta = qk::BACK_THREADS / p.lanes / p.per_token;
-  const int64_t blocks = (tokens + per_cta - 1) / per_cta;
-  for (int i = 0; i < p.sides; ++i) {
-    int64_t share = qk::BACK_CTAS;
-    if (p.sides == 2) {
-      const int64_t q_share = (int64_t)qk::BACK_CTAS * p.side[0].heads / ((int64_t)p.side[0].heads + p.side[1].heads);
-      share = q_share < 1 ? 1 : q_share > qk::BACK_CTAS - 1 ? qk::BACK_CTAS - 1 : q_share;
-      if (i) share = qk::BACK_CTAS - share;
-    }
-    // without tokens a CTA still writes the parameters' gradients, zeros
-    p.ctas[i] = (int)(blocks < 1 ? 1 : blocks < share ? blocks : share);
-  }
-  return qk::launch<true>(p, norm, dim3((unsigned)(p.ctas[0] + p.ctas[1])), stream);
+  return qk::launch<true>(p, norm, stream);  // without tokens a CTA of each side still writes the parameters' gradients, zeros
 }
