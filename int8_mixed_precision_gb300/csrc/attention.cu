@@ -16,6 +16,7 @@
 //
 // Warps: 0 loads, 1 issues S, 2 and 3 issue O += P V of a block each, 4 to 7 relay the MMAs' completion to the rows' warps, which are
 // 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  Every wait on memory is bounded.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -30,7 +31,7 @@ using namespace lora;
 
 constexpr float GROWTH = 8.f;
 constexpr int FWD_STAGES = 6;  // most
-using Regs = Registers<4, 128, 56, 200>;
+using Regs = Registers<4, 128, 48, 208>;
 
 template <int PD>
 struct Fwd {
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   volatile int* abort = &c->abort;
   const Doc& d = w.doc;
   const int row0 = w.row0;
-  const int n = w.ok ? w.end - w.begin : 0;  // tiles
+  const int n = uniform(w.ok ? w.end - w.begin : 0);  // tiles
   const int blocks = w.ok && row0 + p.rows < d.queries ? 2 : 1;
-  const bool work = n > 0 && (int64_t)w.end * COLS < (int64_t)d.keys + COLS;
+  const bool work = n > 0;
 
   if (warp < Regs::FIRST_ROWS) Regs::give();
   if (warp == 0) {
@@ -251,9 +252,9 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     const bool any = __any_sync(0xffffffffu, live);
     const uint32_t at = tmem + ((uint32_t)(warp % 4) << 21);
     // rows behind the last one: nothing is masked and nothing stored
-    const int64_t hi = live ? seen_end(d, p.plan.frame, row) : INT64_MAX;
+    const int hi = live ? (int)seen_end(d, p.plan.frame, row) : INT_MAX - COLS;
     // tiles up to the first one that some row does not see whole
-    const int whole = __reduce_min_sync(0xffffffffu, (int)(min(hi, (int64_t)INT_MAX - COLS) / COLS)) - w.begin;
+    const int whole = __reduce_min_sync(0xffffffffu, hi / COLS) - w.begin;
     float m = -INFINITY, mc = 0.f, l = 0.f;  // the maximum in use, -m c, and the sum
     if (work && t < blocks) {
       const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree);
         if (j >= whole) {
-          const int upto = cols_before<COLS>(hi, (int64_t)(w.begin + j) * COLS);
+          const int upto = hi - (w.begin + j) * COLS;
 #pragma unroll
           for (int i = 0; i < COLS; ++i)
             if (i >= upto) s[i] = 0xff800000u;  // -infinity
@@ -458,8 +459,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid
 #pragma unroll
   for (int r = 0; r < JOIN_EACH; ++r) {
     if (r0 + r >= rows) break;
-    const bool empty = m[r] == -INFINITY && sum[r] == 0.f;  // a query that sees no key
     const int64_t row = (int64_t)w.row0 + r0 + r;
+    const bool empty = seen_end(w.doc, p.plan.frame, row) == 0;  // a query that sees no key
     __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
     const float inv = empty ? 0.f : 1.f / sum[r];
 #pragma unroll
@@ -522,5 +523,6 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
   a.group = plan->heads / plan->kv_heads;
   a.rows = rows_per_tile(a.group);
   a.stall = test_stall();
+  if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
   return plan->dim <= 64 ? launch<64>(a, hq, hk, hv, stream) : launch<128>(a, hq, hk, hv, stream);
 }

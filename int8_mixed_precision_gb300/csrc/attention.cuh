@@ -79,8 +79,11 @@ struct Work {
   int32_t head;
   bool ok;  // the entry fits the plan
 };
-__device__ __forceinline__ bool fits(const Work& w, const dit_attention_plan_t& p) {
+__device__ __forceinline__ bool fits(const Work& w, const dit_attention_plan_t& p, int list) {
   const Doc& d = w.doc;
+  // the streamed operand's tiles lie in the document
+  const int64_t cols = list == FORWARD ? FORWARD_COLS : BACK_COLS, rows = list == GRAD_KV ? d.queries : d.keys;
+  if (list != JOIN && w.end > w.begin && (int64_t)w.end * cols >= rows + cols) return false;
   return d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 && (int64_t)d.k0 + d.keys <= p.k_rows &&
          d.prefix >= 0 && d.tile0 >= 0 && (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.row0 >= 0 && w.begin >= 0;
 }
@@ -117,7 +120,7 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
     const int4 a = __ldg(it), b = __ldg(it + 1), c = __ldg(it + 2);
     w.doc = Doc{a.x, a.y, a.z, a.w, b.x, b.y};
     w.row0 = b.z, w.begin = b.w, w.end = c.x, w.slot = c.y;
-    w.ok = fits(w, p);
+    w.ok = fits(w, p, list);
   }
   if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
   __syncwarp();
@@ -246,12 +249,6 @@ __device__ __forceinline__ float log2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// How many of a tile's columns lie in front of `end`: 0 to N.
-template <int N>
-__device__ __forceinline__ int cols_before(int64_t end, int64_t first) {
-  const int64_t n = end - first;
-  return n < 0 ? 0 : n > N ? N : (int)n;
 }
 // Zeroes rows [from, rows) of a tile of 64-column chunks in shared memory (a row of a chunk is 128 bytes, whatever the
 // swizzle), by a whole warp: what lies behind a document's end must not meet the zeros of p or ds in a product, which

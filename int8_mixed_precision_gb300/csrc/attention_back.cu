@@ -18,6 +18,7 @@
 //
 // Warps: 0 loads; 1 and 6 issue S and T of a stream each; 2 issues A, 3 B; 4, 5 and 7 relay the MMAs' completion; the others hold
 // the rows and take over most of the first ones' registers.  Every wait on memory is bounded.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   const int row0 = w.row0;
   const int x_rows = KEYS ? d.keys : d.queries, y_rows = KEYS ? d.queries : d.keys;  // of the document
   const int x0 = KEYS ? d.k0 : d.q0, y0 = KEYS ? d.q0 : d.k0;
-  const int tiles = w.ok && w.end > w.begin && (int64_t)w.end * COLS < (int64_t)y_rows + COLS ? w.end - w.begin : 0;
+  const int tiles = w.ok && w.end > w.begin ? w.end - w.begin : 0;
   const int n = tiles * (KEYS ? p.group : 1);
 
   const int w_begin = w.begin;
@@ -289,16 +290,16 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     const bool live = w.ok && row < x_rows;
     const uint32_t at = tmem + ((uint32_t)(warp % 4) << 21);
     // the columns that this row meets; rows behind the last one: whatever they hold is not stored
-    int64_t lo = 0, hi = INT64_MAX;
+    int lo = 0, hi = INT_MAX - COLS;
     if (live && KEYS) {
-      lo = seen_from(d, p.plan.frame, row);
+      lo = (int)min(seen_from(d, p.plan.frame, row), (int64_t)d.queries);
       hi = d.queries;
     } else if (live) {
-      hi = seen_end(d, p.plan.frame, row);
+      hi = (int)seen_end(d, p.plan.frame, row);
     }
     // tiles that every row of the warp meets whole
-    const int whole_from = __reduce_max_sync(0xffffffffu, (int)min((lo + COLS - 1) / COLS, (int64_t)INT_MAX));
-    const int whole_to = __reduce_min_sync(0xffffffffu, (int)min(hi / COLS, (int64_t)INT_MAX));
+    const int whole_from = __reduce_max_sync(0xffffffffu, lo / COLS + (lo % COLS != 0));
+    const int whole_to = __reduce_min_sync(0xffffffffu, hi / COLS);
     float lse = 0.f, delta = 0.f;
     if (!KEYS && live) {
       const int64_t i = (int64_t)w.head * p.plan.padded_rows + (int64_t)d.tile0 * TILE + row;
@@ -347,8 +348,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       }
       const int at_tile = w.begin + tile;
       if (at_tile < whole_from || at_tile >= whole_to) {  // masked pairs: p and ds are zero, whatever was there
-        const int64_t col0 = (int64_t)at_tile * COLS + col;
-        const int from = cols_before<MINE>(lo, col0), to = cols_before<MINE>(hi, col0);
+        const int col0 = at_tile * COLS + col, from = lo - col0, to = hi - col0;
 #pragma unroll
         for (int i = 0; i < MINE; ++i)
           if (i < from || i >= to) s[i] = g[i] = 0u;
@@ -499,5 +499,6 @@ extern "C" dit_status dit_attention_backward(const dit_attention_plan_t* plan, c
   a.scale = (float)scale;
   a.group = h / hk;
   a.stall = test_stall();
+  if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
   return dim <= 64 ? backward<64>(a, in, hdq, hdk, hdv, stream) : backward<128>(a, in, hdq, hdk, hdv, stream);
 }

@@ -240,6 +240,76 @@ def test_streams_share_nothing_but_inputs(dit):
     b.check()
 
 
+@pytest.mark.parametrize("lengths,keys", [([0, 0], [5, 300]), ([0], [0]), ([4, 0], [0, 9])])
+def test_documents_without_queries_or_keys(dit, lengths, keys):
+    b = Batch(dit, lengths, 2, 1, 64, kv_lengths=keys, room=400)
+    b.forward()
+    b.backward()
+    b.check()
+
+
+@pytest.mark.parametrize("n,m", [(200, 200), (1, 9000)])  # whole items, and keys cut into pieces
+def test_scores_of_minus_infinity_and_nan(dit, n, m):
+    """A query whose scores are all -infinity gets NaN, as the formula's; one with some of them does not; NaN in a key reaches the
+    queries that see it."""
+    b = Batch(dit, [n], 1, 1, 64, kv_lengths=[m], room=m, train=False)
+    assert (b.plan.info.slots > 0) == (n == 1)
+    b.q[:n] = 1.0
+    key = b.k[1:1 + m]
+    key[7] = float("-inf")
+    b.forward()
+    assert torch.isfinite(b.out[:n]).all()
+    key.fill_(float("-inf"))
+    b.forward()
+    assert torch.isnan(b.out[:n]).all()
+    key.fill_(0.5)
+    key[m // 3] = float("nan")
+    b.forward()
+    assert torch.isnan(b.out[:n]).all()
+
+
+def test_wrong_table_entries_are_skipped(dit):
+    """Entries that do not fit the plan write nothing and raise the status word."""
+    for field, value in ((0, 10 ** 6), (1, 10 ** 6), (2, 10 ** 6), (3, 10 ** 6), (4, -1), (5, 10 ** 6), (6, -128), (7, -1), (8, 10 ** 6)):
+        b = Batch(dit, [100, 60], 2, 2, 64)
+        b.forward()
+        good = b.out.clone()
+        table = b.plan.table.view(-1)[: 16 * sum(b.plan.info.items)].view(-1, 16)
+        table[:, field] = value
+        b.out[:] = 7.0
+        b.forward()
+        assert (b.out == 7.0).all(), field
+        b.backward()
+        assert (b.dq == 5.0).all() and (b.dk == 5.0).all(), field
+        assert dit.device_status(b.ws) == 1 << 1
+        assert not torch.equal(good, b.out)
+
+
+def test_offsets_past_32_bits(dit):
+    """Keys and values far apart: offsets in elements pass 2^31."""
+    n, stride = 34000, 65536
+    cache = torch.empty(n * stride, dtype=BF16, device="cuda")
+    k, v = (cache.as_strided((n, 1, 64), (stride, 64, 1), at) for at in (0, 64))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(5, 1, 64, device="cuda", generator=g).to(BF16)
+    k.copy_(torch.randn(n, 1, 64, device="cuda", generator=g))
+    v.copy_(torch.randn(n, 1, 64, device="cuda", generator=g))
+    plan = dit.AttentionPlan([2, 3], 1, 64, kv_lengths=[10, 300], kv_begins=[3, n - 300], training=True)
+    ws, scratch, saved, out = dit.workspace(), dit.attention_scratch(plan), dit.attention_saved(plan), torch.empty_like(q)
+    dit.attention(plan, q, k, v, out, scratch, ws, saved=saved)
+    grad = torch.empty_like(cache)
+    dk, dv = (grad.as_strided((n, 1, 64), (stride, 64, 1), at) for at in (0, 64))
+    dq, dout = torch.empty_like(q), torch.randn(5, 1, 64, device="cuda", generator=g).to(BF16)
+    dit.attention_backward(plan, q, k, v, out, dout, saved, dq, dk, dv, scratch, ws)
+    for rows, keys in ((slice(0, 2), slice(3, 13)), (slice(2, 5), slice(n - 300, n))):
+        o, p, bound = R.attention(q[rows, 0].double(), k[keys, 0].double(), v[keys, 0].double(), torch.ones(rows.stop - rows.start, keys.stop - keys.start, dtype=torch.bool, device="cuda"), 0.125)
+        assert ((out[rows, 0].double() - o).abs() <= bound).all()
+        grads = R.attention_grads(q[rows, 0].double(), k[keys, 0].double(), v[keys, 0].double(), p, o, dout[rows, 0].double(), 0.125)
+        for got, (want, lim) in zip((dq[rows, 0], dk[keys, 0], dv[keys, 0]), grads):
+            assert ((got.double() - want).abs() <= lim).all()
+    assert dit.device_status(ws) == 0
+
+
 def test_gradients_match_differences(dit):
     """The gradients against differences of the 64-bit formula, so that both could not share a mistake."""
     b = Batch(dit, [9, 20], 2, 1, 64, frame=3, prefix=4)
