@@ -22,6 +22,7 @@
  *   with.  This rests on every kernel of these calls waiting itself before it lets the next one launch: what
  *   precedes it has then completed and reached global memory.  The first kernel of a call waits before any
  *   access and every kernel before its end, so for other work on the stream the order is that of plain launches.
+ *   In dit_attention_backward the kernel of dk and dv runs beside the one of dq in the same way.
  * - The return code covers argument errors found on the host;
  *   errors found on the device (a bounded wait that ran out) are OR-ed into the status
  *   word at byte 0 of the workspace (see dit_ws_status_offset), which the caller reads

@@ -16,6 +16,10 @@
 // warps work at the present one's.  Where tensor memory holds two of everything, the two warpgroups work at tiles in turn
 // (STREAMS 2), so that one's exponentials hide the other's waits; else they share each tile's columns.
 //
+// Ahead of the stream.  The kernel of dk and dv needs nothing of the one of dq before it and starts on the SMs that one leaves.  That one
+// lets it launch only after its own wait, so that the inputs, lse and delta are then complete and in global memory; and
+// it waits itself before it ends, so for what follows on the stream the order is that of plain launches.
+//
 // Warps: 0 loads; 1 and 6 issue S and T of a stream each; 2 issues A, 3 B; 4, 5 and 7 relay the MMAs' completion; the others hold
 // the rows and take over most of the first ones' registers.  Every wait on memory is bounded.
 #include <float.h>
@@ -69,6 +73,7 @@ struct BackArgs {
   void* ws;
   float c, scale;     // scale log2(e); scale
   int group;
+  int ahead;  // the kernel before is the gradient of the queries
   int stall;
 };
 
@@ -79,7 +84,9 @@ __global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__
   const Work w = find_work(p.table, p.plan, GRAD_Q, p.plan.heads, p.ws);
   if (!w.ok) return;
   const int lane = threadIdx.x % 16, dim = p.plan.dim;
-  for (int r = threadIdx.x / 16; r < TILE; r += 16) {
+#pragma unroll
+  for (int i = 0; i < TILE / 16; ++i) {  // all loads at once
+    const int r = threadIdx.x / 16 + 16 * i;
     const int64_t row = (int64_t)w.row0 + r;
     const bool mine = row < w.doc.queries;
     float sum = 0.f;
@@ -89,13 +96,13 @@ __global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__
       const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.dout.ptr + at * p.dout.row + w.head * p.dout.head + 8 * lane));
       const uint32_t a[4] = {o.x, o.y, o.z, o.w}, b[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = bf16x2_to_f2(a[i]), y = bf16x2_to_f2(b[i]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = bf16x2_to_f2(a[k]), y = bf16x2_to_f2(b[k]);
         sum += x.x * y.x + x.y * y.y;
       }
     }
 #pragma unroll
-    for (int i = 8; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     // the rows that pad a document to whole tiles are written too
     if (lane == 0) p.delta[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = sum;
   }
@@ -105,7 +112,10 @@ template <int PD, bool KEYS>
 __global__ void __launch_bounds__(Regs::THREADS, 1)
     k_attention_back(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
                      const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2, const __grid_constant__ BackArgs p) {
-  pdl_launch_dependents();
+  if (!KEYS) {  // before the next kernel starts, everything that it reads is there
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   using F = Back<PD, KEYS>;
   constexpr int COLS = F::COLS, STREAMS = F::STREAMS, MINE = F::MINE;
   extern __shared__ uint8_t raw[];
@@ -137,7 +147,10 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     tmem_alloc(smem_u32(&c->tmem), 512);
     fence_before();
   }
-  pdl_wait();
+  if (KEYS) {
+    if (!p.ahead) pdl_wait();
+    pdl_launch_dependents();
+  }
   const Work w = find_work(p.table, p.plan, KEYS ? GRAD_KV : GRAD_Q, KEYS ? p.plan.kv_heads : p.plan.heads, p.ws);
   __syncthreads();
   fence_after();
@@ -411,6 +424,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       }
     }
   }
+  if (KEYS) pdl_wait();  // whoever follows finds the gradient of the queries complete too
   fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -456,6 +470,7 @@ static dit_status backward(BackArgs a, const Inputs& in, const Heads& dq, const 
   if (e != DIT_OK) return e;
   a.a = dk;
   a.b = dv;
+  a.ahead = a.plan.items[GRAD_Q] > 0;
   return launch<PD, true>(a, in, st);
 }
 

@@ -310,6 +310,34 @@ def test_offsets_past_32_bits(dit):
     assert dit.device_status(ws) == 0
 
 
+def test_calls_back_to_back(dit):
+    """Calls that follow one another without a pause, each on what a kernel just before has written, give the bits of an idle device:
+    the kernel of dk and dv starts ahead of its predecessor's end."""
+    b = Batch(dit, [900, 31, 500], 8, 4, 64, frame=70, prefix=9)
+    n, start = 1431, [t.clone() for t in (b.q, b.k, b.dout)]
+
+    def run(wait):
+        for t, v in zip((b.q, b.k, b.dout), start):
+            t.copy_(v)
+        got = []
+        for i in range(6):
+            for t in (b.q, b.k, b.dout):
+                t[:n].mul_(-0.75)
+            if wait:
+                torch.cuda.synchronize()
+            b.forward()
+            if wait:
+                torch.cuda.synchronize()
+            b.backward()
+            if wait:
+                torch.cuda.synchronize()
+            got += [t[:n].clone() for t in (b.out, b.dq, b.dk, b.dv)]
+        return got
+    apart = run(True)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(apart, run(False)))
+
+
 def test_gradients_match_differences(dit):
     """The gradients against differences of the 64-bit formula, so that both could not share a mistake."""
     b = Batch(dit, [9, 20], 2, 1, 64, frame=3, prefix=4)
