@@ -627,7 +627,7 @@ dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k,
  *           stream may share it.
  * ------------------------------------------------------------------------------------ */
 #define DIT_ATTENTION_LISTS 4
-#define DIT_ATTENTION_BUCKETS 32
+#define DIT_ATTENTION_BUCKETS 16
 typedef struct {
   int64_t q_rows;        /* query tokens */
   int64_t k_rows;        /* 1 + the last key row that a document has */
@@ -641,7 +641,8 @@ typedef struct {
   int32_t training;
   int32_t slots;         /* partial results of a head */
   int32_t items[DIT_ATTENTION_LISTS]; /* forward, joins, gradient of queries, gradients of keys */
-  int32_t buckets[DIT_ATTENTION_LISTS]; /* runs of items of like cost, in the table */
+  int32_t buckets[DIT_ATTENTION_LISTS]; /* runs of items of like cost: their first items and numbers of items */
+  int32_t bucket[DIT_ATTENTION_LISTS][2 * DIT_ATTENTION_BUCKETS];
   int32_t reserved;
 } dit_attention_plan_t;
 

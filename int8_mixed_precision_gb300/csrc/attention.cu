@@ -352,23 +352,30 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       const bool part = w.slot >= 0;
       const bool room = !part || (int64_t)w.slot + row - row0 < p.plan.slots;
       float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.slot + row - row0) * PARTIAL<PD> : nullptr;
+      const uint32_t stage = smem + t * F::Q_BYTES + (warp % 4) * 4096;  // the queries are done with
 #pragma unroll
-      for (int k = 0; k < PD; k += 32) {
-        uint32_t o[32];
+      for (int k = 0; k < PD; k += 64) {
+        uint32_t o[64];
         __syncwarp();
         tmem_ld32(at + F::O + t * PD + k, o);
+        tmem_ld32(at + F::O + t * PD + k + 32, o + 32);
         tmem_wait();
         pin(o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 64; ++i)
           if (empty) o[i] = 0u;
-        if (live && part && room) {
+        uint4 v[8];
+        if (part) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) *reinterpret_cast<uint2*>(mine + k + i) = make_uint2(o[i], o[i + 1]);
-        } else if (live && !part) {
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            if (k + i < p.plan.dim) *reinterpret_cast<uint4*>(out + k + i) = pack8(o + i, empty ? 0.f : inv);
+            for (int i = 0; i < 8; ++i) v[i] = make_uint4(o[32 * h + 4 * i], o[32 * h + 4 * i + 1], o[32 * h + 4 * i + 2], o[32 * h + 4 * i + 3]);
+            store_rows<8>(stage, v, mine + k + 32 * h, live && room, 8);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = pack8(o + 8 * i, empty ? 0.f : inv);
+          store_rows<8>(stage, v, out + k, live, (p.plan.dim - k + 7) / 8);
         }
       }
       const float mc = m == -INFINITY ? -INFINITY : m * p.c;
@@ -499,7 +506,7 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
                                     const dit_heads_t* v, const dit_heads_t* out, double scale, void* saved, size_t saved_bytes,
                                     void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes, dit_stream_t stream) {
   using namespace attn;
-  if (!plan_ok(plan) || !table || !ws || ws_bytes < WS_BYTES || !(scale > 0.0) || !isfinite(scale)) return DIT_ERR_INVALID_ARG;
+  if (!plan_ok(plan) || (!table && plan->table_ints > 0) || !ws || ws_bytes < WS_BYTES || !(scale > 0.0) || !isfinite(scale)) return DIT_ERR_INVALID_ARG;
   if (saved && !plan->training) return DIT_ERR_INVALID_ARG;
   if (saved && saved_bytes < (size_t)plan->saved_bytes) return DIT_ERR_INVALID_ARG;
   if (scratch_bytes < (size_t)plan->scratch_bytes || (plan->scratch_bytes && !scratch)) return DIT_ERR_INVALID_ARG;

@@ -22,8 +22,8 @@ __host__ __device__ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : 
 __host__ __device__ constexpr int partial_floats(int padded) { return padded + 4; }
 constexpr int FORWARD_COLS = 128, BACK_COLS = 64;
 
-// The table, in int32: the items of the four lists behind one another, and DIT_ATTENTION_BUCKETS pairs (first item,
-// items) for each list.  An item has its document with it, so that one load brings all that a CTA asks of the plan.
+// The table, in int32: the items of the four lists behind one another.  An item has its document with it, so that one load brings all
+// that a CTA asks of the plan.
 struct Doc {
   int32_t q0, queries, k0, keys, prefix;
   int32_t tile0;  // its first padded row / 128
@@ -42,10 +42,6 @@ __host__ __device__ inline int64_t first_item(const dit_attention_plan_t& p, int
   for (int i = 0; i < list; ++i) n += p.items[i];
   return ITEM_INTS * n;
 }
-__host__ __device__ inline int64_t first_bucket(const dit_attention_plan_t& p, int list) {
-  return first_item(p, DIT_ATTENTION_LISTS) + (int64_t)list * 2 * DIT_ATTENTION_BUCKETS;
-}
-
 // The keys [0, end) that query `row` of a document sees, and the first query that sees key `key` (monotone both).
 __host__ __device__ inline int64_t seen_end(const Doc& d, int64_t frame, int64_t row) {
   if (frame == 0) return d.keys;
@@ -87,35 +83,20 @@ __device__ __forceinline__ bool fits(const Work& w, const dit_attention_plan_t& 
   return d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 && (int64_t)d.k0 + d.keys <= p.k_rows &&
          d.prefix >= 0 && d.tile0 >= 0 && (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.row0 >= 0 && w.begin >= 0;
 }
-// The item and head of index `at`, by a whole warp, each of whose lanes holds a bucket (first item, items; none: 0 items).
-struct Buckets {
-  int first, many;
-  __device__ __forceinline__ Buckets(const int32_t* table, const dit_attention_plan_t& p, int list) : first(0x7fffffff), many(0) {
-    const int lane = threadIdx.x % 32;
-    if (lane < p.buckets[list]) {
-      const int2 v = __ldg(reinterpret_cast<const int2*>(table + first_bucket(p, list)) + lane);
-      first = v.x;
-      many = v.y;
-    }
-  }
-  // the item's index, -1: none
-  __device__ __forceinline__ int find(int64_t at, int heads, int items, int* head) const {
-    const uint32_t below = __ballot_sync(0xffffffffu, (int64_t)first * heads <= at);
-    if (!below) return -1;
-    const int b = 31 - __clz(below), f = __shfl_sync(0xffffffffu, first, b), m = __shfl_sync(0xffffffffu, many, b);
-    const int64_t r = at - (int64_t)f * heads;
-    if (m <= 0 || f < 0 || r < 0 || r >= (int64_t)m * heads) return -1;
-    *head = (int)(r / m);
-    const int i = f + (int)(r % m);
-    return i < items ? i : -1;
-  }
-};
 // The work of this CTA.
 __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attention_plan_t& p, int list, int heads, void* ws) {
   Work w = {};
-  const Buckets buckets(table, p, list);
-  const int i = buckets.find(blockIdx.x, heads, p.items[list], &w.head);
-  if (i >= 0) {
+  const int64_t at = blockIdx.x;
+  int i = -1;
+  for (int b = 0; b < p.buckets[list]; ++b) {  // a few, out of the kernel's arguments
+    const int first = p.bucket[list][2 * b], many = p.bucket[list][2 * b + 1];
+    const int64_t r = at - (int64_t)first * heads;
+    if (first >= 0 && many > 0 && r >= 0 && r < (int64_t)many * heads) {
+      w.head = (int)((uint32_t)r / (uint32_t)many);
+      i = first + (int)((uint32_t)r % (uint32_t)many);
+    }
+  }
+  if (i >= 0 && i < p.items[list]) {
     const int4* it = reinterpret_cast<const int4*>(table + first_item(p, list)) + (ITEM_INTS / 4) * (int64_t)i;
     const int4 a = __ldg(it), b = __ldg(it + 1), c = __ldg(it + 2);
     w.doc = Doc{a.x, a.y, a.z, a.w, b.x, b.y};
@@ -258,6 +239,25 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int chunk_bytes, int ch
     for (int i = from * 128 + (threadIdx.x & 31) * 16; i < rows * 128; i += 512)
       lora::sts128(tile + c * chunk_bytes + i, make_uint4(0, 0, 0, 0));
   fence_proxy_async();
+  __syncwarp();
+}
+// Rows of CH x 16 bytes, a row to each lane, to `dst` of each lane (if it is live; `chunks` of a row are stored).  By way of the warp's own
+// 512 CH bytes of shared memory, so that a store instruction writes whole lines: straight from the lanes each
+// instruction touched 32 lines, 1900 cycles for two blocks of 128 x 64 bf16.
+template <int CH>
+__device__ __forceinline__ void store_rows(uint32_t smem, const uint4 (&v)[CH], void* dst, bool live, int chunks) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) lora::sts128(smem + lane * CH * 16 + ((c ^ (lane & (CH - 1))) << 4), v[c]);
+  __syncwarp();
+  const uint64_t at = live ? reinterpret_cast<uint64_t>(dst) : 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int row = i * (32 / CH) + lane / CH, c = lane % CH;
+    const uint4 x = lora::lds128(smem + row * CH * 16 + ((c ^ (row & (CH - 1))) << 4));
+    const uint64_t to = __shfl_sync(0xffffffffu, at, row);
+    if (to && c < chunks) reinterpret_cast<uint4*>(to)[c] = x;
+  }
   __syncwarp();
 }
 // Eight columns of fp32 as bf16, 16 bytes.

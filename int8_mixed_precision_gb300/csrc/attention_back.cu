@@ -399,32 +399,28 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       fence_after();
     }
     const bool ok = !__any_sync(0xffffffffu, *abort);
-    if (ok) {
+    if (ok) {  // one warpgroup to each of dk and dv, or to each half of dq's columns
+      const Heads& to = KEYS && half ? p.b : p.a;
+      const float f = KEYS && half ? 1.f : p.scale;
+      constexpr int WIDTH = KEYS ? PD : PD / 2, CH = WIDTH < 64 ? 4 : 8;  // columns of a warp, and chunks of eight at a time
+      const int first = KEYS ? 0 : half * WIDTH;
+      const uint32_t stage = smem + (warp - Regs::FIRST_ROWS) * 4096;  // what stayed is done with
+      __nv_bfloat16* dst = to.ptr + (int64_t)(x0 + row) * to.row + w.head * to.head + first;
 #pragma unroll
-      for (int out = 0; out < (KEYS ? 2 : 1); ++out) {
-        const Heads& to = out ? p.b : p.a;
-        const float f = out ? 1.f : p.scale;
+      for (int k = 0; k < WIDTH; k += 8 * CH) {
+        uint32_t o[8 * CH];
+        __syncwarp();
 #pragma unroll
-        for (int k = half * (PD / 2); k < (half + 1) * (PD / 2); k += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32(at + (out ? F::B : F::A) + k, o);
-          tmem_wait();
-          pin(o);
-          if (n == 0)
+        for (int i = 0; i < 8 * CH; i += 32) tmem_ld32(at + (KEYS && half ? F::B : F::A) + first + k + i, o + i);
+        tmem_wait();
+        pin(o);
+        uint4 v[CH];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
-          if (live) {
-            __nv_bfloat16* dst = to.ptr + (int64_t)(x0 + row) * to.row + w.head * to.head + k;
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              if (k + i < p.plan.dim) *reinterpret_cast<uint4*>(dst + i) = pack8(o + i, f);
-          }
-        }
+        for (int i = 0; i < CH; ++i) v[i] = n == 0 ? make_uint4(0, 0, 0, 0) : pack8(o + 8 * i, f);
+        store_rows<CH>(stage, v, dst + k, live, (p.plan.dim - first - k + 7) / 8);
       }
     }
   }
-  if (KEYS) pdl_wait();  // whoever follows finds the gradient of the queries complete too
   fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -486,7 +482,7 @@ extern "C" dit_status dit_attention_backward(const dit_attention_plan_t* plan, c
                                              void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes,
                                              dit_stream_t stream) {
   using namespace attn;
-  if (!plan_ok(plan) || !table || !ws || ws_bytes < WS_BYTES || !(scale > 0.0) || !isfinite(scale) || !plan->training) return DIT_ERR_INVALID_ARG;
+  if (!plan_ok(plan) || (!table && plan->table_ints > 0) || !ws || ws_bytes < WS_BYTES || !(scale > 0.0) || !isfinite(scale) || !plan->training) return DIT_ERR_INVALID_ARG;
   if (saved_bytes < (size_t)plan->saved_bytes || (plan->saved_bytes && !saved)) return DIT_ERR_INVALID_ARG;
   if (scratch_bytes < (size_t)plan->scratch_bytes || (plan->scratch_bytes && !scratch)) return DIT_ERR_INVALID_ARG;
   BackArgs a = {};

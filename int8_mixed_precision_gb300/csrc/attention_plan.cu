@@ -184,8 +184,12 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     }
     plan->items[l] = (int32_t)list.size();
     plan->buckets[l] = (int32_t)buckets[l].size();
+    for (size_t b = 0; b < buckets[l].size(); ++b) {
+      plan->bucket[l][2 * b] = buckets[l][b].first;
+      plan->bucket[l][2 * b + 1] = buckets[l][b].second;
+    }
   }
-  plan->table_ints = first_bucket(*plan, DIT_ATTENTION_LISTS);
+  plan->table_ints = first_item(*plan, DIT_ATTENTION_LISTS);
   plan->saved_bytes = training ? (int64_t)heads * plan->padded_rows * 4 : 0;
   const int64_t joins = (int64_t)heads * plan->slots * partial_floats(pd) * 4, deltas = plan->saved_bytes;
   plan->scratch_bytes = std::max(joins, deltas);
@@ -197,11 +201,6 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     for (const Costed& c : lists[l]) {
       std::copy_n(reinterpret_cast<const int32_t*>(&c.item), ITEM_INTS, o);
       o += ITEM_INTS;
-    }
-    o = table + first_bucket(*plan, l);
-    for (const auto& b : buckets[l]) {
-      *o++ = b.first;
-      *o++ = b.second;
     }
   }
   return DIT_OK;
@@ -215,7 +214,7 @@ bool plan_ok(const dit_attention_plan_t* p) {
   for (int l = 0; l < DIT_ATTENTION_LISTS; ++l)
     if (p->items[l] < 0 || (int64_t)p->items[l] * p->heads > MAX_ROWS || p->buckets[l] < 0 || p->buckets[l] > DIT_ATTENTION_BUCKETS || (p->items[l] && !p->buckets[l])) return false;
   const int64_t saved = p->training ? (int64_t)p->heads * p->padded_rows * 4 : 0;
-  return p->table_ints == first_bucket(*p, DIT_ATTENTION_LISTS) && p->saved_bytes == saved &&
+  return p->table_ints == first_item(*p, DIT_ATTENTION_LISTS) && p->saved_bytes == saved &&
          p->scratch_bytes == std::max(saved, (int64_t)p->heads * p->slots * partial_floats(padded_dim(p->dim)) * 4);
 }
 

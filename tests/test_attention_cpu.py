@@ -70,11 +70,8 @@ def lists(plan):
     for n in i.items:
         out.append([t[at + 16 * k:at + 16 * k + 10] for k in range(n)])
         at += 16 * n
-    buckets = []
-    for n in i.buckets:
-        buckets.append([t[at + 2 * k:at + 2 * k + 2] for k in range(n)])
-        at += 64
     assert at == i.table_ints
+    buckets = [[list(i.bucket[k][2 * b:2 * b + 2]) for b in range(n)] for k, n in enumerate(i.buckets)]
     return out, buckets
 
 
