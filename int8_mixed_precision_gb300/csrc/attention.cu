@@ -14,6 +14,9 @@
 // P is rounded to bf16 (an operand of the bf16 tensor pipe), 2^-8 of each weight at most; the sum of the weights is of the unrounded
 // ones.  Scores are scaled inside the exponent's multiply-add, in base 2.
 //
+// Few rows.  Where the keys of an item are cut into pieces and it has one block of rows alone, the CTA's halves take its tiles
+// in turn, two blocks of the same rows: a tile's chain of waits is then half as long for two.
+//
 // Warps: 0 loads, 1 issues S, 2 and 3 issue O += P V of a block each, 4 to 7 relay the MMAs' completion to the rows' warps, which are
 // 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  Every wait on memory is bounded.
 #include <float.h>
@@ -120,7 +123,11 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   const Doc& d = w.doc;
   const int row0 = w.row0;
   const int n = uniform(w.ok ? w.end - w.begin : 0);  // tiles
-  const int blocks = w.ok && row0 + p.rows < d.queries ? 2 : 1;
+  // Two blocks of rows, one, or one whose tiles both halves of the CTA take in turn, as two blocks of the same rows.
+  const bool turns = w.ok && w.turns && w.slot >= 0;
+  const int blocks = w.ok && (turns || row0 + p.rows < d.queries) ? 2 : 1, step = turns ? 2 : 1;
+  auto first_of = [&](int t) { return turns ? t : 0; };
+  auto tiles_of = [&](int t) { return t < blocks ? (n - first_of(t) + step - 1) / step : 0; };
   const bool work = n > 0;
 
   if (warp < Regs::FIRST_ROWS) Regs::give();
@@ -130,8 +137,9 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       int s = 0, parity = 1, issued = 0;  // of K; V has as many or one less
       bool ok = true;
       if (!p.stall) {
-        mbar_expect_tx(smem_u32(&c->qfull), blocks * F::CHUNKS * p.rows * p.group * 128);
-        for (int t = 0; t < blocks; ++t)
+        const int loads = turns ? 1 : blocks;
+        mbar_expect_tx(smem_u32(&c->qfull), loads * F::CHUNKS * p.rows * p.group * 128);
+        for (int t = 0; t < loads; ++t)
 #pragma unroll
           for (int k = 0; k < F::CHUNKS; ++k)
             tma_load_3d(smem + t * F::Q_BYTES + k * F::Q_CHUNK, &mq, smem_u32(&c->qfull), k * 64, w.head * p.group, d.q0 + row0 + t * p.rows);
@@ -179,16 +187,17 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       int s = 0, parity = 0;
       for (int j = 0; j < n && ok; ++j) {
         ok = warp_wait(smem_u32(&c->kfull[s]), parity, p.ws, abort);
-        for (int t = 0; t < blocks && ok; ++t) {
-          if (j > 0) ok = warp_wait(smem_u32(F::OVER_S ? &c->pdone[t] : &c->sfree[t]), (j - 1) & 1, p.ws, abort);
+        for (int t = turns ? j & 1 : 0; t < (turns ? (j & 1) + 1 : blocks) && ok; ++t) {
+          const int i = turns ? j >> 1 : j;
+          if (i > 0) ok = warp_wait(smem_u32(F::OVER_S ? &c->pdone[t] : &c->sfree[t]), (i - 1) & 1, p.ws, abort);
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            const uint32_t a = desc_k(smem + t * F::Q_BYTES), b = desc_k(ring + s * F::KV_BYTES), to = tmem + F::S + t * COLS;
+            const uint32_t a = desc_k(smem + (turns ? 0 : t * F::Q_BYTES)), b = desc_k(ring + s * F::KV_BYTES), to = tmem + F::S + t * COLS;
 #pragma unroll
             for (int k = 0; k < PD / 16; ++k) mma(to, a + (k / 4) * (F::Q_CHUNK >> 4) + (k % 4) * 2, b + (k / 4) * (F::KV_CHUNK >> 4) + (k % 4) * 2, id, k > 0);
             mma_commit(smem_u32(&c->sfull[t]));
-            if (t == blocks - 1) mma_commit(smem_u32(&c->kempty[s]));
+            if (turns || t == blocks - 1) mma_commit(smem_u32(&c->kempty[s]));
           }
           __syncwarp();
         }
@@ -203,15 +212,16 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       const uint32_t id = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
       const uint32_t a = tmem + F::P + t * F::P_STEP, to = tmem + F::O + t * PD;
       bool ok = true;
-      int s = 0, parity = 0;
-      int left = d.keys - w.begin * COLS;  // keys from this tile's first on
-      for (int j = 0; j < n && ok; ++j, left -= COLS) {
+      int s = first_of(t), parity = 0;
+      int left = d.keys - (w.begin + s) * COLS;  // keys from this tile's first on
+      const int many = tiles_of(t);
+      for (int j = 0; j < many && ok; ++j, left -= step * COLS) {
         const uint32_t v = smem + 2 * F::Q_BYTES + (F::STAGES + s) * F::KV_BYTES;
         ok = warp_wait(smem_u32(&c->vfull[s]), parity, p.ws, abort);
-        if (ok && left < COLS) {  // the last tile, for both blocks
-          if (t == 0) {
+        if (ok && left < COLS) {  // the document's last tile, for both blocks
+          if (t == 0 || turns) {
             zero_rows(v, F::KV_CHUNK, F::CHUNKS, left, COLS);
-            if (lane == 0) mbar_arrive(smem_u32(&c->tail));
+            if (!turns && lane == 0) mbar_arrive(smem_u32(&c->tail));
             __syncwarp();
           } else {
             ok = warp_wait(smem_u32(&c->tail), 0, p.ws, abort);
@@ -226,10 +236,11 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
           for (int k = 0; k < COLS / 16; ++k) mma_ta(to, a + k * 8, b + k * (2048 >> 4), id, j > 0 || k > 0);
           mma_commit(smem_u32(&c->pdone[t]));
           mma_commit(smem_u32(&c->vempty[s]));
-          if (blocks == 1) mma_commit(smem_u32(&c->vempty[s]));
+          if (blocks == 1 || turns) mma_commit(smem_u32(&c->vempty[s]));
         }
         __syncwarp();
-        if (++s == F::STAGES) s = 0, parity ^= 1;
+        s += step;
+        if (s >= F::STAGES) s -= F::STAGES, parity ^= 1;
       }
     }
     if (work) {
@@ -242,24 +253,25 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     }
   } else if (warp < Regs::FIRST_ROWS) {
     const int t = warp % 2, what = (warp - 4) / 2;
-    if (work && t < blocks) relay<160>(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, n, p.ws, abort);
+    if (work) relay<160>(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, tiles_of(t), p.ws, abort);
   } else {
     Regs::take();
     const int t = (warp - Regs::FIRST_ROWS) / 4;
     const int r = (warp % 4) * 32 + lane;  // this thread's row: a lane of tensor memory
-    const int row = row0 + t * p.rows + r / p.group, head = w.head * p.group + r % p.group;
+    const int row = row0 + (turns ? 0 : t * p.rows) + r / p.group, head = w.head * p.group + r % p.group;
     const bool live = w.ok && t < blocks && r < p.rows * p.group && row < d.queries;
     const bool any = __any_sync(0xffffffffu, live);
     const uint32_t at = tmem + ((uint32_t)(warp % 4) << 21);
     // rows behind the last one: nothing is masked and nothing stored
     const int hi = live ? (int)seen_end(d, p.plan.frame, row) : INT_MAX - COLS;
     // tiles up to the first one that some row does not see whole
-    const int whole = __reduce_min_sync(0xffffffffu, hi / COLS) - w.begin;
+    const int whole = __reduce_min_sync(0xffffffffu, hi / COLS);
+    const int many = uniform(work ? tiles_of(t) : 0);
     float m = -INFINITY, mc = 0.f, l = 0.f;  // the maximum in use, -m c, and the sum
-    if (work && t < blocks) {
+    if (many > 0) {
       const uint32_t s_at = at + F::S + t * COLS, p_at = at + F::P + t * F::P_STEP, o_at = at + F::O + t * PD;
       const uint32_t sfree = smem_u32(&c->sfree[t]), pready = smem_u32(&c->pready[t]);
-      for (int j = 0; j < n && !any; ++j) {  // rows behind the last one alone: nothing to do but to keep step
+      for (int j = 0; j < many && !any; ++j) {  // rows behind the last one alone: nothing to do but to keep step
         __syncwarp();
         meet<160>(1 + t);
         if (lane == 0) mbar_arrive(sfree);
@@ -267,7 +279,8 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         if (j > 0) meet<160>(3 + t);
         if (lane == 0) mbar_arrive(pready);
       }
-      for (int j = 0; j < n && any; ++j) {
+      int tile = w.begin + first_of(t);
+      for (int j = 0; j < many && any; ++j, tile += step) {
         __syncwarp();
         meet<160>(1 + t);
         fence_after();
@@ -281,8 +294,8 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree);
-        if (j >= whole) {
-          const int upto = hi - (w.begin + j) * COLS;
+        if (tile >= whole) {
+          const int upto = hi - tile * COLS;
 #pragma unroll
           for (int i = 0; i < COLS; ++i)
             if (i >= upto) s[i] = 0xff800000u;  // -infinity
@@ -343,15 +356,18 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       meet<160>(3 + t);
       fence_after();
     }
-    const bool ok = !__any_sync(0xffffffffu, *abort);
+    bool ok = !__any_sync(0xffffffffu, *abort);
+    // the other half's products read the same queries, whose place the results pass through
+    if (turns && work) ok = warp_wait(smem_u32(&c->done), 0, p.ws, abort) && ok;
     if (ok && any) {  // a warp's loads of tensor memory are whole; what is not live is not stored
-      const bool empty = !live || hi == 0 || !work;
+      const bool empty = !live || hi == 0 || many == 0;
       const float inv = 1.f / l;
       const int64_t at_row = (int64_t)d.q0 + row;
       __nv_bfloat16* out = p.out.ptr + at_row * p.out.row + head * p.out.head;
       const bool part = w.slot >= 0;
-      const bool room = !part || (int64_t)w.slot + row - row0 < p.plan.slots;
-      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + w.slot + row - row0) * PARTIAL<PD> : nullptr;
+      const int64_t slot = (int64_t)w.slot + row - row0 + (turns && t ? min(p.rows, d.queries - row0) : 0);
+      const bool room = !part || slot < p.plan.slots;
+      float* mine = part ? p.partial + ((int64_t)head * p.plan.slots + slot) * PARTIAL<PD> : nullptr;
       const uint32_t stage = smem + t * F::Q_BYTES + (warp % 4) * 4096;  // the queries are done with
 #pragma unroll
       for (int k = 0; k < PD; k += 64) {
@@ -391,90 +407,130 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   }
 }
 
-// The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order, a warp to two rows of
-// a head.  Bound by latency: a lane holds the maximum and the sum of every 32nd piece, and those and the first pieces' values are
-// asked for at once.
-constexpr int JOIN_WARPS = 8, JOIN_EACH = 2, JOIN_ROWS = JOIN_WARPS * JOIN_EACH;  // rows of a warp and of a CTA
+// The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order.  Bound by latency: a lane
+// holds the maximum and the sum of every 32nd piece, and those and the first pieces' values are asked for at once.  Two rows
+// of a head to a warp, or, where an item has few rows, several warps to a row, each with a share of its pieces.
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2 * JOIN_WARPS;  // of a CTA
 template <int PD>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid_constant__ FwdArgs p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
-  if (!w.ok) return;
-  const int rows = w.slot, pieces = w.end, lane = threadIdx.x % 32;
-  if (rows <= 0 || (int64_t)w.row0 + rows > w.doc.queries || (int64_t)w.begin + (int64_t)rows * pieces > p.plan.slots) {
-    if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
-    return;
-  }
-  constexpr int EACH = PD / 32, AHEAD = 4;
-  using Vec = typename std::conditional<EACH == 2, float2, float4>::type;
-  const int r0 = blockIdx.y * JOIN_ROWS + threadIdx.x / 32 * JOIN_EACH;
-  const int64_t step = (int64_t)rows * PARTIAL<PD>;
-  const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r0) * PARTIAL<PD>;
-  auto stat = [&](int r, int i) {  // maximum and sum of piece i; none: no key seen
-    return r0 + r < rows && i < pieces ? __ldcg(reinterpret_cast<const float2*>(from + r * PARTIAL<PD> + i * step + PD)) : make_float2(-INFINITY, 0.f);
-  };
-  auto value = [&](int r, int i) {
-    return r0 + r < rows && i < pieces ? __ldcg(reinterpret_cast<const Vec*>(from + r * PARTIAL<PD> + i * step) + lane) : Vec{};
-  };
-  float2 ml[JOIN_EACH];
-  Vec v[JOIN_EACH][AHEAD];
-  float m[JOIN_EACH], sum[JOIN_EACH], o[JOIN_EACH][EACH];
+using JoinVec = typename std::conditional<PD == 64, float2, float4>::type;  // a lane's dimensions
+
+// Rows r0 to r0 + EACH - 1, pieces [begin, end): their part of o and of the sum, under the row's maximum over all pieces.
+template <int PD, int EACH, int AHEAD>
+struct Joined {
+  float m[EACH], sum[EACH], o[EACH][PD / 32];
+  __device__ __forceinline__ Joined(const FwdArgs& p, const Work& w, int r0, int begin, int end) {
+    const int rows = w.slot, pieces = w.end, lane = threadIdx.x % 32;
+    const int64_t step = (int64_t)rows * PARTIAL<PD>;
+    const float* from = p.partial + ((int64_t)w.head * p.plan.slots + w.begin + r0) * PARTIAL<PD>;
+    auto stat = [&](int r, int i) {  // maximum and sum of piece i; none: no key seen
+      return r0 + r < rows && i < pieces ? __ldcg(reinterpret_cast<const float2*>(from + r * PARTIAL<PD> + i * step + PD)) : make_float2(-INFINITY, 0.f);
+    };
+    auto value = [&](int r, int i) {
+      return r0 + r < rows && i < end ? __ldcg(reinterpret_cast<const JoinVec<PD>*>(from + r * PARTIAL<PD> + i * step) + lane) : JoinVec<PD>{};
+    };
+    JoinVec<PD> v[EACH][AHEAD];
 #pragma unroll
-  for (int r = 0; r < JOIN_EACH; ++r) {
-    ml[r] = stat(r, lane);
+    for (int r = 0; r < EACH; ++r) {
+      m[r] = stat(r, lane).x;
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, k);
-  }
-#pragma unroll
-  for (int r = 0; r < JOIN_EACH; ++r) {
-    m[r] = ml[r].x;
-    for (int i = lane + 32; i < pieces; i += 32) m[r] = fmaxf(m[r], stat(r, i).x);
-    m[r] = warp_max_f(m[r]);
-    sum[r] = 0.f;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) o[r][e] = 0.f;
-  }
-  for (int first = 0; first < pieces; first += 32) {
-    float f[JOIN_EACH], l[JOIN_EACH];
-#pragma unroll
-    for (int r = 0; r < JOIN_EACH; ++r) {
-      if (first) ml[r] = stat(r, first + lane);
-      f[r] = ml[r].x == -INFINITY ? 0.f : exp2_approx(ml[r].x - m[r]);
-      l[r] = ml[r].x == -INFINITY ? ml[r].y : f[r] * ml[r].y;
-      if (ml[r].x == -INFINITY && ml[r].y == 0.f) f[r] = -1.f;  // it has seen no key of this row
+      for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, begin + k);
     }
-    const int many = min(32, pieces - first);
-    for (int i = 0; i < many; i += AHEAD) {
+    float2 ml[EACH];
 #pragma unroll
-      for (int r = 0; r < JOIN_EACH; ++r) {
-        if (first + i)
+    for (int r = 0; r < EACH; ++r) {
+      ml[r] = begin + lane < end ? stat(r, begin + lane) : make_float2(-INFINITY, 0.f);
+      for (int i = lane + 32; i < pieces; i += 32) m[r] = fmaxf(m[r], stat(r, i).x);
+      m[r] = warp_max_f(m[r]);
+      sum[r] = 0.f;
 #pragma unroll
-          for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, first + i + k);
+      for (int e = 0; e < PD / 32; ++e) o[r][e] = 0.f;
+    }
+    for (int first = begin; first < end; first += 32) {
+      float f[EACH], l[EACH];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {  // lanes behind the last piece have f -1 and l 0
-          const float g = __shfl_sync(0xffffffffu, f[r], i + k);
-          sum[r] += __shfl_sync(0xffffffffu, l[r], i + k);
-          const float* b = reinterpret_cast<const float*>(&v[r][k]);
+      for (int r = 0; r < EACH; ++r) {
+        if (first > begin) ml[r] = first + lane < end ? stat(r, first + lane) : make_float2(-INFINITY, 0.f);
+        f[r] = ml[r].x == -INFINITY ? 0.f : exp2_approx(ml[r].x - m[r]);
+        l[r] = ml[r].x == -INFINITY ? ml[r].y : f[r] * ml[r].y;
+        if (ml[r].x == -INFINITY && ml[r].y == 0.f) f[r] = -1.f;  // it has seen no key of this row
+      }
+      const int many = min(32, end - first);
+      for (int i = 0; i < many; i += AHEAD) {
 #pragma unroll
-          for (int e = 0; e < EACH; ++e)
-            if (!(g < 0.f)) o[r][e] += g * b[e];
+        for (int r = 0; r < EACH; ++r) {
+          if (first + i > begin)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) v[r][k] = value(r, first + i + k);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {  // lanes behind the last piece have f -1 and l 0
+            const float g = __shfl_sync(0xffffffffu, f[r], i + k);
+            sum[r] += __shfl_sync(0xffffffffu, l[r], i + k);
+            const float* b = reinterpret_cast<const float*>(&v[r][k]);
+#pragma unroll
+            for (int e = 0; e < PD / 32; ++e)
+              if (!(g < 0.f)) o[r][e] += g * b[e];
+          }
         }
       }
     }
   }
+};
+
+template <int PD>
+__device__ __forceinline__ void store_joined(const FwdArgs& p, const Work& w, int r, float m, float sum, const float (&o)[PD / 32]) {
+  constexpr int EACH = PD / 32;
+  const int lane = threadIdx.x % 32;
+  const int64_t row = (int64_t)w.row0 + r;
+  const bool empty = seen_end(w.doc, p.plan.frame, row) == 0;  // a query that sees no key
+  __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
+  const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int r = 0; r < JOIN_EACH; ++r) {
-    if (r0 + r >= rows) break;
-    const int64_t row = (int64_t)w.row0 + r0 + r;
-    const bool empty = seen_end(w.doc, p.plan.frame, row) == 0;  // a query that sees no key
-    __nv_bfloat16* out = p.out.ptr + (w.doc.q0 + row) * p.out.row + w.head * p.out.head + lane * EACH;
-    const float inv = empty ? 0.f : 1.f / sum[r];
-#pragma unroll
-    for (int k = 0; k < EACH; k += 2)
-      if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(o[r][k] * inv, o[r][k + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m[r] + log2_approx(sum[r]);
+  for (int k = 0; k < EACH; k += 2)
+    if (lane * EACH + k < p.plan.dim) *reinterpret_cast<uint32_t*>(out + k) = f2_to_bf16x2(o[k] * inv, o[k + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[(int64_t)w.head * p.plan.padded_rows + (int64_t)w.doc.tile0 * TILE + row] = empty ? -INFINITY : m + log2_approx(sum);
+}
+
+template <int PD>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid_constant__ FwdArgs p) {
+  pdl_launch_dependents();
+  __shared__ float parts[JOIN_WARPS][PD + 1];
+  pdl_wait();
+  const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
+  if (!w.ok) return;
+  const int rows = w.slot, pieces = w.end, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (rows <= 0 || (int64_t)w.row0 + rows > w.doc.queries || (int64_t)w.begin + (int64_t)rows * pieces > p.plan.slots) {
+    if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
+    return;
   }
+  if (rows >= JOIN_WARPS) {
+    const int r0 = blockIdx.y * JOIN_ROWS + warp * 2;
+    if (r0 >= rows) return;
+    const Joined<PD, 2, 4> j(p, w, r0, 0, pieces);
+    store_joined<PD>(p, w, r0, j.m[0], j.sum[0], j.o[0]);
+    if (r0 + 1 < rows) store_joined<PD>(p, w, r0 + 1, j.m[1], j.sum[1], j.o[1]);
+    return;
+  }
+  if (blockIdx.y > 0) return;
+  const int each = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;  // warps to a row
+  const int r = warp / each, part = warp % each, per = (pieces + each - 1) / each;
+  float m = 0.f, sum = 0.f, o[PD / 32] = {};
+  if (r < rows) {
+    const Joined<PD, 1, 8> j(p, w, r, min(part * per, pieces), min((part + 1) * per, pieces));
+    m = j.m[0], sum = j.sum[0];
+#pragma unroll
+    for (int e = 0; e < PD / 32; ++e) o[e] = j.o[0][e];
+  }
+#pragma unroll
+  for (int e = 0; e < PD / 32; ++e) parts[warp][lane * (PD / 32) + e] = o[e];
+  if (lane == 0) parts[warp][PD] = sum;
+  __syncthreads();
+  if (r >= rows || part) return;
+  for (int k = 1; k < each; ++k) {  // in the pieces' order
+    sum += parts[warp + k][PD];
+#pragma unroll
+    for (int e = 0; e < PD / 32; ++e) o[e] += parts[warp + k][lane * (PD / 32) + e];
+  }
+  store_joined<PD>(p, w, r, m, sum, o);
 }
 
 template <int PD>

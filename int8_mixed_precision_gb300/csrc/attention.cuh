@@ -33,7 +33,8 @@ struct Item {
   int32_t row0;         // rows of the document: queries, or keys (GRAD_KV)
   int32_t begin, end;   // tiles of the streamed operand; JOIN: the first partial row, the pieces
   int32_t slot;         // FORWARD: the first partial row, -1: the output itself; JOIN: the rows
-  int32_t unused[6];
+  int32_t turns;        // FORWARD: one block of rows whose tiles the CTA's two halves take in turn, each with a partial result
+  int32_t unused[5];
 };
 constexpr int ITEM_INTS = 16;
 static_assert(sizeof(Item) == 4 * ITEM_INTS, "");
@@ -71,7 +72,7 @@ struct Heads {
 // head's items follow one another and share its keys in L2.
 struct Work {
   Doc doc;
-  int32_t row0, begin, end, slot;
+  int32_t row0, begin, end, slot, turns;
   int32_t head;
   bool ok;  // the entry fits the plan
 };
@@ -100,7 +101,7 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
     const int4* it = reinterpret_cast<const int4*>(table + first_item(p, list)) + (ITEM_INTS / 4) * (int64_t)i;
     const int4 a = __ldg(it), b = __ldg(it + 1), c = __ldg(it + 2);
     w.doc = Doc{a.x, a.y, a.z, a.w, b.x, b.y};
-    w.row0 = b.z, w.begin = b.w, w.end = c.x, w.slot = c.y;
+    w.row0 = b.z, w.begin = b.w, w.end = c.x, w.slot = c.y, w.turns = c.z;
     w.ok = fits(w, p, list);
   }
   if (!w.ok && threadIdx.x == 0) raise_status(ws, DIT_ERR_INVALID_ARG);
@@ -116,6 +117,7 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
   w.begin = lora::uniform(w.begin);
   w.end = lora::uniform(w.end);
   w.slot = lora::uniform(w.slot);
+  w.turns = lora::uniform(w.turns);
   w.head = lora::uniform(w.head);
   w.ok = lora::uniform(w.ok);
   return w;

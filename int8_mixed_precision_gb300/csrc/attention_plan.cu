@@ -40,7 +40,9 @@ static double makespan(std::vector<double> pieces, int heads) {
 
 // A forward CTA's time in tiles of one row block: its start and end, then its tiles.  Pieces of a split item write and
 // read partial results besides.
-constexpr double START = 5.0, SPLIT_END = 2.0, JOIN_TIME = 6.0;
+// (START, SPLIT_END), and the joining kernel.  A tile of one block of rows takes as long as one of two, a chain of waits; where it is cut
+// into pieces anyway, the CTA's halves take its tiles in turn.
+constexpr double START = 5.0, SPLIT_END = 2.0, JOIN_TIME = 6.0, LONE = 0.95, TURNS = 0.5;
 
 static dit_status make_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
                             int64_t documents, int64_t frame, int heads, int kv_heads, int dim, int training,
@@ -90,8 +92,8 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     for (int64_t r = 0; r < docs[i].queries; r += 2 * rt) {
       const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
       const int64_t n = (seen_end(docs[i], frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
-      const double each = last - r >= rt ? 1.0 : 0.6;
-      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, {}}, START + each * (double)n});
+      const double each = last - r >= rt ? 1.0 : LONE;
+      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, 0, {}}, START + each * (double)n});
     }
   // Few items: their keys are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
   // brings the end of the last CTA forward most.
@@ -118,7 +120,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
         now.clear();
         for (const Costed& c : lists[FORWARD]) {
           const int64_t n = c.item.end, pieces = (n + len - 1) / len;
-          const double each = n ? (c.cost - START) / (double)n : 0.0;
+          const double each = c.item.row0 + rt >= c.item.doc.queries ? TURNS : 1.0;
           if (pieces <= 1)
             now.push_back(c.cost);
           else
@@ -143,14 +145,16 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
         }
         const Doc& d = c.item.doc;
         const int32_t rows = (int32_t)std::min<int64_t>(2 * rt, d.queries - c.item.row0);
-        const double each = (c.cost - START) / (double)n;
-        lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)pieces, rows, {}}, 1.0});
+        const bool turns = c.item.row0 + rt >= d.queries;
+        const double each = turns ? TURNS : 1.0;
+        lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)(turns ? 2 * pieces : pieces), rows, 0, {}}, 1.0});
         for (int64_t k = 0; k < pieces; ++k) {
           Item it = c.item;
           it.begin = (int32_t)cut(n, longest, evenly, k);
           it.end = (int32_t)cut(n, longest, evenly, k + 1);
           it.slot = plan->slots;
-          plan->slots += rows;
+          it.turns = turns;
+          plan->slots += turns ? 2 * rows : rows;
           lists[FORWARD].push_back({it, START + SPLIT_END + each * (double)(it.end - it.begin)});
         }
       }
@@ -161,12 +165,12 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const Doc& d = docs[i];
       for (int64_t r = 0; r < d.queries; r += TILE) {
         const int64_t n = (seen_end(d, frame, std::min<int64_t>(d.queries, r + TILE) - 1) + cols - 1) / cols;
-        lists[GRAD_Q].push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, {}}, START + (double)n});
+        lists[GRAD_Q].push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, 0, {}}, START + (double)n});
       }
       const int64_t end = ((int64_t)d.queries + cols - 1) / cols;
       for (int64_t k = 0; k < d.keys; k += TILE) {
         const int64_t begin = std::min(end, seen_from(d, frame, k) / cols);
-        lists[GRAD_KV].push_back({Item{d, (int32_t)k, (int32_t)begin, (int32_t)end, -1, {}}, START + (double)(end - begin)});
+        lists[GRAD_KV].push_back({Item{d, (int32_t)k, (int32_t)begin, (int32_t)end, -1, 0, {}}, START + (double)(end - begin)});
       }
     }
   std::vector<std::pair<int32_t, int32_t>> buckets[DIT_ATTENTION_LISTS];

@@ -64,11 +64,11 @@ def test_norm_refusals(dit):
 # ----------------------------------------------------------------------------------------
 
 def lists(plan):
-    """The four lists of items, each (document's q0, queries, k0, keys, prefix, first padded tile; row, begin, end, slot), and the buckets."""
+    """The four lists of items, each (document's q0, queries, k0, keys, prefix, first padded tile; row, begin, end, slot, turns), and the buckets."""
     i, t = plan.info, plan.table.tolist()
     at, out = 0, []
     for n in i.items:
-        out.append([t[at + 16 * k:at + 16 * k + 10] for k in range(n)])
+        out.append([t[at + 16 * k:at + 16 * k + 11] for k in range(n)])
         at += 16 * n
     assert at == i.table_ints
     buckets = [[list(i.bucket[k][2 * b:2 * b + 2]) for b in range(n)] for k, n in enumerate(i.buckets)]
@@ -98,7 +98,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     met = [torch.zeros(n, m, dtype=torch.int32) for n, m in zip(queries, keys)]
     rows = [torch.zeros(n, dtype=torch.int32) for n in queries]
     slots = {}
-    for doc, row0, begin, end, slot in fwd:
+    for doc, row0, begin, end, slot, turns in fwd:
         part = slice(row0, min(queries[doc], row0 + 2 * rt))
         met[doc][part, begin * cols:end * cols] += 1
         assert end * cols < keys[doc] + cols
@@ -106,17 +106,21 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
             rows[doc][part] += 1
         else:
             n = part.stop - part.start
-            slots[slot] = (doc, row0, n, begin, end)
-            assert slot + n <= plan.info.slots
+            # the halves of a CTA that take a lone block's tiles in turn leave a partial result each
+            assert turns == (queries[doc] - row0 <= rt)
+            slots[slot] = (doc, row0, n, begin, end, 2 if turns else 1)
+            assert slot + n * (2 if turns else 1) <= plan.info.slots
     used = torch.zeros(plan.info.slots, dtype=torch.int32)
-    for doc, row0, first, pieces, n in joins:
+    for doc, row0, first, pieces, n, _ in joins:
         rows[doc][row0:row0 + n] += 1
-        at = 0
-        for k in range(pieces):
-            d, r, c, begin, end = slots[first + k * n]
+        at, k = 0, 0
+        while k < pieces:
+            d, r, c, begin, end, halves = slots[first + k * n]
             assert (d, r, c, begin) == (doc, row0, n, at) and end > begin
             at = end
-            used[first + k * n:first + (k + 1) * n] += 1
+            used[first + k * n:first + (k + halves) * n] += 1
+            k += halves
+        assert k == pieces
     assert (used == 1).all()
     for n, m, r, s in zip(queries, keys, rows, seen):
         assert (r == 1).all()

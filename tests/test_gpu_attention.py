@@ -151,6 +151,16 @@ def test_keys_in_a_cache(dit, c):
         b.check()
 
 
+@pytest.mark.parametrize("dim", [40, 64, 128])
+@pytest.mark.parametrize("queries,heads,kv_heads", [(1, 1, 1), (100, 2, 2), (9, 14, 1), (128, 1, 1), (129, 1, 1), (300, 1, 1)])
+def test_pieces_of_one_block_of_rows(dit, queries, heads, kv_heads, dim):
+    """Tiles that the halves of a CTA take in turn, of odd and even numbers, with a last one that is not whole; and items of two blocks."""
+    for keys in (257, 2000, 5000 + queries):
+        b = Batch(dit, [queries, 3], heads, kv_heads, dim, frame=7, prefix=5, kv_lengths=[keys, 700], room=keys + 20, train=False)
+        b.forward()
+        b.check()
+
+
 def test_many_splits(dit):
     """Long keys of one head are cut among the SMs and joined."""
     b = Batch(dit, [3], 1, 1, 64, kv_lengths=[40000], train=False)
