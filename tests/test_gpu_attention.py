@@ -295,6 +295,21 @@ def test_wrong_table_entries_are_skipped(dit):
         assert not torch.equal(good, b.out)
 
 
+def test_pieces_that_nothing_joins_are_skipped(dit):
+    """A plan without joins has no place for partial results: an entry that names one writes nothing and raises the status word."""
+    b = Batch(dit, [100, 60], 2, 2, 64, train=False)
+    assert b.plan.info.items[1] == 0
+    table = b.plan.table.view(-1)[: 16 * b.plan.info.items[0]].view(-1, 16)
+    table[:, 10] = 1  # without a partial result this asks for nothing
+    b.forward()
+    b.check()
+    table[:, 9] = 0
+    b.out[:] = 7.0
+    b.forward()
+    assert (b.out == 7.0).all()
+    assert dit.device_status(b.ws) == 1 << 1
+
+
 def test_offsets_past_32_bits(dit):
     """Keys and values far apart: offsets in elements pass 2^31."""
     n, stride = 34000, 65536
