@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       }
     }
   }
+  if (KEYS) pdl_wait();  // whoever follows finds the gradient of the queries complete too
   fence_before();
   __syncthreads();
   if (warp == 1) {

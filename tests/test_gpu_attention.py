@@ -363,6 +363,24 @@ def test_calls_back_to_back(dit):
         assert all(torch.equal(x, y) for x, y in zip(apart, run(False)))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_whoever_follows_finds_dq_complete(dit, dim):
+    """Few queries over many keys: the kernel of dk and dv has little to do and runs beside a long one of dq.  What comes behind both
+    on the stream, here the norms' gradients, reads all of dq."""
+    b = Batch(dit, [128], 2, 2, dim, kv_lengths=[20000], tail=0)
+    norm = dit.QKNorm(torch.rand(2, dim, device="cuda") + 0.5, "rms")
+    got, want = torch.empty_like(b.q), torch.empty_like(b.q)
+    b.forward()
+    for _ in range(3):
+        b.dq.fill_(5.0)
+        b.backward()
+        dit.qk_norm_rope_backward(b.q, None, b.dq, None, got, None, norm, None, None, None, None, b.ws)
+        torch.cuda.synchronize()
+        dit.qk_norm_rope_backward(b.q, None, b.dq, None, want, None, norm, None, None, None, None, b.ws)
+        assert torch.equal(got, want)
+    b.check()
+
+
 def test_gradients_match_differences(dit):
     """The gradients against differences of the 64-bit formula, so that both could not share a mistake."""
     b = Batch(dit, [9, 20], 2, 1, 64, frame=3, prefix=4)
