@@ -38,11 +38,16 @@ static double makespan(std::vector<double> pieces, int heads) {
   return last;
 }
 
-// A forward CTA's time in tiles of one row block: its start and end, then its tiles.  Pieces of a split item write and
-// read partial results besides.
-// (START, SPLIT_END), and the joining kernel.  A tile of one block of rows takes as long as one of two, a chain of waits; where it is cut
-// into pieces anyway, the CTA's halves take its tiles in turn.
-constexpr double START = 5.0, SPLIT_END = 2.0, JOIN_TIME = 6.0, LONE = 0.95, TURNS = 0.5;
+// Forward times in tiles of two blocks of rows (0.8 us with up to 64 dimensions, 1.8 with up to 128): a CTA's start and end; what a piece of
+// a split item adds, which writes a partial result; the joining kernel whatever it joins; and for each partial row of it.
+// A tile of one block of rows takes as long as one of two, a chain of waits (LONE); where it is cut into pieces anyway, the
+// CTA's halves take its tiles in turn (TURNS).
+struct Times {
+  double start, split_end, join, join_row;
+};
+constexpr Times TIMES[2] = {{5.0, 2.0, 5.0, 1.5e-4}, {3.0, 1.2, 3.0, 0.7e-4}};
+constexpr double LONE = 0.95, TURNS = 0.5;
+constexpr double BACK_START = 5.0;  // of a backward CTA, in tiles
 
 static dit_status make_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
                             int64_t documents, int64_t frame, int heads, int kv_heads, int dim, int training,
@@ -85,6 +90,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   }
 
   const int cols = BACK_COLS, rt = rows_per_tile(group), pd = padded_dim(dim);
+  const Times& time = TIMES[pd > 64];
   std::vector<Costed> lists[DIT_ATTENTION_LISTS];
   // forward: two row blocks to an item.  The second one costs about as much again less what its MMAs hide.
   std::vector<double> costs;
@@ -93,59 +99,76 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
       const int64_t n = (seen_end(docs[i], frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
       const double each = last - r >= rt ? 1.0 : LONE;
-      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, 0, {}}, START + each * (double)n});
+      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, 0, {}}, time.start + each * (double)n});
     }
-  // Few items: their keys are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
-  // brings the end of the last CTA forward most.
+  // Few items: the keys of some are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
+  // brings the end of the last CTA forward most.  Which items: those that are left when zero to three rounds of the SMs have whole ones,
+  // since what is cut has to be joined.  Lone blocks of rows first, whose halves work at a piece together, then the longest.  With
+  // all items cut alike 1350 queries over 8326 keys took 105 us (30 heads of 64), with five of six whole 86.
   auto cut = [](int64_t n, int64_t len, bool even, int64_t k) {  // where piece k begins
     const int64_t pieces = (n + len - 1) / len;
     return even ? n * k / pieces : std::min(n, k * len);
   };
-  const int64_t ctas = (int64_t)lists[FORWARD].size() * kv_heads;
+  auto lone = [&](const Item& it) { return it.row0 + rt >= it.doc.queries; };
+  std::vector<Costed>& items = lists[FORWARD];
+  const int64_t ctas = (int64_t)items.size() * kv_heads;
   if (ctas && ctas < 4 * SMS) {
+    std::stable_sort(items.begin(), items.end(), [&](const Costed& a, const Costed& b) {
+      return lone(a.item) != lone(b.item) ? lone(a.item) : a.item.end > b.item.end;
+    });
     std::vector<double> now;
     int64_t most = 0;
-    for (const Costed& c : lists[FORWARD]) {
+    for (const Costed& c : items) {
       now.push_back(c.cost);
       most = std::max<int64_t>(most, c.item.end);
     }
     double best = makespan(now, kv_heads);
-    int64_t longest = 0;  // tiles of a piece; 0: items stay whole
+    int64_t longest = 0, cuts = 0;  // tiles of a piece, 0: items stay whole; the items that may be cut
     bool evenly = true;
-    for (int64_t len = most; len >= 2; len = len > 24 ? len * 15 / 16 : len - 1) {
-      int64_t total = 0;
-      for (const Costed& c : lists[FORWARD]) total += std::max<int64_t>((c.item.end + len - 1) / len, 1);
-      if (total * kv_heads > 6 * SMS) break;
-      for (int even = 0; even < 2; ++even) {
-        now.clear();
-        for (const Costed& c : lists[FORWARD]) {
-          const int64_t n = c.item.end, pieces = (n + len - 1) / len;
-          const double each = c.item.row0 + rt >= c.item.doc.queries ? TURNS : 1.0;
-          if (pieces <= 1)
-            now.push_back(c.cost);
-          else
-            for (int64_t k = 0; k < pieces; ++k) now.push_back(START + SPLIT_END + each * (double)(cut(n, len, even, k + 1) - cut(n, len, even, k)));
-        }
-        const double t = makespan(now, kv_heads) + JOIN_TIME;
-        if (t < best) {
-          best = t;
-          longest = len;
-          evenly = even;
+    for (int rounds = 0; rounds < 4; ++rounds) {
+      const int64_t may = (int64_t)items.size() - rounds * SMS / kv_heads;
+      if (may <= 0) break;
+      for (int64_t len = most; len >= 2; len = len > 24 ? len * 15 / 16 : len - 1) {
+        int64_t total = 0;
+        for (int64_t i = 0; i < may; ++i) total += std::max<int64_t>((items[(size_t)i].item.end + len - 1) / len, 1);
+        if (total * kv_heads > 6 * SMS) break;
+        for (int even = 0; even < 2; ++even) {
+          now.clear();
+          int64_t joined = 0;
+          for (int64_t i = 0; i < (int64_t)items.size(); ++i) {
+            const Costed& c = items[(size_t)i];
+            const int64_t n = c.item.end, pieces = i < may ? (n + len - 1) / len : 1;
+            const double each = lone(c.item) ? TURNS : 1.0;
+            if (pieces <= 1) {
+              now.push_back(c.cost);
+              continue;
+            }
+            joined += std::min<int64_t>(2 * rt, c.item.doc.queries - c.item.row0) * pieces * (lone(c.item) ? 2 : 1);
+            for (int64_t k = 0; k < pieces; ++k) now.push_back(time.start + time.split_end + each * (double)(cut(n, len, even, k + 1) - cut(n, len, even, k)));
+          }
+          const double t = makespan(now, kv_heads) + time.join + time.join_row * (double)joined * heads;
+          if (t < best) {
+            best = t;
+            longest = len;
+            cuts = may;
+            evenly = even;
+          }
         }
       }
     }
     if (longest) {
       std::vector<Costed> whole;
-      whole.swap(lists[FORWARD]);
-      for (const Costed& c : whole) {
-        const int64_t n = c.item.end, pieces = (n + longest - 1) / longest;
+      whole.swap(items);
+      for (int64_t i = 0; i < (int64_t)whole.size(); ++i) {
+        const Costed& c = whole[(size_t)i];
+        const int64_t n = c.item.end, pieces = i < cuts ? (n + longest - 1) / longest : 1;
         if (pieces <= 1) {
-          lists[FORWARD].push_back(c);
+          items.push_back(c);
           continue;
         }
         const Doc& d = c.item.doc;
         const int32_t rows = (int32_t)std::min<int64_t>(2 * rt, d.queries - c.item.row0);
-        const bool turns = c.item.row0 + rt >= d.queries;
+        const bool turns = lone(c.item);
         const double each = turns ? TURNS : 1.0;
         lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)(turns ? 2 * pieces : pieces), rows, 0, {}}, 1.0});
         for (int64_t k = 0; k < pieces; ++k) {
@@ -155,7 +178,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
           it.slot = plan->slots;
           it.turns = turns;
           plan->slots += turns ? 2 * rows : rows;
-          lists[FORWARD].push_back({it, START + SPLIT_END + each * (double)(it.end - it.begin)});
+          items.push_back({it, time.start + time.split_end + each * (double)(it.end - it.begin)});
         }
       }
     }
@@ -165,12 +188,12 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       const Doc& d = docs[i];
       for (int64_t r = 0; r < d.queries; r += TILE) {
         const int64_t n = (seen_end(d, frame, std::min<int64_t>(d.queries, r + TILE) - 1) + cols - 1) / cols;
-        lists[GRAD_Q].push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, 0, {}}, START + (double)n});
+        lists[GRAD_Q].push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, 0, {}}, BACK_START + (double)n});
       }
       const int64_t end = ((int64_t)d.queries + cols - 1) / cols;
       for (int64_t k = 0; k < d.keys; k += TILE) {
         const int64_t begin = std::min(end, seen_from(d, frame, k) / cols);
-        lists[GRAD_KV].push_back({Item{d, (int32_t)k, (int32_t)begin, (int32_t)end, -1, 0, {}}, START + (double)(end - begin)});
+        lists[GRAD_KV].push_back({Item{d, (int32_t)k, (int32_t)begin, (int32_t)end, -1, 0, {}}, BACK_START + (double)(end - begin)});
       }
     }
   std::vector<std::pair<int32_t, int32_t>> buckets[DIT_ATTENTION_LISTS];

@@ -155,6 +155,16 @@ def test_plan_covers_every_pair_once(dit, c):
     check_plan(dit, *c)
 
 
+def test_items_that_fill_whole_rounds_stay_whole(dit):
+    """5 of 6 items of 30 heads are 150 CTAs, a round of the SMs; the sixth alone, one block of rows, is cut and joined."""
+    plan = check_plan(dit, [1350], [8326], 30, 30, 64, 0, 0)
+    fwd, joins = lists(plan)[0][:2]
+    whole = [item for item in fwd if item[9] < 0]
+    assert [item[6] for item in joins] == [1280] and len(whole) == 5
+    assert all(item[7] == 0 and item[8] == 66 for item in whole)
+    assert all(item[10] == 1 for item in fwd if item[9] >= 0)
+
+
 def test_plans_of_random_batches(dit):
     rng = random.Random(0)
     for _ in range(25):

@@ -381,6 +381,24 @@ def test_whoever_follows_finds_dq_complete(dit, dim):
     b.check()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_whoever_follows_finds_dk_and_dv_complete(dit, dim):
+    """Many queries over few keys: the kernel of dq has little to do beside a long one of dk and dv."""
+    b = Batch(dit, [20000], 2, 2, dim, kv_lengths=[128], tail=0)
+    norm = dit.QKNorm(torch.rand(2, dim, device="cuda") + 0.5, "rms")
+    got, want = torch.empty_like(b.k), torch.empty_like(b.k)
+    b.forward()
+    for dx in (b.dk, b.dv):
+        for _ in range(3):
+            dx.fill_(5.0)
+            b.backward()
+            dit.qk_norm_rope_backward(b.k, None, dx, None, got, None, norm, None, None, None, None, b.ws)
+            torch.cuda.synchronize()
+            dit.qk_norm_rope_backward(b.k, None, dx, None, want, None, norm, None, None, None, None, b.ws)
+            assert torch.equal(got, want)
+    b.check()
+
+
 def test_gradients_match_differences(dit):
     """The gradients against differences of the 64-bit formula, so that both could not share a mistake."""
     b = Batch(dit, [9, 20], 2, 1, 64, frame=3, prefix=4)
