@@ -643,7 +643,7 @@ typedef struct {
   int32_t items[DIT_ATTENTION_LISTS]; /* forward, joins, gradient of queries, gradients of keys */
   int32_t buckets[DIT_ATTENTION_LISTS]; /* runs of items of like cost: their first items and numbers of items */
   int32_t bucket[DIT_ATTENTION_LISTS][2 * DIT_ATTENTION_BUCKETS];
-  int32_t reserved;
+  int32_t row_blocks;    /* forward: blocks of rows to an item, 1 or 2 */
 } dit_attention_plan_t;
 
 dit_status dit_attention_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins,

@@ -31,7 +31,7 @@ class _Rotary(ctypes.Structure):
 class _Plan(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int64) for name in ("q_rows", "k_rows", "padded_rows", "table_ints", "saved_bytes", "scratch_bytes")] + \
         [(name, ctypes.c_int32) for name in ("documents", "heads", "kv_heads", "dim", "frame", "training", "slots")] + \
-        [("items", ctypes.c_int32 * 4), ("buckets", ctypes.c_int32 * 4), ("bucket", ctypes.c_int32 * 32 * 4), ("reserved", ctypes.c_int32)]
+        [("items", ctypes.c_int32 * 4), ("buckets", ctypes.c_int32 * 4), ("bucket", ctypes.c_int32 * 32 * 4), ("row_blocks", ctypes.c_int32)]
 
 
 # ----------------------------------------------------------------------------------------

@@ -17,8 +17,11 @@
 // Few rows.  Where the keys of an item are cut into pieces and it has one block of rows alone, the CTA's halves take its tiles
 // in turn, two blocks of the same rows: a tile's chain of waits is then half as long for two.
 //
+// Short items.  Where no item has many tiles and there are 64 dimensions, a CTA has one block of rows and an SM two CTAs.
+//
 // Warps: 0 loads, 1 issues S, 2 and 3 issue O += P V of a block each, 4 to 7 relay the MMAs' completion to the rows' warps, which are
-// 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  Every wait on memory is bounded.
+// 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  With one block of rows 3 relays, and
+// 4 to 7 have the rows.  Every wait on memory is bounded.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -34,21 +37,24 @@ using namespace lora;
 
 constexpr float GROWTH = 8.f;
 constexpr int FWD_STAGES = 6;  // most
-using Regs = Registers<4, 128, 48, 208>;
 
-template <int PD>
+// BLOCKS: blocks of rows to a CTA.  One, and two CTAs to an SM, for short items.
+template <int PD, int BLOCKS>
 struct Fwd {
+  using Regs = Registers<2 * BLOCKS, 128, 48, 208, BLOCKS>;
   static constexpr int COLS = FORWARD_COLS;
   static constexpr int CHUNKS = PD / 64;
   static constexpr bool OVER_S = PD > 64;  // P takes the place of S
   static constexpr int Q_CHUNK = TILE * 128, Q_BYTES = CHUNKS * Q_CHUNK;
   static constexpr int KV_CHUNK = COLS * 128, KV_BYTES = CHUNKS * KV_CHUNK;
-  static constexpr int STAGES = PD == 64 ? 6 : 2;
-  static constexpr int CONTROL = 2 * Q_BYTES + 2 * STAGES * KV_BYTES;
+  static constexpr int STAGES = PD == 64 && BLOCKS == 2 ? 6 : 2;
+  static constexpr int RING = BLOCKS * Q_BYTES;
+  static constexpr int CONTROL = RING + 2 * STAGES * KV_BYTES;
   static constexpr int SMEM = CONTROL + 1024 + 1024;
   // tensor memory: S and P of each block, then O
-  static constexpr uint32_t S = 0, P = OVER_S ? S : 2 * COLS, P_STEP = OVER_S ? COLS : COLS / 2, O = OVER_S ? 2 * COLS : 3 * COLS;
-  static_assert(O + 2 * PD <= 512 && SMEM <= 227 * 1024, "");
+  static constexpr uint32_t S = 0, P = OVER_S ? S : BLOCKS * COLS, P_STEP = OVER_S ? COLS : COLS / 2, O = P + BLOCKS * P_STEP;
+  static constexpr uint32_t COLUMNS = BLOCKS == 2 ? 512 : 256;
+  static_assert(O + BLOCKS * PD <= COLUMNS && (3 - BLOCKS) * (SMEM + 1024) <= 228 * 1024, "");
 };
 
 struct FwdControl {
@@ -77,12 +83,13 @@ struct FwdArgs {
 
 // SPLIT: some items are pieces of a longer one, whose results are partial.  A kernel that has none is
 // 1.76 ms instead of 1.79 at 17,776 rows of 30 heads of 64.
-template <int PD, bool SPLIT>
-__global__ void __launch_bounds__(Regs::THREADS, 1)
+template <int PD, bool SPLIT, int BLOCKS>
+__global__ void __launch_bounds__(Fwd<PD, BLOCKS>::Regs::THREADS, 3 - BLOCKS)
     k_attention(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ FwdArgs p) {
   pdl_launch_dependents();
-  using F = Fwd<PD>;
+  using F = Fwd<PD, BLOCKS>;
+  using Regs = typename F::Regs;
   constexpr int COLS = F::COLS;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -103,7 +110,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       mbar_init(smem_u32(&c->pdone[t]), 1);
     } else if (lane == 10) {
       mbar_init(smem_u32(&c->qfull), 1);
-      mbar_init(smem_u32(&c->done), 3);
+      mbar_init(smem_u32(&c->done), 1 + BLOCKS);
       mbar_init(smem_u32(&c->tail), 1);
       c->abort = 0;
     }
@@ -113,7 +120,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
     if (lane < 3) prefetch_tmap(lane == 0 ? &mq : lane == 1 ? &mk : &mv);
     __syncwarp();
   } else if (warp == 1) {
-    tmem_alloc(smem_u32(&c->tmem), 512);
+    tmem_alloc(smem_u32(&c->tmem), F::COLUMNS);
     fence_before();
   }
   pdl_wait();
@@ -127,7 +134,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   const int n = uniform(w.ok ? w.end - w.begin : 0);  // tiles
   // Two blocks of rows, one, or one whose tiles both halves of the CTA take in turn, as two blocks of the same rows.
   const bool turns = SPLIT && w.ok && w.turns && w.slot >= 0;
-  const int blocks = w.ok && (turns || row0 + p.rows < d.queries) ? 2 : 1, step = turns ? 2 : 1;
+  const int blocks = BLOCKS == 2 && w.ok && (turns || row0 + p.rows < d.queries) ? 2 : 1, step = turns ? 2 : 1;
   auto first_of = [&](int t) { return turns ? t : 0; };
   auto tiles_of = [&](int t) { return t < blocks ? (n - first_of(t) + step - 1) / step : 0; };
   const bool work = n > 0;
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   if (warp < Regs::FIRST_ROWS) Regs::give();
   if (warp == 0) {
     if (work && elect_one()) {
-      const uint32_t ring = smem + 2 * F::Q_BYTES;
+      const uint32_t ring = smem + F::RING;
       int s = 0, parity = 1, issued = 0;  // of K; V has as many or one less
       bool ok = true;
       if (!p.stall) {
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   } else if (warp == 1) {
     if (work) {  // S of each tile and block, once its warps have the tile before in registers (OVER_S: once P is used up)
       constexpr uint32_t id = idesc(128, COLS, false, false);
-      const uint32_t ring = smem + 2 * F::Q_BYTES;
+      const uint32_t ring = smem + F::RING;
       bool ok = warp_wait(smem_u32(&c->qfull), 0, p.ws, abort);
       int s = 0, parity = 0;
       for (int j = 0; j < n && ok; ++j) {
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       if (elect_one()) mma_commit(smem_u32(&c->done));
       __syncwarp();
     }
-  } else if (warp < 4) {
+  } else if (warp < 2 + BLOCKS) {
     const int t = warp - 2;
     if (work && t < blocks) {  // O += P V of a block
       const uint32_t id = idesc(128, (p.plan.dim + 15) / 16 * 16, false, true);
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
       int left = d.keys - (w.begin + s) * COLS;  // keys from this tile's first on
       const int many = tiles_of(t);
       for (int j = 0; j < many && ok; ++j, left -= step * COLS) {
-        const uint32_t v = smem + 2 * F::Q_BYTES + (F::STAGES + s) * F::KV_BYTES;
+        const uint32_t v = smem + F::RING + (F::STAGES + s) * F::KV_BYTES;
         ok = warp_wait(smem_u32(&c->vfull[s]), parity, p.ws, abort);
         if (ok && left < COLS) {  // the document's last tile, for both blocks
           if (t == 0 || turns) {
@@ -253,6 +260,12 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
         warp_wait(smem_u32(&c->done), 0, p.ws, &never);
       }
     }
+  } else if (BLOCKS == 1 && warp < Regs::FIRST_ROWS) {  // one relay for both, in the order in which the rows' warps ask
+    if (work)
+      for (int j = 0; j <= n; ++j) {
+        if (j < n) relay_one<160>(smem_u32(&c->sfull[0]), 1, j, p.ws, abort);
+        if (j > 0) relay_one<160>(smem_u32(&c->pdone[0]), 3, j - 1, p.ws, abort);
+      }
   } else if (warp < Regs::FIRST_ROWS) {
     const int t = warp % 2, what = (warp - 4) / 2;
     if (work) relay<160>(smem_u32(what ? &c->pdone[t] : &c->sfull[t]), 1 + what * 2 + t, tiles_of(t), p.ws, abort);
@@ -404,7 +417,7 @@ __global__ void __launch_bounds__(Regs::THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     fence_after();
-    tmem_free(tmem, 512);
+    tmem_free(tmem, F::COLUMNS);
   }
 }
 
@@ -534,9 +547,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid
   store_joined<PD>(p, w, r, m, sum, o);
 }
 
-template <int PD, bool SPLIT>
+template <int PD, bool SPLIT, int BLOCKS>
 static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads& v, cudaStream_t st) {
-  using F = Fwd<PD>;
+  using F = Fwd<PD, BLOCKS>;
+  using Regs = typename F::Regs;
   static OncePerDevice checked, once;
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded: any tensor makes a map
@@ -546,8 +560,8 @@ static dit_status launch(FwdArgs& a, const Heads& q, const Heads& k, const Heads
   if (!map_heads(&mq, q, a.plan.dim, a.plan.heads, a.plan.q_rows, a.group, a.rows) ||
       !map_heads(&mk, keys ? k : q, a.plan.dim, k_heads, k_rows, 1, F::COLS) || !map_heads(&mv, keys ? v : q, a.plan.dim, k_heads, k_rows, 1, F::COLS))
     return DIT_ERR_CUDA;
-  if (prepare_kernel<Regs>(checked, once, k_attention<PD, SPLIT>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
-  if (launch_pdl(k_attention<PD, SPLIT>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
+  if (prepare_kernel<Regs>(checked, once, k_attention<PD, SPLIT, BLOCKS>, F::SMEM) != cudaSuccess) return DIT_ERR_CUDA;
+  if (launch_pdl(k_attention<PD, SPLIT, BLOCKS>, dim3((unsigned)(a.plan.items[FORWARD] * a.plan.kv_heads)), dim3(Regs::THREADS), F::SMEM, st, 1, mq, mk, mv, a) != cudaSuccess)
     return DIT_ERR_CUDA;
   if (SPLIT && launch_pdl(k_attention_join<PD>, dim3((unsigned)(a.plan.items[JOIN] * a.plan.heads), (unsigned)(2 * a.rows + JOIN_ROWS - 1) / JOIN_ROWS), dim3(32 * JOIN_WARPS), 0, st, 1, a) != cudaSuccess)
     return DIT_ERR_CUDA;
@@ -588,6 +602,7 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
   a.rows = rows_per_tile(a.group);
   a.stall = test_stall();
   if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
-  if (plan->items[JOIN] > 0) return plan->dim <= 64 ? launch<64, true>(a, hq, hk, hv, stream) : launch<128, true>(a, hq, hk, hv, stream);
-  return plan->dim <= 64 ? launch<64, false>(a, hq, hk, hv, stream) : launch<128, false>(a, hq, hk, hv, stream);
+  if (plan->row_blocks == 1) return launch<64, false, 1>(a, hq, hk, hv, stream);
+  if (plan->items[JOIN] > 0) return plan->dim <= 64 ? launch<64, true, 2>(a, hq, hk, hv, stream) : launch<128, true, 2>(a, hq, hk, hv, stream);
+  return plan->dim <= 64 ? launch<64, false, 2>(a, hq, hk, hv, stream) : launch<128, false, 2>(a, hq, hk, hv, stream);
 }

@@ -129,14 +129,14 @@ dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, He
 bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows);
 
 // ---------------------------------------------------------------------------------------
-// A CTA of warpgroups that load and issue and of two that hold a tile's rows in registers and take over what the first
+// A CTA of warpgroups that load and issue and of HOLD (two) that hold a tile's rows in registers and take over what the first
 // ones need not.  The block is launched with so many registers a thread and the shares add up to those: taking
 // more than the launch brought would wait for ever, so the host checks what the kernel was compiled to.
 // ---------------------------------------------------------------------------------------
-template <int WARPGROUPS, int LAUNCH, int ISSUE, int ROWS>
+template <int WARPGROUPS, int LAUNCH, int ISSUE, int ROWS, int HOLD = 2>
 struct Registers {
-  static constexpr int THREADS = 128 * WARPGROUPS, LAUNCHED = LAUNCH, FIRST_ROWS = 4 * (WARPGROUPS - 2);
-  static_assert((WARPGROUPS - 2) * ISSUE + 2 * ROWS <= WARPGROUPS * LAUNCH && THREADS * LAUNCH <= 65536, "");
+  static constexpr int THREADS = 128 * WARPGROUPS, LAUNCHED = LAUNCH, FIRST_ROWS = 4 * (WARPGROUPS - HOLD);
+  static_assert((WARPGROUPS - HOLD) * ISSUE + HOLD * ROWS <= WARPGROUPS * LAUNCH && THREADS * LAUNCH <= 65536, "");
   static __device__ __forceinline__ void give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE)); }
   static __device__ __forceinline__ void take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROWS)); }
 };
@@ -173,14 +173,16 @@ __device__ __forceinline__ void meet(int barrier) {
 // The relay: passes on the completion of `n` phases.  It meets the row warps in each round, whatever its waits say, so
 // that none is left behind; they look at the flag at the end.
 template <int THREADS>
+__device__ __forceinline__ void relay_one(uint32_t bar, int barrier, int j, void* ws, volatile int* abort) {
+  if (!__any_sync(0xffffffffu, *abort)) lora::warp_wait(bar, j & 1, ws, abort);
+  lora::fence_after();
+  lora::fence_before();
+  __syncwarp();
+  meet<THREADS>(barrier);
+}
+template <int THREADS>
 __device__ __forceinline__ void relay(uint32_t bar, int barrier, int n, void* ws, volatile int* abort) {
-  for (int j = 0; j < n; ++j) {
-    if (!__any_sync(0xffffffffu, *abort)) lora::warp_wait(bar, j & 1, ws, abort);
-    lora::fence_after();
-    lora::fence_before();
-    __syncwarp();
-    meet<THREADS>(barrier);
-  }
+  for (int j = 0; j < n; ++j) relay_one<THREADS>(bar, barrier, j, ws, abort);
 }
 // 32 accumulator columns of this thread's row and the largest of them (NaN counts for nothing); complete after lora::tmem_wait()
 // and pin()

@@ -20,15 +20,15 @@ struct Costed {
   double cost;
 };
 
-// The end of the last of `pieces` on SMS processors that take them in order.
-static double makespan(std::vector<double> pieces, int heads) {
+// The end of the last of `pieces` on `places` processors that take them in order.
+static double makespan(std::vector<double> pieces, int heads, int places = SMS) {
   std::sort(pieces.begin(), pieces.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
   double last = 0.0;
   for (double c : pieces)
     for (int h = 0; h < heads; ++h) {
       double begin = 0.0;
-      if ((int)ends.size() == SMS) {
+      if ((int)ends.size() == places) {
         begin = ends.top();
         ends.pop();
       }
@@ -47,6 +47,11 @@ struct Times {
 };
 constexpr Times TIMES[2] = {{5.0, 2.0, 5.0, 1.5e-4}, {3.0, 1.2, 3.0, 0.7e-4}};
 constexpr double LONE = 0.95, TURNS = 0.5;
+// Short items: with one block of rows to a CTA and two CTAs to an SM the start and end of one hide behind the other's tiles, but each block
+// streams its own keys, and the ring holds two tiles instead of six.  With 64 dimensions (heads in brackets), two blocks and
+// one: 32 documents of 77 tokens (30) 30.9 and 18.1 us, 32 of 156 42.6 and 38.4, 16 of 300 45.5 and 33.8, 9 of 1000 92.5 and
+// 86.9, 5 of 2000, 16 tiles, 153.9 and 153.1; one of 4096 (9) 33.0 and 36.1, of 17,776 (30) 1788 and 1850.
+constexpr int64_t SHORT_TILES = 16;
 constexpr double BACK_START = 5.0;  // of a backward CTA, in tiles
 
 static dit_status make_plan(const int64_t* queries, const int64_t* keys, const int64_t* begins, const int64_t* prefix,
@@ -92,15 +97,31 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   const int cols = BACK_COLS, rt = rows_per_tile(group), pd = padded_dim(dim);
   const Times& time = TIMES[pd > 64];
   std::vector<Costed> lists[DIT_ATTENTION_LISTS];
-  // forward: two row blocks to an item.  The second one costs about as much again less what its MMAs hide.
-  std::vector<double> costs;
-  for (size_t i = 0; i < docs.size(); ++i)
-    for (int64_t r = 0; r < docs[i].queries; r += 2 * rt) {
-      const int64_t last = std::min<int64_t>(docs[i].queries, r + 2 * rt) - 1;
-      const int64_t n = (seen_end(docs[i], frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
-      const double each = last - r >= rt ? 1.0 : LONE;
-      lists[FORWARD].push_back({Item{docs[i], (int32_t)r, 0, (int32_t)n, -1, 0, {}}, time.start + each * (double)n});
-    }
+  // forward: `blocks` row blocks to an item, an item to a head of keys
+  std::vector<Costed>& items = lists[FORWARD];
+  auto list_items = [&](int blocks) {
+    items.clear();
+    for (const Doc& d : docs)
+      for (int64_t r = 0; r < d.queries; r += blocks * rt) {
+        const int64_t last = std::min<int64_t>(d.queries, r + blocks * rt) - 1;
+        const int64_t n = (seen_end(d, frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
+        const double each = last - r >= rt ? 1.0 : LONE;
+        items.push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, 0, {}}, time.start + each * (double)n});
+      }
+  };
+  auto ends = [&](int places) {
+    std::vector<double> all;
+    for (const Costed& c : items) all.push_back(c.cost);
+    return makespan(all, kv_heads, places);
+  };
+  bool brief = pd == 64;
+  for (const Doc& d : docs) brief = brief && (d.queries == 0 || seen_end(d, frame, d.queries - 1) <= SHORT_TILES * FORWARD_COLS);
+  double apart = HUGE_VAL;  // the end with one block to an item
+  if (brief) {
+    list_items(1);
+    if ((int64_t)items.size() * kv_heads < 8 * SMS) apart = ends(2 * SMS);
+  }
+  list_items(2);
   // Few items: the keys of some are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
   // brings the end of the last CTA forward most.  Which items: those that are left when zero to three rounds of the SMs have whole ones,
   // since what is cut has to be joined.  Lone blocks of rows first, whose halves work at a piece together, then the longest.  With
@@ -110,7 +131,6 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     return even ? n * k / pieces : std::min(n, k * len);
   };
   auto lone = [&](const Item& it) { return it.row0 + rt >= it.doc.queries; };
-  std::vector<Costed>& items = lists[FORWARD];
   const int64_t ctas = (int64_t)items.size() * kv_heads;
   if (ctas && ctas < 4 * SMS) {
     std::stable_sort(items.begin(), items.end(), [&](const Costed& a, const Costed& b) {
@@ -118,11 +138,8 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     });
     std::vector<double> now;
     int64_t most = 0;
-    for (const Costed& c : items) {
-      now.push_back(c.cost);
-      most = std::max<int64_t>(most, c.item.end);
-    }
-    double best = makespan(now, kv_heads);
+    for (const Costed& c : items) most = std::max<int64_t>(most, c.item.end);
+    double best = std::min(apart, ends(SMS));
     int64_t longest = 0, cuts = 0;  // tiles of a piece, 0: items stay whole; the items that may be cut
     bool evenly = true;
     for (int rounds = 0; rounds < 4; ++rounds) {
@@ -183,6 +200,11 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       }
     }
   }
+  plan->row_blocks = 2;
+  if (brief && lists[JOIN].empty()) {
+    plan->row_blocks = 1;
+    list_items(1);
+  }
   if (training)
     for (size_t i = 0; i < docs.size(); ++i) {
       const Doc& d = docs[i];
@@ -236,7 +258,8 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
 bool plan_ok(const dit_attention_plan_t* p) {
   if (!p || p->documents < 0 || p->heads < 1 || p->heads > MAX_HEADS || p->kv_heads < 1 || p->heads % p->kv_heads || p->heads / p->kv_heads > MAX_GROUP ||
       p->dim < 8 || p->dim > MAX_DIM || p->dim % 8 || p->frame < 0 || p->q_rows < 0 || p->q_rows > MAX_ROWS || p->k_rows < 0 || p->k_rows > MAX_ROWS ||
-      p->padded_rows < p->q_rows || p->padded_rows % TILE || p->slots < 0)
+      p->padded_rows < p->q_rows || p->padded_rows % TILE || p->slots < 0 ||
+      (p->row_blocks != 2 && (p->row_blocks != 1 || p->dim > 64 || p->items[JOIN])))
     return false;
   for (int l = 0; l < DIT_ATTENTION_LISTS; ++l)
     if (p->items[l] < 0 || (int64_t)p->items[l] * p->heads > MAX_ROWS || p->buckets[l] < 0 || p->buckets[l] > DIT_ATTENTION_BUCKETS || (p->items[l] && !p->buckets[l])) return false;

@@ -86,6 +86,8 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     assert plan.info.padded_rows == at * 128
     fwd, joins, gq, gk = ([(places[tuple(item[:6])], *item[6:]) for item in items] for items in found)
     cols, rt, back = 128, 128 // (heads // kv_heads), 64
+    wide = plan.info.row_blocks * rt
+    assert plan.info.row_blocks in ((1, 2) if dim <= 64 and not joins else (2,))
     assert plan.q_rows == sum(queries)
     for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
         at = 0
@@ -99,7 +101,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     rows = [torch.zeros(n, dtype=torch.int32) for n in queries]
     slots = {}
     for doc, row0, begin, end, slot, turns in fwd:
-        part = slice(row0, min(queries[doc], row0 + 2 * rt))
+        part = slice(row0, min(queries[doc], row0 + wide))
         met[doc][part, begin * cols:end * cols] += 1
         assert end * cols < keys[doc] + cols
         if slot < 0:
@@ -165,6 +167,12 @@ def test_items_that_fill_whole_rounds_stay_whole(dit):
     assert all(item[10] == 1 for item in fwd if item[9] >= 0)
 
 
+@pytest.mark.parametrize("keys,dim,blocks", [(2048, 64, 1), (2049, 64, 2), (2048, 72, 2), (1, 8, 1)])
+def test_short_items_have_one_block_of_rows(dit, keys, dim, blocks):
+    plan = check_plan(dit, [129] * 40, [keys] * 40, 30, 30, dim, 0, 0)
+    assert plan.info.row_blocks == blocks and plan.info.items[0] == 40 * (2 if blocks == 1 else 1) and plan.info.items[1] == 0
+
+
 def test_plans_of_random_batches(dit):
     rng = random.Random(0)
     for _ in range(25):
@@ -225,6 +233,10 @@ def test_attention_refusals(dit):
         return f(ctypes.byref(p) if p is not None else None, table, *(ctypes.byref(v[n]) if v[n] is not None else None for n in names), scale, saved, saved_bytes,
                  scratch, scratch_bytes, ws, ws_bytes, None)
     for back in (False, True):
+        for blocks in (0, 1, 3):  # one block of rows is for 64 dimensions at most, and for items that are whole
+            p = type(plan.info).from_buffer_copy(plan.info)
+            p.row_blocks, p.dim = blocks, 128 if blocks == 1 else 64
+            assert call(back, p=p) == INVALID
         assert call(back, p=None) == INVALID
         assert call(back, table=None) == INVALID
         assert call(back, table=A + 4) == ALIGNMENT

@@ -129,6 +129,31 @@ def test_longer_than_every_ring(dit, dim):
     b.check()
 
 
+@pytest.mark.parametrize("frame,prefix", [(0, 0), (1, 0), (70, 45)])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(60, 60, 64), (12, 4, 128), (120, 60, 40)])
+def test_two_blocks_of_rows_to_a_cta(dit, heads, kv_heads, dim, frame, prefix):
+    """Short documents beside a long one, in items that stay whole: last blocks that are lone or not full."""
+    lengths = [300, 1, 129, 256, 77] + ([2200] if dim <= 64 else [257] * 60)
+    b = Batch(dit, lengths, heads, kv_heads, dim, frame, prefix, train=False)
+    assert b.plan.info.row_blocks == 2 and b.plan.info.items[1] == 0
+    b.forward()
+    b.check()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(3, 3, 64), (6, 2, 64), (14, 1, 40), (128, 1, 8)])
+def test_one_block_of_rows_to_a_cta(dit, heads, kv_heads, dim):
+    """Short documents: no key, one, tiles of all but one and of one more, as many as the ring has and some more."""
+    queries = [5, 1, 127, 128, 129, 300, 0, 2, 260]
+    keys = [0, 1, 127, 256, 129, 1290, 7, 2048, 260]
+    for frame, prefix in ((0, 0), (1, 0), (50, 33)):
+        b = Batch(dit, queries * 8, heads, kv_heads, dim, frame, prefix, kv_lengths=keys * 8, train=frame == 50)
+        assert b.plan.info.row_blocks == 1
+        b.forward()
+        if frame == 50:
+            b.backward()
+        b.check()
+
+
 @pytest.mark.parametrize("c", [
     # queries, keys, heads, kv_heads, dim, frame, prefix, room
     ([1, 1, 1, 1], [700, 1, 65, 3000], 16, 4, 128, 1, 0, 3100),
@@ -428,6 +453,20 @@ def test_gradients_match_differences(dit):
             args[[i for i, t in enumerate(leaves) if t is leaf][0]][at] += sign * step
             moved.append(loss(*args))
         assert abs(float((moved[0] - moved[1]) / (2 * step) - leaf.grad[at])) < 1e-6
+
+
+@pytest.mark.parametrize("keys,heads,dim", [(300, 2, 64), (5000, 2, 64), (300, 8, 128), (5000, 2, 128), (2200, 60, 64)])
+def test_bounded_wait_in_every_form_of_the_forward_pass(dit, monkeypatch, keys, heads, dim):
+    """One and two blocks of rows to a CTA, pieces, halves that take tiles in turn."""
+    b = Batch(dit, [300, 64], heads, heads, dim, kv_lengths=[keys, 64], train=False)
+    monkeypatch.setenv("DIT6_TEST_STALL_PRODUCER", "1")
+    b.forward()
+    assert dit.device_status(b.ws) & (1 << 5)
+    dit.clear_device_status(b.ws)
+    monkeypatch.delenv("DIT6_TEST_STALL_PRODUCER")
+    b.out[:364] = 0
+    b.forward()
+    b.check()
 
 
 def test_bounded_wait_reports_timeout_and_recovers(dit, monkeypatch):
