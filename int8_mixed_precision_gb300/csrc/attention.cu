@@ -1,11 +1,10 @@
 // Attention, forward: o = softmax(scale q k^T) v over the keys that each query sees.
 //
-// One pass over the keys with the running maximum and sum of the softmax.  A CTA holds two blocks of 128 rows (a row is
-// a query and a head of the group that shares the keys) and streams keys and values through shared memory by
-// TMA.  S = Q K^T goes to tensor memory, a thread to each row turns it into P (in bf16, back to tensor memory as
-// the A operand of the next product) and O += P V stays there.  While the warps of one block work at their softmax
-// the tensor cores have the other block's products, and S of the next tile is made as soon as the present one is in
-// registers.
+// One pass over the keys with the running maximum and sum of the softmax.  A block is 128 rows (a row is a query and a head of
+// the group that shares the keys); keys and values stream through shared memory by TMA.  S = Q K^T goes to tensor
+// memory, a thread to each row turns it into P (in bf16, back to tensor memory as the A operand of the next product) and
+// O += P V stays there.  While the warps of one block work at their softmax the tensor cores have another block's products,
+// and S of the next tile is made as soon as the present one is in registers.
 //
 // The running maximum moves only when it grows by more than 2^GROWTH: until then P is larger than 1 by at
 // most that factor, which neither bf16 nor fp32 sums mind, and O need not be rescaled.  The final division takes the
@@ -14,13 +13,20 @@
 // P is rounded to bf16 (an operand of the bf16 tensor pipe), 2^-8 of each weight at most; the sum of the weights is of the unrounded
 // ones.  Scores are scaled inside the exponent's multiply-add, in base 2.
 //
-// Few rows.  Where the keys of an item are cut into pieces and it has one block of rows alone, the CTA's halves take its tiles
+// Two blocks.  With 64 dimensions a CTA has two blocks, which share the keys and a ring of six tiles, and the SM to itself; with
+// 128, and where no item has many tiles, it has one, and an SM two CTAs: the start and end of one hide behind the other's tiles.
+// With 128 P lies over S, so the next S waits for the product with V, and a ring of one tile loses nothing beside that: 17,776
+// rows of 30 heads take 3.35 ms, two blocks to a CTA took 3.47; 5 documents of 2000 (16 heads) 150 us and 167.
+//
+// Few rows.  Where the keys of an item are cut into pieces and a CTA of two blocks has one alone, its halves take its tiles
 // in turn, two blocks of the same rows: a tile's chain of waits is then half as long for two.
 //
-// Short items.  Where no item has many tiles and there are 64 dimensions, a CTA has one block of rows and an SM two CTAs.
+// Bound by the row warps' chain of a tile: with 64 dimensions 1740 cycles for two blocks, 1024 of them exponentials and as many
+// MMAs beside those.  17,776 rows of 30 heads: 1.77 ms, 1370 TFLOP/s, with 128 dimensions 3.35 ms, 1450; 4096 rows of 9 heads 33
+// us and 59.
 //
 // Warps: 0 loads, 1 issues S, 2 and 3 issue O += P V of a block each, 4 to 7 relay the MMAs' completion to the rows' warps, which are
-// 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  With one block of rows 3 relays, and
+// 8 to 11 and 12 to 15, a thread to each row, and take over most of the others' registers.  With one block 3 relays, and
 // 4 to 7 have the rows.  Every wait on memory is bounded.
 #include <float.h>
 #include <limits.h>
@@ -38,7 +44,7 @@ using namespace lora;
 constexpr float GROWTH = 8.f;
 constexpr int FWD_STAGES = 6;  // most
 
-// BLOCKS: blocks of rows to a CTA.  One, and two CTAs to an SM, for short items.
+// BLOCKS: blocks of rows to a CTA.  One, and two CTAs to an SM, with 128 dimensions and for short items.
 template <int PD, int BLOCKS>
 struct Fwd {
   using Regs = Registers<2 * BLOCKS, 128, 48, 208, BLOCKS>;
@@ -47,7 +53,7 @@ struct Fwd {
   static constexpr bool OVER_S = PD > 64;  // P takes the place of S
   static constexpr int Q_CHUNK = TILE * 128, Q_BYTES = CHUNKS * Q_CHUNK;
   static constexpr int KV_CHUNK = COLS * 128, KV_BYTES = CHUNKS * KV_CHUNK;
-  static constexpr int STAGES = PD == 64 && BLOCKS == 2 ? 6 : 2;
+  static constexpr int STAGES = BLOCKS == 2 ? 6 : PD == 64 ? 2 : 1;
   static constexpr int RING = BLOCKS * Q_BYTES;
   static constexpr int CONTROL = RING + 2 * STAGES * KV_BYTES;
   static constexpr int SMEM = CONTROL + 1024 + 1024;
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(Fwd<PD, BLOCKS>::Regs::THREADS, 3 - BLOCKS)
   const int row0 = w.row0;
   const int n = uniform(w.ok ? w.end - w.begin : 0);  // tiles
   // Two blocks of rows, one, or one whose tiles both halves of the CTA take in turn, as two blocks of the same rows.
-  const bool turns = SPLIT && w.ok && w.turns && w.slot >= 0;
+  const bool turns = SPLIT && BLOCKS == 2 && w.ok && w.turns && w.slot >= 0;
   const int blocks = BLOCKS == 2 && w.ok && (turns || row0 + p.rows < d.queries) ? 2 : 1, step = turns ? 2 : 1;
   auto first_of = [&](int t) { return turns ? t : 0; };
   auto tiles_of = [&](int t) { return t < blocks ? (n - first_of(t) + step - 1) / step : 0; };
@@ -423,7 +429,8 @@ __global__ void __launch_bounds__(Fwd<PD, BLOCKS>::Regs::THREADS, 3 - BLOCKS)
 
 // The pieces of a split item, joined: o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i in the pieces' order.  Bound by latency: a lane
 // holds the maximum and the sum of every 32nd piece, and those and the first pieces' values are asked for at once.  Two rows
-// of a head to a warp, or, where an item has few rows, several warps to a row, each with a share of its pieces.
+// of a head to a warp, or, where an item has few rows, several warps to a row, each with a share of its pieces.  4 us for 64 rows of
+// 18 pieces of 128 dimensions behind single tokens; 81,000 partial rows of 64, 22 MB, 13 us.
 constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2 * JOIN_WARPS;  // of a CTA
 template <int PD>
 using JoinVec = typename std::conditional<PD == 64, float2, float4>::type;  // a lane's dimensions
@@ -602,7 +609,8 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
   a.rows = rows_per_tile(a.group);
   a.stall = test_stall();
   if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
+  const bool split = plan->items[JOIN] > 0;
+  if (plan->dim > 64) return split ? launch<128, true, 1>(a, hq, hk, hv, stream) : launch<128, false, 1>(a, hq, hk, hv, stream);
   if (plan->row_blocks == 1) return launch<64, false, 1>(a, hq, hk, hv, stream);
-  if (plan->items[JOIN] > 0) return plan->dim <= 64 ? launch<64, true, 2>(a, hq, hk, hv, stream) : launch<128, true, 2>(a, hq, hk, hv, stream);
-  return plan->dim <= 64 ? launch<64, false, 2>(a, hq, hk, hv, stream) : launch<128, false, 2>(a, hq, hk, hv, stream);
+  return split ? launch<64, true, 2>(a, hq, hk, hv, stream) : launch<64, false, 2>(a, hq, hk, hv, stream);
 }

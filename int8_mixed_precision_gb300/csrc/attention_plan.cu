@@ -21,7 +21,7 @@ struct Costed {
 };
 
 // The end of the last of `pieces` on `places` processors that take them in order.
-static double makespan(std::vector<double> pieces, int heads, int places = SMS) {
+static double makespan(std::vector<double> pieces, int heads, int places) {
   std::sort(pieces.begin(), pieces.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
   double last = 0.0;
@@ -116,12 +116,14 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
   };
   bool brief = pd == 64;
   for (const Doc& d : docs) brief = brief && (d.queries == 0 || seen_end(d, frame, d.queries - 1) <= SHORT_TILES * FORWARD_COLS);
-  double apart = HUGE_VAL;  // the end with one block to an item
+  double apart = HUGE_VAL;  // the end with one block to an item, where there may be either
   if (brief) {
     list_items(1);
     if ((int64_t)items.size() * kv_heads < 8 * SMS) apart = ends(2 * SMS);
   }
-  list_items(2);
+  plan->row_blocks = pd == 64 ? 2 : 1;
+  list_items(plan->row_blocks);
+  const int wide = plan->row_blocks * rt, places = plan->row_blocks == 2 ? SMS : 2 * SMS;  // queries of an item, CTAs at a time
   // Few items: the keys of some are cut into pieces of up to `len` tiles, of one size (even) or all but the last of `len`, whichever
   // brings the end of the last CTA forward most.  Which items: those that are left when zero to three rounds of the SMs have whole ones,
   // since what is cut has to be joined.  Lone blocks of rows first, whose halves work at a piece together, then the longest.  With
@@ -130,25 +132,25 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
     const int64_t pieces = (n + len - 1) / len;
     return even ? n * k / pieces : std::min(n, k * len);
   };
-  auto lone = [&](const Item& it) { return it.row0 + rt >= it.doc.queries; };
+  auto lone = [&](const Item& it) { return wide > rt && it.row0 + rt >= it.doc.queries; };
   const int64_t ctas = (int64_t)items.size() * kv_heads;
-  if (ctas && ctas < 4 * SMS) {
+  if (ctas && ctas < 4 * places) {
     std::stable_sort(items.begin(), items.end(), [&](const Costed& a, const Costed& b) {
       return lone(a.item) != lone(b.item) ? lone(a.item) : a.item.end > b.item.end;
     });
     std::vector<double> now;
     int64_t most = 0;
     for (const Costed& c : items) most = std::max<int64_t>(most, c.item.end);
-    double best = std::min(apart, ends(SMS));
+    double best = std::min(apart, ends(places));
     int64_t longest = 0, cuts = 0;  // tiles of a piece, 0: items stay whole; the items that may be cut
     bool evenly = true;
     for (int rounds = 0; rounds < 4; ++rounds) {
-      const int64_t may = (int64_t)items.size() - rounds * SMS / kv_heads;
+      const int64_t may = (int64_t)items.size() - rounds * places / kv_heads;
       if (may <= 0) break;
       for (int64_t len = most; len >= 2; len = len > 24 ? len * 15 / 16 : len - 1) {
         int64_t total = 0;
         for (int64_t i = 0; i < may; ++i) total += std::max<int64_t>((items[(size_t)i].item.end + len - 1) / len, 1);
-        if (total * kv_heads > 6 * SMS) break;
+        if (total * kv_heads > 6 * places) break;
         for (int even = 0; even < 2; ++even) {
           now.clear();
           int64_t joined = 0;
@@ -160,10 +162,10 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
               now.push_back(c.cost);
               continue;
             }
-            joined += std::min<int64_t>(2 * rt, c.item.doc.queries - c.item.row0) * pieces * (lone(c.item) ? 2 : 1);
+            joined += std::min<int64_t>(wide, c.item.doc.queries - c.item.row0) * pieces * (lone(c.item) ? 2 : 1);
             for (int64_t k = 0; k < pieces; ++k) now.push_back(time.start + time.split_end + each * (double)(cut(n, len, even, k + 1) - cut(n, len, even, k)));
           }
-          const double t = makespan(now, kv_heads) + time.join + time.join_row * (double)joined * heads;
+          const double t = makespan(now, kv_heads, places) + time.join + time.join_row * (double)joined * heads;
           if (t < best) {
             best = t;
             longest = len;
@@ -184,7 +186,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
           continue;
         }
         const Doc& d = c.item.doc;
-        const int32_t rows = (int32_t)std::min<int64_t>(2 * rt, d.queries - c.item.row0);
+        const int32_t rows = (int32_t)std::min<int64_t>(wide, d.queries - c.item.row0);
         const bool turns = lone(c.item);
         const double each = turns ? TURNS : 1.0;
         lists[JOIN].push_back({Item{d, c.item.row0, plan->slots, (int32_t)(turns ? 2 * pieces : pieces), rows, 0, {}}, 1.0});
@@ -200,7 +202,6 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       }
     }
   }
-  plan->row_blocks = 2;
   if (brief && lists[JOIN].empty()) {
     plan->row_blocks = 1;
     list_items(1);
@@ -259,7 +260,7 @@ bool plan_ok(const dit_attention_plan_t* p) {
   if (!p || p->documents < 0 || p->heads < 1 || p->heads > MAX_HEADS || p->kv_heads < 1 || p->heads % p->kv_heads || p->heads / p->kv_heads > MAX_GROUP ||
       p->dim < 8 || p->dim > MAX_DIM || p->dim % 8 || p->frame < 0 || p->q_rows < 0 || p->q_rows > MAX_ROWS || p->k_rows < 0 || p->k_rows > MAX_ROWS ||
       p->padded_rows < p->q_rows || p->padded_rows % TILE || p->slots < 0 ||
-      (p->row_blocks != 2 && (p->row_blocks != 1 || p->dim > 64 || p->items[JOIN])))
+      (p->dim > 64 ? p->row_blocks != 1 : p->row_blocks != 2 && (p->row_blocks != 1 || p->items[JOIN])))
     return false;
   for (int l = 0; l < DIT_ATTENTION_LISTS; ++l)
     if (p->items[l] < 0 || (int64_t)p->items[l] * p->heads > MAX_ROWS || p->buckets[l] < 0 || p->buckets[l] > DIT_ATTENTION_BUCKETS || (p->items[l] && !p->buckets[l])) return false;

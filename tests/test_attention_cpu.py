@@ -87,7 +87,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
     fwd, joins, gq, gk = ([(places[tuple(item[:6])], *item[6:]) for item in items] for items in found)
     cols, rt, back = 128, 128 // (heads // kv_heads), 64
     wide = plan.info.row_blocks * rt
-    assert plan.info.row_blocks in ((1, 2) if dim <= 64 and not joins else (2,))
+    assert plan.info.row_blocks in ((1,) if dim > 64 else (2,) if joins else (1, 2))
     assert plan.q_rows == sum(queries)
     for items, found in zip((fwd, joins, gq, gk), buckets):  # the buckets are the list, in order
         at = 0
@@ -109,7 +109,7 @@ def check_plan(dit, queries, keys, heads, kv_heads, dim, frame, prefix):
         else:
             n = part.stop - part.start
             # the halves of a CTA that take a lone block's tiles in turn leave a partial result each
-            assert turns == (queries[doc] - row0 <= rt)
+            assert turns == (dim <= 64 and queries[doc] - row0 <= rt)
             slots[slot] = (doc, row0, n, begin, end, 2 if turns else 1)
             assert slot + n * (2 if turns else 1) <= plan.info.slots
     used = torch.zeros(plan.info.slots, dtype=torch.int32)
@@ -167,8 +167,8 @@ def test_items_that_fill_whole_rounds_stay_whole(dit):
     assert all(item[10] == 1 for item in fwd if item[9] >= 0)
 
 
-@pytest.mark.parametrize("keys,dim,blocks", [(2048, 64, 1), (2049, 64, 2), (2048, 72, 2), (1, 8, 1)])
-def test_short_items_have_one_block_of_rows(dit, keys, dim, blocks):
+@pytest.mark.parametrize("keys,dim,blocks", [(2048, 64, 1), (2049, 64, 2), (5000, 72, 1), (1, 8, 1)])
+def test_items_of_one_block_of_rows(dit, keys, dim, blocks):
     plan = check_plan(dit, [129] * 40, [keys] * 40, 30, 30, dim, 0, 0)
     assert plan.info.row_blocks == blocks and plan.info.items[0] == 40 * (2 if blocks == 1 else 1) and plan.info.items[1] == 0
 
@@ -235,7 +235,7 @@ def test_attention_refusals(dit):
     for back in (False, True):
         for blocks in (0, 1, 3):  # one block of rows is for 64 dimensions at most, and for items that are whole
             p = type(plan.info).from_buffer_copy(plan.info)
-            p.row_blocks, p.dim = blocks, 128 if blocks == 1 else 64
+            p.row_blocks, p.items[1] = blocks, int(blocks == 1)
             assert call(back, p=p) == INVALID
         assert call(back, p=None) == INVALID
         assert call(back, table=None) == INVALID
