@@ -20,6 +20,11 @@
 // lets it launch only after its own wait, so that the inputs, lse and delta are then complete and in global memory; and
 // it waits itself before it ends, so for what follows on the stream the order is that of plain launches.
 //
+// Bound by the row warps' chain of two tiles of 64 columns, 1515 cycles where queries stay and 1800 where keys do (whose columns'
+// lse and delta come from shared memory), for MMAs of 1024 and 1280.  17,776 rows of 30 heads of 64: 2.66 and 3.14 ms apart, 6.1 ms
+// for the whole backward pass, 995 TFLOP/s of the formulas' ten operations; 4096 rows of 9 heads of 128: 215 us, 897.  With one
+// stream in each the pass took 7.6 ms.
+//
 // Warps: 0 loads; 1 and 6 issue S and T of a stream each; 2 issues A, 3 B; 4, 5 and 7 relay the MMAs' completion; the others hold
 // the rows and take over most of the first ones' registers.  Every wait on memory is bounded.
 #include <float.h>
@@ -77,7 +82,7 @@ struct BackArgs {
   int stall;
 };
 
-// delta of 128 queries of a head, sixteen bytes to a lane.
+// delta of 128 queries of a head, sixteen bytes to a lane.  Bound by memory: 17,776 rows of 30 heads of 64 take 40 us, 3.4 TB/s.
 __global__ void __launch_bounds__(256) k_attention_delta(const __grid_constant__ BackArgs p) {
   pdl_launch_dependents();
   pdl_wait();

@@ -165,7 +165,12 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
             joined += std::min<int64_t>(wide, c.item.doc.queries - c.item.row0) * pieces * (lone(c.item) ? 2 : 1);
             for (int64_t k = 0; k < pieces; ++k) now.push_back(time.start + time.split_end + each * (double)(cut(n, len, even, k + 1) - cut(n, len, even, k)));
           }
-          const double t = makespan(now, kv_heads, places) + time.join + time.join_row * (double)joined * heads;
+          const double join = time.join + time.join_row * (double)joined * heads;
+          // no order ends before the work shared evenly, nor before the longest piece
+          double sum = 0.0, top = 0.0;
+          for (double c : now) sum += c, top = std::max(top, c);
+          if (std::max(sum * kv_heads / places, top) + join >= best) continue;
+          const double t = makespan(now, kv_heads, places) + join;
           if (t < best) {
             best = t;
             longest = len;

