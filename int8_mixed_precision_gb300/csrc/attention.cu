@@ -61,6 +61,10 @@ struct Fwd {
   static constexpr uint32_t S = 0, P = OVER_S ? S : BLOCKS * COLS, P_STEP = OVER_S ? COLS : COLS / 2, O = P + BLOCKS * P_STEP;
   static constexpr uint32_t COLUMNS = BLOCKS == 2 ? 512 : 256;
   static_assert(O + BLOCKS * PD <= COLUMNS && (3 - BLOCKS) * (SMEM + 1024) <= 228 * 1024, "");
+  // A kernel starts early and takes its tensor memory before it waits for the one before, whose last CTAs may not have taken theirs: CTAs
+  // that fit an SM together must find columns together, or they wait for one another.  The library's kernels with 512 columns
+  // leave less than 64 KB of shared memory or no registers, and those with 256 need a third of an SM's or more.
+  static_assert(COLUMNS == 512 ? Regs::THREADS * Regs::LAUNCHED == 65536 : SMEM >= 64 * 1024 && 3 * (SMEM + 1024) > 228 * 1024, "");
 };
 
 struct FwdControl {

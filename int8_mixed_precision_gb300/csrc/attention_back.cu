@@ -57,7 +57,7 @@ struct Back {
   // tensor memory: S and T of each stream, p and dS of each stream, A, B
   static constexpr uint32_t S = 0, T = COLS, S_STEP = 2 * COLS, P = STREAMS * S_STEP, DS = P + COLS / 2, P_STEP = COLS, A = P + STREAMS * P_STEP, B = A + PD;
   static constexpr int MMA_WARPS = STREAMS + 1 + KEYS, ROW_WARPS = 8 / STREAMS, MEET = 32 + 32 * ROW_WARPS;
-  static_assert((KEYS ? B : A) + PD <= 512 && SMEM <= 227 * 1024, "");
+  static_assert((KEYS ? B : A) + PD <= 512 && SMEM <= 227 * 1024 && Regs::THREADS * Regs::LAUNCHED == 65536, "");
 };
 
 struct BackControl {
