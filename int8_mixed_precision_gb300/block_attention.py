@@ -319,10 +319,13 @@ class AttentionPlan:
         self.info = _Plan()
         args = (*(None if a is None else a.data_ptr() for a in arr), n, int(frame), int(heads), kv_heads, int(dim), int(bool(training)),
                 ctypes.byref(self.info))
-        _check(lib().dit_attention_plan(*args, None, 0), "dit_attention_plan")
-        host = torch.empty(self.info.table_ints, dtype=_I32)
-        _check(lib().dit_attention_plan(*args, host.data_ptr(), host.numel()), "dit_attention_plan")
-        self._table = host.to(device)
+        host = torch.empty(1 << 14, dtype=_I32)  # most tables fit: a plan is made once, not a first time for its size
+        st = lib().dit_attention_plan(*args, host.data_ptr(), host.numel())
+        if st and self.info.table_ints > host.numel():
+            host = torch.empty(self.info.table_ints, dtype=_I32)
+            st = lib().dit_attention_plan(*args, host.data_ptr(), host.numel())
+        _check(st, "dit_attention_plan")
+        self._table = host[:self.info.table_ints].clone().to(device)
         self.q_rows, self.k_rows, self.training = self.info.q_rows, self.info.k_rows, bool(training)
         self.heads, self.kv_heads, self.dim = int(heads), kv_heads, int(dim)
         self._info_p, self._table_p = ctypes.c_void_p(ctypes.addressof(self.info)), ctypes.c_void_p(self._table.data_ptr())

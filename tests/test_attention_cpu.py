@@ -173,6 +173,13 @@ def test_items_of_one_block_of_rows(dit, keys, dim, blocks):
     assert plan.info.row_blocks == blocks and plan.info.items[0] == 40 * (2 if blocks == 1 else 1) and plan.info.items[1] == 0
 
 
+def test_tables_of_any_size(dit):
+    """No entry, and more of them than a first buffer holds."""
+    assert dit.AttentionPlan([0, 0], 2, 64, device="cpu").table.numel() == 0
+    plan = check_plan(dit, [3] * 700, [3] * 700, 2, 2, 64, 1, 0)
+    assert plan.table.numel() == plan.info.table_ints == 16 * 3 * 700
+
+
 def test_plans_of_random_batches(dit):
     rng = random.Random(0)
     for _ in range(25):
