@@ -105,7 +105,7 @@ static dit_status make_plan(const int64_t* queries, const int64_t* keys, const i
       for (int64_t r = 0; r < d.queries; r += blocks * rt) {
         const int64_t last = std::min<int64_t>(d.queries, r + blocks * rt) - 1;
         const int64_t n = (seen_end(d, frame, last) + FORWARD_COLS - 1) / FORWARD_COLS;
-        const double each = last - r >= rt ? 1.0 : LONE;
+        const double each = blocks == 1 || last - r >= rt ? 1.0 : LONE;
         items.push_back({Item{d, (int32_t)r, 0, (int32_t)n, -1, 0, {}}, time.start + each * (double)n});
       }
   };

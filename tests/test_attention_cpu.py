@@ -240,10 +240,6 @@ def test_attention_refusals(dit):
         return f(ctypes.byref(p) if p is not None else None, table, *(ctypes.byref(v[n]) if v[n] is not None else None for n in names), scale, saved, saved_bytes,
                  scratch, scratch_bytes, ws, ws_bytes, None)
     for back in (False, True):
-        for blocks in (0, 1, 3):  # one block of rows is for 64 dimensions at most, and for items that are whole
-            p = type(plan.info).from_buffer_copy(plan.info)
-            p.row_blocks, p.items[1] = blocks, int(blocks == 1)
-            assert call(back, p=p) == INVALID
         assert call(back, p=None) == INVALID
         assert call(back, table=None) == INVALID
         assert call(back, table=A + 4) == ALIGNMENT
@@ -274,6 +270,21 @@ def test_attention_refusals(dit):
         bad = _Plan.from_buffer_copy(plan.info)
         setattr(bad, field, value)
         assert call(p=bad) == INVALID, field
+
+
+@pytest.mark.parametrize("keys,dim,good", [([3000], 64, (2,)), ([300] * 400, 64, (1, 2)), ([300] * 400, 128, (1,))])
+def test_plans_have_the_blocks_of_rows_that_kernels_have(dit, keys, dim, good):
+    """Pieces of up to 64 dimensions are of two blocks, whole items of one or two, and more dimensions have one."""
+    L, A, n = dit.lib(), 1 << 20, len(keys)
+    plan = dit.AttentionPlan([3] * n, 4, dim, kv_lengths=keys, device="cpu")
+    assert (plan.info.items[1] > 0) == (n == 1) and plan.info.row_blocks in good
+    view = ctypes.byref(heads(A, 4, dim))
+    for blocks in (-1, 0, 1, 2, 3):
+        p = type(plan.info).from_buffer_copy(plan.info)
+        p.row_blocks = blocks
+        # what passes this check fails at the table's alignment
+        status = L.dit_attention(ctypes.byref(p), A + 4, view, view, view, view, 0.1, None, 0, A, 1 << 40, A, 1 << 16, None)
+        assert status == (ALIGNMENT if blocks in good else INVALID), blocks
 
 
 def test_norm_call_refusals(dit):
