@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attention_join(const __grid
   const Work w = find_work(p.table, p.plan, JOIN, p.plan.heads, p.ws);
   if (!w.ok) return;
   const int rows = w.slot, pieces = w.end, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (rows <= 0 || (int64_t)w.row0 + rows > w.doc.queries || (int64_t)w.begin + (int64_t)rows * pieces > p.plan.slots) {
+  if (rows <= 0 || pieces <= 0 || (int64_t)w.row0 + rows > w.doc.queries || (int64_t)w.begin + (int64_t)rows * pieces > p.plan.slots) {
     if (threadIdx.x == 0) raise_status(p.ws, DIT_ERR_INVALID_ARG);
     return;
   }

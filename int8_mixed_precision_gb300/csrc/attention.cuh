@@ -78,12 +78,14 @@ struct Work {
 };
 __device__ __forceinline__ bool fits(const Work& w, const dit_attention_plan_t& p, int list) {
   const Doc& d = w.doc;
+  // the CTA's own rows begin in the document, with queries' gradients at a whole tile: the statistics of all its rows are written
+  if (w.row0 < 0 || w.row0 >= (list == GRAD_KV ? d.keys : d.queries) || (list == GRAD_Q && w.row0 % TILE != 0)) return false;
   // the streamed operand's tiles lie in the document
   const int64_t cols = list == FORWARD ? FORWARD_COLS : BACK_COLS, rows = list == GRAD_KV ? d.queries : d.keys;
   if (list == FORWARD && w.slot >= 0 && p.items[JOIN] == 0) return false;  // a piece that nothing joins
-  if (list != JOIN && w.end > w.begin && (int64_t)w.end * cols >= rows + cols) return false;
+  if (w.begin < 0 || (list != JOIN && (w.end < w.begin || (w.end > w.begin && (int64_t)w.end * cols >= rows + cols)))) return false;
   return d.q0 >= 0 && d.queries >= 0 && (int64_t)d.q0 + d.queries <= p.q_rows && d.k0 >= 0 && d.keys >= 0 && (int64_t)d.k0 + d.keys <= p.k_rows &&
-         d.prefix >= 0 && d.tile0 >= 0 && (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows && w.row0 >= 0 && w.begin >= 0;
+         d.prefix >= 0 && d.tile0 >= 0 && (int64_t)d.tile0 * TILE + d.queries <= p.padded_rows;
 }
 // The work of this CTA.
 __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attention_plan_t& p, int list, int heads, void* ws) {

@@ -319,6 +319,49 @@ def test_wrong_table_entries_are_skipped(dit):
         assert not torch.equal(good, b.out)
 
 
+@pytest.mark.parametrize("row", [100, 10 ** 6, 2 ** 31 - 1])
+def test_rows_behind_the_document_are_skipped(dit, row):
+    """An entry whose own rows begin behind its document writes nothing, statistics included, and raises the status word."""
+    b = Batch(dit, [100, 60], 2, 2, 64)
+    b.forward()
+    table = b.plan.table.view(-1)[: 16 * sum(b.plan.info.items)].view(-1, 16)
+    table[:, 6] = row
+    b.saved.fill_(255)
+    b.scratch.fill_(255)
+    b.out[:] = 7.0
+    b.forward()
+    b.backward()
+    assert (b.out == 7.0).all() and (b.dq == 5.0).all() and (b.dk == 5.0).all() and (b.dv == 5.0).all()
+    assert (b.saved == 255).all() and (b.scratch == 255).all()
+    assert dit.device_status(b.ws) == 1 << 1
+
+
+def test_entries_that_no_plan_makes_are_skipped(dit):
+    """Queries' gradients that do not begin at a whole tile (their statistics would reach behind the last one), and tiles from the
+    last to the first."""
+    for row, begin, end in ((1, 0, 2), (127, 0, 2), (0, 1, 0)):
+        b = Batch(dit, [128], 2, 2, 64)
+        b.forward()
+        first, n = sum(b.plan.info.items[:2]), b.plan.info.items[2]
+        item = b.plan.table.view(-1)[16 * first: 16 * (first + n)].view(-1, 16)
+        item[:, 6], item[:, 7], item[:, 8] = row, begin, end
+        b.scratch.fill_(255)
+        b.backward()
+        assert (b.dq == 5.0).all() and (b.scratch == 255).all()
+        assert dit.device_status(b.ws) == 1 << 1
+
+
+@pytest.mark.parametrize("pieces", [0, -1])
+def test_joins_of_no_piece_are_skipped(dit, pieces):
+    b = Batch(dit, [3], 1, 1, 64, kv_lengths=[40000], train=False)
+    assert b.plan.info.items[1] == 1
+    item = b.plan.table.view(-1)[16 * b.plan.info.items[0]:].view(-1, 16)
+    item[:, 8] = pieces
+    b.forward()
+    assert (b.out == 7.0).all()
+    assert dit.device_status(b.ws) == 1 << 1
+
+
 def test_pieces_that_nothing_joins_are_skipped(dit):
     """A plan without joins has no place for partial results: an entry that names one writes nothing and raises the status word."""
     b = Batch(dit, [100, 60], 2, 2, 64, train=False)
