@@ -547,7 +547,8 @@ dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensor
  * params    : device float, rows of dim: (q_weight, q_bias, k_weight, k_bias) for the layer norm,
  *             (q_weight, k_weight) for RMS; NULL without a norm.  4-byte aligned.
  * rot       : dit_rotary_t (host struct) with the device table that dit_rotary_table lays out, or NULL: no
- *             rotation.  positions: device int32 [tokens, axes].
+ *             rotation.  positions: device int32 [tokens, axes], with the axes of the table: pairs of an axis that
+ *             rot->axes does not reach are not turned.
  * dq, dk    : device bf16, may be the views dq_out and dk_out themselves.
  * dparams   : device float, the shape of params, overwritten; NULL: not wanted.
  * scratch   : device buffer of dit_qk_norm_scratch_bytes(dim), 16-byte aligned, contents free; calls

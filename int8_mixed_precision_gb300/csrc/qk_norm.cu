@@ -178,9 +178,11 @@ __device__ __forceinline__ void fill_angles(const Args& p, float2* cs, int64_t t
     if (token0 + t < p.tokens) {
       const uint4 e = __ldg(reinterpret_cast<const uint4*>(p.table) + pair);
       const uint64_t freq = (uint64_t)e.y << 32 | e.x;
-      const int64_t pos = __ldg(p.positions + (token0 + t) * p.axes + (int)e.z);
-      const uint64_t turns = (uint64_t)pos * freq;                  // modulo a turn, of either sign
-      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);  // [-1/2, 1/2) of a turn, to 2^-25 of it
+      if (e.z < (uint32_t)p.axes) {  // an axis that the positions do not have turns nothing
+        const int64_t pos = __ldg(p.positions + (token0 + t) * p.axes + (int)e.z);
+        const uint64_t turns = (uint64_t)pos * freq;                  // modulo a turn, of either sign
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);  // [-1/2, 1/2) of a turn, to 2^-25 of it
+      }
     }
     cs[i] = make_float2(c, s);
   }

@@ -113,6 +113,33 @@ def test_far_positions(dit, far):
     run_case(dit, 40, 2, 2, 64, (16, 24, 24), "rms", True, backward=True, far=far, scale=[1.0, 0.375, 0.5])
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_axes_that_the_positions_do_not_have_turn_nothing(dit, interleaved):
+    """A table of three axes in a call with one: the pairs of the first turn, the others' positions are not looked for."""
+    import ctypes
+    from int8_mixed_precision_gb300.block_attention import _Rotary, _lay, _view
+    t, h, dim, dims = 77, 3, 64, (16, 24, 24)
+    x, positions, _, scale, new = case(t, h, 1, dim, dims, None, interleaved)
+    q, at = x[:, :h], positions[:, :1].contiguous()
+    rot = dit.Rotary(dims, dim, interleaved=interleaved)
+    info = _Rotary(rot.table.data_ptr(), sum(dims) // 2, 1, int(interleaved), 0)
+    angle = R.angles(positions, dims, 10000.0, scale)
+    angle[:, dims[0] // 2:] = 0
+    dy, ws = new(t, h, dim).to(BF16), dit.workspace()
+    out, dx = torch.empty_like(dy), torch.empty_like(dy)
+    view = lambda v, name: _view(v, t, h, dim, name, 0)  # noqa: E731
+    rest = (t, dim, 0, None, 0.0, ctypes.byref(info), at.data_ptr())
+    stream = torch.cuda.current_stream().cuda_stream
+    views = _lay(view(q, "q"), None, view(out, "q_out"), None)
+    assert dit.lib().dit_qk_norm_rope(*views, *rest, stream) == 0
+    views = _lay(view(q, "q"), None, view(dy, "dq_out"), None, view(dx, "dq"), None)
+    assert dit.lib().dit_qk_norm_rope_backward(*views, *rest, None, None, 0, ws.data_ptr(), ws.nbytes, stream) == 0
+    for got, v, sign in ((out, q, 1), (dx, dy, -1)):
+        want = R.turn(v.double(), sign * angle, interleaved)
+        bound = R.HALF * want.abs() + R.FINE * R.pair_sum(v.double(), sum(dims) // 2, interleaved) + 1e-30
+        assert ((got.double() - want).abs() <= bound).all()
+
+
 def test_no_tokens(dit):
     x = torch.empty(0, 4, 64, dtype=BF16, device="cuda")
     params = torch.ones(2, 64, device="cuda")
