@@ -540,7 +540,8 @@ dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensor
  *
  * dit_heads_t views one tensor [tokens, heads, dim]: dims are contiguous, strides are in elements.
  * ptr is 16-byte aligned and the strides multiples of 8 (DIT_ERR_ALIGNMENT); dim is a multiple of 8
- * up to 256 (DIT_ERR_UNSUPPORTED).  A stride of a single token or head is not used.
+ * up to 256 (DIT_ERR_UNSUPPORTED).  A stride of a single token or head is not used.  The heads of an output
+ * lie apart from one another (DIT_ERR_INVALID_ARG).
  *
  * q, k      : device bf16; k NULL: queries alone (then k_out, dk_out and dk are NULL too).
  * q_out, k_out: device bf16, may be the views q and k themselves; otherwise apart from what is read.
@@ -620,7 +621,7 @@ dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k,
  * q, out, dout, dq : views of [query rows, heads, dim], at least plan->q_rows rows.
  * k, v, dk, dv     : views of [key rows, kv_heads, dim], at least plan->k_rows rows.
  *                    bf16; dims contiguous, pointers 16-byte aligned, strides multiples of 8 below 2^31
- *                    elements.  Outputs are apart from everything that is read.
+ *                    elements.  Outputs are apart from everything that is read, and their heads from one another.
  * scale   : finite and > 0.
  * saved   : device buffer of plan->saved_bytes, 16-byte aligned, that the forward pass fills for
  *           the backward pass (training plans; otherwise NULL).

@@ -96,6 +96,19 @@ bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool heads_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
+  using wide = __int128;  // strides are the caller's
+  const wide t = token_stride < 0 ? -(wide)token_stride : (wide)token_stride, h = head_stride < 0 ? -(wide)head_stride : (wide)head_stride;
+  if ((tokens > 1 && t < dim) || (heads > 1 && h < dim)) return false;
+  if (tokens <= 1 || heads <= 1 || t >= (heads - 1) * h + dim || h >= (tokens - 1) * t + dim) return true;
+  for (wide i = 1; i < heads; ++i)  // a head of one token against the i-th behind it of the nearest tokens, whatever the strides' signs
+    for (wide j = i * h / t; j <= i * h / t + 1 && j < tokens; ++j) {
+      const wide gap = i * h - j * t;
+      if (gap < dim && -gap < dim) return false;
+    }
+  return true;
+}
+
 bool encode_tmap_heads(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads, uint64_t rows, uint64_t head_bytes,
                        uint64_t row_bytes, uint32_t box_heads, uint32_t box_rows) {
   encode_tiled_fn fn = get_encode_tiled();

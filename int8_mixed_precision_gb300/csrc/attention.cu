@@ -596,7 +596,7 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
   dit_status e = check_view(q, plan->heads, plan->q_rows, plan->dim, &hq);
   if (e == DIT_OK) e = check_view(k, plan->kv_heads, plan->k_rows, plan->dim, &hk);
   if (e == DIT_OK) e = check_view(v, plan->kv_heads, plan->k_rows, plan->dim, &hv);
-  if (e == DIT_OK) e = check_view(out, plan->heads, plan->q_rows, plan->dim, &ho);
+  if (e == DIT_OK) e = check_output(out, plan->heads, plan->q_rows, plan->dim, &ho);
   if (e != DIT_OK) return e;
   if (!aligned32(ws) || (reinterpret_cast<uintptr_t>(table) & 15) || (reinterpret_cast<uintptr_t>(saved) & 15) || (reinterpret_cast<uintptr_t>(scratch) & 15))
     return DIT_ERR_ALIGNMENT;

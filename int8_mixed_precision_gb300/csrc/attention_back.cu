@@ -500,9 +500,9 @@ extern "C" dit_status dit_attention_backward(const dit_attention_plan_t* plan, c
   if (e == DIT_OK) e = check_view(v, hk, plan->k_rows, dim, &in.v);
   if (e == DIT_OK) e = check_view(out, h, plan->q_rows, dim, &a.out);
   if (e == DIT_OK) e = check_view(dout, h, plan->q_rows, dim, &a.dout);
-  if (e == DIT_OK) e = check_view(dq, h, plan->q_rows, dim, &hdq);
-  if (e == DIT_OK) e = check_view(dk, hk, plan->k_rows, dim, &hdk);
-  if (e == DIT_OK) e = check_view(dv, hk, plan->k_rows, dim, &hdv);
+  if (e == DIT_OK) e = check_output(dq, h, plan->q_rows, dim, &hdq);
+  if (e == DIT_OK) e = check_output(dk, hk, plan->k_rows, dim, &hdk);
+  if (e == DIT_OK) e = check_output(dv, hk, plan->k_rows, dim, &hdv);
   if (e != DIT_OK) return e;
   if (!aligned32(ws) || (reinterpret_cast<uintptr_t>(table) & 15) || (reinterpret_cast<uintptr_t>(saved) & 15) || (reinterpret_cast<uintptr_t>(scratch) & 15))
     return DIT_ERR_ALIGNMENT;

@@ -284,6 +284,11 @@ dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, He
   return DIT_OK;
 }
 
+dit_status check_output(const dit_heads_t* v, int heads, int64_t rows, int dim, Heads* o) {
+  const dit_status e = check_view(v, heads, rows, dim, o);
+  return e == DIT_OK && !heads_apart(rows, heads, dim, o->row, o->head) ? DIT_ERR_INVALID_ARG : e;
+}
+
 bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows) {
   return encode_tmap_heads(map, t.ptr, (uint64_t)dim, (uint64_t)heads, (uint64_t)rows, (uint64_t)t.head * 2, (uint64_t)t.row * 2,
                            (uint32_t)box_heads, (uint32_t)box_rows);

@@ -499,6 +499,9 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // loads, so the consumers' bounded waits run out and the kernels report DIT_ERR_TIMEOUT.
 int test_stall();
 bool aligned32(const void* p);
+// Whether the heads [tokens][heads][dim] of a tensor with these strides (in elements) lie apart from one another, as
+// those of an output must: no two of them are nearer than dim.
+bool heads_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride);
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda needed)
 // the block-scale array of an NVFP4 operand of `rows` x `k` as a TMA source (one K stage of
 // box_blocks 128-row blocks per load)

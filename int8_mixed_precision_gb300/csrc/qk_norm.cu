@@ -451,6 +451,7 @@ static dit_status fill(Args& p, const dit_heads_t* q, const dit_heads_t* k, cons
     if (s.heads < 1 || s.heads > (1 << 20)) return DIT_ERR_INVALID_ARG;
     dit_status e = view_of(i ? k : q, s.heads, tokens, dim, &s.x);
     if (e == DIT_OK) e = view_of(i ? k_out : q_out, s.heads, tokens, dim, &s.y);
+    if (e == DIT_OK && !heads_apart(tokens, s.heads, dim, s.y.token, s.y.head)) e = DIT_ERR_INVALID_ARG;
     if (e == DIT_OK && back) e = view_of(i ? dk_out : dq_out, s.heads, tokens, dim, &s.dy);
     if (e != DIT_OK) return e;
     if (norm != DIT_NORM_NONE) {

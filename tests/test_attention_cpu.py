@@ -314,6 +314,42 @@ def test_norm_call_refusals(dit):
     assert call(False, tokens=0) == 0  # nothing to do
 
 
+def test_outputs_whose_heads_overlap_are_refused(dit):
+    """Threads would write over one another.  What passes the check of the views fails at the alignment of a buffer behind it."""
+    L, A, rng = dit.lib(), 1 << 20, random.Random(4)
+
+    def norm(back, v, n, dim, tokens):
+        x = ctypes.byref(heads(A, n, dim))
+        args = (tokens, dim, 0, None, 0.0, None, None)
+        if back:
+            return L.dit_qk_norm_rope_backward(x, None, x, None, ctypes.byref(v), None, *args, None, None, 0, A + 16, 1 << 16, None)
+        return L.dit_qk_norm_rope(x, None, ctypes.byref(v), None, *args, None)
+
+    def attend(v, n, dim, tokens, name=None):
+        plan = dit.AttentionPlan([tokens], n, dim, training=True, device="cpu")
+        views = {k: ctypes.byref(heads(A, n, dim)) for k in ("q", "k", "v", "out") + (() if name == "out" else ("dout", "dq", "dk", "dv"))}
+        views[name] = ctypes.byref(v)
+        f = L.dit_attention if name == "out" else L.dit_attention_backward
+        return f(ctypes.byref(plan.info), A + 4, *views.values(), 0.1, A, 1 << 30, A, 1 << 30, A, 1 << 16, None)
+    seen = set()
+    for _ in range(400):
+        n, tokens, dim = rng.randint(1, 5), rng.randint(1, 6), 8 * rng.randint(1, 3)
+        token, head = (8 * rng.randint(-20, 20) for _ in range(2))
+        at = sorted((t * token if tokens > 1 else 0) + (h * head if n > 1 else 0) for t in range(tokens) for h in range(n))
+        apart = all(b - a >= dim for a, b in zip(at, at[1:]))
+        seen.add(apart)
+        v = heads(A, n, dim, token, head)
+        assert norm(True, v, n, dim, tokens) == (ALIGNMENT if apart else INVALID)
+        if not apart:
+            assert norm(False, v, n, dim, tokens) == INVALID
+        if token > 0 and head > 0:  # the others are refused in any case
+            for name in ("out", "dq", "dk", "dv"):
+                assert attend(v, n, dim, tokens, name) == (ALIGNMENT if apart else INVALID)
+    assert seen == {True, False}
+    big = 1 << 62  # products of strides past 64 bits
+    assert norm(True, heads(A, 4, 64, big, -big), 4, 64, 3) == INVALID and norm(True, heads(A, 1, 64, 0, 0), 1, 64, 1) == ALIGNMENT
+
+
 def test_views_that_share_memory_are_found(dit):
     from int8_mixed_precision_gb300.block_attention import _meet
 
