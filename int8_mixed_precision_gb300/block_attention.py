@@ -107,23 +107,39 @@ def _flat(t, nbytes, what, index, dtype=None, align=4):
 
 
 def _meet(a, b, dim: int) -> bool:
-    """Whether two views share memory (columns of one buffer side by side do not; other interleavings count as shared)."""
+    """Whether two views share memory: exact for views of one pair of strides, as those of one buffer have; of other interleavings those
+    count as apart whose tokens or heads lie in runs that do not touch, or whose strides have a divisor that keeps them apart."""
     if a[4] <= b[0] or b[4] <= a[0] or a[4] == a[0] or b[4] == b[0]:
         return False
     pitch = a[1]
-    if pitch != b[1]:
-        return True
-    apart = (b[0] - a[0]) // 2
-    wide_a, wide_b = (a[3] - 1) * a[2] + dim, (b[3] - 1) * b[2] + dim
-    d = apart % pitch
-    if d >= wide_a and d + wide_b <= pitch:
-        return False
-    step = a[2] if a[3] > 1 else b[2]
-    if (a[3] == 1 or b[3] == 1 or a[2] == b[2]) and pitch % step == 0:
-        d = apart % step
-        if d >= dim and d + dim <= step:
+    if pitch == b[1]:  # the heads of a token lie in one run, repeated for each token
+        d = (b[0] - a[0]) // 2 % pitch
+        if d >= (a[3] - 1) * a[2] + dim and d + (b[3] - 1) * b[2] + dim <= pitch:
             return False
-    return True
+    return _interleave(a, b, dim)
+
+
+def _interleave(a, b, dim):
+    (row_a, head_a, heads_a), (row_b, head_b, heads_b), apart = a[1:4], b[1:4], (b[0] - a[0]) // 2
+    rows_a, rows_b = (1 + ((v[4] - v[0]) // 2 - dim - (v[3] - 1) * v[2]) // v[1] for v in (a, b))
+    # a stride that no access uses is as good as the other's
+    if rows_a == 1 or rows_b == 1:
+        row_a = row_b = max(row_a, row_b) if rows_a == rows_b else row_b if rows_a == 1 else row_a
+    if heads_a == 1 or heads_b == 1:
+        head_a = head_b = max(head_a, head_b) if heads_a == heads_b else head_b if heads_a == 1 else head_a
+    g = math.gcd(row_a, row_b, head_a, head_b)
+    if dim <= apart % g <= g - dim:
+        return False
+    # the tokens of a head lie in one run, repeated for each head
+    if head_a == head_b and (rows_a - 1) * row_a + dim <= apart % head_a <= head_a - (rows_b - 1) * row_b - dim:
+        return False
+    if row_a != row_b or head_a != head_b or row_a < dim:
+        return True
+    for i in range(1 - heads_a, heads_b):  # b's heads against a's that are i heads before, of the tokens that come nearest
+        j = -(apart + i * head_a) // row_a
+        if any(1 - rows_a <= k < rows_b and abs(apart + i * head_a + k * row_a) < dim for k in (j, j + 1)):
+            return True
+    return False
 
 
 def _apart(outputs, inputs, dim, own=()):
@@ -131,7 +147,7 @@ def _apart(outputs, inputs, dim, own=()):
     for i, (name, out) in enumerate(outputs):
         begin, end = out[0], out[4]
         for other, t in (*inputs, *outputs[:i]):
-            if begin < t[4] and t[0] < end and _meet(out, t, dim) and not ((name, other) in own and out == t):
+            if begin < t[4] and t[0] < end and not (out == t and (name, other) in own) and _meet(out, t, dim):
                 raise DitError(f"{name} overlaps {other}")
 
 

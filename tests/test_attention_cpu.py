@@ -371,6 +371,36 @@ def test_views_that_share_memory_are_found(dit):
     assert not meet(x, z) and not meet(x[:0], x)
 
 
+def test_views_that_share_no_memory_are_not_refused(dit):
+    """Against the addresses themselves: buffers whose heads lie in front of their tokens, and views of any strides in one buffer."""
+    from int8_mixed_precision_gb300.block_attention import _meet
+
+    def view(at, rows, heads, dim, row, head):  # as the calls describe a tensor
+        row, head = row if rows > 1 else heads * dim, head if heads > 1 else dim
+        return at, row, head, heads, at + 2 * ((rows - 1) * row + (heads - 1) * head + dim)
+
+    def places(at, rows, heads, dim, row, head):
+        return {at // 2 + t * row + h * head + i for t in range(rows) for h in range(heads) for i in range(dim)}
+    # [heads, 3, tokens, dim]: query, key and value of each head behind one another
+    t, h, d = 50, 6, 64
+    three = [view(2 * i * t * d, t, h, d, d, 3 * t * d) for i in range(3)]
+    assert not any(_meet(three[i], three[j], d) for i in range(3) for j in range(3) if i != j) and all(_meet(v, v, d) for v in three)
+    assert _meet(three[0], view(2 * (t - 1) * d, t, h, d, d, 3 * t * d), d)
+    rng, found = random.Random(7), {}
+    for _ in range(20000):
+        dim, row, head = 8 * rng.randint(1, 2), 8 * rng.randint(1, 24), 8 * rng.randint(1, 24)
+        same = rng.random() < 0.7
+        a = (0, rng.randint(1, 5), rng.randint(1, 5), dim, row, head)
+        b = (16 * rng.randint(0, 40), rng.randint(1, 5), rng.randint(1, 5), dim, *((row, head) if same else (8 * rng.randint(1, 24), 8 * rng.randint(1, 24))))
+        truth, got = bool(places(*a) & places(*b)), _meet(view(*a), view(*b), dim)
+        assert got == _meet(view(*b), view(*a), dim)
+        assert got or not truth, (a, b)
+        if same and row >= dim:
+            assert got == truth, (a, b)
+        found[same, truth] = found.get((same, truth), 0) + 1
+    assert len(found) == 4
+
+
 def test_host_tensors_are_refused(dit):
     x = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
     with pytest.raises(dit.DitError):

@@ -199,3 +199,34 @@ def test_example_runs(example):
     got = example.main(steps=3)
     assert got["rows"] == 122 + 41 + 80 and torch.isfinite(got["y"]).all()
     assert all(v == v for v in got["loss"])
+
+
+def test_heads_in_front_of_tokens(dit):
+    """Queries, keys and values of each head behind one another, [heads, 3, tokens, dim], and their gradients in such a buffer:
+    the bits of the calls on tensors of their own."""
+    h, t, d = 3, 300, 64
+    g = torch.Generator(device="cuda").manual_seed(11)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=g).to(BF16)  # noqa: E731
+    x, dout = new(h, 3, t, d), new(t, h, d)
+    parts = lambda b: [b[:, i].transpose(0, 1) for i in range(3)]  # noqa: E731
+    norm, rot = dit.QKNorm(torch.rand(2, d, device="cuda", generator=g) + 0.5, "rms"), dit.Rotary((16, 24, 24), d)
+    positions = torch.randint(0, 40, (t, 3), device="cuda", generator=g, dtype=torch.int32)
+    plan, ws = dit.AttentionPlan([200, 100], h, d, training=True), dit.workspace()
+    scratch, saved = dit.attention_scratch(plan), dit.attention_saved(plan)
+    got = []
+    for together in (True, False):
+        if together:
+            q, k, v = parts(x.clone())
+            dq, dk, dv = parts(torch.empty_like(x))
+        else:
+            q, k, v = (p.contiguous() for p in parts(x))
+            dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        raw = q.clone(), k.clone()
+        dit.qk_norm_rope(q, k, q, k, norm, rot, positions)
+        out, dparams = torch.empty(t, h, d, dtype=BF16, device="cuda"), torch.empty_like(norm.params)
+        dit.attention(plan, q, k, v, out, scratch, ws, saved=saved)
+        dit.attention_backward(plan, q, k, v, out, dout, saved, dq, dk, dv, scratch, ws)
+        dit.qk_norm_rope_backward(*raw, dq, dk, dq, dk, norm, rot, positions, dparams, dit.qk_norm_scratch(d), ws)
+        got.append([a.clone() for a in (q, k, out, dq, dk, dv, dparams)])
+    assert all(torch.isfinite(a).all() and torch.equal(a, b) for a, b in zip(*got))
+    assert dit.device_status(ws) == 0
