@@ -553,7 +553,8 @@ dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensor
  * dq, dk    : device bf16, may be the views dq_out and dk_out themselves.
  * dparams   : device float, the shape of params, overwritten; NULL: not wanted.
  * scratch   : device buffer of dit_qk_norm_scratch_bytes(dim), 16-byte aligned, contents free; calls
- *             ordered on one stream may share it (only needed with dparams).
+ *             ordered on one stream may share it (only needed with dparams).  It shares no byte with
+ *             another buffer of the call (DIT_ERR_INVALID_ARG for ws, dparams, params and positions).
  * ------------------------------------------------------------------------------------ */
 #define DIT_NORM_NONE 0
 #define DIT_NORM_RMS 1
@@ -626,7 +627,7 @@ dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k,
  * saved   : device buffer of plan->saved_bytes, 16-byte aligned, that the forward pass fills for
  *           the backward pass (training plans; otherwise NULL).
  * scratch : device buffer of plan->scratch_bytes, 16-byte aligned, contents free; calls ordered on one
- *           stream may share it.
+ *           stream may share it.  saved, scratch and ws share no byte (DIT_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------ */
 #define DIT_ATTENTION_LISTS 4
 #define DIT_ATTENTION_BUCKETS 16

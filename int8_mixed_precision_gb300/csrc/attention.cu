@@ -613,6 +613,7 @@ extern "C" dit_status dit_attention(const dit_attention_plan_t* plan, const int3
   a.rows = rows_per_tile(a.group);
   a.stall = test_stall();
   if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
+  if (!buffers_apart(*plan, saved, scratch, ws)) return DIT_ERR_INVALID_ARG;
   const bool split = plan->items[JOIN] > 0;
   if (plan->dim > 64) return split ? launch<128, true, 1>(a, hq, hk, hv, stream) : launch<128, false, 1>(a, hq, hk, hv, stream);
   if (plan->row_blocks == 1) return launch<64, false, 1>(a, hq, hk, hv, stream);

@@ -129,6 +129,7 @@ __device__ __forceinline__ Work find_work(const int32_t* table, const dit_attent
 bool plan_ok(const dit_attention_plan_t* p);
 dit_status check_view(const dit_heads_t* v, int heads, int64_t rows, int dim, Heads* o);
 dit_status check_output(const dit_heads_t* v, int heads, int64_t rows, int dim, Heads* o);  // its heads lie apart too
+bool buffers_apart(const dit_attention_plan_t& p, const void* saved, const void* scratch, const void* ws);
 bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows);
 
 // ---------------------------------------------------------------------------------------

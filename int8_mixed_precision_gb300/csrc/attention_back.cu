@@ -517,5 +517,6 @@ extern "C" dit_status dit_attention_backward(const dit_attention_plan_t* plan, c
   a.group = h / hk;
   a.stall = test_stall();
   if (!(a.c >= FLT_MIN && a.c <= FLT_MAX)) return DIT_ERR_INVALID_ARG;  // in fp32 too
+  if (!buffers_apart(*plan, saved, scratch, ws)) return DIT_ERR_INVALID_ARG;
   return dim <= 64 ? backward<64>(a, in, hdq, hdk, hdv, stream) : backward<128>(a, in, hdq, hdk, hdv, stream);
 }

@@ -289,6 +289,11 @@ dit_status check_output(const dit_heads_t* v, int heads, int64_t rows, int dim, 
   return e == DIT_OK && !heads_apart(rows, heads, dim, o->row, o->head) ? DIT_ERR_INVALID_ARG : e;
 }
 
+bool buffers_apart(const dit_attention_plan_t& p, const void* saved, const void* scratch, const void* ws) {
+  const size_t kept = (size_t)p.saved_bytes, free = (size_t)p.scratch_bytes;
+  return bytes_apart(saved, kept, scratch, free) && bytes_apart(saved, kept, ws, WS_BYTES) && bytes_apart(scratch, free, ws, WS_BYTES);
+}
+
 bool map_heads(CUtensorMap* map, const Heads& t, int dim, int heads, int64_t rows, int box_heads, int box_rows) {
   return encode_tmap_heads(map, t.ptr, (uint64_t)dim, (uint64_t)heads, (uint64_t)rows, (uint64_t)t.head * 2, (uint64_t)t.row * 2,
                            (uint32_t)box_heads, (uint32_t)box_rows);

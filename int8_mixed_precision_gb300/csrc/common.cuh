@@ -499,6 +499,11 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // loads, so the consumers' bounded waits run out and the kernels report DIT_ERR_TIMEOUT.
 int test_stall();
 bool aligned32(const void* p);
+// Whether two buffers share no byte.
+inline bool bytes_apart(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return !a || !b || (x < y ? y - x >= a_bytes || !b_bytes : x - y >= b_bytes || !a_bytes);
+}
 // Whether the heads [tokens][heads][dim] of a tensor with these strides (in elements) lie apart from one another, as
 // those of an output must: no two of them are nearer than dim.
 bool heads_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride);

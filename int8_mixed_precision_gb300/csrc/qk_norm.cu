@@ -564,6 +564,10 @@ extern "C" dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_
     if (norm == DIT_NORM_NONE || !scratch || scratch_bytes < dit_qk_norm_scratch_bytes(dim)) return DIT_ERR_INVALID_ARG;
     if (!qk::aligned16(scratch) || (reinterpret_cast<uintptr_t>(dparams) & 3)) return DIT_ERR_ALIGNMENT;
     const int rows = norm == DIT_NORM_LAYER ? 2 : 1;
+    const size_t sums = dit_qk_norm_scratch_bytes(dim), all = sizeof(float) * p.sides * rows * dim;
+    if (!bytes_apart(scratch, sums, dparams, all) || !bytes_apart(scratch, sums, params, all) || !bytes_apart(scratch, sums, ws, WS_BYTES) ||
+        !bytes_apart(dparams, all, ws, WS_BYTES) || (p.pairs && !bytes_apart(scratch, sums, positions, sizeof(int32_t) * tokens * p.axes)))
+      return DIT_ERR_INVALID_ARG;
     for (int i = 0; i < p.sides; ++i) {
       p.side[i].dw = dparams + (int64_t)i * rows * dim;
       p.side[i].db = p.side[i].dw + dim;

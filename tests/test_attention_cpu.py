@@ -350,6 +350,31 @@ def test_outputs_whose_heads_overlap_are_refused(dit):
     assert norm(True, heads(A, 4, 64, big, -big), 4, 64, 3) == INVALID and norm(True, heads(A, 1, 64, 0, 0), 1, 64, 1) == ALIGNMENT
 
 
+def test_buffers_that_share_memory_are_refused(dit):
+    """What a call keeps, its scratch and its workspace: the scratch of the backward pass would be written over what it reads."""
+    L, A = dit.lib(), 1 << 20
+    plan = dit.AttentionPlan([300, 7], 4, 64, training=True, device="cpu")
+    view, n = ctypes.byref(heads(A, 4, 64)), plan._saved_bytes
+    assert n == 4 * 4 * 512 and plan._scratch_bytes >= n
+
+    def attend(saved, scratch, ws):
+        rest = (0.1, saved, 1 << 30, scratch, 1 << 30, ws, 1 << 16, None)
+        back = L.dit_attention_backward(ctypes.byref(plan.info), A, *[view] * 8, *rest)
+        return {back, L.dit_attention(ctypes.byref(plan.info), A, *[view] * 4, *rest)}
+    far = 1 << 24
+    for saved, scratch, ws in ((far, far, 2 * far), (far, far + n - 32, 2 * far), (far + plan._scratch_bytes - 32, far, 2 * far), (far, 2 * far, far + n - 32),
+                               (far + 65536 - 32, 2 * far, far), (far, 2 * far, 2 * far)):
+        assert attend(saved, scratch, ws) == {INVALID}, (saved, scratch, ws)
+
+    def norm(params=far, dparams=2 * far, scratch=3 * far, ws=4 * far, positions=5 * far):
+        from int8_mixed_precision_gb300.block_attention import _Rotary
+        rot = _Rotary(A, 32, 3, 1, 0)
+        return L.dit_qk_norm_rope_backward(*[view] * 6, 10, 64, 2, params, 1e-6, ctypes.byref(rot), positions, dparams, scratch, 1 << 30, ws, 1 << 16, None)
+    for change in (dict(dparams=3 * far), dict(dparams=3 * far - 4 * 4 * 64 + 4), dict(params=3 * far), dict(ws=3 * far), dict(ws=2 * far), dict(positions=3 * far),
+                   dict(positions=3 * far - 116)):
+        assert norm(**change) == INVALID, change
+
+
 def test_views_that_share_memory_are_found(dit):
     from int8_mixed_precision_gb300.block_attention import _meet
 
