@@ -532,7 +532,7 @@ dit_status dit_adamw_moments(const dit_adamw_tensor* descs_dev, int64_t n_tensor
  * the pair's dimensions being (2p, 2p + 1) if interleaved, else (p, p + pairs); dimensions behind
  * them are not turned.  The angle of pair p is position[axis(p)] times the pair's frequency.  Frequencies
  * are held in turns as 64-bit fractions, so an angle is exact modulo a turn to 2^-21 of a radian at
- * every 32-bit position.  Sums are fp32; y is rounded once to bf16.
+ * every 32-bit position, for frequencies of up to 2^30 radians a position.  Sums are fp32; y is rounded once to bf16.
  *   backward: with dn the gradient dy turned back, per parameter (sums over all tokens and heads)
  *   dw = sum dn xhat, db = sum dn  (xhat = (x - mean) r), and
  *   dx = r (g - mean(g) - xhat mean(g xhat)), g = dn w  (RMS: without mean(g)).
@@ -577,7 +577,8 @@ typedef struct {
 
 /* Host: the table of a rotation.  dims [axes]: even numbers of dimensions of each axis, in the pairs'
  * order; index i of axis a's pairs has the frequency scale[a] * theta^(-2 i / dims[a]) radians a
- * position.  table: sum(dims) / 2 entries of 16 bytes. */
+ * position (finite, else DIT_ERR_INVALID_ARG), whose fraction of a turn is held to 2^-63 up to 2^30 radians.
+ * table: sum(dims) / 2 entries of 16 bytes. */
 dit_status dit_rotary_table(const int32_t* dims, int axes, double theta, const double* scale, void* table,
                             size_t table_bytes);
 size_t dit_qk_norm_scratch_bytes(int dim);

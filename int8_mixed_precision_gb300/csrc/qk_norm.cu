@@ -415,6 +415,35 @@ __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid
   if (threadIdx.x == 0) *ws_u32(p.ws, WS_TICKET) = 0u;
 }
 
+// A number as the sum of two doubles, 106 bits (Dekker, 1971; Knuth): what a rotation's frequencies are made in.  A frequency's
+// fraction of a turn is wanted to 2^-64, and plain doubles leave 2^-53 of the whole frequency.
+struct Wide {
+  double hi, lo;
+};
+static Wide sum_of(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+static Wide product_of(Wide a, Wide b) {
+  const double p = a.hi * b.hi;
+  return sum_of(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
+}
+// theta^(-1/m): a step of Newton's method on theta x^m = 1 doubles the bits that a double has, a second one is for m's sake.
+static Wide root_of(double theta, int m) {
+  Wide x = {pow(theta, -1.0 / m), 0.0};
+  for (int step = 0; step < 2; ++step) {
+    Wide t = {theta, 0.0};
+    for (int i = 0; i < m; ++i) t = product_of(t, x);
+    x = sum_of(x.hi, x.lo - x.hi * ((t.hi - 1.0) + t.lo) / m);
+  }
+  return x;
+}
+// The fraction of a number of turns, times 2^64.
+static uint64_t fraction_of(Wide turns) {
+  const double a = ldexp(turns.hi - nearbyint(turns.hi), 64), b = ldexp(turns.lo - nearbyint(turns.lo), 64), whole = floor(a);
+  return (uint64_t)((__int128)whole + (__int128)nearbyint((a - whole) + b));
+}
+
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // A view's checks, with strides that are not used replaced.
@@ -525,13 +554,17 @@ extern "C" dit_status dit_rotary_table(const int32_t* dims, int axes, double the
   if (2 * pairs > qk::MAX_DIM) return DIT_ERR_UNSUPPORTED;
   if (table_bytes < pairs * sizeof(qk::Pair)) return DIT_ERR_INVALID_ARG;
   qk::Pair* o = reinterpret_cast<qk::Pair*>(table);
-  const double two_pi = 6.283185307179586476925;
-  for (int a = 0; a < axes; ++a)
-    for (int i = 0; i < dims[a] / 2; ++i) {
-      const double turns = scale[a] * pow(theta, -2.0 * i / dims[a]) / two_pi;
-      const double part = turns - floor(turns);  // whole turns a position change nothing
-      *o++ = qk::Pair{part < 1.0 ? (uint64_t)ldexp(part, 64) : 0, a, 0};
+  const qk::Wide turns_a_radian = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+  for (int a = 0; a < axes; ++a) {
+    const int m = dims[a] / 2;
+    qk::Wide power = {1.0, 0.0};
+    const qk::Wide root = m ? qk::root_of(theta, m) : power, first = qk::product_of(turns_a_radian, {scale[a], 0.0});
+    for (int i = 0; i < m; ++i, power = qk::product_of(power, root)) {
+      const qk::Wide turns = qk::product_of(first, power);
+      if (!isfinite(turns.hi) || !isfinite(turns.lo)) return DIT_ERR_INVALID_ARG;
+      *o++ = qk::Pair{qk::fraction_of(turns), a, 0};
     }
+  }
   return DIT_OK;
 }
 

@@ -1,6 +1,7 @@
 """Host side of the norms and the attention, without a GPU: the rotation's table, the plan's cuts and what is refused."""
 import copy
 import ctypes
+import decimal
 import math
 import os
 import random
@@ -41,6 +42,32 @@ def test_rotary_table_holds_turns(dit):
             assert abs(held - turns) < 2.0 ** -49
             assert int(words[p, 1]) & 0xffffffff == a
             p += 1
+
+
+@pytest.mark.parametrize("theta", [10000.0, 500000.0, 1e8, 1.0, 0.3, 1e300])
+@pytest.mark.parametrize("scales", [(1.0, 0.375, 7.5), (100.0, 1 / 3, -2.5), (1e6, 1e-9, 2.0 ** 30)])
+def test_rotary_table_against_long_arithmetic(dit, theta, scales):
+    """A position has 32 bits and an angle is promised to 2^-21 of a radian, so a turn's fraction is to be right to 2^-55 at
+    least; 64 bits hold it to 2^-64.  Against 80 decimal digits."""
+    decimal.getcontext().prec = 80
+    tau = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534")
+    dims = (16, 24, 216)
+    words = dit.Rotary(dims, 256, theta=theta, scale=scales, device="cpu").table.view(-1, 2).tolist()
+    p = 0
+    for d, s in zip(dims, scales):
+        for i in range(d // 2):
+            frequency = decimal.Decimal(s) * decimal.Decimal(theta) ** (decimal.Decimal(-2 * i) / d)
+            off = (frequency / tau - decimal.Decimal(words[p][0] & (2 ** 64 - 1)) / 2 ** 64) % 1
+            off = min(abs(off), 1 - abs(off))
+            assert abs(frequency) > 2 ** 30 or off <= decimal.Decimal(2) ** -63, (d, i, float(off * 2 ** 64))
+            p += 1
+
+
+def test_rotary_refuses_frequencies_without_bounds(dit):
+    for theta, scale in ((1e-300, 1e200), (1e-300, -1e200)):
+        with pytest.raises(dit.DitError):
+            dit.Rotary((64,), 64, theta=theta, scale=scale, device="cpu")
+    assert dit.Rotary((64,), 64, theta=1e-300, device="cpu").table.numel() == 64
 
 
 @pytest.mark.parametrize("kw", [dict(dims=(16, 23, 25)), dict(dims=(32, 48)), dict(dims=(8,) * 5), dict(dims=()), dict(dims=(64,), scale=(1.0, 1.0)),
