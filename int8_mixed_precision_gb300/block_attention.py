@@ -151,6 +151,14 @@ def _apart(outputs, inputs, dim, own=()):
                 raise DitError(f"{name} overlaps {other}")
 
 
+def _each(value, n, kind):
+    """n numbers from one, of whatever library, or from as many as there are."""
+    try:
+        return [kind(v) for v in value]
+    except TypeError:
+        return [kind(value)] * n
+
+
 # ----------------------------------------------------------------------------------------
 # norms and rotation
 # ----------------------------------------------------------------------------------------
@@ -166,7 +174,7 @@ class Rotary:
     def __init__(self, dims, head_dim: int, theta: float = 10000.0, scale=1.0, interleaved: bool = True, device="cuda"):
         self.dims, self.head_dim, self.interleaved = tuple(int(d) for d in dims), int(head_dim), bool(interleaved)
         axes = len(self.dims)
-        scale = [float(scale)] * axes if isinstance(scale, (int, float)) else [float(s) for s in scale]
+        scale = _each(scale, axes, float)
         if not 1 <= axes <= MAX_AXES or len(scale) != axes:
             raise DitError(f"Rotary: one to {MAX_AXES} axes, and a scale for each")
         if any(d < 0 or d % 2 for d in self.dims) or sum(self.dims) > self.head_dim:
@@ -321,7 +329,7 @@ class AttentionPlan:
         lengths = [int(v) for v in lengths]
         n = len(lengths)
         kv_lengths = lengths if kv_lengths is None else [int(v) for v in kv_lengths]
-        prefix = [int(prefix)] * n if isinstance(prefix, int) else [int(v) for v in prefix]
+        prefix = _each(prefix, n, int)
         begins = None if kv_begins is None else [int(v) for v in kv_begins]
         for name, v in (("kv_lengths", kv_lengths), ("prefix", prefix), ("kv_begins", begins)):
             if v is not None and len(v) != n:

@@ -218,6 +218,15 @@ def test_plans_of_random_batches(dit):
         check_plan(dit, queries, keys, kv * rng.choice([1, 2, 3]), kv, 8 * rng.randint(1, 16), frame, rng.choice([0, rng.randint(1, 90)]) if frame else 0)
 
 
+def test_numbers_of_other_libraries(dit):
+    """One prefix or scale for all is a number, whoever made it."""
+    import numpy as np
+    plans = [dit.AttentionPlan([10, 20], 2, 64, frame=2, prefix=p, device="cpu").table for p in (3, np.int64(3), torch.tensor(3), [3, 3], np.array([3, 3]))]
+    assert all(torch.equal(plans[0], t) for t in plans)
+    tables = [dit.Rotary((32, 32), 64, scale=s, device="cpu").table for s in (2.0, np.float32(2.0), torch.tensor(2.0), [2, 2], np.array([2.0, 2.0]))]
+    assert all(torch.equal(tables[0], t) for t in tables)
+
+
 def test_few_rows_are_split_over_the_keys(dit):
     plan = dit.AttentionPlan([1], 4, 128, kv_heads=1, kv_lengths=[20000], frame=1, device="cpu")
     assert plan.info.items[0] > 50 and plan.info.items[1] == 1
