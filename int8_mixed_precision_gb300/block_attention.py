@@ -14,7 +14,7 @@ import threading
 
 import torch
 
-from . import DitError, _check
+from . import ROUTE_BF16, ROUTE_INT8, DitError, _bias_ok, _check, _dt, _p, _same_device
 from ._lib import lib
 from .adapters import raw_stream
 
@@ -432,6 +432,30 @@ def attention_backward(plan: AttentionPlan, q, k, v, out, dout, saved, dq, dk, d
         _check(st, "dit_attention_backward")
 
 
+def _projectable(linear, x, route, y, bias, what):
+    """What a routed projection of x into y refuses, for a caller that launches something before it.  Along the BF16 route x is
+    read while y is written."""
+    w, rows = linear.w, x.shape[0]
+    if route == ROUTE_BF16:
+        if w.bf16 is None:
+            raise DitError(f"{what}: the BF16 route needs QuantizedWeight(..., keep_bf16=True)")
+        if x.data_ptr() < y.data_ptr() + y.nbytes and y.data_ptr() < x.data_ptr() + x.nbytes:
+            raise DitError(f"{what}: the output overlaps what the BF16 route reads")
+    else:
+        room = (linear.a8["q"] if route == ROUTE_INT8 else linear.a4["codes"]).shape[0]
+        if rows > room:
+            raise DitError(f"{what}: {rows} tokens, the projection was made for {room}")
+    _bias_ok(bias, w.n)
+    if y.numel() < rows * w.n:
+        raise DitError(f"{what}: an output of {y.numel()} elements, the projection writes {rows * w.n}")
+    if _dt(y) > 1:
+        raise DitError(f"{what}: unsupported dtype {y.dtype}")
+    _same_device(x, y, bias, linear.ws)
+    _p(y), _p(bias)
+    if y.data_ptr() % 32 or (bias is not None and bias.data_ptr() % 16):
+        raise DitError(f"{what}: {lib().dit_status_str(2).decode()}")
+
+
 class RoutedAttention:
     """The attention part of a block between two routed quantised projections: QKV, norms and rotation in place,
     attention, output projection.  The QKV projection's outputs are all query heads, all key heads, all value heads."""
@@ -448,7 +472,7 @@ class RoutedAttention:
     def __call__(self, x, routes, y, plan: AttentionPlan, qkv, attended, scratch, positions=None, bias=(None, None), stream=None):
         """y = attention of x's tokens along routes[0] (QKV) and routes[1] (output).  qkv [tokens, heads + 2 kv_heads, dim] and
         attended [tokens, heads, dim] are bf16 buffers of the caller; the plan is one of these heads whose keys are the batch's
-        own tokens."""
+        own tokens.  A call that is refused has written nothing."""
         t, h, hk, d = x.shape[0], self.heads, self.kv_heads, self.dim
         if (plan.heads, plan.kv_heads, plan.dim) != (h, hk, d) or plan.q_rows > t or plan.k_rows > t:
             raise DitError("RoutedAttention: a plan of other heads, or of more tokens")
@@ -457,6 +481,10 @@ class RoutedAttention:
                 raise DitError(f"RoutedAttention: {name} is a contiguous bf16 [{t}, {width}, {d}]")
         if plan.q_rows < t:
             raise DitError(f"RoutedAttention: a plan of {plan.q_rows} tokens, {t} are given")
+        if len(routes) != 2 or len(bias) != 2:
+            raise DitError("RoutedAttention: a route and a bias for each of the two projections")
+        _projectable(self.qkv, x, routes[0], qkv, bias[0], "RoutedAttention, QKV")
+        _projectable(self.out, attended, routes[1], y, bias[1], "RoutedAttention, output")
         q, k, v = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
         steps = [_attention_call(plan, q, k, v, attended, scratch, self.out.ws, None, None, stream)]
         if self.norm is not None or self.rotary is not None:

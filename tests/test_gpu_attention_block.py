@@ -230,3 +230,35 @@ def test_heads_in_front_of_tokens(dit):
         got.append([a.clone() for a in (q, k, out, dq, dk, dv, dparams)])
     assert all(torch.isfinite(a).all() and torch.equal(a, b) for a, b in zip(*got))
     assert dit.device_status(ws) == 0
+
+
+def test_what_the_projections_refuse_is_refused_first(dit):
+    heads, dim, t = 2, 64, 50
+    ws = dit.workspace()
+    weight = lambda n, **kw: dit.QuantizedWeight(torch.randn(n, 128, device="cuda"), 64, ws, **kw)  # noqa: E731
+    lin, out = dit.RoutedLinear(weight(3 * 128), t, ws), dit.RoutedLinear(weight(128), t, ws)
+    part, small = dit.RoutedAttention(lin, out, heads), dit.RoutedAttention(lin, dit.RoutedLinear(weight(128), t - 1, ws), heads)
+    plan = dit.AttentionPlan([t], heads, dim)
+    buffers = dict(y=torch.full((t, 128), 3.0, dtype=BF16, device="cuda"), qkv=torch.full((t, 6, dim), 4.0, dtype=BF16, device="cuda"),
+                   attended=torch.full((t, 2, dim), 5.0, dtype=BF16, device="cuda"))
+    ok = dict(x=torch.randn(t, 128, device="cuda").to(BF16), routes=(1, 0), plan=plan, scratch=dit.attention_scratch(plan), **buffers)
+    y, bias = ok["y"], torch.zeros(128, device="cuda")
+    room = torch.full((t * 128 + 8,), 3.0, dtype=BF16, device="cuda")
+    for change in (dict(routes=(1,)), dict(routes=(1, dit.ROUTE_BF16)), dict(routes=(dit.ROUTE_BF16, 1)), dict(y=y[:-1]), dict(y=y.T), dict(y=y.cpu()),
+                   dict(y=y.to(torch.float16)), dict(y=room[8:].view(t, 128)), dict(bias=(None,)), dict(bias=(None, bias.double())), dict(bias=(None, bias[:-1])),
+                   dict(bias=(bias, None)), dict(bias=(None, bias.cpu()))):
+        with pytest.raises(dit.DitError):
+            part(**{**ok, **change})
+    with pytest.raises(dit.DitError):
+        small(**ok)
+    torch.cuda.synchronize()
+    assert (ok["y"] == 3).all() and (ok["qkv"] == 4).all() and (ok["attended"] == 5).all() and (room == 3).all()
+    part(**ok)
+    want = y.clone()
+    part(**{**ok, "y": ok["attended"].view(t, 128)})  # a quantised route has read the attention before it writes
+    assert torch.equal(want, ok["attended"].view(t, 128))
+    kept = dit.RoutedAttention(lin, dit.RoutedLinear(weight(128, keep_bf16=True), t, ws), heads)
+    kept(**{**ok, "routes": (1, dit.ROUTE_BF16)})
+    with pytest.raises(dit.DitError):
+        kept(**{**ok, "routes": (1, dit.ROUTE_BF16), "y": ok["attended"].view(t, 128)})
+    assert dit.device_status(ws) == 0
