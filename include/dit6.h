@@ -22,7 +22,12 @@
  *   with.  This rests on every kernel of these calls waiting itself before it lets the next one launch: what
  *   precedes it has then completed and reached global memory.  The first kernel of a call waits before any
  *   access and every kernel before its end, so for other work on the stream the order is that of plain launches.
- *   In dit_attention_backward the kernel of dk and dv runs beside the one of dq in the same way.
+ *   In dit_attention_backward the kernel of dk and dv runs beside the one of dq: ahead of its wait it reads what was
+ *   complete before dq's kernel started, and it writes what that one does not touch.  Of the call's kernels only dq's
+ *   waits before it lets the next one launch, so only its successor may read ahead.  Nothing that follows dk and dv may:
+ *   their kernel lets the next one launch while dq may still be on its way, and waits before its own end.
+ *   In general a kernel may read ahead of its wait only where its direct predecessor on the stream waits before
+ *   it lets it launch, and then what was complete before that predecessor started.
  * - The return code covers argument errors found on the host;
  *   errors found on the device (a bounded wait that ran out) are OR-ed into the status
  *   word at byte 0 of the workspace (see dit_ws_status_offset), which the caller reads
@@ -608,15 +613,18 @@ dit_status dit_qk_norm_rope_backward(const dit_heads_t* q, const dit_heads_t* k,
  * Operands enter the tensor cores in bf16 (p and ds are rounded to bf16), sums are fp32; outputs are
  * rounded once.  All sums have a fixed order (no atomics on values): a call with the same arguments
  * gives the same bits.  What a document's tokens hold reaches no other document's results, nor
- * does what lies in rows of no document (NaN included); rows of no document are not written.
+ * does what lies in rows of no document (NaN included); rows of no document are not written.  Inside a document a pair
+ * that the mask hides counts as a weight of zero in products over whole tiles: a NaN or an infinity in a value (in
+ * the gradients in a key, a query or dout as well) may reach rows that do not see it, as 0 * NaN does.
  *
  * The plan.  dit_attention_plan (host, no device work) cuts the documents into work for the kernels; a plan
- * serves every block and step with the same batch.  Call it with table = NULL to learn the sizes,
+ * serves every block and step with the same lengths (a cache that grows wants a new one each step).  Call it with table = NULL to learn the sizes,
  * then with a host buffer of table_ints int32, and copy the table to the device (16-byte aligned).
  *   queries, keys : host int64 [documents].   begins : host int64 [documents], or NULL: packed in order.
  *   prefix : host int64 [documents], or NULL: none.   training : 1 for plans that the backward pass takes:
  *   there no key row belongs to two documents (DIT_ERR_INVALID_ARG).
- *   heads, kv_heads: heads % kv_heads == 0, heads up to 4096; dim: a multiple of 8 up to 128.
+ *   heads, kv_heads: heads % kv_heads == 0, heads up to 4096, up to 128 of them to a key head; dim: a multiple of 8
+ *   up to 128; up to 2^22 documents (DIT_ERR_UNSUPPORTED).
  * The kernels check the table's entries against the plan: a wrong one is skipped and raises
  * DIT_ERR_INVALID_ARG in the device status word.
  *

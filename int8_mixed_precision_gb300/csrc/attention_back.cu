@@ -18,12 +18,15 @@
 //
 // Ahead of the stream.  The kernel of dk and dv needs nothing of the one of dq before it and starts on the SMs that one leaves.  That one
 // lets it launch only after its own wait, so that the inputs, lse and delta are then complete and in global memory; and
-// it waits itself before it ends, so for what follows on the stream the order is that of plain launches.
+// it waits itself before it ends, so for what follows on the stream the order is that of plain launches.  The kernels of delta
+// and of dk and dv let their successors launch before they have waited: those wait before they read anything.
 //
-// Bound by the row warps' chain of two tiles of 64 columns, 1515 cycles where queries stay and 1800 where keys do (whose columns'
-// lse and delta come from shared memory), for MMAs of 1024 and 1280.  17,776 rows of 30 heads of 64: 2.66 and 3.14 ms apart, 6.1 ms
-// for the whole backward pass, 995 TFLOP/s of the formulas' ten operations; 4096 rows of 9 heads of 128: 215 us, 897.  With one
-// stream in each the pass took 7.6 ms.
+// Bound by the row warps' chains and the MMAs, which do not quite hide each other.  17,776 rows of 30 heads of 64, seconds of it under
+// the power cap: 2.79 ms where queries stay (at 1965 MHz) and 3.38 where keys do (1935 MHz; their columns' lse and delta
+// come from shared memory), apart.  To two tiles of 64 columns that is 1435 and 1720 cycles, a CTA's start and end included, for
+// MMAs of 1024 and 1280: the tensor pipe has work for 71 and 74 % of the time.  The whole backward pass takes 6.3 ms so and 6.1
+// among other work, 995 TFLOP/s of the formulas' ten operations; 4096 rows of 9 heads of 128: 216 us, 893.  With one stream in
+// each the pass took 7.6 ms.
 //
 // Warps: 0 loads; 1 and 6 issue S and T of a stream each; 2 issues A, 3 B; 4, 5 and 7 relay the MMAs' completion; the others hold
 // the rows and take over most of the first ones' registers.  Every wait on memory is bounded.

@@ -455,7 +455,8 @@ int num_sms();  // SM count of the current device (cached per device)
 // kernel's memory operations visible, before its own first global memory access (pdl_wait).
 // The next kernel's CTAs thus launch and run their prologue (barrier initialisation, tensor
 // memory allocation) while this one drains.  The adapters' kernels order the two the other way round and read
-// ahead of the wait (adapters.cu says what and why that is sound).  After a launch without the attribute, or after a
+// ahead of the wait (adapters.cu says what and why that is sound); the attention's kernel of dq does as they do, so that
+// the one of dk and dv behind it may read ahead (attention_back.cu).  After a launch without the attribute, or after a
 // stream operation other than a kernel, both are no-ops.
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_launch_dependents() {

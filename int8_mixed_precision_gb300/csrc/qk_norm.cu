@@ -196,8 +196,9 @@ __device__ __forceinline__ Angles load_angles(const Args& p, const float2* cs, i
 
 // CTAs are persistent and take every ctas-th block of tokens; a thread's next rows are always on their way, into the next block, and
 // the angles of that block are made during the present one.  104,746 tokens of 30 + 30 heads of 64: 308 us with the RMS norm, 5.2
-// TB/s.  17,776 tokens with the layer norm: 65 us, 4.2 TB/s; there it is bound by some 190 instructions to eight dimensions of a
-// row, 62 % of the issue slots.
+// TB/s.  17,776 tokens with the layer norm: 65 us, 4.2 TB/s; neither memory (40 % of the DRAM's) nor the issue slots (62 %, some 190
+// instructions to eight dimensions of a row) are full there: six warps to a scheduler wait for fixed latencies, the blocks' barrier and
+// memory in about equal parts.
 template <int NORM, bool SPLIT, int LANES>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid_constant__ Args p) {
   pdl_launch_dependents();
@@ -270,7 +271,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) k_norm_rope(const __grid
 
 // Each thread sums its parameters' gradients over all of its rows, the CTA adds them up over its groups, and the CTA that finishes
 // last over the CTAs, always in the same order.  One CTA of 512 threads to an SM makes few rows for that last sum; with 608 it took 27 us.
-// 17,776 tokens of 30 + 30 heads of 64, layer norm: 109 us, 3.8 TB/s, bound by instructions too.
+// 17,776 tokens of 30 + 30 heads of 64, layer norm: 109 us, 3.8 TB/s, 42 % of the issue slots and 40 % of the DRAM's.  It is bound by
+// latency: with four warps to a scheduler and two rows of a thread on their way a warp waits 2.2 of some 8 cycles between its
+// instructions for memory and 1.4 at the blocks' barriers.
 template <int NORM, bool SPLIT, int LANES>
 __global__ void __launch_bounds__(BACK_THREADS, 1) k_norm_rope_back(const __grid_constant__ Args p) {
   pdl_launch_dependents();
