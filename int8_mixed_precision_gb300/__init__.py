@@ -516,6 +516,8 @@ class RoutedLinear:
     def __call__(self, x, route: int, y, bias=None, tensor_scale_in=None, act=ACT_NONE, stream=None):
         m = x.shape[0]
         w = self.w
+        if x.dim() != 2 or x.shape[1] != w.k:  # the codes of other rows would be read as this weight's
+            raise DitError(f"RoutedLinear: x is {tuple(x.shape)}, the weight takes [tokens, {w.k}]")
         if route == ROUTE_BF16:
             if w.bf16 is None:
                 raise DitError("BF16 route needs QuantizedWeight(..., keep_bf16=True)")

@@ -262,3 +262,20 @@ def test_what_the_projections_refuse_is_refused_first(dit):
     with pytest.raises(dit.DitError):
         kept(**{**ok, "routes": (1, dit.ROUTE_BF16), "y": ok["attended"].view(t, 128)})
     assert dit.device_status(ws) == 0
+
+
+def test_projections_refuse_rows_of_another_width(dit):
+    """Codes of narrower rows would be read as rows of the weight's width."""
+    t, ws = 50, dit.workspace()
+    weight = lambda n: dit.QuantizedWeight(torch.randn(n, 128, device="cuda"), 64, ws, keep_bf16=True)  # noqa: E731
+    lin, out = dit.RoutedLinear(weight(3 * 128), t, ws), dit.RoutedLinear(weight(128), t, ws)
+    plan = dit.AttentionPlan([t], 2, 64)
+    y, qkv, attended = (torch.full(s, 3.0, dtype=BF16, device="cuda") for s in ((t, 128), (t, 6, 64), (t, 2, 64)))
+    for route in (0, 1, 2):
+        for x in (torch.randn(t, 64, device="cuda"), torch.randn(t, 192, device="cuda"), torch.randn(t, 1, 128, device="cuda")):
+            with pytest.raises(dit.DitError):
+                out(x.to(BF16), route, y)
+            with pytest.raises(dit.DitError):
+                dit.RoutedAttention(lin, out, 2)(x.to(BF16), (route, 1), y, plan, qkv, attended, dit.attention_scratch(plan))
+    torch.cuda.synchronize()
+    assert (y == 3).all() and (qkv == 3).all() and (attended == 3).all()
