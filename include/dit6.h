@@ -582,8 +582,8 @@ typedef struct {
 
 /* Host: the table of a rotation.  dims [axes]: even numbers of dimensions of each axis, in the pairs'
  * order; index i of axis a's pairs has the frequency scale[a] * theta^(-2 i / dims[a]) radians a
- * position (finite, else DIT_ERR_INVALID_ARG), whose fraction of a turn is held to 2^-63 up to 2^30 radians.
- * table: sum(dims) / 2 entries of 16 bytes. */
+ * position (finite, else DIT_ERR_INVALID_ARG), whose fraction of a turn is held to 2^-63 up to 2^30 radians
+ * (scale 0 or at least 2^-900).  table: sum(dims) / 2 entries of 16 bytes. */
 dit_status dit_rotary_table(const int32_t* dims, int axes, double theta, const double* scale, void* table,
                             size_t table_bytes);
 size_t dit_qk_norm_scratch_bytes(int dim);

@@ -431,13 +431,15 @@ static Wide product_of(Wide a, Wide b) {
   const double p = a.hi * b.hi;
   return sum_of(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
 }
-// theta^(-1/m): a step of Newton's method on theta x^m = 1 doubles the bits that a double has, a second one is for m's sake.
+// theta^(-1/m): a step of Newton's method on theta x^m = 1 doubles the bits that a double has, a second one is for m's sake.  Products
+// with the smallest thetas are made 2^300 times as large, so that their low parts are held.
 static Wide root_of(double theta, int m) {
+  const int up = theta < 0x1p-600 ? 300 : 0;
   Wide x = {pow(theta, -1.0 / m), 0.0};
   for (int step = 0; step < 2; ++step) {
-    Wide t = {theta, 0.0};
+    Wide t = {ldexp(theta, up), 0.0};
     for (int i = 0; i < m; ++i) t = product_of(t, x);
-    x = sum_of(x.hi, x.lo - x.hi * ((t.hi - 1.0) + t.lo) / m);
+    x = sum_of(x.hi, x.lo - x.hi * ((ldexp(t.hi, -up) - 1.0) + ldexp(t.lo, -up)) / m);
   }
   return x;
 }
@@ -560,10 +562,9 @@ extern "C" dit_status dit_rotary_table(const int32_t* dims, int axes, double the
   const qk::Wide turns_a_radian = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
   for (int a = 0; a < axes; ++a) {
     const int m = dims[a] / 2;
-    qk::Wide power = {1.0, 0.0};
-    const qk::Wide root = m ? qk::root_of(theta, m) : power, first = qk::product_of(turns_a_radian, {scale[a], 0.0});
-    for (int i = 0; i < m; ++i, power = qk::product_of(power, root)) {
-      const qk::Wide turns = qk::product_of(first, power);
+    const qk::Wide root = m ? qk::root_of(theta, m) : qk::Wide{};
+    qk::Wide turns = qk::product_of(turns_a_radian, {scale[a], 0.0});
+    for (int i = 0; i < m; ++i, turns = qk::product_of(turns, root)) {
       if (!isfinite(turns.hi) || !isfinite(turns.lo)) return DIT_ERR_INVALID_ARG;
       *o++ = qk::Pair{qk::fraction_of(turns), a, 0};
     }

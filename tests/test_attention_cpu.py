@@ -63,6 +63,17 @@ def test_rotary_table_against_long_arithmetic(dit, theta, scales):
             p += 1
 
 
+@pytest.mark.parametrize("theta", [5e-324, 1e-310, 1e-300, 1.7e308])
+def test_rotary_table_of_extreme_bases(dit, theta):
+    """Bases without low parts of their own, and powers of them past the range of doubles under a small scale."""
+    decimal.getcontext().prec = 80
+    words = dit.Rotary((64,), 64, theta=theta, scale=1e-12, device="cpu").table.view(-1, 2).tolist()
+    for i in range(3):
+        turns = decimal.Decimal(1e-12) * decimal.Decimal(theta) ** (decimal.Decimal(-2 * i) / 64) / decimal.Decimal(2 * math.pi)
+        off = (turns - decimal.Decimal(words[i][0] & (2 ** 64 - 1)) / 2 ** 64) % 1
+        assert min(abs(off), 1 - abs(off)) <= 2.0 ** -40 * float(turns) + 2.0 ** -63
+
+
 def test_rotary_refuses_frequencies_without_bounds(dit):
     for theta, scale in ((1e-300, 1e200), (1e-300, -1e200)):
         with pytest.raises(dit.DitError):
